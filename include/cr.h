@@ -46,7 +46,9 @@
 extern "C" {
 #endif
 
-typedef enum { CR_F32 = 1, CR_F64 = 2 } cr_dtype;
+/* CR_BF16 and CR_F16 are types of the model operators' tensors only; the
+ * reductions and scans take CR_F32 and CR_F64. */
+typedef enum { CR_F32 = 1, CR_F64 = 2, CR_BF16 = 3, CR_F16 = 4 } cr_dtype;
 
 /* Scan expression policies (P4229R0, Summary). */
 typedef enum {
@@ -298,6 +300,194 @@ cr_status cr_inclusive_scan_batched_host(const void* x_host, void* out_host, int
  *   - It allocates no device memory and frees none. */
 cr_status cr_reduce_noalloc(const void* x, int64_t n, int32_t L, const void* init_host,
                             cr_dtype dt, void* out_dev, void* stream);
+
+/* ------------------------------------------------------ model operators
+ * The token path of a recurrent language model: embedding lookup, short
+ * causal convolution and selective state space scan, each with its gradient
+ * and (the last two) its form for single tokens.
+ *   - Element types: CR_F32, CR_BF16 or CR_F16 for the tensors called "of
+ *     dt"; weights, states of the scan, sums and statistics are binary32
+ *     (const float*). CR_F64 is INVALID_ARG.
+ *   - Layout: token-major. A tensor of (batch, len, dim) has a batch stride
+ *     and a time stride in elements (any values >= 0 for inputs) and unit
+ *     channel stride; parameters and states are contiguous. Accesses are 16
+ *     bytes wide where pointers and strides allow it and elementwise where
+ *     they do not; results do not depend on which.
+ *   - lengths: NULL, or one count a sequence (index_bytes 4 or 8 wide),
+ *     clamped to [0, len]. Positions at or past a sequence's length are not
+ *     read and their outputs are zero.
+ *   - Every result is one fixed expression of the inputs: sums are ordered,
+ *     no value is summed by atomics, and repeated calls give the same bits.
+ *   - Outputs must not overlap inputs or each other, except where a call says
+ *     so. An output pointer equal to a pointer the call reads is INVALID_ARG.
+ *   - Conventions on streams, ownership, workspaces and errors as above; none
+ *     of these calls waits on the device, and none uses a status word. */
+
+/* out[i] = scale * table[tokens[i]], i < n (rounded once, to dt). A token
+ * outside [0, vocab) is padding and reads as a zero row.
+ *   tokens    device, n indices of index_bytes (4 or 8: int32_t or int64_t)
+ *   table     device, vocab rows of dim elements of dt, row_stride >= dim apart
+ *   out       device, n rows of dim elements of dt, out_stride >= dim apart */
+cr_status cr_embedding(const void* tokens, int32_t index_bytes, int64_t n, const void* table,
+                       int64_t vocab, int64_t dim, int64_t row_stride, float scale, cr_dtype dt,
+                       void* out, int64_t out_stride, void* stream);
+
+/* The gradient of cr_embedding with respect to its table, in binary32:
+ *   dW[v] = scale * tree(grad[p0], grad[p1], ...)
+ * over the positions p0 < p1 < ... with tokens[p] == v, tree() being the
+ * shift-reduce tree of cr_reduce (L = 1) in binary32 for every column: the
+ * bits are those of a reduction of the rows in order. Rows without a token
+ * are zero; with accumulate != 0 they are left as they are and the others
+ * become dW[v] + scale * tree(...). Tokens outside [0, vocab) contribute
+ * nothing.
+ *   grad      device, n rows of dim elements of dt, grad_stride apart
+ *   dw        device, vocab rows of dim floats, dw_stride >= dim apart
+ * n < 2^31, vocab < 2^31. */
+size_t cr_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+cr_status cr_embedding_backward(const void* tokens, int32_t index_bytes, int64_t n,
+                                const void* grad, int64_t grad_stride, int64_t vocab,
+                                int64_t dim, float scale, cr_dtype dt, int32_t accumulate,
+                                float* dw, int64_t dw_stride, void* ws, size_t ws_bytes,
+                                void* stream);
+
+typedef enum { CR_ACT_NONE = 0, CR_ACT_SILU = 1 } cr_activation;
+
+/* Depthwise causal convolution over time:
+ *   y[b,t,d] = act(bias[d] + sum_{k<K} w[d,k] x[b, t-(K-1)+k, d])
+ * with x[b, -j, d] (0 < j < K) = state[b, K-1-j, d], zero without a state;
+ * act(v) = v or v / (1 + exp(-v)). Sums run over k upwards, from bias. */
+typedef struct {
+  int64_t batch, len, dim;
+  int32_t width;          /* K: 2, 3 or 4 (others: CR_ERR_UNSUPPORTED)        */
+  int32_t activation;     /* cr_activation                                    */
+  int32_t dt;             /* cr_dtype of x, state and the outputs             */
+  int32_t index_bytes;    /* of lengths                                       */
+  const void* x;          /* of dt                                            */
+  int64_t x_batch_stride, x_time_stride;
+  const float* weight;    /* dim x K, contiguous                              */
+  const float* bias;      /* dim, or NULL                                     */
+  const void* state;      /* batch x (K-1) x dim of dt, contiguous, or NULL   */
+  const void* lengths;    /* batch counts, or NULL                            */
+} cr_causal_conv_args;
+
+/* Forward. y: of dt with its own strides. final_state: NULL, or batch x
+ * (K-1) x dim of dt: the last K-1 inputs of each sequence (the state's own
+ * entries, or zeros, where the sequence is shorter). */
+cr_status cr_causal_conv(const cr_causal_conv_args* args, void* y, int64_t y_batch_stride,
+                         int64_t y_time_stride, void* final_state, void* stream);
+
+/* Backward, for the same args: dy (of dt, strided) to
+ *   dx      of dt, strided, or NULL
+ *   dweight dim x K floats;  dbias dim floats, or NULL
+ *   dstate  batch x (K-1) x dim of dt, or NULL
+ * dfinal: the gradient of final_state (of dt, contiguous), or NULL. */
+typedef struct {
+  const void* dy;
+  int64_t dy_batch_stride, dy_time_stride;
+  const void* dfinal;
+  void* dx;
+  int64_t dx_batch_stride, dx_time_stride;
+  float* dweight;
+  float* dbias;
+  void* dstate;
+} cr_causal_conv_grads;
+size_t cr_causal_conv_backward_workspace_bytes(int64_t batch, int64_t len, int64_t dim,
+                                               int32_t width);
+cr_status cr_causal_conv_backward(const cr_causal_conv_args* args,
+                                  const cr_causal_conv_grads* grads, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* One token for each of `batch` running streams: the same expression with
+ * x[b] (batch rows of dim, x_stride apart) after its state row, which is
+ * shifted by one token in place. Stream b uses state row slots[b] of
+ * state_rows rows (each (K-1) x dim of dt, contiguous), row b without slots;
+ * a slot outside [0, state_rows) is padding: y[b] is zero and no state
+ * changes. Two streams of one call must not share a slot. */
+cr_status cr_causal_conv_step(const void* x, int64_t x_stride, void* state, int64_t state_rows,
+                              const void* slots, int32_t index_bytes, const float* weight,
+                              const float* bias, int32_t activation, int64_t batch, int64_t dim,
+                              int32_t width, cr_dtype dt, void* y, int64_t y_stride,
+                              void* stream);
+
+/* Selective state space scan: for each sequence b and channel d
+ *   delta[t] = softplus(dt[t] + dt_bias)  (or dt[t] + dt_bias without softplus)
+ *   h[t,n]   = exp(delta[t] A[d,n]) h[t-1,n] + delta[t] u[t] B[t,n]
+ *   y[t]     = (sum_n C[t,n] h[t,n] + D[d] u[t]) * z[t] / (1 + exp(-z[t]))
+ * with h[-1] = state (zero without one). B and C are shared by the dim /
+ * groups consecutive channels of a group. All arithmetic is binary32; a decay
+ * exp(delta A) below 2^-126 is zero. */
+typedef struct {
+  int64_t batch, len, dim;
+  int32_t dstate;         /* states a channel, 1..128 (more: CR_ERR_UNSUPPORTED) */
+  int32_t groups;         /* divides dim                                      */
+  int32_t softplus;       /* 0 or 1                                           */
+  int32_t dt_type;        /* cr_dtype of u, dt, B, C, z and their gradients   */
+  int32_t index_bytes;    /* of lengths                                       */
+  int32_t reserved;       /* 0                                                */
+  const void* u;          /* batch x len x dim, of dt, strided                */
+  int64_t u_batch_stride, u_time_stride;
+  const void* dt;         /* like u                                           */
+  int64_t dt_batch_stride, dt_time_stride;
+  const void* z;          /* like u, or NULL: no gate                         */
+  int64_t z_batch_stride, z_time_stride;
+  const void* B;          /* batch x len x groups x dstate, of dt; the last   */
+  int64_t B_batch_stride, B_time_stride; /* two axes contiguous               */
+  const void* C;          /* like B                                           */
+  int64_t C_batch_stride, C_time_stride;
+  const float* A;         /* dim x dstate                                     */
+  const float* D;         /* dim, or NULL                                     */
+  const float* dt_bias;   /* dim, or NULL                                     */
+  const float* state;     /* batch x dim x dstate, or NULL                    */
+  const void* lengths;    /* batch counts, or NULL                            */
+} cr_selective_scan_args;
+
+/* Number of checkpoints cr_selective_scan keeps for a sequence of len steps
+ * (a checkpoint: dim x dstate floats, the state before every so many steps). */
+int64_t cr_selective_scan_checkpoints(int64_t len);
+
+/* Forward. y: of dt, strided. final_state: NULL, or batch x dim x dstate
+ * floats (may be `state` itself). checkpoints: NULL, or batch x
+ * cr_selective_scan_checkpoints(len) x dim x dstate floats for the backward. */
+size_t cr_selective_scan_workspace_bytes(int64_t batch, int64_t len, int64_t dim,
+                                         int32_t dstate);
+cr_status cr_selective_scan(const cr_selective_scan_args* args, void* y, int64_t y_batch_stride,
+                            int64_t y_time_stride, float* final_state, float* checkpoints,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* Backward, for the same args. dy: the gradient of y. dfinal: the gradient
+ * of final_state, or NULL. checkpoints: as written by the forward call.
+ * Outputs: du, ddt, dz (NULL without z) like u, contiguous; dB, dC batch x
+ * len x groups x dstate of dt, contiguous; dA dim x dstate, dD and ddt_bias
+ * dim floats (each NULL when the argument is); dstate batch x dim x dstate
+ * floats, or NULL. */
+typedef struct {
+  const void* dy;
+  int64_t dy_batch_stride, dy_time_stride;
+  const float* dfinal;
+  const float* checkpoints;
+  void* du;
+  void* ddt;
+  void* dz;
+  void* dB;
+  void* dC;
+  float* dA;
+  float* dD;
+  float* ddt_bias;
+  float* dstate;
+} cr_selective_scan_grads;
+size_t cr_selective_scan_backward_workspace_bytes(int64_t batch, int64_t len, int64_t dim,
+                                                  int32_t dstate, int32_t groups);
+cr_status cr_selective_scan_backward(const cr_selective_scan_args* args,
+                                     const cr_selective_scan_grads* grads, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* One token for each of args->batch running streams (args->len is 1; the
+ * time strides, lengths and state of args are not used): state rows are
+ * updated in place. Slots as for cr_causal_conv_step; a row is dim x dstate
+ * floats. y: batch rows, y_batch_stride apart. */
+cr_status cr_selective_scan_step(const cr_selective_scan_args* args, float* state,
+                                 int64_t state_rows, const void* slots, void* y,
+                                 int64_t y_batch_stride, void* stream);
 
 /* ------------------------------------------------------------- utilities */
 

@@ -14,7 +14,10 @@ andyD123/canonical-reduce):
   * ``inclusive_scan(x, policy, B)``: P4229R0's prefix observations of the
     named expression policies left_fold, pairwise, iterated_pairwise,
     block_dyadic<B>;
-  * batched/strided variants of both over one axis of a 2-D tensor.
+  * batched/strided variants of both over one axis of a 2-D tensor;
+  * the operators of a recurrent language model's token path (``model.py``):
+    embedding lookup, short causal convolution, selective state space scan,
+    with their gradients and single-token forms.
 Results are bit-identical to the named expression on any GPU and launch shape.
 """
 from __future__ import annotations
@@ -80,6 +83,22 @@ SIGNATURES = {
     "cr_measure_int_add_rate": (_INT, [_P, _SZ, _P, ctypes.POINTER(ctypes.c_double)]),
     "cr_measure_add_peak": (_INT, [_INT, _P, _SZ, _P, ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_double)]),
+    "cr_embedding": (_INT, [_P, _I32, _I64, _P, _I64, _I64, _I64, ctypes.c_float, _INT, _P, _I64,
+                            _P]),
+    "cr_embedding_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "cr_embedding_backward": (_INT, [_P, _I32, _I64, _P, _I64, _I64, _I64, ctypes.c_float, _INT,
+                                     _I32, _P, _I64, _P, _SZ, _P]),
+    "cr_causal_conv": (_INT, [_P, _P, _I64, _I64, _P, _P]),
+    "cr_causal_conv_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "cr_causal_conv_backward": (_INT, [_P, _P, _P, _SZ, _P]),
+    "cr_causal_conv_step": (_INT, [_P, _I64, _P, _I64, _P, _I32, _P, _P, _I32, _I64, _I64, _I32,
+                                   _INT, _P, _I64, _P]),
+    "cr_selective_scan_checkpoints": (_I64, [_I64]),
+    "cr_selective_scan_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "cr_selective_scan": (_INT, [_P, _P, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "cr_selective_scan_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
+    "cr_selective_scan_backward": (_INT, [_P, _P, _P, _SZ, _P]),
+    "cr_selective_scan_step": (_INT, [_P, _P, _I64, _P, _P, _I64, _P]),
 }
 
 
@@ -580,7 +599,14 @@ def measure_int_add_rate(device="cuda", stream=None) -> float:
     return rate.value
 
 
+from .model import (causal_conv, causal_conv_backward, causal_conv_step,  # noqa: E402
+                    embedding, embedding_backward, selective_scan, selective_scan_backward,
+                    selective_scan_step)
+
 __all__ = ["reduce", "reduce_batched", "reduce_policy", "inclusive_scan",
            "inclusive_scan_batched",
            "exclusive_scan", "scan_include_initial", "exclusive_scan_batched",
-           "scan_include_initial_batched", "MODES", "sync_status", "lib", "workspace", "launch_count", "profile_enable", "profile_collect", "measure_add_peak", "add_pairs_int", "measure_int_add_rate", "CrError", "POLICIES", "SIGNATURES"]
+           "scan_include_initial_batched", "MODES", "sync_status", "lib", "workspace", "launch_count", "profile_enable", "profile_collect", "measure_add_peak", "add_pairs_int", "measure_int_add_rate", "CrError", "POLICIES", "SIGNATURES",
+           "embedding", "embedding_backward", "causal_conv", "causal_conv_backward",
+           "causal_conv_step", "selective_scan", "selective_scan_backward",
+           "selective_scan_step"]

@@ -77,7 +77,11 @@ const char* kernel_name(int id) {
       "scan_seq_block_kernel", "row_reduce_kernel",
       "chain_link_kernel",     "chain_verify_kernel",   "chain_walk_fix_kernel",
       "scan_local_again_kernel", "fixup_again_kernel", "pairwise_tile_prefix_kernel",
-      "chain_round_sum_kernel", "scan_seq_left2_kernel"};
+      "chain_round_sum_kernel", "scan_seq_left2_kernel", "embedding_kernel",
+      "token_sort_kernel", "embedding_rows_kernel", "causal_conv_kernel",
+      "causal_conv_backward_kernel", "causal_conv_sum_kernel", "causal_conv_step_kernel",
+      "selective_scan_kernel", "selective_scan_backward_kernel", "selective_scan_sum_kernel",
+      "selective_scan_step_kernel"};
   return (id >= 0 && id < kKernelCount) ? names[id] : "unknown";
 }
 

@@ -44,6 +44,17 @@ enum KernelId : int {
   kKPairwisePrefix,
   kKChainRoundSum,
   kKScanSeqLeft2,
+  kKEmbedding,
+  kKTokenSort,
+  kKEmbeddingRows,
+  kKCausalConv,
+  kKCausalConvBackward,
+  kKCausalConvSum,
+  kKCausalConvStep,
+  kKSelectiveScan,
+  kKSelectiveScanBackward,
+  kKSelectiveScanSum,
+  kKSelectiveScanStep,
   kKernelCount
 };
 

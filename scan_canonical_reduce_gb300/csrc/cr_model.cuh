@@ -1,0 +1,138 @@
+// Shared pieces of the model operators (embedding, causal convolution,
+// selective scan): element types, vector access, the two nonlinearities, and
+// the host-side argument checks.
+//
+// Tensors of 16-bit types are read and written as such; everything between
+// is binary32. Rounding to 16 bits happens once, when a result is stored.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "cr.h"
+
+namespace cr {
+
+// ------------------------------------------------------------ elements
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+template <class T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T v[V];
+};
+
+// V consecutive elements as binary32. wide: p is aligned to the whole pack
+// and all V elements exist; otherwise the first `have` are read one by one
+// and the rest are zero.
+template <class T, int V>
+__device__ __forceinline__ void load_f32(const T* p, bool wide, int have, float (&f)[V]) {
+  if (wide) {
+    const Pack<T, V> q = *reinterpret_cast<const Pack<T, V>*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f32(q.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = i < have ? to_f32(p[i]) : 0.0f;
+  }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_f32(T* p, bool wide, int have, const float (&f)[V]) {
+  if (wide) {
+    Pack<T, V> q;
+#pragma unroll
+    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<Pack<T, V>*>(p) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < have) p[i] = from_f32<T>(f[i]);
+  }
+}
+
+// An index of 4 or 8 bytes.
+__device__ __forceinline__ int64_t load_index(const void* p, int bytes, int64_t i) {
+  return bytes == 8 ? static_cast<const int64_t*>(p)[i]
+                    : (int64_t)static_cast<const int32_t*>(p)[i];
+}
+
+// Sequence b's length, clamped to [0, len].
+__device__ __forceinline__ int64_t sequence_length(const void* lengths, int bytes, int64_t b,
+                                                   int64_t len) {
+  if (lengths == nullptr) return len;
+  const int64_t n = load_index(lengths, bytes, b);
+  return n < 0 ? 0 : n > len ? len : n;
+}
+
+// ------------------------------------------------------ nonlinearities
+// 1 / (1 + exp(-v)); 0 and 1 in the limits.
+__device__ __forceinline__ float sigmoid(float v) {
+  return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+
+// softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(exp(-|v|)): the second
+// term keeps its relative accuracy where softplus is small.
+__device__ __forceinline__ float softplus(float v) {
+  return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
+}
+
+// 2^v of a decay (v <= 0 in use), zero below 2^-126. The instruction's error
+// is at most 1.4e-7 relative on [-20, 0], its mean -5e-9 near 0 and -5e-8
+// from -1 on (measured over 2^20 points an interval).
+__device__ __forceinline__ float exp2_decay(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.44269504088896341f;
+
+// ------------------------------------------------------------ host side
+inline size_t model_esize(int dt) {
+  switch (dt) {
+    case CR_F32: return 4;
+    case CR_BF16:
+    case CR_F16: return 2;
+    default: return 0;
+  }
+}
+
+inline bool ptr_aligned(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+// Whether rows of a (batch, time) strided tensor all start on `bytes`.
+inline bool rows_aligned(const void* p, int64_t bs, int64_t ts, size_t es, size_t bytes) {
+  return ptr_aligned(p, bytes) && ((size_t)bs * es) % bytes == 0 && ((size_t)ts * es) % bytes == 0;
+}
+
+inline bool index_width_ok(int bytes) { return bytes == 4 || bytes == 8; }
+
+inline size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxBlocks = 0x7FFFFFFF;  // of a grid's x axis
+
+}  // namespace cr
+
+// Runs EXPR with T bound to the element type that DT names.
+#define CR_MODEL_TYPE(DT, ...)                     \
+  switch (DT) {                                    \
+    case CR_F32: { using T = float; __VA_ARGS__; break; }          \
+    case CR_BF16: { using T = __nv_bfloat16; __VA_ARGS__; break; } \
+    default: { using T = __half; __VA_ARGS__; break; }             \
+  }

@@ -1,0 +1,171 @@
+"""Embedding lookup and its gradient. The lookup is one product rounded once;
+the gradient is scale * the canonical tree over a token's rows in order, so
+both are compared bit for bit with the oracle's reduction."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module")
+def scr():
+    import scan_canonical_reduce_gb300 as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def skewed(n, V, seed, pad=0.05):
+    g = gen(seed)
+    t = (torch.exp(torch.rand(n, generator=g, dtype=torch.float64) * np.log(V)) - 1).long()
+    t = t.clamp(0, V - 1) * 7919 % V
+    t[torch.rand(n, generator=g) < pad] = -1
+    t[torch.rand(n, generator=g) < pad / 2] = V + 3
+    return t
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,D", [(1, 1, 1), (5, 100, 1024), (33, 7, 77), (300, 1000, 130),
+                                   (257, 50, 2056), (0, 10, 16), (4, 10, 0)])
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_lookup(scr, dtype, n, V, D, index):
+    table = torch.randn(V, D, generator=gen(1)).to(dtype)
+    tok = skewed(n, V, 2)
+    got = scr.embedding(tok.to(index).to(DEV), table.to(DEV), 1.7)
+    ok = (tok >= 0) & (tok < V)
+    want = table[tok.clamp(0, V - 1)].float() * torch.tensor(1.7, dtype=torch.float32)
+    want = torch.where(ok[:, None], want, 0.0).to(dtype)
+    assert got.dtype == dtype and torch.equal(got.cpu(), want)
+
+
+def test_lookup_shapes_and_strides(scr):
+    table = torch.randn(40, 64, generator=gen(3)).to(torch.bfloat16).to(DEV)
+    tok = torch.randint(0, 40, (3, 5), generator=gen(4)).to(DEV)
+    want = (table[tok].float() * 0.5).to(torch.bfloat16)
+    assert torch.equal(scr.embedding(tok, table, 0.5), want)
+    # a table whose rows start off 16 bytes, one that is transposed, tokens in steps
+    odd = torch.zeros(40, 67, dtype=torch.bfloat16, device=DEV)[:, 3:]
+    odd.copy_(table)
+    assert torch.equal(scr.embedding(tok, odd, 0.5), want)
+    assert torch.equal(scr.embedding(tok, table.t().contiguous().t(), 0.5), want)
+    wide = torch.zeros(3, 10, dtype=torch.int64, device=DEV)
+    wide[:, ::2] = tok
+    assert torch.equal(scr.embedding(wide[:, ::2], table, 0.5), want)
+    out = torch.full((16, 70), float("nan"), dtype=torch.bfloat16, device=DEV)
+    r = scr.embedding(tok.flatten(), table, 0.5, out=out[:15, 1:65])
+    assert torch.equal(r, want.view(15, 64))
+    assert out[:, 0].isnan().all() and out[:, 65:].isnan().all() and out[15].isnan().all()
+
+
+def tree(rows):
+    """The canonical tree over rows (k, D) float32, column by column."""
+    x = np.ascontiguousarray(rows.T.astype(np.float32))
+    return oracle.reduce_batched(x.reshape(-1), x.shape[0], x.shape[1], 1, x.shape[1], 1,
+                                 np.float32(-0.0))
+
+
+def want_grad(tok, grad, V, scale):
+    g = grad.float().numpy()
+    out = np.zeros((V, g.shape[1]), np.float32)
+    for v in range(V):
+        at = np.nonzero(tok.numpy() == v)[0]
+        if len(at):
+            out[v] = tree(g[at]) * np.float32(scale)
+    return out
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,D", [(1, 1, 1), (2, 3, 5), (700, 31, 77), (1037, 1500, 130),
+                                   (5000, 3, 12), (4099, 300, 33), (0, 10, 16)])
+def test_gradient_bits(scr, dtype, n, V, D):
+    tok = skewed(n, V, 5)
+    grad = torch.randn(n, D, generator=gen(6)).to(dtype)
+    got = scr.embedding_backward(tok.to(DEV), grad.to(DEV), V, 0.3)
+    assert got.dtype == torch.float32
+    assert got.cpu().numpy().tobytes() == want_grad(tok, grad, V, 0.3).tobytes()
+
+
+@pytest.mark.parametrize("count", [1, 7, 8, 9, 63, 64, 65, 127, 128, 200, 1000, 4096, 12345])
+def test_gradient_of_one_frequent_token(scr, count):
+    """Rows of every length around the sizes at which the tree is split."""
+    n, V, D = count + 50, 20, 9
+    tok = torch.randint(0, V, (n,), generator=gen(7))
+    tok[torch.randperm(n, generator=gen(8))[:count]] = 11
+    grad = torch.randn(n, D, generator=gen(9))
+    got = scr.embedding_backward(tok.to(DEV), grad.to(DEV), V, 1.0)
+    assert got.cpu().numpy().tobytes() == want_grad(tok, grad, V, 1.0).tobytes()
+
+
+def test_gradient_large_vocabulary(scr):
+    """More rows than one block sorts, and tokens of 32 bits."""
+    n, V, D = 3000, 200_003, 4
+    tok = skewed(n, V, 10)
+    grad = torch.randn(n, D, generator=gen(11))
+    got = scr.embedding_backward(tok.to(torch.int32).to(DEV), grad.to(DEV), V).cpu().numpy()
+    used = np.unique(tok.numpy()[(tok.numpy() >= 0) & (tok.numpy() < V)])
+    for v in used[::17]:
+        assert got[v].tobytes() == tree(grad.numpy()[tok.numpy() == v]).tobytes()
+    mask = np.ones(V, bool)
+    mask[used] = False
+    assert not got[mask].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradient_accumulates(scr, dtype):
+    """out + scale * tree on rows with tokens, others untouched (NaN stays)."""
+    n, V, D = 500, 900, 68
+    tok = skewed(n, V, 12)
+    grad = torch.randn(n, D, generator=gen(13)).to(dtype)
+    old = torch.randn(V, D, generator=gen(14))
+    have = np.isin(np.arange(V), tok.numpy())
+    old[torch.from_numpy(~have)] = float("nan")
+    out = old.to(DEV)
+    r = scr.embedding_backward(tok.to(DEV), grad.to(DEV), V, 2.0, out=out, accumulate=True)
+    assert r.data_ptr() == out.data_ptr()
+    want = np.where(have[:, None], old.numpy() + want_grad(tok, grad, V, 2.0), old.numpy())
+    assert out.cpu().numpy().tobytes() == want.astype(np.float32).tobytes()
+
+
+def test_gradient_skips_padding_rows(scr):
+    """Gradients of padding positions may hold anything."""
+    tok = torch.tensor([3, -1, 5, 3, 99])
+    grad = torch.randn(5, 40, generator=gen(15))
+    grad[1], grad[4] = float("nan"), float("inf")
+    got = scr.embedding_backward(tok.to(DEV), grad.to(DEV), 10).cpu()
+    assert torch.equal(got[3], grad[0] + grad[3]) and torch.equal(got[5], grad[2])
+    assert not got[[0, 1, 2, 4, 6, 7, 8, 9]].any()
+
+
+def test_gradient_strided(scr):
+    tok = skewed(200, 30, 16)
+    base = torch.full((200, 150), float("nan"))
+    base[:, 5:138] = torch.randn(200, 133, generator=gen(17))
+    out = torch.full((30, 140), -1.0, device=DEV)
+    scr.embedding_backward(tok.to(DEV), base.to(DEV)[:, 5:138], 30, out=out[:, 3:136])
+    got = out.cpu().numpy()
+    assert got[:, 3:136].tobytes() == want_grad(tok, base[:, 5:138], 30, 1.0).tobytes()
+    assert (got[:, :3] == -1).all() and (got[:, 136:] == -1).all()
+    one = torch.randn(133, generator=gen(18))
+    got = scr.embedding_backward(tok.to(DEV), one.to(DEV).expand(200, 133), 30).cpu().numpy()
+    assert got.tobytes() == want_grad(tok, one.expand(200, 133), 30, 1.0).tobytes()
+
+
+def test_gradient_matches_differences(scr):
+    """The lookup is linear in its table: its change along a direction is the
+    gradient's product with the direction."""
+    tok = skewed(300, 40, 19)
+    grad = torch.randn(300, 16, generator=gen(20))
+    direction = torch.randn(40, 16, generator=gen(21))
+    moved = scr.embedding(tok.to(DEV), direction.to(DEV), 0.7).cpu().double()
+    dw = scr.embedding_backward(tok.to(DEV), grad.to(DEV), 40, 0.7).cpu().double()
+    left, right = (moved * grad.double()).sum(), (dw * direction.double()).sum()
+    # each side: 300 x 16 terms of one product, at most 300 roundings each
+    scale = (moved * grad.double()).abs().sum()
+    assert abs(left - right) <= 300 * 2.0 ** -23 * scale

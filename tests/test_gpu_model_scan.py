@@ -1,0 +1,276 @@
+"""Selective state space scan: forward, gradient and single tokens against a
+plain 64-bit evaluation (tests/model_reference.py says how the tolerances
+follow from the number of roundings)."""
+import numpy as np
+import pytest
+import torch
+
+from . import model_reference as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+NAN = float("nan")
+SEQ = ("u", "dt", "z", "B", "C")
+
+
+@pytest.fixture(scope="module")
+def scr():
+    import scan_canonical_reduce_gb300 as m
+    return m
+
+
+def make(batch, T, D, N, groups, dtype, seed, lengths=None, plain=False):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    s = {"u": r(batch, T, D).to(dtype), "dt": (r(batch, T, D) * 0.7 - 1).to(dtype),
+         "A": -torch.exp(r(D, N)), "B": r(batch, T, groups, N).to(dtype),
+         "C": r(batch, T, groups, N).to(dtype), "D": r(D), "z": r(batch, T, D).to(dtype),
+         "dt_bias": r(D) * 0.5 - 1, "state": r(batch, D, N),
+         "lengths": None if lengths is None else torch.tensor(lengths)}
+    dy, dfinal = r(batch, T, D).to(dtype), r(batch, D, N)
+    if plain:
+        for k in ("D", "z", "dt_bias", "state"):
+            s[k] = None
+    if lengths is not None:
+        for b, n in enumerate(lengths):
+            for k in SEQ:
+                if s[k] is not None:
+                    s[k][b, max(n, 0):] = NAN
+            dy[b, max(n, 0):] = NAN
+    return s, dy, dfinal
+
+
+def dev(s):
+    return {k: v if v is None else v.to(DEV) for k, v in s.items()}
+
+
+def reference(s, softplus=True, dy=None, dfinal=None):
+    n = None if s["lengths"] is None else s["lengths"].tolist()
+    return R.scan(*(R.f64(s[k]) for k in ("u", "dt", "A", "B", "C", "D", "z", "dt_bias")),
+                  softplus, R.f64(s["state"]), n, R.f64(dy), R.f64(dfinal))
+
+
+def steps(T, N, sums=0):
+    """Roundings of a result: up to 8 a time step, the sum over the states, the
+    softplus, the gate, and where a result is summed over rows, those."""
+    return 8 * T + N + 32 + sums
+
+
+SHAPES = [(1, 1, 1, 1, 1), (1, 1, 40, 16, 1), (2, 3, 5, 2, 1), (2, 17, 33, 16, 1),
+          (1, 70, 260, 16, 1), (2, 37, 66, 13, 2), (1, 33, 40, 8, 4), (1, 40, 24, 32, 1),
+          (1, 35, 10, 64, 2), (1, 20, 6, 128, 1), (2, 50, 130, 4, 1), (1, 21, 300, 3, 1),
+          (2, 0, 16, 16, 1)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward(scr, dtype, shape):
+    T, N = shape[1], shape[3]
+    s, _, _ = make(*shape, dtype, 1)
+    y, final, kept = scr.selective_scan(**dev(s), return_state=True, return_checkpoints=True)
+    ref = reference(s)
+    R.close(y, *ref["y"], steps(T, N), "y")
+    R.close(final, *ref["final"], steps(T, N), "state")
+    if T:
+        assert torch.equal(kept[:, 0].cpu(), s["state"])
+    s, _, _ = make(*shape, dtype, 2, plain=True)
+    y, final = scr.selective_scan(**dev(s), return_state=True)
+    ref = reference(s)
+    R.close(y, *ref["y"], steps(T, N), "plain y")
+    R.close(final, *ref["final"], steps(T, N), "plain state")
+
+
+def check_grads(g, ref, batch, T, D, N, groups):
+    for name, v in g.items():
+        sums = {"A": batch * T, "D": batch * T, "dt_bias": batch * T, "B": D // groups,
+                "C": D // groups}.get(name, 0)
+        R.close(v, *ref[name], steps(2 * T, N, sums), name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_backward(scr, dtype, shape):
+    s, dy, dfinal = make(*shape, dtype, 3)
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    assert set(g) == set(s) - {"lengths"}
+    check_grads(g, reference(s, True, dy, dfinal)["grads"], *shape)
+    s, dy, _ = make(*shape, dtype, 4, plain=True)
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s))
+    assert set(g) == {"u", "dt", "A", "B", "C"}
+    check_grads(g, reference(s, True, dy)["grads"], *shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_without_softplus(scr, dtype):
+    s, dy, _ = make(2, 20, 40, 16, 1, dtype, 5)
+    s["dt"] = (s["dt"].abs() * 0.1).to(dtype)
+    s["dt_bias"] = s["dt_bias"].abs() * 0.1
+    ref = reference(s, False, dy)
+    R.close(scr.selective_scan(**dev(s), softplus=False), *ref["y"], steps(20, 16), "y")
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), softplus=False)
+    check_grads(g, ref["grads"], 2, 20, 40, 16, 1)
+
+
+LENGTHS = [[70, 0, 1, 2, 33, 69], [16, 15, 17, 300, -4, 64]]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lengths", LENGTHS)
+@pytest.mark.parametrize("N,groups", [(16, 1), (5, 2)])
+def test_lengths(scr, dtype, lengths, N, groups):
+    """What lies past a length is not read (NaN here), gives zeros, and leaves
+    the state; an empty sequence returns its state and its gradient as they came."""
+    s, dy, dfinal = make(6, 70, 38, N, groups, dtype, 6, lengths=lengths)
+    y, final = scr.selective_scan(**dev(s), return_state=True)
+    ref = reference(s, True, dy, dfinal)
+    R.close(y, *ref["y"], steps(70, N), "y")
+    R.close(final, *ref["final"], steps(70, N), "state")
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    check_grads(g, ref["grads"], 6, 70, 38, N, groups)
+    for b, n in enumerate(lengths):
+        n = max(0, min(n, 70))
+        assert not y[b, n:].any()
+        assert not any(g[k][b, n:].any() for k in SEQ)
+        if n == 0:
+            assert torch.equal(final[b].cpu(), s["state"][b])
+            assert torch.equal(g["state"][b].cpu(), dfinal[b])
+
+
+def test_gradient_matches_differences(scr):
+    """The gradient's product with a direction against central differences of
+    the 64-bit formula: their error is eps^2 / 6 of the third derivative, which
+    eps = 1e-4 takes far below the gradient's own binary32 rounding."""
+    s, dy, dfinal = make(2, 9, 6, 5, 2, torch.float32, 7)
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    gen = torch.Generator().manual_seed(8)
+    for name in g:
+        v = torch.randn(s[name].shape, generator=gen, dtype=torch.float64)
+        ends = []
+        for sign in (1, -1):
+            m = {k: R.f64(t) for k, t in s.items()}
+            m[name] = m[name] + sign * 1e-4 * v.numpy()
+            ref = R.scan(*(m[k] for k in ("u", "dt", "A", "B", "C", "D", "z", "dt_bias")), True,
+                         m["state"], None)
+            ends.append((ref["y"][0] * R.f64(dy)).sum() + (ref["final"][0] * R.f64(dfinal)).sum())
+        want = (ends[0] - ends[1]) / 2e-4
+        got = (R.f64(g[name]) * v.numpy()).sum()
+        size = (np.abs(R.f64(g[name])) * np.abs(v.numpy())).sum()
+        assert abs(got - want) <= 1e-5 * size, name
+
+
+def test_extreme_steps(scr):
+    """Steps so small that the softplus is its exponential, and so large that
+    the decay underflows to zero."""
+    s, dy, _ = make(1, 30, 16, 16, 1, torch.float32, 9)
+    s["dt"][0, :, :4] = -30.0
+    s["dt"][0, :, 4:8] = 60.0
+    s["dt"][0, ::3, 8:12] = 200.0
+    s["z"][0, :, 2] = -200.0
+    s["z"][0, :, 3] = 200.0
+    ref = reference(s, True, dy)
+    R.close(scr.selective_scan(**dev(s)), *ref["y"], steps(30, 16), "y")
+    check_grads(scr.selective_scan_backward(dy.to(DEV), **dev(s)), ref["grads"], 1, 30, 16, 16, 1)
+
+
+def test_strides_and_alignment(scr):
+    """The same bits from strided, misaligned and transposed inputs, and from
+    B and C without a group axis."""
+    s, dy, _ = make(3, 40, 24, 16, 1, torch.bfloat16, 10)
+    d = dev(s)
+    want = scr.selective_scan(**d)
+    gwant = scr.selective_scan_backward(dy.to(DEV), **d)
+    def same(**changed):
+        m = {**d, **changed}
+        assert torch.equal(scr.selective_scan(**m), want)
+        g = scr.selective_scan_backward(dy.to(DEV), **m)
+        assert all(torch.equal(g[k].view_as(gwant[k]), gwant[k]) for k in g)
+    for at in (5, 8):
+        wide = torch.full((3, 40, 24 * 3 + 16), NAN, dtype=torch.bfloat16, device=DEV)
+        views = {}
+        for i, k in enumerate(("u", "dt", "z")):
+            views[k] = wide[:, :, at + 24 * i:at + 24 * (i + 1)]
+            views[k].copy_(d[k])
+        same(**views)
+    same(u=d["u"].permute(2, 0, 1).contiguous().permute(1, 2, 0))
+    same(z=d["z"].transpose(0, 1).contiguous().transpose(0, 1))
+    both = torch.cat([d["B"], d["C"]], 3)
+    same(B=both[..., :16], C=both[..., 16:])
+    same(B=both[..., :16].squeeze(2), C=both[..., 16:].squeeze(2))
+    odd = torch.zeros(3, 40, 1, 19, dtype=torch.bfloat16, device=DEV)
+    odd[..., 3:] = d["B"]
+    same(B=odd[..., 3:])
+    same(A=d["A"].t().contiguous().t())
+    out = torch.full((3, 40, 27), NAN, dtype=torch.bfloat16, device=DEV)
+    scr.selective_scan(**d, out=out[:, :, 2:26])
+    assert torch.equal(out[:, :, 2:26], want)
+    assert out[:, :, :2].isnan().all() and out[:, :, 26:].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_single_tokens(scr, dtype):
+    """Single tokens after a prompt: within the roundings of the formula of
+    the whole sequence."""
+    s, _, _ = make(2, 24, 36, 16, 1, dtype, 11)
+    d = dev(s)
+    ref = reference(s)
+    cut = {k: (v[:, :20] if k in SEQ else v) for k, v in d.items()}
+    y, state = scr.selective_scan(**cut, return_state=True)
+    R.close(y, ref["y"][0][:, :20], ref["y"][1][:, :20], steps(20, 16), "prompt")
+    for t in range(20, 24):
+        y = scr.selective_scan_step(d["u"][:, t], d["dt"][:, t], d["A"], d["B"][:, t],
+                                    d["C"][:, t], state, d["D"], d["z"][:, t], d["dt_bias"])
+        R.close(y, ref["y"][0][:, t], ref["y"][1][:, t], steps(t + 1, 16), "token %d" % t)
+    R.close(state, *ref["final"], steps(24, 16), "state")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,D,N,groups", [(1, 1, 1, 1), (5, 70, 16, 1), (64, 130, 13, 2),
+                                              (3, 40, 64, 1), (3, 9, 128, 1)])
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_step_slots(scr, dtype, batch, D, N, groups, index):
+    s, _, _ = make(batch, 1, D, N, groups, dtype, 12)
+    rows = batch + 4
+    g = torch.Generator().manual_seed(13)
+    pool = torch.randn(rows, D, N, generator=g)
+    slots = torch.randperm(rows, generator=g)[:batch]
+    if batch > 2:
+        slots[0], slots[2] = -1, rows
+    state = pool.to(DEV)
+    one = {k: s[k][:, 0].to(DEV) for k in SEQ}
+    y = scr.selective_scan_step(one["u"], one["dt"], s["A"].to(DEV), one["B"], one["C"], state,
+                                s["D"].to(DEV), one["z"], s["dt_bias"].to(DEV),
+                                slots=slots.to(index).to(DEV))
+    real = [b for b in range(batch) if 0 <= slots[b] < rows]
+    none = [b for b in range(batch) if b not in real]
+    s["state"] = torch.stack([pool[slots[b]] if b in real else torch.zeros(D, N)
+                              for b in range(batch)])
+    ref = reference(s)
+    if real:
+        R.close(y[real], ref["y"][0][real, 0], ref["y"][1][real, 0], steps(1, N), "y")
+        at = [int(slots[b]) for b in real]
+        R.close(state[at], ref["final"][0][real], ref["final"][1][real], steps(1, N), "state")
+    assert not y[none].any()
+    left = [r for r in range(rows) if r not in [int(slots[b]) for b in real]]
+    assert torch.equal(state[left].cpu(), pool[left])
+
+
+def test_long_sequence(scr):
+    """Thousands of steps, a few channels."""
+    s, dy, _ = make(1, 2500, 8, 16, 1, torch.float32, 14)
+    ref = reference(s, True, dy)
+    R.close(scr.selective_scan(**dev(s)), *ref["y"], steps(2500, 16), "y")
+    check_grads(scr.selective_scan_backward(dy.to(DEV), **dev(s)), ref["grads"], 1, 2500, 8, 16, 1)
+
+
+def test_repeated_calls_give_the_same_bits(scr):
+    s, dy, _ = make(2, 300, 260, 16, 1, torch.bfloat16, 15)
+    d = dev(s)
+    y, kept = scr.selective_scan(**d, return_checkpoints=True)
+    first = scr.selective_scan_backward(dy.to(DEV), **d, checkpoints=kept)
+    again = scr.selective_scan_backward(dy.to(DEV), **d)  # computes its own checkpoints
+    assert all(torch.equal(first[k], again[k]) for k in first)
+    for _ in range(3):
+        assert torch.equal(scr.selective_scan(**d), y)
+        again = scr.selective_scan_backward(dy.to(DEV), **d, checkpoints=kept)
+        assert all(torch.equal(first[k], again[k]) for k in first)
