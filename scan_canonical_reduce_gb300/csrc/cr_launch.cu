@@ -80,7 +80,8 @@ const char* kernel_name(int id) {
       "chain_round_sum_kernel", "scan_seq_left2_kernel", "embedding_kernel",
       "token_sort_kernel", "embedding_rows_kernel", "causal_conv_kernel",
       "causal_conv_backward_kernel", "causal_conv_sum_kernel", "causal_conv_step_kernel",
-      "selective_scan_kernel", "selective_scan_backward_kernel", "selective_scan_sum_kernel",
+      "selective_scan_kernel", "selective_scan_states_kernel", "selective_scan_backward_kernel",
+      "selective_scan_sum_kernel",
       "selective_scan_step_kernel"};
   return (id >= 0 && id < kKernelCount) ? names[id] : "unknown";
 }

@@ -52,6 +52,7 @@ enum KernelId : int {
   kKCausalConvSum,
   kKCausalConvStep,
   kKSelectiveScan,
+  kKSelectiveScanStates,
   kKSelectiveScanBackward,
   kKSelectiveScanSum,
   kKSelectiveScanStep,

@@ -84,10 +84,22 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __fdividef(1.0f, 1.0f + __expf(-v));
 }
 
-// softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(exp(-|v|)): the second
-// term keeps its relative accuracy where softplus is small.
+// softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|). With
+// s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 +
+// ...): seven terms leave (1/9)^7 / 15 = 1.4e-8 of the value, and the result
+// keeps its relative accuracy where it is small (a few units of binary32).
 __device__ __forceinline__ float softplus(float v) {
-  return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
+  const float e = __expf(-fabsf(v));
+  const float s = __fdividef(e, 2.0f + e);
+  const float w = s * s;
+  float p = 1.0f / 13.0f;
+  p = fmaf(p, w, 1.0f / 11.0f);
+  p = fmaf(p, w, 1.0f / 9.0f);
+  p = fmaf(p, w, 1.0f / 7.0f);
+  p = fmaf(p, w, 1.0f / 5.0f);
+  p = fmaf(p, w, 1.0f / 3.0f);
+  p = fmaf(p, w, 1.0f);
+  return fmaf(s + s, p, fmaxf(v, 0.0f));
 }
 
 // 2^v of a decay (v <= 0 in use), zero below 2^-126. The instruction's error
@@ -99,6 +111,34 @@ __device__ __forceinline__ float exp2_decay(float v) {
   return r;
 }
 constexpr float kLog2e = 1.44269504088896341f;
+
+// ------------------------------------------------- pairs of binary32
+// Two binary32 values in one 64-bit register pair, for the packed
+// arithmetic (one issue for two operations, each rounded to nearest).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // ------------------------------------------------------------ host side
 inline size_t model_esize(int dt) {

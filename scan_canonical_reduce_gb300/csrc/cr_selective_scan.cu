@@ -74,56 +74,366 @@ __device__ __forceinline__ void load_states(const T* p, int n0, int N, float (&f
   for (int k = 0; k < kS; ++k) f[k] = n0 + k < N ? to_f32(p[n0 + k]) : 0.0f;
 }
 
-template <class T, int G>
-__global__ void __launch_bounds__(kScanThreads)
-selective_scan_kernel(ScanIn<T> in, T* __restrict__ y, int64_t ybs, int64_t yts,
-                      float* __restrict__ final_state, float* __restrict__ checkpoints,
-                      int64_t n_check) {
-  const Place p = place<G>(in.group_dim, in.groups);
-  const int n0 = p.g * kS;
-  const int64_t len = sequence_length(in.lengths, in.index_bytes, p.b, in.len);
-  float A[kS], h[kS];
-  load_states(in.A + p.d * in.N, n0, in.N, A);
-  const int64_t row = (p.b * in.dim + p.d) * in.N;
-  if (in.state != nullptr) load_states(in.state + row, n0, in.N, h);
-  else
+// One lane's four states of a channel: decays and states as two pairs.
+struct Lane {
+  F2 A[2];  // A log2(e)
+  F2 h[2];
+};
+
+__device__ __forceinline__ void lane_init(Lane& l, const float (&A)[kS], const float (&h)[kS]) {
 #pragma unroll
-    for (int k = 0; k < kS; ++k) h[k] = 0.0f;
-  const float Dd = in.D != nullptr ? in.D[p.d] : 0.0f;
-  const float bias = in.dt_bias != nullptr ? in.dt_bias[p.d] : 0.0f;
-  for (int64_t t = 0; t < in.len; ++t) {
-    if (checkpoints != nullptr && t % kCheckpoint == 0 && p.live) {
-      float* q = checkpoints + ((p.b * n_check + t / kCheckpoint) * in.dim + p.d) * in.N;
-#pragma unroll
-      for (int k = 0; k < kS; ++k)
-        if (n0 + k < in.N) q[n0 + k] = h[k];
-    }
-    float o = 0.0f;
-    if (t < len) {
-      float B[kS], C[kS];
-      load_states(in.B + p.b * in.Bbs + t * in.Bts + (int64_t)p.group * in.N, n0, in.N, B);
-      load_states(in.C + p.b * in.Cbs + t * in.Cts + (int64_t)p.group * in.N, n0, in.N, C);
-      const float u = to_f32(in.u[p.b * in.ubs + t * in.uts + p.d]);
-      float delta = to_f32(in.dt[p.b * in.dbs + t * in.dts + p.d]) + bias;
-      if (in.softplus) delta = softplus(delta);
-      float acc = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kS; ++k) {
-        h[k] = fmaf(exp2_decay(delta * (A[k] * kLog2e)), h[k], delta * u * B[k]);
-        acc = fmaf(C[k], h[k], acc);
-      }
-      o = fmaf(Dd, u, sum_lanes<G>(acc));
-      if (in.z != nullptr) {
-        const float z = to_f32(in.z[p.b * in.zbs + t * in.zts + p.d]);
-        o *= z * sigmoid(z);
-      }
-    }
-    if (p.live && p.g == 0) y[p.b * ybs + t * yts + p.d] = from_f32<T>(o);
+  for (int j = 0; j < 2; ++j) {
+    l.A[j] = pack2(A[2 * j] * kLog2e, A[2 * j + 1] * kLog2e);
+    l.h[j] = pack2(h[2 * j], h[2 * j + 1]);
   }
-  if (final_state != nullptr && p.live) {
+}
+
+__device__ __forceinline__ void lane_states(const Lane& l, float (&h)[kS]) {
+  unpack2(l.h[0], h[0], h[1]);
+  unpack2(l.h[1], h[2], h[3]);
+}
+
+// h = exp(delta A) h + (delta u) B, with delta and delta u given twice.
+__device__ __forceinline__ void lane_step(Lane& l, F2 delta, F2 du, F2 B0, F2 B1) {
+  const F2 B[2] = {B0, B1};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float x0, x1;
+    unpack2(mul2(delta, l.A[j]), x0, x1);
+    l.h[j] = fma2(pack2(exp2_decay(x0), exp2_decay(x1)), l.h[j], mul2(du, B[j]));
+  }
+}
+
+// This lane's part of C.h: (C0 h0 + C2 h2) + (C1 h1 + C3 h3).
+__device__ __forceinline__ float lane_dot(const Lane& l, F2 C0, F2 C1) {
+  float lo, hi;
+  unpack2(fma2(C1, l.h[1], mul2(C0, l.h[0])), lo, hi);
+  return lo + hi;
+}
+
+// Sums of four values over the G lanes of a channel, as a tree over the lane
+// numbers. Halving exchanges: lane g ends with value 2 (g & 1) + (g >> 1 & 1)
+// (G = 2: with two of them, G = 1: all four), at 3 shuffles for 4 values.
+template <int G>
+__device__ __forceinline__ void sum_lanes4(float (&v)[4], int g) {
+  if (G >= 2) {
+    const bool up = g & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float keep = up ? v[i + 2] : v[i], send = up ? v[i] : v[i + 2];
+      v[i] = keep + __shfl_xor_sync(~0u, send, 1);
+    }
+  }
+  if (G >= 4) {
+    const bool up = g & 2;
+    const float keep = up ? v[1] : v[0], send = up ? v[0] : v[1];
+    v[0] = keep + __shfl_xor_sync(~0u, send, 2);
+  }
+#pragma unroll
+  for (int s = 4; s < G; s *= 2) v[0] += __shfl_xor_sync(~0u, v[0], s);
+}
+
+// A block's time tile. The elements of u, dt, z and y are handled by all
+// threads, VE neighbouring channels at a time; the recurrence by G lanes a
+// channel.
+template <class T, int G>
+struct Tile {
+  static constexpr int CH = kScanThreads / G;        // channels of a block
+  static constexpr int TT = G == 1 ? 16 : 32;        // steps of a tile
+  static constexpr int E = TT * CH / kScanThreads;   // elements a thread
+  static constexpr int W = 16 / (int)sizeof(T);
+  static constexpr int VE = E < W ? E : W;           // channels of an access
+  static constexpr int NV = CH / VE;                 // accesses a row
+  static constexpr int NL = E / VE;                  // accesses a thread
+  static constexpr int NP = G * kS;                  // states, padded
+  static constexpr int NBC = (TT * G + kScanThreads - 1) / kScanThreads;
+  static constexpr int YS = CH + (G >= 4 ? 8 : 0);   // row of the y tile: 4 rows, 4 bank groups
+  static_assert(TT % 4 == 0 && kCheckpoint % 4 == 0 && TT % kCheckpoint == 0, "tile");
+
+  // Where channel c of row t stands in a row of (delta, delta, du, du)
+  // quadruples: the 16-byte pieces of a vector are permuted so that the
+  // threads that write at once, and the lanes that read a step, meet
+  // different banks.
+  static __device__ __forceinline__ int slot(int t, int c) {
+    const int v = c / VE, i = t * NV + v;
+    const int f = VE == 8 ? (i & 7) : VE == 4 ? (i >> 1 & 3) : 0;
+    return t * CH + v * VE + ((c % VE) ^ f);
+  }
+};
+
+// A tensor's rows as accesses of a tile see them.
+template <class T>
+struct Rows {
+  const T* p;   // row 0 of the sequence at the block's first channel
+  int64_t ts;
+  bool wide;
+};
+
+// Reads rows [t0, t0 + TT) of the tile into registers; rows at or past `end`
+// are zero and not read.
+template <class TL, class T>
+__device__ __forceinline__ void tile_load(const Rows<T>& r, int64_t t0, int64_t end, int channels,
+                                          Pack<T, TL::VE> (&out)[TL::NL]) {
+#pragma unroll
+  for (int i = 0; i < TL::NL; ++i) {
+    const int idx = i * kScanThreads + threadIdx.x;
+    const int64_t t = t0 + idx / TL::NV;
+    const int c = idx % TL::NV * TL::VE;
+    const T* p = r.p + t * r.ts + c;
+    if (t < end && r.wide && c + TL::VE <= channels) {
+      out[i] = *reinterpret_cast<const Pack<T, TL::VE>*>(p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < TL::VE; ++k)
+        out[i].v[k] = (t < end && c + k < channels) ? p[k] : from_f32<T>(0.0f);
+    }
+  }
+}
+
+// The same for B or C: four states of a step at a time.
+template <class TL, class T>
+__device__ __forceinline__ void tile_load_states(const Rows<T>& r, int64_t t0, int64_t end, int N,
+                                                 Pack<T, kS> (&out)[TL::NBC]) {
+  constexpr int G = TL::NP / kS;
+#pragma unroll
+  for (int i = 0; i < TL::NBC; ++i) {
+    const int idx = i * kScanThreads + threadIdx.x;
+    const int64_t t = t0 + idx / G;
+    const int n = idx % G * kS;
+    const T* p = r.p + t * r.ts + n;
+    const bool in = idx < TL::TT * G && t < end;
+    if (in && r.wide && n + kS <= N) {
+      out[i] = *reinterpret_cast<const Pack<T, kS>*>(p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kS; ++k) out[i].v[k] = (in && n + k < N) ? p[k] : from_f32<T>(0.0f);
+    }
+  }
+}
+
+template <class TL, class T>
+__device__ __forceinline__ void tile_put_states(const Pack<T, kS> (&in)[TL::NBC], float* tile) {
+  constexpr int G = TL::NP / kS;
+#pragma unroll
+  for (int i = 0; i < TL::NBC; ++i) {
+    const int idx = i * kScanThreads + threadIdx.x;
+    if (idx < TL::TT * G)
+      reinterpret_cast<float4*>(tile)[idx] = make_float4(to_f32(in[i].v[0]), to_f32(in[i].v[1]),
+                                                         to_f32(in[i].v[2]), to_f32(in[i].v[3]));
+  }
+}
+
+// Sequences with few channels are cut into segments that run side by side:
+// a first launch (kStates) takes every segment but the last from a zero state
+// to its end and its sum of delta, the second starts a segment from the
+// state that these give, H' = exp(A sum delta) H + E in segment order.
+struct Segments {
+  int64_t count, len;
+  float* E;     // [count - 1][batch][dim][NP]
+  float* sum;   // [count - 1][batch][dim]
+};
+
+template <class T>
+struct ScanOut {
+  T* y;
+  int64_t ybs, yts;
+  float* final_state;
+  float* checkpoints;
+  int64_t n_check;
+  bool wide, wide_y, wide_BC;
+};
+
+template <class T, int G, bool kStates>
+__global__ void __launch_bounds__(kScanThreads)
+selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
+  using TL = Tile<T, G>;
+  __shared__ float4 dd[TL::TT * TL::CH];
+  __shared__ __align__(16) float Bs[TL::TT * TL::NP];
+  __shared__ __align__(16) float Cs[kStates ? 4 : TL::TT * TL::NP];
+  __shared__ __align__(16) float ys[kStates ? 4 : TL::TT * TL::YS];
+  __shared__ __align__(16) float Ds[TL::CH], biases[TL::CH];
+
+  const int tid = threadIdx.x, g = tid % G, c = tid / G, n0 = g * kS;
+  const int64_t per_group = (in.group_dim + TL::CH - 1) / TL::CH;
+  int64_t i = blockIdx.x;
+  const int64_t blk = i % (per_group * in.groups);
+  i /= per_group * in.groups;
+  const int64_t seg = i % (kStates ? sg.count - 1 : sg.count), b = i / (kStates ? sg.count - 1 : sg.count);
+  const int64_t group = blk / per_group, first = blk % per_group * TL::CH;
+  const int channels = (int)min((int64_t)TL::CH, in.group_dim - first);
+  const int64_t d0 = group * in.group_dim + first;
+  const bool live = c < channels;
+  const int64_t d = d0 + (live ? c : 0);
+  const int64_t len = sequence_length(in.lengths, in.index_bytes, b, in.len);
+  const int64_t begin = seg * sg.len, end = min(in.len, begin + sg.len), stop = min(len, end);
+
+  if (tid < TL::CH) {
+    Ds[tid] = (in.D != nullptr && tid < channels) ? in.D[d0 + tid] : 0.0f;
+    biases[tid] = (in.dt_bias != nullptr && tid < channels) ? in.dt_bias[d0 + tid] : 0.0f;
+  }
+  Lane l;
+  {
+    float A[kS], h[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
+    load_states(in.A + d * in.N, n0, in.N, A);
+    if (!kStates && in.state != nullptr)
+      load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
+    lane_init(l, A, h);
+    if (!kStates) {
+      const float* E = sg.E + (b * in.dim + d) * TL::NP + n0;
+      const float* sum = sg.sum + b * in.dim + d;
+#pragma unroll 4
+      for (int64_t s = 0; s < seg; ++s) {
+        const float4 e = *reinterpret_cast<const float4*>(E + s * in.batch * in.dim * TL::NP);
+        const float x = sum[s * in.batch * in.dim];
+        const F2 ee[2] = {pack2(e.x, e.y), pack2(e.z, e.w)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x0, x1;
+          unpack2(mul2(pack2(x, x), l.A[j]), x0, x1);
+          l.h[j] = fma2(pack2(exp2_decay(x0), exp2_decay(x1)), l.h[j], ee[j]);
+        }
+      }
+    }
+  }
+
+  const Rows<T> ru = {in.u + b * in.ubs + d0, in.uts, out.wide};
+  const Rows<T> rd = {in.dt + b * in.dbs + d0, in.dts, out.wide};
+  const Rows<T> rz = {in.z + b * in.zbs + d0, in.zts, out.wide};
+  const Rows<T> rB = {in.B + b * in.Bbs + group * in.N, in.Bts, out.wide_BC};
+  const Rows<T> rC = {in.C + b * in.Cbs + group * in.N, in.Cts, out.wide_BC};
+  const bool gated = !kStates && in.z != nullptr;
+  Pack<T, TL::VE> pu[TL::NL], pd[TL::NL], pz[TL::NL];
+  Pack<T, kS> pB[TL::NBC], pC[TL::NBC];
+  auto load = [&](int64_t t0) {
+    tile_load<TL>(ru, t0, stop, channels, pu);
+    tile_load<TL>(rd, t0, stop, channels, pd);
+    if (gated) tile_load<TL>(rz, t0, stop, channels, pz);
+    tile_load_states<TL>(rB, t0, stop, in.N, pB);
+    if (!kStates) tile_load_states<TL>(rC, t0, stop, in.N, pC);
+  };
+  load(begin);
+  __syncthreads();  // Ds, biases
+  float total = 0.0f;
+
+  int64_t t0 = begin;
+  for (; t0 < stop; t0 += TL::TT) {
+    // elements: delta and delta u into the tile; u and z stay for the end
+    Pack<T, TL::VE> ku[TL::NL], kz[TL::NL];
+#pragma unroll
+    for (int i = 0; i < TL::NL; ++i) {
+      const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
+      const bool in_seq = t0 + t < stop;
+#pragma unroll
+      for (int k = 0; k < TL::VE; ++k) {
+        float delta = to_f32(pd[i].v[k]) + biases[c0 + k];
+        if (in.softplus) delta = softplus(delta);
+        delta = in_seq ? delta : 0.0f;
+        const float du = delta * to_f32(pu[i].v[k]);
+        dd[TL::slot(t, c0 + k)] = make_float4(delta, delta, du, du);
+      }
+      if (!kStates) ku[i] = pu[i];
+      if (gated) kz[i] = pz[i];
+    }
+    tile_put_states<TL>(pB, Bs);
+    if (!kStates) tile_put_states<TL>(pC, Cs);
+    __syncthreads();
+    if (t0 + TL::TT < stop) load(t0 + TL::TT);
+
+    // recurrence
+#pragma unroll 2
+    for (int t = 0; t < TL::TT; t += 4) {
+      if (!kStates && out.checkpoints != nullptr && t % kCheckpoint == 0 && live &&
+          t0 + t < end) {
+        float h[kS];
+        lane_states(l, h);
+        float* q = out.checkpoints +
+                   ((b * out.n_check + (t0 + t) / kCheckpoint) * in.dim + d) * in.N + n0;
+#pragma unroll
+        for (int k = 0; k < kS; ++k)
+          if (n0 + k < in.N) q[k] = h[k];
+      }
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const ulonglong2 e = reinterpret_cast<const ulonglong2*>(dd)[TL::slot(t + k, c)];
+        const ulonglong2 B = reinterpret_cast<const ulonglong2*>(Bs)[(t + k) * G + g];
+        lane_step(l, e.x, e.y, B.x, B.y);
+        if (!kStates) {
+          const ulonglong2 C = reinterpret_cast<const ulonglong2*>(Cs)[(t + k) * G + g];
+          v[k] = lane_dot(l, C.x, C.y);
+        } else {
+          float a, a2;
+          unpack2(e.x, a, a2);
+          total += a;
+        }
+      }
+      if (!kStates) {
+        sum_lanes4<G>(v, g);
+        if (G == 1) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ys[(t + k) * TL::YS + c] = v[k];
+        } else if (G == 2) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) ys[(t + 2 * g + k) * TL::YS + c] = v[k];
+        } else if (G == 4 || g < 4) {
+          ys[(t + 2 * (g & 1) + (g >> 1 & 1)) * TL::YS + c] = v[0];
+        }
+      }
+    }
+    __syncthreads();
+
+    // elements: D u, the gate, and out
+    if (!kStates) {
+#pragma unroll
+      for (int i = 0; i < TL::NL; ++i) {
+        const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
+        float f[TL::VE];
+        const bool in_seq = t0 + t < stop;
+#pragma unroll
+        for (int k = 0; k < TL::VE; ++k) {
+          float v = fmaf(Ds[c0 + k], to_f32(ku[i].v[k]), ys[t * TL::YS + c0 + k]);
+          if (gated) {
+            const float z = to_f32(kz[i].v[k]);
+            v *= z * sigmoid(z);
+          }
+          f[k] = in_seq ? v : 0.0f;
+        }
+        const int have = min(TL::VE, channels - c0);
+        if (t0 + t < end && have > 0)
+          store_f32<T, TL::VE>(out.y + b * out.ybs + (t0 + t) * out.yts + d0 + c0,
+                               out.wide_y && have == TL::VE, have, f);
+      }
+    }
+  }
+  if (kStates) {
+    if (live) {
+      float h[kS];
+      lane_states(l, h);
+      const int64_t row = (seg * in.batch + b) * in.dim + d;
+      *reinterpret_cast<float4*>(sg.E + row * TL::NP + n0) = make_float4(h[0], h[1], h[2], h[3]);
+      if (g == 0) sg.sum[row] = total;
+    }
+    return;
+  }
+  for (; t0 < end; t0 += TL::TT) {  // past the sequence's length
+#pragma unroll
+    for (int i = 0; i < TL::NL; ++i) {
+      const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
+      const int have = min(TL::VE, channels - c0);
+      float f[TL::VE];
+#pragma unroll
+      for (int k = 0; k < TL::VE; ++k) f[k] = 0.0f;
+      if (t0 + t < end && have > 0)
+        store_f32<T, TL::VE>(out.y + b * out.ybs + (t0 + t) * out.yts + d0 + c0,
+                             out.wide_y && have == TL::VE, have, f);
+    }
+  }
+  if (out.final_state != nullptr && seg == sg.count - 1 && live) {
+    float h[kS];
+    lane_states(l, h);
 #pragma unroll
     for (int k = 0; k < kS; ++k)
-      if (n0 + k < in.N) final_state[row + n0 + k] = h[k];
+      if (n0 + k < in.N) out.final_state[(b * in.dim + d) * in.N + n0 + k] = h[k];
   }
 }
 
@@ -313,12 +623,12 @@ selective_scan_step_kernel(ScanIn<T> in, float* __restrict__ state, int64_t stat
     float delta = to_f32(in.dt[p.b * in.dbs + p.d]);
     if (in.dt_bias != nullptr) delta += in.dt_bias[p.d];
     if (in.softplus) delta = softplus(delta);
-    float acc = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kS; ++k) {
-      h[k] = fmaf(exp2_decay(delta * (A[k] * kLog2e)), h[k], delta * u * B[k]);
-      acc = fmaf(C[k], h[k], acc);
-    }
+    const float du = delta * u;
+    Lane l;
+    lane_init(l, A, h);
+    lane_step(l, pack2(delta, delta), pack2(du, du), pack2(B[0], B[1]), pack2(B[2], B[3]));
+    const float acc = lane_dot(l, pack2(C[0], C[1]), pack2(C[2], C[3]));
+    lane_states(l, h);
     o = fmaf(in.D != nullptr ? in.D[p.d] : 0.0f, u, sum_lanes<G>(acc));
     if (in.z != nullptr) {
       const float z = to_f32(in.z[p.b * in.zbs + p.d]);
@@ -344,6 +654,31 @@ int64_t scan_blocks(int64_t batch, int64_t dim, int groups, int G) {
   const int64_t per_group = ceil_div(dim / groups, kScanThreads / G);
   const int64_t all = per_group * groups;
   return all > kMaxBlocks / (batch > 0 ? batch : 1) ? 0 : all * batch;
+}
+
+// How a call's sequences are cut. A rule on sizes alone, so that results do
+// not depend on the GPU.
+#ifndef CR_SCAN_WARPS
+#define CR_SCAN_WARPS 2432
+#endif
+#ifndef CR_SCAN_SPLIT_BELOW
+#define CR_SCAN_SPLIT_BELOW 700
+#endif
+Segments scan_segments(int64_t batch, int64_t len, int64_t dim, int lanes) {
+  constexpr int64_t kTile = 32;
+  Segments sg;
+  sg.E = sg.sum = nullptr;
+  sg.count = 1;
+  const int64_t warps = batch * ceil_div(dim * lanes, 32);
+  if (warps < CR_SCAN_SPLIT_BELOW && warps > 0 && len >= 8 * kTile) {
+    sg.count = CR_SCAN_WARPS / warps;
+    const int64_t most = len / (4 * kTile);
+    if (sg.count > most) sg.count = most;
+    if (sg.count > 64) sg.count = 64;
+  }
+  sg.len = len > 0 ? ceil_div(ceil_div(len, sg.count), kTile) * kTile : kTile;
+  sg.count = len > 0 ? ceil_div(len, sg.len) : 1;
+  return sg;
 }
 
 cr_status check_scan(const cr_selective_scan_args* a, bool step) {
@@ -428,8 +763,10 @@ int64_t cr_selective_scan_checkpoints(int64_t len) {
 
 size_t cr_selective_scan_workspace_bytes(int64_t batch, int64_t len, int64_t dim,
                                          int32_t dstate) {
+  using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || dstate < 1) return 0;
-  return 256;
+  const int64_t segs = scan_segments(batch, len, dim, scan_lanes(dstate)).count;
+  return round256((size_t)(segs - 1) * batch * dim * (scan_lanes(dstate) * kS + 1) * 4) + 256;
 }
 
 cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_batch_stride,
@@ -452,13 +789,38 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
   if (a->batch == 0 || a->dim == 0) return CR_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int lanes = scan_lanes(a->dstate);
-  const unsigned blocks = (unsigned)scan_blocks(a->batch, a->dim, a->groups, lanes);
-  const int64_t n_check = cr_selective_scan_checkpoints(a->len);
+  const int64_t blocks = scan_blocks(a->batch, a->dim, a->groups, lanes);
+  Segments sg = scan_segments(a->batch, a->len, a->dim, lanes);
+  if (blocks > kMaxBlocks / sg.count) return CR_ERR_UNSUPPORTED;
+  sg.E = static_cast<float*>(ws);
+  sg.sum = sg.E + (sg.count - 1) * a->batch * a->dim * lanes * kS;
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
+    using TL = Tile<T, G>;
+    const size_t bytes = TL::VE * es;
+    const bool group_ok = a->groups == 1 || (a->dim / a->groups) % TL::VE == 0;
+    ScanOut<T> out;
+    out.y = static_cast<T*>(y);
+    out.ybs = y_batch_stride;
+    out.yts = y_time_stride;
+    out.final_state = final_state;
+    out.checkpoints = checkpoints;
+    out.n_check = cr_selective_scan_checkpoints(a->len);
+    out.wide = group_ok && rows_aligned(a->u, a->u_batch_stride, a->u_time_stride, es, bytes) &&
+               rows_aligned(a->dt, a->dt_batch_stride, a->dt_time_stride, es, bytes) &&
+               (a->z == nullptr ||
+                rows_aligned(a->z, a->z_batch_stride, a->z_time_stride, es, bytes));
+    out.wide_y = group_ok && rows_aligned(y, y_batch_stride, y_time_stride, es, bytes);
+    out.wide_BC = a->dstate % kS == 0 &&
+                  rows_aligned(a->B, a->B_batch_stride, a->B_time_stride, es, kS * es) &&
+                  rows_aligned(a->C, a->C_batch_stride, a->C_time_stride, es, kS * es);
+    if (sg.count > 1)
+      CR_LAUNCH(kKSelectiveScanStates, s,
+                selective_scan_kernel<T, G, true>
+                <<<(unsigned)(blocks * (sg.count - 1)), kScanThreads, 0, s>>>(scan_in<T>(a), out,
+                                                                              sg));
     CR_LAUNCH(kKSelectiveScan, s,
-              selective_scan_kernel<T, G><<<blocks, kScanThreads, 0, s>>>(
-                  scan_in<T>(a), static_cast<T*>(y), y_batch_stride, y_time_stride, final_state,
-                  checkpoints, n_check));
+              selective_scan_kernel<T, G, false>
+              <<<(unsigned)(blocks * sg.count), kScanThreads, 0, s>>>(scan_in<T>(a), out, sg));
   }));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
