@@ -7,6 +7,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,6 +65,56 @@ __device__ __forceinline__ void store_f32(T* p, bool wide, int have, const float
   }
 }
 
+// V consecutive elements as they stand in memory, in 32-bit words: a load
+// into one of these is not waited for before its elements are used.
+template <class T, int V>
+struct Raw {
+  static constexpr int kWords = (V * (int)sizeof(T) + 3) / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+    const uint32_t q = w[k / 2];
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(k % 2 ? q & 0xFFFF0000u : q << 16);
+    else
+      return __half2float(__ushort_as_half((unsigned short)(k % 2 ? q >> 16 : q & 0xFFFFu)));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // wide: p is aligned to V elements, which all exist; otherwise `have` do,
+  // the rest are zero.
+  __device__ __forceinline__ void load(const T* p, bool wide, int have) {
+    if (wide) {
+      if constexpr (V * sizeof(T) == 16) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+      } else if constexpr (V * sizeof(T) == 8) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+        w[0] = q.x, w[1] = q.y;
+      } else if constexpr (V * sizeof(T) == 4) {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else {
+        w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+      }
+    } else {
+      zero();
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (k < have) {
+          if constexpr (sizeof(T) == 4)
+            w[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + k);
+          else
+            w[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + k)
+                        << (k % 2 * 16);
+        }
+      }
+    }
+  }
+};
+
 // An index of 4 or 8 bytes.
 __device__ __forceinline__ int64_t load_index(const void* p, int bytes, int64_t i) {
   return bytes == 8 ? static_cast<const int64_t*>(p)[i]
@@ -79,9 +130,26 @@ __device__ __forceinline__ int64_t sequence_length(const void* lengths, int byte
 }
 
 // ------------------------------------------------------ nonlinearities
+// 2^v, zero below 2^-126. The instruction's error is at most 1.4e-7 relative
+// on [-20, 0], its mean -5e-9 near 0 and -5e-8 from -1 on (measured over 2^20
+// points an interval).
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.44269504088896341f;
+
+// 1 / v for v >= 1 (infinity gives 0); one unit of error.
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // 1 / (1 + exp(-v)); 0 and 1 in the limits.
 __device__ __forceinline__ float sigmoid(float v) {
-  return __fdividef(1.0f, 1.0f + __expf(-v));
+  return reciprocal(1.0f + exp2_fast(v * -kLog2e));
 }
 
 // softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|). With
@@ -89,8 +157,8 @@ __device__ __forceinline__ float sigmoid(float v) {
 // ...): seven terms leave (1/9)^7 / 15 = 1.4e-8 of the value, and the result
 // keeps its relative accuracy where it is small (a few units of binary32).
 __device__ __forceinline__ float softplus(float v) {
-  const float e = __expf(-fabsf(v));
-  const float s = __fdividef(e, 2.0f + e);
+  const float e = exp2_fast(fabsf(v) * -kLog2e);
+  const float s = e * reciprocal(2.0f + e);
   const float w = s * s;
   float p = 1.0f / 13.0f;
   p = fmaf(p, w, 1.0f / 11.0f);
@@ -101,16 +169,6 @@ __device__ __forceinline__ float softplus(float v) {
   p = fmaf(p, w, 1.0f);
   return fmaf(s + s, p, fmaxf(v, 0.0f));
 }
-
-// 2^v of a decay (v <= 0 in use), zero below 2^-126. The instruction's error
-// is at most 1.4e-7 relative on [-20, 0], its mean -5e-9 near 0 and -5e-8
-// from -1 on (measured over 2^20 points an interval).
-__device__ __forceinline__ float exp2_decay(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-constexpr float kLog2e = 1.44269504088896341f;
 
 // ------------------------------------------------- pairs of binary32
 // Two binary32 values in one 64-bit register pair, for the packed

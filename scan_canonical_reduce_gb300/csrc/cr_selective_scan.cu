@@ -61,13 +61,6 @@ __device__ __forceinline__ Place place(int64_t group_dim, int groups) {
   return p;
 }
 
-template <int G>
-__device__ __forceinline__ float sum_lanes(float v) {
-#pragma unroll
-  for (int s = 1; s < G; s *= 2) v += __shfl_xor_sync(~0u, v, s);
-  return v;
-}
-
 template <class T>
 __device__ __forceinline__ void load_states(const T* p, int n0, int N, float (&f)[kS]) {
 #pragma unroll
@@ -100,7 +93,7 @@ __device__ __forceinline__ void lane_step(Lane& l, F2 delta, F2 du, F2 B0, F2 B1
   for (int j = 0; j < 2; ++j) {
     float x0, x1;
     unpack2(mul2(delta, l.A[j]), x0, x1);
-    l.h[j] = fma2(pack2(exp2_decay(x0), exp2_decay(x1)), l.h[j], mul2(du, B[j]));
+    l.h[j] = fma2(pack2(exp2_fast(x0), exp2_fast(x1)), l.h[j], mul2(du, B[j]));
   }
 }
 
@@ -111,26 +104,26 @@ __device__ __forceinline__ float lane_dot(const Lane& l, F2 C0, F2 C1) {
   return lo + hi;
 }
 
-// Sums of four values over the G lanes of a channel, as a tree over the lane
-// numbers. Halving exchanges: lane g ends with value 2 (g & 1) + (g >> 1 & 1)
-// (G = 2: with two of them, G = 1: all four), at 3 shuffles for 4 values.
+// The sum over the G lanes of a channel: lanes g, g + 4, g + 8, ... first,
+// which leaves four partial sums, then (p0 + p1) + (p2 + p3).
 template <int G>
-__device__ __forceinline__ void sum_lanes4(float (&v)[4], int g) {
-  if (G >= 2) {
-    const bool up = g & 1;
+__device__ __forceinline__ float partial_lanes(float v) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float keep = up ? v[i + 2] : v[i], send = up ? v[i] : v[i + 2];
-      v[i] = keep + __shfl_xor_sync(~0u, send, 1);
-    }
-  }
-  if (G >= 4) {
-    const bool up = g & 2;
-    const float keep = up ? v[1] : v[0], send = up ? v[0] : v[1];
-    v[0] = keep + __shfl_xor_sync(~0u, send, 2);
-  }
+  for (int s = 4; s < G; s *= 2) v += __shfl_xor_sync(~0u, v, s);
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float sum_lanes(float v) {
+  v = partial_lanes<G>(v);
 #pragma unroll
-  for (int s = 4; s < G; s *= 2) v[0] += __shfl_xor_sync(~0u, v[0], s);
+  for (int s = 1; s < G && s < 4; s *= 2) v += __shfl_xor_sync(~0u, v, s);
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float sum_partials(float4 p) {
+  return G == 1 ? p.x : G == 2 ? p.x + p.y : (p.x + p.y) + (p.z + p.w);
 }
 
 // A block's time tile. The elements of u, dt, z and y are handled by all
@@ -139,7 +132,7 @@ __device__ __forceinline__ void sum_lanes4(float (&v)[4], int g) {
 template <class T, int G>
 struct Tile {
   static constexpr int CH = kScanThreads / G;        // channels of a block
-  static constexpr int TT = G == 1 ? 16 : 32;        // steps of a tile
+  static constexpr int TT = G <= 2 ? 16 : 32;        // steps of a tile
   static constexpr int E = TT * CH / kScanThreads;   // elements a thread
   static constexpr int W = 16 / (int)sizeof(T);
   static constexpr int VE = E < W ? E : W;           // channels of an access
@@ -147,17 +140,19 @@ struct Tile {
   static constexpr int NL = E / VE;                  // accesses a thread
   static constexpr int NP = G * kS;                  // states, padded
   static constexpr int NBC = (TT * G + kScanThreads - 1) / kScanThreads;
-  static constexpr int YS = CH + (G >= 4 ? 8 : 0);   // row of the y tile: 4 rows, 4 bank groups
   static_assert(TT % 4 == 0 && kCheckpoint % 4 == 0 && TT % kCheckpoint == 0, "tile");
 
-  // Where channel c of row t stands in a row of (delta, delta, du, du)
-  // quadruples: the 16-byte pieces of a vector are permuted so that the
-  // threads that write at once, and the lanes that read a step, meet
-  // different banks.
+  // Element (t, c) of the tile is a quadruple of floats: (delta, delta, du,
+  // du) for the recurrence, then the partial sums of y. The quadruples of an
+  // access are permuted so that the threads that write at once, and the lanes
+  // that read a step, meet different banks: quadruple k of access v in row t
+  // is at (t CH + v VE + k) ^ f, f < VE.
+  static __device__ __forceinline__ int flip(int t, int v) {
+    const int i = t * NV + v;
+    return VE == 8 ? (i & 7) : VE == 4 ? (i >> 1 & 3) : 0;
+  }
   static __device__ __forceinline__ int slot(int t, int c) {
-    const int v = c / VE, i = t * NV + v;
-    const int f = VE == 8 ? (i & 7) : VE == 4 ? (i >> 1 & 3) : 0;
-    return t * CH + v * VE + ((c % VE) ^ f);
+    return t * CH + (c ^ flip(t, c / VE));
   }
 };
 
@@ -173,53 +168,45 @@ struct Rows {
 // are zero and not read.
 template <class TL, class T>
 __device__ __forceinline__ void tile_load(const Rows<T>& r, int64_t t0, int64_t end, int channels,
-                                          Pack<T, TL::VE> (&out)[TL::NL]) {
+                                          Raw<T, TL::VE> (&out)[TL::NL]) {
 #pragma unroll
   for (int i = 0; i < TL::NL; ++i) {
     const int idx = i * kScanThreads + threadIdx.x;
     const int64_t t = t0 + idx / TL::NV;
     const int c = idx % TL::NV * TL::VE;
-    const T* p = r.p + t * r.ts + c;
-    if (t < end && r.wide && c + TL::VE <= channels) {
-      out[i] = *reinterpret_cast<const Pack<T, TL::VE>*>(p);
-    } else {
-#pragma unroll
-      for (int k = 0; k < TL::VE; ++k)
-        out[i].v[k] = (t < end && c + k < channels) ? p[k] : from_f32<T>(0.0f);
-    }
+    if (t < end)
+      out[i].load(r.p + t * r.ts + c, r.wide && c + TL::VE <= channels, channels - c);
+    else
+      out[i].zero();
   }
 }
 
 // The same for B or C: four states of a step at a time.
 template <class TL, class T>
 __device__ __forceinline__ void tile_load_states(const Rows<T>& r, int64_t t0, int64_t end, int N,
-                                                 Pack<T, kS> (&out)[TL::NBC]) {
+                                                 Raw<T, kS> (&out)[TL::NBC]) {
   constexpr int G = TL::NP / kS;
 #pragma unroll
   for (int i = 0; i < TL::NBC; ++i) {
     const int idx = i * kScanThreads + threadIdx.x;
     const int64_t t = t0 + idx / G;
     const int n = idx % G * kS;
-    const T* p = r.p + t * r.ts + n;
-    const bool in = idx < TL::TT * G && t < end;
-    if (in && r.wide && n + kS <= N) {
-      out[i] = *reinterpret_cast<const Pack<T, kS>*>(p);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kS; ++k) out[i].v[k] = (in && n + k < N) ? p[k] : from_f32<T>(0.0f);
-    }
+    if (idx < TL::TT * G && t < end)
+      out[i].load(r.p + t * r.ts + n, r.wide && n + kS <= N, N - n);
+    else
+      out[i].zero();
   }
 }
 
 template <class TL, class T>
-__device__ __forceinline__ void tile_put_states(const Pack<T, kS> (&in)[TL::NBC], float* tile) {
+__device__ __forceinline__ void tile_put_states(const Raw<T, kS> (&in)[TL::NBC], float* tile) {
   constexpr int G = TL::NP / kS;
 #pragma unroll
   for (int i = 0; i < TL::NBC; ++i) {
     const int idx = i * kScanThreads + threadIdx.x;
     if (idx < TL::TT * G)
-      reinterpret_cast<float4*>(tile)[idx] = make_float4(to_f32(in[i].v[0]), to_f32(in[i].v[1]),
-                                                         to_f32(in[i].v[2]), to_f32(in[i].v[3]));
+      reinterpret_cast<float4*>(tile)[idx] =
+          make_float4(in[i].get(0), in[i].get(1), in[i].get(2), in[i].get(3));
   }
 }
 
@@ -243,14 +230,16 @@ struct ScanOut {
   bool wide, wide_y, wide_BC;
 };
 
+#ifndef CR_SCAN_BLOCKS
+#define CR_SCAN_BLOCKS 4
+#endif
 template <class T, int G, bool kStates>
-__global__ void __launch_bounds__(kScanThreads)
+__global__ void __launch_bounds__(kScanThreads, CR_SCAN_BLOCKS)
 selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
   using TL = Tile<T, G>;
   __shared__ float4 dd[TL::TT * TL::CH];
   __shared__ __align__(16) float Bs[TL::TT * TL::NP];
   __shared__ __align__(16) float Cs[kStates ? 4 : TL::TT * TL::NP];
-  __shared__ __align__(16) float ys[kStates ? 4 : TL::TT * TL::YS];
   __shared__ __align__(16) float Ds[TL::CH], biases[TL::CH];
 
   const int tid = threadIdx.x, g = tid % G, c = tid / G, n0 = g * kS;
@@ -290,7 +279,7 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
         for (int j = 0; j < 2; ++j) {
           float x0, x1;
           unpack2(mul2(pack2(x, x), l.A[j]), x0, x1);
-          l.h[j] = fma2(pack2(exp2_decay(x0), exp2_decay(x1)), l.h[j], ee[j]);
+          l.h[j] = fma2(pack2(exp2_fast(x0), exp2_fast(x1)), l.h[j], ee[j]);
         }
       }
     }
@@ -302,8 +291,8 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
   const Rows<T> rB = {in.B + b * in.Bbs + group * in.N, in.Bts, out.wide_BC};
   const Rows<T> rC = {in.C + b * in.Cbs + group * in.N, in.Cts, out.wide_BC};
   const bool gated = !kStates && in.z != nullptr;
-  Pack<T, TL::VE> pu[TL::NL], pd[TL::NL], pz[TL::NL];
-  Pack<T, kS> pB[TL::NBC], pC[TL::NBC];
+  Raw<T, TL::VE> pu[TL::NL], pd[TL::NL], pz[TL::NL];
+  Raw<T, kS> pB[TL::NBC], pC[TL::NBC];
   auto load = [&](int64_t t0) {
     tile_load<TL>(ru, t0, stop, channels, pu);
     tile_load<TL>(rd, t0, stop, channels, pd);
@@ -318,18 +307,25 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
   int64_t t0 = begin;
   for (; t0 < stop; t0 += TL::TT) {
     // elements: delta and delta u into the tile; u and z stay for the end
-    Pack<T, TL::VE> ku[TL::NL], kz[TL::NL];
+    Raw<T, TL::VE> ku[TL::NL], kz[TL::NL];
 #pragma unroll
     for (int i = 0; i < TL::NL; ++i) {
       const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
       const bool in_seq = t0 + t < stop;
+      const int at = TL::slot(t, c0) * 16;
+      float delta[TL::VE];
+#pragma unroll
+      for (int k = 0; k < TL::VE; ++k) delta[k] = pd[i].get(k) + biases[c0 + k];
+      if (in.softplus) {
+#pragma unroll
+        for (int k = 0; k < TL::VE; ++k) delta[k] = softplus(delta[k]);
+      }
 #pragma unroll
       for (int k = 0; k < TL::VE; ++k) {
-        float delta = to_f32(pd[i].v[k]) + biases[c0 + k];
-        if (in.softplus) delta = softplus(delta);
-        delta = in_seq ? delta : 0.0f;
-        const float du = delta * to_f32(pu[i].v[k]);
-        dd[TL::slot(t, c0 + k)] = make_float4(delta, delta, du, du);
+        const float dt = in_seq ? delta[k] : 0.0f;
+        const float du = dt * pu[i].get(k);
+        *reinterpret_cast<float4*>(reinterpret_cast<char*>(dd) + (at ^ (k * 16))) =
+            make_float4(dt, dt, du, du);
       }
       if (!kStates) ku[i] = pu[i];
       if (gated) kz[i] = pz[i];
@@ -341,7 +337,8 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
 
     // recurrence
 #pragma unroll 2
-    for (int t = 0; t < TL::TT; t += 4) {
+    for (int t4 = 0; t4 < TL::TT / 4; ++t4) {
+      const int t = t4 * 4;
       if (!kStates && out.checkpoints != nullptr && t % kCheckpoint == 0 && live &&
           t0 + t < end) {
         float h[kS];
@@ -360,7 +357,7 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
         lane_step(l, e.x, e.y, B.x, B.y);
         if (!kStates) {
           const ulonglong2 C = reinterpret_cast<const ulonglong2*>(Cs)[(t + k) * G + g];
-          v[k] = lane_dot(l, C.x, C.y);
+          v[k] = partial_lanes<G>(lane_dot(l, C.x, C.y));
         } else {
           float a, a2;
           unpack2(e.x, a, a2);
@@ -368,16 +365,10 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
         }
       }
       if (!kStates) {
-        sum_lanes4<G>(v, g);
-        if (G == 1) {
+        __syncwarp();  // the lanes of a channel have read what they overwrite
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ys[(t + k) * TL::YS + c] = v[k];
-        } else if (G == 2) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) ys[(t + 2 * g + k) * TL::YS + c] = v[k];
-        } else if (G == 4 || g < 4) {
-          ys[(t + 2 * (g & 1) + (g >> 1 & 1)) * TL::YS + c] = v[0];
-        }
+        for (int k = 0; k < 4; ++k)
+          if (G <= 4 || g < 4) reinterpret_cast<float*>(dd)[TL::slot(t + k, c) * 4 + g] = v[k];
       }
     }
     __syncthreads();
@@ -387,13 +378,16 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
 #pragma unroll
       for (int i = 0; i < TL::NL; ++i) {
         const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
+        const int at = TL::slot(t, c0) * 16;
         float f[TL::VE];
         const bool in_seq = t0 + t < stop;
 #pragma unroll
         for (int k = 0; k < TL::VE; ++k) {
-          float v = fmaf(Ds[c0 + k], to_f32(ku[i].v[k]), ys[t * TL::YS + c0 + k]);
+          const float4 p = *reinterpret_cast<const float4*>(reinterpret_cast<const char*>(dd) +
+                                                            (at ^ (k * 16)));
+          float v = fmaf(Ds[c0 + k], ku[i].get(k), sum_partials<G>(p));
           if (gated) {
-            const float z = to_f32(kz[i].v[k]);
+            const float z = kz[i].get(k);
             v *= z * sigmoid(z);
           }
           f[k] = in_seq ? v : 0.0f;
@@ -487,7 +481,7 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o, int64_t n_check) {
         if (in.softplus) delta = softplus(delta);
 #pragma unroll
         for (int k = 0; k < kS; ++k)
-          h[i + 1][k] = fmaf(exp2_decay(delta * (A[k] * kLog2e)), h[i][k], delta * u * B[k]);
+          h[i + 1][k] = fmaf(exp2_fast(delta * (A[k] * kLog2e)), h[i][k], delta * u * B[k]);
       }
     }
 #pragma unroll
@@ -521,7 +515,7 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o, int64_t n_check) {
           dC[k] = pt * h[i + 1][k];
           dB[k] = g * (delta * u);
           gB = fmaf(g, B[k], gB);
-          carry[k] = g * exp2_decay(delta * (A[k] * kLog2e));
+          carry[k] = g * exp2_fast(delta * (A[k] * kLog2e));
           const float q = carry[k] * h[i][k];
           dA[k] = fmaf(q, delta, dA[k]);
           qA = fmaf(q, A[k], qA);
