@@ -152,24 +152,6 @@ __device__ __forceinline__ float sigmoid(float v) {
   return reciprocal(1.0f + exp2_fast(v * -kLog2e));
 }
 
-// softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|). With
-// s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 +
-// ...): seven terms leave (1/9)^7 / 15 = 1.4e-8 of the value, and the result
-// keeps its relative accuracy where it is small (a few units of binary32).
-__device__ __forceinline__ float softplus(float v) {
-  const float e = exp2_fast(fabsf(v) * -kLog2e);
-  const float s = e * reciprocal(2.0f + e);
-  const float w = s * s;
-  float p = 1.0f / 13.0f;
-  p = fmaf(p, w, 1.0f / 11.0f);
-  p = fmaf(p, w, 1.0f / 9.0f);
-  p = fmaf(p, w, 1.0f / 7.0f);
-  p = fmaf(p, w, 1.0f / 5.0f);
-  p = fmaf(p, w, 1.0f / 3.0f);
-  p = fmaf(p, w, 1.0f);
-  return fmaf(s + s, p, fmaxf(v, 0.0f));
-}
-
 // ------------------------------------------------- pairs of binary32
 // Two binary32 values in one 64-bit register pair, for the packed
 // arithmetic (one issue for two operations, each rounded to nearest).
@@ -196,6 +178,31 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), of two
+// values. With s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3
+// + s^4/5 + ...): seven terms leave (1/9)^7 / 15 = 1.4e-8 of the value, and
+// the result keeps its relative accuracy where it is small (a few units of
+// binary32).
+__device__ __forceinline__ void softplus2(float& v0, float& v1) {
+  const float e0 = exp2_fast(fabsf(v0) * -kLog2e), e1 = exp2_fast(fabsf(v1) * -kLog2e);
+  const F2 s = mul2(pack2(e0, e1), pack2(reciprocal(2.0f + e0), reciprocal(2.0f + e1)));
+  const F2 w = mul2(s, s);
+  F2 p = pack2(1.0f / 13.0f, 1.0f / 13.0f);
+  p = fma2(p, w, pack2(1.0f / 11.0f, 1.0f / 11.0f));
+  p = fma2(p, w, pack2(1.0f / 9.0f, 1.0f / 9.0f));
+  p = fma2(p, w, pack2(1.0f / 7.0f, 1.0f / 7.0f));
+  p = fma2(p, w, pack2(1.0f / 5.0f, 1.0f / 5.0f));
+  p = fma2(p, w, pack2(1.0f / 3.0f, 1.0f / 3.0f));
+  p = fma2(p, w, pack2(1.0f, 1.0f));
+  unpack2(fma2(add2(s, s), p, pack2(fmaxf(v0, 0.0f), fmaxf(v1, 0.0f))), v0, v1);
+}
+
+__device__ __forceinline__ float softplus(float v) {
+  float v1 = v;
+  softplus2(v, v1);
+  return v;
 }
 
 // ------------------------------------------------------------ host side

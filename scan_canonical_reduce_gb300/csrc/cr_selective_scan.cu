@@ -36,6 +36,36 @@ struct ScanIn {
   int index_bytes;
 };
 
+template <class T>
+__device__ __forceinline__ void load_states(const T* p, int n0, int N, float (&f)[kS]) {
+#pragma unroll
+  for (int k = 0; k < kS; ++k) f[k] = n0 + k < N ? to_f32(p[n0 + k]) : 0.0f;
+}
+
+// A lane's states in a row of N floats; wide: N % 4 == 0 and 16-byte rows.
+__device__ __forceinline__ void store_states(float* p, int n0, int N, bool wide,
+                                             const float (&f)[kS]) {
+  if (wide) {
+    if (n0 < N) *reinterpret_cast<float4*>(p + n0) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kS; ++k)
+      if (n0 + k < N) p[n0 + k] = f[k];
+  }
+}
+
+// Lanes of a warp: lane = g (32 / G) + c, so that neighbouring lanes read the
+// same B and C (a 16-byte shared load takes 2 cycles where lane pairs agree
+// and 4 where they do not).
+template <int G>
+struct Lanes {
+  static constexpr int kChannels = 32 / G;  // of a warp
+  __device__ static __forceinline__ int g() { return (threadIdx.x % 32) / kChannels; }
+  __device__ static __forceinline__ int c() {
+    return threadIdx.x / 32 * kChannels + threadIdx.x % kChannels;
+  }
+};
+
 // A block's channels lie in one group: block i of a sequence is block
 // i % per_group of group i / per_group.
 struct Place {
@@ -53,161 +83,162 @@ __device__ __forceinline__ Place place(int64_t group_dim, int groups) {
   const int64_t blk = i % (per_group * groups);
   p.b = i / (per_group * groups);
   p.group = (int)(blk / per_group);
-  p.c = threadIdx.x / G;
-  p.g = threadIdx.x % G;
+  p.c = Lanes<G>::c();
+  p.g = Lanes<G>::g();
   const int64_t in_group = blk % per_group * CH + p.c;
   p.live = in_group < group_dim;
   p.d = p.group * group_dim + (p.live ? in_group : 0);
   return p;
 }
 
-template <class T>
-__device__ __forceinline__ void load_states(const T* p, int n0, int N, float (&f)[kS]) {
-#pragma unroll
-  for (int k = 0; k < kS; ++k) f[k] = n0 + k < N ? to_f32(p[n0 + k]) : 0.0f;
-}
-
-// One lane's four states of a channel: decays and states as two pairs.
-struct Lane {
-  F2 A[2];  // A log2(e)
-  F2 h[2];
-};
-
-__device__ __forceinline__ void lane_init(Lane& l, const float (&A)[kS], const float (&h)[kS]) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    l.A[j] = pack2(A[2 * j] * kLog2e, A[2 * j + 1] * kLog2e);
-    l.h[j] = pack2(h[2 * j], h[2 * j + 1]);
-  }
-}
-
-__device__ __forceinline__ void lane_states(const Lane& l, float (&h)[kS]) {
-  unpack2(l.h[0], h[0], h[1]);
-  unpack2(l.h[1], h[2], h[3]);
-}
-
-// h = exp(delta A) h + (delta u) B, with delta and delta u given twice.
-__device__ __forceinline__ void lane_step(Lane& l, F2 delta, F2 du, F2 B0, F2 B1) {
-  const F2 B[2] = {B0, B1};
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float x0, x1;
-    unpack2(mul2(delta, l.A[j]), x0, x1);
-    l.h[j] = fma2(pack2(exp2_fast(x0), exp2_fast(x1)), l.h[j], mul2(du, B[j]));
-  }
-}
-
-// This lane's part of C.h: (C0 h0 + C2 h2) + (C1 h1 + C3 h3).
-__device__ __forceinline__ float lane_dot(const Lane& l, F2 C0, F2 C1) {
-  float lo, hi;
-  unpack2(fma2(C1, l.h[1], mul2(C0, l.h[0])), lo, hi);
-  return lo + hi;
-}
-
-// The sum over the G lanes of a channel: lanes g, g + 4, g + 8, ... first,
-// which leaves four partial sums, then (p0 + p1) + (p2 + p3).
+// The sum over the G lanes of a channel: as a tree over the bits of g from
+// bit 2 upwards, then bit 0, then bit 1. Two pairs of time steps at once: the
+// last two levels halve the values instead of repeating them, so that lane g
+// ends with step 2 (g & 1) + (g >> 1 & 1) in v[0] (G = 2: a pair in v[0..1],
+// G = 1: all four).
 template <int G>
-__device__ __forceinline__ float partial_lanes(float v) {
+__device__ __forceinline__ void sum_lanes4(F2 p0, F2 p1, int g, float (&v)[4]) {
+  constexpr int L = 32 / G;
+  unpack2(p0, v[0], v[1]);
+  unpack2(p1, v[2], v[3]);
 #pragma unroll
-  for (int s = 4; s < G; s *= 2) v += __shfl_xor_sync(~0u, v, s);
-  return v;
+  for (int s = 4; s < G; s *= 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(~0u, v[i], s * L);
+  if (G >= 2) {
+    const bool up = g & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float keep = up ? v[i + 2] : v[i], send = up ? v[i] : v[i + 2];
+      v[i] = keep + __shfl_xor_sync(~0u, send, L);
+    }
+  }
+  if (G >= 4) {
+    const bool up = g & 2;
+    const float keep = up ? v[1] : v[0], send = up ? v[0] : v[1];
+    v[0] = keep + __shfl_xor_sync(~0u, send, 2 * L);
+  }
 }
 
+// The same sum of one value, for every lane.
 template <int G>
 __device__ __forceinline__ float sum_lanes(float v) {
-  v = partial_lanes<G>(v);
+  constexpr int L = 32 / G;
 #pragma unroll
-  for (int s = 1; s < G && s < 4; s *= 2) v += __shfl_xor_sync(~0u, v, s);
+  for (int s = 4; s < G; s *= 2) v += __shfl_xor_sync(~0u, v, s * L);
+#pragma unroll
+  for (int s = 1; s < G && s < 4; s *= 2) v += __shfl_xor_sync(~0u, v, s * L);
   return v;
-}
-
-template <int G>
-__device__ __forceinline__ float sum_partials(float4 p) {
-  return G == 1 ? p.x : G == 2 ? p.x + p.y : (p.x + p.y) + (p.z + p.w);
 }
 
 // A block's time tile. The elements of u, dt, z and y are handled by all
-// threads, VE neighbouring channels at a time; the recurrence by G lanes a
-// channel.
-template <class T, int G>
+// threads, two steps of VE neighbouring channels at a time; the recurrence by
+// G lanes a channel, two steps at a time.
+template <class T, int G, int kSteps = (G <= 2 ? 16 : 32)>
 struct Tile {
-  static constexpr int CH = kScanThreads / G;        // channels of a block
-  static constexpr int TT = G <= 2 ? 16 : 32;        // steps of a tile
-  static constexpr int E = TT * CH / kScanThreads;   // elements a thread
+  static constexpr int CH = kScanThreads / G;         // channels of a block
+  static constexpr int TT = kSteps;                   // steps of a tile
+  static constexpr int TP = TT / 2;                   // pairs of steps
+  static constexpr int E = TP * CH / kScanThreads;    // pairs a thread
   static constexpr int W = 16 / (int)sizeof(T);
-  static constexpr int VE = E < W ? E : W;           // channels of an access
-  static constexpr int NV = CH / VE;                 // accesses a row
-  static constexpr int NL = E / VE;                  // accesses a thread
-  static constexpr int NP = G * kS;                  // states, padded
-  static constexpr int NBC = (TT * G + kScanThreads - 1) / kScanThreads;
-  static_assert(TT % 4 == 0 && kCheckpoint % 4 == 0 && TT % kCheckpoint == 0, "tile");
+  static constexpr int VE = E < 1 ? 1 : E < W ? E : W;  // channels of an access
+  static constexpr int NV = CH / VE;                  // accesses a row
+  static constexpr int ACC = TP * NV;                 // accesses of the tile
+  static constexpr int NL = (ACC + kScanThreads - 1) / kScanThreads;
+  static constexpr int NP = G * kS;                   // states, padded
+  static constexpr int ACC_BC = TP * G;
+  static constexpr int NBC = (ACC_BC + kScanThreads - 1) / kScanThreads;
+  static constexpr int YS = CH + 8;                   // row of the y tile, in floats
+  static_assert(TT % kCheckpoint == 0 && kCheckpoint % 4 == 0, "tile");
 
-  // Element (t, c) of the tile is a quadruple of floats: (delta, delta, du,
-  // du) for the recurrence, then the partial sums of y. The quadruples of an
-  // access are permuted so that the threads that write at once, and the lanes
-  // that read a step, meet different banks: quadruple k of access v in row t
-  // is at (t CH + v VE + k) ^ f, f < VE.
-  static __device__ __forceinline__ int flip(int t, int v) {
-    const int i = t * NV + v;
-    return VE == 8 ? (i & 7) : VE == 4 ? (i >> 1 & 3) : 0;
-  }
-  static __device__ __forceinline__ int slot(int t, int c) {
-    return t * CH + (c ^ flip(t, c / VE));
+  // Pair tp of channel c is a quadruple (delta, delta', du, du') of its two
+  // steps. The quadruples of an access are permuted within VE, so that eight
+  // threads that write at once meet different banks.
+  static __device__ __forceinline__ int slot(int tp, int c) {
+    constexpr int kGroup = VE < 8 ? 8 / VE : 1;
+    return tp * CH + (c ^ (c / VE / kGroup % VE));
   }
 };
 
-// A tensor's rows as accesses of a tile see them.
-template <class T>
+// A thread's accesses to a tensor's tiles: two rows of V elements each,
+// `PER_ROW` accesses a row and ALL a tile. `p` is where the first stands and
+// moves on by a tile.
+template <class T, int V, int NACC, int ALL, int PER_ROW>
 struct Rows {
-  const T* p;   // row 0 of the sequence at the block's first channel
-  int64_t ts;
+  const T* p;
+  int64_t ts, tile;  // elements between rows and between tiles
+  int have;          // elements of the access that exist, at most V
   bool wide;
+
+  // base: row 0 of the sequence at the block's first channel or state
+  __device__ __forceinline__ Rows(const T* base, int64_t ts_, int64_t t0, int tile_steps,
+                                  int elements, bool wide_) {
+    const int c = threadIdx.x % PER_ROW * V;
+    p = base + (t0 + threadIdx.x / PER_ROW * 2) * ts_ + c;
+    ts = ts_;
+    tile = tile_steps * ts_;
+    have = min(V, elements - c);
+    wide = wide_ && have == V;
+  }
+  // Reads the next tile into registers; rows at or past `left` are zero and
+  // not read.
+  __device__ __forceinline__ void load(int left, Raw<T, V> (&out)[NACC][2]) {
+#pragma unroll
+    for (int i = 0; i < NACC; ++i) {
+      const int t = (i * kScanThreads + threadIdx.x) / PER_ROW * 2;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (t + j < left && (ALL % kScanThreads == 0 || i * kScanThreads + threadIdx.x < ALL))
+          out[i][j].load(p + (i * (kScanThreads / PER_ROW) * 2 + j) * ts, wide, have);
+        else
+          out[i][j].zero();
+      }
+    }
+    p += tile;
+  }
 };
 
-// Reads rows [t0, t0 + TT) of the tile into registers; rows at or past `end`
-// are zero and not read.
+// B or C as pairs of steps: quadruples (n, n', n + 1, n' + 1).
 template <class TL, class T>
-__device__ __forceinline__ void tile_load(const Rows<T>& r, int64_t t0, int64_t end, int channels,
-                                          Raw<T, TL::VE> (&out)[TL::NL]) {
-#pragma unroll
-  for (int i = 0; i < TL::NL; ++i) {
-    const int idx = i * kScanThreads + threadIdx.x;
-    const int64_t t = t0 + idx / TL::NV;
-    const int c = idx % TL::NV * TL::VE;
-    if (t < end)
-      out[i].load(r.p + t * r.ts + c, r.wide && c + TL::VE <= channels, channels - c);
-    else
-      out[i].zero();
-  }
-}
-
-// The same for B or C: four states of a step at a time.
-template <class TL, class T>
-__device__ __forceinline__ void tile_load_states(const Rows<T>& r, int64_t t0, int64_t end, int N,
-                                                 Raw<T, kS> (&out)[TL::NBC]) {
-  constexpr int G = TL::NP / kS;
+__device__ __forceinline__ void tile_put_states(const Raw<T, kS> (&in)[TL::NBC][2], float4* tile) {
 #pragma unroll
   for (int i = 0; i < TL::NBC; ++i) {
     const int idx = i * kScanThreads + threadIdx.x;
-    const int64_t t = t0 + idx / G;
-    const int n = idx % G * kS;
-    if (idx < TL::TT * G && t < end)
-      out[i].load(r.p + t * r.ts + n, r.wide && n + kS <= N, N - n);
-    else
-      out[i].zero();
+    if (idx < TL::ACC_BC) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        tile[idx * 2 + k] = make_float4(in[i][0].get(2 * k), in[i][1].get(2 * k),
+                                        in[i][0].get(2 * k + 1), in[i][1].get(2 * k + 1));
+    }
   }
 }
 
-template <class TL, class T>
-__device__ __forceinline__ void tile_put_states(const Raw<T, kS> (&in)[TL::NBC], float* tile) {
-  constexpr int G = TL::NP / kS;
+// Two steps of a lane's four states: h' = a h + du B with a = exp2(delta A),
+// A holding log2(e) A twice, and where C is given the pair of C.h (a chain
+// over the four states).
+template <bool kDot>
+__device__ __forceinline__ F2 lane_steps(const F2 (&A)[kS], float (&h)[kS], const float4& e4,
+                                         const float4* Bq, const float4* Cq) {
+  const F2 delta = pack2(e4.x, e4.y), du = pack2(e4.z, e4.w);
+  F2 p = 0;
 #pragma unroll
-  for (int i = 0; i < TL::NBC; ++i) {
-    const int idx = i * kScanThreads + threadIdx.x;
-    if (idx < TL::TT * G)
-      reinterpret_cast<float4*>(tile)[idx] =
-          make_float4(in[i].get(0), in[i].get(1), in[i].get(2), in[i].get(3));
+  for (int j = 0; j < 2; ++j) {
+    const float4 B = Bq[j];
+    const float4 C = kDot ? Cq[j] : B;
+    const F2 Bn[2] = {pack2(B.x, B.y), pack2(B.z, B.w)};
+    const F2 Cn[2] = {pack2(C.x, C.y), pack2(C.z, C.w)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = 2 * j + i;
+      float x0, x1, b0, b1;
+      unpack2(mul2(delta, A[n]), x0, x1);
+      unpack2(mul2(du, Bn[i]), b0, b1);
+      const float h0 = fmaf(exp2_fast(x0), h[n], b0);
+      h[n] = fmaf(exp2_fast(x1), h0, b1);
+      if (kDot) p = n == 0 ? mul2(Cn[i], pack2(h0, h[n])) : fma2(Cn[i], pack2(h0, h[n]), p);
+    }
   }
+  return p;
 }
 
 // Sequences with few channels are cut into segments that run side by side:
@@ -227,27 +258,34 @@ struct ScanOut {
   float* final_state;
   float* checkpoints;
   int64_t n_check;
-  bool wide, wide_y, wide_BC;
+  bool wide, wide_y, wide_BC, wide_check;
 };
 
+#ifndef CR_SCAN_UNROLL
+#define CR_SCAN_UNROLL 2
+#endif
 #ifndef CR_SCAN_BLOCKS
 #define CR_SCAN_BLOCKS 4
 #endif
+constexpr int kUnroll = CR_SCAN_UNROLL;
 template <class T, int G, bool kStates>
 __global__ void __launch_bounds__(kScanThreads, CR_SCAN_BLOCKS)
 selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
   using TL = Tile<T, G>;
-  __shared__ float4 dd[TL::TT * TL::CH];
-  __shared__ __align__(16) float Bs[TL::TT * TL::NP];
-  __shared__ __align__(16) float Cs[kStates ? 4 : TL::TT * TL::NP];
+  constexpr int VE = TL::VE;
+  __shared__ float4 dd[TL::TP * TL::CH];
+  __shared__ float4 Bs[TL::ACC_BC * 2];
+  __shared__ float4 Cs[kStates ? 1 : TL::ACC_BC * 2];
+  __shared__ __align__(16) float ys[kStates ? 4 : TL::TT * TL::YS];
   __shared__ __align__(16) float Ds[TL::CH], biases[TL::CH];
 
-  const int tid = threadIdx.x, g = tid % G, c = tid / G, n0 = g * kS;
+  const int tid = threadIdx.x, g = Lanes<G>::g(), c = Lanes<G>::c(), n0 = g * kS;
   const int64_t per_group = (in.group_dim + TL::CH - 1) / TL::CH;
+  const int64_t segs = kStates ? sg.count - 1 : sg.count;
   int64_t i = blockIdx.x;
   const int64_t blk = i % (per_group * in.groups);
   i /= per_group * in.groups;
-  const int64_t seg = i % (kStates ? sg.count - 1 : sg.count), b = i / (kStates ? sg.count - 1 : sg.count);
+  const int64_t seg = i % segs, b = i / segs;
   const int64_t group = blk / per_group, first = blk % per_group * TL::CH;
   const int channels = (int)min((int64_t)TL::CH, in.group_dim - first);
   const int64_t d0 = group * in.group_dim + first;
@@ -260,174 +298,178 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
     Ds[tid] = (in.D != nullptr && tid < channels) ? in.D[d0 + tid] : 0.0f;
     biases[tid] = (in.dt_bias != nullptr && tid < channels) ? in.dt_bias[d0 + tid] : 0.0f;
   }
-  Lane l;
+  F2 A[kS];
+  float h[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
   {
-    float A[kS], h[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
-    load_states(in.A + d * in.N, n0, in.N, A);
-    if (!kStates && in.state != nullptr)
-      load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
-    lane_init(l, A, h);
-    if (!kStates) {
-      const float* E = sg.E + (b * in.dim + d) * TL::NP + n0;
-      const float* sum = sg.sum + b * in.dim + d;
-#pragma unroll 4
-      for (int64_t s = 0; s < seg; ++s) {
-        const float4 e = *reinterpret_cast<const float4*>(E + s * in.batch * in.dim * TL::NP);
-        const float x = sum[s * in.batch * in.dim];
-        const F2 ee[2] = {pack2(e.x, e.y), pack2(e.z, e.w)};
+    float a[kS];
+    load_states(in.A + d * in.N, n0, in.N, a);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x0, x1;
-          unpack2(mul2(pack2(x, x), l.A[j]), x0, x1);
-          l.h[j] = fma2(pack2(exp2_fast(x0), exp2_fast(x1)), l.h[j], ee[j]);
-        }
+    for (int k = 0; k < kS; ++k) A[k] = pack2(a[k] * kLog2e, a[k] * kLog2e);
+  }
+  if (!kStates) {
+    if (in.state != nullptr) load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
+    const float* E = sg.E + (b * in.dim + d) * TL::NP + n0;
+    const float* sum = sg.sum + b * in.dim + d;
+#pragma unroll 4
+    for (int64_t s = 0; s < seg; ++s) {
+      const float4 e4 = *reinterpret_cast<const float4*>(E + s * in.batch * in.dim * TL::NP);
+      const float x = sum[s * in.batch * in.dim], e[kS] = {e4.x, e4.y, e4.z, e4.w};
+#pragma unroll
+      for (int k = 0; k < kS; ++k) {
+        float a, a2;
+        unpack2(A[k], a, a2);
+        h[k] = fmaf(exp2_fast(x * a), h[k], e[k]);
       }
     }
   }
 
-  const Rows<T> ru = {in.u + b * in.ubs + d0, in.uts, out.wide};
-  const Rows<T> rd = {in.dt + b * in.dbs + d0, in.dts, out.wide};
-  const Rows<T> rz = {in.z + b * in.zbs + d0, in.zts, out.wide};
-  const Rows<T> rB = {in.B + b * in.Bbs + group * in.N, in.Bts, out.wide_BC};
-  const Rows<T> rC = {in.C + b * in.Cbs + group * in.N, in.Cts, out.wide_BC};
+  using RowsE = Rows<T, VE, TL::NL, TL::ACC, TL::NV>;
+  using RowsBC = Rows<T, kS, TL::NBC, TL::ACC_BC, G>;
+  static_assert(kScanThreads % TL::NV == 0, "a thread's accesses are of one column");
+  RowsE ru(in.u + b * in.ubs + d0, in.uts, begin, TL::TT, channels, out.wide);
+  RowsE rd(in.dt + b * in.dbs + d0, in.dts, begin, TL::TT, channels, out.wide);
+  RowsE rz(in.z + b * in.zbs + d0, in.zts, begin, TL::TT, channels, out.wide);
+  RowsBC rB(in.B + b * in.Bbs + group * in.N, in.Bts, begin, TL::TT, in.N, out.wide_BC);
+  RowsBC rC(in.C + b * in.Cbs + group * in.N, in.Cts, begin, TL::TT, in.N, out.wide_BC);
   const bool gated = !kStates && in.z != nullptr;
-  Raw<T, TL::VE> pu[TL::NL], pd[TL::NL], pz[TL::NL];
-  Raw<T, kS> pB[TL::NBC], pC[TL::NBC];
-  auto load = [&](int64_t t0) {
-    tile_load<TL>(ru, t0, stop, channels, pu);
-    tile_load<TL>(rd, t0, stop, channels, pd);
-    if (gated) tile_load<TL>(rz, t0, stop, channels, pz);
-    tile_load_states<TL>(rB, t0, stop, in.N, pB);
-    if (!kStates) tile_load_states<TL>(rC, t0, stop, in.N, pC);
+  Raw<T, VE> pu[TL::NL][2], pd[TL::NL][2], pz[TL::NL][2];
+  Raw<T, kS> pB[TL::NBC][2], pC[TL::NBC][2];
+  auto load = [&](int left) {
+    ru.load(left, pu);
+    rd.load(left, pd);
+    if (gated) rz.load(left, pz);
+    rB.load(left, pB);
+    if (!kStates) rC.load(left, pC);
   };
-  load(begin);
+  const int c0 = tid % TL::NV * VE;  // this thread's elements: channels c0 .. c0 + have
+  const int have = min(VE, channels - c0);
+  T* yp = out.y + b * out.ybs + (begin + tid / TL::NV * 2) * out.yts + d0 + c0;
+  load((int)min(stop - begin, (int64_t)TL::TT));
   __syncthreads();  // Ds, biases
-  float total = 0.0f;
+  F2 total = 0;
 
   int64_t t0 = begin;
   for (; t0 < stop; t0 += TL::TT) {
+    const int left = (int)min(stop - t0, (int64_t)TL::TT);
     // elements: delta and delta u into the tile; u and z stay for the end
-    Raw<T, TL::VE> ku[TL::NL], kz[TL::NL];
+    Raw<T, VE> ku[TL::NL][2], kz[TL::NL][2];
+    const Pack<float, VE> bias = *reinterpret_cast<const Pack<float, VE>*>(biases + c0);
 #pragma unroll
     for (int i = 0; i < TL::NL; ++i) {
-      const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
-      const bool in_seq = t0 + t < stop;
-      const int at = TL::slot(t, c0) * 16;
-      float delta[TL::VE];
+      const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
+      const int at = TL::slot(tp, c0) * 16;
+      const bool in0 = 2 * tp < left, in1 = 2 * tp + 1 < left;
 #pragma unroll
-      for (int k = 0; k < TL::VE; ++k) delta[k] = pd[i].get(k) + biases[c0 + k];
-      if (in.softplus) {
-#pragma unroll
-        for (int k = 0; k < TL::VE; ++k) delta[k] = softplus(delta[k]);
+      for (int k = 0; k < VE; ++k) {
+        float a = pd[i][0].get(k) + bias.v[k], a1 = pd[i][1].get(k) + bias.v[k];
+        if (in.softplus) softplus2(a, a1);
+        a = in0 ? a : 0.0f;
+        a1 = in1 ? a1 : 0.0f;
+        if (TL::ACC % kScanThreads == 0 || idx < TL::ACC)
+          *reinterpret_cast<float4*>(reinterpret_cast<char*>(dd) + (at ^ (k * 16))) =
+              make_float4(a, a1, a * pu[i][0].get(k), a1 * pu[i][1].get(k));
       }
 #pragma unroll
-      for (int k = 0; k < TL::VE; ++k) {
-        const float dt = in_seq ? delta[k] : 0.0f;
-        const float du = dt * pu[i].get(k);
-        *reinterpret_cast<float4*>(reinterpret_cast<char*>(dd) + (at ^ (k * 16))) =
-            make_float4(dt, dt, du, du);
+      for (int j = 0; j < 2; ++j) {
+        if (!kStates) ku[i][j] = pu[i][j];
+        if (gated) kz[i][j] = pz[i][j];
       }
-      if (!kStates) ku[i] = pu[i];
-      if (gated) kz[i] = pz[i];
     }
     tile_put_states<TL>(pB, Bs);
     if (!kStates) tile_put_states<TL>(pC, Cs);
     __syncthreads();
-    if (t0 + TL::TT < stop) load(t0 + TL::TT);
+    if (t0 + TL::TT < stop) load((int)min(stop - t0 - TL::TT, (int64_t)TL::TT));
 
     // recurrence
-#pragma unroll 2
+    const float4* dl = dd + TL::slot(0, c);
+    const float4 *Bl = Bs + 2 * g, *Cl = Cs + 2 * g;
+#pragma unroll kUnroll
     for (int t4 = 0; t4 < TL::TT / 4; ++t4) {
-      const int t = t4 * 4;
-      if (!kStates && out.checkpoints != nullptr && t % kCheckpoint == 0 && live &&
-          t0 + t < end) {
-        float h[kS];
-        lane_states(l, h);
-        float* q = out.checkpoints +
-                   ((b * out.n_check + (t0 + t) / kCheckpoint) * in.dim + d) * in.N + n0;
-#pragma unroll
-        for (int k = 0; k < kS; ++k)
-          if (n0 + k < in.N) q[k] = h[k];
+      if (!kStates && out.checkpoints != nullptr && t4 * 4 % kCheckpoint == 0 && live &&
+          t0 + t4 * 4 < end) {
+        store_states(out.checkpoints +
+                         ((b * out.n_check + (t0 + t4 * 4) / kCheckpoint) * in.dim + d) * in.N,
+                     n0, in.N, out.wide_check, h);
       }
-      float v[4];
+      F2 p[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const ulonglong2 e = reinterpret_cast<const ulonglong2*>(dd)[TL::slot(t + k, c)];
-        const ulonglong2 B = reinterpret_cast<const ulonglong2*>(Bs)[(t + k) * G + g];
-        lane_step(l, e.x, e.y, B.x, B.y);
-        if (!kStates) {
-          const ulonglong2 C = reinterpret_cast<const ulonglong2*>(Cs)[(t + k) * G + g];
-          v[k] = partial_lanes<G>(lane_dot(l, C.x, C.y));
-        } else {
-          float a, a2;
-          unpack2(e.x, a, a2);
-          total += a;
-        }
+      for (int j = 0; j < 2; ++j) {
+        const int tp = t4 * 2 + j;
+        const float4 e = dl[tp * TL::CH];
+        if (kStates) total = add2(total, pack2(e.x, e.y));
+        p[j] = lane_steps<!kStates>(A, h, e, Bl + tp * 2 * G, Cl + (kStates ? 0 : tp * 2 * G));
       }
       if (!kStates) {
-        __syncwarp();  // the lanes of a channel have read what they overwrite
+        float v[4];
+        sum_lanes4<G>(p[0], p[1], g, v);
+        float* y = ys + t4 * 4 * TL::YS + c;
+        if (G == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (G <= 4 || g < 4) reinterpret_cast<float*>(dd)[TL::slot(t + k, c) * 4 + g] = v[k];
+          for (int k = 0; k < 4; ++k) y[k * TL::YS] = v[k];
+        } else if (G == 2) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) y[(2 * g + k) * TL::YS] = v[k];
+        } else if (G == 4 || g < 4) {
+          y[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
+        }
       }
     }
     __syncthreads();
 
     // elements: D u, the gate, and out
     if (!kStates) {
+      const Pack<float, VE> Dv = *reinterpret_cast<const Pack<float, VE>*>(Ds + c0);
+      const int rows = (int)min(end - t0, (int64_t)TL::TT);
 #pragma unroll
       for (int i = 0; i < TL::NL; ++i) {
-        const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
-        const int at = TL::slot(t, c0) * 16;
-        float f[TL::VE];
-        const bool in_seq = t0 + t < stop;
+        const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
+        const bool mine = TL::ACC % kScanThreads == 0 || idx < TL::ACC;
 #pragma unroll
-        for (int k = 0; k < TL::VE; ++k) {
-          const float4 p = *reinterpret_cast<const float4*>(reinterpret_cast<const char*>(dd) +
-                                                            (at ^ (k * 16)));
-          float v = fmaf(Ds[c0 + k], ku[i].get(k), sum_partials<G>(p));
-          if (gated) {
-            const float z = kz[i].get(k);
-            v *= z * sigmoid(z);
+        for (int j = 0; j < 2; ++j) {
+          const int t = 2 * tp + j;
+          float f[VE];
+          if (mine) {
+            const Pack<float, VE> yv =
+                *reinterpret_cast<const Pack<float, VE>*>(ys + t * TL::YS + c0);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) f[k] = fmaf(Dv.v[k], ku[i][j].get(k), yv.v[k]);
+            if (gated) {
+#pragma unroll
+              for (int k = 0; k < VE; ++k) {
+                const float z = kz[i][j].get(k);
+                f[k] *= z * sigmoid(z);
+              }
+            }
+            if (t >= left) {
+#pragma unroll
+              for (int k = 0; k < VE; ++k) f[k] = 0.0f;
+            }
+            if (t < rows && have > 0)
+              store_f32<T, VE>(yp + (i * (kScanThreads / TL::NV) * 2 + j) * out.yts,
+                               out.wide_y && have == VE, have, f);
           }
-          f[k] = in_seq ? v : 0.0f;
         }
-        const int have = min(TL::VE, channels - c0);
-        if (t0 + t < end && have > 0)
-          store_f32<T, TL::VE>(out.y + b * out.ybs + (t0 + t) * out.yts + d0 + c0,
-                               out.wide_y && have == TL::VE, have, f);
       }
+      yp += TL::TT * out.yts;
     }
   }
-  if (kStates) {
+  if constexpr (kStates) {
     if (live) {
-      float h[kS];
-      lane_states(l, h);
       const int64_t row = (seg * in.batch + b) * in.dim + d;
       *reinterpret_cast<float4*>(sg.E + row * TL::NP + n0) = make_float4(h[0], h[1], h[2], h[3]);
-      if (g == 0) sg.sum[row] = total;
+      float lo, hi;
+      unpack2(total, lo, hi);
+      if (g == 0) sg.sum[row] = lo + hi;
     }
-    return;
-  }
-  for (; t0 < end; t0 += TL::TT) {  // past the sequence's length
-#pragma unroll
-    for (int i = 0; i < TL::NL; ++i) {
-      const int idx = i * kScanThreads + tid, t = idx / TL::NV, c0 = idx % TL::NV * TL::VE;
-      const int have = min(TL::VE, channels - c0);
-      float f[TL::VE];
-#pragma unroll
-      for (int k = 0; k < TL::VE; ++k) f[k] = 0.0f;
-      if (t0 + t < end && have > 0)
-        store_f32<T, TL::VE>(out.y + b * out.ybs + (t0 + t) * out.yts + d0 + c0,
-                             out.wide_y && have == TL::VE, have, f);
-    }
-  }
+  } else {
+  for (int64_t t = t0; t < end; ++t)  // past the sequence's length
+    for (int k = tid; k < channels; k += kScanThreads)
+      out.y[b * out.ybs + t * out.yts + d0 + k] = from_f32<T>(0.0f);
   if (out.final_state != nullptr && seg == sg.count - 1 && live) {
-    float h[kS];
-    lane_states(l, h);
 #pragma unroll
     for (int k = 0; k < kS; ++k)
       if (n0 + k < in.N) out.final_state[(b * in.dim + d) * in.N + n0 + k] = h[k];
+  }
   }
 }
 
@@ -439,145 +481,417 @@ struct ScanBack {
   const float* checkpoints;
   T *du, *ddt, *dz;
   float* dstate;
-  float* part_BC;  // [batch][len][groups][warps][2][G kS]
+  float* part_BC;  // [batch][len][groups][blocks][2][NP]: dB, dC
   float* part_A;   // [batch][dim][N + 2]: dA, dD, ddt_bias
-  int64_t warps;   // a group's, of a sequence
+  int64_t n_check;
+  bool wide, wide_out, wide_BC, wide_check;
 };
 
-template <class T, int G>
-__global__ void __launch_bounds__(kScanThreads)
-selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o, int64_t n_check) {
-  constexpr int NP = G * kS;
-  const Place p = place<G>(in.group_dim, in.groups);
-  const int n0 = p.g * kS;
-  const int64_t len = sequence_length(in.lengths, in.index_bytes, p.b, in.len);
-  const int64_t row = (p.b * in.dim + p.d) * in.N;
-  const int64_t per_group = (in.group_dim + kScanThreads / G - 1) / (kScanThreads / G);
-  const int64_t warp =
-      (blockIdx.x % (per_group * in.groups)) % per_group * (kScanThreads / 32) + threadIdx.x / 32;
-  float A[kS], carry[kS], dA[kS];
-  load_states(in.A + p.d * in.N, n0, in.N, A);
-#pragma unroll
-  for (int k = 0; k < kS; ++k) carry[k] = dA[k] = 0.0f;
-  if (o.dfinal != nullptr) load_states(o.dfinal + row, n0, in.N, carry);
-  const float Dd = in.D != nullptr ? in.D[p.d] : 0.0f;
-  const float bias = in.dt_bias != nullptr ? in.dt_bias[p.d] : 0.0f;
-  float dD = 0.0f, dbias = 0.0f;
-  const int64_t chunks = (in.len + kCheckpoint - 1) / kCheckpoint;
-  for (int64_t ch = chunks - 1; ch >= 0; --ch) {
-    const int64_t t0 = ch * kCheckpoint;
-    float h[kCheckpoint + 1][kS];
-    load_states(o.checkpoints + ((p.b * n_check + ch) * in.dim + p.d) * in.N, n0, in.N, h[0]);
-#pragma unroll
-    for (int i = 0; i < kCheckpoint; ++i) {
-      const int64_t t = t0 + i;
-#pragma unroll
-      for (int k = 0; k < kS; ++k) h[i + 1][k] = h[i][k];
-      if (t < len) {
-        float B[kS];
-        load_states(in.B + p.b * in.Bbs + t * in.Bts + (int64_t)p.group * in.N, n0, in.N, B);
-        const float u = to_f32(in.u[p.b * in.ubs + t * in.uts + p.d]);
-        float delta = to_f32(in.dt[p.b * in.dbs + t * in.dts + p.d]) + bias;
-        if (in.softplus) delta = softplus(delta);
-#pragma unroll
-        for (int k = 0; k < kS; ++k)
-          h[i + 1][k] = fmaf(exp2_fast(delta * (A[k] * kLog2e)), h[i][k], delta * u * B[k]);
-      }
+// Sums over the channels of a warp. A lane holds, for a pair of steps, dB
+// (v[0..3]) and dC (v[4..7]) of its four state slots; slot k of lane c is
+// state k ^ 2 where c is in the upper half of the warp's channels, so that
+// the first level keeps slots 0 and 1 and sends 2 and 3 in every lane. The
+// next levels halve over slots, kind and step; at the end lane c owns what
+// its bits say (see owned()).
+template <int G>
+struct ChannelSum {
+  static constexpr int L = 32 / G;  // lanes that are summed
+  static constexpr int kPairs = L >= 8 ? 1 : L == 4 ? 2 : L == 2 ? 4 : 8;  // left of 8
+
+  static __device__ __forceinline__ F2 exchange(F2 keep, F2 send, int mask) {
+    float a, b;
+    unpack2(send, a, b);
+    a = __shfl_xor_sync(~0u, a, mask);
+    b = __shfl_xor_sync(~0u, b, mask);
+    return add2(keep, pack2(a, b));
+  }
+  static __device__ __forceinline__ F2 select(bool s, F2 a, F2 b) { return s ? a : b; }
+
+  // v[8] -> v[0 .. kPairs)
+  static __device__ __forceinline__ void run(F2 (&v)[8], int c) {
+    if (L >= 2) {  // slots {0, 1} or {2, 3}: v = B0 B1 C0 C1
+      v[0] = exchange(v[0], v[2], L / 2);
+      v[1] = exchange(v[1], v[3], L / 2);
+      v[2] = exchange(v[4], v[6], L / 2);
+      v[3] = exchange(v[5], v[7], L / 2);
+    }
+    if (L >= 4) {  // slot 0 or 1: v = B C
+      const bool up = c & (L / 4);
+      const F2 b = exchange(select(up, v[1], v[0]), select(up, v[0], v[1]), L / 4);
+      v[1] = exchange(select(up, v[3], v[2]), select(up, v[2], v[3]), L / 4);
+      v[0] = b;
+    }
+    if (L >= 8) {  // B or C
+      const bool up = c & (L / 8);
+      v[0] = exchange(select(up, v[1], v[0]), select(up, v[0], v[1]), L / 8);
     }
 #pragma unroll
-    for (int i = kCheckpoint - 1; i >= 0; --i) {
-      const int64_t t = t0 + i;
-      if (t >= in.len) continue;
-      float dB[kS] = {0.0f, 0.0f, 0.0f, 0.0f}, dC[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
-      float du = 0.0f, ddt = 0.0f, dz = 0.0f;
-      if (t < len) {
-        float B[kS], C[kS];
-        load_states(in.B + p.b * in.Bbs + t * in.Bts + (int64_t)p.group * in.N, n0, in.N, B);
-        load_states(in.C + p.b * in.Cbs + t * in.Cts + (int64_t)p.group * in.N, n0, in.N, C);
-        const float u = to_f32(in.u[p.b * in.ubs + t * in.uts + p.d]);
-        const float raw = to_f32(in.dt[p.b * in.dbs + t * in.dts + p.d]) + bias;
-        const float delta = in.softplus ? softplus(raw) : raw;
-        float pt = to_f32(o.dy[p.b * o.dybs + t * o.dyts + p.d]);
-        if (in.z != nullptr) {
-          const float z = to_f32(in.z[p.b * in.zbs + t * in.zts + p.d]);
-          const float s = sigmoid(z);
-          float yv = 0.0f;
+    for (int s = L / 16; s >= 1; s /= 2) v[0] = exchange(v[0], v[0], s);
+  }
+  // Which (kind, slot) pair i of lane c is: kind * NP + state, within a row.
+  static __device__ __forceinline__ int owned(int i, int c, int g) {
+    constexpr int NP = G * kS;
+    int kind = i / (kPairs == 8 ? 4 : kPairs == 4 ? 2 : 1) % 2, slot = i % (kPairs == 8 ? 4 : 2);
+    if (L == 2) slot = i % 2 + (c & 1 ? 2 : 0);
+    if (L >= 4) slot = (c & (L / 2) ? 2 : 0) + (c & (L / 4) ? 1 : 0);
+    if (L >= 8) kind = c & (L / 8) ? 1 : 0;
+    return kind * NP + g * kS + slot;
+  }
+  // Lanes that only repeat another's result (L > 8) do not write.
+  static __device__ __forceinline__ bool writes(int c) { return L <= 8 || c % (L > 8 ? L / 8 : 1) == 0; }
+};
+
+// A block walks its channels' tiles of kCheckpoint steps from the last to the
+// first: it takes the tile's states forward from the checkpoint, holding all
+// of them in registers, then the adjoint states back, with the decays
+// computed again (holding them too spilled registers).
+#ifndef CR_SCAN_BACK_BLOCKS
+#define CR_SCAN_BACK_BLOCKS 2
+#endif
+template <class T, int G>
+__global__ void __launch_bounds__(kScanThreads, CR_SCAN_BACK_BLOCKS)
+selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
+  using TL = Tile<T, G, kCheckpoint>;
+  using CS = ChannelSum<G>;
+  constexpr int VE = TL::VE, TT = TL::TT, TP = TL::TP, NP = TL::NP, kWarps = kScanThreads / 32;
+  __shared__ float4 dd[TP * TL::CH];               // delta, delta', du, du'
+  __shared__ __align__(16) float2 pp[TP * TL::CH];  // p, p'
+  __shared__ float4 Bs[TL::ACC_BC * 2], Cs[TL::ACC_BC * 2];
+  // y, sum_n g B, sum_n q A of the steps
+  __shared__ __align__(16) float ys[TT * TL::YS], gs[TT * TL::YS], qs[TT * TL::YS];
+  __shared__ float2 sums[kWarps * TP * 2 * NP];
+  __shared__ __align__(16) float Ds[TL::CH], biases[TL::CH];
+
+  const int tid = threadIdx.x, g = Lanes<G>::g(), c = Lanes<G>::c(), n0 = g * kS;
+  const int lane_c = c % CS::L;
+  const int flip = (CS::L >= 2 && (lane_c & (CS::L / 2))) ? 2 : 0;  // slot k holds state k ^ flip
+  const int64_t per_group = (in.group_dim + TL::CH - 1) / TL::CH;
+  const int64_t blk = blockIdx.x % (per_group * in.groups), b = blockIdx.x / (per_group * in.groups);
+  const int64_t group = blk / per_group, first = blk % per_group * TL::CH;
+  const int channels = (int)min((int64_t)TL::CH, in.group_dim - first);
+  const int64_t d0 = group * in.group_dim + first;
+  const bool live = c < channels;
+  const int64_t d = d0 + (live ? c : 0);
+  const int64_t len = sequence_length(in.lengths, in.index_bytes, b, in.len);
+  const int64_t row = (b * in.dim + d) * in.N;
+
+  if (tid < TL::CH) {
+    Ds[tid] = (in.D != nullptr && tid < channels) ? in.D[d0 + tid] : 0.0f;
+    biases[tid] = (in.dt_bias != nullptr && tid < channels) ? in.dt_bias[d0 + tid] : 0.0f;
+  }
+  F2 A[kS], dA[kS];
+  float carry[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
+  {
+    float a[kS], f[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
+    load_states(in.A + d * in.N, n0, in.N, a);
+    if (o.dfinal != nullptr && live) load_states(o.dfinal + row, n0, in.N, f);
 #pragma unroll
-          for (int k = 0; k < kS; ++k) yv = fmaf(C[k], h[i + 1][k], yv);
-          yv = fmaf(Dd, u, sum_lanes<G>(yv));
-          dz = pt * yv * (s * fmaf(z, 1.0f - s, 1.0f));
-          pt *= z * s;
+    for (int k = 0; k < kS; ++k) {
+      A[k] = pack2(flip ? a[k ^ 2] : a[k], flip ? a[k ^ 2] : a[k]);
+      carry[k] = flip ? f[k ^ 2] : f[k];
+      dA[k] = 0;
+    }
+  }
+
+  // Tiles past the sequence's length: zeros.
+  const int64_t tiles = (len + TT - 1) / TT;
+  const int c0 = tid % TL::NV * VE, have = min(VE, channels - c0);
+  for (int64_t t = tiles * TT; t < in.len; ++t) {
+    for (int k = tid; k < channels; k += kScanThreads) {
+      const int64_t at = (b * in.len + t) * in.dim + d0 + k;
+      o.du[at] = o.ddt[at] = from_f32<T>(0.0f);
+      if (o.dz != nullptr) o.dz[at] = from_f32<T>(0.0f);
+    }
+    for (int k = tid; k < 2 * NP; k += kScanThreads)
+      o.part_BC[(((b * in.len + t) * in.groups + group) * per_group + first / TL::CH) * 2 * NP + k] =
+          0.0f;
+  }
+
+  using RowsE = Rows<T, VE, TL::NL, TL::ACC, TL::NV>;
+  using RowsBC = Rows<T, kS, TL::NBC, TL::ACC_BC, G>;
+  const int64_t last = (tiles - 1) * TT;
+  RowsE ru(in.u + b * in.ubs + d0, in.uts, last, -TT, channels, o.wide);
+  RowsE rd(in.dt + b * in.dbs + d0, in.dts, last, -TT, channels, o.wide);
+  RowsE rz(in.z + b * in.zbs + d0, in.zts, last, -TT, channels, o.wide);
+  RowsE ry(o.dy + b * o.dybs + d0, o.dyts, last, -TT, channels, o.wide);
+  RowsBC rB(in.B + b * in.Bbs + group * in.N, in.Bts, last, -TT, in.N, o.wide_BC);
+  RowsBC rC(in.C + b * in.Cbs + group * in.N, in.Cts, last, -TT, in.N, o.wide_BC);
+  const bool gated = in.z != nullptr;
+  Raw<T, VE> pu[TL::NL][2], pd[TL::NL][2], pz[TL::NL][2], py[TL::NL][2];
+  Raw<T, kS> pB[TL::NBC][2], pC[TL::NBC][2];
+  float next[kS];
+  auto load = [&](int64_t tile) {
+    const int left = (int)min(len - tile * TT, (int64_t)TT);
+    ru.load(left, pu);
+    rd.load(left, pd);
+    if (gated) rz.load(left, pz);
+    ry.load(left, py);
+    rB.load(left, pB);
+    rC.load(left, pC);
+    const float* q = o.checkpoints + ((b * o.n_check + tile) * in.dim + d) * in.N;
+    if (o.wide_check && n0 < in.N) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(q + n0));
+      next[0] = f.x, next[1] = f.y, next[2] = f.z, next[3] = f.w;
+    } else {
+      load_states(q, n0, in.N, next);
+    }
+  };
+  if (tiles > 0) load(tiles - 1);
+  __syncthreads();  // Ds, biases
+  float dD[VE], dbias[VE];
+#pragma unroll
+  for (int k = 0; k < VE; ++k) dD[k] = dbias[k] = 0.0f;
+
+  for (int64_t tile = tiles - 1; tile >= 0; --tile) {
+    const int64_t t0 = tile * TT;
+    const int left = (int)min(len - t0, (int64_t)TT);
+    // elements: delta, delta u and p into the tile
+    Raw<T, VE> ku[TL::NL][2], kd[TL::NL][2], kz[TL::NL][2], ky[TL::NL][2];
+    const Pack<float, VE> bias = *reinterpret_cast<const Pack<float, VE>*>(biases + c0);
+    const Pack<float, VE> Dv = *reinterpret_cast<const Pack<float, VE>*>(Ds + c0);
+#pragma unroll
+    for (int i = 0; i < TL::NL; ++i) {
+      const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
+      const int at = TL::slot(tp, c0);
+      const bool in0 = 2 * tp < left, in1 = 2 * tp + 1 < left;
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        float a = pd[i][0].get(k) + bias.v[k], a1 = pd[i][1].get(k) + bias.v[k];
+        if (in.softplus) softplus2(a, a1);
+        a = in0 ? a : 0.0f;
+        a1 = in1 ? a1 : 0.0f;
+        float p = py[i][0].get(k), p1 = py[i][1].get(k);
+        if (gated) {
+          const float z = pz[i][0].get(k), z1 = pz[i][1].get(k);
+          p *= z * sigmoid(z);
+          p1 *= z1 * sigmoid(z1);
         }
-        float gB = 0.0f, qA = 0.0f;
+        if (TL::ACC % kScanThreads == 0 || idx < TL::ACC) {
+          dd[at ^ k] = make_float4(a, a1, a * pu[i][0].get(k), a1 * pu[i][1].get(k));
+          pp[at ^ k] = make_float2(p, p1);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        ku[i][j] = pu[i][j];
+        kd[i][j] = pd[i][j];
+        ky[i][j] = py[i][j];
+        if (gated) kz[i][j] = pz[i][j];
+      }
+    }
+    tile_put_states<TL>(pB, Bs);
+    tile_put_states<TL>(pC, Cs);
+    float h[TT + 1][kS];
+#pragma unroll
+    for (int k = 0; k < kS; ++k) h[0][k] = flip ? next[k ^ 2] : next[k];
+    __syncthreads();
+    if (tile > 0) load(tile - 1);
+
+    // the states, forward; the quads of B and C in slot order
+    const float4* dl = dd + TL::slot(0, c);
+    const float2* pl = pp + TL::slot(0, c);
+    const float4 *Bl = Bs + 2 * g, *Cl = Cs + 2 * g;
+    const int q0 = flip / 2, q1 = 1 - q0;
+#pragma unroll
+    for (int t4 = 0; t4 < TT / 4; ++t4) {
+      F2 yp[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tp = t4 * 2 + j, t = tp * 2;
+        const float4 e = dl[tp * TL::CH];
+        const F2 delta = pack2(e.x * kLog2e, e.y * kLog2e), du = pack2(e.z, e.w);
+        const float4 B[2] = {Bl[tp * 2 * G + q0], Bl[tp * 2 * G + q1]};
+        const float4 C[2] = {Cl[tp * 2 * G + q0], Cl[tp * 2 * G + q1]};
 #pragma unroll
         for (int k = 0; k < kS; ++k) {
-          const float g = fmaf(C[k], pt, carry[k]);
-          dC[k] = pt * h[i + 1][k];
-          dB[k] = g * (delta * u);
-          gB = fmaf(g, B[k], gB);
-          carry[k] = g * exp2_fast(delta * (A[k] * kLog2e));
-          const float q = carry[k] * h[i][k];
-          dA[k] = fmaf(q, delta, dA[k]);
-          qA = fmaf(q, A[k], qA);
+          const F2 Bk = k % 2 ? pack2(B[k / 2].z, B[k / 2].w) : pack2(B[k / 2].x, B[k / 2].y);
+          const F2 Ck = k % 2 ? pack2(C[k / 2].z, C[k / 2].w) : pack2(C[k / 2].x, C[k / 2].y);
+          float x0, x1, b0, b1;
+          unpack2(mul2(delta, A[k]), x0, x1);
+          unpack2(mul2(du, Bk), b0, b1);
+          h[t + 1][k] = fmaf(exp2_fast(x0), h[t][k], b0);
+          h[t + 2][k] = fmaf(exp2_fast(x1), h[t + 1][k], b1);
+          const F2 hp = pack2(h[t + 1][k], h[t + 2][k]);
+          yp[j] = k == 0 ? mul2(Ck, hp) : fma2(Ck, hp, yp[j]);
         }
-        gB = sum_lanes<G>(gB);
-        qA = sum_lanes<G>(qA);
-        du = fmaf(delta, gB, Dd * pt);
-        ddt = fmaf(u, gB, qA);
-        if (in.softplus) ddt *= sigmoid(raw);
-        dD = fmaf(pt, u, dD);
-        dbias += ddt;
       }
-      if (p.live && p.g == 0) {
-        const int64_t at = (p.b * in.len + t) * in.dim + p.d;
-        o.du[at] = from_f32<T>(du);
-        o.ddt[at] = from_f32<T>(ddt);
-        if (o.dz != nullptr) o.dz[at] = from_f32<T>(dz);
+      if (gated) {
+        float v[4];
+        sum_lanes4<G>(yp[0], yp[1], g, v);
+        float* y = ys + t4 * 4 * TL::YS + c;
+        if (G == 1) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k * TL::YS] = v[k];
+        } else if (G == 2) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) y[(2 * g + k) * TL::YS] = v[k];
+        } else if (G == 4 || g < 4) {
+          y[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
+        }
       }
-      float* q = o.part_BC + (((p.b * in.len + t) * in.groups + p.group) * o.warps + warp) * 2 * NP;
+    }
+
+    // the adjoint states, backward; the tile is read again, so that nothing of
+    // the pass above but h is held in registers
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int tp = TP - 1; tp >= 0; --tp) {
+      const int t = tp * 2;
+      const float4 e = dl[tp * TL::CH];
+      const float2 p2 = pl[tp * TL::CH];
+      const F2 delta = pack2(e.x, e.y), du = pack2(e.z, e.w), p = pack2(p2.x, p2.y);
+      const F2 delta2 = pack2(e.x * kLog2e, e.y * kLog2e);
+      const float4 B[2] = {Bl[tp * 2 * G + q0], Bl[tp * 2 * G + q1]};
+      const float4 C[2] = {Cl[tp * 2 * G + q0], Cl[tp * 2 * G + q1]};
+      F2 v[8], gB = 0, qA = 0;
 #pragma unroll
       for (int k = 0; k < kS; ++k) {
-        float vB = p.live ? dB[k] : 0.0f, vC = p.live ? dC[k] : 0.0f;
+        const F2 Bk = k % 2 ? pack2(B[k / 2].z, B[k / 2].w) : pack2(B[k / 2].x, B[k / 2].y);
+        const F2 Ck = k % 2 ? pack2(C[k / 2].z, C[k / 2].w) : pack2(C[k / 2].x, C[k / 2].y);
+        float c0, c1, x0, x1;
+        unpack2(mul2(Ck, p), c0, c1);
+        unpack2(mul2(delta2, A[k]), x0, x1);
+        const float g1 = c1 + carry[k], r1 = g1 * exp2_fast(x1);
+        const float g0 = c0 + r1, r0 = g0 * exp2_fast(x0);
+        carry[k] = r0;
+        const F2 gp = pack2(g0, g1), q = pack2(r0 * h[t][k], r1 * h[t + 1][k]);
+        dA[k] = fma2(q, delta, dA[k]);
+        qA = k == 0 ? mul2(q, A[k]) : fma2(q, A[k], qA);
+        gB = k == 0 ? mul2(gp, Bk) : fma2(gp, Bk, gB);
+        v[k] = mul2(gp, du);
+        v[4 + k] = mul2(p, pack2(h[t + 1][k], h[t + 2][k]));
+      }
+      CS::run(v, lane_c);
+      if (CS::writes(lane_c)) {
 #pragma unroll
-        for (int s = G; s < 32; s *= 2) {
-          vB += __shfl_xor_sync(~0u, vB, s);
-          vC += __shfl_xor_sync(~0u, vC, s);
+        for (int i = 0; i < CS::kPairs; ++i) {
+          float lo, hi;
+          unpack2(v[i], lo, hi);
+          sums[(tid / 32 * TP + tp) * 2 * NP + CS::owned(i, lane_c, g)] = make_float2(lo, hi);
         }
-        if (threadIdx.x % 32 < G) {
-          q[n0 + k] = vB;
-          q[NP + n0 + k] = vC;
+      }
+      float w[4];
+      sum_lanes4<G>(gB, qA, g, w);
+      float *gl = gs + t * TL::YS + c, *ql = qs + t * TL::YS + c;
+      if (G == 1) {
+        gl[0] = w[0], gl[TL::YS] = w[1], ql[0] = w[2], ql[TL::YS] = w[3];
+      } else if (G == 2) {
+        float* q = g ? ql : gl;
+        q[0] = w[0], q[TL::YS] = w[1];
+      } else if (G == 4 || g < 4) {
+        (g & 1 ? ql : gl)[(g >> 1 & 1) * TL::YS] = w[0];
+      }
+    }
+    __syncthreads();
+
+    // dB and dC of the block's channels: the warps in order
+    for (int k = tid; k < TP * 2 * NP; k += kScanThreads) {
+      float2 s = sums[k];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float2 v = sums[w * TP * 2 * NP + k];
+        s.x += v.x;
+        s.y += v.y;
+      }
+      const int64_t t = t0 + k / (2 * NP) * 2;
+      const int64_t stride = (int64_t)in.groups * per_group * 2 * NP;
+      float* q = o.part_BC + (b * in.len + t) * stride +
+                 (group * per_group + first / TL::CH) * 2 * NP + k % (2 * NP);
+      if (t < in.len) q[0] = s.x;
+      if (t + 1 < in.len) q[stride] = s.y;
+    }
+    // elements: du, ddt, dz out
+#pragma unroll
+    for (int i = 0; i < TL::NL; ++i) {
+      const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
+      if (TL::ACC % kScanThreads != 0 && idx >= TL::ACC) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = 2 * tp + j;
+        const Pack<float, VE> yv = *reinterpret_cast<const Pack<float, VE>*>(ys + t * TL::YS + c0);
+        const Pack<float, VE> gv = *reinterpret_cast<const Pack<float, VE>*>(gs + t * TL::YS + c0);
+        const Pack<float, VE> qv = *reinterpret_cast<const Pack<float, VE>*>(qs + t * TL::YS + c0);
+        float fu[VE], fd[VE], fz[VE];
+        const bool in_seq = t < left;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          const float u = ku[i][j].get(k);
+          const float4 e = dd[TL::slot(tp, c0) ^ k];
+          const float2 p2 = pp[TL::slot(tp, c0) ^ k];
+          const float delta = j ? e.y : e.x, p = j ? p2.y : p2.x;
+          fu[k] = fmaf(delta, gv.v[k], Dv.v[k] * p);
+          fd[k] = fmaf(u, gv.v[k], qv.v[k]);
+          if (in.softplus) fd[k] *= sigmoid(kd[i][j].get(k) + bias.v[k]);
+          fz[k] = 0.0f;
+          if (gated) {
+            const float z = kz[i][j].get(k), sg = sigmoid(z);
+            fz[k] = ky[i][j].get(k) * fmaf(Dv.v[k], u, yv.v[k]) * (sg * fmaf(z, 1.0f - sg, 1.0f));
+          }
+          if (in_seq) {
+            dD[k] = fmaf(p, u, dD[k]);
+            dbias[k] += fd[k];
+          } else {
+            fu[k] = fd[k] = fz[k] = 0.0f;
+          }
+        }
+        if (t0 + t < in.len && have > 0) {
+          const int64_t at = (b * in.len + t0 + t) * in.dim + d0 + c0;
+          const bool w = o.wide_out && have == VE;
+          store_f32<T, VE>(o.du + at, w, have, fu);
+          store_f32<T, VE>(o.ddt + at, w, have, fd);
+          if (o.dz != nullptr) store_f32<T, VE>(o.dz + at, w, have, fz);
         }
       }
     }
+    // the next tile's elements overwrite dd and pp where this thread read them
   }
-  if (!p.live) return;
-  float* q = o.part_A + (p.b * in.dim + p.d) * (in.N + 2);
+
+  // dD and ddt_bias: the threads of a channel in order
+  float* red = ys;  // [rows of threads][CH]
+  constexpr int kRows = kScanThreads / TL::NV;
+  static_assert(kRows * TL::CH <= TT * TL::YS, "the y tile holds a value of every thread's");
+  __syncthreads();
+  if (live) {
+    float* q = o.part_A + (b * in.dim + d) * (in.N + 2);
 #pragma unroll
-  for (int k = 0; k < kS; ++k) {
-    if (n0 + k < in.N) {
-      q[n0 + k] = dA[k];
-      if (o.dstate != nullptr) o.dstate[row + n0 + k] = carry[k];
+    for (int k = 0; k < kS; ++k) {
+      const int n = n0 + (k ^ flip);
+      float lo, hi;
+      unpack2(dA[k], lo, hi);
+      if (n < in.N) {
+        q[n] = lo + hi;
+        if (o.dstate != nullptr) o.dstate[row + n] = carry[k];
+      }
     }
   }
-  if (p.g == 0) {
-    q[in.N] = dD;
-    q[in.N + 1] = dbias;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (tid / TL::NV < kRows && c0 < TL::CH) {
+#pragma unroll
+      for (int k = 0; k < VE; ++k) red[tid / TL::NV * TL::CH + c0 + k] = pass ? dbias[k] : dD[k];
+    }
+    __syncthreads();
+    if (tid < channels) {
+      float s = 0.0f;
+      for (int r = 0; r < kRows; ++r) s += red[r * TL::CH + tid];
+      o.part_A[(b * in.dim + d0 + tid) * (in.N + 2) + in.N + pass] = s;
+    }
+    __syncthreads();
   }
 }
 
-// dB and dC: the warps' partials of a (sequence, step, group), in order.
+// dB and dC: the blocks' partials of a (sequence, step, group), in order.
 template <class T>
 __global__ void __launch_bounds__(kScanThreads)
-selective_scan_sum_bc_kernel(const float* __restrict__ part, int64_t rows, int64_t warps, int NP,
+selective_scan_sum_bc_kernel(const float* __restrict__ part, int64_t rows, int64_t blocks, int NP,
                              int N, T* __restrict__ dB, T* __restrict__ dC) {
   const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
   if (i >= rows * 2 * N) return;
   const int64_t r = i / (2 * N);
   const int j = (int)(i % (2 * N));
   const int which = j / N, n = j % N;
-  const float* q = part + r * warps * 2 * NP + which * NP + n;
+  const float* q = part + r * blocks * 2 * NP + which * NP + n;
   float s = 0.0f;
-  for (int64_t w = 0; w < warps; ++w) s += q[w * 2 * NP];
+  for (int64_t w = 0; w < blocks; ++w) s += q[w * 2 * NP];
   (which ? dC : dB)[r * N + n] = from_f32<T>(s);
 }
 
@@ -618,11 +932,12 @@ selective_scan_step_kernel(ScanIn<T> in, float* __restrict__ state, int64_t stat
     if (in.dt_bias != nullptr) delta += in.dt_bias[p.d];
     if (in.softplus) delta = softplus(delta);
     const float du = delta * u;
-    Lane l;
-    lane_init(l, A, h);
-    lane_step(l, pack2(delta, delta), pack2(du, du), pack2(B[0], B[1]), pack2(B[2], B[3]));
-    const float acc = lane_dot(l, pack2(C[0], C[1]), pack2(C[2], C[3]));
-    lane_states(l, h);
+    float acc = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      h[k] = fmaf(exp2_fast(delta * (A[k] * kLog2e)), h[k], du * B[k]);
+      acc = k == 0 ? C[k] * h[k] : fmaf(C[k], h[k], acc);
+    }
     o = fmaf(in.D != nullptr ? in.D[p.d] : 0.0f, u, sum_lanes<G>(acc));
     if (in.z != nullptr) {
       const float z = to_f32(in.z[p.b * in.zbs + p.d]);
@@ -790,7 +1105,7 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
   sg.sum = sg.E + (sg.count - 1) * a->batch * a->dim * lanes * kS;
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
     using TL = Tile<T, G>;
-    const size_t bytes = TL::VE * es;
+    const size_t bytes = TL::VE * es;  // of an access
     const bool group_ok = a->groups == 1 || (a->dim / a->groups) % TL::VE == 0;
     ScanOut<T> out;
     out.y = static_cast<T*>(y);
@@ -804,6 +1119,7 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
                (a->z == nullptr ||
                 rows_aligned(a->z, a->z_batch_stride, a->z_time_stride, es, bytes));
     out.wide_y = group_ok && rows_aligned(y, y_batch_stride, y_time_stride, es, bytes);
+    out.wide_check = a->dstate % kS == 0 && ptr_aligned(checkpoints, 16);
     out.wide_BC = a->dstate % kS == 0 &&
                   rows_aligned(a->B, a->B_batch_stride, a->B_time_stride, es, kS * es) &&
                   rows_aligned(a->C, a->C_batch_stride, a->C_time_stride, es, kS * es);
@@ -819,8 +1135,9 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
-static int64_t backward_warps(int64_t dim, int32_t groups, int lanes) {
-  return cr::ceil_div(dim / groups, cr::kScanThreads / lanes) * (cr::kScanThreads / 32);
+// Blocks that share a group of a sequence: each leaves its own dB and dC.
+static int64_t group_blocks(int64_t dim, int32_t groups, int lanes) {
+  return cr::ceil_div(dim / groups, cr::kScanThreads / lanes);
 }
 
 size_t cr_selective_scan_backward_workspace_bytes(int64_t batch, int64_t len, int64_t dim,
@@ -828,7 +1145,7 @@ size_t cr_selective_scan_backward_workspace_bytes(int64_t batch, int64_t len, in
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || dstate < 1 || groups < 1 || dim % groups != 0) return 0;
   const int lanes = scan_lanes(dstate);
-  const size_t bc = (size_t)batch * len * groups * backward_warps(dim, groups, lanes) * 2 *
+  const size_t bc = (size_t)batch * len * groups * group_blocks(dim, groups, lanes) * 2 *
                     (lanes * kS) * 4;
   return round256(bc) + round256((size_t)batch * dim * (dstate + 2) * 4) + 256;
 }
@@ -863,11 +1180,11 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
   if (ws == nullptr || !ptr_aligned(ws, 256) || ws_bytes < need) return CR_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int lanes = scan_lanes(a->dstate);
-  const int64_t warps = backward_warps(a->dim, a->groups, lanes);
+  const int64_t parts = group_blocks(a->dim, a->groups, lanes);
   const int64_t rows = a->batch * a->len * a->groups;
   float* part_BC = static_cast<float*>(ws);
   float* part_A = reinterpret_cast<float*>(
-      static_cast<char*>(ws) + round256((size_t)rows * warps * 2 * (lanes * kS) * 4));
+      static_cast<char*>(ws) + round256((size_t)rows * parts * 2 * (lanes * kS) * 4));
   if (a->batch > 0) {
     const unsigned blocks = (unsigned)scan_blocks(a->batch, a->dim, a->groups, lanes);
     const int64_t n_check = cr_selective_scan_checkpoints(a->len);
@@ -884,10 +1201,25 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
       o.dstate = g->dstate;
       o.part_BC = part_BC;
       o.part_A = part_A;
-      o.warps = warps;
+      o.n_check = n_check;
+      using TL = Tile<T, G, kCheckpoint>;
+      const size_t bytes = TL::VE * es;  // of an access
+      const bool group_ok = a->groups == 1 || (a->dim / a->groups) % TL::VE == 0;
+      o.wide = group_ok && rows_aligned(a->u, a->u_batch_stride, a->u_time_stride, es, bytes) &&
+               rows_aligned(a->dt, a->dt_batch_stride, a->dt_time_stride, es, bytes) &&
+               rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, bytes) &&
+               (a->z == nullptr ||
+                rows_aligned(a->z, a->z_batch_stride, a->z_time_stride, es, bytes));
+      o.wide_out = group_ok && rows_aligned(g->du, a->dim, a->dim, es, bytes) &&
+                   rows_aligned(g->ddt, a->dim, a->dim, es, bytes) &&
+                   rows_aligned(o.dz, a->dim, a->dim, es, bytes);
+      o.wide_BC = a->dstate % kS == 0 &&
+                  rows_aligned(a->B, a->B_batch_stride, a->B_time_stride, es, kS * es) &&
+                  rows_aligned(a->C, a->C_batch_stride, a->C_time_stride, es, kS * es);
+      o.wide_check = a->dstate % kS == 0 && ptr_aligned(g->checkpoints, 16);
       CR_LAUNCH(kKSelectiveScanBackward, s,
                 selective_scan_backward_kernel<T, G><<<blocks, kScanThreads, 0, s>>>(
-                    scan_in<T>(a), o, n_check));
+                    scan_in<T>(a), o));
     }));
     if (cudaGetLastError() != cudaSuccess) return CR_ERR_CUDA;
     const int64_t sums = ceil_div(rows * 2 * a->dstate, kScanThreads);
@@ -896,7 +1228,7 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
       CR_MODEL_TYPE(a->dt_type, {
         CR_LAUNCH(kKSelectiveScanSum, s,
                   selective_scan_sum_bc_kernel<T><<<(unsigned)sums, kScanThreads, 0, s>>>(
-                      part_BC, rows, warps, lanes * kS, a->dstate, static_cast<T*>(g->dB),
+                      part_BC, rows, parts, lanes * kS, a->dstate, static_cast<T*>(g->dB),
                       static_cast<T*>(g->dC)));
       });
     }
