@@ -16,6 +16,8 @@ same bits.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 
 import torch
 
@@ -23,6 +25,24 @@ from . import _P, _I32, _I64, _WS, _check, lib
 
 _TYPES = {torch.float32: 1, torch.bfloat16: 3, torch.float16: 4}  # cr_dtype
 _ACTIVATIONS = {None: 0, "silu": 1}
+_F32 = torch.float32
+
+# A single-token call is a few microseconds on the device, so the host side is
+# kept to what it must do: one test an argument, no temporary objects, and the
+# argument blocks packed at once.
+_current_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
+_current_device = torch._C._cuda_getDevice
+
+
+def _entry(name):
+    """A libcr function that raises on an error code."""
+    fn = getattr(lib(), name)
+
+    def call(*args):
+        code = fn(*args)
+        if code:
+            _check(code, name)
+    return call
 
 
 class _ConvArgs(ctypes.Structure):
@@ -60,6 +80,33 @@ class _ScanGrads(ctypes.Structure):
                 ("dA", _P), ("dD", _P), ("ddt_bias", _P), ("dstate", _P)]
 
 
+def _packer(structure):
+    """struct.Struct with the layout of a ctypes Structure."""
+    codes = {_I64: "q", _I32: "i", _P: "P"}
+    packed = struct.Struct("@" + "".join(codes[t] for _, t in structure._fields_))
+    assert packed.size == ctypes.sizeof(structure)
+    return packed.pack
+
+
+_pack_conv, _pack_conv_grads = _packer(_ConvArgs), _packer(_ConvGrads)
+_pack_scan, _pack_scan_grads = _packer(_ScanArgs), _packer(_ScanGrads)
+
+_c_embedding = _entry("cr_embedding")
+_c_embedding_backward = _entry("cr_embedding_backward")
+_c_conv = _entry("cr_causal_conv")
+_c_conv_backward = _entry("cr_causal_conv_backward")
+_c_conv_step = _entry("cr_causal_conv_step")
+_c_scan = _entry("cr_selective_scan")
+_c_scan_backward = _entry("cr_selective_scan_backward")
+_c_scan_step = _entry("cr_selective_scan_step")
+
+
+# workspace sizes and checkpoint counts of the shapes a program keeps using
+@functools.lru_cache(maxsize=256)
+def _size(name, *sizes):
+    return getattr(lib(), name)(*sizes)
+
+
 # ------------------------------------------------------------ arguments
 def _type_code(t: torch.Tensor) -> int:
     code = _TYPES.get(t.dtype)
@@ -68,92 +115,99 @@ def _type_code(t: torch.Tensor) -> int:
     return code
 
 
-def _like(t, name, shape, dtype, device):
-    """Checks an argument; None stays None."""
-    if t is None:
-        return None
+def _need(t, name, shape, dtype, index):
+    """Raises unless t has this shape and type and is on CUDA device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    return t
+    raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
 
 
-def _device(t: torch.Tensor, name: str) -> torch.device:
+def _device(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor (the model operators have no host form)" % name)
-    return t.device
+    return t.get_device()
 
 
-def _indices(t, name, shape, device):
-    """(tensor, bytes an index) of a contiguous int32 or int64 tensor."""
+def _indices(t, name, shape, index):
+    """A contiguous int32 or int64 tensor (None stays None)."""
     if t is None:
-        return None, 4
-    if t.dtype not in (torch.int32, torch.int64):
+        return None
+    if t.dtype is not torch.int32 and t.dtype is not torch.int64:
         raise TypeError("%s must be int32 or int64, got %s" % (name, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    return t.contiguous(), t.element_size()
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _rows(t):
-    """t with a contiguous last axis (and, for B and C, last two axes)."""
-    return t if t is None or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+    """t with a contiguous last axis."""
+    return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
 
 
-def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+def _dense(t):
+    return t if t.is_contiguous() else t.contiguous()
 
 
 class _On:
-    """The device and stream of a call: allocates its outputs there, and tells
-    the allocator about inputs of other streams."""
+    """Where a call runs: its device index, its stream, the stream's handle.
+    With a stream other than the current one, outputs are allocated on it and
+    the allocator is told which inputs it reads."""
+    __slots__ = ("index", "stream", "ptr")
 
-    def __init__(self, device, stream):
-        current = torch.cuda.current_stream(device)
-        self.device = device
-        self.stream = current if stream is None else stream
-        self.foreign = self.stream != current
-        self.ptr = self.stream.cuda_stream
-        self.kept = []
+    def __init__(self, index, stream):
+        self.index = index
+        self.stream = None
+        self.ptr = _current_stream(index)
+        if stream is not None and stream.cuda_stream != self.ptr:
+            self.stream = stream
+            self.ptr = stream.cuda_stream
 
     def empty(self, shape, dtype):
-        if not self.foreign:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.index)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=self.index)
 
-    def reads(self, *tensors):
-        if self.foreign:
+    def like(self, t):
+        """An uninitialised contiguous tensor of t's shape and type."""
+        if self.stream is None and t.is_contiguous():
+            return torch.empty_like(t)
+        return self.empty(t.shape, t.dtype)
+
+    def output(self, out, shape, dtype):
+        if out is None:
+            return self.empty(shape, dtype)
+        _need(out, "out", shape, dtype, self.index)
+        if out.stride(-1) != 1 and out.shape[-1] > 1:
+            raise ValueError("out must have a contiguous last axis")
+        return out
+
+    def run(self, call, tensors, *args):
+        """call(*args, stream), which uses `tensors`."""
+        if self.stream is not None:
             for t in tensors:
                 if t is not None:
                     t.record_stream(self.stream)
-
-    def call(self, name, *args):
-        if self.device.index == torch.cuda.current_device():
-            _check(getattr(lib(), name)(*args, self.ptr), name)
+        if self.index == _current_device():
+            call(*args, self.ptr)
         else:
-            with torch.cuda.device(self.device):
-                _check(getattr(lib(), name)(*args, self.ptr), name)
+            with torch.cuda.device(self.index):
+                call(*args, self.ptr)
 
     def workspace(self, nbytes, name):
         if nbytes == 0:
             raise ValueError("invalid %s arguments" % name)
-        return _WS.get(self.device, self.stream, nbytes)
-
-
-def _output(on, out, shape, dtype):
-    if out is None:
-        return on.empty(shape, dtype)
-    _like(out, "out", shape, dtype, on.device)
-    if out.shape[-1] > 1 and out.stride(-1) != 1:
-        raise ValueError("out must have a contiguous last axis")
-    on.reads(out)
-    return out
+        buf = _WS._bufs.get((self.index, self.ptr))
+        if buf is None or buf.numel() < nbytes:
+            where = torch.device("cuda", self.index)
+            buf = _WS.get(where, self.stream or torch.cuda.current_stream(where), nbytes)
+        return buf
 
 
 # ------------------------------------------------------------ embedding
@@ -161,20 +215,19 @@ def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """``scale * table[tokens]``: tokens (any shape, int32 or int64), table
     (vocab, dim). A token outside [0, vocab) is padding: a zero row."""
-    device = _device(table, "table")
+    index = _device(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be 2-D (vocab, dim)")
-    dt = _type_code(table)
-    tok, nbytes = _indices(tokens, "tokens", None, device)
+    code = _type_code(table)
+    tok = _indices(tokens, "tokens", None, index)
     table = _rows(table)
-    on = _On(device, stream)
+    on = _On(index, stream)
     n, (vocab, dim) = tok.numel(), table.shape
-    o = _output(on, out, tuple(tokens.shape) + (dim,), table.dtype)
+    o = on.output(out, tokens.shape + (dim,), table.dtype)
     flat = o if o.dim() == 2 else o.view(n, dim)
-    on.reads(tok, table)
-    on.call("cr_embedding", _ptr(tok), nbytes, n, _ptr(table), vocab, dim,
-            max(table.stride(0), dim), float(scale), dt, _ptr(flat),
-            max(flat.stride(0), dim) if n > 1 else dim)
+    on.run(_c_embedding, (tok, table, o), tok.data_ptr(), tok.element_size(), n, table.data_ptr(),
+           vocab, dim, max(table.stride(0), dim), scale, code, flat.data_ptr(),
+           max(flat.stride(0), dim))
     return o
 
 
@@ -185,27 +238,27 @@ def embedding_backward(tokens: torch.Tensor, grad: torch.Tensor, vocab: int, sca
     row v is ``scale * tree(grad rows with token v, in order)``, tree being
     the canonical reduction's (L = 1). ``out`` receives it; with
     ``accumulate`` it is added to ``out``, whose rows without tokens stay."""
-    device = _device(grad, "grad")
-    if grad.dim() != tokens.dim() + 1 or tuple(grad.shape[:-1]) != tuple(tokens.shape):
+    index = _device(grad, "grad")
+    if grad.dim() != tokens.dim() + 1 or grad.shape[:-1] != tokens.shape:
         raise ValueError("grad must have the shape of tokens and a channel axis")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if vocab < 0:
         raise ValueError("vocab must be >= 0")
-    dt = _type_code(grad)
-    tok, nbytes = _indices(tokens, "tokens", None, device)
+    code = _type_code(grad)
+    tok = _indices(tokens, "tokens", None, index)
     n, dim = tok.numel(), grad.shape[-1]
     rows = _rows(grad if grad.dim() == 2 else grad.reshape(n, dim))
     if n > 1 and rows.stride(0) < dim:  # rows repeated by a zero stride
         rows = rows.contiguous()
-    on = _On(device, stream)
-    o = _output(on, out, (vocab, dim), torch.float32)
-    ws = on.workspace(lib().cr_embedding_backward_workspace_bytes(n, vocab, dim),
+    on = _On(index, stream)
+    o = on.output(out, (vocab, dim), _F32)
+    ws = on.workspace(_size("cr_embedding_backward_workspace_bytes", n, vocab, dim),
                       "embedding_backward")
-    on.reads(tok, rows)
-    on.call("cr_embedding_backward", _ptr(tok), nbytes, n, _ptr(rows),
-            rows.stride(0) if n > 1 else dim, vocab, dim, float(scale), dt, int(accumulate),
-            _ptr(o), o.stride(0) if vocab > 1 else dim, ws.data_ptr(), ws.numel())
+    on.run(_c_embedding_backward, (tok, rows, o), tok.data_ptr(), tok.element_size(), n,
+           rows.data_ptr(), rows.stride(0) if n > 1 else dim, vocab, dim, scale, code,
+           int(accumulate), o.data_ptr(), o.stride(0) if vocab > 1 else dim, ws.data_ptr(),
+           ws.numel())
     return o
 
 
@@ -217,24 +270,33 @@ def _activation(name) -> int:
 
 
 def _conv_args(x, weight, bias, activation, state, lengths):
-    device = _device(x, "x")
+    index = _device(x, "x")
     if x.dim() != 3:
         raise ValueError("x must be (batch, time, channel)")
-    dt = _type_code(x)
+    code = _type_code(x)
     batch, T, dim = x.shape
     if weight.dim() != 2:
         raise ValueError("weight must be (channel, width)")
     K = weight.shape[1]
-    _like(weight, "weight", (dim, K), torch.float32, device)
-    _like(bias, "bias", (dim,), torch.float32, device)
-    _like(state, "state", (batch, K - 1, dim), x.dtype, device)
-    lengths, ib = _indices(lengths, "lengths", (batch,), device)
-    x, weight = _rows(x), weight.contiguous()
-    bias = None if bias is None else bias.contiguous()
-    state = None if state is None else state.contiguous()
-    a = _ConvArgs(batch, T, dim, K, _activation(activation), dt, ib, _ptr(x), x.stride(0),
-                  x.stride(1), _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths))
-    return device, a, (x, weight, bias, state, lengths)
+    _need(weight, "weight", (dim, K), _F32, index)
+    x, weight = _rows(x), _dense(weight)
+    b = st = ln = 0
+    if bias is not None:
+        _need(bias, "bias", (dim,), _F32, index)
+        bias = _dense(bias)
+        b = bias.data_ptr()
+    if state is not None:
+        _need(state, "state", (batch, K - 1, dim), x.dtype, index)
+        state = _dense(state)
+        st = state.data_ptr()
+    ib = 4
+    if lengths is not None:
+        lengths = _indices(lengths, "lengths", (batch,), index)
+        ln, ib = lengths.data_ptr(), lengths.element_size()
+    xs = x.stride()
+    a = _pack_conv(batch, T, dim, K, _activation(activation), code, ib, x.data_ptr(), xs[0], xs[1],
+                   weight.data_ptr(), b, st, ln)
+    return index, a, (x, weight, bias, state, lengths)
 
 
 def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
@@ -247,12 +309,15 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None
     the inputs before time 0 (zeros without it). ``lengths`` (batch): later
     positions are not read and give zeros. Returns y, or (y, state after the
     last position) with ``return_state``."""
-    device, a, held = _conv_args(x, weight, bias, activation, state, lengths)
-    on = _On(device, stream)
-    y = _output(on, out, tuple(x.shape), x.dtype)
-    final = on.empty((a.batch, a.width - 1, a.dim), x.dtype) if return_state else None
-    on.reads(*held)
-    on.call("cr_causal_conv", ctypes.byref(a), _ptr(y), y.stride(0), y.stride(1), _ptr(final))
+    index, a, held = _conv_args(x, weight, bias, activation, state, lengths)
+    on = _On(index, stream)
+    y = on.like(x) if out is None else on.output(out, x.shape, x.dtype)
+    final = None
+    if return_state:
+        final = on.empty((x.shape[0], weight.shape[1] - 1, x.shape[2]), x.dtype)
+    ys = y.stride()
+    on.run(_c_conv, held + (y,), a, y.data_ptr(), ys[0], ys[1],
+           final.data_ptr() if return_state else None)
     return (y, final) if return_state else y
 
 
@@ -263,27 +328,28 @@ def causal_conv_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     """The gradients of :func:`causal_conv` for the same arguments: a dict
     with "x" and "weight", and "bias" and "state" where those were given.
     ``dfinal``: the gradient of the returned state, if it was used."""
-    device, a, held = _conv_args(x, weight, bias, activation, state, lengths)
-    _like(dy, "dy", x.shape, x.dtype, device)
-    _like(dfinal, "dfinal", (a.batch, a.width - 1, a.dim), x.dtype, device)
+    index, a, held = _conv_args(x, weight, bias, activation, state, lengths)
+    (batch, T, dim), K = x.shape, weight.shape[1]
+    _need(dy, "dy", x.shape, x.dtype, index)
     dy = _rows(dy)
-    dfinal = None if dfinal is None else dfinal.contiguous()
-    on = _On(device, stream)
-    g = {"x": on.empty(tuple(x.shape), x.dtype), "weight": on.empty((a.dim, a.width),
-                                                                   torch.float32)}
+    if dfinal is not None:
+        _need(dfinal, "dfinal", (batch, K - 1, dim), x.dtype, index)
+        dfinal = _dense(dfinal)
+    on = _On(index, stream)
+    g = {"x": on.like(x), "weight": on.like(weight)}
+    db = ds = 0
     if bias is not None:
-        g["bias"] = on.empty((a.dim,), torch.float32)
+        g["bias"] = on.like(bias)
+        db = g["bias"].data_ptr()
     if state is not None:
-        g["state"] = on.empty((a.batch, a.width - 1, a.dim), x.dtype)
-    ws = on.workspace(lib().cr_causal_conv_backward_workspace_bytes(a.batch, a.len, a.dim,
-                                                                    a.width),
+        g["state"] = on.like(state)
+        ds = g["state"].data_ptr()
+    ws = on.workspace(_size("cr_causal_conv_backward_workspace_bytes", batch, T, dim, K),
                       "causal_conv_backward")
-    c = _ConvGrads(_ptr(dy), dy.stride(0), dy.stride(1), _ptr(dfinal), _ptr(g["x"]),
-                   g["x"].stride(0), g["x"].stride(1), _ptr(g["weight"]), _ptr(g.get("bias")),
-                   _ptr(g.get("state")))
-    on.reads(dy, dfinal, *held)
-    on.call("cr_causal_conv_backward", ctypes.byref(a), ctypes.byref(c), ws.data_ptr(),
-            ws.numel())
+    ys, xs = dy.stride(), g["x"].stride()
+    c = _pack_conv_grads(dy.data_ptr(), ys[0], ys[1], 0 if dfinal is None else dfinal.data_ptr(),
+                         g["x"].data_ptr(), xs[0], xs[1], g["weight"].data_ptr(), db, ds)
+    on.run(_c_conv_backward, held + (dy, dfinal), a, c, ws.data_ptr(), ws.numel())
     return g
 
 
@@ -296,80 +362,96 @@ def causal_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor,
     contiguous; stream b uses row ``slots[b]`` (b without slots); a slot
     outside [0, rows) is padding (zeros, no state changes). Slots must differ.
     Returns y (batch, dim)."""
-    device = _device(x, "x")
+    index = _device(x, "x")
     if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be (batch, dim), weight (dim, K), state (rows, K-1, dim)")
-    dt = _type_code(x)
+    code = _type_code(x)
     batch, dim = x.shape
-    K = weight.shape[1]
-    _like(weight, "weight", (dim, K), torch.float32, device)
-    _like(bias, "bias", (dim,), torch.float32, device)
-    _like(state, "state", (state.shape[0], K - 1, dim), x.dtype, device)
+    K, rows = weight.shape[1], state.shape[0]
+    _need(weight, "weight", (dim, K), _F32, index)
+    _need(state, "state", (rows, K - 1, dim), x.dtype, index)
     if not state.is_contiguous():
         raise ValueError("state must be contiguous (it is updated in place)")
-    if slots is None and state.shape[0] < batch:
+    x, weight = _rows(x), _dense(weight)
+    b = sl = 0
+    ib = 4
+    if bias is not None:
+        _need(bias, "bias", (dim,), _F32, index)
+        bias = _dense(bias)
+        b = bias.data_ptr()
+    if slots is not None:
+        slots = _indices(slots, "slots", (batch,), index)
+        sl, ib = slots.data_ptr(), slots.element_size()
+    elif rows < batch:
         raise ValueError("state must have a row for each of the %d streams" % batch)
-    slots, ib = _indices(slots, "slots", (batch,), device)
-    x, weight = _rows(x), weight.contiguous()
-    bias = None if bias is None else bias.contiguous()
-    on = _On(device, stream)
-    y = _output(on, out, (batch, dim), x.dtype)
-    on.reads(x, state, weight, bias, slots)
-    on.call("cr_causal_conv_step", _ptr(x), x.stride(0), _ptr(state), state.shape[0],
-            _ptr(slots), ib, _ptr(weight), _ptr(bias), _activation(activation), batch, dim, K,
-            dt, _ptr(y), y.stride(0))
+    on = _On(index, stream)
+    y = on.like(x) if out is None else on.output(out, x.shape, x.dtype)
+    on.run(_c_conv_step, (x, state, weight, bias, slots, y), x.data_ptr(), x.stride(0),
+           state.data_ptr(), rows, sl, ib, weight.data_ptr(), b, _activation(activation), batch,
+           dim, K, code, y.data_ptr(), y.stride(0))
     return y
 
 
 # ------------------------------------------------------ selective scan
+def _states(t, name, lead, N, dtype, index):
+    """B or C as (..., groups, N) with the last two axes contiguous."""
+    if t.dim() == len(lead) + 1:  # one group
+        t = t.unsqueeze(-2)
+    _need(t, name, lead + (t.shape[-2], N), dtype, index)
+    s = t.stride()
+    if (N > 1 and s[-1] != 1) or (t.shape[-2] > 1 and s[-2] != N):
+        t = t.contiguous()
+    return t
+
+
 def _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, step):
-    device = _device(u, "u")
-    lead = 1 if step else 2
-    if u.dim() != lead + 1:
+    """(device index, packed argument block, tensors that it points to)."""
+    index = _device(u, "u")
+    shape, dtype = u.shape, u.dtype
+    if len(shape) != (2 if step else 3):
         raise ValueError("u must be (batch, dim)" if step else "u must be (batch, time, dim)")
     code = _type_code(u)
-    batch, dim = u.shape[0], u.shape[-1]
-    T = 1 if step else u.shape[1]
+    batch, dim = shape[0], shape[-1]
     if A.dim() != 2:
         raise ValueError("A must be (dim, dstate)")
     N = A.shape[1]
-    if B.dim() == lead + 1:  # one group
-        B = B.unsqueeze(lead)
-    if C.dim() == lead + 1:
-        C = C.unsqueeze(lead)
-    groups = B.shape[lead] if B.dim() == lead + 2 else 0
-    if groups < 1 or dim % groups:
-        raise ValueError("B must be (..., groups, dstate) with groups dividing dim")
-    _like(dt, "dt", u.shape, u.dtype, device)
-    _like(z, "z", u.shape, u.dtype, device)
-    _like(B, "B", tuple(u.shape[:-1]) + (groups, N), u.dtype, device)
-    _like(C, "C", tuple(u.shape[:-1]) + (groups, N), u.dtype, device)
-    _like(A, "A", (dim, N), torch.float32, device)
-    _like(D, "D", (dim,), torch.float32, device)
-    _like(dt_bias, "dt_bias", (dim,), torch.float32, device)
-    u, dt, z = _rows(u), _rows(dt), _rows(z)
-    if N > 1 and (B.stride(-1) != 1 or (groups > 1 and B.stride(-2) != N)):
-        B = B.contiguous()
-    if N > 1 and (C.stride(-1) != 1 or (groups > 1 and C.stride(-2) != N)):
-        C = C.contiguous()
-    if N == 1 and groups > 1:
-        B, C = B.contiguous(), C.contiguous()
-    A = A.contiguous()
-    D = None if D is None else D.contiguous()
-    dt_bias = None if dt_bias is None else dt_bias.contiguous()
-    if not step:
-        _like(state, "state", (batch, dim, N), torch.float32, device)
-        state = None if state is None else state.contiguous()
-    lengths, ib = _indices(lengths, "slots" if step else "lengths", (batch,), device)
-    t = 0 if step else 1
-
-    def strides(v):
-        return (None, 0, 0) if v is None else (_ptr(v), v.stride(0), v.stride(t) if t else 0)
-
-    a = _ScanArgs(batch, T, dim, N, groups, int(bool(softplus)), code, ib, 0, *strides(u),
-                  *strides(dt), *strides(z), *strides(B), *strides(C), _ptr(A), _ptr(D),
-                  _ptr(dt_bias), None if step else _ptr(state), None if step else _ptr(lengths))
-    return device, a, (u, dt, z, B, C, A, D, dt_bias, state, lengths)
+    _need(A, "A", (dim, N), _F32, index)
+    _need(dt, "dt", shape, dtype, index)
+    B = _states(B, "B", shape[:-1], N, dtype, index)
+    C = _states(C, "C", shape[:-1], N, dtype, index)
+    groups = B.shape[-2]
+    if groups < 1 or dim % groups or C.shape[-2] != groups:
+        raise ValueError("B and C must be (..., groups, dstate) with groups dividing dim")
+    u, dt, A = _rows(u), _rows(dt), _dense(A)
+    us, ds, bs, cs = u.stride(), dt.stride(), B.stride(), C.stride()
+    zs = (0, 0)
+    zp = Dp = bp = sp = lp = 0
+    if z is not None:
+        _need(z, "z", shape, dtype, index)
+        z = _rows(z)
+        zs, zp = z.stride(), z.data_ptr()
+    if D is not None:
+        _need(D, "D", (dim,), _F32, index)
+        D = _dense(D)
+        Dp = D.data_ptr()
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", (dim,), _F32, index)
+        dt_bias = _dense(dt_bias)
+        bp = dt_bias.data_ptr()
+    if state is not None:
+        _need(state, "state", (batch, dim, N), _F32, index)
+        state = _dense(state)
+        sp = state.data_ptr()
+    ib = 4
+    if lengths is not None:  # of a step: its slots
+        lengths = _indices(lengths, "slots" if step else "lengths", (batch,), index)
+        ib = lengths.element_size()
+        lp = 0 if step else lengths.data_ptr()
+    a = _pack_scan(batch, 1 if step else shape[1], dim, N, groups, 1 if softplus else 0, code, ib,
+                   0, u.data_ptr(), us[0], us[1], dt.data_ptr(), ds[0], ds[1], zp, zs[0], zs[1],
+                   B.data_ptr(), bs[0], bs[1], C.data_ptr(), cs[0], cs[1], A.data_ptr(), Dp, bp,
+                   sp, lp)
+    return index, a, (u, dt, z, B, C, A, D, dt_bias, state, lengths)
 
 
 def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -393,21 +475,24 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     zeros and leave the state. Returns y, followed by the last state
     (``return_state``) and the checkpoints that the backward call takes
     (``return_checkpoints``)."""
-    device, a, held = _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, False)
-    on = _On(device, stream)
-    y = _output(on, out, tuple(u.shape), u.dtype)
-    final = on.empty((a.batch, a.dim, a.dstate), torch.float32) if return_state else None
-    kept = None
+    index, a, held = _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, False)
+    (batch, T, dim), N = u.shape, A.shape[1]
+    on = _On(index, stream)
+    y = on.like(u) if out is None else on.output(out, u.shape, u.dtype)
+    final = kept = None
+    if return_state:
+        final = on.empty((batch, dim, N), _F32)
     if return_checkpoints:
-        kept = on.empty((a.batch, lib().cr_selective_scan_checkpoints(a.len), a.dim, a.dstate),
-                        torch.float32)
-    ws = on.workspace(lib().cr_selective_scan_workspace_bytes(a.batch, a.len, a.dim, a.dstate),
+        kept = on.empty((batch, _size("cr_selective_scan_checkpoints", T), dim, N), _F32)
+    ws = on.workspace(_size("cr_selective_scan_workspace_bytes", batch, T, dim, N),
                       "selective_scan")
-    on.reads(*held)
-    on.call("cr_selective_scan", ctypes.byref(a), _ptr(y), y.stride(0), y.stride(1), _ptr(final),
-            _ptr(kept), ws.data_ptr(), ws.numel())
-    result = (y,) + ((final,) if return_state else ()) + ((kept,) if return_checkpoints else ())
-    return result if len(result) > 1 else y
+    ys = y.stride()
+    on.run(_c_scan, held + (y,), a, y.data_ptr(), ys[0], ys[1],
+           final.data_ptr() if return_state else None,
+           kept.data_ptr() if return_checkpoints else None, ws.data_ptr(), ws.numel())
+    if return_state:
+        return (y, final, kept) if return_checkpoints else (y, final)
+    return (y, kept) if return_checkpoints else y
 
 
 def selective_scan_backward(dy: torch.Tensor, u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
@@ -422,39 +507,33 @@ def selective_scan_backward(dy: torch.Tensor, u: torch.Tensor, dt: torch.Tensor,
     those were given. ``dfinal``: the gradient of the returned state, if it
     was used. ``checkpoints``: from the forward call (computed again without
     them)."""
-    device, a, held = _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, False)
-    _like(dy, "dy", u.shape, u.dtype, device)
-    _like(dfinal, "dfinal", (a.batch, a.dim, a.dstate), torch.float32, device)
-    n_check = lib().cr_selective_scan_checkpoints(a.len)
+    index, a, held = _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, False)
+    (batch, T, dim), N, groups = u.shape, A.shape[1], held[3].shape[-2]
+    _need(dy, "dy", u.shape, u.dtype, index)
+    dy = _rows(dy)
+    if dfinal is not None:
+        _need(dfinal, "dfinal", (batch, dim, N), _F32, index)
+        dfinal = _dense(dfinal)
     if checkpoints is None:
         checkpoints = selective_scan(u, dt, A, B, C, D, None, dt_bias, softplus, state, lengths,
                                      return_checkpoints=True, stream=stream)[1]
-    _like(checkpoints, "checkpoints", (a.batch, n_check, a.dim, a.dstate), torch.float32, device)
+    _need(checkpoints, "checkpoints",
+          (batch, _size("cr_selective_scan_checkpoints", T), dim, N), _F32, index)
     if not checkpoints.is_contiguous():
         raise ValueError("checkpoints must be contiguous, as the forward call returns them")
-    dy = _rows(dy)
-    dfinal = None if dfinal is None else dfinal.contiguous()
-    on = _On(device, stream)
-    f32 = torch.float32
-    g = {"u": on.empty(tuple(u.shape), u.dtype), "dt": on.empty(tuple(u.shape), u.dtype),
-         "A": on.empty((a.dim, a.dstate), f32), "B": on.empty(tuple(B.shape), u.dtype),
-         "C": on.empty(tuple(C.shape), u.dtype)}
-    if D is not None:
-        g["D"] = on.empty((a.dim,), f32)
-    if z is not None:
-        g["z"] = on.empty(tuple(u.shape), u.dtype)
-    if dt_bias is not None:
-        g["dt_bias"] = on.empty((a.dim,), f32)
-    if state is not None:
-        g["state"] = on.empty((a.batch, a.dim, a.dstate), f32)
-    ws = on.workspace(lib().cr_selective_scan_backward_workspace_bytes(
-        a.batch, a.len, a.dim, a.dstate, a.groups), "selective_scan_backward")
-    c = _ScanGrads(_ptr(dy), dy.stride(0), dy.stride(1), _ptr(dfinal), _ptr(checkpoints),
-                   *(_ptr(g.get(k)) for k in ("u", "dt", "z", "B", "C", "A", "D", "dt_bias",
-                                              "state")))
-    on.reads(dy, dfinal, checkpoints, *held)
-    on.call("cr_selective_scan_backward", ctypes.byref(a), ctypes.byref(c), ws.data_ptr(),
-            ws.numel())
+    on = _On(index, stream)
+    g = {"u": on.like(u), "dt": on.like(dt), "A": on.like(A), "B": on.like(B), "C": on.like(C)}
+    for name, t in (("D", D), ("z", z), ("dt_bias", dt_bias), ("state", state)):
+        if t is not None:
+            g[name] = on.like(t)
+    ws = on.workspace(_size("cr_selective_scan_backward_workspace_bytes", batch, T, dim, N, groups),
+                      "selective_scan_backward")
+    ys = dy.stride()
+    c = _pack_scan_grads(dy.data_ptr(), ys[0], ys[1], 0 if dfinal is None else dfinal.data_ptr(),
+                         checkpoints.data_ptr(),
+                         *(g[k].data_ptr() if k in g else 0
+                           for k in ("u", "dt", "z", "B", "C", "A", "D", "dt_bias", "state")))
+    on.run(_c_scan_backward, held + (dy, dfinal, checkpoints), a, c, ws.data_ptr(), ws.numel())
     return g
 
 
@@ -468,19 +547,20 @@ def selective_scan_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
     dstate), float32, contiguous, is updated in place; stream b uses row
     ``slots[b]`` (b without slots); a slot outside [0, rows) is padding
     (zeros, no state changes). Slots must differ. Returns y (batch, dim)."""
-    device, a, held = _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, None, slots, True)
+    index, a, held = _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus, None, slots, True)
+    batch, dim = u.shape
     if state.dim() != 3:
         raise ValueError("state must be (rows, dim, dstate)")
-    _like(state, "state", (state.shape[0], a.dim, a.dstate), torch.float32, device)
+    rows = state.shape[0]
+    _need(state, "state", (rows, dim, A.shape[1]), _F32, index)
     if not state.is_contiguous():
         raise ValueError("state must be contiguous (it is updated in place)")
-    if slots is None and state.shape[0] < a.batch:
-        raise ValueError("state must have a row for each of the %d streams" % a.batch)
-    on = _On(device, stream)
-    y = _output(on, out, (a.batch, a.dim), u.dtype)
-    on.reads(state, *held)
-    on.call("cr_selective_scan_step", ctypes.byref(a), _ptr(state), state.shape[0],
-            _ptr(held[-1]), _ptr(y), y.stride(0))
+    if slots is None and rows < batch:
+        raise ValueError("state must have a row for each of the %d streams" % batch)
+    on = _On(index, stream)
+    y = on.like(u) if out is None else on.output(out, u.shape, u.dtype)
+    on.run(_c_scan_step, held + (state, y), a, state.data_ptr(), rows,
+           None if slots is None else held[-1].data_ptr(), y.data_ptr(), y.stride(0))
     return y
 
 
