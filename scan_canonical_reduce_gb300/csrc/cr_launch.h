@@ -46,6 +46,7 @@ enum KernelId : int {
   kKScanSeqLeft2,
   kKEmbedding,
   kKTokenSort,
+  kKEmbeddingLong,
   kKEmbeddingRows,
   kKCausalConv,
   kKCausalConvBackward,

@@ -103,6 +103,18 @@ def test_gradient_of_one_frequent_token(scr, count):
     assert got.cpu().numpy().tobytes() == want_grad(tok, grad, V, 1.0).tobytes()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,D,count", [(5000, 40, 1030, 3000), (700, 9, 520, 577),
+                                         (9000, 700, 260, 8200)])
+def test_gradient_of_long_rows(scr, dtype, n, V, D, count):
+    """Long rows of many columns beside short ones: several warps to a row."""
+    tok = torch.randint(0, V, (n,), generator=gen(22))
+    tok[torch.randperm(n, generator=gen(23))[:count]] = 3
+    grad = torch.randn(n, D, generator=gen(24)).to(dtype)
+    got = scr.embedding_backward(tok.to(DEV), grad.to(DEV), V, 0.5)
+    assert got.cpu().numpy().tobytes() == want_grad(tok, grad, V, 0.5).tobytes()
+
+
 def test_gradient_large_vocabulary(scr):
     """More rows than one block sorts, and tokens of 32 bits."""
     n, V, D = 3000, 200_003, 4
