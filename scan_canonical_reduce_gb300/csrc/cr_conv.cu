@@ -5,9 +5,11 @@
 //   dpre[t] = dy[t] act'(pre[t])
 //   dx[p] = sum_{k<K} w[k] dpre[p+(K-1)-k],  dw[k] = sum_t dpre[t] x[t-(K-1)+k]
 //
-// A thread takes V neighbouring channels and a run of time steps, and keeps
-// the last K inputs (backward: and the last K of dpre) in registers, so that
-// each input is read once, plus K-1 steps of halo a run.
+// A thread takes four neighbouring channels, as two pairs for the packed
+// arithmetic, and a run of time steps, and keeps the last K inputs (backward:
+// and the last K of dpre) in registers, so that each input is read once, plus
+// K-1 steps of halo a run. Steps go in groups, the next group's reads in
+// flight.
 #include <cstdint>
 
 #include "cr_device.cuh"
@@ -22,17 +24,22 @@ constexpr int kV = 4;  // channels a thread
 
 struct ConvShape {
   int64_t batch, len, dim;
-  int64_t runs;       // runs of kRun steps a sequence (at least 1)
+  int64_t run;        // steps a thread takes
+  int64_t runs;       // of a sequence (at least 1)
   int64_t col_blocks; // blocks along the channels
 };
-constexpr int kRun = 64;
 
+// Runs of 64 steps read 5 % of halo (K = 4) and keep the backward's partial
+// sums small; where that leaves too few threads they are halved, down to 16.
+// A rule on sizes alone: the sums over time depend on it.
 ConvShape conv_shape(int64_t batch, int64_t len, int64_t dim) {
   ConvShape c;
   c.batch = batch;
   c.len = len;
   c.dim = dim;
-  c.runs = len > 0 ? ceil_div(len, kRun) : 1;
+  c.run = 64;
+  while (c.run > 16 && batch * ceil_div(len, c.run) * ceil_div(dim, kV) < 100000) c.run /= 2;
+  c.runs = len > 0 ? ceil_div(len, c.run) : 1;
   c.col_blocks = ceil_div(dim, kConvThreads * kV);
   return c;
 }
@@ -65,21 +72,75 @@ __device__ __forceinline__ void conv_input(const ConvIn<T>& in, const ConvShape&
   }
 }
 
+// Four channels as two pairs.
+struct Quad {
+  F2 p[2];
+};
+
+__device__ __forceinline__ Quad quad(const float (&f)[kV]) {
+  return {{pack2(f[0], f[1]), pack2(f[2], f[3])}};
+}
+__device__ __forceinline__ void unquad(const Quad& q, float (&f)[kV]) {
+  unpack2(q.p[0], f[0], f[1]);
+  unpack2(q.p[1], f[2], f[3]);
+}
+template <class T>
+__device__ __forceinline__ Quad quad(const Raw<T, kV>& r) {
+  return {{pack2(r.get(0), r.get(1)), pack2(r.get(2), r.get(3))}};
+}
+
 template <int K>
 __device__ __forceinline__ void conv_weights(const float* weight, const float* bias, int64_t c,
-                                             int have, float (&w)[K][kV], float (&b0)[kV]) {
+                                             int have, Quad (&w)[K], Quad& b0) {
+  float f[kV];
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    b0[j] = (bias != nullptr && j < have) ? bias[c + j] : 0.0f;
+  for (int j = 0; j < kV; ++j) f[j] = (bias != nullptr && j < have) ? bias[c + j] : 0.0f;
+  b0 = quad(f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][j] = j < have ? weight[(c + j) * K + k] : 0.0f;
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) f[j] = j < have ? weight[(c + j) * K + k] : 0.0f;
+    w[k] = quad(f);
   }
 }
+
+// pre = bias + sum_k w[k] x[k], k upwards.
+template <int K>
+__device__ __forceinline__ Quad conv_pre(const Quad (&w)[K], const Quad& b0, const Quad* x) {
+  Quad p = b0;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p.p[i] = fma2(w[k].p[i], x[k].p[i], p.p[i]);
+  return p;
+}
+
+__device__ __forceinline__ void conv_act(bool silu, float (&f)[kV]) {
+  if (silu) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) f[j] = f[j] * sigmoid(f[j]);
+  }
+}
+
+// Rows [t, t + U) of a tensor's four channels; rows at or past `end` are zero
+// and not read.
+template <class T, int U>
+__device__ __forceinline__ void load_group(const T* p, int64_t ts, int64_t t, int64_t end,
+                                           bool wide, int have, Raw<T, kV> (&r)[U]) {
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (t + i < end) r[i].load(p + (t + i) * ts, wide, have);
+    else r[i].zero();
+  }
+}
+
+constexpr int kForward = 8, kBackward = 4;  // steps of a group
 
 template <class T, int K>
 __global__ void __launch_bounds__(kConvThreads)
 causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, int64_t yts,
                    bool wide_y, T* __restrict__ final_state) {
+  constexpr int U = kForward;
   int64_t i = blockIdx.x;
   const int64_t c = (i % sh.col_blocks * kConvThreads + threadIdx.x) * kV;
   i /= sh.col_blocks;
@@ -87,35 +148,40 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
   if (c >= sh.dim) return;
   const int have = (int)min((int64_t)kV, sh.dim - c);
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
-  const int64_t t0 = run * kRun, t1 = min(sh.len, t0 + kRun);
-  const bool wy = wide_y && have == kV;
+  const int64_t t0 = run * sh.run, t1 = min(sh.len, t0 + sh.run), stop = min(t1, len);
+  const bool wy = wide_y && have == kV, wx = in.wide && have == kV;
+  const T* x = in.x + b * in.bs + c;
+  y += b * ybs + c;
 
-  if (t0 < len) {
-    float w[K][kV], b0[kV], win[K][kV];
+  if (t0 < stop) {
+    Raw<T, kV> next[U];
+    load_group<T, U>(x, in.ts, t0, stop, wx, have, next);
+    Quad w[K], b0, win[K - 1 + U];
     conv_weights<K>(in.weight, in.bias, c, have, w, b0);
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k)
-      conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, win[k + 1]);
-    for (int64_t t = t0; t < min(t1, len); ++t) {
+    for (int k = 0; k < K - 1; ++k) {
+      float f[kV];
+      conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, f);
+      win[k] = quad(f);
+    }
+#pragma unroll 1
+    for (int64_t t = t0; t < stop; t += U) {
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k)
+      for (int u = 0; u < U; ++u) win[K - 1 + u] = quad(next[u]);
+      if (t + U < stop) load_group<T, U>(x, in.ts, t + U, stop, wx, have, next);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) win[k][j] = win[k + 1][j];
-      conv_input<T, K>(in, sh, b, t, c, have, win[K - 1]);
-      float o[kV];
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        float p = b0[j];
-#pragma unroll
-        for (int k = 0; k < K; ++k) p = fmaf(w[k][j], win[k][j], p);
-        o[j] = in.silu ? p * sigmoid(p) : p;
+      for (int u = 0; u < U; ++u) {
+        float f[kV];
+        unquad(conv_pre<K>(w, b0, win + u), f);
+        conv_act(in.silu, f);
+        if (t + u < stop) store_f32<T, kV>(y + (t + u) * yts, wy, have, f);
       }
-      store_f32<T, kV>(y + b * ybs + t * yts + c, wy, have, o);
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) win[k] = win[U + k];
     }
   }
   const float zero[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t t = max(t0, len); t < t1; ++t)
-    store_f32<T, kV>(y + b * ybs + t * yts + c, wy, have, zero);
+  for (int64_t t = max(t0, len); t < t1; ++t) store_f32<T, kV>(y + t * yts, wy, have, zero);
   if (run == 0 && final_state != nullptr) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
@@ -143,8 +209,9 @@ struct ConvBack {
 // dx of its own steps (run 0: of the state's too) and the sums of
 // dpre x and dpre over its own steps.
 template <class T, int K>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, 4)
 causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
+  constexpr int U = kBackward;
   int64_t i = blockIdx.x;
   const int64_t c = (i % sh.col_blocks * kConvThreads + threadIdx.x) * kV;
   i /= sh.col_blocks;
@@ -152,105 +219,134 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
   if (c >= sh.dim) return;
   const int have = (int)min((int64_t)kV, sh.dim - c);
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
-  const int64_t t0 = run * kRun, t1 = min(sh.len, t0 + kRun);
+  const int64_t t0 = run * sh.run, t1 = min(sh.len, t0 + sh.run);
+  const bool wide = in.wide && have == kV, wide_dx = g.wide_dx && have == kV;
+  const bool wide_state = in.wide_state && have == kV;
+  const T* x = in.x + b * in.bs + c;
+  const T* dy = g.dy + b * g.dybs + c;
+  T* dx = g.dx + b * g.dxbs + c;
+  const int64_t final0 = len - (K - 1);  // the first of the state's positions
 
-  float w[K][kV], b0[kV], win[K][kV], dp[K][kV], dw[K][kV], db[kV];
-  conv_weights<K>(in.weight, in.bias, c, have, w, b0);
+  Quad dw[K], db = {{0, 0}};
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int j = 0; j < kV; ++j) win[k][j] = dp[k][j] = dw[k][j] = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kV; ++j) db[j] = 0.0f;
+  for (int k = 0; k < K; ++k) dw[k] = {{0, 0}};
   if (t0 < len || run == 0) {
+    Raw<T, kV> nx[U], ny[U];
+    load_group<T, U>(x, in.ts, t0, len, wide, have, nx);
+    load_group<T, U>(dy, g.dyts, t0, len, wide, have, ny);
+    Quad w[K], b0, win[K - 1 + U], dp[K - 1 + U];
+    conv_weights<K>(in.weight, in.bias, c, have, w, b0);
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k)
-      conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, win[k + 1]);
-    // after step t the window dp holds dpre[t-K+1 .. t], which completes
-    // dx at p = t - K + 1
-    for (int64_t t = t0; t < t1 + K - 1; ++t) {
+    for (int k = 0; k < K - 1; ++k) {
+      float f[kV];
+      conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, f);
+      win[k] = quad(f);
+      dp[k] = {{0, 0}};
+    }
+    // after step t the window of dpre ends at t, which completes dx at
+    // p = t - (K - 1)
+#pragma unroll 1
+    for (int64_t t = t0; t < t1 + K - 1; t += U) {
+      Quad d[U];
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k)
+      for (int u = 0; u < U; ++u) {
+        win[K - 1 + u] = quad(nx[u]);
+        d[u] = quad(ny[u]);
+      }
+      if (t + U < t1 + K - 1) {
+        load_group<T, U>(x, in.ts, t + U, len, wide, have, nx);
+        load_group<T, U>(dy, g.dyts, t + U, len, wide, have, ny);
+      }
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          win[k][j] = win[k + 1][j];
-          dp[k][j] = dp[k + 1][j];
+      for (int u = 0; u < U; ++u) {
+        if (in.silu) {
+          float f[kV], s[kV];
+          unquad(conv_pre<K>(w, b0, win + u), f);
+#pragma unroll
+          for (int j = 0; j < kV; ++j) s[j] = sigmoid(f[j]);
+          // act' = s (1 + pre (1 - s)) = s + (pre s) (1 - s)
+#pragma unroll
+          for (int j = 0; j < kV; ++j) f[j] = fmaf(f[j] * s[j], 1.0f - s[j], s[j]);
+          const Quad a = quad(f);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) d[u].p[j] = mul2(d[u].p[j], a.p[j]);
         }
-      if (t < len) {
-        float d[kV];
-        conv_input<T, K>(in, sh, b, t, c, have, win[K - 1]);
-        load_f32<T, kV>(g.dy + b * g.dybs + t * g.dyts + c, in.wide && have == kV, have, d);
+        dp[K - 1 + u] = d[u];  // zero past the sequence, as dy is
+        if (t + u < t1) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          float p = b0[j];
+          for (int j = 0; j < 2; ++j) {
+            db.p[j] = add2(db.p[j], d[u].p[j]);
 #pragma unroll
-          for (int k = 0; k < K; ++k) p = fmaf(w[k][j], win[k][j], p);
-          if (in.silu) {
-            const float s = sigmoid(p);
-            d[j] = d[j] * (s * fmaf(p, 1.0f - s, 1.0f));
-          }
-          dp[K - 1][j] = d[j];
-          if (t < t1) {
-            db[j] += d[j];
-#pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][j] = fmaf(d[j], win[k][j], dw[k][j]);
+            for (int k = 0; k < K; ++k) dw[k].p[j] = fma2(d[u].p[j], win[u + k].p[j], dw[k].p[j]);
           }
         }
-      } else {
+        const int64_t p = t + u - (K - 1);
+        if ((p >= t0 || run == 0) && p < t1) {  // earlier ones are the run before's
+          Quad o = {{0, 0}};
 #pragma unroll
-        for (int j = 0; j < kV; ++j) dp[K - 1][j] = 0.0f;
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              o.p[j] = fma2(w[k].p[j], dp[u + K - 1 - k].p[j], o.p[j]);
+          float f[kV];
+          unquad(o, f);
+          if (g.dfinal != nullptr && p >= final0 && p < len) {
+            float e[kV];
+            load_f32<T, kV>(g.dfinal + (b * (K - 1) + (p - final0)) * sh.dim + c, wide_state, have,
+                            e);
+#pragma unroll
+            for (int j = 0; j < kV; ++j) f[j] += e[j];
+          }
+          if (p >= 0) {
+            if (g.dx != nullptr) store_f32<T, kV>(dx + p * g.dxts, wide_dx, have, f);
+          } else if (g.dstate != nullptr) {
+            store_f32<T, kV>(g.dstate + (b * (K - 1) + (K - 1 + p)) * sh.dim + c, wide_state, have,
+                             f);
+          }
+        }
       }
-      const int64_t p = t - (K - 1);
-      if (p < t0 && run != 0) continue;  // the run before writes it
-      float o[kV];
 #pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        o[j] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) o[j] = fmaf(w[k][j], dp[K - 1 - k][j], o[j]);
-      }
-      if (g.dfinal != nullptr && p >= len - (K - 1) && p < len) {
-        float f[kV];
-        load_f32<T, kV>(g.dfinal + (b * (K - 1) + (p - (len - (K - 1)))) * sh.dim + c,
-                        in.wide_state && have == kV, have, f);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) o[j] += f[j];
-      }
-      if (p >= 0) {
-        if (g.dx != nullptr && p < sh.len)
-          store_f32<T, kV>(g.dx + b * g.dxbs + p * g.dxts + c, g.wide_dx && have == kV, have, o);
-      } else if (g.dstate != nullptr) {
-        store_f32<T, kV>(g.dstate + (b * (K - 1) + (K - 1 + p)) * sh.dim + c,
-                         in.wide_state && have == kV, have, o);
+      for (int k = 0; k < K - 1; ++k) {
+        win[k] = win[U + k];
+        dp[k] = dp[U + k];
       }
     }
   } else if (g.dx != nullptr) {
     const float zero[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t t = t0; t < t1; ++t)
-      store_f32<T, kV>(g.dx + b * g.dxbs + t * g.dxts + c, g.wide_dx && have == kV, have, zero);
+    for (int64_t t = t0; t < t1; ++t) store_f32<T, kV>(dx + t * g.dxts, wide_dx, have, zero);
   }
-  float* part = g.part + ((b * sh.runs + run) * sh.dim + c) * (K + 1);
+  // [run][K + 1][dim]: neighbouring threads write neighbours
+  float* part = g.part + (b * sh.runs + run) * (K + 1) * sh.dim + c;
+  const bool wp = sh.dim % kV == 0;
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    if (j < have) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) part[j * (K + 1) + k] = dw[k][j];
-      part[j * (K + 1) + K] = db[j];
-    }
+  for (int k = 0; k <= K; ++k) {
+    float f[kV];
+    unquad(k < K ? dw[k < K ? k : 0] : db, f);
+    store_f32<float, kV>(part + k * sh.dim, wp, have, f);
   }
 }
 
-// Sums the runs' partials in order: thread i takes one (channel, tap).
-__global__ void __launch_bounds__(kConvThreads)
+// Sums the runs' partials: eight threads take every eighth run of a column
+// (tap and channel) in order, then one adds the eight.
+__global__ void __launch_bounds__(256)
 causal_conv_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t dim, int K,
                        float* __restrict__ dweight, float* __restrict__ dbias) {
+  __shared__ float sums[8][32];
   const int64_t n = dim * (K + 1);
-  const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  if (i >= n) return;
+  const int lane = threadIdx.x % 32, row = threadIdx.x / 32;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int64_t p = 0; p < parts; ++p) s += part[p * n + i];
-  const int64_t d = i / (K + 1);
-  const int k = (int)(i % (K + 1));
+  if (i < n) {
+#pragma unroll 8
+    for (int64_t p = row; p < parts; p += 8) s += part[p * n + i];
+  }
+  sums[row][lane] = s;
+  __syncthreads();
+  if (row != 0 || i >= n) return;
+#pragma unroll
+  for (int r = 1; r < 8; ++r) s += sums[r][lane];
+  const int64_t d = i % dim;
+  const int k = (int)(i / dim);
   if (k < K) dweight[d * K + k] = s;
   else if (dbias != nullptr) dbias[d] = s;
 }
@@ -270,22 +366,26 @@ causal_conv_step_kernel(const T* __restrict__ x, int64_t x_stride, T* __restrict
   const int64_t row = slots != nullptr ? load_index(slots, index_bytes, b) : b;
   float o[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (row >= 0 && row < state_rows) {
-    float w[K][kV], b0[kV], win[K][kV];
-    conv_weights<K>(weight, bias, c, have, w, b0);
+    Quad win[K];
     T* st = state + row * (K - 1) * dim + c;
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) load_f32<T, kV>(st + k * dim, wide_state && full, have, win[k]);
-    load_f32<T, kV>(x + b * x_stride + c, wide && full, have, win[K - 1]);
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      float p = b0[j];
-#pragma unroll
-      for (int k = 0; k < K; ++k) p = fmaf(w[k][j], win[k][j], p);
-      o[j] = silu ? p * sigmoid(p) : p;
+    for (int k = 0; k < K - 1; ++k) {
+      float f[kV];
+      load_f32<T, kV>(st + k * dim, wide_state && full, have, f);
+      win[k] = quad(f);
     }
+    Quad w[K], b0;
+    conv_weights<K>(weight, bias, c, have, w, b0);
+    float f[kV];
+    load_f32<T, kV>(x + b * x_stride + c, wide && full, have, f);
+    win[K - 1] = quad(f);
+    unquad(conv_pre<K>(w, b0, win), o);
+    conv_act(silu, o);
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k)
-      store_f32<T, kV>(st + k * dim, wide_state && full, have, win[k + 1]);
+    for (int k = 0; k < K - 1; ++k) {
+      unquad(win[k + 1], f);
+      store_f32<T, kV>(st + k * dim, wide_state && full, have, f);
+    }
   }
   store_f32<T, kV>(y + b * y_stride + c, wide && full, have, o);
 }
@@ -435,7 +535,7 @@ cr_status cr_causal_conv_backward(const cr_causal_conv_args* a, const cr_causal_
   }
   const int64_t n = a->dim * (a->width + 1);
   CR_LAUNCH(kKCausalConvSum, s,
-            causal_conv_sum_kernel<<<(unsigned)ceil_div(n, kConvThreads), kConvThreads, 0, s>>>(
+            causal_conv_sum_kernel<<<(unsigned)ceil_div(n, 32), 256, 0, s>>>(
                 static_cast<const float*>(ws), a->batch * sh.runs, a->dim, a->width, g->dweight,
                 g->dbias));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
