@@ -122,22 +122,38 @@ __device__ __forceinline__ void conv_act(bool silu, float (&f)[kV]) {
   }
 }
 
-// Rows [t, t + U) of a tensor's four channels; rows at or past `end` are zero
-// and not read.
-template <class T, int U>
-__device__ __forceinline__ void load_group(const T* p, int64_t ts, int64_t t, int64_t end,
-                                           bool wide, int have, Raw<T, kV> (&r)[U]) {
+// U rows of a tensor's four channels from p on. kFull: all of them exist and
+// are read whole; otherwise the first `rows` do, the others are zero and not
+// read. Most groups are full, and the checks cost more than their arithmetic.
+template <bool kFull, class T, int U>
+__device__ __forceinline__ void load_group(const T* p, int64_t ts, int rows, bool wide, int have,
+                                           Raw<T, kV> (&r)[U]) {
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    if (t + i < end) r[i].load(p + (t + i) * ts, wide, have);
+    if (kFull) r[i].load(p + i * ts, true, kV);
+    else if (i < rows) r[i].load(p + i * ts, wide, have);
     else r[i].zero();
   }
 }
 
-constexpr int kForward = 8, kBackward = 4;  // steps of a group
+template <bool kFull, class T>
+__device__ __forceinline__ void store_row(T* p, bool wide, int have, const float (&f)[kV]) {
+  store_f32<T, kV>(p, kFull || wide, kFull ? kV : have, f);
+}
 
+#ifndef CR_CONV_FORWARD
+#define CR_CONV_FORWARD 8
+#endif
+constexpr int kForward = CR_CONV_FORWARD, kBackward = 4;  // steps of a group
+
+#ifndef CR_CONV_BLOCKS
+#define CR_CONV_BLOCKS 4
+#endif
+#ifndef CR_CONV_BACK_BLOCKS
+#define CR_CONV_BACK_BLOCKS 3
+#endif
 template <class T, int K>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, CR_CONV_BLOCKS)
 causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, int64_t yts,
                    bool wide_y, T* __restrict__ final_state) {
   constexpr int U = kForward;
@@ -150,12 +166,15 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
   const int64_t t0 = run * sh.run, t1 = min(sh.len, t0 + sh.run), stop = min(t1, len);
   const bool wy = wide_y && have == kV, wx = in.wide && have == kV;
-  const T* x = in.x + b * in.bs + c;
   y += b * ybs + c;
 
   if (t0 < stop) {
+    const int rows = (int)(stop - t0);
+    const T* x = in.x + b * in.bs + t0 * in.ts + c;  // of the next group
+    T* o = y + t0 * yts;
     Raw<T, kV> next[U];
-    load_group<T, U>(x, in.ts, t0, stop, wx, have, next);
+    load_group<false, T, U>(x, in.ts, rows, wx, have, next);
+    x += U * in.ts;
     Quad w[K], b0, win[K - 1 + U];
     conv_weights<K>(in.weight, in.bias, c, have, w, b0);
 #pragma unroll
@@ -164,21 +183,30 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
       conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, f);
       win[k] = quad(f);
     }
-#pragma unroll 1
-    for (int64_t t = t0; t < stop; t += U) {
+    auto group = [&](auto full, int left) {
+      constexpr bool kFull = decltype(full)::value;
 #pragma unroll
       for (int u = 0; u < U; ++u) win[K - 1 + u] = quad(next[u]);
-      if (t + U < stop) load_group<T, U>(x, in.ts, t + U, stop, wx, have, next);
+      load_group<kFull, T, U>(x, in.ts, left - U, wx, have, next);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float f[kV];
         unquad(conv_pre<K>(w, b0, win + u), f);
         conv_act(in.silu, f);
-        if (t + u < stop) store_f32<T, kV>(y + (t + u) * yts, wy, have, f);
+        if (kFull || u < left) store_row<kFull>(o + u * yts, wy, have, f);
       }
 #pragma unroll
       for (int k = 0; k < K - 1; ++k) win[k] = win[U + k];
+      x += U * in.ts;
+      o += U * yts;
+    };
+    int left = rows;
+    if (wx && wy) {
+#pragma unroll 1
+      for (; left >= 2 * U; left -= U) group(std::true_type{}, left);
     }
+#pragma unroll 1
+    for (; left > 0; left -= U) group(std::false_type{}, left);
   }
   const float zero[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int64_t t = max(t0, len); t < t1; ++t) store_f32<T, kV>(y + t * yts, wy, have, zero);
@@ -209,7 +237,7 @@ struct ConvBack {
 // dx of its own steps (run 0: of the state's too) and the sums of
 // dpre x and dpre over its own steps.
 template <class T, int K>
-__global__ void __launch_bounds__(kConvThreads, 4)
+__global__ void __launch_bounds__(kConvThreads, CR_CONV_BACK_BLOCKS)
 causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
   constexpr int U = kBackward;
   int64_t i = blockIdx.x;
@@ -222,8 +250,6 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
   const int64_t t0 = run * sh.run, t1 = min(sh.len, t0 + sh.run);
   const bool wide = in.wide && have == kV, wide_dx = g.wide_dx && have == kV;
   const bool wide_state = in.wide_state && have == kV;
-  const T* x = in.x + b * in.bs + c;
-  const T* dy = g.dy + b * g.dybs + c;
   T* dx = g.dx + b * g.dxbs + c;
   const int64_t final0 = len - (K - 1);  // the first of the state's positions
 
@@ -231,9 +257,14 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
 #pragma unroll
   for (int k = 0; k < K; ++k) dw[k] = {{0, 0}};
   if (t0 < len || run == 0) {
+    const T* x = in.x + b * in.bs + t0 * in.ts + c;  // of the next group
+    const T* dy = g.dy + b * g.dybs + t0 * g.dyts + c;
     Raw<T, kV> nx[U], ny[U];
-    load_group<T, U>(x, in.ts, t0, len, wide, have, nx);
-    load_group<T, U>(dy, g.dyts, t0, len, wide, have, ny);
+    const int rows = (int)min(len - t0, (int64_t)1 << 30);  // that exist, from t0 on
+    load_group<false, T, U>(x, in.ts, rows, wide, have, nx);
+    load_group<false, T, U>(dy, g.dyts, rows, wide, have, ny);
+    x += U * in.ts;
+    dy += U * g.dyts;
     Quad w[K], b0, win[K - 1 + U], dp[K - 1 + U];
     conv_weights<K>(in.weight, in.bias, c, have, w, b0);
 #pragma unroll
@@ -243,36 +274,37 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
       win[k] = quad(f);
       dp[k] = {{0, 0}};
     }
-    // after step t the window of dpre ends at t, which completes dx at
-    // p = t - (K - 1)
-#pragma unroll 1
-    for (int64_t t = t0; t < t1 + K - 1; t += U) {
+    const int own = (int)(t1 - t0);  // steps of this run
+    T* o = dx + (t0 - (K - 1)) * g.dxts;  // of position t - (K - 1)
+    // After step t the window of dpre ends at t, which completes dx at t -
+    // (K - 1). Full: steps and positions all lie inside the run and the
+    // sequence (and the next group's rows inside the sequence).
+    auto group = [&](auto full, int s) {
+      constexpr bool kFull = decltype(full)::value;
       Quad d[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         win[K - 1 + u] = quad(nx[u]);
         d[u] = quad(ny[u]);
       }
-      if (t + U < t1 + K - 1) {
-        load_group<T, U>(x, in.ts, t + U, len, wide, have, nx);
-        load_group<T, U>(dy, g.dyts, t + U, len, wide, have, ny);
-      }
+      load_group<kFull, T, U>(x, in.ts, rows - s - U, wide, have, nx);
+      load_group<kFull, T, U>(dy, g.dyts, rows - s - U, wide, have, ny);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (in.silu) {
-          float f[kV], s[kV];
+          float f[kV], sg[kV];
           unquad(conv_pre<K>(w, b0, win + u), f);
 #pragma unroll
-          for (int j = 0; j < kV; ++j) s[j] = sigmoid(f[j]);
+          for (int j = 0; j < kV; ++j) sg[j] = sigmoid(f[j]);
           // act' = s (1 + pre (1 - s)) = s + (pre s) (1 - s)
 #pragma unroll
-          for (int j = 0; j < kV; ++j) f[j] = fmaf(f[j] * s[j], 1.0f - s[j], s[j]);
+          for (int j = 0; j < kV; ++j) f[j] = fmaf(f[j] * sg[j], 1.0f - sg[j], sg[j]);
           const Quad a = quad(f);
 #pragma unroll
           for (int j = 0; j < 2; ++j) d[u].p[j] = mul2(d[u].p[j], a.p[j]);
         }
         dp[K - 1 + u] = d[u];  // zero past the sequence, as dy is
-        if (t + u < t1) {
+        if (kFull || s + u < own) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             db.p[j] = add2(db.p[j], d[u].p[j]);
@@ -280,28 +312,33 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
             for (int k = 0; k < K; ++k) dw[k].p[j] = fma2(d[u].p[j], win[u + k].p[j], dw[k].p[j]);
           }
         }
-        const int64_t p = t + u - (K - 1);
-        if ((p >= t0 || run == 0) && p < t1) {  // earlier ones are the run before's
-          Quad o = {{0, 0}};
+        const int q = s + u - (K - 1);  // the position, from t0
+        if (kFull || ((q >= 0 || run == 0) && q < own)) {  // others: the run before's
+          Quad v = {{0, 0}};
 #pragma unroll
           for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              o.p[j] = fma2(w[k].p[j], dp[u + K - 1 - k].p[j], o.p[j]);
+              v.p[j] = fma2(w[k].p[j], dp[u + K - 1 - k].p[j], v.p[j]);
           float f[kV];
-          unquad(o, f);
-          if (g.dfinal != nullptr && p >= final0 && p < len) {
-            float e[kV];
-            load_f32<T, kV>(g.dfinal + (b * (K - 1) + (p - final0)) * sh.dim + c, wide_state, have,
-                            e);
+          unquad(v, f);
+          if (kFull) {
+            store_row<true>(o + u * g.dxts, wide_dx, have, f);
+          } else {
+            const int64_t p = t0 + q;
+            if (g.dfinal != nullptr && p >= final0 && p < len) {
+              float e[kV];
+              load_f32<T, kV>(g.dfinal + (b * (K - 1) + (p - final0)) * sh.dim + c, wide_state,
+                              have, e);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) f[j] += e[j];
-          }
-          if (p >= 0) {
-            if (g.dx != nullptr) store_f32<T, kV>(dx + p * g.dxts, wide_dx, have, f);
-          } else if (g.dstate != nullptr) {
-            store_f32<T, kV>(g.dstate + (b * (K - 1) + (K - 1 + p)) * sh.dim + c, wide_state, have,
-                             f);
+              for (int j = 0; j < kV; ++j) f[j] += e[j];
+            }
+            if (p >= 0) {
+              if (g.dx != nullptr) store_row<false>(o + u * g.dxts, wide_dx, have, f);
+            } else if (g.dstate != nullptr) {
+              store_f32<T, kV>(g.dstate + (b * (K - 1) + (K - 1 + p)) * sh.dim + c, wide_state,
+                               have, f);
+            }
           }
         }
       }
@@ -310,7 +347,21 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
         win[k] = win[U + k];
         dp[k] = dp[U + k];
       }
+      x += U * in.ts;
+      dy += U * g.dyts;
+      o += U * g.dxts;
+    };
+    static_assert(U >= K - 1, "the group after the first has no position before the run");
+    int s = 0;
+    group(std::false_type{}, s);
+    s += U;
+    if (wide && wide_dx && g.dx != nullptr) {
+      const int full = (int)min((int64_t)own, (int64_t)rows - U);  // the last with a next group
+#pragma unroll 1
+      for (; s + U <= full; s += U) group(std::true_type{}, s);
     }
+#pragma unroll 1
+    for (; s < own + K - 1; s += U) group(std::false_type{}, s);
   } else if (g.dx != nullptr) {
     const float zero[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int64_t t = t0; t < t1; ++t) store_f32<T, kV>(dx + t * g.dxts, wide_dx, have, zero);
