@@ -43,6 +43,15 @@ __device__ __forceinline__ void load_states(const T* p, int n0, int N, float (&f
 }
 
 // A lane's states in a row of N floats; wide: N % 4 == 0 and 16-byte rows.
+__device__ __forceinline__ void read_states(const float* p, int n0, int N, bool wide,
+                                            float (&f)[kS]) {
+  if (wide && n0 < N) {
+    const float4 v = *reinterpret_cast<const float4*>(p + n0);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  } else {
+    load_states(p, n0, N, f);
+  }
+}
 __device__ __forceinline__ void store_states(float* p, int n0, int N, bool wide,
                                              const float (&f)[kS]) {
   if (wide) {
@@ -262,7 +271,7 @@ struct ScanOut {
 };
 
 #ifndef CR_SCAN_UNROLL
-#define CR_SCAN_UNROLL 2
+#define CR_SCAN_UNROLL 4
 #endif
 #ifndef CR_SCAN_BLOCKS
 #define CR_SCAN_BLOCKS 4
@@ -383,35 +392,40 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
     // recurrence
     const float4* dl = dd + TL::slot(0, c);
     const float4 *Bl = Bs + 2 * g, *Cl = Cs + 2 * g;
-#pragma unroll kUnroll
-    for (int t4 = 0; t4 < TL::TT / 4; ++t4) {
-      if (!kStates && out.checkpoints != nullptr && t4 * 4 % kCheckpoint == 0 && live &&
-          t0 + t4 * 4 < end) {
+    float* yl = ys + c;
+#pragma unroll 1
+    for (int tb = 0; tb < TL::TT; tb += kCheckpoint) {
+      if (!kStates && out.checkpoints != nullptr && live && t0 + tb < end)
         store_states(out.checkpoints +
-                         ((b * out.n_check + (t0 + t4 * 4) / kCheckpoint) * in.dim + d) * in.N,
+                         ((b * out.n_check + (t0 + tb) / kCheckpoint) * in.dim + d) * in.N,
                      n0, in.N, out.wide_check, h);
-      }
-      F2 p[2];
+      // straight code: the reads and decays of later steps run ahead
+#pragma unroll kUnroll
+      for (int t4 = 0; t4 < kCheckpoint / 4; ++t4) {
+        F2 p[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int tp = t4 * 2 + j;
-        const float4 e = dl[tp * TL::CH];
-        if (kStates) total = add2(total, pack2(e.x, e.y));
-        p[j] = lane_steps<!kStates>(A, h, e, Bl + tp * 2 * G, Cl + (kStates ? 0 : tp * 2 * G));
-      }
-      if (!kStates) {
-        float v[4];
-        sum_lanes4<G>(p[0], p[1], g, v);
-        float* y = ys + t4 * 4 * TL::YS + c;
-        if (G == 1) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k * TL::YS] = v[k];
-        } else if (G == 2) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) y[(2 * g + k) * TL::YS] = v[k];
-        } else if (G == 4 || g < 4) {
-          y[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
+        for (int j = 0; j < 2; ++j) {
+          const float4 e = dl[j * TL::CH];
+          if (kStates) total = add2(total, pack2(e.x, e.y));
+          p[j] = lane_steps<!kStates>(A, h, e, Bl + j * 2 * G, kStates ? Bl : Cl + j * 2 * G);
         }
+        if (!kStates) {
+          float v[4];
+          sum_lanes4<G>(p[0], p[1], g, v);
+          if (G == 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) yl[k * TL::YS] = v[k];
+          } else if (G == 2) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) yl[(2 * g + k) * TL::YS] = v[k];
+          } else if (G == 4 || g < 4) {
+            yl[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
+          }
+          Cl += 4 * G;
+          yl += 4 * TL::YS;
+        }
+        dl += 2 * TL::CH;
+        Bl += 4 * G;
       }
     }
     __syncthreads();
@@ -629,12 +643,7 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
     rB.load(left, pB);
     rC.load(left, pC);
     const float* q = o.checkpoints + ((b * o.n_check + tile) * in.dim + d) * in.N;
-    if (o.wide_check && n0 < in.N) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(q + n0));
-      next[0] = f.x, next[1] = f.y, next[2] = f.z, next[3] = f.w;
-    } else {
-      load_states(q, n0, in.N, next);
-    }
+    read_states(q, n0, in.N, o.wide_check, next);
   };
   if (tiles > 0) load(tiles - 1);
   __syncthreads();  // Ds, biases
@@ -912,42 +921,42 @@ selective_scan_sum_a_kernel(const float* __restrict__ part, int64_t batch, int64
   else if (k == N + 1 && dbias != nullptr) dbias[d] = s;
 }
 
+// One token: a thread takes four states of a channel, 16 bytes at a time
+// where rows allow it.
 template <class T, int G>
 __global__ void __launch_bounds__(kScanThreads)
 selective_scan_step_kernel(ScanIn<T> in, float* __restrict__ state, int64_t state_rows,
-                           const void* __restrict__ slots, T* __restrict__ y, int64_t ybs) {
+                           const void* __restrict__ slots, T* __restrict__ y, int64_t ybs,
+                           bool wide, bool wide_BC) {
   const Place p = place<G>(in.group_dim, in.groups);
   const int n0 = p.g * kS;
   const int64_t slot = slots != nullptr ? load_index(slots, in.index_bytes, p.b) : p.b;
   float o = 0.0f;
   if (slot >= 0 && slot < state_rows) {  // the same for the whole block
     float* st = state + (slot * in.dim + p.d) * in.N;
-    float A[kS], B[kS], C[kS], h[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
-    load_states(in.A + p.d * in.N, n0, in.N, A);
-    load_states(in.B + p.b * in.Bbs + (int64_t)p.group * in.N, n0, in.N, B);
-    load_states(in.C + p.b * in.Cbs + (int64_t)p.group * in.N, n0, in.N, C);
-    if (p.live) load_states(st, n0, in.N, h);
+    float A[kS], h[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
+    Raw<T, kS> B, C;
+    if (p.live) read_states(st, n0, in.N, wide, h);
+    read_states(in.A + p.d * in.N, n0, in.N, wide, A);
+    const int have = min(kS, in.N - n0);
+    B.load(in.B + p.b * in.Bbs + (int64_t)p.group * in.N + n0, wide_BC && have == kS, have);
+    C.load(in.C + p.b * in.Cbs + (int64_t)p.group * in.N + n0, wide_BC && have == kS, have);
     const float u = to_f32(in.u[p.b * in.ubs + p.d]);
     float delta = to_f32(in.dt[p.b * in.dbs + p.d]);
+    const float z = in.z != nullptr ? to_f32(in.z[p.b * in.zbs + p.d]) : 0.0f;
+    const float D = in.D != nullptr ? in.D[p.d] : 0.0f;
     if (in.dt_bias != nullptr) delta += in.dt_bias[p.d];
     if (in.softplus) delta = softplus(delta);
     const float du = delta * u;
     float acc = 0.0f;
 #pragma unroll
     for (int k = 0; k < kS; ++k) {
-      h[k] = fmaf(exp2_fast(delta * (A[k] * kLog2e)), h[k], du * B[k]);
-      acc = k == 0 ? C[k] * h[k] : fmaf(C[k], h[k], acc);
+      h[k] = fmaf(exp2_fast(delta * (A[k] * kLog2e)), h[k], du * B.get(k));
+      acc = k == 0 ? C.get(k) * h[k] : fmaf(C.get(k), h[k], acc);
     }
-    o = fmaf(in.D != nullptr ? in.D[p.d] : 0.0f, u, sum_lanes<G>(acc));
-    if (in.z != nullptr) {
-      const float z = to_f32(in.z[p.b * in.zbs + p.d]);
-      o *= z * sigmoid(z);
-    }
-    if (p.live) {
-#pragma unroll
-      for (int k = 0; k < kS; ++k)
-        if (n0 + k < in.N) st[n0 + k] = h[k];
-    }
+    o = fmaf(D, u, sum_lanes<G>(acc));
+    if (in.z != nullptr) o *= z * sigmoid(z);
+    if (p.live) store_states(st, n0, in.N, wide, h);
   }
   if (p.live && p.g == 0) y[p.b * ybs + p.d] = from_f32<T>(o);
 }
@@ -1260,10 +1269,14 @@ cr_status cr_selective_scan_step(const cr_selective_scan_args* a, float* state,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int lanes = scan_lanes(a->dstate);
   const unsigned blocks = (unsigned)scan_blocks(a->batch, a->dim, a->groups, lanes);
+  const bool wide = a->dstate % kS == 0 && ptr_aligned(state, 16) && ptr_aligned(a->A, 16);
+  const bool wide_BC = a->dstate % kS == 0 && rows_aligned(a->B, a->B_batch_stride, 0, es, kS * es) &&
+                       rows_aligned(a->C, a->C_batch_stride, 0, es, kS * es);
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
     CR_LAUNCH(kKSelectiveScanStep, s,
               selective_scan_step_kernel<T, G><<<blocks, kScanThreads, 0, s>>>(
-                  scan_in<T>(a), state, state_rows, slots, static_cast<T*>(y), y_batch_stride));
+                  scan_in<T>(a), state, state_rows, slots, static_cast<T*>(y), y_batch_stride, wide,
+                  wide_BC));
   }));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
