@@ -1,7 +1,9 @@
 """Builds libcr.so, the CUDA library of this package, for sm_103a (GB300).
 
 Each translation unit is compiled in parallel with nvcc, then linked into a
-shared library next to this file (``_build/libcr.so``). The flags keep every
+shared library next to this file (``_build/libcr.so``). Beside it goes
+``_build/cr_model_binding.so``, the Python side of the model operators, which
+is host code against PyTorch's headers. The flags keep every
 floating-point add an explicit round-to-nearest operation: no FMA
 contraction, no flush-to-zero, IEEE division and square root, never
 --use_fast_math.
@@ -9,15 +11,19 @@ contraction, no flush-to-zero, IEEE division and square root, never
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libcr.so")
+BINDING_SRC = os.path.join(CSRC, "model_binding.cpp")
+BINDING = os.path.join(OUT_DIR, "cr_model_binding.so")
 SOURCES = ["cr_api.cu", "cr_calibrate.cu", "cr_chain.cu", "cr_conv.cu", "cr_embedding.cu",
            "cr_host_batched.cu", "cr_launch.cu", "cr_noalloc.cu", "cr_reduce.cu",
            "cr_reduce_policy.cu", "cr_scan.cu", "cr_selective_scan.cu"]
@@ -48,6 +54,20 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command(nvcc: str, out: str) -> list:
+    """g++ on the binding, with PyTorch's headers and libraries found without
+    importing it."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    include = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            *("-I" + d for d in include), BINDING_SRC, "-o", out,
+            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False, defines=(), out_dir: str | None = None) -> str:
     """Compiles the sources (those changed since their object, or all with
     force) and links the library; returns its path. `defines` ("NAME=value"
@@ -69,14 +89,21 @@ def build(force: bool = False, verbose: bool = False, defines=(), out_dir: str |
         objs.append(o)
         if force or _stale(o, s):
             jobs.append([nvcc, *flags, "-c", s, "-o", o])
+    link = bool(jobs)
+    new_binding = None
+    if out_dir is None and (force or _stale(BINDING, BINDING_SRC)):
+        new_binding = BINDING + ".tmp.%d" % os.getpid()
+        jobs.append(_binding_command(nvcc, new_binding))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             for r in ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs):
                 if verbose or r.returncode:
                     print(r.stdout + r.stderr)
                 if r.returncode:
-                    raise RuntimeError("nvcc failed: " + " ".join(r.args))
-    if force or jobs or not os.path.exists(lib):
+                    raise RuntimeError("compilation failed: " + " ".join(r.args))
+    if new_binding is not None:
+        os.replace(new_binding, BINDING)
+    if force or link or not os.path.exists(lib):
         tmp = lib + ".tmp.%d" % os.getpid()
         subprocess.run([nvcc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs], check=True)
         os.replace(tmp, lib)
