@@ -157,10 +157,9 @@ __global__ void __launch_bounds__(kConvThreads, CR_CONV_BLOCKS)
 causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, int64_t yts,
                    bool wide_y, T* __restrict__ final_state) {
   constexpr int U = kForward;
-  int64_t i = blockIdx.x;
-  const int64_t c = (i % sh.col_blocks * kConvThreads + threadIdx.x) * kV;
-  i /= sh.col_blocks;
-  const int64_t run = i % sh.runs, b = i / sh.runs;
+  int64_t c, run;
+  const int64_t b = divide(divide(blockIdx.x, sh.col_blocks, c), sh.runs, run);
+  c = (c * kConvThreads + threadIdx.x) * kV;
   if (c >= sh.dim) return;
   const int have = (int)min((int64_t)kV, sh.dim - c);
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
@@ -240,10 +239,9 @@ template <class T, int K>
 __global__ void __launch_bounds__(kConvThreads, CR_CONV_BACK_BLOCKS)
 causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
   constexpr int U = kBackward;
-  int64_t i = blockIdx.x;
-  const int64_t c = (i % sh.col_blocks * kConvThreads + threadIdx.x) * kV;
-  i /= sh.col_blocks;
-  const int64_t run = i % sh.runs, b = i / sh.runs;
+  int64_t c, run;
+  const int64_t b = divide(divide(blockIdx.x, sh.col_blocks, c), sh.runs, run);
+  c = (c * kConvThreads + threadIdx.x) * kV;
   if (c >= sh.dim) return;
   const int have = (int)min((int64_t)kV, sh.dim - c);
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
@@ -396,8 +394,8 @@ causal_conv_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t di
   if (row != 0 || i >= n) return;
 #pragma unroll
   for (int r = 1; r < 8; ++r) s += sums[r][lane];
-  const int64_t d = i % dim;
-  const int k = (int)(i / dim);
+  int64_t d;
+  const int k = (int)divide(i, dim, d);
   if (k < K) dweight[d * K + k] = s;
   else if (dbias != nullptr) dbias[d] = s;
 }
@@ -409,8 +407,9 @@ causal_conv_step_kernel(const T* __restrict__ x, int64_t x_stride, T* __restrict
                         const float* __restrict__ weight, const float* __restrict__ bias,
                         bool silu, int64_t dim, int64_t col_blocks, bool wide, bool wide_state,
                         T* __restrict__ y, int64_t y_stride) {
-  const int64_t b = blockIdx.x / col_blocks;
-  const int64_t c = (blockIdx.x % col_blocks * kConvThreads + threadIdx.x) * kV;
+  int64_t c;
+  const int64_t b = divide(blockIdx.x, col_blocks, c);
+  c = (c * kConvThreads + threadIdx.x) * kV;
   if (c >= dim) return;
   const int have = (int)min((int64_t)kV, dim - c);
   const bool full = have == kV;

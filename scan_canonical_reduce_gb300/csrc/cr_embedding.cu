@@ -228,10 +228,11 @@ template <class T>
 __device__ __forceinline__ void sum_part(const Grad<T>& grad, const Sorted& in, int64_t item,
                                          int64_t dim, int64_t part_warps, float* sums) {
   const int lane = threadIdx.x % 32;
-  const int64_t k = item / part_warps;
+  int64_t c0;
+  const int64_t k = divide(item, part_warps, c0);
   const int32_t first = in.part[k];
   if (first < 0) return;
-  const int64_t c0 = item % part_warps * kPartColumns + lane * 4;
+  c0 = c0 * kPartColumns + lane * 4;
   const int32_t at = in.order[first + lane % kLong];
   const int64_t pitch = (dim + 3) / 4 * 4;
 #pragma unroll 1
@@ -415,7 +416,9 @@ embedding_long_kernel(Grad<T> grad, Sorted in, const float* __restrict__ sums, i
                       int64_t dim, int64_t long_warps, Table out) {
   const int lane = threadIdx.x % 32;
   const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int64_t k = item / long_warps * kLongParts, c = item % long_warps * 128 + lane * 4;
+  int64_t c;
+  const int64_t k = divide(item, long_warps, c) * kLongParts;
+  c = c * 128 + lane * 4;
   const int32_t v = lane < kLongParts && k + lane < parts ? in.part_row[k + lane] : -1;
   for (uint32_t todo = __ballot_sync(~0u, v >= 0); todo != 0; todo &= todo - 1) {
     const int i = __ffs(todo) - 1;
@@ -446,12 +449,15 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
     return;
   }
   item -= part_items;
-  const int64_t v = item / row_warps, c0 = item % row_warps * kRowColumns + lane * 4;
+  int64_t begin;  // of the warp's columns
+  const int64_t v = divide(item, row_warps, begin);
+  begin *= kRowColumns;
+  const int64_t c0 = begin + lane * 4;
   if (v >= vocab) return;
   const int32_t first = in.row_start[v], count = in.row_start[v + 1] - first;
   if (count >= kLong || (count == 0 && out.accumulate)) return;
-  const int steps = (int)min((int64_t)kRowSteps, (dim - item % row_warps * kRowColumns + 127) / 128);
-  const bool full = grad.wide && out.wide && c0 - lane * 4 + steps * 128 <= dim;
+  const int steps = (int)min((int64_t)kRowSteps, (dim - begin + 127) / 128);
+  const bool full = grad.wide && out.wide && begin + steps * 128 <= dim;
   auto have = [&](int i) {
     return full ? 4 : (int)max((int64_t)0, min((int64_t)4, dim - c0 - i * 128));
   };

@@ -115,6 +115,20 @@ struct Raw {
   }
 };
 
+// i / d with the remainder in r, for i >= 0 and d > 0: in 32 bits where both
+// fit, since a 64-bit division is about a hundred instructions (three of them
+// took longer than all else of a single-token step).
+__device__ __forceinline__ int64_t divide(int64_t i, int64_t d, int64_t& r) {
+  if (((uint64_t)i | (uint64_t)d) >> 32 == 0) {
+    const uint32_t q = (uint32_t)i / (uint32_t)d;
+    r = (uint32_t)i - q * (uint32_t)d;
+    return q;
+  }
+  const int64_t q = i / d;
+  r = i - q * d;
+  return q;
+}
+
 // An index of 4 or 8 bytes.
 __device__ __forceinline__ int64_t load_index(const void* p, int bytes, int64_t i) {
   return bytes == 8 ? static_cast<const int64_t*>(p)[i]

@@ -84,17 +84,16 @@ struct Place {
 };
 
 template <int G>
-__device__ __forceinline__ Place place(int64_t group_dim, int groups) {
+__device__ __forceinline__ Place place(int64_t group_dim, int groups, int c, int g) {
   constexpr int CH = kScanThreads / G;
   const int64_t per_group = (group_dim + CH - 1) / CH;
   Place p;
-  const int64_t i = blockIdx.x;
-  const int64_t blk = i % (per_group * groups);
-  p.b = i / (per_group * groups);
-  p.group = (int)(blk / per_group);
-  p.c = Lanes<G>::c();
-  p.g = Lanes<G>::g();
-  const int64_t in_group = blk % per_group * CH + p.c;
+  int64_t blk, in_blocks;
+  p.b = divide(blockIdx.x, per_group * groups, blk);
+  p.group = (int)divide(blk, per_group, in_blocks);
+  p.c = c;
+  p.g = g;
+  const int64_t in_group = in_blocks * CH + p.c;
   p.live = in_group < group_dim;
   p.d = p.group * group_dim + (p.live ? in_group : 0);
   return p;
@@ -129,14 +128,13 @@ __device__ __forceinline__ void sum_lanes4(F2 p0, F2 p1, int g, float (&v)[4]) {
   }
 }
 
-// The same sum of one value, for every lane.
+// The same sum of one value where neighbouring lanes share a channel.
 template <int G>
 __device__ __forceinline__ float sum_lanes(float v) {
-  constexpr int L = 32 / G;
 #pragma unroll
-  for (int s = 4; s < G; s *= 2) v += __shfl_xor_sync(~0u, v, s * L);
+  for (int s = 4; s < G; s *= 2) v += __shfl_xor_sync(~0u, v, s);
 #pragma unroll
-  for (int s = 1; s < G && s < 4; s *= 2) v += __shfl_xor_sync(~0u, v, s * L);
+  for (int s = 1; s < G && s < 4; s *= 2) v += __shfl_xor_sync(~0u, v, s);
   return v;
 }
 
@@ -291,11 +289,10 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
   const int tid = threadIdx.x, g = Lanes<G>::g(), c = Lanes<G>::c(), n0 = g * kS;
   const int64_t per_group = (in.group_dim + TL::CH - 1) / TL::CH;
   const int64_t segs = kStates ? sg.count - 1 : sg.count;
-  int64_t i = blockIdx.x;
-  const int64_t blk = i % (per_group * in.groups);
-  i /= per_group * in.groups;
-  const int64_t seg = i % segs, b = i / segs;
-  const int64_t group = blk / per_group, first = blk % per_group * TL::CH;
+  int64_t blk, seg, first;
+  const int64_t i = divide(blockIdx.x, per_group * in.groups, blk), b = divide(i, segs, seg);
+  const int64_t group = divide(blk, per_group, first);
+  first *= TL::CH;
   const int channels = (int)min((int64_t)TL::CH, in.group_dim - first);
   const int64_t d0 = group * in.group_dim + first;
   const bool live = c < channels;
@@ -580,8 +577,9 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
   const int lane_c = c % CS::L;
   const int flip = (CS::L >= 2 && (lane_c & (CS::L / 2))) ? 2 : 0;  // slot k holds state k ^ flip
   const int64_t per_group = (in.group_dim + TL::CH - 1) / TL::CH;
-  const int64_t blk = blockIdx.x % (per_group * in.groups), b = blockIdx.x / (per_group * in.groups);
-  const int64_t group = blk / per_group, first = blk % per_group * TL::CH;
+  int64_t blk, block;
+  const int64_t b = divide(blockIdx.x, per_group * in.groups, blk);
+  const int64_t group = divide(blk, per_group, block), first = block * TL::CH;
   const int channels = (int)min((int64_t)TL::CH, in.group_dim - first);
   const int64_t d0 = group * in.group_dim + first;
   const bool live = c < channels;
@@ -617,8 +615,7 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
       if (o.dz != nullptr) o.dz[at] = from_f32<T>(0.0f);
     }
     for (int k = tid; k < 2 * NP; k += kScanThreads)
-      o.part_BC[(((b * in.len + t) * in.groups + group) * per_group + first / TL::CH) * 2 * NP + k] =
-          0.0f;
+      o.part_BC[((b * in.len + t) * in.groups * per_group + blk) * 2 * NP + k] = 0.0f;
   }
 
   using RowsE = Rows<T, VE, TL::NL, TL::ACC, TL::NV>;
@@ -805,7 +802,7 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
       const int64_t t = t0 + k / (2 * NP) * 2;
       const int64_t stride = (int64_t)in.groups * per_group * 2 * NP;
       float* q = o.part_BC + (b * in.len + t) * stride +
-                 (group * per_group + first / TL::CH) * 2 * NP + k % (2 * NP);
+                 blk * 2 * NP + k % (2 * NP);
       if (t < in.len) q[0] = s.x;
       if (t + 1 < in.len) q[stride] = s.y;
     }
@@ -895,9 +892,9 @@ selective_scan_sum_bc_kernel(const float* __restrict__ part, int64_t rows, int64
                              int N, T* __restrict__ dB, T* __restrict__ dC) {
   const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
   if (i >= rows * 2 * N) return;
-  const int64_t r = i / (2 * N);
-  const int j = (int)(i % (2 * N));
-  const int which = j / N, n = j % N;
+  int64_t j;
+  const int64_t r = divide(i, 2 * N, j);
+  const int which = j >= N, n = (int)j - which * N;
   const float* q = part + r * blocks * 2 * NP + which * NP + n;
   float s = 0.0f;
   for (int64_t w = 0; w < blocks; ++w) s += q[w * 2 * NP];
@@ -914,51 +911,77 @@ selective_scan_sum_a_kernel(const float* __restrict__ part, int64_t batch, int64
   if (i >= n) return;
   float s = 0.0f;
   for (int64_t b = 0; b < batch; ++b) s += part[b * n + i];
-  const int64_t d = i / (N + 2);
-  const int k = (int)(i % (N + 2));
+  int64_t k;
+  const int64_t d = divide(i, N + 2, k);
   if (k < N) dA[d * N + k] = s;
   else if (k == N && dD != nullptr) dD[d] = s;
   else if (k == N + 1 && dbias != nullptr) dbias[d] = s;
 }
 
 // One token: a thread takes four states of a channel, 16 bytes at a time
-// where rows allow it.
-template <class T, int G>
+// where rows allow it, of kStreams streams, whose reads are in flight
+// together and share what belongs to the channel.
+template <class T, int G, int kStreams>
 __global__ void __launch_bounds__(kScanThreads)
 selective_scan_step_kernel(ScanIn<T> in, float* __restrict__ state, int64_t state_rows,
                            const void* __restrict__ slots, T* __restrict__ y, int64_t ybs,
                            bool wide, bool wide_BC) {
-  const Place p = place<G>(in.group_dim, in.groups);
-  const int n0 = p.g * kS;
-  const int64_t slot = slots != nullptr ? load_index(slots, in.index_bytes, p.b) : p.b;
-  float o = 0.0f;
-  if (slot >= 0 && slot < state_rows) {  // the same for the whole block
-    float* st = state + (slot * in.dim + p.d) * in.N;
-    float A[kS], h[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
-    Raw<T, kS> B, C;
-    if (p.live) read_states(st, n0, in.N, wide, h);
-    read_states(in.A + p.d * in.N, n0, in.N, wide, A);
-    const int have = min(kS, in.N - n0);
-    B.load(in.B + p.b * in.Bbs + (int64_t)p.group * in.N + n0, wide_BC && have == kS, have);
-    C.load(in.C + p.b * in.Cbs + (int64_t)p.group * in.N + n0, wide_BC && have == kS, have);
-    const float u = to_f32(in.u[p.b * in.ubs + p.d]);
-    float delta = to_f32(in.dt[p.b * in.dbs + p.d]);
-    const float z = in.z != nullptr ? to_f32(in.z[p.b * in.zbs + p.d]) : 0.0f;
-    const float D = in.D != nullptr ? in.D[p.d] : 0.0f;
-    if (in.dt_bias != nullptr) delta += in.dt_bias[p.d];
-    if (in.softplus) delta = softplus(delta);
-    const float du = delta * u;
-    float acc = 0.0f;
+  // here lane = c G + g: a warp's states are consecutive in memory, and nothing
+  // is shared through a tile
+  const Place p = place<G>(in.group_dim, in.groups, threadIdx.x / G, threadIdx.x % G);
+  const int n0 = p.g * kS, have = min(kS, in.N - n0);
+  const bool wBC = wide_BC && have == kS;
+  const int64_t b0 = p.b * kStreams;  // p.b counts groups of streams
+  float h[kStreams][kS], u[kStreams], delta[kStreams], z[kStreams];
+  Raw<T, kS> B[kStreams], C[kStreams];
+  float* st[kStreams];
+  bool real[kStreams];  // the same for the whole block
 #pragma unroll
-    for (int k = 0; k < kS; ++k) {
-      h[k] = fmaf(exp2_fast(delta * (A[k] * kLog2e)), h[k], du * B.get(k));
-      acc = k == 0 ? C.get(k) * h[k] : fmaf(C.get(k), h[k], acc);
+  for (int i = 0; i < kStreams; ++i) {
+    const int64_t b = b0 + i;
+    const int64_t slot = b >= in.batch ? -1 : slots != nullptr ? load_index(slots, in.index_bytes, b) : b;
+    real[i] = slot >= 0 && slot < state_rows;
+    st[i] = state + ((real[i] ? slot : 0) * in.dim + p.d) * in.N;
+#pragma unroll
+    for (int k = 0; k < kS; ++k) h[i][k] = 0.0f;
+    u[i] = delta[i] = z[i] = 0.0f;
+    B[i].zero();
+    C[i].zero();
+    if (real[i]) {
+      if (p.live) read_states(st[i], n0, in.N, wide, h[i]);
+      B[i].load(in.B + b * in.Bbs + (int64_t)p.group * in.N + n0, wBC, have);
+      C[i].load(in.C + b * in.Cbs + (int64_t)p.group * in.N + n0, wBC, have);
+      u[i] = to_f32(in.u[b * in.ubs + p.d]);
+      delta[i] = to_f32(in.dt[b * in.dbs + p.d]);
+      if (in.z != nullptr) z[i] = to_f32(in.z[b * in.zbs + p.d]);
     }
-    o = fmaf(D, u, sum_lanes<G>(acc));
-    if (in.z != nullptr) o *= z * sigmoid(z);
-    if (p.live) store_states(st, n0, in.N, wide, h);
   }
-  if (p.live && p.g == 0) y[p.b * ybs + p.d] = from_f32<T>(o);
+  float A[kS];
+  read_states(in.A + p.d * in.N, n0, in.N, wide, A);
+  const float D = in.D != nullptr ? in.D[p.d] : 0.0f;
+  const float bias = in.dt_bias != nullptr ? in.dt_bias[p.d] : 0.0f;
+#pragma unroll
+  for (int k = 0; k < kS; ++k) A[k] *= kLog2e;
+#pragma unroll
+  for (int i = 0; i < kStreams; ++i) {
+    if (b0 + i >= in.batch) return;  // the same for the whole block
+    float o = 0.0f;
+    if (real[i]) {
+      float d = delta[i] + bias;
+      if (in.softplus) d = softplus(d);
+      const float du = d * u[i];
+      float acc = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kS; ++k) {
+        h[i][k] = fmaf(exp2_fast(d * A[k]), h[i][k], du * B[i].get(k));
+        acc = k == 0 ? C[i].get(k) * h[i][k] : fmaf(C[i].get(k), h[i][k], acc);
+      }
+      o = fmaf(D, u[i], sum_lanes<G>(acc));
+      if (in.z != nullptr) o *= z[i] * sigmoid(z[i]);
+      if (p.live) store_states(st[i], n0, in.N, wide, h[i]);
+    }
+    if (p.live && p.g == 0) y[(b0 + i) * ybs + p.d] = from_f32<T>(o);
+  }
 }
 
 int scan_lanes(int N) {
@@ -979,6 +1002,9 @@ int64_t scan_blocks(int64_t batch, int64_t dim, int groups, int G) {
 #ifndef CR_SCAN_WARPS
 #define CR_SCAN_WARPS 2432
 #endif
+#ifndef CR_SCAN_LEAST
+#define CR_SCAN_LEAST 1
+#endif
 #ifndef CR_SCAN_SPLIT_BELOW
 #define CR_SCAN_SPLIT_BELOW 700
 #endif
@@ -988,9 +1014,9 @@ Segments scan_segments(int64_t batch, int64_t len, int64_t dim, int lanes) {
   sg.E = sg.sum = nullptr;
   sg.count = 1;
   const int64_t warps = batch * ceil_div(dim * lanes, 32);
-  if (warps < CR_SCAN_SPLIT_BELOW && warps > 0 && len >= 8 * kTile) {
+  if (warps < CR_SCAN_SPLIT_BELOW && warps > 0 && len >= 2 * CR_SCAN_LEAST * kTile) {
     sg.count = CR_SCAN_WARPS / warps;
-    const int64_t most = len / (4 * kTile);
+    const int64_t most = len / (CR_SCAN_LEAST * kTile);
     if (sg.count > most) sg.count = most;
     if (sg.count > 64) sg.count = 64;
   }
@@ -1268,15 +1294,27 @@ cr_status cr_selective_scan_step(const cr_selective_scan_args* a, float* state,
   if (!ptr_aligned(y, es) || !ptr_aligned(state, 4)) return CR_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int lanes = scan_lanes(a->dstate);
-  const unsigned blocks = (unsigned)scan_blocks(a->batch, a->dim, a->groups, lanes);
+  // Several streams a thread where that leaves threads for the whole GPU: 200
+  // streams of 4096 channels take TIME us with four a thread, TIME with one;
+  // one stream of 2048 channels TIME and TIME.
+#ifndef CR_STEP_STREAMS
+#define CR_STEP_STREAMS 4
+#endif
+  const bool many = a->batch >= 8 && a->batch * a->dim * lanes >= (1 << 20);
   const bool wide = a->dstate % kS == 0 && ptr_aligned(state, 16) && ptr_aligned(a->A, 16);
   const bool wide_BC = a->dstate % kS == 0 && rows_aligned(a->B, a->B_batch_stride, 0, es, kS * es) &&
                        rows_aligned(a->C, a->C_batch_stride, 0, es, kS * es);
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
-    CR_LAUNCH(kKSelectiveScanStep, s,
-              selective_scan_step_kernel<T, G><<<blocks, kScanThreads, 0, s>>>(
-                  scan_in<T>(a), state, state_rows, slots, static_cast<T*>(y), y_batch_stride, wide,
-                  wide_BC));
+    auto launch = [&](auto streams) {
+      constexpr int R = decltype(streams)::value;
+      CR_LAUNCH(kKSelectiveScanStep, s,
+                selective_scan_step_kernel<T, G, R>
+                <<<(unsigned)scan_blocks(ceil_div(a->batch, R), a->dim, a->groups, lanes),
+                   kScanThreads, 0, s>>>(scan_in<T>(a), state, state_rows, slots,
+                                         static_cast<T*>(y), y_batch_stride, wide, wide_BC));
+    };
+    if (many) launch(std::integral_constant<int, CR_STEP_STREAMS>{});
+    else launch(std::integral_constant<int, 1>{});
   }));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
