@@ -10,6 +10,7 @@
 //   dA = sum q delta,  dD = sum p u,  dz = dy (C.h + D u) silu'(z)
 //
 // G lanes share a channel, four states each; a warp holds 32 / G channels.
+#include <algorithm>
 #include <cstdint>
 
 #include "cr_device.cuh"
@@ -74,30 +75,6 @@ struct Lanes {
     return threadIdx.x / 32 * kChannels + threadIdx.x % kChannels;
   }
 };
-
-// A block's channels lie in one group: block i of a sequence is block
-// i % per_group of group i / per_group.
-struct Place {
-  int64_t b, d;
-  int group, g, c;
-  bool live;
-};
-
-template <int G>
-__device__ __forceinline__ Place place(int64_t group_dim, int groups, int c, int g) {
-  constexpr int CH = kScanThreads / G;
-  const int64_t per_group = (group_dim + CH - 1) / CH;
-  Place p;
-  int64_t blk, in_blocks;
-  p.b = divide(blockIdx.x, per_group * groups, blk);
-  p.group = (int)divide(blk, per_group, in_blocks);
-  p.c = c;
-  p.g = g;
-  const int64_t in_group = in_blocks * CH + p.c;
-  p.live = in_group < group_dim;
-  p.d = p.group * group_dim + (p.live ? in_group : 0);
-  return p;
-}
 
 // The sum over the G lanes of a channel: as a tree over the bits of g from
 // bit 2 upwards, then bit 0, then bit 1. Two pairs of time steps at once: the
@@ -918,70 +895,109 @@ selective_scan_sum_a_kernel(const float* __restrict__ part, int64_t batch, int64
   else if (k == N + 1 && dbias != nullptr) dbias[d] = s;
 }
 
-// One token: a thread takes four states of a channel, 16 bytes at a time
-// where rows allow it, of kStreams streams, whose reads are in flight
-// together and share what belongs to the channel.
-template <class T, int G, int kStreams>
+// One token. A warp takes 32 channels of a group: first a lane each, for
+// delta, delta u and the gate, then G rounds of 32 / G channels by G lanes
+// each, lane = c G + g, so that a round's states are consecutive in memory.
+// All rounds' reads are in flight together. kWide: rows of states, A, B and C
+// allow accesses of four elements.
+template <class T, int G, bool kWide>
 __global__ void __launch_bounds__(kScanThreads)
 selective_scan_step_kernel(ScanIn<T> in, float* __restrict__ state, int64_t state_rows,
-                           const void* __restrict__ slots, T* __restrict__ y, int64_t ybs,
-                           bool wide, bool wide_BC) {
-  // here lane = c G + g: a warp's states are consecutive in memory, and nothing
-  // is shared through a tile
-  const Place p = place<G>(in.group_dim, in.groups, threadIdx.x / G, threadIdx.x % G);
-  const int n0 = p.g * kS, have = min(kS, in.N - n0);
-  const bool wBC = wide_BC && have == kS;
-  const int64_t b0 = p.b * kStreams;  // p.b counts groups of streams
-  float h[kStreams][kS], u[kStreams], delta[kStreams], z[kStreams];
-  Raw<T, kS> B[kStreams], C[kStreams];
-  float* st[kStreams];
-  bool real[kStreams];  // the same for the whole block
-#pragma unroll
-  for (int i = 0; i < kStreams; ++i) {
-    const int64_t b = b0 + i;
-    const int64_t slot = b >= in.batch ? -1 : slots != nullptr ? load_index(slots, in.index_bytes, b) : b;
-    real[i] = slot >= 0 && slot < state_rows;
-    st[i] = state + ((real[i] ? slot : 0) * in.dim + p.d) * in.N;
-#pragma unroll
-    for (int k = 0; k < kS; ++k) h[i][k] = 0.0f;
-    u[i] = delta[i] = z[i] = 0.0f;
-    B[i].zero();
-    C[i].zero();
-    if (real[i]) {
-      if (p.live) read_states(st[i], n0, in.N, wide, h[i]);
-      B[i].load(in.B + b * in.Bbs + (int64_t)p.group * in.N + n0, wBC, have);
-      C[i].load(in.C + b * in.Cbs + (int64_t)p.group * in.N + n0, wBC, have);
-      u[i] = to_f32(in.u[b * in.ubs + p.d]);
-      delta[i] = to_f32(in.dt[b * in.dbs + p.d]);
-      if (in.z != nullptr) z[i] = to_f32(in.z[b * in.zbs + p.d]);
-    }
+                           const void* __restrict__ slots, T* __restrict__ y, int64_t ybs) {
+  constexpr int L = 32 / G, kWarps = kScanThreads / 32;
+  constexpr int kAhead = G < 8 ? G : 8;  // rounds in flight
+  const int lane = threadIdx.x % 32, g = lane % G;
+  const uint32_t warp = blockIdx.x * kWarps + threadIdx.x / 32;
+  const uint32_t per_group = (uint32_t)((in.group_dim + 31) / 32);
+  const int64_t group = in.groups == 1 ? 0 : warp / per_group;
+  const int64_t first = (int64_t)(warp - (uint32_t)group * per_group) * 32;  // in the group
+  // the grid's other axes count streams: what depends on them alone is
+  // computed once a warp
+  const int64_t b = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (b >= in.batch || group >= in.groups || first >= in.group_dim) return;
+  const int channels = (int)min((int64_t)32, in.group_dim - first);
+  const int64_t d0 = group * in.group_dim + first, d = d0 + min(lane, channels - 1);
+  const int64_t slot = slots != nullptr ? load_index(slots, in.index_bytes, b) : b;
+  if (slot < 0 || slot >= state_rows) {  // the same for the whole warp
+    if (lane < channels) y[b * ybs + d] = from_f32<T>(0.0f);
+    return;
   }
-  float A[kS];
-  read_states(in.A + p.d * in.N, n0, in.N, wide, A);
-  const float D = in.D != nullptr ? in.D[p.d] : 0.0f;
-  const float bias = in.dt_bias != nullptr ? in.dt_bias[p.d] : 0.0f;
+  const int n0 = g * kS, have = kWide ? (n0 < in.N ? kS : 0) : min(kS, in.N - n0);
+  auto floats = [&](const float* q, bool read, float (&f)[kS]) {
+    if (kWide) {
+      const float4 v =
+          read && have > 0 ? *reinterpret_cast<const float4*>(q) : make_float4(0, 0, 0, 0);
+      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    } else {
 #pragma unroll
-  for (int k = 0; k < kS; ++k) A[k] *= kLog2e;
+      for (int k = 0; k < kS; ++k) f[k] = read && k < have ? q[k] : 0.0f;
+    }
+  };
+  auto elements = [&](const T* q, Raw<T, kS>& r) {
+    if (!kWide) r.load(q, false, have);
+    else if (have > 0) r.load(q, true, kS);
+    else r.zero();
+  };
+  float* st = state + (slot * in.dim + d0) * in.N + n0;
+  const float* A0 = in.A + d0 * in.N + n0;
+  float h[kAhead][kS], A[kAhead][kS];
+  auto read = [&](int r0) {
 #pragma unroll
-  for (int i = 0; i < kStreams; ++i) {
-    if (b0 + i >= in.batch) return;  // the same for the whole block
-    float o = 0.0f;
-    if (real[i]) {
-      float d = delta[i] + bias;
-      if (in.softplus) d = softplus(d);
-      const float du = d * u[i];
+    for (int r = 0; r < kAhead; ++r) {
+      const int c = (r0 + r) * L + lane / G;
+      floats(st + c * in.N, c < channels, h[r]);
+      floats(A0 + c * in.N, c < channels, A[r]);
+    }
+  };
+  read(0);
+  Raw<T, kS> Braw, Craw;
+  elements(in.B + b * in.Bbs + group * in.N + n0, Braw);
+  elements(in.C + b * in.Cbs + group * in.N + n0, Craw);
+  const float u = to_f32(in.u[b * in.ubs + d]);
+  float delta = to_f32(in.dt[b * in.dbs + d]);
+  const float z = in.z != nullptr ? to_f32(in.z[b * in.zbs + d]) : 0.0f;
+  const float D = in.D != nullptr ? in.D[d] : 0.0f;
+  if (in.dt_bias != nullptr) delta += in.dt_bias[d];
+  if (in.softplus) delta = softplus(delta);
+  const float du = delta * u;
+  float B[kS], C[kS], mine = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kS; ++k) {
+    B[k] = Braw.get(k);
+    C[k] = Craw.get(k);
+  }
+#pragma unroll
+  for (int r0 = 0; r0 < G; r0 += kAhead) {
+    if (r0 > 0) read(r0);
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      const int c = (r0 + r) * L + lane / G;
+      const float dc = __shfl_sync(~0u, delta, c), duc = __shfl_sync(~0u, du, c);
       float acc = 0.0f;
 #pragma unroll
       for (int k = 0; k < kS; ++k) {
-        h[i][k] = fmaf(exp2_fast(d * A[k]), h[i][k], du * B[i].get(k));
-        acc = k == 0 ? C[i].get(k) * h[i][k] : fmaf(C[i].get(k), h[i][k], acc);
+        h[r][k] = fmaf(exp2_fast(dc * (A[r][k] * kLog2e)), h[r][k], duc * B[k]);
+        acc = k == 0 ? C[k] * h[r][k] : fmaf(C[k], h[r][k], acc);
       }
-      o = fmaf(D, u[i], sum_lanes<G>(acc));
-      if (in.z != nullptr) o *= z[i] * sigmoid(z[i]);
-      if (p.live) store_states(st[i], n0, in.N, wide, h[i]);
+      if (c < channels) {
+        if (kWide) {
+          if (have > 0)
+            *reinterpret_cast<float4*>(st + c * in.N) =
+                make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kS; ++k)
+            if (k < have) st[c * in.N + k] = h[r][k];
+        }
+      }
+      // back to the lane that has the channel
+      const float v = __shfl_sync(~0u, sum_lanes<G>(acc), lane % L * G);
+      if (lane / L == r0 + r) mine = v;
     }
-    if (p.live && p.g == 0) y[(b0 + i) * ybs + p.d] = from_f32<T>(o);
   }
+  float o = fmaf(D, u, mine);
+  if (in.z != nullptr) o *= z * sigmoid(z);
+  if (lane < channels) y[b * ybs + d] = from_f32<T>(o);
 }
 
 int scan_lanes(int N) {
@@ -1294,27 +1310,20 @@ cr_status cr_selective_scan_step(const cr_selective_scan_args* a, float* state,
   if (!ptr_aligned(y, es) || !ptr_aligned(state, 4)) return CR_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int lanes = scan_lanes(a->dstate);
-  // Several streams a thread where that leaves threads for the whole GPU: 200
-  // streams of 4096 channels take TIME us with four a thread, TIME with one;
-  // one stream of 2048 channels TIME and TIME.
-#ifndef CR_STEP_STREAMS
-#define CR_STEP_STREAMS 4
-#endif
-  const bool many = a->batch >= 8 && a->batch * a->dim * lanes >= (1 << 20);
-  const bool wide = a->dstate % kS == 0 && ptr_aligned(state, 16) && ptr_aligned(a->A, 16);
-  const bool wide_BC = a->dstate % kS == 0 && rows_aligned(a->B, a->B_batch_stride, 0, es, kS * es) &&
-                       rows_aligned(a->C, a->C_batch_stride, 0, es, kS * es);
+  const bool wide = a->dstate % kS == 0 && ptr_aligned(state, 16) && ptr_aligned(a->A, 16) &&
+                    rows_aligned(a->B, a->B_batch_stride, 0, es, kS * es) &&
+                    rows_aligned(a->C, a->C_batch_stride, 0, es, kS * es);
+  constexpr int64_t kRows = 65535;  // of a grid's second and third axes
+  const int64_t blocks = ceil_div(ceil_div(a->dim / a->groups, 32) * a->groups, kScanThreads / 32);
+  if (ceil_div(a->batch, kRows) > kRows || blocks > kMaxBlocks / 4) return CR_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (unsigned)std::min(a->batch, kRows),
+                  (unsigned)ceil_div(a->batch, kRows));
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
-    auto launch = [&](auto streams) {
-      constexpr int R = decltype(streams)::value;
-      CR_LAUNCH(kKSelectiveScanStep, s,
-                selective_scan_step_kernel<T, G, R>
-                <<<(unsigned)scan_blocks(ceil_div(a->batch, R), a->dim, a->groups, lanes),
-                   kScanThreads, 0, s>>>(scan_in<T>(a), state, state_rows, slots,
-                                         static_cast<T*>(y), y_batch_stride, wide, wide_BC));
-    };
-    if (many) launch(std::integral_constant<int, CR_STEP_STREAMS>{});
-    else launch(std::integral_constant<int, 1>{});
+    auto kernel = wide ? selective_scan_step_kernel<T, G, true>
+                       : selective_scan_step_kernel<T, G, false>;
+    CR_LAUNCH(kKSelectiveScanStep, s,
+              kernel<<<grid, kScanThreads, 0, s>>>(scan_in<T>(a), state, state_rows, slots,
+                                                   static_cast<T*>(y), y_batch_stride));
   }));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
