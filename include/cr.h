@@ -320,8 +320,9 @@ cr_status cr_reduce_noalloc(const void* x, int64_t n, int32_t L, const void* ini
  *     no value is summed by atomics, and repeated calls give the same bits.
  *   - Outputs must not overlap inputs or each other, except where a call says
  *     so. An output pointer equal to a pointer the call reads is INVALID_ARG.
- *   - Conventions on streams, ownership, workspaces and errors as above; none
- *     of these calls waits on the device, and none uses a status word. */
+ *   - Conventions on streams, ownership, workspaces and errors as above. None
+ *     of these calls waits on the device or has a status word; the first 256
+ *     bytes of a workspace, where other calls have theirs, are left alone. */
 
 /* out[i] = scale * table[tokens[i]], i < n (rounded once, to dt). A token
  * outside [0, vocab) is padding and reads as a zero row.

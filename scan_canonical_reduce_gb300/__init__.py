@@ -170,6 +170,7 @@ class _Workspace:
             if buf is None or buf.numel() < nbytes:
                 with torch.cuda.stream(s):  # allocated on the stream that uses it
                     buf = torch.empty(max(nbytes, 4096), dtype=torch.uint8, device=device)
+                    buf[:256].zero_()  # no status, for calls that leave the word alone
                 self._bufs[key] = buf
             return buf
 

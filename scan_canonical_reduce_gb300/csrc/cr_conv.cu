@@ -529,7 +529,7 @@ size_t cr_causal_conv_backward_workspace_bytes(int64_t batch, int64_t len, int64
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || width < 1) return 0;
   const ConvShape sh = conv_shape(batch, len, dim);
-  return round256((size_t)(batch * sh.runs) * (size_t)dim * (width + 1) * 4) + 256;
+  return round256((size_t)(batch * sh.runs) * (size_t)dim * (width + 1) * 4) + kStatusBytes;
 }
 
 cr_status cr_causal_conv_backward(const cr_causal_conv_args* a, const cr_causal_conv_grads* g,
@@ -575,7 +575,7 @@ cr_status cr_causal_conv_backward(const cr_causal_conv_args* a, const cr_causal_
       gb.dxbs = g->dx_batch_stride;
       gb.dxts = g->dx_time_stride;
       gb.dstate = static_cast<T*>(g->dstate);
-      gb.part = static_cast<float*>(ws);
+      gb.part = reinterpret_cast<float*>(past_status(ws));
       gb.wide_dx = wide_dx;
       CR_LAUNCH(kKCausalConvBackward, s,
                 causal_conv_backward_kernel<T, K><<<blocks, kConvThreads, 0, s>>>(
@@ -586,7 +586,7 @@ cr_status cr_causal_conv_backward(const cr_causal_conv_args* a, const cr_causal_
   const int64_t n = a->dim * (a->width + 1);
   CR_LAUNCH(kKCausalConvSum, s,
             causal_conv_sum_kernel<<<(unsigned)ceil_div(n, 32), 256, 0, s>>>(
-                static_cast<const float*>(ws), a->batch * sh.runs, a->dim, a->width, g->dweight,
+                reinterpret_cast<const float*>(past_status(ws)), a->batch * sh.runs, a->dim, a->width, g->dweight,
                 g->dbias));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }

@@ -575,7 +575,7 @@ size_t cr_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t d
   if (n < 0 || vocab < 0 || dim < 0 || n > INT32_MAX || vocab > INT32_MAX) return 0;
   return round256(((size_t)vocab + 1) * 4) + round256((size_t)n * 4) +
          2 * round256((size_t)(n / kLong) * 4) +
-         round256((size_t)(n / kLong) * ((size_t)(dim + 3) / 4 * 4) * 4) + 256;
+         round256((size_t)(n / kLong) * ((size_t)(dim + 3) / 4 * 4) * 4) + kStatusBytes;
 }
 
 cr_status cr_embedding_backward(const void* tokens, int32_t index_bytes, int64_t n,
@@ -600,7 +600,7 @@ cr_status cr_embedding_backward(const void* tokens, int32_t index_bytes, int64_t
   const int64_t parts = n / kLong, part_warps = ceil_div(dim, kPartColumns);
   if (row_warps > kMaxBlocks / 2 / vocab || (parts > 0 && long_cols > kMaxBlocks / parts))
     return CR_ERR_UNSUPPORTED;
-  char* at = static_cast<char*>(ws);
+  char* at = past_status(ws);
   Sorted sorted;
   sorted.row_start = reinterpret_cast<int32_t*>(at);
   at += round256(((size_t)vocab + 1) * 4);

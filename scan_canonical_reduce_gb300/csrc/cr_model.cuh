@@ -246,6 +246,11 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kMaxBlocks = 0x7FFFFFFF;  // of a grid's x axis
 
+// A workspace begins with the status word of the calls that wait on the
+// device (cr_sync_status); the model operators leave it as it is.
+constexpr size_t kStatusBytes = 256;
+inline char* past_status(void* ws) { return static_cast<char*>(ws) + kStatusBytes; }
+
 }  // namespace cr
 
 // Runs EXPR with T bound to the element type that DT names.

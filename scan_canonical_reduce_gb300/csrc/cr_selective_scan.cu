@@ -1126,7 +1126,8 @@ size_t cr_selective_scan_workspace_bytes(int64_t batch, int64_t len, int64_t dim
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || dstate < 1) return 0;
   const int64_t segs = scan_segments(batch, len, dim, scan_lanes(dstate)).count;
-  return round256((size_t)(segs - 1) * batch * dim * (scan_lanes(dstate) * kS + 1) * 4) + 256;
+  return round256((size_t)(segs - 1) * batch * dim * (scan_lanes(dstate) * kS + 1) * 4) +
+         kStatusBytes;
 }
 
 cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_batch_stride,
@@ -1152,7 +1153,7 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
   const int64_t blocks = scan_blocks(a->batch, a->dim, a->groups, lanes);
   Segments sg = scan_segments(a->batch, a->len, a->dim, lanes);
   if (blocks > kMaxBlocks / sg.count) return CR_ERR_UNSUPPORTED;
-  sg.E = static_cast<float*>(ws);
+  sg.E = reinterpret_cast<float*>(past_status(ws));
   sg.sum = sg.E + (sg.count - 1) * a->batch * a->dim * lanes * kS;
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
     using TL = Tile<T, G>;
@@ -1198,7 +1199,7 @@ size_t cr_selective_scan_backward_workspace_bytes(int64_t batch, int64_t len, in
   const int lanes = scan_lanes(dstate);
   const size_t bc = (size_t)batch * len * groups * group_blocks(dim, groups, lanes) * 2 *
                     (lanes * kS) * 4;
-  return round256(bc) + round256((size_t)batch * dim * (dstate + 2) * 4) + 256;
+  return round256(bc) + round256((size_t)batch * dim * (dstate + 2) * 4) + kStatusBytes;
 }
 
 cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
@@ -1233,9 +1234,9 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
   const int lanes = scan_lanes(a->dstate);
   const int64_t parts = group_blocks(a->dim, a->groups, lanes);
   const int64_t rows = a->batch * a->len * a->groups;
-  float* part_BC = static_cast<float*>(ws);
+  float* part_BC = reinterpret_cast<float*>(past_status(ws));
   float* part_A = reinterpret_cast<float*>(
-      static_cast<char*>(ws) + round256((size_t)rows * parts * 2 * (lanes * kS) * 4));
+      past_status(ws) + round256((size_t)rows * parts * 2 * (lanes * kS) * 4));
   if (a->batch > 0) {
     const unsigned blocks = (unsigned)scan_blocks(a->batch, a->dim, a->groups, lanes);
     const int64_t n_check = cr_selective_scan_checkpoints(a->len);

@@ -228,8 +228,9 @@ struct On {
   }
 
   // The binding's workspace of this stream (held here too, so that a call
-  // does not ask Python for it).
-  const at::Tensor& workspace(size_t bytes, const char* name, PyObject* stream) const {
+  // does not ask Python for it). Asking may let other threads in, so nothing
+  // of the list is kept across it, and the tensor is returned by value.
+  at::Tensor workspace(size_t bytes, const char* name, PyObject* stream) const {
     struct Kept {
       int index;
       cudaStream_t stream;
@@ -237,22 +238,19 @@ struct On {
     };
     static std::vector<Kept>* kept = new std::vector<Kept>;  // not destroyed: outlives CUDA
     if (bytes == 0) bad_value(join("invalid ", name, " arguments"));
-    Kept* k = nullptr;
-    for (Kept& q : *kept)
-      if (q.index == index && q.stream == ptr) k = &q;
-    if (k == nullptr || (size_t)k->t.numel() < bytes) {
-      PyObject* r = PyObject_CallFunction(g_workspace, "iOn", index, stream, (Py_ssize_t)bytes);
-      if (r == nullptr) throw Error{nullptr, ""};
-      const at::Tensor t = tensor(r, "workspace");
-      Py_DECREF(r);
-      if (k == nullptr) {
-        kept->push_back({index, ptr, t});
-        k = &kept->back();
-      } else {
-        k->t = t;
-      }
-    }
-    return k->t;
+    auto find = [&]() -> Kept* {
+      for (Kept& q : *kept)
+        if (q.index == index && q.stream == ptr) return &q;
+      return nullptr;
+    };
+    if (const Kept* k = find(); k != nullptr && (size_t)k->t.numel() >= bytes) return k->t;
+    PyObject* r = PyObject_CallFunction(g_workspace, "iOn", index, stream, (Py_ssize_t)bytes);
+    if (r == nullptr) throw Error{nullptr, ""};
+    const at::Tensor t = tensor(r, "workspace");
+    Py_DECREF(r);
+    if (Kept* k = find()) k->t = t;
+    else kept->push_back({index, ptr, t});
+    return t;
   }
 };
 
@@ -312,7 +310,7 @@ PyObject* embedding_backward(PyObject* const* a) {
   at::Tensor grad = rows(grad0.dim() == 2 ? grad0 : grad0.reshape({n, dim}));
   if (n > 1 && grad.stride(0) < dim) grad = grad.contiguous();  // a zero stride
   const at::Tensor o = on.output(a[4], {vocab, dim}, at::kFloat);
-  const at::Tensor& ws = on.workspace(f_embedding_backward_workspace_bytes(n, vocab, dim),
+  const at::Tensor ws = on.workspace(f_embedding_backward_workspace_bytes(n, vocab, dim),
                                       "embedding_backward", a[6]);
   on.uses(tok.t, grad);
   check(f_embedding_backward(tok.p, tok.bytes, n, grad.data_ptr(), n > 1 ? grad.stride(0) : dim,
@@ -398,7 +396,7 @@ PyObject* causal_conv_backward(PyObject* const* a) {
   const at::Tensor dw = c.on.empty({c.args.dim, K}, at::kFloat);
   if (c.bias.p != nullptr || c.bias.t.defined()) db = c.on.empty({c.args.dim}, at::kFloat);
   if (c.state.defined()) ds = c.on.empty(c.state.sizes(), type);
-  const at::Tensor& ws = c.on.workspace(
+  const at::Tensor ws = c.on.workspace(
       f_causal_conv_backward_workspace_bytes(c.args.batch, c.args.len, c.args.dim, (int32_t)K),
       "causal_conv_backward", a[8]);
   c.on.uses(dy, dfinal);
@@ -566,7 +564,7 @@ PyObject* selective_scan(PyObject* const* a) {
   if (return_state) final = s.on.empty({batch, dim, N}, at::kFloat);
   if (return_checkpoints)
     kept = s.on.empty({batch, f_selective_scan_checkpoints(s.args.len), dim, N}, at::kFloat);
-  const at::Tensor& ws =
+  const at::Tensor ws =
       s.on.workspace(f_selective_scan_workspace_bytes(batch, s.args.len, dim, (int32_t)N),
                      "selective_scan", a[14]);
   check(f_selective_scan(&s.args, y.data_ptr(), y.stride(0), y.stride(1),
@@ -613,7 +611,7 @@ PyObject* selective_scan_backward(PyObject* const* a) {
   if (s.z.defined()) dz.t = s.on.empty(s.u0.sizes(), type);
   if (s.dt_bias.t.defined()) db.t = s.on.empty({dim}, at::kFloat);
   if (s.state.t.defined()) ds.t = s.on.empty({batch, dim, N}, at::kFloat);
-  const at::Tensor& ws = s.on.workspace(
+  const at::Tensor ws = s.on.workspace(
       f_selective_scan_backward_workspace_bytes(batch, s.args.len, dim, (int32_t)N,
                                                 s.args.groups),
       "selective_scan_backward", a[14]);
