@@ -202,7 +202,7 @@ __device__ __forceinline__ void tile_put_states(const Raw<T, kS> (&in)[TL::NBC][
 // over the four states).
 template <bool kDot>
 __device__ __forceinline__ F2 lane_steps(const F2 (&A)[kS], float (&h)[kS], const float4& e4,
-                                         const float4* Bq, const float4* Cq) {
+                                         const float4 (&Bq)[2], const float4 (&Cq)[2]) {
   const F2 delta = pack2(e4.x, e4.y), du = pack2(e4.z, e4.w);
   F2 p = 0;
 #pragma unroll
@@ -245,13 +245,9 @@ struct ScanOut {
   bool wide, wide_y, wide_BC, wide_check;
 };
 
-#ifndef CR_SCAN_UNROLL
-#define CR_SCAN_UNROLL 4
-#endif
 #ifndef CR_SCAN_BLOCKS
 #define CR_SCAN_BLOCKS 4
 #endif
-constexpr int kUnroll = CR_SCAN_UNROLL;
 template <class T, int G, bool kStates>
 __global__ void __launch_bounds__(kScanThreads, CR_SCAN_BLOCKS)
 selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
@@ -342,15 +338,23 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
       const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
       const int at = TL::slot(tp, c0) * 16;
       const bool in0 = 2 * tp < left, in1 = 2 * tp + 1 < left;
+      float a[VE], a1[VE];
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
-        float a = pd[i][0].get(k) + bias.v[k], a1 = pd[i][1].get(k) + bias.v[k];
-        if (in.softplus) softplus2(a, a1);
-        a = in0 ? a : 0.0f;
-        a1 = in1 ? a1 : 0.0f;
+        a[k] = pd[i][0].get(k) + bias.v[k];
+        a1[k] = pd[i][1].get(k) + bias.v[k];
+      }
+      if (in.softplus) {  // all of them in one block: their chains overlap
+#pragma unroll
+        for (int k = 0; k < VE; ++k) softplus2(a[k], a1[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        a[k] = in0 ? a[k] : 0.0f;
+        a1[k] = in1 ? a1[k] : 0.0f;
         if (TL::ACC % kScanThreads == 0 || idx < TL::ACC)
           *reinterpret_cast<float4*>(reinterpret_cast<char*>(dd) + (at ^ (k * 16))) =
-              make_float4(a, a1, a * pu[i][0].get(k), a1 * pu[i][1].get(k));
+              make_float4(a[k], a1[k], a[k] * pu[i][0].get(k), a1[k] * pu[i][1].get(k));
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -374,33 +378,51 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
                          ((b * out.n_check + (t0 + tb) / kCheckpoint) * in.dim + d) * in.N,
                      n0, in.N, out.wide_check, h);
       // straight code: the reads and decays of later steps run ahead
-#pragma unroll kUnroll
+      float4 e_next, B_next[2], C_next[2];
+      auto read = [&](int tp) {
+        e_next = dl[tp * TL::CH];
+        B_next[0] = Bl[tp * 2 * G], B_next[1] = Bl[tp * 2 * G + 1];
+        if (!kStates) C_next[0] = Cl[tp * 2 * G], C_next[1] = Cl[tp * 2 * G + 1];
+        else C_next[0] = C_next[1] = B_next[0];
+      };
+      read(0);
+      F2 q[2] = {0, 0};
+      auto finish = [&](int t4) {
+        float v[4];
+        sum_lanes4<G>(q[0], q[1], g, v);
+        float* y = yl + t4 * 4 * TL::YS;
+        if (G == 1) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k * TL::YS] = v[k];
+        } else if (G == 2) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) y[(2 * g + k) * TL::YS] = v[k];
+        } else if (G == 4 || g < 4) {
+          y[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
+        }
+      };
+#pragma unroll
       for (int t4 = 0; t4 < kCheckpoint / 4; ++t4) {
         F2 p[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float4 e = dl[j * TL::CH];
+          const float4 e = e_next, B[2] = {B_next[0], B_next[1]};
+          const float4 C[2] = {C_next[0], C_next[1]};
+          if (2 * t4 + j + 1 < kCheckpoint / 2) read(2 * t4 + j + 1);
           if (kStates) total = add2(total, pack2(e.x, e.y));
-          p[j] = lane_steps<!kStates>(A, h, e, Bl + j * 2 * G, kStates ? Bl : Cl + j * 2 * G);
+          p[j] = lane_steps<!kStates>(A, h, e, B, C);
         }
         if (!kStates) {
-          float v[4];
-          sum_lanes4<G>(p[0], p[1], g, v);
-          if (G == 1) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) yl[k * TL::YS] = v[k];
-          } else if (G == 2) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) yl[(2 * g + k) * TL::YS] = v[k];
-          } else if (G == 4 || g < 4) {
-            yl[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
-          }
-          Cl += 4 * G;
-          yl += 4 * TL::YS;
+          if (t4 > 0) finish(t4 - 1);
+          q[0] = p[0];
+          q[1] = p[1];
         }
-        dl += 2 * TL::CH;
-        Bl += 4 * G;
       }
+      if (!kStates) finish(kCheckpoint / 4 - 1);
+      dl += kCheckpoint / 2 * TL::CH;
+      Bl += kCheckpoint * G;
+      if (!kStates) Cl += kCheckpoint * G;
+      yl += kCheckpoint * TL::YS;
     }
     __syncthreads();
 
@@ -411,31 +433,34 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
 #pragma unroll
       for (int i = 0; i < TL::NL; ++i) {
         const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
-        const bool mine = TL::ACC % kScanThreads == 0 || idx < TL::ACC;
+        if (TL::ACC % kScanThreads != 0 && idx >= TL::ACC) continue;
+        float f[2][VE];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const Pack<float, VE> yv =
+              *reinterpret_cast<const Pack<float, VE>*>(ys + (2 * tp + j) * TL::YS + c0);
+#pragma unroll
+          for (int k = 0; k < VE; ++k) f[j][k] = fmaf(Dv.v[k], ku[i][j].get(k), yv.v[k]);
+        }
+        if (gated) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+              const float z = kz[i][j].get(k);
+              f[j][k] *= z * sigmoid(z);
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int t = 2 * tp + j;
-          float f[VE];
-          if (mine) {
-            const Pack<float, VE> yv =
-                *reinterpret_cast<const Pack<float, VE>*>(ys + t * TL::YS + c0);
+          if (t >= left) {
 #pragma unroll
-            for (int k = 0; k < VE; ++k) f[k] = fmaf(Dv.v[k], ku[i][j].get(k), yv.v[k]);
-            if (gated) {
-#pragma unroll
-              for (int k = 0; k < VE; ++k) {
-                const float z = kz[i][j].get(k);
-                f[k] *= z * sigmoid(z);
-              }
-            }
-            if (t >= left) {
-#pragma unroll
-              for (int k = 0; k < VE; ++k) f[k] = 0.0f;
-            }
-            if (t < rows && have > 0)
-              store_f32<T, VE>(yp + (i * (kScanThreads / TL::NV) * 2 + j) * out.yts,
-                               out.wide_y && have == VE, have, f);
+            for (int k = 0; k < VE; ++k) f[j][k] = 0.0f;
           }
+          if (t < rows && have > 0)
+            store_f32<T, VE>(yp + (i * (kScanThreads / TL::NV) * 2 + j) * out.yts,
+                             out.wide_y && have == VE, have, f[j]);
         }
       }
       yp += TL::TT * out.yts;
@@ -637,21 +662,33 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
       const int idx = i * kScanThreads + tid, tp = idx / TL::NV;
       const int at = TL::slot(tp, c0);
       const bool in0 = 2 * tp < left, in1 = 2 * tp + 1 < left;
+      float a[VE], a1[VE], p[VE], p1[VE];
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
-        float a = pd[i][0].get(k) + bias.v[k], a1 = pd[i][1].get(k) + bias.v[k];
-        if (in.softplus) softplus2(a, a1);
-        a = in0 ? a : 0.0f;
-        a1 = in1 ? a1 : 0.0f;
-        float p = py[i][0].get(k), p1 = py[i][1].get(k);
-        if (gated) {
+        a[k] = pd[i][0].get(k) + bias.v[k];
+        a1[k] = pd[i][1].get(k) + bias.v[k];
+        p[k] = py[i][0].get(k);
+        p1[k] = py[i][1].get(k);
+      }
+      if (in.softplus) {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) softplus2(a[k], a1[k]);
+      }
+      if (gated) {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
           const float z = pz[i][0].get(k), z1 = pz[i][1].get(k);
-          p *= z * sigmoid(z);
-          p1 *= z1 * sigmoid(z1);
+          p[k] *= z * sigmoid(z);
+          p1[k] *= z1 * sigmoid(z1);
         }
+      }
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        a[k] = in0 ? a[k] : 0.0f;
+        a1[k] = in1 ? a1[k] : 0.0f;
         if (TL::ACC % kScanThreads == 0 || idx < TL::ACC) {
-          dd[at ^ k] = make_float4(a, a1, a * pu[i][0].get(k), a1 * pu[i][1].get(k));
-          pp[at ^ k] = make_float2(p, p1);
+          dd[at ^ k] = make_float4(a[k], a1[k], a[k] * pu[i][0].get(k), a1[k] * pu[i][1].get(k));
+          pp[at ^ k] = make_float2(p[k], p1[k]);
         }
       }
 #pragma unroll
@@ -675,6 +712,21 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
     const float2* pl = pp + TL::slot(0, c);
     const float4 *Bl = Bs + 2 * g, *Cl = Cs + 2 * g;
     const int q0 = flip / 2, q1 = 1 - q0;
+    F2 yq[2] = {0, 0};  // of the four steps before: summed behind the next ones
+    auto put_y = [&](int t4) {
+      float v[4];
+      sum_lanes4<G>(yq[0], yq[1], g, v);
+      float* y = ys + t4 * 4 * TL::YS + c;
+      if (G == 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k * TL::YS] = v[k];
+      } else if (G == 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) y[(2 * g + k) * TL::YS] = v[k];
+      } else if (G == 4 || g < 4) {
+        y[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
+      }
+    };
 #pragma unroll
     for (int t4 = 0; t4 < TT / 4; ++t4) {
       F2 yp[2];
@@ -698,25 +750,41 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
           yp[j] = k == 0 ? mul2(Ck, hp) : fma2(Ck, hp, yp[j]);
         }
       }
-      if (gated) {
-        float v[4];
-        sum_lanes4<G>(yp[0], yp[1], g, v);
-        float* y = ys + t4 * 4 * TL::YS + c;
-        if (G == 1) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k * TL::YS] = v[k];
-        } else if (G == 2) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) y[(2 * g + k) * TL::YS] = v[k];
-        } else if (G == 4 || g < 4) {
-          y[(2 * (g & 1) + (g >> 1 & 1)) * TL::YS] = v[0];
-        }
-      }
+      if (t4 > 0) put_y(t4 - 1);
+      yq[0] = yp[0];
+      yq[1] = yp[1];
     }
+    put_y(TT / 4 - 1);
 
     // the adjoint states, backward; the tile is read again, so that nothing of
     // the pass above but h is held in registers
     asm volatile("" ::: "memory");
+    // the sums of a pair of steps: their exchanges are issued after the next
+    // pair's arithmetic, which hides them
+    F2 pv[8], pg = 0, pq = 0;
+    auto finish = [&](int tp) {
+      const int t = tp * 2;
+      CS::run(pv, lane_c);
+      if (CS::writes(lane_c)) {
+#pragma unroll
+        for (int i = 0; i < CS::kPairs; ++i) {
+          float lo, hi;
+          unpack2(pv[i], lo, hi);
+          sums[(tid / 32 * TP + tp) * 2 * NP + CS::owned(i, lane_c, g)] = make_float2(lo, hi);
+        }
+      }
+      float w[4];
+      sum_lanes4<G>(pg, pq, g, w);
+      float *gl = gs + t * TL::YS + c, *ql = qs + t * TL::YS + c;
+      if (G == 1) {
+        gl[0] = w[0], gl[TL::YS] = w[1], ql[0] = w[2], ql[TL::YS] = w[3];
+      } else if (G == 2) {
+        float* q = g ? ql : gl;
+        q[0] = w[0], q[TL::YS] = w[1];
+      } else if (G == 4 || g < 4) {
+        (g & 1 ? ql : gl)[(g >> 1 & 1) * TL::YS] = w[0];
+      }
+    };
 #pragma unroll
     for (int tp = TP - 1; tp >= 0; --tp) {
       const int t = tp * 2;
@@ -744,27 +812,13 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
         v[k] = mul2(gp, du);
         v[4 + k] = mul2(p, pack2(h[t + 1][k], h[t + 2][k]));
       }
-      CS::run(v, lane_c);
-      if (CS::writes(lane_c)) {
+      if (tp < TP - 1) finish(tp + 1);
 #pragma unroll
-        for (int i = 0; i < CS::kPairs; ++i) {
-          float lo, hi;
-          unpack2(v[i], lo, hi);
-          sums[(tid / 32 * TP + tp) * 2 * NP + CS::owned(i, lane_c, g)] = make_float2(lo, hi);
-        }
-      }
-      float w[4];
-      sum_lanes4<G>(gB, qA, g, w);
-      float *gl = gs + t * TL::YS + c, *ql = qs + t * TL::YS + c;
-      if (G == 1) {
-        gl[0] = w[0], gl[TL::YS] = w[1], ql[0] = w[2], ql[TL::YS] = w[3];
-      } else if (G == 2) {
-        float* q = g ? ql : gl;
-        q[0] = w[0], q[TL::YS] = w[1];
-      } else if (G == 4 || g < 4) {
-        (g & 1 ? ql : gl)[(g >> 1 & 1) * TL::YS] = w[0];
-      }
+      for (int k = 0; k < 8; ++k) pv[k] = v[k];
+      pg = gB;
+      pq = qA;
     }
+    finish(0);
     __syncthreads();
 
     // dB and dC of the block's channels: the warps in order
@@ -794,24 +848,33 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
         const Pack<float, VE> yv = *reinterpret_cast<const Pack<float, VE>*>(ys + t * TL::YS + c0);
         const Pack<float, VE> gv = *reinterpret_cast<const Pack<float, VE>*>(gs + t * TL::YS + c0);
         const Pack<float, VE> qv = *reinterpret_cast<const Pack<float, VE>*>(qs + t * TL::YS + c0);
-        float fu[VE], fd[VE], fz[VE];
+        float fu[VE], fd[VE], fz[VE], p[VE], u[VE];
         const bool in_seq = t < left;
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
-          const float u = ku[i][j].get(k);
+          u[k] = ku[i][j].get(k);
           const float4 e = dd[TL::slot(tp, c0) ^ k];
           const float2 p2 = pp[TL::slot(tp, c0) ^ k];
-          const float delta = j ? e.y : e.x, p = j ? p2.y : p2.x;
-          fu[k] = fmaf(delta, gv.v[k], Dv.v[k] * p);
-          fd[k] = fmaf(u, gv.v[k], qv.v[k]);
-          if (in.softplus) fd[k] *= sigmoid(kd[i][j].get(k) + bias.v[k]);
+          p[k] = j ? p2.y : p2.x;
+          fu[k] = fmaf(j ? e.y : e.x, gv.v[k], Dv.v[k] * p[k]);
+          fd[k] = fmaf(u[k], gv.v[k], qv.v[k]);
           fz[k] = 0.0f;
-          if (gated) {
+        }
+        if (in.softplus) {
+#pragma unroll
+          for (int k = 0; k < VE; ++k) fd[k] *= sigmoid(kd[i][j].get(k) + bias.v[k]);
+        }
+        if (gated) {
+#pragma unroll
+          for (int k = 0; k < VE; ++k) {
             const float z = kz[i][j].get(k), sg = sigmoid(z);
-            fz[k] = ky[i][j].get(k) * fmaf(Dv.v[k], u, yv.v[k]) * (sg * fmaf(z, 1.0f - sg, 1.0f));
+            fz[k] = ky[i][j].get(k) * fmaf(Dv.v[k], u[k], yv.v[k]) * (sg * fmaf(z, 1.0f - sg, 1.0f));
           }
+        }
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
           if (in_seq) {
-            dD[k] = fmaf(p, u, dD[k]);
+            dD[k] = fmaf(p[k], u[k], dD[k]);
             dbias[k] += fd[k];
           } else {
             fu[k] = fd[k] = fz[k] = 0.0f;
@@ -874,6 +937,7 @@ selective_scan_sum_bc_kernel(const float* __restrict__ part, int64_t rows, int64
   const int which = j >= N, n = (int)j - which * N;
   const float* q = part + r * blocks * 2 * NP + which * NP + n;
   float s = 0.0f;
+#pragma unroll 16
   for (int64_t w = 0; w < blocks; ++w) s += q[w * 2 * NP];
   (which ? dC : dB)[r * N + n] = from_f32<T>(s);
 }
