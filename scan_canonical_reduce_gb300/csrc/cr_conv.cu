@@ -22,6 +22,39 @@ namespace {
 constexpr int kConvThreads = 128;
 constexpr int kV = 4;  // channels a thread
 
+// Where a thread's four channels are. Wide: neighbours, accessed at once.
+// Otherwise (rows that start anywhere) 32 apart, so that a warp's accesses,
+// one channel a thread, are consecutive.
+template <bool kWide>
+struct Channels {
+  static constexpr int kStep = kWide ? 1 : 32;
+  // block: of kConvThreads kV channels
+  static __device__ __forceinline__ int64_t first(int64_t block) {
+    if (kWide) return (block * kConvThreads + threadIdx.x) * kV;
+    return block * kConvThreads * kV + threadIdx.x / 32 * 32 * kV + threadIdx.x % 32;
+  }
+  static __device__ __forceinline__ int have(int64_t c, int64_t dim) {
+    const int64_t n = (dim - c + kStep - 1) / kStep;
+    return (int)min((int64_t)kV, n);
+  }
+};
+
+template <class T, bool kWide>
+using Four = Raw<T, kV, kWide, Channels<kWide>::kStep>;
+
+template <class T, bool kWide>
+__device__ __forceinline__ void read_four(const T* p, bool whole, int have, float (&f)[kV]) {
+  Four<T, kWide> r;
+  r.load(p, whole, have);
+#pragma unroll
+  for (int j = 0; j < kV; ++j) f[j] = r.get(j);
+}
+
+template <class T, bool kWide>
+__device__ __forceinline__ void write_four(T* p, bool whole, int have, const float (&f)[kV]) {
+  store_raw<T, kV, kWide, Channels<kWide>::kStep>(p, whole, have, f);
+}
+
 struct ConvShape {
   int64_t batch, len, dim;
   int64_t run;        // steps a thread takes
@@ -54,18 +87,18 @@ struct ConvIn {
   const T* state;
   const void* lengths;
   int index_bytes;
-  bool silu, wide, wide_state;
+  bool silu, wide, wide_state, wide_weight;
 };
 
 // Input at extended time t (t < 0: the state's) of channels c .. c + have.
-template <class T, int K>
+template <class T, int K, bool kWide>
 __device__ __forceinline__ void conv_input(const ConvIn<T>& in, const ConvShape& sh, int64_t b,
                                            int64_t t, int64_t c, int have, float (&f)[kV]) {
   if (t >= 0) {
-    load_f32<T, kV>(in.x + b * in.bs + t * in.ts + c, in.wide && have == kV, have, f);
+    read_four<T, kWide>(in.x + b * in.bs + t * in.ts + c, in.wide && have == kV, have, f);
   } else if (in.state != nullptr) {
-    load_f32<T, kV>(in.state + (b * (K - 1) + (K - 1 + t)) * sh.dim + c,
-                    in.wide_state && have == kV, have, f);
+    read_four<T, kWide>(in.state + (b * (K - 1) + (K - 1 + t)) * sh.dim + c,
+                        in.wide_state && have == kV, have, f);
   } else {
 #pragma unroll
     for (int j = 0; j < kV; ++j) f[j] = 0.0f;
@@ -77,31 +110,43 @@ struct Quad {
   F2 p[2];
 };
 
-__device__ __forceinline__ Quad quad(const float (&f)[kV]) {
+__device__ __forceinline__ Quad quad_of(const float (&f)[kV]) {
   return {{pack2(f[0], f[1]), pack2(f[2], f[3])}};
 }
 __device__ __forceinline__ void unquad(const Quad& q, float (&f)[kV]) {
   unpack2(q.p[0], f[0], f[1]);
   unpack2(q.p[1], f[2], f[3]);
 }
-template <class T>
-__device__ __forceinline__ Quad quad(const Raw<T, kV>& r) {
+template <class R>
+__device__ __forceinline__ Quad quad(const R& r) {
   return {{pack2(r.get(0), r.get(1)), pack2(r.get(2), r.get(3))}};
 }
 
-template <int K>
-__device__ __forceinline__ void conv_weights(const float* weight, const float* bias, int64_t c,
-                                             int have, Quad (&w)[K], Quad& b0) {
+template <int K, bool kWide>
+__device__ __forceinline__ void conv_weights(const float* weight, const float* bias,
+                                             bool wide_weight, int64_t c, int have, Quad (&w)[K],
+                                             Quad& b0) {
+  constexpr int kStep = Channels<kWide>::kStep;
   float f[kV];
 #pragma unroll
-  for (int j = 0; j < kV; ++j) f[j] = (bias != nullptr && j < have) ? bias[c + j] : 0.0f;
-  b0 = quad(f);
+  for (int j = 0; j < kV; ++j) f[j] = (bias != nullptr && j < have) ? bias[c + j * kStep] : 0.0f;
+  b0 = quad_of(f);
+  float v[K][kV];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int j = 0; j < kV; ++j) {
+    const float* q = weight + (c + j * kStep) * K;
+    if (K != 3 && wide_weight && j < have) {  // a channel's taps at once
+      Raw<float, K == 3 ? 1 : K> r;
+      r.load(q, true, K);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) f[j] = j < have ? weight[(c + j) * K + k] : 0.0f;
-    w[k] = quad(f);
+      for (int k = 0; k < K; ++k) v[k][j] = r.get(K == 3 ? 0 : k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k][j] = j < have ? q[k] : 0.0f;
+    }
   }
+#pragma unroll
+  for (int k = 0; k < K; ++k) w[k] = quad_of(v[k]);
 }
 
 // pre = bias + sum_k w[k] x[k], k upwards.
@@ -125,9 +170,9 @@ __device__ __forceinline__ void conv_act(bool silu, float (&f)[kV]) {
 // U rows of a tensor's four channels from p on. kFull: all of them exist and
 // are read whole; otherwise the first `rows` do, the others are zero and not
 // read. Most groups are full, and the checks cost more than their arithmetic.
-template <bool kFull, class T, int U>
+template <bool kFull, class T, int U, class R>
 __device__ __forceinline__ void load_group(const T* p, int64_t ts, int rows, bool wide, int have,
-                                           Raw<T, kV> (&r)[U]) {
+                                           R (&r)[U]) {
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     if (kFull) r[i].load(p + i * ts, true, kV);
@@ -136,9 +181,9 @@ __device__ __forceinline__ void load_group(const T* p, int64_t ts, int rows, boo
   }
 }
 
-template <bool kFull, class T>
+template <bool kFull, bool kWide, class T>
 __device__ __forceinline__ void store_row(T* p, bool wide, int have, const float (&f)[kV]) {
-  store_f32<T, kV>(p, kFull || wide, kFull ? kV : have, f);
+  write_four<T, kWide>(p, kFull || wide, kFull ? kV : have, f);
 }
 
 #ifndef CR_CONV_FORWARD
@@ -152,16 +197,16 @@ constexpr int kForward = CR_CONV_FORWARD, kBackward = 4;  // steps of a group
 #ifndef CR_CONV_BACK_BLOCKS
 #define CR_CONV_BACK_BLOCKS 3
 #endif
-template <class T, int K>
+template <class T, int K, bool kWide>
 __global__ void __launch_bounds__(kConvThreads, CR_CONV_BLOCKS)
 causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, int64_t yts,
                    bool wide_y, T* __restrict__ final_state) {
   constexpr int U = kForward;
   int64_t c, run;
   const int64_t b = divide(divide(blockIdx.x, sh.col_blocks, c), sh.runs, run);
-  c = (c * kConvThreads + threadIdx.x) * kV;
+  c = Channels<kWide>::first(c);
   if (c >= sh.dim) return;
-  const int have = (int)min((int64_t)kV, sh.dim - c);
+  const int have = Channels<kWide>::have(c, sh.dim);
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
   const int64_t t0 = run * sh.run, t1 = min(sh.len, t0 + sh.run), stop = min(t1, len);
   const bool wy = wide_y && have == kV, wx = in.wide && have == kV;
@@ -171,16 +216,16 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
     const int rows = (int)(stop - t0);
     const T* x = in.x + b * in.bs + t0 * in.ts + c;  // of the next group
     T* o = y + t0 * yts;
-    Raw<T, kV> next[U];
+    Four<T, kWide> next[U];
     load_group<false, T, U>(x, in.ts, rows, wx, have, next);
     x += U * in.ts;
     Quad w[K], b0, win[K - 1 + U];
-    conv_weights<K>(in.weight, in.bias, c, have, w, b0);
+    conv_weights<K, kWide>(in.weight, in.bias, in.wide_weight, c, have, w, b0);
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
       float f[kV];
-      conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, f);
-      win[k] = quad(f);
+      conv_input<T, K, kWide>(in, sh, b, t0 - (K - 1) + k, c, have, f);
+      win[k] = quad_of(f);
     }
     auto group = [&](auto full, int left) {
       constexpr bool kFull = decltype(full)::value;
@@ -192,7 +237,7 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
         float f[kV];
         unquad(conv_pre<K>(w, b0, win + u), f);
         conv_act(in.silu, f);
-        if (kFull || u < left) store_row<kFull>(o + u * yts, wy, have, f);
+        if (kFull || u < left) store_row<kFull, kWide>(o + u * yts, wy, have, f);
       }
 #pragma unroll
       for (int k = 0; k < K - 1; ++k) win[k] = win[U + k];
@@ -200,7 +245,7 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
       o += U * yts;
     };
     int left = rows;
-    if (wx && wy) {
+    if (kWide ? wx && wy : have == kV) {
 #pragma unroll 1
       for (; left >= 2 * U; left -= U) group(std::true_type{}, left);
     }
@@ -208,14 +253,14 @@ causal_conv_kernel(ConvIn<T> in, ConvShape sh, T* __restrict__ y, int64_t ybs, i
     for (; left > 0; left -= U) group(std::false_type{}, left);
   }
   const float zero[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t t = max(t0, len); t < t1; ++t) store_f32<T, kV>(y + t * yts, wy, have, zero);
+  for (int64_t t = max(t0, len); t < t1; ++t) write_four<T, kWide>(y + t * yts, wy, have, zero);
   if (run == 0 && final_state != nullptr) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       float f[kV];
-      conv_input<T, K>(in, sh, b, len - (K - 1) + j, c, have, f);
-      store_f32<T, kV>(final_state + (b * (K - 1) + j) * sh.dim + c, in.wide_state && have == kV,
-                       have, f);
+      conv_input<T, K, kWide>(in, sh, b, len - (K - 1) + j, c, have, f);
+      write_four<T, kWide>(final_state + (b * (K - 1) + j) * sh.dim + c,
+                           in.wide_state && have == kV, have, f);
     }
   }
 }
@@ -235,15 +280,15 @@ struct ConvBack {
 // A run computes dpre for its own steps and the K-1 after them; it writes
 // dx of its own steps (run 0: of the state's too) and the sums of
 // dpre x and dpre over its own steps.
-template <class T, int K>
+template <class T, int K, bool kWide>
 __global__ void __launch_bounds__(kConvThreads, CR_CONV_BACK_BLOCKS)
 causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
   constexpr int U = kBackward;
   int64_t c, run;
   const int64_t b = divide(divide(blockIdx.x, sh.col_blocks, c), sh.runs, run);
-  c = (c * kConvThreads + threadIdx.x) * kV;
+  c = Channels<kWide>::first(c);
   if (c >= sh.dim) return;
-  const int have = (int)min((int64_t)kV, sh.dim - c);
+  const int have = Channels<kWide>::have(c, sh.dim);
   const int64_t len = sequence_length(in.lengths, in.index_bytes, b, sh.len);
   const int64_t t0 = run * sh.run, t1 = min(sh.len, t0 + sh.run);
   const bool wide = in.wide && have == kV, wide_dx = g.wide_dx && have == kV;
@@ -257,19 +302,19 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
   if (t0 < len || run == 0) {
     const T* x = in.x + b * in.bs + t0 * in.ts + c;  // of the next group
     const T* dy = g.dy + b * g.dybs + t0 * g.dyts + c;
-    Raw<T, kV> nx[U], ny[U];
+    Four<T, kWide> nx[U], ny[U];
     const int rows = (int)min(len - t0, (int64_t)1 << 30);  // that exist, from t0 on
     load_group<false, T, U>(x, in.ts, rows, wide, have, nx);
     load_group<false, T, U>(dy, g.dyts, rows, wide, have, ny);
     x += U * in.ts;
     dy += U * g.dyts;
     Quad w[K], b0, win[K - 1 + U], dp[K - 1 + U];
-    conv_weights<K>(in.weight, in.bias, c, have, w, b0);
+    conv_weights<K, kWide>(in.weight, in.bias, in.wide_weight, c, have, w, b0);
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
       float f[kV];
-      conv_input<T, K>(in, sh, b, t0 - (K - 1) + k, c, have, f);
-      win[k] = quad(f);
+      conv_input<T, K, kWide>(in, sh, b, t0 - (K - 1) + k, c, have, f);
+      win[k] = quad_of(f);
       dp[k] = {{0, 0}};
     }
     const int own = (int)(t1 - t0);  // steps of this run
@@ -297,7 +342,7 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
           // act' = s (1 + pre (1 - s)) = s + (pre s) (1 - s)
 #pragma unroll
           for (int j = 0; j < kV; ++j) f[j] = fmaf(f[j] * sg[j], 1.0f - sg[j], sg[j]);
-          const Quad a = quad(f);
+          const Quad a = quad_of(f);
 #pragma unroll
           for (int j = 0; j < 2; ++j) d[u].p[j] = mul2(d[u].p[j], a.p[j]);
         }
@@ -321,21 +366,21 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
           float f[kV];
           unquad(v, f);
           if (kFull) {
-            store_row<true>(o + u * g.dxts, wide_dx, have, f);
+            store_row<true, kWide>(o + u * g.dxts, wide_dx, have, f);
           } else {
             const int64_t p = t0 + q;
             if (g.dfinal != nullptr && p >= final0 && p < len) {
               float e[kV];
-              load_f32<T, kV>(g.dfinal + (b * (K - 1) + (p - final0)) * sh.dim + c, wide_state,
-                              have, e);
+              read_four<T, kWide>(g.dfinal + (b * (K - 1) + (p - final0)) * sh.dim + c, wide_state,
+                                  have, e);
 #pragma unroll
               for (int j = 0; j < kV; ++j) f[j] += e[j];
             }
             if (p >= 0) {
-              if (g.dx != nullptr) store_row<false>(o + u * g.dxts, wide_dx, have, f);
+              if (g.dx != nullptr) store_row<false, kWide>(o + u * g.dxts, wide_dx, have, f);
             } else if (g.dstate != nullptr) {
-              store_f32<T, kV>(g.dstate + (b * (K - 1) + (K - 1 + p)) * sh.dim + c, wide_state,
-                               have, f);
+              write_four<T, kWide>(g.dstate + (b * (K - 1) + (K - 1 + p)) * sh.dim + c, wide_state,
+                                   have, f);
             }
           }
         }
@@ -353,7 +398,7 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
     int s = 0;
     group(std::false_type{}, s);
     s += U;
-    if (wide && wide_dx && g.dx != nullptr) {
+    if ((kWide ? wide && wide_dx : have == kV) && g.dx != nullptr) {
       const int full = (int)min((int64_t)own, (int64_t)rows - U);  // the last with a next group
 #pragma unroll 1
       for (; s + U <= full; s += U) group(std::true_type{}, s);
@@ -362,16 +407,16 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
     for (; s < own + K - 1; s += U) group(std::false_type{}, s);
   } else if (g.dx != nullptr) {
     const float zero[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t t = t0; t < t1; ++t) store_f32<T, kV>(dx + t * g.dxts, wide_dx, have, zero);
+    for (int64_t t = t0; t < t1; ++t) write_four<T, kWide>(dx + t * g.dxts, wide_dx, have, zero);
   }
   // [run][K + 1][dim]: neighbouring threads write neighbours
   float* part = g.part + (b * sh.runs + run) * (K + 1) * sh.dim + c;
-  const bool wp = sh.dim % kV == 0;
+  const bool wp = kWide && sh.dim % kV == 0;
 #pragma unroll
   for (int k = 0; k <= K; ++k) {
     float f[kV];
     unquad(k < K ? dw[k < K ? k : 0] : db, f);
-    store_f32<float, kV>(part + k * sh.dim, wp, have, f);
+    write_four<float, kWide>(part + k * sh.dim, wp, have, f);
   }
 }
 
@@ -400,18 +445,19 @@ causal_conv_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t di
   else if (dbias != nullptr) dbias[d] = s;
 }
 
-template <class T, int K>
+template <class T, int K, bool kWide>
 __global__ void __launch_bounds__(kConvThreads)
 causal_conv_step_kernel(const T* __restrict__ x, int64_t x_stride, T* __restrict__ state,
                         int64_t state_rows, const void* __restrict__ slots, int index_bytes,
                         const float* __restrict__ weight, const float* __restrict__ bias,
                         bool silu, int64_t dim, int64_t col_blocks, bool wide, bool wide_state,
+                        bool wide_weight,
                         T* __restrict__ y, int64_t y_stride) {
   int64_t c;
   const int64_t b = divide(blockIdx.x, col_blocks, c);
-  c = (c * kConvThreads + threadIdx.x) * kV;
+  c = Channels<kWide>::first(c);
   if (c >= dim) return;
-  const int have = (int)min((int64_t)kV, dim - c);
+  const int have = Channels<kWide>::have(c, dim);
   const bool full = have == kV;
   const int64_t row = slots != nullptr ? load_index(slots, index_bytes, b) : b;
   float o[kV] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -421,23 +467,23 @@ causal_conv_step_kernel(const T* __restrict__ x, int64_t x_stride, T* __restrict
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
       float f[kV];
-      load_f32<T, kV>(st + k * dim, wide_state && full, have, f);
-      win[k] = quad(f);
+      read_own<T, kV, kWide, Channels<kWide>::kStep>(st + k * dim, wide_state && full, have, f);
+      win[k] = quad_of(f);
     }
     Quad w[K], b0;
-    conv_weights<K>(weight, bias, c, have, w, b0);
+    conv_weights<K, kWide>(weight, bias, wide_weight, c, have, w, b0);
     float f[kV];
-    load_f32<T, kV>(x + b * x_stride + c, wide && full, have, f);
-    win[K - 1] = quad(f);
+    read_four<T, kWide>(x + b * x_stride + c, wide && full, have, f);
+    win[K - 1] = quad_of(f);
     unquad(conv_pre<K>(w, b0, win), o);
     conv_act(silu, o);
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
       unquad(win[k + 1], f);
-      store_f32<T, kV>(st + k * dim, wide_state && full, have, f);
+      write_four<T, kWide>(st + k * dim, wide_state && full, have, f);
     }
   }
-  store_f32<T, kV>(y + b * y_stride + c, wide && full, have, o);
+  write_four<T, kWide>(y + b * y_stride + c, wide && full, have, o);
 }
 
 // The checks that the forward and the backward call share.
@@ -479,6 +525,7 @@ ConvIn<T> conv_in(const cr_causal_conv_args* a, bool wide, bool wide_state) {
   in.silu = a->activation == CR_ACT_SILU;
   in.wide = wide;
   in.wide_state = wide_state;
+  in.wide_weight = ptr_aligned(a->weight, (size_t)a->width * 4);
   return in;
 }
 
@@ -517,7 +564,8 @@ cr_status cr_causal_conv(const cr_causal_conv_args* a, void* y, int64_t y_batch_
                           rows_aligned(final_state, a->dim, a->dim, es, kV * es);
   CR_MODEL_TYPE(a->dt, CR_CONV_WIDTH(a->width, {
     CR_LAUNCH(kKCausalConv, s,
-              causal_conv_kernel<T, K><<<blocks, kConvThreads, 0, s>>>(
+              (wide && wide_y ? causal_conv_kernel<T, K, true> : causal_conv_kernel<T, K, false>)
+              <<<blocks, kConvThreads, 0, s>>>(
                   conv_in<T>(a, wide, wide_state), sh, static_cast<T*>(y), y_batch_stride,
                   y_time_stride, wide_y, static_cast<T*>(final_state)));
   }));
@@ -578,7 +626,9 @@ cr_status cr_causal_conv_backward(const cr_causal_conv_args* a, const cr_causal_
       gb.part = reinterpret_cast<float*>(past_status(ws));
       gb.wide_dx = wide_dx;
       CR_LAUNCH(kKCausalConvBackward, s,
-                causal_conv_backward_kernel<T, K><<<blocks, kConvThreads, 0, s>>>(
+                (wide && wide_dx ? causal_conv_backward_kernel<T, K, true>
+                                 : causal_conv_backward_kernel<T, K, false>)
+                <<<blocks, kConvThreads, 0, s>>>(
                     conv_in<T>(a, wide, wide_state), sh, gb));
     }));
     if (cudaGetLastError() != cudaSuccess) return CR_ERR_CUDA;
@@ -620,10 +670,13 @@ cr_status cr_causal_conv_step(const void* x, int64_t x_stride, void* state, int6
   const bool wide_state = rows_aligned(state, dim, 0, es, kV * es);
   CR_MODEL_TYPE(dt, CR_CONV_WIDTH(width, {
     CR_LAUNCH(kKCausalConvStep, s,
-              causal_conv_step_kernel<T, K><<<(unsigned)(batch * col_blocks), kConvThreads, 0, s>>>(
+              (wide && wide_state ? causal_conv_step_kernel<T, K, true>
+                                  : causal_conv_step_kernel<T, K, false>)
+              <<<(unsigned)(batch * col_blocks), kConvThreads, 0, s>>>(
                   static_cast<const T*>(x), x_stride, static_cast<T*>(state), state_rows, slots,
                   index_bytes, weight, bias, activation == CR_ACT_SILU, dim, col_blocks, wide,
-                  wide_state, static_cast<T*>(y), y_stride));
+                  wide_state, ptr_aligned(weight, (size_t)width * 4), static_cast<T*>(y),
+                  y_stride));
   }));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }

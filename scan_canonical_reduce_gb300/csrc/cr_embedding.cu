@@ -17,31 +17,45 @@ namespace cr {
 namespace {
 
 // ------------------------------------------------------------- lookup
-// A block covers blockDim.y tokens; the threads of a row walk its columns.
-template <class T, int V>
+// A block covers blockDim.y tokens; the threads of a row walk its columns, V at
+// a time: neighbours in one access (kWide), or blockDim.x apart, so that the
+// threads' accesses are consecutive.
+template <class T, int V, bool kWide>
 __global__ void __launch_bounds__(256)
 embedding_kernel(const void* __restrict__ tokens, int index_bytes, int64_t n,
                  const T* __restrict__ table, int64_t vocab, int64_t dim, int64_t row_stride,
-                 float scale, T* __restrict__ out, int64_t out_stride, bool wide) {
+                 float scale, T* __restrict__ out, int64_t out_stride) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (i >= n) return;
   const int64_t v = load_index(tokens, index_bytes, i);
   const bool real = v >= 0 && v < vocab;
   const T* src = table + (real ? v : 0) * row_stride;
   T* dst = out + i * out_stride;
-  for (int64_t c = (int64_t)threadIdx.x * V; c < dim; c += (int64_t)blockDim.x * V) {
-    const int have = (int)min((int64_t)V, dim - c);
-    const bool w = wide && have == V;
-    float f[V];
-    if (real) {
-      load_f32<T, V>(src + c, w, have, f);
+  const int tx = threadIdx.x, nx = blockDim.x;
+  if (kWide) {
+    for (int64_t c = (int64_t)tx * V; c < dim; c += (int64_t)nx * V) {
+      const int have = (int)min((int64_t)V, dim - c);
+      float f[V];
+      if (real) {
+        load_f32<T, V>(src + c, have == V, have, f);
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = f[k] * scale;
-    } else {
+        for (int k = 0; k < V; ++k) f[k] = f[k] * scale;
+      } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = 0.0f;
+        for (int k = 0; k < V; ++k) f[k] = 0.0f;
+      }
+      store_f32<T, V>(dst + c, have == V, have, f);
     }
-    store_f32<T, V>(dst + c, w, have, f);
+  } else {
+    for (int64_t c = tx; c < dim; c += (int64_t)nx * V) {
+      float f[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        f[k] = real && c + k * nx < dim ? to_f32(src[c + k * nx]) * scale : 0.0f;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (c + k * nx < dim) dst[c + k * nx] = from_f32<T>(f[k]);
+    }
   }
 }
 
@@ -209,8 +223,34 @@ template <class T>
 struct Grad {
   const T* p;
   int64_t stride;
-  bool wide;
 };
+
+// A lane's four columns among 128 of a warp: neighbours, read and written at
+// once (kWide: rows of the gradient and of the table allow it), or 32 apart,
+// so that the warp's accesses are consecutive. Columns are summed by
+// themselves, so this changes no result.
+template <bool kWide>
+struct Columns {
+  static constexpr int kStep = kWide ? 1 : 32;
+  static __device__ __forceinline__ int first(int lane) { return kWide ? lane * 4 : lane; }
+  static __device__ __forceinline__ int have(int64_t c, int64_t dim) {
+    return (int)max((int64_t)0, min((int64_t)4, (dim - c + kStep - 1) / kStep));
+  }
+};
+template <class T, bool kWide>
+using Four = Raw<T, 4, kWide, Columns<kWide>::kStep, !kWide>;
+
+template <class T, bool kWide>
+__device__ __forceinline__ void read_four(const T* p, int have, float (&f)[4]) {
+  Four<T, kWide> r;
+  r.load(p, have == 4, have);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = r.get(j);
+}
+template <bool kWide>
+__device__ __forceinline__ void write_four(float* p, int have, const float (&f)[4]) {
+  store_raw<float, 4, kWide, Columns<kWide>::kStep>(p, have == 4, have, f);
+}
 
 // The perfect tree over kRowGroup values a column.
 __device__ __forceinline__ void group_tree(float (&g)[kRowGroup][4]) {
@@ -224,7 +264,7 @@ __device__ __forceinline__ void group_tree(float (&g)[kRowGroup][4]) {
 
 // The parts of long rows: a warp takes one and 512 columns, 128 at a time.
 constexpr int kPartSteps = 4, kPartColumns = 128 * kPartSteps;
-template <class T>
+template <class T, bool kWide>
 __device__ __forceinline__ void sum_part(const Grad<T>& grad, const Sorted& in, int64_t item,
                                          int64_t dim, int64_t part_warps, float* sums) {
   const int lane = threadIdx.x % 32;
@@ -232,17 +272,17 @@ __device__ __forceinline__ void sum_part(const Grad<T>& grad, const Sorted& in, 
   const int64_t k = divide(item, part_warps, c0);
   const int32_t first = in.part[k];
   if (first < 0) return;
-  c0 = c0 * kPartColumns + lane * 4;
+  c0 = c0 * kPartColumns + Columns<kWide>::first(lane);
   const int32_t at = in.order[first + lane % kLong];
   const int64_t pitch = (dim + 3) / 4 * 4;
 #pragma unroll 1
   for (int i = 0; i < kPartSteps; ++i) {
     const int64_t c = c0 + i * 128;
-    const int have = (int)max((int64_t)0, min((int64_t)4, dim - c));
-    Raw<T, 4> raw[kLong];
+    const int have = Columns<kWide>::have(c, dim);
+    Four<T, kWide> raw[kLong];
 #pragma unroll
     for (int q = 0; q < kLong; ++q)
-      raw[q].load(grad.p + __shfl_sync(~0u, at, q) * grad.stride + c, grad.wide && have == 4, have);
+      raw[q].load(grad.p + __shfl_sync(~0u, at, q) * grad.stride + c, have == 4, have);
     float g[2][kRowGroup][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -253,10 +293,10 @@ __device__ __forceinline__ void sum_part(const Grad<T>& grad, const Sorted& in, 
       group_tree(g[h]);
     }
     static_assert(kLong == 2 * kRowGroup, "a part is two groups");
-    if (have > 0)
-      *reinterpret_cast<float4*>(sums + k * pitch + c) =
-          make_float4(add_rn(g[0][0][0], g[1][0][0]), add_rn(g[0][0][1], g[1][0][1]),
-                      add_rn(g[0][0][2], g[1][0][2]), add_rn(g[0][0][3], g[1][0][3]));
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = add_rn(g[0][0][j], g[1][0][j]);
+    write_four<kWide>(sums + k * pitch + c, have, f);
   }
 }
 
@@ -276,32 +316,31 @@ struct Table {
   float* dw;
   int64_t stride;
   float scale;
-  bool accumulate, wide;
+  bool accumulate;
 
+  template <bool kWide>
   __device__ __forceinline__ void put(int64_t v, int64_t c, int have, float (&acc)[4]) const {
     float* dst = dw + v * stride + c;
-    const bool w = wide && have == 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = acc[j] * scale;
     if (accumulate) {
       float old[4];
-      load_f32<float, 4>(dst, w, have, old);
+      read_own<float, 4, kWide, Columns<kWide>::kStep>(dst, have == 4, have, old);
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = add_rn(old[j], acc[j]);
     }
-    store_f32<float, 4>(dst, w, have, acc);
+    write_four<kWide>(dst, have, acc);
   }
 };
 
 // A long row, 128 columns, by a warp: the parts' sums eight at a time with the
 // next eight in flight, then the rows after them.
-template <class T>
+template <class T, bool kWide>
 __device__ __forceinline__ void long_row(const Grad<T>& grad, const Sorted& in, const float* sums,
                                          int64_t begin, int32_t v, int64_t c, int64_t dim,
                                          const Table& out) {
   const int lane = threadIdx.x % 32;
-  const int have = (int)max((int64_t)0, min((int64_t)4, dim - c));
-  const bool w = grad.wide && have == 4;
+  const int have = Columns<kWide>::have(c, dim);
   const int32_t first = in.row_start[v], count = in.row_start[v + 1] - first;
   const int32_t n = count / kLong, tail0 = first + n * kLong;
   const int rest = count % kLong, group = rest / kRowGroup, tail = rest % kRowGroup;
@@ -310,13 +349,13 @@ __device__ __forceinline__ void long_row(const Grad<T>& grad, const Sorted& in, 
   const float* s = sums + begin * pitch + c;
   // the rows after the parts: a group of 8, and fewer than 8
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  Raw<T, 4> r[2][kRowGroup];
+  Four<T, kWide> r[2][kRowGroup];
 #pragma unroll
   for (int k = 0; k < kRowGroup; ++k) {
     const int64_t p = __shfl_sync(~0u, at, k) * grad.stride;
     const int64_t q = __shfl_sync(~0u, at, group * kRowGroup + k) * grad.stride;
-    if (group > 0) r[0][k].load(grad.p + p + c, w, have);
-    if (k < tail) r[1][k].load(grad.p + q + c, w, have);
+    if (group > 0) r[0][k].load(grad.p + p + c, have == 4, have);
+    if (k < tail) r[1][k].load(grad.p + q + c, have == 4, have);
   }
   bool has = tail > 0;
   if (has) {
@@ -347,7 +386,7 @@ __device__ __forceinline__ void long_row(const Grad<T>& grad, const Sorted& in, 
     const int many = i < groups ? kRowGroup : n % kRowGroup;
 #pragma unroll
     for (int k = 0; k < kRowGroup; ++k)
-      if (k < many) load_f32<float, 4>(s + (i * kRowGroup + k) * pitch, have > 0, 0, next[k]);
+      if (k < many) read_four<float, kWide>(s + (i * kRowGroup + k) * pitch, have, next[k]);
   };
   load(0);
 #pragma unroll 1
@@ -402,7 +441,7 @@ __device__ __forceinline__ void long_row(const Grad<T>& grad, const Sorted& in, 
       has = true;
     }
   }
-  if (have > 0) out.put(v, c, have, acc);
+  if (have > 0) out.template put<kWide>(v, c, have, acc);
 }
 
 // The long rows: a warp takes 128 columns of those that begin among kLongParts
@@ -410,7 +449,7 @@ __device__ __forceinline__ void long_row(const Grad<T>& grad, const Sorted& in, 
 // positions: 40 us with 8 parts or one a warp; 123 us with 32 parts a block,
 // where rows wait for one another).
 constexpr int kLongParts = 8;
-template <class T>
+template <class T, bool kWide>
 __global__ void __launch_bounds__(256)
 embedding_long_kernel(Grad<T> grad, Sorted in, const float* __restrict__ sums, int64_t parts,
                       int64_t dim, int64_t long_warps, Table out) {
@@ -418,11 +457,11 @@ embedding_long_kernel(Grad<T> grad, Sorted in, const float* __restrict__ sums, i
   const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   int64_t c;
   const int64_t k = divide(item, long_warps, c) * kLongParts;
-  c = c * 128 + lane * 4;
+  c = c * 128 + Columns<kWide>::first(lane);
   const int32_t v = lane < kLongParts && k + lane < parts ? in.part_row[k + lane] : -1;
   for (uint32_t todo = __ballot_sync(~0u, v >= 0); todo != 0; todo &= todo - 1) {
     const int i = __ffs(todo) - 1;
-    long_row(grad, in, sums, k + i, __shfl_sync(~0u, v, i), c, dim, out);
+    long_row<T, kWide>(grad, in, sums, k + i, __shfl_sync(~0u, v, i), c, dim, out);
   }
 }
 
@@ -437,7 +476,7 @@ embedding_long_kernel(Grad<T> grad, Sorted in, const float* __restrict__ sums, i
 #define CR_EMBEDDING_BLOCKS 4
 #endif
 constexpr int kRowSteps = CR_EMBEDDING_STEPS, kRowColumns = 128 * kRowSteps;
-template <class T>
+template <class T, bool kWide>
 __global__ void __launch_bounds__(256, CR_EMBEDDING_BLOCKS)
 embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_warps,
                       float* __restrict__ sums, int64_t vocab, int64_t dim, int64_t row_warps,
@@ -445,29 +484,27 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
   const int lane = threadIdx.x % 32;
   int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   if (item < part_items) {
-    sum_part(grad, in, item, dim, part_warps, sums);
+    sum_part<T, kWide>(grad, in, item, dim, part_warps, sums);
     return;
   }
   item -= part_items;
   int64_t begin;  // of the warp's columns
   const int64_t v = divide(item, row_warps, begin);
   begin *= kRowColumns;
-  const int64_t c0 = begin + lane * 4;
+  const int64_t c0 = begin + Columns<kWide>::first(lane);
   if (v >= vocab) return;
   const int32_t first = in.row_start[v], count = in.row_start[v + 1] - first;
   if (count >= kLong || (count == 0 && out.accumulate)) return;
   const int steps = (int)min((int64_t)kRowSteps, (dim - begin + 127) / 128);
-  const bool full = grad.wide && out.wide && begin + steps * 128 <= dim;
-  auto have = [&](int i) {
-    return full ? 4 : (int)max((int64_t)0, min((int64_t)4, dim - c0 - i * 128));
-  };
+  const bool full = begin + steps * 128 <= dim;
+  auto have = [&](int i) { return full ? 4 : Columns<kWide>::have(c0 + i * 128, dim); };
   float* dst = out.dw + v * out.stride + c0;
   if (count == 0) {
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
       if (i < steps) {
         const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        store_f32<float, 4>(dst + i * 128, out.wide && have(i) == 4, have(i), zero);
+        write_four<kWide>(dst + i * 128, have(i), zero);
       }
     }
     return;
@@ -475,15 +512,15 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
   const int32_t at0 = in.order[first + min(lane, count - 1)];
   if (count == 1) {
     const T* src = grad.p + at0 * grad.stride + c0;
-    Raw<T, 4> r[kRowSteps];
+    Four<T, kWide> r[kRowSteps];
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i)
-      if (i < steps) r[i].load(src + i * 128, grad.wide && have(i) == 4, have(i));
+      if (i < steps) r[i].load(src + i * 128, have(i) == 4, have(i));
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
       if (i < steps) {
         float acc[4] = {r[i].get(0), r[i].get(1), r[i].get(2), r[i].get(3)};
-        out.put(v, c0 + i * 128, have(i), acc);
+        out.template put<kWide>(v, c0 + i * 128, have(i), acc);
       }
     }
     return;
@@ -493,10 +530,10 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
   for (int i = 0; i < steps; ++i) {
     const T* src = grad.p + c0 + i * 128;
     const int hv = have(i);
-    const bool w = grad.wide && hv == 4;
+    const bool w = hv == 4;
     float acc[4];
     if (tail > 0) {
-      Raw<T, 4> r[kRowGroup];
+      Four<T, kWide> r[kRowGroup];
 #pragma unroll
       for (int k = 0; k < kRowGroup - 1; ++k) {
         const int32_t q = __shfl_sync(~0u, at0, groups * kRowGroup + k);
@@ -510,7 +547,7 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
       tail_tree(g, tail, acc);
     }
     if (groups > 0) {
-      Raw<T, 4> r[kRowGroup];
+      Four<T, kWide> r[kRowGroup];
 #pragma unroll
       for (int k = 0; k < kRowGroup; ++k)
         r[k].load(src + __shfl_sync(~0u, at0, k) * grad.stride, w, hv);
@@ -523,7 +560,7 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = tail > 0 ? add_rn(g[0][j], acc[j]) : g[0][j];
     }
-    out.put(v, c0 + i * 128, hv, acc);
+    out.template put<kWide>(v, c0 + i * 128, hv, acc);
   }
 }
 
@@ -563,9 +600,10 @@ cr_status cr_embedding(const void* tokens, int32_t index_bytes, int64_t n, const
   CR_MODEL_TYPE(dt, {
     constexpr int V = 16 / sizeof(T);
     CR_LAUNCH(kKEmbedding, s,
-              embedding_kernel<T, V><<<(unsigned)blocks, block, 0, s>>>(
+              (wide ? embedding_kernel<T, V, true> : embedding_kernel<T, V, false>)
+              <<<(unsigned)blocks, block, 0, s>>>(
                   tokens, index_bytes, n, static_cast<const T*>(table), vocab, dim, row_stride,
-                  scale, static_cast<T*>(out), out_stride, wide));
+                  scale, static_cast<T*>(out), out_stride));
   });
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
@@ -623,17 +661,18 @@ cr_status cr_embedding_backward(const void* tokens, int32_t index_bytes, int64_t
   CR_LAUNCH(kKTokenSort, s,
             token_sort_kernel<<<(unsigned)ceil_div(vocab, rows), sort_threads, smem, s>>>(
                 tokens, index_bytes, n, vocab, rows, sorted));
-  const Table out = {dw, dw_stride, scale, accumulate != 0, rows_aligned(dw, dw_stride, 0, 4, 16)};
+  const Table out = {dw, dw_stride, scale, accumulate != 0};
+  const bool wide = rows_aligned(grad, grad_stride, 0, es, 4 * es) &&
+                    rows_aligned(dw, dw_stride, 0, 4, 16);
   CR_MODEL_TYPE(dt, {
-    const Grad<T> in = {static_cast<const T*>(grad), grad_stride,
-                        rows_aligned(grad, grad_stride, 0, es, 4 * es)};
+    const Grad<T> in = {static_cast<const T*>(grad), grad_stride};
     CR_LAUNCH(kKEmbeddingRows, s,
-              embedding_rows_kernel<T>
+              (wide ? embedding_rows_kernel<T, true> : embedding_rows_kernel<T, false>)
               <<<(unsigned)ceil_div(parts * part_warps + vocab * row_warps, 8), 256, 0, s>>>(
                   in, sorted, parts * part_warps, part_warps, sums, vocab, dim, row_warps, out));
     if (parts > 0)
       CR_LAUNCH(kKEmbeddingLong, s,
-                embedding_long_kernel<T>
+                (wide ? embedding_long_kernel<T, true> : embedding_long_kernel<T, false>)
                 <<<(unsigned)ceil_div(ceil_div(parts, kLongParts) * long_cols, 8), 256, 0, s>>>(
                     in, sorted, sums, parts, dim, long_cols, out));
   });

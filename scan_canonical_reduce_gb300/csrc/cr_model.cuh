@@ -65,29 +65,59 @@ __device__ __forceinline__ void store_f32(T* p, bool wide, int have, const float
   }
 }
 
-// V consecutive elements as they stand in memory, in 32-bit words: a load
-// into one of these is not waited for before its elements are used.
-template <class T, int V>
+// V elements as they stand in memory, not waited for before they are used.
+// kWide: consecutive ones, packed into 32-bit words and read at once where
+// they are aligned and all exist. Otherwise (rows that start anywhere) a word
+// each, read one by one, kStride elements apart: neighbouring threads read
+// neighbours. (Putting them together on arrival, kPack, waits for them: for
+// kernels that have other warps to run and need the registers.)
+template <class T, int V, bool kWide = true, int kStride = 1, bool kPack = false>
 struct Raw {
-  static constexpr int kWords = (V * (int)sizeof(T) + 3) / 4;
+  static constexpr bool kPacked = kWide || kPack;
+  static constexpr int kWords = kPacked ? (V * (int)sizeof(T) + 3) / 4 : V;
+  static_assert(!kWide || kStride == 1, "wide accesses are of consecutive elements");
   uint32_t w[kWords];
 
+  static __device__ __forceinline__ uint32_t bits(const T* p) {
+    if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const uint32_t*>(p));
+    else return __ldg(reinterpret_cast<const unsigned short*>(p));
+  }
   __device__ __forceinline__ float get(int k) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
-    const uint32_t q = w[k / 2];
+    const uint32_t q = kPacked ? w[k / 2] : w[k];
+    const bool high = kPacked && k % 2;
     if constexpr (std::is_same<T, __nv_bfloat16>::value)
-      return __uint_as_float(k % 2 ? q & 0xFFFF0000u : q << 16);
+      return __uint_as_float(high ? q & 0xFFFF0000u : q << 16);
     else
-      return __half2float(__ushort_as_half((unsigned short)(k % 2 ? q >> 16 : q & 0xFFFFu)));
+      return __half2float(__ushort_as_half((unsigned short)(high ? q >> 16 : q & 0xFFFFu)));
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-  // wide: p is aligned to V elements, which all exist; otherwise `have` do,
-  // the rest are zero.
-  __device__ __forceinline__ void load(const T* p, bool wide, int have) {
-    if (wide) {
+  // whole: p is aligned to V elements, which all exist; otherwise the first
+  // `have` do, the rest are zero.
+  __device__ __forceinline__ void load(const T* p, bool whole, int have) {
+    if constexpr (!kWide && kPack && sizeof(T) == 2) {
+      if (have >= V) {
+#pragma unroll
+        for (int k = 0; k < V; k += 2)
+          w[k / 2] = bits(p + k * kStride) | bits(p + (k + 1) * kStride) << 16;
+      } else {
+        zero();
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (k < have) w[k / 2] |= bits(p + k * kStride) << (k % 2 * 16);
+      }
+    } else if constexpr (!kWide) {
+      if (have >= V) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) w[k] = bits(p + k * kStride);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) w[k] = k < have ? bits(p + k * kStride) : 0;
+      }
+    } else if (whole) {
       if constexpr (V * sizeof(T) == 16) {
         const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
         w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
@@ -104,16 +134,39 @@ struct Raw {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         if (k < have) {
-          if constexpr (sizeof(T) == 4)
-            w[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + k);
-          else
-            w[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + k)
-                        << (k % 2 * 16);
+          if constexpr (sizeof(T) == 4) w[k] = bits(p + k);
+          else w[k / 2] |= bits(p + k) << (k % 2 * 16);
         }
       }
     }
   }
 };
+
+// V float values from memory that the same kernel writes (no read-only path).
+template <class T, int V, bool kWide, int kStride>
+__device__ __forceinline__ void read_own(const T* p, bool whole, int have, float (&f)[V]) {
+  if constexpr (kWide) {
+    load_f32<T, V>(p, whole, have, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = k < have ? to_f32(p[k * kStride]) : 0.0f;
+  }
+}
+
+// The same for a store of float values, rounded once.
+template <class T, int V, bool kWide, int kStride>
+__device__ __forceinline__ void store_raw(T* p, bool whole, int have, const float (&f)[V]) {
+  if constexpr (kWide) {
+    store_f32<T, V>(p, whole, have, f);
+  } else if (have >= V) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) p[k * kStride] = from_f32<T>(f[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (k < have) p[k * kStride] = from_f32<T>(f[k]);
+  }
+}
 
 // i / d with the remainder in r, for i >= 0 and d > 0: in 32 bits where both
 // fit, since a 64-bit division is about a hundred instructions (three of them
