@@ -10,6 +10,12 @@
 // and the last K of dpre) in registers, so that each input is read once, plus
 // K-1 steps of halo a run. Steps go in groups, the next group's reads in
 // flight.
+//
+// Measured, bf16, 4 x 4096 steps of 4096 channels, K = 4, SiLU: forward 60 us
+// (268 MB, 4.4 TB/s), backward 105 us (403 MB, 3.8 TB/s) and 10 us for the sums
+// over runs; DRAM and issue bound both (about 45 and 80 instructions for a step
+// of four channels). One token of 64 streams of 4096 channels 5.6 us with its
+// call.
 #include <cstdint>
 
 #include "cr_device.cuh"
@@ -191,6 +197,8 @@ __device__ __forceinline__ void store_row(T* p, bool wide, int have, const float
 #endif
 constexpr int kForward = CR_CONV_FORWARD, kBackward = 4;  // steps of a group
 
+// Blocks an SM (registers): forward 4 (118 registers; 5: the same, 6: 74 us),
+// backward 3 (108 us; 4: 115, 5: 208, with spills).
 #ifndef CR_CONV_BLOCKS
 #define CR_CONV_BLOCKS 4
 #endif

@@ -7,6 +7,12 @@
 // for one: the shift-reduce tree over the rows in order. Equal tokens are
 // brought together by a stable counting sort (integers only, so its result is
 // unique), then every row of the table is one tree.
+//
+// Measured, bf16: lookup of 32,805 rows of 4096 columns in a table of 65,536,
+// 68 us (537 MB at 7.9 TB/s, since repeated rows come from L2); gradient of
+// 65,536 rows of 2048 columns into 65,536 rows, the most frequent token 4,096
+// times, 207 us against 119 us for its 806 MB at the copy rate: 23 us sort,
+// 150 us rows and parts, 39 us long rows, each with its launch.
 #include <cstdint>
 
 #include "cr_device.cuh"
@@ -17,6 +23,7 @@ namespace cr {
 namespace {
 
 // ------------------------------------------------------------- lookup
+// Bound by DRAM; few tokens are bound by the call (3.7 us).
 // A block covers blockDim.y tokens; the threads of a row walk its columns, V at
 // a time: neighbours in one access (kWide), or blockDim.x apart, so that the
 // threads' accesses are consecutive.
@@ -100,7 +107,10 @@ __device__ __forceinline__ void load_tokens(const void* tokens, int index_bytes,
 // Warp w owns the w-th contiguous part of the positions in both sweeps; its
 // counters are its own, and within 32 positions equal tokens are ranked by
 // lane, so the order is that of the positions. All counts are integers: the
-// result is unique whatever the order of the atomics.
+// result is unique whatever the order of the atomics. Every block reading all
+// tokens costs L2 reads (65,536 tokens: 152 x 512 KB, about 4 us a sweep) and
+// saves the launches and the traffic of a sort by digits; a warp's own tokens
+// are kept from the first sweep, which halves the second's time for most.
 //
 // A row with kLong positions or more has its complete groups of kLong summed
 // by blocks of their own. Group k of the row that begins at s is number
@@ -467,7 +477,9 @@ embedding_long_kernel(Grad<T> grad, Sorted in, const float* __restrict__ sums, i
 
 // The other rows: a warp takes one and kRowSteps times 128 columns, so that
 // a row of one position, the most frequent length, has kRowSteps reads in
-// flight behind the two that find it. The first blocks take the parts of the
+// flight behind the two that find it. Bound by DRAM and by those reads' latency
+// (4 steps and 4 blocks an SM measured 127 us of rows alone where 2 steps took
+// 155, 3 blocks 134). The first blocks take the parts of the
 // long rows, which need no more than the sort either.
 #ifndef CR_EMBEDDING_STEPS
 #define CR_EMBEDDING_STEPS 4

@@ -105,7 +105,7 @@ def test_gradient_of_one_frequent_token(scr, count):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,V,D,count", [(5000, 40, 1030, 3000), (700, 9, 520, 577),
-                                         (9000, 700, 260, 8200)])
+                                         (9000, 700, 260, 8200), (17000, 300, 130, 15001)])
 def test_gradient_of_long_rows(scr, dtype, n, V, D, count):
     """Long rows of many columns beside short ones: several warps to a row."""
     tok = torch.randint(0, V, (n,), generator=gen(22))

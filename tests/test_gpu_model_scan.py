@@ -274,3 +274,20 @@ def test_repeated_calls_give_the_same_bits(scr):
         assert torch.equal(scr.selective_scan(**d), y)
         again = scr.selective_scan_backward(dy.to(DEV), **d, checkpoints=kept)
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_overflow_stays_in_its_sequence(scr):
+    """A state that has overflowed: positions past the length still give zeros,
+    and the other sequences what they give without it."""
+    s, dy, _ = make(3, 40, 24, 16, 1, torch.float32, 16, lengths=[40, 21, 33])
+    want = scr.selective_scan(**dev(s))
+    gwant = scr.selective_scan_backward(dy.to(DEV), **dev(s))
+    s["u"][1, 5] = float("inf")
+    y, final = scr.selective_scan(**dev(s), return_state=True)
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s))
+    assert not torch.isfinite(final[1]).all()
+    for b in (0, 2):
+        assert torch.equal(y[b], want[b])
+        assert all(torch.equal(g[k][b], gwant[k][b]) for k in SEQ + ("state",))
+    assert not y[1, 21:].any()
+    assert not any(g[k][1, 21:].any() for k in SEQ)
