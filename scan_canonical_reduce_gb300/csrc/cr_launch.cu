@@ -78,7 +78,7 @@ const char* kernel_name(int id) {
       "chain_link_kernel",     "chain_verify_kernel",   "chain_walk_fix_kernel",
       "scan_local_again_kernel", "fixup_again_kernel", "pairwise_tile_prefix_kernel",
       "chain_round_sum_kernel", "scan_seq_left2_kernel", "embedding_kernel",
-      "token_sort_kernel", "embedding_long_kernel", "embedding_rows_kernel", "causal_conv_kernel",
+      "token_sort_kernel", "embedding_few_kernel", "embedding_long_kernel", "embedding_rows_kernel", "causal_conv_kernel",
       "causal_conv_backward_kernel", "causal_conv_sum_kernel", "causal_conv_step_kernel",
       "selective_scan_kernel", "selective_scan_states_kernel", "selective_scan_backward_kernel",
       "selective_scan_sum_kernel",

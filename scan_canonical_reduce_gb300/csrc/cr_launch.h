@@ -46,6 +46,7 @@ enum KernelId : int {
   kKScanSeqLeft2,
   kKEmbedding,
   kKTokenSort,
+  kKEmbeddingFew,
   kKEmbeddingLong,
   kKEmbeddingRows,
   kKCausalConv,

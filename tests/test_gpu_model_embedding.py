@@ -130,9 +130,10 @@ def test_gradient_large_vocabulary(scr):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_gradient_accumulates(scr, dtype):
+@pytest.mark.parametrize("n,V,D", [(500, 900, 68), (5000, 9000, 68), (3000, 2000, 37),
+                                   (2048, 700, 130), (2049, 700, 130)])
+def test_gradient_accumulates(scr, dtype, n, V, D):
     """out + scale * tree on rows with tokens, others untouched (NaN stays)."""
-    n, V, D = 500, 900, 68
     tok = skewed(n, V, 12)
     grad = torch.randn(n, D, generator=gen(13)).to(dtype)
     old = torch.randn(V, D, generator=gen(14))
@@ -155,18 +156,19 @@ def test_gradient_skips_padding_rows(scr):
     assert not got[[0, 1, 2, 4, 6, 7, 8, 9]].any()
 
 
-def test_gradient_strided(scr):
-    tok = skewed(200, 30, 16)
-    base = torch.full((200, 150), float("nan"))
-    base[:, 5:138] = torch.randn(200, 133, generator=gen(17))
+@pytest.mark.parametrize("n", [200, 3000])
+def test_gradient_strided(scr, n):
+    tok = skewed(n, 30, 16)
+    base = torch.full((n, 150), float("nan"))
+    base[:, 5:138] = torch.randn(n, 133, generator=gen(17))
     out = torch.full((30, 140), -1.0, device=DEV)
     scr.embedding_backward(tok.to(DEV), base.to(DEV)[:, 5:138], 30, out=out[:, 3:136])
     got = out.cpu().numpy()
     assert got[:, 3:136].tobytes() == want_grad(tok, base[:, 5:138], 30, 1.0).tobytes()
     assert (got[:, :3] == -1).all() and (got[:, 136:] == -1).all()
     one = torch.randn(133, generator=gen(18))
-    got = scr.embedding_backward(tok.to(DEV), one.to(DEV).expand(200, 133), 30).cpu().numpy()
-    assert got.tobytes() == want_grad(tok, one.expand(200, 133), 30, 1.0).tobytes()
+    got = scr.embedding_backward(tok.to(DEV), one.to(DEV).expand(n, 133), 30).cpu().numpy()
+    assert got.tobytes() == want_grad(tok, one.expand(n, 133), 30, 1.0).tobytes()
 
 
 def test_gradient_matches_differences(scr):

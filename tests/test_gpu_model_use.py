@@ -128,17 +128,20 @@ def test_threads_on_their_own_streams(scr):
 
 
 def test_launches_are_counted_and_named(scr):
-    t = inputs(5)
+    t, many = inputs(5), inputs(5, T=900)  # the gradient of the lookup: few tokens, and many
     calls(scr, t)
+    calls(scr, many)
     before = scr.launch_count()
     scr.profile_enable(True)
     scr.profile_collect()
     calls(scr, t)
+    calls(scr, many)
     torch.cuda.synchronize()
     records = scr.profile_collect()
     scr.profile_enable(False)
     assert scr.launch_count() - before == len(records)
     names = {n for n, _ in records}
+    assert "embedding_few_kernel" in names
     assert {"embedding_kernel", "token_sort_kernel", "embedding_rows_kernel", "causal_conv_kernel",
             "causal_conv_backward_kernel", "causal_conv_step_kernel", "selective_scan_kernel",
             "selective_scan_backward_kernel", "selective_scan_step_kernel"} <= names
