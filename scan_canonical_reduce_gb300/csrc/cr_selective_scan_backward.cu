@@ -171,16 +171,9 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
   };
   if (tiles > 0) load(tiles - 1);
   __syncthreads();  // Ds, biases
-  // sums over thousands of steps, with what each addition rounded off beside
-  // them (Kahan's summation; two additions a tile, nothing beside the rest)
-  float dD[VE], dbias[VE], lost_D[VE], lost_bias[VE];
+  float dD[VE], dbias[VE];
 #pragma unroll
-  for (int k = 0; k < VE; ++k) dD[k] = dbias[k] = lost_D[k] = lost_bias[k] = 0.0f;
-  auto add = [](float& sum, float& lost, float v) {
-    const float x = v - lost, t = sum + x;
-    lost = (t - sum) - x;
-    sum = t;
-  };
+  for (int k = 0; k < VE; ++k) dD[k] = dbias[k] = 0.0f;
 
   for (int64_t tile = tiles - 1; tile >= 0; --tile) {
     const int64_t t0 = tile * TT;
@@ -409,8 +402,8 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
           if (in_seq) {
-            add(dD[k], lost_D[k], p[k] * u[k]);
-            add(dbias[k], lost_bias[k], fd[k]);
+            dD[k] = fmaf(p[k], u[k], dD[k]);
+            dbias[k] += fd[k];
           } else {
             fu[k] = fd[k] = fz[k] = 0.0f;
           }
