@@ -492,6 +492,26 @@ selective_scan_sum_a_kernel(const float* __restrict__ part, int64_t batch, int64
 
 extern "C" {
 
+// Lanes that share a channel: those of its states, or more (whose states are
+// zero) where the call has few warps, as each then walks its steps with less
+// to do. A rule on sizes alone, so that results do not depend on the GPU; a
+// GB300 has 608 schedulers, and 1,216 of these warps are resident. Gradient
+// kernel, 4 states, 2048 steps, with 1, 2 and 4 lanes: 512 channels 529, 432
+// and 364 us; 4 x 2048 channels (256 warps of one lane) 560, 514 and 493, with
+// 2047 channels 1193, 610 and 551; 1024 steps of 8 x 2048 (512) 303, 282 and
+// 494, of 16 x 2048 365, 556 and 981. 8 states, 4 x 2048 channels (512 warps
+// of two lanes): 467 with 2, 492 with 4. 8 lanes lose from 512 channels up
+// (16 states: 332 us with 4, 343 with 8).
+static int backward_lanes(int64_t batch, int64_t dim, int dstate) {
+  int lanes = cr::scan_lanes(dstate);
+  while (lanes < 4) {
+    const int64_t most = lanes == 1 ? 1216 : 608;  // warps with twice the lanes
+    if (batch > most || dim > most * 32 || batch * cr::ceil_div(dim * lanes * 2, 32) > most) break;
+    lanes *= 2;
+  }
+  return lanes;
+}
+
 // Blocks that share a group of a sequence: each leaves its own dB and dC.
 static int64_t group_blocks(int64_t dim, int32_t groups, int lanes) {
   return cr::ceil_div(dim / groups, cr::kScanThreads / lanes);
@@ -501,7 +521,7 @@ size_t cr_selective_scan_backward_workspace_bytes(int64_t batch, int64_t len, in
                                                   int32_t dstate, int32_t groups) {
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || dstate < 1 || groups < 1 || dim % groups != 0) return 0;
-  const int lanes = scan_lanes(dstate);
+  const int lanes = backward_lanes(batch, dim, dstate);
   const size_t bc = (size_t)batch * len * groups * group_blocks(dim, groups, lanes) * 2 *
                     (lanes * kS) * 4;
   return round256(bc) + round256((size_t)batch * dim * (dstate + 2) * 4) + kStatusBytes;
@@ -536,7 +556,7 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
                                                                  a->dstate, a->groups);
   if (ws == nullptr || !ptr_aligned(ws, 256) || ws_bytes < need) return CR_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int lanes = scan_lanes(a->dstate);
+  const int lanes = backward_lanes(a->batch, a->dim, a->dstate);
   const int64_t parts = group_blocks(a->dim, a->groups, lanes);
   const int64_t rows = a->batch * a->len * a->groups;
   float* part_BC = reinterpret_cast<float*>(past_status(ws));

@@ -291,3 +291,21 @@ def test_overflow_stays_in_its_sequence(scr):
         assert all(torch.equal(g[k][b], gwant[k][b]) for k in SEQ + ("state",))
     assert not y[1, 21:].any()
     assert not any(g[k][1, 21:].any() for k in SEQ)
+
+
+# few states: the gradient shares a channel among one, two or four lanes,
+# by how many channels there are
+MANY = [(2, 19, 20000, 4, 1), (2, 17, 20010, 3, 3), (2, 33, 5002, 8, 1), (1, 20, 5001, 7, 1),
+        (1, 20, 10000, 4, 1), (1, 34, 1032, 4, 1), (3, 18, 501, 6, 3)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", MANY)
+def test_backward_of_few_states(scr, dtype, shape):
+    batch, T = shape[:2]
+    lengths = [T, T // 2, 0][:batch]
+    s, dy, dfinal = make(*shape, dtype, 17, lengths=lengths)
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    check_grads(g, reference(s, True, dy, dfinal)["grads"], *shape)
+    for b, n in enumerate(lengths):
+        assert not any(g[k][b, n:].any() for k in SEQ)
