@@ -277,16 +277,18 @@ PyObject* embedding(PyObject* const* a) {
   const On on(index, a[4]);
   if (a[0] == Py_None) bad_type("tokens must be a tensor");
   const Indices tok = indices(a[0], "tokens", std::nullopt, index);
-  const at::Tensor table = rows(table0);
-  const int64_t n = tok.t.numel(), vocab = table.size(0), dim = table.size(1);
+  const int64_t n = tok.t.numel(), vocab = table0.size(0), dim = table0.size(1);
+  at::Tensor table = rows(table0);
+  if (vocab > 1 && table.stride(0) < dim) table = table.contiguous();  // rows that overlap
   std::vector<int64_t> shape = tok.t.sizes().vec();
   shape.push_back(dim);
   const at::Tensor o = on.output(a[3], shape, table.scalar_type());
   const at::Tensor flat = o.dim() == 2 ? o : o.view({n, dim});
   on.uses(tok.t, table);
+  // a single row's stride means nothing; those of several are the tensors' own
   check(f_embedding(tok.p, tok.bytes, n, table.data_ptr(), vocab, dim,
-                    std::max(table.stride(0), dim), scale, code, flat.data_ptr(),
-                    std::max(flat.stride(0), dim), on.ptr),
+                    vocab > 1 ? table.stride(0) : dim, scale, code, flat.data_ptr(),
+                    n > 1 ? flat.stride(0) : dim, on.ptr),
         "cr_embedding");
   return wrap(o);
 }

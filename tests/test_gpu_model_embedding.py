@@ -64,6 +64,28 @@ def test_lookup_shapes_and_strides(scr):
     assert out[:, 0].isnan().all() and out[:, 65:].isnan().all() and out[15].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_lookup_of_overlapping_rows(scr, dtype):
+    """A table whose rows share memory gives what its copy gives; an output
+    whose rows do is refused. Inside a larger buffer, so that a row taken from
+    the wrong place is still a row of the buffer."""
+    base = torch.randn(4096, generator=gen(30)).to(dtype).to(DEV)
+    tok = torch.tensor([3, 0, -1, 6, 5, 7], device=DEV)
+    for table in (base[:24].expand(7, 24), base[:40].unfold(0, 24, 1)[:7],
+                  base[:200].unfold(0, 24, 8)[:7], base[5:29].expand(7, 24)):
+        assert torch.equal(scr.embedding(tok, table, 0.5),
+                           scr.embedding(tok, table.contiguous(), 0.5))
+    table = base[:7 * 24].view(7, 24)
+    one = torch.tensor([4], device=DEV)  # a single row may stand anywhere
+    assert torch.equal(scr.embedding(one * 0, table[2:3].expand(1, 24)), table[2:3])
+    out = torch.full((64, 24), 7.0, dtype=dtype, device=DEV)
+    for bad in (out[:1].expand(6, 24), out.view(-1)[:64].unfold(0, 24, 8)[:6]):
+        with pytest.raises(scr.CrError):
+            scr.embedding(tok, table, out=bad)
+    assert (out == 7).all()
+    assert torch.equal(scr.embedding(one, table, out=out[:1].expand(1, 24))[0], table[4])
+
+
 def tree(rows):
     """The canonical tree over rows (k, D) float32, column by column."""
     x = np.ascontiguousarray(rows.T.astype(np.float32))
