@@ -118,49 +118,6 @@ void need(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::Scal
     bad_value(join(name, " must be on cuda:", index, ", got ", t.device()));
 }
 
-// t with a contiguous last axis.
-at::Tensor rows(const at::Tensor& t) {
-  return t.size(-1) <= 1 || t.stride(-1) == 1 ? t : t.contiguous();
-}
-
-at::Tensor dense(const at::Tensor& t) { return t.is_contiguous() ? t : t.contiguous(); }
-
-// An int32 or int64 tensor of indices, contiguous.
-struct Indices {
-  at::Tensor t;
-  const void* p = nullptr;
-  int32_t bytes = 4;
-};
-
-Indices indices(PyObject* o, const char* name, std::optional<at::IntArrayRef> shape, int index) {
-  Indices r;
-  if (o == Py_None) return r;
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong)
-    bad_type(join(name, " must be int32 or int64, got ", t.scalar_type()));
-  need(t, name, shape ? *shape : t.sizes(), t.scalar_type(), index);
-  r.t = dense(t);
-  r.p = r.t.data_ptr();
-  r.bytes = (int32_t)r.t.element_size();
-  return r;
-}
-
-// An optional float32 vector or array, contiguous.
-struct Floats {
-  at::Tensor t;
-  float* p = nullptr;
-};
-
-Floats floats(PyObject* o, const char* name, at::IntArrayRef shape, int index) {
-  Floats r;
-  if (o == Py_None) return r;
-  const at::Tensor& t = tensor(o, name);
-  need(t, name, shape, at::kFloat, index);
-  r.t = dense(t);
-  r.p = static_cast<float*>(r.t.data_ptr());
-  return r;
-}
-
 int32_t activation(PyObject* o) {
   if (o == Py_None) return CR_ACT_NONE;
   if (PyUnicode_Check(o) && PyUnicode_CompareWithASCIIString(o, "silu") == 0) return CR_ACT_SILU;
@@ -219,12 +176,7 @@ struct On {
     return t;
   }
   void uses(const at::Tensor& t) const {
-    if (other && t.defined()) t.record_stream(*other);
-  }
-  template <class... A>
-  void uses(const at::Tensor& t, const A&... more) const {
-    uses(t);
-    uses(more...);
+    if (other) t.record_stream(*other);
   }
 
   // The binding's workspace of this stream (held here too, so that a call
@@ -254,6 +206,57 @@ struct On {
   }
 };
 
+// An argument as the calls take it, copied where its layout asks for it. The
+// copy is made on the call's stream, so it is the caller's tensor that the
+// allocator is told about: the copy is of that stream's own memory.
+// With a contiguous last axis:
+at::Tensor rows(const On& on, const at::Tensor& t) {
+  on.uses(t);
+  return t.size(-1) <= 1 || t.stride(-1) == 1 ? t : t.contiguous();
+}
+
+at::Tensor dense(const On& on, const at::Tensor& t) {
+  on.uses(t);
+  return t.is_contiguous() ? t : t.contiguous();
+}
+
+// An int32 or int64 tensor of indices, contiguous.
+struct Indices {
+  at::Tensor t;
+  const void* p = nullptr;
+  int32_t bytes = 4;
+};
+
+Indices indices(const On& on, PyObject* o, const char* name,
+                std::optional<at::IntArrayRef> shape) {
+  Indices r;
+  if (o == Py_None) return r;
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong)
+    bad_type(join(name, " must be int32 or int64, got ", t.scalar_type()));
+  need(t, name, shape ? *shape : t.sizes(), t.scalar_type(), on.index);
+  r.t = dense(on, t);
+  r.p = r.t.data_ptr();
+  r.bytes = (int32_t)r.t.element_size();
+  return r;
+}
+
+// An optional float32 vector or array, contiguous.
+struct Floats {
+  at::Tensor t;
+  float* p = nullptr;
+};
+
+Floats floats(const On& on, PyObject* o, const char* name, at::IntArrayRef shape) {
+  Floats r;
+  if (o == Py_None) return r;
+  const at::Tensor& t = tensor(o, name);
+  need(t, name, shape, at::kFloat, on.index);
+  r.t = dense(on, t);
+  r.p = static_cast<float*>(r.t.data_ptr());
+  return r;
+}
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
 void put(PyObject* dict, const char* name, const at::Tensor& t) {
@@ -276,15 +279,14 @@ PyObject* embedding(PyObject* const* a) {
   const float scale = real(a[2]);
   const On on(index, a[4]);
   if (a[0] == Py_None) bad_type("tokens must be a tensor");
-  const Indices tok = indices(a[0], "tokens", std::nullopt, index);
+  const Indices tok = indices(on, a[0], "tokens", std::nullopt);
   const int64_t n = tok.t.numel(), vocab = table0.size(0), dim = table0.size(1);
-  at::Tensor table = rows(table0);
+  at::Tensor table = rows(on, table0);
   if (vocab > 1 && table.stride(0) < dim) table = table.contiguous();  // rows that overlap
   std::vector<int64_t> shape = tok.t.sizes().vec();
   shape.push_back(dim);
   const at::Tensor o = on.output(a[3], shape, table.scalar_type());
   const at::Tensor flat = o.dim() == 2 ? o : o.view({n, dim});
-  on.uses(tok.t, table);
   // a single row's stride means nothing; those of several are the tensors' own
   check(f_embedding(tok.p, tok.bytes, n, table.data_ptr(), vocab, dim,
                     vocab > 1 ? table.stride(0) : dim, scale, code, flat.data_ptr(),
@@ -307,14 +309,14 @@ PyObject* embedding_backward(PyObject* const* a) {
   const float scale = real(a[3]);
   const cr_dtype code = type_code(grad0);
   const On on(index, a[6]);
-  const Indices tok = indices(a[0], "tokens", std::nullopt, index);
+  const Indices tok = indices(on, a[0], "tokens", std::nullopt);
   const int64_t n = tok.t.numel(), dim = grad0.size(-1);
-  at::Tensor grad = rows(grad0.dim() == 2 ? grad0 : grad0.reshape({n, dim}));
+  on.uses(grad0);  // which reshape may copy
+  at::Tensor grad = rows(on, grad0.dim() == 2 ? grad0 : grad0.reshape({n, dim}));
   if (n > 1 && grad.stride(0) < dim) grad = grad.contiguous();  // a zero stride
   const at::Tensor o = on.output(a[4], {vocab, dim}, at::kFloat);
   const at::Tensor ws = on.workspace(f_embedding_backward_workspace_bytes(n, vocab, dim),
                                       "embedding_backward", a[6]);
-  on.uses(tok.t, grad);
   check(f_embedding_backward(tok.p, tok.bytes, n, grad.data_ptr(), n > 1 ? grad.stride(0) : dim,
                              vocab, dim, scale, code, accumulate,
                              static_cast<float*>(o.data_ptr()), vocab > 1 ? o.stride(0) : dim,
@@ -349,17 +351,16 @@ struct Conv {
     const at::Tensor& w = tensor(a[1], "weight");
     if (w.dim() != 2) bad_value("weight must be (channel, width)");
     const int64_t K = w.size(1);
-    weight = floats(a[1], "weight", {dim, K}, index);
-    bias = floats(a[2], "bias", {dim}, index);
+    weight = floats(on, a[1], "weight", {dim, K});
+    bias = floats(on, a[2], "bias", {dim});
     const int32_t act = activation(a[3]);
     if (a[4] != Py_None) {
       const at::Tensor& s = tensor(a[4], "state");
       need(s, "state", {batch, K - 1, dim}, x0.scalar_type(), index);
-      state = dense(s);
+      state = dense(on, s);
     }
-    lengths = indices(a[5], "lengths", at::IntArrayRef({batch}), index);
-    x = rows(x0);
-    on.uses(x, weight.t, bias.t, state, lengths.t);
+    lengths = indices(on, a[5], "lengths", at::IntArrayRef({batch}));
+    x = rows(on, x0);
     args = {batch, len, dim, (int32_t)K, act, code, lengths.bytes, x.data_ptr(), x.stride(0),
             x.stride(1), weight.p, bias.p, state.defined() ? state.data_ptr() : nullptr,
             lengths.p};
@@ -386,13 +387,13 @@ PyObject* causal_conv_backward(PyObject* const* a) {
   const at::ScalarType type = c.x0.scalar_type();
   const at::Tensor& dy0 = tensor(a[6], "dy");
   need(dy0, "dy", c.x0.sizes(), type, c.index);
-  const at::Tensor dy = rows(dy0);
+  const at::Tensor dy = rows(c.on, dy0);
   const int64_t K = c.args.width;
   at::Tensor dfinal, db, ds;
   if (a[7] != Py_None) {
     const at::Tensor& t = tensor(a[7], "dfinal");
     need(t, "dfinal", {c.args.batch, K - 1, c.args.dim}, type, c.index);
-    dfinal = dense(t);
+    dfinal = dense(c.on, t);
   }
   const at::Tensor dx = c.on.empty(c.x0.sizes(), type);
   const at::Tensor dw = c.on.empty({c.args.dim, K}, at::kFloat);
@@ -401,7 +402,6 @@ PyObject* causal_conv_backward(PyObject* const* a) {
   const at::Tensor ws = c.on.workspace(
       f_causal_conv_backward_workspace_bytes(c.args.batch, c.args.len, c.args.dim, (int32_t)K),
       "causal_conv_backward", a[8]);
-  c.on.uses(dy, dfinal);
   const cr_causal_conv_grads g = {dy.data_ptr(),
                                   dy.stride(0),
                                   dy.stride(1),
@@ -424,14 +424,15 @@ PyObject* causal_conv_backward(PyObject* const* a) {
 }
 
 // A state that a step updates in place: (rows, ...), contiguous.
-const at::Tensor& step_state(PyObject* o, at::IntArrayRef row, at::ScalarType dtype, int index,
+const at::Tensor& step_state(const On& on, PyObject* o, at::IntArrayRef row, at::ScalarType dtype,
                              int64_t batch, bool slots) {
   const at::Tensor& t = tensor(o, "state");
   if (t.dim() != 3) bad_value("state must be 3-D (rows, then what a row holds)");
-  need(t, "state", {t.size(0), row[0], row[1]}, dtype, index);
+  need(t, "state", {t.size(0), row[0], row[1]}, dtype, on.index);
   if (!t.is_contiguous()) bad_value("state must be contiguous (it is updated in place)");
   if (!slots && t.size(0) < batch)
     bad_value(join("state must have a row for each of the ", batch, " streams"));
+  on.uses(t);
   return t;
 }
 
@@ -444,14 +445,13 @@ PyObject* causal_conv_step(PyObject* const* a) {
   const cr_dtype code = type_code(x0);
   const On on(index, a[7]);
   const int64_t batch = x0.size(0), dim = x0.size(1), K = w.size(1);
-  const Floats weight = floats(a[2], "weight", {dim, K}, index);
-  const Floats bias = floats(a[3], "bias", {dim}, index);
-  const Indices slots = indices(a[5], "slots", at::IntArrayRef({batch}), index);
+  const Floats weight = floats(on, a[2], "weight", {dim, K});
+  const Floats bias = floats(on, a[3], "bias", {dim});
+  const Indices slots = indices(on, a[5], "slots", at::IntArrayRef({batch}));
   const at::Tensor& state =
-      step_state(a[1], {K - 1, dim}, x0.scalar_type(), index, batch, a[5] != Py_None);
-  const at::Tensor x = rows(x0);
+      step_state(on, a[1], {K - 1, dim}, x0.scalar_type(), batch, a[5] != Py_None);
+  const at::Tensor x = rows(on, x0);
   const at::Tensor y = on.output(a[6], x0.sizes(), x0.scalar_type());
-  on.uses(x, state, weight.t, bias.t, slots.t);
   check(f_causal_conv_step(x.data_ptr(), x.stride(0), state.data_ptr(), state.size(0), slots.p,
                            slots.bytes, weight.p, bias.p, activation(a[4]), batch, dim,
                            (int32_t)K, code, y.data_ptr(), y.stride(0), on.ptr),
@@ -490,6 +490,7 @@ struct Scan {
     shape.push_back(t.size(-2));
     shape.push_back(N);
     need(t, name, shape, u0.scalar_type(), index);
+    on.uses(t);
     if ((N > 1 && t.stride(-1) != 1) || (t.size(-2) > 1 && t.stride(-2) != N)) t = t.contiguous();
     return t;
   }
@@ -497,7 +498,7 @@ struct Scan {
   at::Tensor like_u(PyObject* o, const char* name) {
     const at::Tensor& t = tensor(o, name);
     need(t, name, u0.sizes(), u0.scalar_type(), index);
-    return rows(t);
+    return rows(on, t);
   }
 
   Scan(PyObject* const* a, PyObject* state0, PyObject* lengths0, PyObject* stream, bool step)
@@ -507,21 +508,20 @@ struct Scan {
     const at::Tensor& A0 = tensor(a[2], "A");
     if (A0.dim() != 2) bad_value("A must be (dim, dstate)");
     const int64_t N = A0.size(1);
-    A = floats(a[2], "A", {dim, N}, index);
-    u = rows(u0);
+    A = floats(on, a[2], "A", {dim, N});
+    u = rows(on, u0);
     dt = like_u(a[1], "dt");
     B = states(a[3], "B", N);
     C = states(a[4], "C", N);
     const int64_t groups = B.size(-2);
     if (groups < 1 || dim % groups != 0 || C.size(-2) != groups)
       bad_value("B and C must be (..., groups, dstate) with groups dividing dim");
-    D = floats(a[5], "D", {dim}, index);
+    D = floats(on, a[5], "D", {dim});
     if (a[6] != Py_None) z = like_u(a[6], "z");
-    dt_bias = floats(a[7], "dt_bias", {dim}, index);
+    dt_bias = floats(on, a[7], "dt_bias", {dim});
     const bool softplus = flag(a[8]);
-    if (state0 != Py_None) state = floats(state0, "state", {batch, dim, N}, index);
-    lengths = indices(lengths0, step ? "slots" : "lengths", at::IntArrayRef({batch}), index);
-    on.uses(u, dt, z, B, C, A.t, D.t, dt_bias.t, state.t, lengths.t);
+    if (state0 != Py_None) state = floats(on, state0, "state", {batch, dim, N});
+    lengths = indices(on, lengths0, step ? "slots" : "lengths", at::IntArrayRef({batch}));
     const int64_t t = step ? 0 : 1;
     args = {batch,
             len,
@@ -589,8 +589,8 @@ PyObject* selective_scan_backward(PyObject* const* a) {
   const at::ScalarType type = s.u0.scalar_type();
   const at::Tensor& dy0 = tensor(a[11], "dy");
   need(dy0, "dy", s.u0.sizes(), type, s.index);
-  const at::Tensor dy = rows(dy0);
-  const Floats dfinal = floats(a[12], "dfinal", {batch, dim, N}, s.index);
+  const at::Tensor dy = rows(s.on, dy0);
+  const Floats dfinal = floats(s.on, a[12], "dfinal", {batch, dim, N});
   const at::Tensor& kept = tensor(a[13], "checkpoints");
   need(kept, "checkpoints", {batch, f_selective_scan_checkpoints(s.args.len), dim, N}, at::kFloat,
        s.index);
@@ -617,7 +617,7 @@ PyObject* selective_scan_backward(PyObject* const* a) {
       f_selective_scan_backward_workspace_bytes(batch, s.args.len, dim, (int32_t)N,
                                                 s.args.groups),
       "selective_scan_backward", a[14]);
-  s.on.uses(dy, dfinal.t, kept);
+  s.on.uses(kept);
   const cr_selective_scan_grads g = {dy.data_ptr(), dy.stride(0), dy.stride(1), dfinal.p,
                                      static_cast<const float*>(kept.data_ptr()),
                                      du.p(), ddt.p(), dz.p(), dB.p(), dC.p(), dA.f(), dD.f(),
@@ -636,9 +636,8 @@ PyObject* selective_scan_step(PyObject* const* a) {
   const Scan s(a, Py_None, a[10], a[12], true);
   const int64_t batch = s.args.batch, dim = s.args.dim;
   const at::Tensor& state =
-      step_state(a[9], {dim, s.args.dstate}, at::kFloat, s.index, batch, a[10] != Py_None);
+      step_state(s.on, a[9], {dim, s.args.dstate}, at::kFloat, batch, a[10] != Py_None);
   const at::Tensor y = s.on.output(a[11], s.u0.sizes(), s.u0.scalar_type());
-  s.on.uses(state);
   check(f_selective_scan_step(&s.args, static_cast<float*>(state.data_ptr()), state.size(0),
                               s.lengths.p, y.data_ptr(), y.stride(0), s.on.ptr),
         "cr_selective_scan_step");

@@ -83,6 +83,63 @@ def test_other_streams(scr):
     del junk
 
 
+def test_other_streams_copy_inputs(scr):
+    """Inputs that the calls copy, as their layout is not one that they take: what
+    the copy reads stays the caller's until the busy stream has come to it."""
+    def turned(v):  # the same values, the last axis not contiguous
+        return v.transpose(0, -1).contiguous().transpose(0, -1)
+
+    def spread(v):  # every second element of a longer tensor
+        return torch.stack([v, v], -1)[..., 0]
+
+    def run(stream):
+        t = inputs(21)
+        u = {k: turned(t[k]) for k in ("table", "x", "dt", "z", "B", "C", "A", "weight", "conv",
+                                       "scan", "dy")}
+        u.update({k: spread(t[k]) for k in ("tokens", "D", "dt_bias", "bias")})
+        lengths = spread(torch.tensor([150, 3, 77], device=DEV))
+        rows = t["x"][0, :1].clone()
+        pools = t["conv"].clone(), t["scan"].clone()
+        slots = spread(torch.tensor([2, 0, 1], device=DEV))
+        dfinal = turned(t["scan"]), turned(t["conv"])
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(DEV))
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+        k = dict(stream=stream)
+        out = [scr.embedding(u["tokens"], u["table"], 2.0, **k),
+               scr.embedding(u["tokens"], rows.expand(500, 200), **k),
+               scr.embedding_backward(u["tokens"], u["dy"], 500, **k),
+               scr.embedding_backward(u["tokens"], rows[:, None].expand(3, 150, 200), 500, **k)]
+        conv = dict(activation="silu", state=u["conv"], lengths=lengths, **k)
+        out += scr.causal_conv(u["x"], u["weight"], u["bias"], return_state=True, **conv)
+        out += scr.causal_conv_backward(u["dy"], u["x"], u["weight"], u["bias"], dfinal=dfinal[1],
+                                        **conv).values()
+        scan = dict(D=u["D"], z=u["z"], dt_bias=u["dt_bias"], **k)
+        main = (u["x"], u["dt"], u["A"], u["B"], u["C"])
+        out += scr.selective_scan(*main, state=u["scan"], lengths=lengths, return_state=True,
+                                  **scan)
+        out += scr.selective_scan_backward(u["dy"], *main, state=u["scan"], lengths=lengths,
+                                           dfinal=dfinal[0], **scan).values()
+        one = {n: u[n][:, 0] for n in ("x", "dt", "z", "B", "C")}
+        out.append(scr.causal_conv_step(one["x"], pools[0], u["weight"], u["bias"], "silu", slots,
+                                        **k))
+        out.append(scr.selective_scan_step(one["x"], one["dt"], u["A"], one["B"], one["C"],
+                                           pools[1], u["D"], one["z"], u["dt_bias"], slots=slots,
+                                           **k))
+        held = list(u.values()) + [lengths, rows, slots, *dfinal]
+        return out, [(v.shape, v.dtype) for v in held]
+
+    want, _ = run(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(DEV)
+    got, shapes = run(s)  # every input is dropped here, its memory asked for again at once
+    junk = [torch.full(shape, 77, dtype=dtype, device=DEV) for shape, dtype in shapes * 3]
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+    del junk
+
+
 def test_graph_replay(scr):
     """Captured once, replayed on new contents of the same buffers."""
     t = inputs(2)
