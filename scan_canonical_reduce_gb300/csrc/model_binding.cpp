@@ -42,7 +42,6 @@ std::string join(const A&... a) {
 [[noreturn]] void bad_type(const std::string& s) { throw Error{PyExc_TypeError, s}; }
 
 PyObject* g_check = nullptr;      // model._check(code, name): raises CrError
-PyObject* g_workspace = nullptr;  // model._workspace(device index, stream, bytes): a tensor
 
 // ------------------------------------------------------------ libcr calls
 decltype(&cr_embedding) f_embedding;
@@ -179,30 +178,13 @@ struct On {
     if (other) t.record_stream(*other);
   }
 
-  // The binding's workspace of this stream (held here too, so that a call
-  // does not ask Python for it). Asking may let other threads in, so nothing
-  // of the list is kept across it, and the tensor is returned by value.
-  at::Tensor workspace(size_t bytes, const char* name, PyObject* stream) const {
-    struct Kept {
-      int index;
-      cudaStream_t stream;
-      at::Tensor t;
-    };
-    static std::vector<Kept>* kept = new std::vector<Kept>;  // not destroyed: outlives CUDA
+  // A call's workspace: its own, from the stream's allocator, which may have
+  // it back when the call has been enqueued. (Held from call to call it would
+  // be replaced by a larger call's while a captured graph still writes to it,
+  // or shared by two graphs of one stream that are replayed on two.)
+  at::Tensor workspace(size_t bytes, const char* name) const {
     if (bytes == 0) bad_value(join("invalid ", name, " arguments"));
-    auto find = [&]() -> Kept* {
-      for (Kept& q : *kept)
-        if (q.index == index && q.stream == ptr) return &q;
-      return nullptr;
-    };
-    if (const Kept* k = find(); k != nullptr && (size_t)k->t.numel() >= bytes) return k->t;
-    PyObject* r = PyObject_CallFunction(g_workspace, "iOn", index, stream, (Py_ssize_t)bytes);
-    if (r == nullptr) throw Error{nullptr, ""};
-    const at::Tensor t = tensor(r, "workspace");
-    Py_DECREF(r);
-    if (Kept* k = find()) k->t = t;
-    else kept->push_back({index, ptr, t});
-    return t;
+    return empty({(int64_t)bytes}, at::kByte);
   }
 };
 
@@ -316,7 +298,7 @@ PyObject* embedding_backward(PyObject* const* a) {
   if (n > 1 && grad.stride(0) < dim) grad = grad.contiguous();  // a zero stride
   const at::Tensor o = on.output(a[4], {vocab, dim}, at::kFloat);
   const at::Tensor ws = on.workspace(f_embedding_backward_workspace_bytes(n, vocab, dim),
-                                      "embedding_backward", a[6]);
+                                     "embedding_backward");
   check(f_embedding_backward(tok.p, tok.bytes, n, grad.data_ptr(), n > 1 ? grad.stride(0) : dim,
                              vocab, dim, scale, code, accumulate,
                              static_cast<float*>(o.data_ptr()), vocab > 1 ? o.stride(0) : dim,
@@ -401,7 +383,7 @@ PyObject* causal_conv_backward(PyObject* const* a) {
   if (c.state.defined()) ds = c.on.empty(c.state.sizes(), type);
   const at::Tensor ws = c.on.workspace(
       f_causal_conv_backward_workspace_bytes(c.args.batch, c.args.len, c.args.dim, (int32_t)K),
-      "causal_conv_backward", a[8]);
+      "causal_conv_backward");
   const cr_causal_conv_grads g = {dy.data_ptr(),
                                   dy.stride(0),
                                   dy.stride(1),
@@ -568,7 +550,7 @@ PyObject* selective_scan(PyObject* const* a) {
     kept = s.on.empty({batch, f_selective_scan_checkpoints(s.args.len), dim, N}, at::kFloat);
   const at::Tensor ws =
       s.on.workspace(f_selective_scan_workspace_bytes(batch, s.args.len, dim, (int32_t)N),
-                     "selective_scan", a[14]);
+                     "selective_scan");
   check(f_selective_scan(&s.args, y.data_ptr(), y.stride(0), y.stride(1),
                          return_state ? static_cast<float*>(final.data_ptr()) : nullptr,
                          return_checkpoints ? static_cast<float*>(kept.data_ptr()) : nullptr,
@@ -616,7 +598,7 @@ PyObject* selective_scan_backward(PyObject* const* a) {
   const at::Tensor ws = s.on.workspace(
       f_selective_scan_backward_workspace_bytes(batch, s.args.len, dim, (int32_t)N,
                                                 s.args.groups),
-      "selective_scan_backward", a[14]);
+      "selective_scan_backward");
   s.on.uses(kept);
   const cr_selective_scan_grads g = {dy.data_ptr(), dy.stride(0), dy.stride(1), dfinal.p,
                                      static_cast<const float*>(kept.data_ptr()),
@@ -679,10 +661,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-// bind(addresses by name, check, workspace)
+// bind(addresses by name, check)
 PyObject* bind(PyObject*, PyObject* args) {
-  PyObject *names = nullptr, *chk = nullptr, *ws = nullptr;
-  if (!PyArg_ParseTuple(args, "O!OO", &PyDict_Type, &names, &chk, &ws)) return nullptr;
+  PyObject *names = nullptr, *chk = nullptr;
+  if (!PyArg_ParseTuple(args, "O!O", &PyDict_Type, &names, &chk)) return nullptr;
   bool ok = true;
   auto get = [&](const char* name, auto& f) {
     PyObject* v = PyDict_GetItemString(names, name);
@@ -711,8 +693,6 @@ PyObject* bind(PyObject*, PyObject* args) {
   }
   Py_INCREF(chk);
   Py_XSETREF(g_check, chk);
-  Py_INCREF(ws);
-  Py_XSETREF(g_workspace, ws);
   Py_RETURN_NONE;
 }
 

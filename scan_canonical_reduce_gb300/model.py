@@ -10,7 +10,9 @@ are token-major, ``(batch, time, channel)``, of one type among float32,
 bfloat16 and float16; weights, scan states and sums are float32. Tensors
 whose last axis is not contiguous are copied first; any other strides are
 used as they are. ``stream`` is where the call runs (the current stream by
-default); copies and outputs are made on it.
+default); copies, outputs and the call's workspace are made on it, so that a
+call may be captured into a CUDA graph (whose outputs and workspaces are then
+the graph's own) without another one before it.
 
 Every result is one fixed expression of the inputs: repeated calls give the
 same bits.
@@ -24,7 +26,7 @@ import os
 
 import torch
 
-from . import _HERE, _I32, _I64, _P, _WS, SIGNATURES, _check, lib
+from . import _HERE, _I32, _I64, _P, SIGNATURES, _check, lib
 
 BINDING_PATH = os.path.join(_HERE, "_build", "cr_model_binding.so")
 
@@ -65,11 +67,6 @@ class _ScanGrads(ctypes.Structure):
                 ("dA", _P), ("dD", _P), ("ddt_bias", _P), ("dstate", _P)]
 
 
-def _workspace(index: int, stream, nbytes: int) -> torch.Tensor:
-    where = torch.device("cuda", index)
-    return _WS.get(where, torch.cuda.current_stream(where) if stream is None else stream, nbytes)
-
-
 def _load():
     """The native module, given the functions of the libcr that is loaded."""
     if not os.path.exists(BINDING_PATH):
@@ -82,8 +79,7 @@ def _load():
     loader.exec_module(module)
     names = [n for n in SIGNATURES if n.startswith(("cr_embedding", "cr_causal_conv",
                                                    "cr_selective_scan"))]
-    module.bind({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names}, _check,
-                _workspace)
+    module.bind({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names}, _check)
     return module
 
 

@@ -161,6 +161,68 @@ def test_graph_replay(scr):
         assert same(got, calls(scr, new)), seed
 
 
+# calls whose scratch memory a captured graph has to keep
+def scratch_calls(scr, t):
+    main = (t["x"], t["dt"], t["A"], t["B"], t["C"])
+    y, kept = scr.selective_scan(*main, return_checkpoints=True)
+    out = {"y": y, "dW": scr.embedding_backward(t["tokens"], t["dy"], 500)}
+    out.update({"conv_" + k: v for k, v in scr.causal_conv_backward(
+        t["dy"], t["x"], t["weight"], t["bias"], "silu").items()})
+    out.update(scr.selective_scan_backward(t["dy"], *main, checkpoints=kept))
+    return out
+
+
+def captured(scr, t, s):
+    s.wait_stream(torch.cuda.current_stream(DEV))
+    with torch.cuda.stream(s):
+        scratch_calls(scr, t)
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = scratch_calls(scr, t)
+    return graph, got
+
+
+def test_graph_replay_after_larger_calls(scr):
+    """A graph's scratch memory is not given to tensors that are made after a
+    larger call on its stream, nor do they lose what they hold to a replay."""
+    t = inputs(22, T=400)  # a scan of seven segments
+    want = scratch_calls(scr, t)
+    s = torch.cuda.Stream(DEV)
+    graph, got = captured(scr, t, s)
+    with torch.cuda.stream(s):
+        scratch_calls(scr, inputs(23, batch=8, T=900, D=520, V=5000))
+        s.synchronize()
+        held = [torch.full((1 << k,), 7, dtype=torch.uint8, device=DEV)
+                for k in (12, 16, 18, 20, 22, 24) for _ in range(8)]
+    torch.cuda.synchronize()
+    for v in got.values():
+        v.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert same(got, want)
+    assert all(bool((h == 7).all()) for h in held)
+
+
+def test_graphs_of_one_stream_replayed_on_two(scr):
+    t = [inputs(24, T=400), inputs(25, T=420)]
+    want = [scratch_calls(scr, x) for x in t]
+    s = torch.cuda.Stream(DEV)
+    graphs = [captured(scr, x, s) for x in t]
+    streams = [torch.cuda.Stream(DEV) for _ in t]
+    for _ in range(20):
+        for _, got in graphs:
+            for v in got.values():
+                v.zero_()
+        torch.cuda.synchronize()
+        for (graph, _), on in zip(graphs, streams):
+            with torch.cuda.stream(on):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(got, w) for (_, got), w in zip(graphs, want))
+
+
 def test_threads_on_their_own_streams(scr):
     want = {seed: calls(scr, inputs(seed)) for seed in range(10, 14)}
     torch.cuda.synchronize()
