@@ -153,12 +153,24 @@ def _resolve(device) -> torch.device:
     return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
+def _capturing(stream) -> bool:
+    """Whether a call's stream (None: the current one) is being captured into a
+    CUDA graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Workspace:
     """One growing device workspace per (device, stream); calls on one stream
-    are ordered, so they may share it."""
+    are ordered, so they may share it. A buffer that a captured graph uses is
+    kept when a larger one takes its place."""
 
     def __init__(self):
         self._bufs = {}
+        self._captured = set()  # keys whose present buffer a graph may hold
+        self._outgrown = []
         self._lock = threading.Lock()
 
     def get(self, device: torch.device, stream, nbytes: int) -> torch.Tensor:
@@ -168,10 +180,15 @@ class _Workspace:
         with self._lock:
             buf = self._bufs.get(key)
             if buf is None or buf.numel() < nbytes:
+                if key in self._captured:
+                    self._outgrown.append(buf)
+                    self._captured.discard(key)
                 with torch.cuda.stream(s):  # allocated on the stream that uses it
                     buf = torch.empty(max(nbytes, 4096), dtype=torch.uint8, device=device)
                     buf[:256].zero_()  # no status, for calls that leave the word alone
                 self._bufs[key] = buf
+            if key not in self._captured and _capturing(stream):
+                self._captured.add(key)
             return buf
 
 
@@ -183,7 +200,8 @@ def workspace(device, stream=None, nbytes: int = 4096) -> torch.Tensor:
     a uint8 device tensor that grows on demand and is reused by every call
     on that stream (calls on one stream run in order). A capture into a CUDA
     graph should make one call first, so that no allocation happens inside
-    the capture."""
+    the capture. Graphs captured on one stream share its workspace: replays of
+    them, and calls on that stream, must not overlap in time."""
     return _WS.get(torch.device(device), stream, nbytes)
 
 

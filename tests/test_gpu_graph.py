@@ -54,3 +54,35 @@ def test_graph_replay(scr, kind, policy, B):
         got = out.cpu().numpy().copy()
         want = run(scr, kind, policy, B, x, torch.empty_like(out), None).cpu().numpy()
         assert got.tobytes() == want.tobytes(), (kind, policy, B, seed)
+
+
+@pytest.mark.parametrize("kind,policy,B", CALLS)
+def test_graph_replay_after_a_larger_call(scr, kind, policy, B):
+    """The workspace that a graph was captured with stays the graph's when a
+    larger call on its stream gets a larger one."""
+    n = 16 * 3000 + 5
+    x = torch.from_numpy(W.family3(n)).to(DEV)
+    out = torch.empty(1 if kind.startswith("reduce") else n, dtype=torch.float64, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(scr, kind, policy, B, x, out, s)
+    s.synchronize()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        run(scr, kind, policy, B, x, out, s)
+    before = scr.workspace(DEV, s)
+    address, size = before.data_ptr(), before.numel()
+    del before
+    with torch.cuda.stream(s):
+        after = scr.workspace(DEV, s, size + (1 << 16))
+        assert after.numel() > size and after.data_ptr() != address
+        held = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert all(h.data_ptr() != address for h in held)
+    out.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert out.cpu().numpy().tobytes() == want.cpu().numpy().tobytes(), (kind, policy, B)
+    assert all(bool((h == 7).all()) for h in held)
