@@ -17,11 +17,15 @@ namespace {
 // Sequences with few channels are cut into segments that run side by side:
 // a first launch (kStates) takes every segment but the last from a zero state
 // to its end and its sum of delta, the second starts a segment from the
-// state that these give, H' = exp(A sum delta) H + E in segment order.
+// state that these give, H' = exp(A sum delta) H + E in segment order. Every
+// segment of the second launch reads the initial state, while the last one may
+// be done: where the final state goes to the same place, the first launch
+// leaves a copy for them.
 struct Segments {
   int64_t count, len;
-  float* E;     // [count - 1][batch][dim][NP]
-  float* sum;   // [count - 1][batch][dim]
+  float* E;        // [count - 1][batch][dim][NP]
+  float* initial;  // [batch][dim][NP], or NULL: the call's own
+  float* sum;      // [count - 1][batch][dim]
 };
 
 template <class T>
@@ -77,7 +81,10 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
     for (int k = 0; k < kS; ++k) A[k] = pack2(a[k] * kLog2e, a[k] * kLog2e);
   }
   if (!kStates) {
-    if (in.state != nullptr) load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
+    if (sg.initial != nullptr)
+      read_states(sg.initial + (b * in.dim + d) * TL::NP, n0, TL::NP, true, h);
+    else if (in.state != nullptr)
+      load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
     const float* E = sg.E + (b * in.dim + d) * TL::NP + n0;
     const float* sum = sg.sum + b * in.dim + d;
 #pragma unroll 4
@@ -264,6 +271,10 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
       float lo, hi;
       unpack2(total, lo, hi);
       if (g == 0) sg.sum[row] = lo + hi;
+      if (seg == 0 && sg.initial != nullptr) {
+        load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
+        store_states(sg.initial + (b * in.dim + d) * TL::NP, n0, TL::NP, true, h);
+      }
     }
   } else {
   for (int64_t t = t0; t < end; ++t)  // past the sequence's length
@@ -293,7 +304,7 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
 Segments scan_segments(int64_t batch, int64_t len, int64_t dim, int lanes) {
   constexpr int64_t kTile = 32;
   Segments sg;
-  sg.E = sg.sum = nullptr;
+  sg.E = sg.initial = sg.sum = nullptr;
   sg.count = 1;
   const int64_t warps = batch * ceil_div(dim * lanes, 32);
   if (warps < CR_SCAN_SPLIT_BELOW && warps > 0 && len >= 2 * kTile) {
@@ -428,9 +439,10 @@ size_t cr_selective_scan_workspace_bytes(int64_t batch, int64_t len, int64_t dim
                                          int32_t dstate) {
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || dstate < 1) return 0;
-  const int64_t segs = scan_segments(batch, len, dim, scan_lanes(dstate)).count;
-  return round256((size_t)(segs - 1) * batch * dim * (scan_lanes(dstate) * kS + 1) * 4) +
-         kStatusBytes;
+  const int lanes = scan_lanes(dstate);
+  const int64_t segs = scan_segments(batch, len, dim, lanes).count;
+  if (segs == 1) return kStatusBytes;
+  return round256((size_t)batch * dim * (segs * lanes * kS + segs - 1) * 4) + kStatusBytes;
 }
 
 cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_batch_stride,
@@ -456,8 +468,12 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
   const int64_t blocks = scan_blocks(a->batch, a->dim, a->groups, lanes);
   Segments sg = scan_segments(a->batch, a->len, a->dim, lanes);
   if (blocks > kMaxBlocks / sg.count) return CR_ERR_UNSUPPORTED;
-  sg.E = reinterpret_cast<float*>(past_status(ws));
-  sg.sum = sg.E + (sg.count - 1) * a->batch * a->dim * lanes * kS;
+  if (sg.count > 1) {
+    const int64_t states = a->batch * a->dim * lanes * kS;
+    sg.E = reinterpret_cast<float*>(past_status(ws));
+    if (a->state != nullptr && final_state == a->state) sg.initial = sg.E + (sg.count - 1) * states;
+    sg.sum = sg.E + sg.count * states;
+  }
   CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
     using TL = Tile<T, G>;
     const size_t bytes = TL::VE * es;  // of an access

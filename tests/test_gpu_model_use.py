@@ -385,6 +385,38 @@ def test_buffers_of_exact_size(scr, D):
     assert all(b.intact() for b in bands)
 
 
+@pytest.mark.parametrize("batch,T,D,N", [(1, 2500, 8, 16), (5, 301, 40, 13), (3, 64, 16, 4),
+                                         (2, 40, 36, 16), (1, 900, 6, 128)])
+def test_state_in_place(scr, batch, T, D, N):
+    """The C call may write the final state over the initial one: whole, and cut
+    into segments, with a last segment that has nothing to do."""
+    from scan_canonical_reduce_gb300 import model as m
+    L = scr.lib()
+    t = inputs(26, batch=batch, T=T, D=D, N=N)
+    lengths = torch.tensor([T, 7, 0, T // 2, T - 1][:batch], device=DEV)
+    main = (t["x"], t["dt"], t["A"], t["B"], t["C"])
+    extra = dict(D=t["D"], z=t["z"], dt_bias=t["dt_bias"], lengths=lengths)
+    stream = torch.cuda.current_stream(DEV).cuda_stream
+    size = L.cr_selective_scan_workspace_bytes(batch, T, D, N)
+    for _ in range(5):
+        y, final, kept = scr.selective_scan(*main, state=t["scan"], return_state=True,
+                                            return_checkpoints=True, **extra)
+        state, y2, kept2 = t["scan"].clone(), torch.empty_like(y), torch.empty_like(kept)
+        kept2.copy_(kept)  # those past a length are not written and may hold anything
+        ws = Guarded(nbytes=size)
+        args = m._ScanArgs(batch, T, D, N, 1, 1, 3, 8, 0, *(
+            v for k in ("x", "dt", "z") for v in (t[k].data_ptr(), T * D, D)), *(
+            v for k in ("B", "C") for v in (t[k].data_ptr(), T * N, N)), t["A"].data_ptr(),
+            t["D"].data_ptr(), t["dt_bias"].data_ptr(), state.data_ptr(), lengths.data_ptr())
+        assert L.cr_selective_scan(ctypes.byref(args), y2.data_ptr(), T * D, D, state.data_ptr(),
+                                   kept2.data_ptr(), ws.ptr, size, stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(final, state)
+        assert torch.equal(kept.view(torch.int32), kept2.view(torch.int32))
+        assert ws.intact()
+        t["scan"] = torch.randn_like(t["scan"])
+
+
 def test_offsets_past_32_bits(scr):
     """Rows that begin more than 2^31 elements into their tensors."""
     gap = (1 << 31) + 4096
