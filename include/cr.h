@@ -319,7 +319,8 @@ cr_status cr_reduce_noalloc(const void* x, int64_t n, int32_t L, const void* ini
  *   - Every result is one fixed expression of the inputs: sums are ordered,
  *     no value is summed by atomics, and repeated calls give the same bits.
  *   - Outputs must not overlap inputs or each other, except where a call says
- *     so. An output pointer equal to a pointer the call reads is INVALID_ARG.
+ *     so. An output pointer equal to a pointer the call reads is INVALID_ARG;
+ *     other overlaps are not looked for.
  *   - Conventions on streams, ownership, workspaces and errors as above. None
  *     of these calls waits on the device or has a status word; the first 256
  *     bytes of a workspace, where other calls have theirs, are left alone. */

@@ -558,10 +558,12 @@ cr_status cr_causal_conv(const cr_causal_conv_args* a, void* y, int64_t y_batch_
   const size_t es = model_esize(a->dt);
   if (y_batch_stride < 0 || y_time_stride < 0) return CR_ERR_INVALID_ARG;
   if (a->batch == 0 || a->dim == 0) return CR_OK;
-  if (a->len > 0 && (y == nullptr || y == a->x || (a->len > 1 && y_time_stride < a->dim) ||
+  if (a->len > 0 && (y == nullptr || (a->len > 1 && y_time_stride < a->dim) ||
                      (a->batch > 1 && y_batch_stride < a->dim)))
     return CR_ERR_INVALID_ARG;
-  if (!ptr_aligned(y, es) || !ptr_aligned(final_state, es)) return CR_ERR_INVALID_ARG;
+  if (!ptr_aligned(y, es) || !ptr_aligned(final_state, es) ||
+      overwrites({y, final_state}, {a->x, a->weight, a->bias, a->state, a->lengths}))
+    return CR_ERR_INVALID_ARG;
   if (a->len == 0 && final_state == nullptr) return CR_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const ConvShape sh = conv_shape(a->batch, a->len, a->dim);
@@ -600,14 +602,15 @@ cr_status cr_causal_conv_backward(const cr_causal_conv_args* a, const cr_causal_
   if (a->dim == 0) return CR_OK;
   if (g->dweight == nullptr) return CR_ERR_INVALID_ARG;
   if (a->batch > 0 && a->len > 0) {
-    if (g->dy == nullptr || (g->dx != nullptr && (g->dx == g->dy || g->dx == a->x)))
-      return CR_ERR_INVALID_ARG;
+    if (g->dy == nullptr) return CR_ERR_INVALID_ARG;
     if (g->dx != nullptr && ((a->len > 1 && g->dx_time_stride < a->dim) ||
                              (a->batch > 1 && g->dx_batch_stride < a->dim)))
       return CR_ERR_INVALID_ARG;
   }
   if (!ptr_aligned(g->dy, es) || !ptr_aligned(g->dx, es) || !ptr_aligned(g->dfinal, es) ||
-      !ptr_aligned(g->dstate, es) || !ptr_aligned(g->dweight, 4) || !ptr_aligned(g->dbias, 4))
+      !ptr_aligned(g->dstate, es) || !ptr_aligned(g->dweight, 4) || !ptr_aligned(g->dbias, 4) ||
+      overwrites({g->dx, g->dweight, g->dbias, g->dstate},
+                 {a->x, a->weight, a->bias, a->state, a->lengths, g->dy, g->dfinal}))
     return CR_ERR_INVALID_ARG;
   const size_t need = cr_causal_conv_backward_workspace_bytes(a->batch, a->len, a->dim, a->width);
   if (ws == nullptr || !ptr_aligned(ws, 256) || ws_bytes < need) return CR_ERR_WORKSPACE;
@@ -664,7 +667,9 @@ cr_status cr_causal_conv_step(const void* x, int64_t x_stride, void* state, int6
                        : state_rows < batch)
     return CR_ERR_INVALID_ARG;
   if (batch == 0 || dim == 0) return CR_OK;
-  if (x == nullptr || weight == nullptr || y == nullptr || y == x || y == state || x == state ||
+  if (x == nullptr || weight == nullptr || y == nullptr ||
+      overwrites({y}, {x, state, slots, weight, bias}) ||
+      overwrites({state}, {x, slots, weight, bias}) ||
       (state == nullptr && state_rows > 0) || (batch > 1 && y_stride < dim) || y_stride < 0)
     return CR_ERR_INVALID_ARG;
   if (!ptr_aligned(x, es) || !ptr_aligned(state, es) || !ptr_aligned(y, es) ||

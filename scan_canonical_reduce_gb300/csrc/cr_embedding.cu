@@ -731,7 +731,8 @@ cr_status cr_embedding(const void* tokens, int32_t index_bytes, int64_t n, const
     return CR_ERR_INVALID_ARG;
   if (row_stride < dim || out_stride < dim) return CR_ERR_INVALID_ARG;
   if (n == 0 || dim == 0) return CR_OK;
-  if (tokens == nullptr || out == nullptr || (vocab > 0 && table == nullptr) || out == table)
+  if (tokens == nullptr || out == nullptr || (vocab > 0 && table == nullptr) ||
+      overwrites({out}, {tokens, table}))
     return CR_ERR_INVALID_ARG;
   if (!ptr_aligned(tokens, index_bytes) || !ptr_aligned(table, es) || !ptr_aligned(out, es))
     return CR_ERR_INVALID_ARG;
@@ -774,7 +775,8 @@ cr_status cr_embedding_backward(const void* tokens, int32_t index_bytes, int64_t
   if (es == 0 || need == 0 || !index_width_ok(index_bytes)) return CR_ERR_INVALID_ARG;
   if (grad_stride < dim || dw_stride < dim) return CR_ERR_INVALID_ARG;
   if (n > 0 && dim > 0 && (tokens == nullptr || grad == nullptr)) return CR_ERR_INVALID_ARG;
-  if (vocab > 0 && dim > 0 && (dw == nullptr || dw == grad)) return CR_ERR_INVALID_ARG;
+  if (vocab > 0 && dim > 0 && (dw == nullptr || overwrites({dw}, {tokens, grad})))
+    return CR_ERR_INVALID_ARG;
   if ((tokens && !ptr_aligned(tokens, index_bytes)) || (grad && !ptr_aligned(grad, es)) ||
       (dw && !ptr_aligned(dw, 4)))
     return CR_ERR_INVALID_ARG;

@@ -7,6 +7,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -289,6 +290,15 @@ inline bool ptr_aligned(const void* p, size_t a) {
 // Whether rows of a (batch, time) strided tensor all start on `bytes`.
 inline bool rows_aligned(const void* p, int64_t bs, int64_t ts, size_t es, size_t bytes) {
   return ptr_aligned(p, bytes) && ((size_t)bs * es) % bytes == 0 && ((size_t)ts * es) % bytes == 0;
+}
+
+// Whether an output pointer is one that the call reads (NULL: none).
+inline bool overwrites(std::initializer_list<const void*> outs,
+                       std::initializer_list<const void*> ins) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o != nullptr && o == i) return true;
+  return false;
 }
 
 inline bool index_width_ok(int bytes) { return bytes == 4 || bytes == 8; }

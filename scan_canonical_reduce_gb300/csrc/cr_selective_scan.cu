@@ -456,8 +456,13 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
   if (!ptr_aligned(y, es) || !ptr_aligned(final_state, 4) || !ptr_aligned(checkpoints, 4))
     return CR_ERR_INVALID_ARG;
   if (a->batch > 0 && a->dim > 0 && a->len > 0 &&
-      (y == nullptr || y == a->u || y == a->dt || y == a->z ||
-       (a->len > 1 && y_time_stride < a->dim) || (a->batch > 1 && y_batch_stride < a->dim)))
+      (y == nullptr || (a->len > 1 && y_time_stride < a->dim) ||
+       (a->batch > 1 && y_batch_stride < a->dim)))
+    return CR_ERR_INVALID_ARG;
+  const std::initializer_list<const void*> ins = {a->u, a->dt, a->z,       a->B,       a->C,
+                                                  a->A, a->D,  a->dt_bias, a->lengths};
+  if (a->batch > 0 && a->dim > 0 &&
+      (overwrites({y, final_state, checkpoints}, ins) || overwrites({y, checkpoints}, {a->state})))
     return CR_ERR_INVALID_ARG;
   const size_t need =
       cr_selective_scan_workspace_bytes(a->batch, a->len, a->dim, a->dstate);
@@ -519,8 +524,10 @@ cr_status cr_selective_scan_step(const cr_selective_scan_args* a, float* state,
                        : state_rows < a->batch)
     return CR_ERR_INVALID_ARG;
   if (a->batch == 0 || a->dim == 0) return CR_OK;
-  if (y == nullptr || y == a->u || y == a->dt || y == a->z ||
-      (state == nullptr && state_rows > 0) || (a->batch > 1 && y_batch_stride < a->dim))
+  const std::initializer_list<const void*> ins = {a->u, a->dt, a->z,       a->B, a->C,
+                                                  a->A, a->D,  a->dt_bias, slots};
+  if (y == nullptr || (state == nullptr && state_rows > 0) ||
+      (a->batch > 1 && y_batch_stride < a->dim) || overwrites({y, state}, ins) || y == state)
     return CR_ERR_INVALID_ARG;
   if (!ptr_aligned(y, es) || !ptr_aligned(state, 4)) return CR_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -541,13 +541,14 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
       (g->dy == nullptr || g->checkpoints == nullptr || g->du == nullptr || g->ddt == nullptr ||
        g->dB == nullptr || g->dC == nullptr || (a->z != nullptr && g->dz == nullptr)))
     return CR_ERR_INVALID_ARG;
-  const void* ins[6] = {a->u, a->dt, a->z, a->B, a->C, g->dy};
-  const void* outs[5] = {g->du, g->ddt, g->dz, g->dB, g->dC};
-  for (const void* o : outs) {
+  const std::initializer_list<const void*> of_type = {g->du, g->ddt, g->dz, g->dB, g->dC};
+  for (const void* o : of_type)
     if (!ptr_aligned(o, es)) return CR_ERR_INVALID_ARG;
-    for (const void* i : ins)
-      if (o != nullptr && o == i) return CR_ERR_INVALID_ARG;
-  }
+  const std::initializer_list<const void*> ins = {
+      a->u, a->dt,      a->z,     a->B,       a->C,  a->A,      a->D,
+      a->dt_bias, a->state, a->lengths, g->dy, g->dfinal, g->checkpoints};
+  if (overwrites(of_type, ins) || overwrites({g->dA, g->dD, g->ddt_bias, g->dstate}, ins))
+    return CR_ERR_INVALID_ARG;
   if (!ptr_aligned(g->dy, es) || !ptr_aligned(g->dfinal, 4) || !ptr_aligned(g->checkpoints, 4) ||
       !ptr_aligned(g->dA, 4) || !ptr_aligned(g->dD, 4) || !ptr_aligned(g->ddt_bias, 4) ||
       !ptr_aligned(g->dstate, 4))

@@ -284,3 +284,45 @@ def test_reference_gradients(m):
     for k, n in (("x", "x"), ("w", "weight"), ("bias", "bias"), ("state", "state")):
         want, v = numeric(conv_loss, a, k, rng)
         assert abs((g[n][0] * v).sum() - want) < 1e-6, k
+
+
+def scan_back_dstate(m, dstate_out, **k):
+    """scan_back with the gradient of the state, whose name the argument block
+    gives to the number of states."""
+    g = {n: at(12 + i) for i, (n, t) in enumerate(m._ScanGrads._fields_)}
+    g.update(dy_batch_stride=80, dy_time_stride=16)
+    g.update({n: v for n, v in k.items() if n in g}, dstate=dstate_out)
+    c = m._ScanGrads(*(g[n] for n, _ in m._ScanGrads._fields_))
+    return m.lib().cr_selective_scan_backward(ctypes.byref(scan_args(m, **k)), ctypes.byref(c),
+                                              at(30), 1 << 26, None)
+
+
+SCAN_BACK_READ = dict(u=at(0), dt=at(1), z=at(2), B=at(3), C=at(4), A=at(5), D=at(6),
+                      dt_bias=at(7), state=at(8), lengths=at(9), dy=at(40), dfinal=at(41),
+                      checkpoints=at(42))
+# what a call reads, by its name in the calls above, and what it writes
+READ_AND_WRITTEN = [
+    (embed, dict(tokens=at(0), table=at(1)), ("out",)),
+    (embed_grad, dict(tokens=at(0), grad=at(1)), ("dw",)),
+    (conv, dict(x=at(0), weight=at(1), bias=at(2), state=at(3), lengths=at(4)), ("y", "final")),
+    (conv_back, dict(x=at(0), weight=at(1), bias=at(2), state=at(3), lengths=at(4), dy=at(5),
+                     dfinal=at(40)), ("dx", "dweight", "dbias", "dstate")),
+    (conv_step, dict(x=at(0), state=at(1), slots=at(41), weight=at(2), bias=at(42)), ("y",)),
+    (conv_step, dict(x=at(0), slots=at(41), weight=at(2), bias=at(42)), ("state",)),
+    (scan, dict(u=at(0), dt=at(1), z=at(2), B=at(3), C=at(4), A=at(5), D=at(6), dt_bias=at(7),
+                lengths=at(9)), ("y", "final", "kept")),
+    (scan, dict(state=at(8)), ("y", "kept")),  # the final state may take its place
+    (scan_back, SCAN_BACK_READ, ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias")),
+    (scan_back_dstate, SCAN_BACK_READ, ("dstate_out",)),
+    (scan_step, dict(u=at(0), dt=at(1), z=at(2), B=at(3), C=at(4), A=at(5), D=at(6),
+                     dt_bias=at(7), slots=at(9), state=at(8)), ("y",)),
+    (scan_step, dict(u=at(0), dt=at(1), z=at(2), B=at(3), C=at(4), A=at(5), D=at(6),
+                     dt_bias=at(7), slots=at(9)), ("state",)),
+]
+
+
+@pytest.mark.parametrize("call,read,written", READ_AND_WRITTEN)
+def test_outputs_that_are_inputs_are_refused(m, call, read, written):
+    for name in written:
+        for other, pointer in read.items():
+            assert call(m, **{**read, name: pointer}) == INVALID, (name, other)
