@@ -93,9 +93,15 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
       const float x = sum[s * in.batch * in.dim], e[kS] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
       for (int k = 0; k < kS; ++k) {
+        // a segment's growth or decay may leave the range that the states
+        // stay in: then half of its exponent at a time (and so far that even
+        // that leaves it, only a zero state stays finite)
         float a, a2;
         unpack2(A[k], a, a2);
-        h[k] = fmaf(exp2_fast(x * a), h[k], e[k]);
+        const float v = x * a;
+        const bool far = fabsf(v) > 126.0f;
+        const float f = exp2_fast(far ? fminf(0.5f * v, 127.0f) : v);
+        h[k] = fmaf(f, far ? f * h[k] : h[k], e[k]);
       }
     }
   }

@@ -263,6 +263,35 @@ def test_long_sequence(scr):
     check_grads(scr.selective_scan_backward(dy.to(DEV), **dev(s)), ref["grads"], 1, 2500, 8, 16, 1)
 
 
+@pytest.mark.parametrize("rate,state,first", [(1.2, 0.0, 4950), (-1.2, 1e30, 0), (1.0, 1e-30, 0)])
+def test_segments_that_grow_or_decay_far(scr, rate, state, first):
+    """A segment's whole growth or decay may lie outside binary32's range where
+    the states themselves do not: 5000 steps in segments of 96, with inputs from
+    step `first` on (none: the state alone, as far as it stays normal)."""
+    T, D = 5000, 8
+    f32 = dict(dtype=torch.float32, device=DEV)
+    u = torch.zeros(1, T, D, **f32)
+    if first:
+        u[:, first:] = 1.0
+    one = torch.ones(1, T, 1, **f32)
+    y, final = scr.selective_scan(u, torch.ones(1, T, D, **f32), torch.full((D, 1), rate, **f32),
+                                  one, one, softplus=False, return_state=True,
+                                  state=torch.full((1, D, 1), state, **f32))
+    a, h, want = float(np.exp(np.float64(np.float32(rate)))), float(np.float32(state)), []
+    for t in range(T):
+        h = a * h + float(u[0, t, 0])
+        want.append(h)
+    want = np.array(want)
+    n = T if first else int(np.argmax((np.abs(want) < 2.0 ** -120) | (np.abs(want) > 2.0 ** 120)))
+    assert n > 120
+    got = R.f64(y)[0, :n]
+    # a step's decay: 1.4e-7 of the instruction, 2^-23 |log2 a| of its argument;
+    # one rounding of the product and one of the sum; a factor 2 of room
+    step = 2 * (1.4e-7 + 2.0 ** -23 * (abs(rate) * 1.4427 + 1))
+    off = np.abs(got - want[:n, None])
+    assert (off <= step * np.arange(1, n + 1)[:, None] * np.abs(want[:n, None])).all()
+
+
 def test_repeated_calls_give_the_same_bits(scr):
     s, dy, _ = make(2, 300, 260, 16, 1, torch.bfloat16, 15)
     d = dev(s)
