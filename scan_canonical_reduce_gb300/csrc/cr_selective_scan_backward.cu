@@ -535,7 +535,17 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
   if (ok != CR_OK) return ok;
   const size_t es = model_esize(a->dt_type);
   if (g == nullptr || g->dy_batch_stride < 0 || g->dy_time_stride < 0) return CR_ERR_INVALID_ARG;
-  if (a->dim == 0) return CR_OK;
+  if (a->dim == 0) {  // B and C are there all the same, and reach nothing
+    const size_t bytes = (size_t)a->batch * a->len * a->groups * a->dstate * es;
+    for (void* o : {g->dB, g->dC}) {
+      if (bytes > 0 && (o == nullptr || !ptr_aligned(o, es) || overwrites({o}, {a->B, a->C})))
+        return CR_ERR_INVALID_ARG;
+      if (bytes > 0 &&
+          cudaMemsetAsync(o, 0, bytes, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return CR_ERR_CUDA;
+    }
+    return CR_OK;
+  }
   if (g->dA == nullptr) return CR_ERR_INVALID_ARG;
   if (a->batch > 0 && a->len > 0 &&
       (g->dy == nullptr || g->checkpoints == nullptr || g->du == nullptr || g->ddt == nullptr ||

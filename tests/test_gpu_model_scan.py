@@ -292,6 +292,33 @@ def test_segments_that_grow_or_decay_far(scr, rate, state, first):
     assert (off <= step * np.arange(1, n + 1)[:, None] * np.abs(want[:n, None])).all()
 
 
+def test_no_channels(scr):
+    """Without channels the gradients of B and C, which then reach nothing, are
+    zero, whatever their memory held."""
+    import ctypes
+
+    from scan_canonical_reduce_gb300 import model as m
+    s, dy, dfinal = make(2, 37, 0, 16, 2, torch.bfloat16, 18)
+    y, final = scr.selective_scan(**dev(s), return_state=True)
+    assert y.shape == (2, 37, 0) and final.shape == (2, 0, 16)
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    assert g["B"].shape == g["C"].shape == (2, 37, 2, 16)
+    assert all(not v.any() for v in g.values())
+    B, C = s["B"].to(DEV), s["C"].to(DEV)
+    dB, dC = torch.full_like(B, 3.0), torch.full_like(C, 3.0)
+    sizes = dict(batch=2, len=37, dim=0, dstate=16, groups=2, softplus=1, dt_type=3,
+                 B=B.data_ptr(), B_batch_stride=37 * 32, B_time_stride=32, C=C.data_ptr(),
+                 C_batch_stride=37 * 32, C_time_stride=32)
+    args = m._ScanArgs(**sizes)
+    grads = m._ScanGrads(dB=dB.data_ptr(), dC=dC.data_ptr())
+    n = scr.lib().cr_selective_scan_backward_workspace_bytes(2, 37, 0, 16, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.current_stream(DEV).cuda_stream
+    assert scr.lib().cr_selective_scan_backward(ctypes.byref(args), ctypes.byref(grads),
+                                                ws.data_ptr(), n, stream) == 0
+    assert not dB.any() and not dC.any()
+
+
 def test_repeated_calls_give_the_same_bits(scr):
     s, dy, _ = make(2, 300, 260, 16, 1, torch.bfloat16, 15)
     d = dev(s)
