@@ -326,6 +326,9 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
       dp[k] = {{0, 0}};
     }
     const int own = (int)(t1 - t0);  // steps of this run
+    // Steps past the sequence add nothing, even where dy's zeros would meet a
+    // NaN or an infinity in the window.
+    const int live = min(own, rows);
     T* o = dx + (t0 - (K - 1)) * g.dxts;  // of position t - (K - 1)
     // After step t the window of dpre ends at t, which completes dx at t -
     // (K - 1). Full: steps and positions all lie inside the run and the
@@ -354,8 +357,9 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) d[u].p[j] = mul2(d[u].p[j], a.p[j]);
         }
-        dp[K - 1 + u] = d[u];  // zero past the sequence, as dy is
-        if (kFull || s + u < own) {
+        if (!kFull && s + u >= rows) d[u] = {{0, 0}};
+        dp[K - 1 + u] = d[u];
+        if (kFull || s + u < live) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             db.p[j] = add2(db.p[j], d[u].p[j]);

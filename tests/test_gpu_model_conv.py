@@ -202,3 +202,26 @@ def test_repeated_calls_give_the_same_bits(scr):
     for _ in range(3):
         again = scr.causal_conv_backward(dy.to(DEV), **dev(s), activation="silu")
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_what_no_position_uses(scr, act, K):
+    """The state of an empty sequence may hold anything (a slot that no stream
+    has): it reaches no gradient. And a position that holds NaN or infinity
+    reaches none past its sequence's length."""
+    s, dy, dfinal = make(4, 40, 36, K, torch.float32, 11, lengths=[40, 0, 7, 0])
+    kinds = dict(activation=act, dfinal=dfinal.to(DEV))
+    want = scr.causal_conv_backward(dy.to(DEV), **dev(s), **kinds)
+    s["state"][1] = NAN
+    s["state"][3, :, ::2], s["state"][3, :, 1::2] = float("inf"), float("-inf")
+    g = scr.causal_conv_backward(dy.to(DEV), **dev(s), **kinds)
+    for k in g:
+        assert torch.equal(g[k], want[k]), k
+    y, final = scr.causal_conv(**dev(s), activation=act, return_state=True)
+    assert not y[1].any() and not y[3].any() and final[1].isnan().all()
+    for bad in (NAN, float("inf"), float("-inf")):
+        s["x"][2, 6] = bad
+        g = scr.causal_conv_backward(dy.to(DEV), **dev(s), **kinds)
+        assert not g["x"][2, 7:].any()
+        assert torch.equal(g["x"][0], want["x"][0])
