@@ -310,39 +310,48 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
         (g & 1 ? ql : gl)[(g >> 1 & 1) * TL::YS] = w[0];
       }
     };
+    // past the sequence's end the state that q is a multiple of may have
+    // overflowed, with nothing to multiply
+    auto adjoint = [&](auto partial) {
+      constexpr bool kPartial = decltype(partial)::value;
 #pragma unroll
-    for (int tp = TP - 1; tp >= 0; --tp) {
-      const int t = tp * 2;
-      const float4 e = dl[tp * TL::CH];
-      const float2 p2 = pl[tp * TL::CH];
-      const F2 delta = pack2(e.x, e.y), du = pack2(e.z, e.w), p = pack2(p2.x, p2.y);
-      const F2 delta2 = pack2(e.x * kLog2e, e.y * kLog2e);
-      const float4 B[2] = {Bl[tp * 2 * G + q0], Bl[tp * 2 * G + q1]};
-      const float4 C[2] = {Cl[tp * 2 * G + q0], Cl[tp * 2 * G + q1]};
-      F2 v[8], gB = 0, qA = 0;
+      for (int tp = TP - 1; tp >= 0; --tp) {
+        const int t = tp * 2;
+        const float4 e = dl[tp * TL::CH];
+        const float2 p2 = pl[tp * TL::CH];
+        const F2 delta = pack2(e.x, e.y), du = pack2(e.z, e.w), p = pack2(p2.x, p2.y);
+        const F2 delta2 = pack2(e.x * kLog2e, e.y * kLog2e);
+        const float4 B[2] = {Bl[tp * 2 * G + q0], Bl[tp * 2 * G + q1]};
+        const float4 C[2] = {Cl[tp * 2 * G + q0], Cl[tp * 2 * G + q1]};
+        F2 v[8], gB = 0, qA = 0;
 #pragma unroll
-      for (int k = 0; k < kS; ++k) {
-        const F2 Bk = k % 2 ? pack2(B[k / 2].z, B[k / 2].w) : pack2(B[k / 2].x, B[k / 2].y);
-        const F2 Ck = k % 2 ? pack2(C[k / 2].z, C[k / 2].w) : pack2(C[k / 2].x, C[k / 2].y);
-        float c0, c1, x0, x1;
-        unpack2(mul2(Ck, p), c0, c1);
-        unpack2(mul2(delta2, A[k]), x0, x1);
-        const float g1 = c1 + carry[k], r1 = g1 * exp2_fast(x1);
-        const float g0 = c0 + r1, r0 = g0 * exp2_fast(x0);
-        carry[k] = r0;
-        const F2 gp = pack2(g0, g1), q = pack2(r0 * h[t][k], r1 * h[t + 1][k]);
-        dA[k] = fma2(q, delta, dA[k]);
-        qA = k == 0 ? mul2(q, A[k]) : fma2(q, A[k], qA);
-        gB = k == 0 ? mul2(gp, Bk) : fma2(gp, Bk, gB);
-        v[k] = mul2(gp, du);
-        v[4 + k] = mul2(p, pack2(h[t + 1][k], h[t + 2][k]));
+        for (int k = 0; k < kS; ++k) {
+          const F2 Bk = k % 2 ? pack2(B[k / 2].z, B[k / 2].w) : pack2(B[k / 2].x, B[k / 2].y);
+          const F2 Ck = k % 2 ? pack2(C[k / 2].z, C[k / 2].w) : pack2(C[k / 2].x, C[k / 2].y);
+          float c0, c1, x0, x1;
+          unpack2(mul2(Ck, p), c0, c1);
+          unpack2(mul2(delta2, A[k]), x0, x1);
+          const float g1 = c1 + carry[k], r1 = g1 * exp2_fast(x1);
+          const float g0 = c0 + r1, r0 = g0 * exp2_fast(x0);
+          carry[k] = r0;
+          const F2 gp = pack2(g0, g1);
+          const F2 q = pack2(kPartial && t >= left ? 0.0f : r0 * h[t][k],
+                             kPartial && t + 1 >= left ? 0.0f : r1 * h[t + 1][k]);
+          dA[k] = fma2(q, delta, dA[k]);
+          qA = k == 0 ? mul2(q, A[k]) : fma2(q, A[k], qA);
+          gB = k == 0 ? mul2(gp, Bk) : fma2(gp, Bk, gB);
+          v[k] = mul2(gp, du);
+          v[4 + k] = mul2(p, pack2(h[t + 1][k], h[t + 2][k]));
+        }
+        if (tp < TP - 1) finish(tp + 1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pv[k] = v[k];
+        pg = gB;
+        pq = qA;
       }
-      if (tp < TP - 1) finish(tp + 1);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) pv[k] = v[k];
-      pg = gB;
-      pq = qA;
-    }
+    };
+    if (left == TT) adjoint(std::false_type{});
+    else adjoint(std::true_type{});
     finish(0);
     __syncthreads();
 

@@ -349,6 +349,21 @@ def test_overflow_stays_in_its_sequence(scr):
     assert not any(g[k][1, 21:].any() for k in SEQ)
 
 
+@pytest.mark.parametrize("T", [20, 33, 47])
+@pytest.mark.parametrize("N", [4, 16, 64])
+def test_overflow_in_the_last_step(scr, T, N):
+    """A state that overflows in the last step is part of no decay's gradient:
+    that of A is what it is without the overflow."""
+    s, dy, dfinal = make(1, T, 24, N, 1, torch.float32, 19)
+    want = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    s["u"][0, T - 1] = 3e38
+    s["B"][0, T - 1] = 3e38
+    _, final = scr.selective_scan(**dev(s), return_state=True)
+    assert final.isinf().all()
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    assert torch.equal(g["A"], want["A"])
+
+
 # few states: the gradient shares a channel among one, two or four lanes,
 # by how many channels there are
 MANY = [(2, 19, 20000, 4, 1), (2, 17, 20010, 3, 3), (2, 33, 5002, 8, 1), (1, 20, 5001, 7, 1),
