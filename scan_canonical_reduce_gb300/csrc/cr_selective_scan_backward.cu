@@ -157,7 +157,7 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
   const bool gated = in.z != nullptr;
   Raw<T, VE, kWide> pu[TL::NL][2], pd[TL::NL][2], pz[TL::NL][2], py[TL::NL][2];
   Raw<T, kS, kWide> pB[TL::NBC][2], pC[TL::NBC][2];
-  float next[kS];
+  float next[kS] = {0.0f, 0.0f, 0.0f, 0.0f};
   auto load = [&](int64_t tile) {
     const int left = (int)min(len - tile * TT, (int64_t)TT);
     ru.load(left, pu);
@@ -166,8 +166,10 @@ selective_scan_backward_kernel(ScanIn<T> in, ScanBack<T> o) {
     ry.load(left, py);
     rB.load(left, pB);
     rC.load(left, pC);
+    // a lane without a channel holds none of another's states, which its own
+    // decays could take out of range
     const float* q = o.checkpoints + ((b * o.n_check + tile) * in.dim + d) * in.N;
-    read_states(q, n0, in.N, o.wide_check, next);
+    if (live) read_states(q, n0, in.N, o.wide_check, next);
   };
   if (tiles > 0) load(tiles - 1);
   __syncthreads();  // Ds, biases

@@ -364,6 +364,18 @@ def test_overflow_in_the_last_step(scr, T, N):
     assert torch.equal(g["A"], want["A"])
 
 
+@pytest.mark.parametrize("shape", [(1, 40, 40, 16, 1), (2, 33, 66, 16, 2), (1, 40, 33, 4, 1),
+                                   (1, 20, 9, 64, 1)])
+def test_channels_that_grow(scr, shape):
+    """A channel with a growth of its own, at steps so small that its states stay
+    as they are: lanes that have no channel do not take it further."""
+    s, dy, dfinal = make(*shape, torch.float32, 20)
+    s["A"] = s["A"].abs() + 9
+    s["dt_bias"] -= 20
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    check_grads(g, reference(s, True, dy, dfinal)["grads"], *shape)
+
+
 # few states: the gradient shares a channel among one, two or four lanes,
 # by how many channels there are
 MANY = [(2, 19, 20000, 4, 1), (2, 17, 20010, 3, 3), (2, 33, 5002, 8, 1), (1, 20, 5001, 7, 1),
