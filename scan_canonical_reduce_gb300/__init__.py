@@ -618,6 +618,7 @@ def measure_int_add_rate(device="cuda", stream=None) -> float:
     return rate.value
 
 
+from . import model  # noqa: E402
 from .model import (causal_conv, causal_conv_backward, causal_conv_step,  # noqa: E402
                     embedding, embedding_backward, selective_scan, selective_scan_backward,
                     selective_scan_step)

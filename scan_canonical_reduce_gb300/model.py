@@ -23,6 +23,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -67,8 +68,28 @@ class _ScanGrads(ctypes.Structure):
                 ("dA", _P), ("dD", _P), ("ddt_bias", _P), ("dstate", _P)]
 
 
+_lock = threading.Lock()
+
+
+def load():
+    """The native module, given the functions of the libcr that is loaded. It is
+    loaded by the first call of a model operator: the reductions and scans work
+    without it."""
+    global _native
+    with _lock:
+        if isinstance(_native, _Unloaded):
+            _native = _load()
+    return _native
+
+
+class _Unloaded:
+    """Stands where the native module will be."""
+
+    def __getattr__(self, name):
+        return getattr(load(), name)
+
+
 def _load():
-    """The native module, given the functions of the libcr that is loaded."""
     if not os.path.exists(BINDING_PATH):
         raise ImportError(
             "cr_model_binding.so is missing (%s): build it first with "
@@ -83,7 +104,7 @@ def _load():
     return module
 
 
-_native = _load()
+_native = _Unloaded()
 
 
 # ------------------------------------------------------------ embedding

@@ -2,6 +2,9 @@
 is enqueued (no GPU needed), and the tests' 64-bit gradient formulas against
 differences of their forward formulas."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -18,6 +21,35 @@ def m():
     __graft_entry__.build()
     from scan_canonical_reduce_gb300 import model
     return model
+
+
+WITHOUT_BINDING = """
+import os
+exists = os.path.exists
+os.path.exists = lambda p: not str(p).endswith("cr_model_binding.so") and exists(p)
+import scan_canonical_reduce_gb300 as cr
+assert cr.lib().cr_version() > 0
+assert cr.lib().cr_reduce_workspace_bytes(1000, 16, cr.CR_F64) > 0
+import torch
+for call in (lambda: cr.embedding(torch.zeros(3).long(), torch.zeros(4, 4)),
+             lambda: cr.causal_conv(torch.zeros(2, 3, 4), torch.zeros(4, 4))):
+    try:
+        call()
+    except ImportError as e:
+        assert "cr_model_binding.so" in str(e)
+    else:
+        raise AssertionError("no ImportError")
+print("fine")
+"""
+
+
+def test_reductions_and_scans_need_no_binding(m):
+    """Without the model operators' native module everything else works, and
+    they say what is missing."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", WITHOUT_BINDING], cwd=root, capture_output=True,
+                       text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr
 
 
 def at(k):
