@@ -15,6 +15,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +25,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libcr.so")
 BINDING_SRC = os.path.join(CSRC, "model_binding.cpp")
 BINDING = os.path.join(OUT_DIR, "cr_model_binding.so")
+BINDING_STAMP = BINDING + ".stamp"  # what it was built against
 SOURCES = ["cr_api.cu", "cr_calibrate.cu", "cr_chain.cu", "cr_conv.cu", "cr_embedding.cu",
            "cr_host_batched.cu", "cr_launch.cu", "cr_noalloc.cu", "cr_reduce.cu",
            "cr_reduce_policy.cu", "cr_scan.cu", "cr_selective_scan.cu",
@@ -69,6 +71,20 @@ def _binding_command(nvcc: str, out: str) -> list:
             "-ltorch_python"]
 
 
+def _binding_stamp(command: list) -> str:
+    """The versions whose ABI the binding has, and how it was compiled."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "\n".join([sys.version, f.read(), *command])
+
+
+def _binding_stale(stamp: str) -> bool:
+    if _stale(BINDING, BINDING_SRC) or not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != stamp
+
+
 def build(force: bool = False, verbose: bool = False, defines=(), out_dir: str | None = None) -> str:
     """Compiles the sources (those changed since their object, or all with
     force) and links the library; returns its path. `defines` ("NAME=value"
@@ -92,7 +108,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), out_dir: str |
             jobs.append([nvcc, *flags, "-c", s, "-o", o])
     link = bool(jobs)
     new_binding = None
-    if out_dir is None and (force or _stale(BINDING, BINDING_SRC)):
+    stamp = _binding_stamp(_binding_command(nvcc, BINDING))
+    if out_dir is None and (force or _binding_stale(stamp)):
         new_binding = BINDING + ".tmp.%d" % os.getpid()
         jobs.append(_binding_command(nvcc, new_binding))
     if jobs:
@@ -104,6 +121,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), out_dir: str |
                     raise RuntimeError("compilation failed: " + " ".join(r.args))
     if new_binding is not None:
         os.replace(new_binding, BINDING)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(stamp)
     if force or link or not os.path.exists(lib):
         tmp = lib + ".tmp.%d" % os.getpid()
         subprocess.run([nvcc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs], check=True)

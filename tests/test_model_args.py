@@ -52,6 +52,38 @@ def test_reductions_and_scans_need_no_binding(m):
     assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr
 
 
+def test_binding_is_built_anew_for_another_pytorch(m, tmp_path, monkeypatch):
+    import importlib.util
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "_cr_build_for_test", os.path.join(root, "scan_canonical_reduce_gb300", "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    assert os.path.exists(b.BINDING)
+    jobs = []
+
+    def run(command, **kw):
+        jobs.append(command)
+        raise RuntimeError("not compiled here")
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+    b.build()  # up to date: nothing to do
+    assert not jobs
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '99.0'")
+    find = b.importlib.util.find_spec
+
+    class Other:
+        submodule_search_locations = [str(other)]
+
+    monkeypatch.setattr(b.importlib.util, "find_spec",
+                        lambda n: Other if n == "torch" else find(n))
+    with pytest.raises(RuntimeError):
+        b.build()
+    assert len(jobs) == 1 and b.BINDING_SRC in jobs[0]
+
+
 def at(k):
     return FAKE * (k + 1)
 
