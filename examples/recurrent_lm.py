@@ -5,8 +5,8 @@ on a made-up sequence and then continued one token at a time.
     python examples/recurrent_lm.py
 
 The matrix products are torch's; everything between is this library's, with
-its own gradients. Training is bit-reproducible: the operators sum in one
-fixed order, so two runs end with the same parameters.
+its own gradients where autograd asks for them. Training is bit-reproducible: the
+operators sum in one fixed order, so two runs end with the same parameters.
 """
 import math
 import os
@@ -16,46 +16,6 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import scan_canonical_reduce_gb300 as cr  # noqa: E402
-
-
-class Embedding(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, tokens, table, scale):
-        ctx.save_for_backward(tokens)
-        ctx.vocab, ctx.scale = table.shape[0], scale
-        return cr.embedding(tokens, table, scale)
-
-    @staticmethod
-    def backward(ctx, grad):
-        (tokens,) = ctx.saved_tensors
-        return None, cr.embedding_backward(tokens, grad.contiguous(), ctx.vocab, ctx.scale), None
-
-
-class CausalConv(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, bias):
-        ctx.save_for_backward(x, weight, bias)
-        return cr.causal_conv(x, weight, bias, "silu")
-
-    @staticmethod
-    def backward(ctx, dy):
-        x, weight, bias = ctx.saved_tensors
-        g = cr.causal_conv_backward(dy.contiguous(), x, weight, bias, "silu")
-        return g["x"], g["weight"], g["bias"]
-
-
-class SelectiveScan(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, u, dt, A, B, C, D, z, dt_bias):
-        y, kept = cr.selective_scan(u, dt, A, B, C, D, z, dt_bias, return_checkpoints=True)
-        ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, kept)
-        return y
-
-    @staticmethod
-    def backward(ctx, dy):
-        *args, kept = ctx.saved_tensors
-        g = cr.selective_scan_backward(dy.contiguous(), *args, checkpoints=kept)
-        return tuple(g[k] for k in ("u", "dt", "A", "B", "C", "D", "z", "dt_bias"))
 
 
 class RecurrentLM:
@@ -92,11 +52,11 @@ class RecurrentLM:
     def logits(self, tokens):
         """(batch, time) tokens to (batch, time, vocab) logits, with gradients."""
         p = self.p
-        x = Embedding.apply(tokens, p["table"], self.scale)
+        x = cr.embedding(tokens, p["table"], self.scale)
         x, z = (x @ p["in"]).chunk(2, -1)
-        x = CausalConv.apply(x, p["conv_w"], p["conv_b"])
+        x = cr.causal_conv(x, p["conv_w"], p["conv_b"], "silu")
         dt, B, C = self._mix(x)
-        y = SelectiveScan.apply(x, dt, -torch.exp(p["log_A"]), B, C, p["D"], z, p["dt_bias"])
+        y = cr.selective_scan(x, dt, -torch.exp(p["log_A"]), B, C, p["D"], z, p["dt_bias"])
         return y @ p["out"]
 
     @torch.no_grad()

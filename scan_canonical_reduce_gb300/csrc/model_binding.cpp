@@ -11,12 +11,14 @@
 #include <array>
 #include <cstdint>
 #include <exception>
+#include <initializer_list>
 #include <optional>
 #include <sstream>
 #include <string>
 #include <vector>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -251,9 +253,28 @@ void put(PyObject* dict, const char* name, const at::Tensor& t) {
   Py_DECREF(v);
 }
 
+// Whether autograd has to know of a call: it records, and one of these
+// arguments requires a gradient; or one has a tangent. The call then returns
+// NotImplemented and model.py makes it part of the graph.
+bool recorded(PyObject* const* a, std::initializer_list<int> which) {
+  const bool records = c10::GradMode::is_enabled();
+  for (int i : which) {
+    if (!THPVariable_Check(a[i])) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if ((records && t.requires_grad()) || t._fw_grad(0).defined()) return true;
+  }
+  return false;
+}
+
+PyObject* not_implemented() {
+  Py_INCREF(Py_NotImplemented);
+  return Py_NotImplemented;
+}
+
 // ------------------------------------------------------------- embedding
 // (tokens, table, scale, out, stream)
 PyObject* embedding(PyObject* const* a) {
+  if (recorded(a, {1})) return not_implemented();
   const at::Tensor& table0 = tensor(a[1], "table");
   const int index = device_of(table0, "table");
   if (table0.dim() != 2) bad_value("table must be 2-D (vocab, dim)");
@@ -351,6 +372,7 @@ struct Conv {
 
 // (x, weight, bias, activation, state, lengths, return_state, out, stream)
 PyObject* causal_conv(PyObject* const* a) {
+  if (recorded(a, {0, 1, 2, 4})) return not_implemented();
   const Conv c(a, a[8]);
   const bool return_state = flag(a[6]);
   const at::Tensor y = c.on.output(a[7], c.x0.sizes(), c.x0.scalar_type());
@@ -540,6 +562,7 @@ struct Scan {
 // (u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, return_state,
 //  return_checkpoints, out, stream)
 PyObject* selective_scan(PyObject* const* a) {
+  if (recorded(a, {0, 1, 2, 3, 4, 5, 6, 7, 9})) return not_implemented();
   const Scan s(a, a[9], a[10], a[14], false);
   const bool return_state = flag(a[11]), return_checkpoints = flag(a[12]);
   const int64_t batch = s.args.batch, dim = s.args.dim, N = s.args.dstate;

@@ -16,6 +16,11 @@ the graph's own) without another one before it.
 
 Every result is one fixed expression of the inputs: repeated calls give the
 same bits.
+
+``embedding``, ``causal_conv`` and ``selective_scan`` are differentiable: where
+autograd records, their results' gradients are those of the ``*_backward``
+calls, which may also be called directly. Those and the single-token calls
+are never recorded.
 """
 from __future__ import annotations
 
@@ -26,6 +31,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _HERE, _I32, _I64, _P, SIGNATURES, _check, lib
 
@@ -107,12 +113,102 @@ def _load():
 _native = _Unloaded()
 
 
+# ------------------------------------------------------------- autograd
+def _no_out(out) -> None:
+    if out is not None:
+        raise RuntimeError("a call with out= is not recorded by autograd, but one of its "
+                           "arguments requires a gradient (or has a tangent)")
+
+
+def _backward_on(stream, call):
+    """call(stream) for a backward call, on its forward call's stream, between what
+    the engine's stream has made and what it does with the results."""
+    if stream is None:
+        return call(None)
+    here = torch.cuda.current_stream(stream.device)
+    stream.wait_stream(here)
+    out = call(stream)
+    here.wait_stream(stream)
+    for t in out.values():
+        t.record_stream(here)
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, table, scale, stream):
+        ctx.save_for_backward(tokens)
+        ctx.rest = table.shape[0], table.dtype, scale, stream
+        return _native.embedding(tokens, table, scale, None, stream)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (tokens,) = ctx.saved_tensors
+        vocab, dtype, scale, stream = ctx.rest
+        g = _backward_on(stream, lambda s: {"table": embedding_backward(tokens, dy, vocab, scale,
+                                                                        stream=s)})
+        return None, g["table"].to(dtype), None, None
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, lengths, activation, return_state, stream):
+        ctx.save_for_backward(x, weight, bias, state, lengths)
+        ctx.rest = activation, stream
+        ctx.set_materialize_grads(False)
+        return _native.causal_conv(x, weight, bias, activation, state, lengths, return_state, None,
+                                   stream)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfinal=None):
+        x, weight, bias, state, lengths = ctx.saved_tensors
+        activation, stream = ctx.rest
+        dy = torch.zeros_like(x) if dy is None else dy
+        g = _backward_on(stream, lambda s: causal_conv_backward(
+            dy, x, weight, bias, activation, state, lengths, dfinal, s))
+        return g["x"], g["weight"], g.get("bias"), g.get("state"), None, None, None, None
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, D, z, dt_bias, state, lengths, softplus, return_state,
+                return_checkpoints, stream):
+        out = _native.selective_scan(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths,
+                                     return_state, True, None, stream)
+        kept = out[-1]
+        ctx.mark_non_differentiable(kept)
+        ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, state, lengths, kept)
+        ctx.rest = softplus, return_state, stream
+        ctx.set_materialize_grads(False)
+        if return_checkpoints:
+            return out
+        return out[:-1] if return_state else out[0]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, *more):
+        u, dt, A, B, C, D, z, dt_bias, state, lengths, kept = ctx.saved_tensors
+        softplus, return_state, stream = ctx.rest
+        dy = torch.zeros_like(u) if dy is None else dy
+        g = _backward_on(stream, lambda s: selective_scan_backward(
+            dy, u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths,
+            more[0] if return_state else None, kept, s))
+        return (*(g.get(k) for k in ("u", "dt", "A", "B", "C", "D", "z", "dt_bias", "state")),
+                None, None, None, None, None)
+
+
 # ------------------------------------------------------------ embedding
 def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """``scale * table[tokens]``: tokens (any shape, int32 or int64), table
     (vocab, dim). A token outside [0, vocab) is padding: a zero row."""
-    return _native.embedding(tokens, table, scale, out, stream)
+    y = _native.embedding(tokens, table, scale, out, stream)
+    if y is NotImplemented:
+        _no_out(out)
+        return _Embedding.apply(tokens, table, scale, stream)
+    return y
 
 
 def embedding_backward(tokens: torch.Tensor, grad: torch.Tensor, vocab: int, scale: float = 1.0,
@@ -136,8 +232,11 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None
     the inputs before time 0 (zeros without it). ``lengths`` (batch): later
     positions are not read and give zeros. Returns y, or (y, state after the
     last position) with ``return_state``."""
-    return _native.causal_conv(x, weight, bias, activation, state, lengths, return_state, out,
-                               stream)
+    y = _native.causal_conv(x, weight, bias, activation, state, lengths, return_state, out, stream)
+    if y is NotImplemented:
+        _no_out(out)
+        return _CausalConv.apply(x, weight, bias, state, lengths, activation, return_state, stream)
+    return y
 
 
 def causal_conv_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
@@ -185,8 +284,13 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     zeros and leave the state. Returns y, followed by the last state
     (``return_state``) and the checkpoints that the backward call takes
     (``return_checkpoints``)."""
-    return _native.selective_scan(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths,
-                                  return_state, return_checkpoints, out, stream)
+    y = _native.selective_scan(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths,
+                               return_state, return_checkpoints, out, stream)
+    if y is NotImplemented:
+        _no_out(out)
+        return _SelectiveScan.apply(u, dt, A, B, C, D, z, dt_bias, state, lengths, softplus,
+                                    return_state, return_checkpoints, stream)
+    return y
 
 
 def selective_scan_backward(dy: torch.Tensor, u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
@@ -202,8 +306,9 @@ def selective_scan_backward(dy: torch.Tensor, u: torch.Tensor, dt: torch.Tensor,
     was used. ``checkpoints``: from the forward call (computed again without
     them)."""
     if checkpoints is None:
-        checkpoints = selective_scan(u, dt, A, B, C, D, None, dt_bias, softplus, state, lengths,
-                                     return_checkpoints=True, stream=stream)[1]
+        with torch.no_grad():
+            checkpoints = selective_scan(u, dt, A, B, C, D, None, dt_bias, softplus, state,
+                                         lengths, return_checkpoints=True, stream=stream)[1]
     return _native.selective_scan_backward(u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths,
                                            dy, dfinal, checkpoints, stream)
 

@@ -506,6 +506,102 @@ def test_binding_refusals(scr):
         scr.embedding_backward(t["tokens"][:, :3], t["dy"], 500)
 
 
+def with_grad(t, names):
+    return {k: v.clone().requires_grad_(k in names) for k, v in t.items()}
+
+
+SCAN_ARGS = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")  # and their names in the gradients
+SCAN_GRADS = ("u",) + SCAN_ARGS[1:]
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_autograd_gives_the_backward_calls(scr, other):
+    """What autograd finds for a recorded call is, to the bit, what the backward
+    call gives: with states and lengths, on the current stream and on another."""
+    t = inputs(30)
+    lengths = torch.tensor([150, 0, 77], device=DEV)
+    dconv, dscan = torch.randn_like(t["conv"]), torch.randn_like(t["scan"])
+    stream = torch.cuda.Stream(DEV) if other else None
+
+    def joined(call):
+        if not other:
+            return call(None)
+        stream.wait_stream(torch.cuda.current_stream(DEV))
+        torch.cuda._sleep(2_000_000)
+        out = call(stream)
+        torch.cuda.current_stream(DEV).wait_stream(stream)
+        return out
+
+    p = with_grad(t, t.keys() - {"tokens", "dy"})
+    y = joined(lambda s: scr.embedding(p["tokens"], p["table"], 2.0, stream=s))
+    y.backward(t["dy"])
+    want = scr.embedding_backward(t["tokens"], t["dy"], 500, 2.0).to(t["table"].dtype)
+    assert torch.equal(p["table"].grad, want)
+
+    y, last = joined(lambda s: scr.causal_conv(p["x"], p["weight"], p["bias"], "silu", p["conv"],
+                                               lengths, return_state=True, stream=s))
+    torch.autograd.backward([y, last], [t["dy"], dconv])
+    want = scr.causal_conv_backward(t["dy"], t["x"], t["weight"], t["bias"], "silu", t["conv"],
+                                    lengths, dconv)
+    for k, name in (("x", "x"), ("weight", "weight"), ("bias", "bias"), ("conv", "state")):
+        assert torch.equal(p[k].grad, want[name]), k
+        p[k].grad = None
+
+    y, last, kept = joined(lambda s: scr.selective_scan(
+        *(p[k] for k in SCAN_ARGS), state=p["scan"], lengths=lengths, return_state=True,
+        return_checkpoints=True, stream=s))
+    assert not kept.requires_grad
+    torch.autograd.backward([y, last], [t["dy"], dscan])
+    want = scr.selective_scan_backward(t["dy"], *(t[k] for k in SCAN_ARGS), state=t["scan"],
+                                       lengths=lengths, dfinal=dscan)
+    for k, name in zip(SCAN_ARGS + ("scan",), SCAN_GRADS + ("state",)):
+        assert torch.equal(p[k].grad, want[name]), k
+
+
+def test_autograd_of_some_arguments_and_results(scr):
+    t = inputs(31)
+    main = [t[k] for k in SCAN_ARGS]
+    # one argument that requires a gradient, the state alone used
+    A = t["A"].clone().requires_grad_()
+    y, last = scr.selective_scan(*main[:2], A, *main[3:], return_state=True)
+    last.sum().backward()
+    want = scr.selective_scan_backward(torch.zeros_like(t["dy"]), *main,
+                                       dfinal=torch.ones_like(last))
+    assert torch.equal(A.grad, want["A"]) and y.requires_grad
+    y = scr.selective_scan(*main[:2], A, *main[3:])
+    assert torch.equal(y.detach(), scr.selective_scan(*main))
+    weight = t["weight"].clone().requires_grad_()
+    _, last = scr.causal_conv(t["x"], weight, return_state=True)
+    last.float().sum().backward()
+    assert not weight.grad.any()
+    # an expanded gradient, a view of the table, tokens of any shape
+    base = torch.randn(2, 500, 200, device=DEV, requires_grad=True)
+    scr.embedding(t["tokens"], base[1], 3.0).sum().backward()
+    want = scr.embedding_backward(t["tokens"], torch.ones(3, 150, 200, device=DEV), 500, 3.0)
+    assert torch.equal(base.grad[1], want) and not base.grad[0].any()
+    # nothing is recorded where nothing asks for it, or where recording is off
+    assert not scr.embedding(t["tokens"], t["table"]).requires_grad
+    with torch.no_grad():
+        assert not scr.embedding(t["tokens"], base[0]).requires_grad
+        assert not scr.causal_conv(t["x"], weight).requires_grad
+
+
+def test_autograd_refusals(scr):
+    import torch.autograd.forward_ad as forward_ad
+    t = inputs(32)
+    weight = t["weight"].clone().requires_grad_()
+    with pytest.raises(RuntimeError):  # out= leaves no history
+        scr.causal_conv(t["x"], weight, out=torch.empty_like(t["x"]))
+    y = scr.causal_conv(t["x"], weight, activation="silu")
+    with pytest.raises(RuntimeError):  # no gradient of a gradient
+        (g,) = torch.autograd.grad(y.float().square().sum(), weight, create_graph=True)
+        g.sum().backward()
+    with forward_ad.dual_level():  # no tangents
+        dual = forward_ad.make_dual(t["table"].float(), torch.ones(500, 200, device=DEV))
+        with pytest.raises(RuntimeError):
+            scr.embedding(t["tokens"], dual)
+
+
 def example():
     sys.path.insert(0, os.path.join(ROOT, "examples"))
     try:
