@@ -173,11 +173,17 @@ struct On {
     const at::Tensor& t = tensor(out, "out");
     need(t, "out", shape, dtype, index);
     if (t.size(-1) > 1 && t.stride(-1) != 1) bad_value("out must have a contiguous last axis");
-    uses(t);
+    writes(t);
     return t;
   }
   void uses(const at::Tensor& t) const {
     if (other) t.record_stream(*other);
+  }
+
+  // t is written: autograd sees that it is no longer what a call may have saved.
+  void writes(const at::Tensor& t) const {
+    uses(t);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
   }
 
   // A call's workspace: its own, from the stream's allocator, which may have
@@ -436,7 +442,7 @@ const at::Tensor& step_state(const On& on, PyObject* o, at::IntArrayRef row, at:
   if (!t.is_contiguous()) bad_value("state must be contiguous (it is updated in place)");
   if (!slots && t.size(0) < batch)
     bad_value(join("state must have a row for each of the ", batch, " streams"));
-  on.uses(t);
+  on.writes(t);
   return t;
 }
 

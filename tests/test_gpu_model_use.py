@@ -586,6 +586,34 @@ def test_autograd_of_some_arguments_and_results(scr):
         assert not scr.causal_conv(t["x"], weight).requires_grad
 
 
+def test_autograd_notices_what_is_overwritten(scr):
+    """A state that a recorded call has saved and a step then moves on, or a saved
+    input that another call's out= replaces, is an error in the backward."""
+    t = inputs(33)
+    step = scr.selective_scan_step, scr.causal_conv_step
+    A, weight = t["A"].clone().requires_grad_(), t["weight"].clone().requires_grad_()
+    main = [t[k] for k in SCAN_ARGS]
+    one = [v[:, 0] if v.dim() == 3 else v for v in main]
+    for touch in (False, True):
+        y = scr.selective_scan(*main[:2], A, *main[3:], state=t["scan"])
+        x = scr.causal_conv(t["x"], weight, state=t["conv"])
+        if touch:
+            step[0](*one[:5], t["scan"], one[5], one[6], one[7])
+            step[1](t["x"][:, 0], t["conv"], t["weight"])
+            for out in (y, x):
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    out.sum().backward()
+        else:
+            y.sum().backward(), x.sum().backward()
+    x = scr.causal_conv(t["x"], weight)
+    scr.causal_conv(t["z"], t["weight"], out=t["x"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        x.sum().backward()
+    with torch.inference_mode():  # states of inference: no counter, no complaint
+        state = t["conv"].clone()
+    scr.causal_conv_step(t["x"][:, 0], state, t["weight"])
+
+
 def test_autograd_refusals(scr):
     import torch.autograd.forward_ad as forward_ad
     t = inputs(32)
