@@ -196,6 +196,27 @@ def test_step_slots(scr, dtype, B, D, K, index):
     assert torch.equal(state.cpu(), want)
 
 
+def test_gradients_past_32_bits(scr):
+    """Results that begin more than 2^31 elements into their tensors, against a
+    call on the last sequence alone."""
+    batch, T, D, K = 66, 16384, 2048, 4
+    g = torch.Generator(device=DEV).manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    x, dy, w, bias = r(1, T, D), r(1, T, D), r(D, K).float(), r(D).float()
+
+    def whole(v):
+        out = torch.zeros(batch, T, D, dtype=v.dtype, device=DEV)
+        out[-1:] = v
+        return out
+
+    y = scr.causal_conv(whole(x), w, bias, "silu")
+    assert y.numel() > 1 << 31
+    assert torch.equal(y[-1:], scr.causal_conv(x, w, bias, "silu"))
+    del y
+    got = scr.causal_conv_backward(whole(dy), whole(x), w, bias, "silu")["x"]
+    assert torch.equal(got[-1:], scr.causal_conv_backward(dy, x, w, bias, "silu")["x"])
+
+
 def test_repeated_calls_give_the_same_bits(scr):
     s, dy, _ = make(2, 300, 260, 4, torch.bfloat16, 10)
     first = scr.causal_conv_backward(dy.to(DEV), **dev(s), activation="silu")

@@ -151,6 +151,21 @@ def test_gradient_large_vocabulary(scr):
     assert not got[mask].any()
 
 
+@pytest.mark.parametrize("n", [1500, 6000])
+def test_gradient_past_32_bits(scr, n):
+    """Rows of the gradient that begin more than 2^31 elements into it."""
+    V, D = (1 << 20) + 5000, 2052
+    tok = torch.randint(V - 300, V, (n,), generator=gen(31))
+    tok[:20] = torch.arange(20)
+    grad = torch.randn(n, D, generator=gen(32)).to(torch.bfloat16)
+    got = scr.embedding_backward(tok.to(DEV), grad.to(DEV), V, 0.5)
+    assert got.numel() > 1 << 31
+    assert not got[20:V - 300].any()
+    want = want_grad(tok - (V - 300), grad, 300, 0.5)
+    assert got[V - 300:].cpu().numpy().tobytes() == want.tobytes()
+    assert torch.equal(got[:20].cpu(), grad[:20].float() * 0.5)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,V,D", [(500, 900, 68), (5000, 9000, 68), (3000, 2000, 37),
                                    (2048, 700, 130), (2049, 700, 130)])

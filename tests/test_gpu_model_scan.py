@@ -255,6 +255,53 @@ def test_step_slots(scr, dtype, batch, D, N, groups, index):
     assert torch.equal(state[left].cpu(), pool[left])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,N,groups", [(36, 16, 1), (70, 13, 2), (9, 1, 1), (33, 8, 3), (10, 64, 2),
+                                        (5, 128, 1)])
+def test_steps_give_the_bits_of_a_prompt(scr, dtype, D, N, groups):
+    """Sequences short enough not to be cut: one call, two calls and single tokens
+    evaluate the same expression."""
+    s, _, _ = make(2, 60, D, N, groups, dtype, 21)
+    d = dev(s)
+    want, last = scr.selective_scan(**d, return_state=True)
+    cut = {k: (v[:, :23] if k in SEQ else v) for k, v in d.items()}
+    y, state = scr.selective_scan(**cut, return_state=True)
+    assert torch.equal(y, want[:, :23])
+    rest = {**{k: (v[:, 23:] if k in SEQ else v) for k, v in d.items()}, "state": state}
+    y, end = scr.selective_scan(**rest, return_state=True)
+    assert torch.equal(y, want[:, 23:]) and torch.equal(end, last)
+    for t in range(23, 60):
+        y = scr.selective_scan_step(d["u"][:, t], d["dt"][:, t], d["A"], d["B"][:, t],
+                                    d["C"][:, t], state, d["D"], d["z"][:, t], d["dt_bias"])
+        assert torch.equal(y, want[:, t]), t
+    assert torch.equal(state, last)
+
+
+@pytest.mark.parametrize("batch", [1, 800])
+def test_long_sequence_that_forgets(scr, batch):
+    """Decays of at most e^-0.5 keep an error for 1 / (1 - e^-0.5) = 2.6 steps, so
+    that thousands of steps leave no more than tens of roundings: 8 a step for
+    2.6 steps, the sums over the states and the outputs', with room to 64. Cut into
+    segments (one sequence) and whole (800 of them)."""
+    T, D, N = 2500 if batch == 1 else 300, 8, 16
+    s, dy, dfinal = make(1, T, D, N, 1, torch.float32, 22)
+    s["dt"] = s["dt"].abs().clamp(max=0.5) + 0.5
+    s["A"] = -1 - torch.rand(D, N, generator=torch.Generator().manual_seed(23))
+    s["dt_bias"] = torch.zeros(D)
+    ref = reference(s, False, dy, dfinal)
+    many = {k: v if v is None or k in ("A", "D", "dt_bias") else
+            v.expand(batch, *v.shape[1:]) for k, v in s.items()}
+    y, final = scr.selective_scan(**dev(many), softplus=False, return_state=True)
+    R.close(y[:1], *ref["y"], 64, "y")
+    R.close(final[:1], *ref["final"], 64, "state")
+    assert torch.equal(y[0].expand_as(y), y) and torch.equal(final[0].expand_as(final), final)
+    if batch == 1:
+        g = scr.selective_scan_backward(dy.to(DEV), **dev(s), softplus=False,
+                                        dfinal=dfinal.to(DEV))
+        for k in ("u", "dt", "z", "B", "C", "state"):
+            R.close(g[k], *ref["grads"][k], 2 * 64 + (D if k in ("B", "C") else 0), k)
+
+
 def test_long_sequence(scr):
     """Thousands of steps, a few channels."""
     s, dy, _ = make(1, 2500, 8, 16, 1, torch.float32, 14)
@@ -374,6 +421,44 @@ def test_channels_that_grow(scr, shape):
     s["dt_bias"] -= 20
     g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
     check_grads(g, reference(s, True, dy, dfinal)["grads"], *shape)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(2, 35, 130, 33, 1), (1, 50, 200, 64, 2), (2, 19, 70, 100, 1),
+                                   (1, 33, 96, 128, 3)])
+def test_backward_of_many_states(scr, dtype, shape):
+    """More than 32 states and more channels than a block has."""
+    s, dy, dfinal = make(*shape, dtype, 24, lengths=[shape[1], 18][:shape[0]])
+    g = scr.selective_scan_backward(dy.to(DEV), **dev(s), dfinal=dfinal.to(DEV))
+    check_grads(g, reference(s, True, dy, dfinal)["grads"], *shape)
+
+
+def test_gradients_past_32_bits(scr):
+    """Results that begin more than 2^31 elements into their tensors, against a
+    call on the last sequences alone (enough of them not to be cut)."""
+    batch, T, D, N = 66, 16384, 2048, 4
+    g = torch.Generator(device=DEV).manual_seed(25)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    last = {k: r(12, T, D) for k in ("u", "dt", "z")}
+    last.update({k: r(12, T, 1, N) for k in ("B", "C")})
+    dy = r(12, T, D)
+
+    def whole(v):
+        out = torch.zeros(batch, *v.shape[1:], dtype=v.dtype, device=DEV)
+        out[-12:] = v
+        return out
+
+    rest = {"A": -torch.exp(r(D, N).float()), "D": r(D).float(), "dt_bias": r(D).float() - 3}
+    y, final = scr.selective_scan(**{k: whole(v) for k, v in last.items()}, **rest,
+                                  return_state=True)
+    assert y.numel() > 1 << 31
+    want, want_final = scr.selective_scan(**last, **rest, return_state=True)
+    assert torch.equal(y[-12:], want) and torch.equal(final[-12:], want_final)
+    del y
+    want = scr.selective_scan_backward(dy, **last, **rest)
+    got = scr.selective_scan_backward(whole(dy), **{k: whole(v) for k, v in last.items()}, **rest)
+    for k in SEQ:
+        assert torch.equal(got[k][-12:], want[k]), k
 
 
 # few states: the gradient shares a channel among one, two or four lanes,
