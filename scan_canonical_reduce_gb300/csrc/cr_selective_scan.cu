@@ -24,7 +24,7 @@ namespace {
 struct Segments {
   int64_t count, len;
   float* E;        // [count - 1][batch][dim][NP]
-  float* initial;  // [batch][dim][NP], or NULL: the call's own
+  float* initial;  // [batch][dim][N], or NULL: no copy
   float* sum;      // [count - 1][batch][dim]
 };
 
@@ -81,10 +81,7 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
     for (int k = 0; k < kS; ++k) A[k] = pack2(a[k] * kLog2e, a[k] * kLog2e);
   }
   if (!kStates) {
-    if (sg.initial != nullptr)
-      read_states(sg.initial + (b * in.dim + d) * TL::NP, n0, TL::NP, true, h);
-    else if (in.state != nullptr)
-      load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
+    if (in.state != nullptr) load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
     const float* E = sg.E + (b * in.dim + d) * TL::NP + n0;
     const float* sum = sg.sum + b * in.dim + d;
 #pragma unroll 4
@@ -278,8 +275,9 @@ selective_scan_kernel(ScanIn<T> in, ScanOut<T> out, Segments sg) {
       unpack2(total, lo, hi);
       if (g == 0) sg.sum[row] = lo + hi;
       if (seg == 0 && sg.initial != nullptr) {
-        load_states(in.state + (b * in.dim + d) * in.N, n0, in.N, h);
-        store_states(sg.initial + (b * in.dim + d) * TL::NP, n0, TL::NP, true, h);
+        const int64_t at = (b * in.dim + d) * in.N;
+        load_states(in.state + at, n0, in.N, h);
+        store_states(sg.initial + at, n0, in.N, false, h);
       }
     }
   } else {
@@ -506,14 +504,15 @@ cr_status cr_selective_scan(const cr_selective_scan_args* a, void* y, int64_t y_
                          rows_aligned(a->B, a->B_batch_stride, a->B_time_stride, es, kS * es) &&
                          rows_aligned(a->C, a->C_batch_stride, a->C_time_stride, es, kS * es);
     const bool wide = wide_u && wide_BC;
+    ScanIn<T> in = scan_in<T>(a);
     if (sg.count > 1)
       CR_LAUNCH(kKSelectiveScanStates, s,
                 (wide ? selective_scan_kernel<T, G, true, true>
-                      : selective_scan_kernel<T, G, true, false>)<<<(unsigned)(blocks * (sg.count - 1)), kScanThreads, 0, s>>>(scan_in<T>(a), out,
-                                                                              sg));
+                      : selective_scan_kernel<T, G, true, false>)<<<(unsigned)(blocks * (sg.count - 1)), kScanThreads, 0, s>>>(in, out, sg));
+    if (sg.initial != nullptr) in.state = sg.initial;
     CR_LAUNCH(kKSelectiveScan, s,
               (wide ? selective_scan_kernel<T, G, false, true>
-                    : selective_scan_kernel<T, G, false, false>)<<<(unsigned)(blocks * sg.count), kScanThreads, 0, s>>>(scan_in<T>(a), out, sg));
+                    : selective_scan_kernel<T, G, false, false>)<<<(unsigned)(blocks * sg.count), kScanThreads, 0, s>>>(in, out, sg));
   }));
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
