@@ -548,13 +548,13 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
   if (g == nullptr || g->dy_batch_stride < 0 || g->dy_time_stride < 0) return CR_ERR_INVALID_ARG;
   if (a->dim == 0) {  // B and C are there all the same, and reach nothing
     const size_t bytes = (size_t)a->batch * a->len * a->groups * a->dstate * es;
-    for (void* o : {g->dB, g->dC}) {
-      if (bytes > 0 && (o == nullptr || !ptr_aligned(o, es) || overwrites({o}, {a->B, a->C})))
-        return CR_ERR_INVALID_ARG;
-      if (bytes > 0 &&
-          cudaMemsetAsync(o, 0, bytes, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (bytes == 0) return CR_OK;
+    if (g->dB == nullptr || g->dC == nullptr || !ptr_aligned(g->dB, es) ||
+        !ptr_aligned(g->dC, es) || overwrites({g->dB, g->dC}, {a->B, a->C}))
+      return CR_ERR_INVALID_ARG;
+    for (void* o : {g->dB, g->dC})
+      if (cudaMemsetAsync(o, 0, bytes, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return CR_ERR_CUDA;
-    }
     return CR_OK;
   }
   if (g->dA == nullptr) return CR_ERR_INVALID_ARG;
@@ -581,11 +581,14 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
   const int lanes = backward_lanes(a->batch, a->dim, a->dstate);
   const int64_t parts = group_blocks(a->dim, a->groups, lanes);
   const int64_t rows = a->batch * a->len * a->groups;
+  const int64_t all = a->batch > 0 ? scan_blocks(a->batch, a->dim, a->groups, lanes) : 0;
+  const int64_t sums = ceil_div(rows * 2 * a->dstate, kScanThreads);
+  if ((a->batch > 0 && all == 0) || sums > kMaxBlocks) return CR_ERR_UNSUPPORTED;
   float* part_BC = reinterpret_cast<float*>(past_status(ws));
   float* part_A = reinterpret_cast<float*>(
       past_status(ws) + round256((size_t)rows * parts * 2 * (lanes * kS) * 4));
   if (a->batch > 0) {
-    const unsigned blocks = (unsigned)scan_blocks(a->batch, a->dim, a->groups, lanes);
+    const unsigned blocks = (unsigned)all;
     const int64_t n_check = cr_selective_scan_checkpoints(a->len);
     CR_MODEL_TYPE(a->dt_type, CR_SCAN_LANES(lanes, {
       ScanBack<T> o;
@@ -622,8 +625,6 @@ cr_status cr_selective_scan_backward(const cr_selective_scan_args* a,
                     scan_in<T>(a), o));
     }));
     if (cudaGetLastError() != cudaSuccess) return CR_ERR_CUDA;
-    const int64_t sums = ceil_div(rows * 2 * a->dstate, kScanThreads);
-    if (sums > kMaxBlocks) return CR_ERR_UNSUPPORTED;
     if (sums > 0) {
       CR_MODEL_TYPE(a->dt_type, {
         CR_LAUNCH(kKSelectiveScanSum, s,

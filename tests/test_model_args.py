@@ -285,6 +285,17 @@ def test_scan_backward_workspace(m):
     assert scan_back(m, dstate=129) == UNSUPPORTED
 
 
+def test_scan_backward_refuses_before_it_starts(m):
+    """What cannot be done is refused with nothing enqueued: more sums of B and C
+    than a grid has blocks, and one gradient of two that is missing."""
+    size = 1 << 62
+    assert scan_back(m, size=size, batch=1 << 10, len=1 << 27, groups=1) == UNSUPPORTED
+    assert scan_back(m, dim=0, dC=None) == INVALID
+    assert scan_back(m, dim=0, dB=at(13) + 1) == INVALID
+    assert scan_back(m, dim=0, dC=at(3)) == INVALID
+    assert scan_back(m, dim=0, len=0, dC=None) == OK
+
+
 def scan_step(m, **k):
     y = dict(state=at(8), rows=2, slots=None, y=at(10), ybs=16)
     y.update({n: v for n, v in k.items() if n in y})
