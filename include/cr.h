@@ -318,6 +318,10 @@ cr_status cr_reduce_noalloc(const void* x, int64_t n, int32_t L, const void* ini
  *     read and their outputs are zero.
  *   - Every result is one fixed expression of the inputs: sums are ordered,
  *     no value is summed by atomics, and repeated calls give the same bits.
+ *     The lookup and its gradient are multiplications and additions, rounded
+ *     to nearest; the nonlinearities of the others (decays, SiLU, softplus)
+ *     use the GPU's approximate exponential and reciprocal, whose bits a CPU
+ *     does not repeat.
  *   - Outputs must not overlap inputs or each other, except where a call says
  *     so. An output pointer equal to a pointer the call reads is INVALID_ARG;
  *     other overlaps are not looked for.

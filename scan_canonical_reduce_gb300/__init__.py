@@ -14,11 +14,17 @@ andyD123/canonical-reduce):
   * ``inclusive_scan(x, policy, B)``: P4229R0's prefix observations of the
     named expression policies left_fold, pairwise, iterated_pairwise,
     block_dyadic<B>;
-  * batched/strided variants of both over one axis of a 2-D tensor;
-  * the operators of a recurrent language model's token path (``model.py``):
-    embedding lookup, short causal convolution, selective state space scan,
-    with their gradients and single-token forms.
-Results are bit-identical to the named expression on any GPU and launch shape.
+  * batched/strided variants of both over one axis of a 2-D tensor.
+Their results are bit-identical to the named expression on any GPU and launch
+shape.
+
+Beside them stand the operators of a recurrent language model's token path
+(``model.py``): embedding lookup, short causal convolution, selective state
+space scan, with their gradients and single-token forms. Their sums have one
+order each, whatever the launch, so that repeated calls give the same bits;
+the lookup and its gradient are exact expressions as above, while decays,
+SiLU and softplus rest on the GPU's approximate exponential and reciprocal
+instructions, which no CPU evaluation repeats bit for bit.
 """
 from __future__ import annotations
 

@@ -4,9 +4,10 @@ Each translation unit is compiled in parallel with nvcc, then linked into a
 shared library next to this file (``_build/libcr.so``). Beside it goes
 ``_build/cr_model_binding.so``, the Python side of the model operators, which
 is host code against PyTorch's headers. The flags keep every
-floating-point add an explicit round-to-nearest operation: no FMA
-contraction, no flush-to-zero, IEEE division and square root, never
---use_fast_math.
+floating-point operation what the source says: no FMA contraction, no
+flush-to-zero, IEEE division and square root, never --use_fast_math. (The
+convolution and the scan ask for fused multiply-adds and for the approximate
+exponential and reciprocal by name.)
 """
 from __future__ import annotations
 

@@ -11,8 +11,9 @@
 // Measured, bf16: lookup of 32,805 rows of 4096 columns in a table of 65,536,
 // 68 us (537 MB at 7.9 TB/s, since repeated rows come from L2); gradient of
 // 65,536 rows of 2048 columns into 65,536 rows, the most frequent token 4,096
-// times, 207 us against 119 us for its 806 MB at the copy rate: 23 us sort,
-// 150 us rows and parts, 39 us long rows, each with its launch.
+// times, 210 us against 119 us for its 806 MB at the copy rate (its launches
+// one by one, with the events around them: 23 us sort, 153 us rows and parts,
+// 39 us long rows).
 #include <cstdint>
 
 #include "cr_device.cuh"
@@ -23,7 +24,7 @@ namespace cr {
 namespace {
 
 // ------------------------------------------------------------- lookup
-// Bound by DRAM; few tokens are bound by the call (3.7 us).
+// Bound by DRAM; few tokens are bound by the call (4 us).
 // A block covers blockDim.y tokens; the threads of a row walk its columns, V at
 // a time: neighbours in one access (kWide), or blockDim.x apart, so that the
 // threads' accesses are consecutive.
@@ -108,9 +109,10 @@ __device__ __forceinline__ void load_tokens(const void* tokens, int index_bytes,
 // counters are its own, and within 32 positions equal tokens are ranked by
 // lane, so the order is that of the positions. All counts are integers: the
 // result is unique whatever the order of the atomics. Every block reading all
-// tokens costs L2 reads (65,536 tokens: 152 x 512 KB, about 4 us a sweep) and
-// saves the launches and the traffic of a sort by digits; a warp's own tokens
-// are kept from the first sweep, which halves the second's time for most.
+// tokens costs L2 reads (65,536 tokens: 152 x 512 KB a sweep, of a sort of
+// 23 us in all) and saves the launches and the traffic of a sort by digits; a
+// warp's own tokens are kept from the first sweep, which spares most warps the
+// second.
 //
 // A row with kLong positions or more has its complete groups of kLong summed
 // by blocks of their own. Group k of the row that begins at s is number
@@ -579,8 +581,11 @@ embedding_rows_kernel(Grad<T> grad, Sorted in, int64_t part_items, int64_t part_
 // ------------------------------------------------------- few positions
 // Up to kFewTokens positions take one launch: a block sorts the positions of
 // kFewRows rows of the table in shared memory and sums them, a warp a row and
-// 128 columns at a time. (One token that had most positions would be
-// summed by one block: for many positions the launches above share it out.)
+// 128 columns at a time. A token's positions are summed by one warp for every
+// 128 columns, one group of 8 after another, which the launches above share
+// out: 2,048 equal tokens of 64 columns take 209 us here, where as many spread
+// ones take 9 us and 2,049 equal ones, in three launches, 33 us. (The rule
+// between the two knows sizes, not tokens.)
 constexpr int kFewTokens = 2048, kFewRows = 16;
 constexpr int kFewEach = kFewTokens / 256;  // tokens a thread
 
