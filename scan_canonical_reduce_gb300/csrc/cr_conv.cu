@@ -362,7 +362,7 @@ causal_conv_backward_kernel(ConvIn<T> in, ConvShape sh, ConvBack<T> g) {
         if (kFull || s + u < live) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            db.p[j] = add2(db.p[j], d[u].p[j]);
+            db.p[j] = add2_products(db.p[j], d[u].p[j]);
 #pragma unroll
             for (int k = 0; k < K; ++k) dw[k].p[j] = fma2(d[u].p[j], win[u + k].p[j], dw[k].p[j]);
           }

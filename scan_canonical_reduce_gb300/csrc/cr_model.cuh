@@ -222,7 +222,8 @@ __device__ __forceinline__ float sigmoid(float v) {
 
 // ------------------------------------------------- pairs of binary32
 // Two binary32 values in one 64-bit register pair, for the packed
-// arithmetic (one issue for two operations, each rounded to nearest).
+// arithmetic (one issue for two operations; fma and mul are rounded to nearest
+// one by one, for sums see add2).
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 pack2(float lo, float hi) {
   F2 r;
@@ -242,10 +243,22 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Not for products: given a packed product as an operand, a packed addition is
+// joined with it into one rounding (nvcc 13.0, in spite of .rn and of
+// --fmad=false), in some variants of a kernel and not in others.
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// The same of any operands, as two single additions (the scan's gradient, 4 x 2048
+// x 2048: 450 us with packed ones alone, 456 with these where products are
+// summed, 468 with these alone).
+__device__ __forceinline__ F2 add2_products(F2 a, F2 b) {
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
 }
 
 // softplus(v) = log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), of two
@@ -264,7 +277,7 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
   p = fma2(p, w, pack2(1.0f / 5.0f, 1.0f / 5.0f));
   p = fma2(p, w, pack2(1.0f / 3.0f, 1.0f / 3.0f));
   p = fma2(p, w, pack2(1.0f, 1.0f));
-  unpack2(fma2(add2(s, s), p, pack2(fmaxf(v0, 0.0f), fmaxf(v1, 0.0f))), v0, v1);
+  unpack2(fma2(mul2(s, pack2(2.0f, 2.0f)), p, pack2(fmaxf(v0, 0.0f), fmaxf(v1, 0.0f))), v0, v1);
 }
 
 __device__ __forceinline__ float softplus(float v) {

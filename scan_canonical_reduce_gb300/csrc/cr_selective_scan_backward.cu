@@ -36,22 +36,28 @@ struct ChannelSum {
   static constexpr int L = 32 / G;  // lanes that are summed
   static constexpr int kPairs = L >= 8 ? 1 : L == 4 ? 2 : L == 2 ? 4 : 8;  // left of 8
 
-  static __device__ __forceinline__ F2 exchange(F2 keep, F2 send, int mask) {
+  static __device__ __forceinline__ F2 other(F2 send, int mask) {
     float a, b;
     unpack2(send, a, b);
     a = __shfl_xor_sync(~0u, a, mask);
     b = __shfl_xor_sync(~0u, b, mask);
-    return add2(keep, pack2(a, b));
+    return pack2(a, b);
+  }
+  static __device__ __forceinline__ F2 exchange(F2 keep, F2 send, int mask) {
+    return add2(keep, other(send, mask));
+  }
+  static __device__ __forceinline__ F2 first(F2 keep, F2 send) {  // of products
+    return add2_products(keep, other(send, L / 2));
   }
   static __device__ __forceinline__ F2 select(bool s, F2 a, F2 b) { return s ? a : b; }
 
   // v[8] -> v[0 .. kPairs)
   static __device__ __forceinline__ void run(F2 (&v)[8], int c) {
     if (L >= 2) {  // slots {0, 1} or {2, 3}: v = B0 B1 C0 C1
-      v[0] = exchange(v[0], v[2], L / 2);
-      v[1] = exchange(v[1], v[3], L / 2);
-      v[2] = exchange(v[4], v[6], L / 2);
-      v[3] = exchange(v[5], v[7], L / 2);
+      v[0] = first(v[0], v[2]);
+      v[1] = first(v[1], v[3]);
+      v[2] = first(v[4], v[6]);
+      v[3] = first(v[5], v[7]);
     }
     if (L >= 4) {  // slot 0 or 1: v = B C
       const bool up = c & (L / 4);

@@ -151,6 +151,27 @@ def test_strides_and_alignment(scr):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_unaligned_rows_give_the_same_bits(scr, dtype, K, act):
+    s, dy, dfinal = make(2, 90, 136, K, dtype, 13, lengths=[90, 41])
+    d = dev(s)
+
+    def off(v):  # the same values, rows that start an element later
+        wide = torch.zeros(*v.shape[:-1], v.shape[-1] + 8, dtype=v.dtype, device=DEV)
+        wide[..., 1:1 + v.shape[-1]] = v
+        return wide[..., 1:1 + v.shape[-1]]
+
+    def results(d, dy):
+        y = scr.causal_conv(**d, activation=act)
+        return y, scr.causal_conv_backward(dy, **d, activation=act, dfinal=dfinal.to(DEV))
+
+    y, g = results(d, dy.to(DEV))
+    y2, g2 = results({**d, "x": off(d["x"])}, off(dy.to(DEV)))
+    assert torch.equal(y, y2) and all(torch.equal(g[k], g2[k]) for k in g)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_parts_give_the_whole(scr, dtype):
     """A sequence cut anywhere, and single tokens, give the bits of one call."""
     s, _, _ = make(2, 90, 20, 4, dtype, 7)

@@ -208,6 +208,66 @@ def test_strides_and_alignment(scr):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [4, 8, 16, 32, 64, 128])
+def test_unaligned_rows_give_the_same_bits(scr, dtype, N):
+    """Whole accesses and elementwise ones, for every number of lanes a channel:
+    forward, gradients and single tokens."""
+    s, dy, dfinal = make(2, 37, 72, N, 1, dtype, 26)
+    d = {**dev(s), "dy": dy.to(DEV)}
+
+    def off(v):  # the same values, rows that start an element later
+        wide = torch.zeros(*v.shape[:-1], v.shape[-1] + 8, dtype=v.dtype, device=DEV)
+        wide[..., 1:1 + v.shape[-1]] = v
+        return wide[..., 1:1 + v.shape[-1]]
+
+    def results(d):
+        dy, rest = d["dy"], {k: v for k, v in d.items() if k != "dy"}
+        y, final = scr.selective_scan(**rest, return_state=True)
+        g = scr.selective_scan_backward(dy, **rest, dfinal=dfinal.to(DEV))
+        state = rest["state"].clone()
+        one = scr.selective_scan_step(rest["u"][:, 0], rest["dt"][:, 0], rest["A"],
+                                      rest["B"][:, 0], rest["C"][:, 0], state, rest["D"],
+                                      rest["z"][:, 0], rest["dt_bias"])
+        return {"y": y, "final": final, "one": one, "after": state,
+                **{"d" + k: v for k, v in g.items()}}
+
+    want = results(d)
+    B, C = off(d["B"].squeeze(2)), off(d["C"].squeeze(2))
+    got = results({**d, **{k: off(d[k]) for k in ("u", "dt", "z", "dy")}, "B": B, "C": C})
+    for k in want:
+        assert torch.equal(got[k].view(want[k].shape), want[k]), k
+
+
+@pytest.mark.parametrize("N", [1, 4, 8, 16, 32, 64, 128])
+@pytest.mark.parametrize("off", [0, 1])
+def test_sums_over_channels_are_of_rounded_products(scr, N, off):
+    """One step of two channels, whichever two: dB and dC are the rounded sums of
+    two rounded products, to the bit. (Joined into one rounding they would depend
+    on how the compiler has arranged a variant of the kernel.)"""
+    D = 64
+    g = torch.Generator().manual_seed(27)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    u, dy = torch.zeros(D - 1, 1, D), torch.zeros(D - 1, 1, D)
+    for j in range(1, D):
+        for v in (u, dy):
+            v[j - 1, 0, 0], v[j - 1, 0, j] = r(1), r(1)
+    B, C = r(D - 1, 1, N), r(D - 1, 1, N)
+    wide = torch.zeros(D - 1, 1, D + 4, device=DEV)
+    wide[..., off:off + D] = u.to(DEV)
+    got = scr.selective_scan_backward(dy.to(DEV), wide[..., off:off + D],
+                                      torch.ones(D - 1, 1, D, device=DEV), -r(D, N).abs().to(DEV),
+                                      B.to(DEV), C.to(DEV), softplus=False)
+    u, dy, B, C = u.numpy(), dy.numpy(), B.numpy(), C.numpy()
+    for j in range(1, D):
+        two = [(dy[j - 1, 0, d], u[j - 1, 0, d]) for d in (0, j)]
+        b, c = B[j - 1, 0], C[j - 1, 0]
+        dB = [(c * y) * x for y, x in two]
+        dC = [y * (x * b) for y, x in two]
+        assert np.array_equal(got["B"][j - 1, 0].cpu().numpy(), dB[0] + dB[1]), j
+        assert np.array_equal(got["C"][j - 1, 0].cpu().numpy(), dC[0] + dC[1]), j
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_single_tokens(scr, dtype):
     """Single tokens after a prompt: within the roundings of the formula of
     the whole sequence."""
