@@ -240,31 +240,34 @@ def test_unaligned_rows_give_the_same_bits(scr, dtype, N):
 
 @pytest.mark.parametrize("N", [1, 4, 8, 16, 32, 64, 128])
 @pytest.mark.parametrize("off", [0, 1])
-def test_sums_over_channels_are_of_rounded_products(scr, N, off):
-    """One step of two channels, whichever two: dB and dC are the rounded sums of
-    two rounded products, to the bit. (Joined into one rounding they would depend
-    on how the compiler has arranged a variant of the kernel.)"""
-    D = 64
+@pytest.mark.parametrize("T", [1, 16])
+def test_sums_over_channels_are_of_rounded_products(scr, N, off, T):
+    """One step of two channels, whichever two, alone or the last of a whole tile:
+    dB and dC are the rounded sums of two rounded products, to the bit. (Joined
+    into one rounding they would depend on how the compiler has arranged a variant
+    of the kernel.)"""
+    D, last = 64, T - 1
     g = torch.Generator().manual_seed(27)
     r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
-    u, dy = torch.zeros(D - 1, 1, D), torch.zeros(D - 1, 1, D)
+    u, dy = torch.zeros(D - 1, T, D), torch.zeros(D - 1, T, D)
     for j in range(1, D):
         for v in (u, dy):
-            v[j - 1, 0, 0], v[j - 1, 0, j] = r(1), r(1)
-    B, C = r(D - 1, 1, N), r(D - 1, 1, N)
-    wide = torch.zeros(D - 1, 1, D + 4, device=DEV)
+            v[j - 1, last, 0], v[j - 1, last, j] = r(1), r(1)
+    B, C = r(D - 1, T, N), r(D - 1, T, N)
+    wide = torch.zeros(D - 1, T, D + 4, device=DEV)
     wide[..., off:off + D] = u.to(DEV)
     got = scr.selective_scan_backward(dy.to(DEV), wide[..., off:off + D],
-                                      torch.ones(D - 1, 1, D, device=DEV), -r(D, N).abs().to(DEV),
+                                      torch.ones(D - 1, T, D, device=DEV), -r(D, N).abs().to(DEV),
                                       B.to(DEV), C.to(DEV), softplus=False)
     u, dy, B, C = u.numpy(), dy.numpy(), B.numpy(), C.numpy()
     for j in range(1, D):
-        two = [(dy[j - 1, 0, d], u[j - 1, 0, d]) for d in (0, j)]
-        b, c = B[j - 1, 0], C[j - 1, 0]
+        two = [(dy[j - 1, last, d], u[j - 1, last, d]) for d in (0, j)]
+        b, c = B[j - 1, last], C[j - 1, last]
         dB = [(c * y) * x for y, x in two]
         dC = [y * (x * b) for y, x in two]
-        assert np.array_equal(got["B"][j - 1, 0].cpu().numpy(), dB[0] + dB[1]), j
-        assert np.array_equal(got["C"][j - 1, 0].cpu().numpy(), dC[0] + dC[1]), j
+        assert np.array_equal(got["B"][j - 1, last].cpu().numpy(), dB[0] + dB[1]), j
+        assert np.array_equal(got["C"][j - 1, last].cpu().numpy(), dC[0] + dC[1]), j
+    assert not got["B"][:, :last].any() and not got["C"][:, :last].any()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
