@@ -3,7 +3,7 @@
 //
 // Bound by latency at few warps: about 123 instructions a warp for a step of 8
 // channels, a third of them for the sums of dB and dC over channels, issued in
-// half of the cycles. 4 x 2048 steps of 2048 channels, 16 states, bf16: 434 us;
+// half of the cycles. 4 x 2048 steps of 2048 channels, 16 states, bf16: 442 us;
 // its 256 blocks are 1.7 an SM, of the two that the registers of 16 steps of
 // states allow.
 #include "cr_selective_scan.cuh"
@@ -89,11 +89,11 @@ struct ChannelSum {
 // first: it takes the tile's states forward from the checkpoint, holding all
 // of them in registers, then the adjoint states back, with the decays
 // computed again (holding them too spilled registers).
-// Two blocks an SM (239 registers); three spill and measured 609 us for 461.
+// Two blocks an SM (235 registers); three spill and measured 609 us for 461.
 // The last tile of a sequence that ends inside it has a copy of the adjoint
 // loop that leaves out the steps past the end: selects within one loop would be
 // 8 more instructions of some 250 for a pair of steps in every tile. (With the
-// copy: no change at 16 states, 2 % more at 4 and 8 states.)
+// copy: no change at 16 states, 2 % more at 8.)
 #ifndef CR_SCAN_BACK_BLOCKS
 #define CR_SCAN_BACK_BLOCKS 2
 #endif
