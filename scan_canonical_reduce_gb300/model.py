@@ -8,11 +8,11 @@ CPU path. The tensors are taken apart by a small native module
 microseconds on the device; the functions here name its arguments. Tensors
 are token-major, ``(batch, time, channel)``, of one type among float32,
 bfloat16 and float16; weights, scan states and sums are float32. Tensors
-whose last axis is not contiguous are copied first; any other strides are
-used as they are. ``stream`` is where the call runs (the current stream by
-default); copies, outputs and the call's workspace are made on it, so that a
-call may be captured into a CUDA graph (whose outputs and workspaces are then
-the graph's own) without another one before it.
+whose last axis is not contiguous are copied first, as is a table or its
+gradient whose rows overlap; any other strides are used as they are. ``stream``
+is where the call runs (the current stream by default); copies, outputs and
+the call's workspace are made on it: those of a captured call are the graph's
+own.
 
 Every result is one fixed expression of the inputs: repeated calls give the
 same bits.
