@@ -495,6 +495,133 @@ cr_status cr_selective_scan_step(const cr_selective_scan_args* args, float* stat
                                  int64_t state_rows, const void* slots, void* y,
                                  int64_t y_batch_stride, void* stream);
 
+/* Layer norm over the rows of x (batch x len of them, dim elements each):
+ *   y = (x - mean) * rstd * weight + bias,  mean = sum(x) / dim,
+ *   rstd = 1 / sqrt(sum((x - mean)^2) / dim + eps)
+ * The mean is kept in two binary32 numbers, so that a row whose mean is large
+ * beside its spread loses nothing. Sums of x and of squares have to fit
+ * binary32. */
+typedef struct {
+  int64_t batch, len, dim;
+  int32_t dt;             /* cr_dtype of x, y and dy                          */
+  float eps;              /* >= 0                                             */
+  const void* x;          /* of dt                                            */
+  int64_t x_batch_stride, x_time_stride;
+  const float* weight;    /* dim, or NULL: ones                               */
+  const float* bias;      /* dim, or NULL: zeros                              */
+} cr_layer_norm_args;
+
+/* Forward. y: of dt with its own strides. stats: NULL, or batch x len x 3
+ * floats for the backward call (the mean, what binary32 lacks of it, rstd). */
+cr_status cr_layer_norm(const cr_layer_norm_args* args, void* y, int64_t y_batch_stride,
+                        int64_t y_time_stride, float* stats, void* stream);
+
+/* Backward, for the same args: with g = dy * weight and n = (x - mean) * rstd
+ *   dx      = rstd * (g - sum(g) / dim - n * sum(g * n) / dim), of dt, strided
+ *   dweight = sum of dy * n over the rows, dim floats, or NULL
+ *   dbias   = sum of dy over the rows, dim floats, or NULL
+ * stats: from the forward call, or NULL: computed again. */
+typedef struct {
+  const void* dy;
+  int64_t dy_batch_stride, dy_time_stride;
+  const float* stats;
+  void* dx;
+  int64_t dx_batch_stride, dx_time_stride;
+  float* dweight;
+  float* dbias;
+} cr_layer_norm_grads;
+size_t cr_layer_norm_backward_workspace_bytes(int64_t batch, int64_t len, int64_t dim);
+cr_status cr_layer_norm_backward(const cr_layer_norm_args* args, const cr_layer_norm_grads* grads,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Gated linear recurrence: for each sequence and channel
+ *   a[t] = 1 / (1 + exp(-gate[t]))
+ *   h[t] = a[t] h[t-1] + (1 - a[t]) x[t],  h[-1] = state (zero without one)
+ *   y[t] = h[t] * z[t] / (1 + exp(-z[t]))  (h[t] without z)
+ * All arithmetic is binary32. */
+typedef struct {
+  int64_t batch, len, dim;
+  int32_t dt;             /* cr_dtype of x, gate, z, y and their gradients    */
+  int32_t index_bytes;    /* of lengths                                       */
+  const void* x;          /* batch x len x dim, of dt, strided                */
+  int64_t x_batch_stride, x_time_stride;
+  const void* gate;       /* like x                                           */
+  int64_t gate_batch_stride, gate_time_stride;
+  const void* z;          /* like x, or NULL                                  */
+  int64_t z_batch_stride, z_time_stride;
+  const float* state;     /* batch x dim, or NULL                             */
+  const void* lengths;    /* batch counts, or NULL                            */
+} cr_gated_scan_args;
+
+/* Number of checkpoints cr_gated_scan keeps for a sequence of len steps (a
+ * checkpoint: dim floats, the state before every so many steps). */
+int64_t cr_gated_scan_checkpoints(int64_t len);
+
+/* Forward. y: of dt, strided. final_state: NULL, or batch x dim floats.
+ * checkpoints: NULL, or batch x cr_gated_scan_checkpoints(len) x dim floats
+ * for the backward. */
+cr_status cr_gated_scan(const cr_gated_scan_args* args, void* y, int64_t y_batch_stride,
+                        int64_t y_time_stride, float* final_state, float* checkpoints,
+                        void* stream);
+
+/* Backward, for the same args. dy: the gradient of y. dfinal: that of
+ * final_state (batch x dim floats), or NULL. checkpoints: as written by the
+ * forward call. Outputs: dx, dgate, dz (NULL without z) batch x len x dim of
+ * dt, contiguous; dstate batch x dim floats, or NULL. */
+typedef struct {
+  const void* dy;
+  int64_t dy_batch_stride, dy_time_stride;
+  const float* dfinal;
+  const float* checkpoints;
+  void* dx;
+  void* dgate;
+  void* dz;
+  float* dstate;
+} cr_gated_scan_grads;
+cr_status cr_gated_scan_backward(const cr_gated_scan_args* args, const cr_gated_scan_grads* grads,
+                                 void* stream);
+
+/* One token for each of args->batch running streams (args->len is 1; the
+ * time strides, lengths and state of args are not used): state rows (dim
+ * floats) are updated in place. Slots as for cr_causal_conv_step. y: batch
+ * rows, y_batch_stride apart. */
+cr_status cr_gated_scan_step(const cr_gated_scan_args* args, float* state, int64_t state_rows,
+                             const void* slots, void* y, int64_t y_batch_stride, void* stream);
+
+/* The next token of each row of logits, from a uniform number u of that row.
+ * The row's tokens, in the order of falling logits, equal ones by rising
+ * index, have the weights w = exp((logit - largest) / temperature). Kept are
+ * the first of them, as many as all of these allow, and one at least:
+ *   top_k   the first top_k (0 or less: no limit)
+ *   top_p   those before which less than top_p times the weight of the first
+ *           top_k lies (1 or more, or NaN: no limit)
+ *   min_p   those with w >= min_p (0 or less, or NaN: no limit)
+ * The token is the first whose running sum of kept weights exceeds u times
+ * their sum. A temperature that is not above 0 takes the first token. u below
+ * 0 or NaN is taken as 0, u of 1 or more as 1 - 2^-24. A logit of -inf or NaN
+ * is no candidate; where one is +inf, those of +inf have w = 1, the others 0.
+ * A row without candidates gives -1.
+ * Weights are evaluated to 2^-35 of their value and summed as integers, in
+ * units of 2^-44 of the largest: the token is that of exact arithmetic unless u or top_p
+ * lies that near to a border. */
+typedef struct {
+  int64_t rows, vocab;    /* vocab <= 2^20 (more: CR_ERR_UNSUPPORTED)         */
+  int32_t dt;             /* cr_dtype of logits                               */
+  int32_t index_bytes;    /* of top_ks                                        */
+  const void* logits;     /* rows of vocab elements of dt                     */
+  int64_t row_stride;
+  const float* u;         /* rows                                             */
+  double temperature;     /* for every row, where its array below is NULL     */
+  double top_p;
+  double min_p;
+  int64_t top_k;
+  const float* temperatures; /* rows, or NULL                                 */
+  const float* top_ps;
+  const float* min_ps;
+  const void* top_ks;     /* rows of index_bytes, or NULL                     */
+} cr_sample_args;
+cr_status cr_sample(const cr_sample_args* args, int64_t* tokens, void* stream);
+
 /* ------------------------------------------------------------- utilities */
 
 /* Synchronises `stream`, then reports the device-side status of the most

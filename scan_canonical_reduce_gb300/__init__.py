@@ -105,6 +105,14 @@ SIGNATURES = {
     "cr_selective_scan_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
     "cr_selective_scan_backward": (_INT, [_P, _P, _P, _SZ, _P]),
     "cr_selective_scan_step": (_INT, [_P, _P, _I64, _P, _P, _I64, _P]),
+    "cr_layer_norm": (_INT, [_P, _P, _I64, _I64, _P, _P]),
+    "cr_layer_norm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "cr_layer_norm_backward": (_INT, [_P, _P, _P, _SZ, _P]),
+    "cr_gated_scan_checkpoints": (_I64, [_I64]),
+    "cr_gated_scan": (_INT, [_P, _P, _I64, _I64, _P, _P, _P]),
+    "cr_gated_scan_backward": (_INT, [_P, _P, _P]),
+    "cr_gated_scan_step": (_INT, [_P, _P, _I64, _P, _P, _I64, _P]),
+    "cr_sample": (_INT, [_P, _P, _P]),
 }
 
 
@@ -626,8 +634,9 @@ def measure_int_add_rate(device="cuda", stream=None) -> float:
 
 from . import model  # noqa: E402
 from .model import (causal_conv, causal_conv_backward, causal_conv_step,  # noqa: E402
-                    embedding, embedding_backward, selective_scan, selective_scan_backward,
-                    selective_scan_step)
+                    embedding, embedding_backward, gated_scan, gated_scan_backward,
+                    gated_scan_step, layer_norm, layer_norm_backward, sample, selective_scan,
+                    selective_scan_backward, selective_scan_step)
 
 __all__ = ["reduce", "reduce_batched", "reduce_policy", "inclusive_scan",
            "inclusive_scan_batched",
@@ -635,4 +644,5 @@ __all__ = ["reduce", "reduce_batched", "reduce_policy", "inclusive_scan",
            "scan_include_initial_batched", "MODES", "sync_status", "lib", "workspace", "launch_count", "profile_enable", "profile_collect", "measure_add_peak", "add_pairs_int", "measure_int_add_rate", "CrError", "POLICIES", "SIGNATURES",
            "embedding", "embedding_backward", "causal_conv", "causal_conv_backward",
            "causal_conv_step", "selective_scan", "selective_scan_backward",
-           "selective_scan_step"]
+           "selective_scan_step", "layer_norm", "layer_norm_backward", "gated_scan",
+           "gated_scan_backward", "gated_scan_step", "sample"]

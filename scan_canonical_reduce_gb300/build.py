@@ -28,9 +28,9 @@ BINDING_SRC = os.path.join(CSRC, "model_binding.cpp")
 BINDING = os.path.join(OUT_DIR, "cr_model_binding.so")
 BINDING_STAMP = BINDING + ".stamp"  # what it was built against
 SOURCES = ["cr_api.cu", "cr_calibrate.cu", "cr_chain.cu", "cr_conv.cu", "cr_embedding.cu",
-           "cr_host_batched.cu", "cr_launch.cu", "cr_noalloc.cu", "cr_reduce.cu",
-           "cr_reduce_policy.cu", "cr_scan.cu", "cr_selective_scan.cu",
-           "cr_selective_scan_backward.cu"]
+           "cr_gated_scan.cu", "cr_host_batched.cu", "cr_launch.cu", "cr_noalloc.cu",
+           "cr_norm.cu", "cr_reduce.cu", "cr_reduce_policy.cu", "cr_sample.cu", "cr_scan.cu",
+           "cr_selective_scan.cu", "cr_selective_scan_backward.cu"]
 HEADERS = ["cr_chain.h", "cr_chain_map.h", "cr_device.cuh", "cr_launch.h", "cr_model.cuh",
            "cr_plan.h", "cr_scan.h", "cr_selective_scan.cuh"]
 

@@ -82,7 +82,9 @@ const char* kernel_name(int id) {
       "causal_conv_backward_kernel", "causal_conv_sum_kernel", "causal_conv_step_kernel",
       "selective_scan_kernel", "selective_scan_states_kernel", "selective_scan_backward_kernel",
       "selective_scan_sum_kernel",
-      "selective_scan_step_kernel"};
+      "selective_scan_step_kernel", "layer_norm_kernel", "layer_norm_backward_kernel",
+      "layer_norm_sum_kernel", "gated_scan_kernel", "gated_scan_backward_kernel",
+      "gated_scan_step_kernel", "sample_kernel"};
   return (id >= 0 && id < kKernelCount) ? names[id] : "unknown";
 }
 

@@ -58,6 +58,13 @@ enum KernelId : int {
   kKSelectiveScanBackward,
   kKSelectiveScanSum,
   kKSelectiveScanStep,
+  kKLayerNorm,
+  kKLayerNormBackward,
+  kKLayerNormSum,
+  kKGatedScan,
+  kKGatedScanBackward,
+  kKGatedScanStep,
+  kKSample,
   kKernelCount
 };
 

@@ -59,6 +59,14 @@ decltype(&cr_selective_scan) f_selective_scan;
 decltype(&cr_selective_scan_backward_workspace_bytes) f_selective_scan_backward_workspace_bytes;
 decltype(&cr_selective_scan_backward) f_selective_scan_backward;
 decltype(&cr_selective_scan_step) f_selective_scan_step;
+decltype(&cr_layer_norm) f_layer_norm;
+decltype(&cr_layer_norm_backward_workspace_bytes) f_layer_norm_backward_workspace_bytes;
+decltype(&cr_layer_norm_backward) f_layer_norm_backward;
+decltype(&cr_gated_scan_checkpoints) f_gated_scan_checkpoints;
+decltype(&cr_gated_scan) f_gated_scan;
+decltype(&cr_gated_scan_backward) f_gated_scan_backward;
+decltype(&cr_gated_scan_step) f_gated_scan_step;
+decltype(&cr_sample) f_sample;
 
 void check(cr_status code, const char* name) {
   if (code == CR_OK) return;
@@ -655,6 +663,316 @@ PyObject* selective_scan_step(PyObject* const* a) {
   return wrap(y);
 }
 
+// ------------------------------------------------------------ layer norm
+// A tensor's rows (all axes but the last) as two axes with a stride each: up to
+// three axes as they are, more of them as one, copied where their strides ask
+// for it.
+struct RowAxes {
+  at::Tensor t;
+  int64_t batch, len, bs, ts;
+
+  explicit RowAxes(const at::Tensor& x) : t(x) {
+    if (x.dim() > 3) {
+      int64_t n = 1;
+      for (const int64_t v : x.sizes().slice(0, x.dim() - 1)) n *= v;
+      t = x.reshape({n, x.size(-1)});
+    }
+    batch = t.dim() == 3 ? t.size(0) : 1;
+    len = t.dim() >= 2 ? t.size(-2) : 1;
+    bs = t.dim() == 3 ? t.stride(0) : 0;
+    ts = t.dim() >= 2 ? t.stride(-2) : 0;
+  }
+};
+
+// What the forward and the backward call share: (x, weight, bias, eps) and the
+// stream.
+struct Norm {
+  const at::Tensor& x0;
+  int index;
+  On on;
+  RowAxes x;
+  Floats weight, bias;
+  std::vector<int64_t> stats_shape;
+  cr_layer_norm_args args;
+
+  static const at::Tensor& checked(PyObject* o) {
+    const at::Tensor& t = tensor(o, "x");
+    device_of(t, "x");
+    if (t.dim() < 1) bad_value("x must have a channel axis");
+    return t;
+  }
+
+  Norm(PyObject* const* a, PyObject* stream)
+      : x0(checked(a[0])), index(x0.get_device()), on(index, stream), x(rows(on, x0)) {
+    const cr_dtype code = type_code(x0);
+    const int64_t dim = x0.size(-1);
+    weight = floats(on, a[1], "weight", {dim});
+    bias = floats(on, a[2], "bias", {dim});
+    const float eps = real(a[3]);
+    if (!(eps >= 0.0f)) bad_value("eps must be >= 0");
+    stats_shape = x0.sizes().vec();
+    stats_shape.back() = 3;
+    args = {x.batch, x.len, dim, code, eps, x.t.data_ptr(), x.bs, x.ts, weight.p, bias.p};
+  }
+};
+
+// (x, weight, bias, eps, return_stats, out, stream)
+PyObject* layer_norm(PyObject* const* a) {
+  if (recorded(a, {0, 1, 2})) return not_implemented();
+  const Norm c(a, a[6]);
+  const bool return_stats = flag(a[4]);
+  const at::Tensor y = c.on.output(a[5], c.x0.sizes(), c.x0.scalar_type());
+  if (y.dim() > 3 && !y.is_contiguous()) bad_value("out with more than 3 axes must be contiguous");
+  const RowAxes o(y);
+  at::Tensor stats;
+  if (return_stats) stats = c.on.empty(c.stats_shape, at::kFloat);
+  check(f_layer_norm(&c.args, o.t.data_ptr(), o.bs, o.ts,
+                     return_stats ? static_cast<float*>(stats.data_ptr()) : nullptr, c.on.ptr),
+        "cr_layer_norm");
+  return return_stats ? Py_BuildValue("(NN)", wrap(y), wrap(stats)) : wrap(y);
+}
+
+// (x, weight, bias, eps, dy, stats, stream)
+PyObject* layer_norm_backward(PyObject* const* a) {
+  const Norm c(a, a[6]);
+  const at::ScalarType type = c.x0.scalar_type();
+  const at::Tensor& dy0 = tensor(a[4], "dy");
+  need(dy0, "dy", c.x0.sizes(), type, c.index);
+  const RowAxes dy(rows(c.on, dy0));
+  const Floats stats = floats(c.on, a[5], "stats", c.stats_shape);
+  const at::Tensor dx = c.on.empty(c.x0.sizes(), type);
+  const RowAxes o(dx);
+  at::Tensor dw, db;
+  if (c.weight.t.defined()) dw = c.on.empty({c.args.dim}, at::kFloat);
+  if (c.bias.t.defined()) db = c.on.empty({c.args.dim}, at::kFloat);
+  const at::Tensor ws = c.on.workspace(
+      f_layer_norm_backward_workspace_bytes(c.args.batch, c.args.len, c.args.dim),
+      "layer_norm_backward");
+  const cr_layer_norm_grads g = {dy.t.data_ptr(),
+                                 dy.bs,
+                                 dy.ts,
+                                 stats.p,
+                                 o.t.data_ptr(),
+                                 o.bs,
+                                 o.ts,
+                                 dw.defined() ? static_cast<float*>(dw.data_ptr()) : nullptr,
+                                 db.defined() ? static_cast<float*>(db.data_ptr()) : nullptr};
+  check(f_layer_norm_backward(&c.args, &g, ws.data_ptr(), ws.numel(), c.on.ptr),
+        "cr_layer_norm_backward");
+  PyObject* r = PyDict_New();
+  if (r == nullptr) throw Error{nullptr, ""};
+  put(r, "x", dx);
+  if (dw.defined()) put(r, "weight", dw);
+  if (db.defined()) put(r, "bias", db);
+  return r;
+}
+
+// ------------------------------------------------------------ gated scan
+// What the calls share: (x, gate, z), a state (None for a step), lengths or
+// slots, and the stream.
+struct Gated {
+  const at::Tensor& x0;
+  int index;
+  On on;
+  at::Tensor x, gate, z;
+  Floats state;
+  Indices lengths;
+  cr_gated_scan_args args;
+
+  static const at::Tensor& checked(PyObject* o, bool step) {
+    const at::Tensor& t = tensor(o, "x");
+    device_of(t, "x");
+    if (t.dim() != (step ? 2 : 3))
+      bad_value(step ? "x must be (batch, dim)" : "x must be (batch, time, dim)");
+    return t;
+  }
+
+  Gated(PyObject* const* a, PyObject* state0, PyObject* lengths0, PyObject* stream, bool step)
+      : x0(checked(a[0], step)), index(x0.get_device()), on(index, stream) {
+    const cr_dtype code = type_code(x0);
+    const int64_t batch = x0.size(0), len = step ? 1 : x0.size(1), dim = x0.size(-1);
+    auto like_x = [&](PyObject* o, const char* name) {
+      const at::Tensor& t = tensor(o, name);
+      need(t, name, x0.sizes(), x0.scalar_type(), index);
+      return rows(on, t);
+    };
+    x = rows(on, x0);
+    gate = like_x(a[1], "gate");
+    if (a[2] != Py_None) z = like_x(a[2], "z");
+    if (state0 != Py_None) state = floats(on, state0, "state", {batch, dim});
+    lengths = indices(on, lengths0, step ? "slots" : "lengths", at::IntArrayRef({batch}));
+    const int64_t t = step ? 0 : 1;
+    args = {batch,
+            len,
+            dim,
+            code,
+            lengths.bytes,
+            x.data_ptr(),
+            x.stride(0),
+            x.stride(t),
+            gate.data_ptr(),
+            gate.stride(0),
+            gate.stride(t),
+            z.defined() ? z.data_ptr() : nullptr,
+            z.defined() ? z.stride(0) : 0,
+            z.defined() ? z.stride(t) : 0,
+            state.p,
+            step ? nullptr : lengths.p};
+  }
+};
+
+// (x, gate, z, state, lengths, return_state, return_checkpoints, out, stream)
+PyObject* gated_scan(PyObject* const* a) {
+  if (recorded(a, {0, 1, 2, 3})) return not_implemented();
+  const Gated s(a, a[3], a[4], a[8], false);
+  const bool return_state = flag(a[5]), return_checkpoints = flag(a[6]);
+  const int64_t batch = s.args.batch, dim = s.args.dim;
+  const at::Tensor y = s.on.output(a[7], s.x0.sizes(), s.x0.scalar_type());
+  at::Tensor final, kept;
+  if (return_state) final = s.on.empty({batch, dim}, at::kFloat);
+  if (return_checkpoints)
+    kept = s.on.empty({batch, f_gated_scan_checkpoints(s.args.len), dim}, at::kFloat);
+  check(f_gated_scan(&s.args, y.data_ptr(), y.stride(0), y.stride(1),
+                     return_state ? static_cast<float*>(final.data_ptr()) : nullptr,
+                     return_checkpoints ? static_cast<float*>(kept.data_ptr()) : nullptr,
+                     s.on.ptr),
+        "cr_gated_scan");
+  if (return_state && return_checkpoints)
+    return Py_BuildValue("(NNN)", wrap(y), wrap(final), wrap(kept));
+  if (return_state) return Py_BuildValue("(NN)", wrap(y), wrap(final));
+  if (return_checkpoints) return Py_BuildValue("(NN)", wrap(y), wrap(kept));
+  return wrap(y);
+}
+
+// (x, gate, z, state, lengths, dy, dfinal, checkpoints, stream)
+PyObject* gated_scan_backward(PyObject* const* a) {
+  const Gated s(a, a[3], a[4], a[8], false);
+  const int64_t batch = s.args.batch, dim = s.args.dim;
+  const at::ScalarType type = s.x0.scalar_type();
+  const at::Tensor& dy0 = tensor(a[5], "dy");
+  need(dy0, "dy", s.x0.sizes(), type, s.index);
+  const at::Tensor dy = rows(s.on, dy0);
+  const Floats dfinal = floats(s.on, a[6], "dfinal", {batch, dim});
+  const at::Tensor& kept = tensor(a[7], "checkpoints");
+  need(kept, "checkpoints", {batch, f_gated_scan_checkpoints(s.args.len), dim}, at::kFloat,
+       s.index);
+  if (!kept.is_contiguous())
+    bad_value("checkpoints must be contiguous, as the forward call returns them");
+  at::Tensor dz, ds;
+  const at::Tensor dx = s.on.empty(s.x0.sizes(), type), dgate = s.on.empty(s.x0.sizes(), type);
+  if (s.z.defined()) dz = s.on.empty(s.x0.sizes(), type);
+  if (s.state.t.defined()) ds = s.on.empty({batch, dim}, at::kFloat);
+  s.on.uses(kept);
+  const cr_gated_scan_grads g = {dy.data_ptr(),
+                                 dy.stride(0),
+                                 dy.stride(1),
+                                 dfinal.p,
+                                 static_cast<const float*>(kept.data_ptr()),
+                                 dx.data_ptr(),
+                                 dgate.data_ptr(),
+                                 dz.defined() ? dz.data_ptr() : nullptr,
+                                 ds.defined() ? static_cast<float*>(ds.data_ptr()) : nullptr};
+  check(f_gated_scan_backward(&s.args, &g, s.on.ptr), "cr_gated_scan_backward");
+  PyObject* r = PyDict_New();
+  if (r == nullptr) throw Error{nullptr, ""};
+  put(r, "x", dx);
+  put(r, "gate", dgate);
+  if (dz.defined()) put(r, "z", dz);
+  if (ds.defined()) put(r, "state", ds);
+  return r;
+}
+
+// (x, gate, state, z, slots, out, stream)
+PyObject* gated_scan_step(PyObject* const* a) {
+  PyObject* const main[] = {a[0], a[1], a[3]};
+  const Gated s(main, Py_None, a[4], a[6], true);
+  const at::Tensor& state = tensor(a[2], "state");
+  if (state.dim() != 2) bad_value("state must be (rows, dim)");
+  need(state, "state", {state.size(0), s.args.dim}, at::kFloat, s.index);
+  if (!state.is_contiguous()) bad_value("state must be contiguous (it is updated in place)");
+  if (a[4] == Py_None && state.size(0) < s.args.batch)
+    bad_value(join("state must have a row for each of the ", s.args.batch, " streams"));
+  s.on.writes(state);
+  const at::Tensor y = s.on.output(a[5], s.x0.sizes(), s.x0.scalar_type());
+  check(f_gated_scan_step(&s.args, static_cast<float*>(state.data_ptr()), state.size(0),
+                          s.lengths.p, y.data_ptr(), y.stride(0), s.on.ptr),
+        "cr_gated_scan_step");
+  return wrap(y);
+}
+
+// -------------------------------------------------------------- sampling
+// A setting: a number for every row, or a tensor with one a row.
+struct Setting {
+  double value;
+  Floats each;
+};
+
+Setting setting(const On& on, PyObject* o, const char* name, at::IntArrayRef shape, double none) {
+  Setting r{none, {}};
+  if (o == Py_None) return r;
+  if (THPVariable_Check(o)) {
+    r.each = floats(on, o, name, shape);
+    return r;
+  }
+  r.value = PyFloat_AsDouble(o);
+  if (r.value == -1.0 && PyErr_Occurred()) throw Error{nullptr, ""};
+  return r;
+}
+
+// (logits, u, temperature, top_k, top_p, min_p, out, stream)
+PyObject* sample(PyObject* const* a) {
+  const at::Tensor& x0 = tensor(a[0], "logits");
+  const int index = device_of(x0, "logits");
+  if (x0.dim() < 1) bad_value("logits must be (..., vocab)");
+  const cr_dtype code = type_code(x0);
+  const On on(index, a[7]);
+  const at::IntArrayRef shape = x0.sizes().slice(0, x0.dim() - 1);
+  if (a[1] == Py_None) bad_type("u must be a tensor");
+  const Floats u = floats(on, a[1], "u", shape);
+  const Setting temperature = setting(on, a[2], "temperature", shape, 1.0);
+  const Setting top_p = setting(on, a[4], "top_p", shape, 1.0);
+  const Setting min_p = setting(on, a[5], "min_p", shape, 0.0);
+  if (!(temperature.value >= 0.0)) bad_value("temperature must be >= 0");
+  if (!(top_p.value >= 0.0)) bad_value("top_p must be >= 0");
+  if (!(min_p.value >= 0.0 && min_p.value <= 1.0)) bad_value("min_p must be in [0, 1]");
+  Indices ks;
+  int64_t top_k = 0;
+  if (a[3] != Py_None) {
+    if (THPVariable_Check(a[3])) ks = indices(on, a[3], "top_k", shape);
+    else top_k = integer(a[3]);
+  }
+  if (top_k < 0) bad_value("top_k must be >= 0");
+  at::Tensor x = rows(on, x0);
+  if (x.dim() != 2) x = x.reshape({u.t.numel(), x0.size(-1)});
+  at::Tensor out;
+  if (a[6] == Py_None) {
+    out = on.empty(shape, at::kLong);
+  } else {
+    out = tensor(a[6], "out");
+    need(out, "out", shape, at::kLong, index);
+    if (!out.is_contiguous()) bad_value("out must be contiguous");
+    on.writes(out);
+  }
+  const int64_t n = x.size(0), vocab = x.size(1);
+  const cr_sample_args args = {n,
+                               vocab,
+                               code,
+                               ks.bytes,
+                               x.data_ptr(),
+                               n > 1 ? x.stride(0) : vocab,
+                               u.p,
+                               temperature.value,
+                               top_p.value,
+                               min_p.value,
+                               top_k,
+                               temperature.each.p,
+                               top_p.each.p,
+                               min_p.each.p,
+                               ks.p};
+  check(f_sample(&args, static_cast<int64_t*>(out.data_ptr()), on.ptr), "cr_sample");
+  return wrap(out);
+}
+
 // ---------------------------------------------------------------- module
 // One entry: the number of arguments, and every C++ exception turned into a
 // Python one.
@@ -715,6 +1033,14 @@ PyObject* bind(PyObject*, PyObject* args) {
   CR_BIND(selective_scan_backward_workspace_bytes);
   CR_BIND(selective_scan_backward);
   CR_BIND(selective_scan_step);
+  CR_BIND(layer_norm);
+  CR_BIND(layer_norm_backward_workspace_bytes);
+  CR_BIND(layer_norm_backward);
+  CR_BIND(gated_scan_checkpoints);
+  CR_BIND(gated_scan);
+  CR_BIND(gated_scan_backward);
+  CR_BIND(gated_scan_step);
+  CR_BIND(sample);
 #undef CR_BIND
   if (!ok) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "a libcr function is missing");
@@ -738,6 +1064,12 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                          CR_ENTRY(selective_scan, 15),
                          CR_ENTRY(selective_scan_backward, 15),
                          CR_ENTRY(selective_scan_step, 13),
+                         CR_ENTRY(layer_norm, 7),
+                         CR_ENTRY(layer_norm_backward, 7),
+                         CR_ENTRY(gated_scan, 9),
+                         CR_ENTRY(gated_scan_backward, 9),
+                         CR_ENTRY(gated_scan_step, 7),
+                         CR_ENTRY(sample, 8),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "cr_model_binding", nullptr, -1, methods,

@@ -1,6 +1,7 @@
-"""Model operators of libcr: embedding lookup, short causal convolution and
-selective state space scan, each with its gradient and, for the last two, its
-form for single tokens (the token path of a recurrent language model).
+"""Model operators of libcr: embedding lookup, layer norm, short causal
+convolution, selective state space scan and gated scan, each with its gradient
+and, for the last three, its form for single tokens, and sampling of the next
+token (the token path of a recurrent language model).
 
 Everything is computed in libcr's kernels (``include/cr.h``) and there is no
 CPU path. The tensors are taken apart by a small native module
@@ -17,10 +18,10 @@ own.
 Every result is one fixed expression of the inputs: repeated calls give the
 same bits.
 
-``embedding``, ``causal_conv`` and ``selective_scan`` are differentiable: where
-autograd records, their results' gradients are those of the ``*_backward``
-calls, which may also be called directly. Those and the single-token calls
-are never recorded.
+``embedding``, ``layer_norm``, ``causal_conv``, ``selective_scan`` and
+``gated_scan`` are differentiable: where autograd records, their results'
+gradients are those of the ``*_backward`` calls, which may also be called
+directly. Those, the single-token calls and ``sample`` are never recorded.
 """
 from __future__ import annotations
 
@@ -74,6 +75,45 @@ class _ScanGrads(ctypes.Structure):
                 ("dA", _P), ("dD", _P), ("ddt_bias", _P), ("dstate", _P)]
 
 
+class _NormArgs(ctypes.Structure):
+    """cr_layer_norm_args"""
+    _fields_ = [("batch", _I64), ("len", _I64), ("dim", _I64), ("dt", _I32),
+                ("eps", ctypes.c_float), ("x", _P), ("x_batch_stride", _I64),
+                ("x_time_stride", _I64), ("weight", _P), ("bias", _P)]
+
+
+class _NormGrads(ctypes.Structure):
+    """cr_layer_norm_grads"""
+    _fields_ = [("dy", _P), ("dy_batch_stride", _I64), ("dy_time_stride", _I64), ("stats", _P),
+                ("dx", _P), ("dx_batch_stride", _I64), ("dx_time_stride", _I64),
+                ("dweight", _P), ("dbias", _P)]
+
+
+class _GateArgs(ctypes.Structure):
+    """cr_gated_scan_args"""
+    _fields_ = [("batch", _I64), ("len", _I64), ("dim", _I64), ("dt", _I32),
+                ("index_bytes", _I32),
+                ("x", _P), ("x_batch_stride", _I64), ("x_time_stride", _I64),
+                ("gate", _P), ("gate_batch_stride", _I64), ("gate_time_stride", _I64),
+                ("z", _P), ("z_batch_stride", _I64), ("z_time_stride", _I64),
+                ("state", _P), ("lengths", _P)]
+
+
+class _GateGrads(ctypes.Structure):
+    """cr_gated_scan_grads"""
+    _fields_ = [("dy", _P), ("dy_batch_stride", _I64), ("dy_time_stride", _I64), ("dfinal", _P),
+                ("checkpoints", _P), ("dx", _P), ("dgate", _P), ("dz", _P), ("dstate", _P)]
+
+
+class _SampleArgs(ctypes.Structure):
+    """cr_sample_args"""
+    _fields_ = [("rows", _I64), ("vocab", _I64), ("dt", _I32), ("index_bytes", _I32),
+                ("logits", _P), ("row_stride", _I64), ("u", _P),
+                ("temperature", ctypes.c_double), ("top_p", ctypes.c_double),
+                ("min_p", ctypes.c_double), ("top_k", _I64), ("temperatures", _P),
+                ("top_ps", _P), ("min_ps", _P), ("top_ks", _P)]
+
+
 _lock = threading.Lock()
 
 
@@ -104,8 +144,9 @@ def _load():
     spec = importlib.util.spec_from_file_location("cr_model_binding", BINDING_PATH, loader=loader)
     module = importlib.util.module_from_spec(spec)
     loader.exec_module(module)
-    names = [n for n in SIGNATURES if n.startswith(("cr_embedding", "cr_causal_conv",
-                                                   "cr_selective_scan"))]
+    names = [n for n in SIGNATURES if n.startswith((
+        "cr_embedding", "cr_causal_conv", "cr_selective_scan", "cr_layer_norm", "cr_gated_scan",
+        "cr_sample"))]
     module.bind({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names}, _check)
     return module
 
@@ -197,6 +238,51 @@ class _SelectiveScan(torch.autograd.Function):
             more[0] if return_state else None, kept, s))
         return (*(g.get(k) for k in ("u", "dt", "A", "B", "C", "D", "z", "dt_bias", "state")),
                 None, None, None, None, None)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, return_stats, stream):
+        y, stats = _native.layer_norm(x, weight, bias, eps, True, None, stream)
+        ctx.mark_non_differentiable(stats)
+        ctx.save_for_backward(x, weight, bias, stats)
+        ctx.rest = eps, stream
+        ctx.set_materialize_grads(False)
+        return (y, stats) if return_stats else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dstats=None):
+        if dy is None:
+            return (None,) * 6
+        x, weight, bias, stats = ctx.saved_tensors
+        eps, stream = ctx.rest
+        g = _backward_on(stream, lambda s: layer_norm_backward(dy, x, weight, bias, eps, stats, s))
+        return g["x"], g.get("weight"), g.get("bias"), None, None, None
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, z, state, lengths, return_state, return_checkpoints, stream):
+        out = _native.gated_scan(x, gate, z, state, lengths, return_state, True, None, stream)
+        kept = out[-1]
+        ctx.mark_non_differentiable(kept)
+        ctx.save_for_backward(x, gate, z, state, lengths, kept)
+        ctx.rest = return_state, stream
+        ctx.set_materialize_grads(False)
+        if return_checkpoints:
+            return out
+        return out[:-1] if return_state else out[0]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, *more):
+        x, gate, z, state, lengths, kept = ctx.saved_tensors
+        return_state, stream = ctx.rest
+        dy = torch.zeros_like(x) if dy is None else dy
+        g = _backward_on(stream, lambda s: gated_scan_backward(
+            dy, x, gate, z, state, lengths, more[0] if return_state else None, kept, s))
+        return (*(g.get(k) for k in ("x", "gate", "z", "state")), None, None, None, None)
 
 
 # ------------------------------------------------------------ embedding
@@ -327,6 +413,103 @@ def selective_scan_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
                                        stream)
 
 
-__all__ = ["embedding", "embedding_backward", "causal_conv", "causal_conv_backward",
+# ---------------------------------------------------------- layer norm
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, eps: float = 1e-5, return_stats: bool = False,
+               out: torch.Tensor | None = None, stream=None):
+    """``(x - mean) / sqrt(var + eps) * weight + bias`` over the last axis of x
+    (any leading axes); weight and bias (dim), float32, each optional. Returns
+    y, or (y, stats) with ``return_stats``: what the backward call takes of each
+    row, (..., 3) float32."""
+    y = _native.layer_norm(x, weight, bias, eps, return_stats, out, stream)
+    if y is NotImplemented:
+        _no_out(out)
+        return _LayerNorm.apply(x, weight, bias, eps, return_stats, stream)
+    return y
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None,
+                        bias: torch.Tensor | None = None, eps: float = 1e-5,
+                        stats: torch.Tensor | None = None, stream=None) -> dict:
+    """The gradients of :func:`layer_norm` for the same arguments: a dict with
+    "x", and "weight" and "bias" where those were given. ``stats``: from the
+    forward call (computed again without them)."""
+    return _native.layer_norm_backward(x, weight, bias, eps, dy, stats, stream)
+
+
+# ---------------------------------------------------------- gated scan
+def gated_scan(x: torch.Tensor, gate: torch.Tensor, z: torch.Tensor | None = None,
+               state: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+               return_state: bool = False, return_checkpoints: bool = False,
+               out: torch.Tensor | None = None, stream=None):
+    """Gated linear recurrence over time, per channel:
+
+        a[t] = sigmoid(gate[t])
+        h[t] = a[t] h[t-1] + (1 - a[t]) x[t]
+        y[t] = h[t] * silu(z[t])
+
+    x, gate, z (batch, time, dim), z optional; ``state`` (batch, dim), float32:
+    h before time 0 (zeros without it). ``lengths`` (batch): later positions are
+    not read, give zeros and leave the state. Returns y, followed by the last
+    state (``return_state``) and the checkpoints that the backward call takes
+    (``return_checkpoints``)."""
+    y = _native.gated_scan(x, gate, z, state, lengths, return_state, return_checkpoints, out,
+                           stream)
+    if y is NotImplemented:
+        _no_out(out)
+        return _GatedScan.apply(x, gate, z, state, lengths, return_state, return_checkpoints,
+                                stream)
+    return y
+
+
+def gated_scan_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
+                        z: torch.Tensor | None = None, state: torch.Tensor | None = None,
+                        lengths: torch.Tensor | None = None,
+                        dfinal: torch.Tensor | None = None,
+                        checkpoints: torch.Tensor | None = None, stream=None) -> dict:
+    """The gradients of :func:`gated_scan` for the same arguments: a dict with
+    "x" and "gate", and "z" and "state" where those were given. ``dfinal``: the
+    gradient of the returned state, if it was used. ``checkpoints``: from the
+    forward call (computed again without them)."""
+    if checkpoints is None:
+        with torch.no_grad():
+            checkpoints = gated_scan(x, gate, None, state, lengths, return_checkpoints=True,
+                                     stream=stream)[1]
+    return _native.gated_scan_backward(x, gate, z, state, lengths, dy, dfinal, checkpoints, stream)
+
+
+def gated_scan_step(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor,
+                    z: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token of each of ``batch`` running streams: x, gate, z (batch, dim).
+    ``state`` (rows, dim), float32, contiguous, is updated in place; stream b
+    uses row ``slots[b]`` (b without slots); a slot outside [0, rows) is padding
+    (zeros, no state changes). Slots must differ. Returns y (batch, dim)."""
+    return _native.gated_scan_step(x, gate, state, z, slots, out, stream)
+
+
+# ------------------------------------------------------------ sampling
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The next token of each row of logits (..., vocab), int64, from the uniform
+    numbers u (...), float32 in [0, 1).
+
+    A row's tokens, in the order of falling logits (equal ones by index), have
+    the weights ``w = exp((logit - largest) / temperature)``. Kept are the first
+    ``top_k`` (0: all); of these, those before which less than ``top_p`` of
+    their weight lies; and of these, those with ``w >= min_p``; the first in any
+    case. The token is the first whose running sum of kept weights exceeds u
+    times their sum. A temperature of 0 takes the first. A logit of -inf or NaN
+    is no candidate; a row without candidates gives -1, which
+    :func:`embedding` takes as padding.
+
+    Each setting is a number, or a tensor (...) with one a row: float32, and
+    int32 or int64 for top_k. The result is that of exact arithmetic (weights to
+    2^-35, sums in integers) and never differentiated."""
+    return _native.sample(logits, u, temperature, top_k, top_p, min_p, out, stream)
+
+
+__all__ = ["layer_norm", "layer_norm_backward", "gated_scan", "gated_scan_backward",
+           "gated_scan_step", "sample", "embedding", "embedding_backward", "causal_conv", "causal_conv_backward",
            "causal_conv_step", "selective_scan", "selective_scan_backward",
            "selective_scan_step"]
