@@ -5,13 +5,13 @@
 //   G[t] = dy[t] silu(z[t]) + a[t+1] G[t+1]
 //   dx = r G,  dgate = (h[t-1] - x) G a r,  dz = dy h silu'(z)
 //
-// What is kept of a gate is the smaller of a and r, with the gate's sign. Where
-// a memory is long, a is near 1 and has few digits of r left: a step that
-// multiplied by it would forget at a rate that is off by 2^-25 / r. So
-//   gate >= 0:  h + r (x - h),  a G = G - r G
-//   gate < 0:   x + a (h - x),  a G = a G.
+// The state goes by r alone: where a memory is long, a is near 1 and binary32
+// keeps few digits of r in it (a product by a would forget at a rate that is
+// off by 2^-25 / r). So a h is h - r h, one rounding, exact for r = 0 and 1.
 #include <algorithm>
 #include <cstdint>
+
+#include <cstddef>
 
 #include <cooperative_groups.h>
 
@@ -39,47 +39,133 @@ struct GateIn {
   int32_t index_bytes;
 };
 
-// The smaller of a and r, negative where that is a.
-__device__ __forceinline__ float gate_coef(float g) {
-  const float e = exp2_fast(fabsf(g) * -kLog2e);
-  return copysignf(e * reciprocal(1.0f + e), g);
+// C values that are worked on at once.
+template <int C>
+struct Vec;
+template <>
+struct Vec<1> {
+  float v;
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ explicit Vec(float f) : v(f) {}
+  __device__ __forceinline__ float get(int) const { return v; }
+  __device__ __forceinline__ void set(int, float f) { v = f; }
+};
+template <>
+struct Vec<2> {
+  F2 v;
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ explicit Vec(float f) : v(pack2(f, f)) {}
+  __device__ __forceinline__ Vec(float lo, float hi) : v(pack2(lo, hi)) {}
+  __device__ __forceinline__ float get(int k) const {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return k ? hi : lo;
+  }
+  __device__ __forceinline__ void set(int k, float f) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    v = k ? pack2(lo, f) : pack2(f, hi);
+  }
+};
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) {
+  return Vec<1>(fmaf(a.v, b.v, c.v));
 }
-__device__ __forceinline__ bool holds(float c) { return __float_as_int(c) >= 0; }
-__device__ __forceinline__ float gate_step(float c, float h, float x) {
-  return fmaf(c, x - h, holds(c) ? h : x);
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return Vec<1>(a.v * b.v); }
+// not of a product (see add2)
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return Vec<1>(a.v + b.v); }
+__device__ __forceinline__ Vec<1> exp2_of(Vec<1> a) { return Vec<1>(exp2_fast(a.v)); }
+__device__ __forceinline__ Vec<1> reciprocal_of(Vec<1> a) { return Vec<1>(reciprocal(a.v)); }
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+  Vec<2> r;
+  r.v = fma2(a.v, b.v, c.v);
+  return r;
 }
-__device__ __forceinline__ float keep(float c) { return (holds(c) ? 1.0f : 0.0f) - c; }  // a
-__device__ __forceinline__ float take(float c) { return holds(c) ? c : 1.0f + c; }  // r
-__device__ __forceinline__ float forget(float c, float G) {  // a G
-  return holds(c) ? fmaf(-c, G, G) : -c * G;
+__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  r.v = mul2(a.v, b.v);
+  return r;
+}
+__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  r.v = add2(a.v, b.v);
+  return r;
+}
+__device__ __forceinline__ Vec<2> exp2_of(Vec<2> a) {
+  return Vec<2>(exp2_fast(a.get(0)), exp2_fast(a.get(1)));
+}
+__device__ __forceinline__ Vec<2> reciprocal_of(Vec<2> a) {
+  return Vec<2>(reciprocal(a.get(0)), reciprocal(a.get(1)));
+}
+
+// -1 / (1 + exp2(v s)), s = log2(e) or its negative. The product's rounding is
+// |v| / 2 roundings of the result.
+template <int C>
+__device__ __forceinline__ Vec<C> minus_sigmoid(Vec<C> v, float s, Vec<C>* e_out = nullptr) {
+  const Vec<C> e = exp2_of(mul(v, Vec<C>(s)));
+  if (e_out != nullptr) *e_out = e;
+  return reciprocal_of(fma(e, Vec<C>(-1.0f), Vec<C>(-1.0f)));
+}
+
+// A step for r: p - r p, and with what is added.
+template <int C>
+__device__ __forceinline__ Vec<C> decay(Vec<C> minus_r, Vec<C> p) {
+  return fma(minus_r, p, p);
 }
 
 // What a run of steps does to the state: h -> L + P h. Where P is near 1 its
 // digits are in Q = 1 - P, where it is near 0 in P: kept is Q, or -P from 1 -
 // 2^-7 on (below that, P's error is 2^-17 of itself at most).
-__device__ __forceinline__ float map_keep(float Q, float P) {
-  return Q <= 1.0f - 0x1p-7f ? Q : -P;
+template <int C>
+struct alignas(8 * C) Map {
+  float L[C], F[C];
+  __device__ __forceinline__ void apply(float (&h)[C]) const {
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const float v = fmaf(-F[k], h[k], L[k]);
+      h[k] = __float_as_int(F[k]) >= 0 ? v + h[k] : v;
+    }
+  }
+};
+template <int C>
+__device__ __forceinline__ Map<C> run_map(Vec<C> L, Vec<C> minus_Q, Vec<C> P) {
+  Map<C> m;
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    m.L[k] = L.get(k);
+    // (fabsf: the zero of a run that holds the state is not negative)
+    m.F[k] = minus_Q.get(k) >= 0x1p-7f - 1.0f ? fabsf(minus_Q.get(k)) : -P.get(k);
+  }
+  return m;
 }
-__device__ __forceinline__ float map_apply(float L, float F, float h) {
-  const float v = fmaf(-F, h, L);
-  return __float_as_int(F) >= 0 ? v + h : v;
-}
-// The map L, F after the map l, f: both as (L, F).
-__device__ __forceinline__ void map_join(float& L, float& F, float l, float f) {
-  const bool n0 = __float_as_int(F) >= 0, n1 = __float_as_int(f) >= 0;
-  const float P0 = n0 ? 1.0f - F : -F, P1 = n1 ? 1.0f - f : -f;
-  const float Q0 = n0 ? F : 1.0f + F, Q1 = n1 ? f : 1.0f + f;
-  L = map_apply(l, f, L);
-  F = map_keep(fmaf(Q1, P0, Q0), P0 * P1);
+// The map b after the map a.
+template <int C>
+__device__ __forceinline__ Map<C> map_join(const Map<C>& a, const Map<C>& b) {
+  Vec<C> L, q, p;
+  float l[C];
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    const bool na = __float_as_int(a.F[k]) >= 0, nb = __float_as_int(b.F[k]) >= 0;
+    const float Pa = na ? 1.0f - a.F[k] : -a.F[k], Pb = nb ? 1.0f - b.F[k] : -b.F[k];
+    const float qa = na ? -a.F[k] : -a.F[k] - 1.0f, qb = nb ? -b.F[k] : -b.F[k] - 1.0f;  // P - 1
+    q.set(k, fmaf(qb, Pa, qa));
+    p.set(k, Pa * Pb);
+    l[k] = a.L[k];
+  }
+  b.apply(l);
+#pragma unroll
+  for (int k = 0; k < C; ++k) L.set(k, l[k]);
+  return run_map(L, q, p);
 }
 
 // A tile: 8 warps, each a run of kRun steps, a lane 32 bits of each step: one
-// channel of binary32, two of 16 bits: neighbours (kWide), or 32 apart where
-// rows start anywhere.
+// channel of binary32, two neighbours of 16 bits, which come by way of shared
+// memory, 16 bytes an access, a tile ahead of their use (kWide: rows on 16
+// bytes). Otherwise a lane reads its channels one by one, two of 16 bits 32
+// apart.
 constexpr int kRun = kGateCheckpoint;
 constexpr int kGateWarps = 8;
 constexpr int kTileSteps = kRun * kGateWarps;
-constexpr int kMostCluster = 16;
+constexpr int kMostCluster = 8;
 
 template <class T>
 struct Lane {
@@ -92,35 +178,121 @@ struct Word {
   static __device__ __forceinline__ uint32_t load(const T* p, int have) {
     if constexpr (sizeof(T) == 4) {
       return have > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
-    } else if constexpr (kWide) {
-      return have > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
     } else {
+      static_assert(!kWide, "by way of shared memory");
       const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
       const uint32_t lo = have > 0 ? __ldg(q) : 0u, hi = have > 1 ? __ldg(q + 32) : 0u;
       return lo | hi << 16;
     }
   }
-  static __device__ __forceinline__ float get(uint32_t w, int k) {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+  static __device__ __forceinline__ Vec<C> get(uint32_t w) {
+    if constexpr (sizeof(T) == 4) return Vec<C>(__uint_as_float(w));
     else if constexpr (std::is_same<T, __nv_bfloat16>::value)
-      return __uint_as_float(k ? w & 0xFFFF0000u : w << 16);
-    else
-      return __half2float(__ushort_as_half((unsigned short)(k ? w >> 16 : w & 0xFFFFu)));
-  }
-  static __device__ __forceinline__ void store(T* p, int have, const float (&f)[C]) {
-    if constexpr (sizeof(T) == 4) {
-      if (have > 0) *p = f[0];
-    } else if constexpr (kWide) {
-      if (have > 0) {
-        Pack<T, 2> q;
-        q.v[0] = from_f32<T>(f[0]);
-        q.v[1] = from_f32<T>(f[1]);
-        *reinterpret_cast<Pack<T, 2>*>(p) = q;
-      }
-    } else {
-      if (have > 0) p[0] = from_f32<T>(f[0]);
-      if (have > 1) p[32] = from_f32<T>(f[1]);
+      return Vec<C>(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      return Vec<C>(f.x, f.y);
     }
+  }
+  static constexpr uint32_t kHeld =  // a gate of +infinity
+      sizeof(T) == 4 ? 0x7F800000u : std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+  // gates of at most 80, whose exponential is finite (NaN stays)
+  static __device__ __forceinline__ uint32_t bounded(uint32_t w) {
+    if constexpr (sizeof(T) == 4) {
+      asm("min.NaN.f32 %0, %0, 0f42A00000;" : "+r"(w));
+    } else if constexpr (std::is_same<T, __half>::value) {
+      asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(w) : "r"(0x55005500u));
+    } else {
+      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x42A042A0u));
+    }
+    return w;
+  }
+  static __device__ __forceinline__ uint32_t round(Vec<C> f) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(f.get(0));
+    else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 q = __floats2half2_rn(f.get(0), f.get(1));
+      return *reinterpret_cast<const uint32_t*>(&q);
+    } else {
+      const __nv_bfloat162 q = __floats2bfloat162_rn(f.get(0), f.get(1));
+      return *reinterpret_cast<const uint32_t*>(&q);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int have, uint32_t w) {
+    if constexpr (sizeof(T) == 4 || kWide) {
+      if (have > 0) *reinterpret_cast<uint32_t*>(p) = w;
+    } else {
+      unsigned short* q = reinterpret_cast<unsigned short*>(p);
+      if (have > 0) q[0] = (unsigned short)w;
+      if (have > 1) q[32] = (unsigned short)(w >> 16);
+    }
+  }
+};
+
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A run of one tensor in shared memory, a warp's own: kRun rows of 128 bytes.
+struct Staged {
+  uint32_t w[kRun][32];
+};
+
+// One input's runs: through shared memory (kWide), or straight into registers.
+// Steps past the end read as `past` (two channels of it).
+template <class T, bool kWide>
+struct Runs {
+  Staged* staged;
+  const T* p;  // this lane's first access (kWide), or its channel, of step 0
+  int64_t ts;
+  int have;
+  uint32_t past;
+  __device__ __forceinline__ Runs(const Strided<T>& s, int64_t b, int64_t group, int64_t d, int h,
+                                  int64_t dim, Staged* st, uint32_t past_ = 0u)
+      : staged(st), ts(s.ts), past(past_) {
+    const T* row = s.p + b * s.bs;
+    if constexpr (kWide) {
+      constexpr int E = 16 / sizeof(T);  // elements of an access, which divide dim
+      const int lane = threadIdx.x % 32;
+      const int64_t c = group * 32 * Lane<T>::C + lane % 8 * E;
+      have = c < dim;
+      p = row + (have ? c : 0) + lane / 8 * ts;
+    } else {
+      p = row + d;
+      have = h;
+    }
+  }
+  // begins to fetch steps t0 .. t0 + m
+  __device__ __forceinline__ void ask(int64_t t0, int m) const {
+    if constexpr (kWide) {
+      const int lane = threadIdx.x % 32;
+      const T* from = p + t0 * ts;
+      uint32_t* to = &staged->w[lane / 8][lane % 8 * 4];
+      if (m == kRun) {
+#pragma unroll
+        for (int j = 0; j < kRun / 4; ++j)
+          if (have) copy16(to + j * 128, from + j * 4 * ts);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kRun / 4; ++j) {
+          if (j * 4 + lane / 8 >= m)
+            *reinterpret_cast<uint4*>(to + j * 128) = make_uint4(past, past, past, past);
+          else if (have)
+            copy16(to + j * 128, from + j * 4 * ts);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t get(int64_t t0, int m, int i) const {
+    if constexpr (kWide) return staged->w[i][threadIdx.x % 32];
+    else return i < m ? Word<T, kWide>::load(p + (t0 + i) * ts, have) : past;
   }
 };
 
@@ -128,7 +300,7 @@ struct Word {
 template <class T, bool kWide>
 struct Channels {
   static constexpr int C = Lane<T>::C;
-  static constexpr int kStep = kWide ? 1 : 32;
+  static constexpr int kStep = kWide || C == 1 ? 1 : 32;
   int64_t d;
   int have;
   __device__ Channels(int64_t group, int64_t dim) {
@@ -144,65 +316,58 @@ struct Channels {
 // one before, which another block of the cluster may still be reading.
 template <int C>
 struct Joints {
-  float2 warp[2][kGateWarps][32 * C];
-  float2 tile[2][kMostCluster][32 * C];
+  Map<C> warp[2][kGateWarps][32];
+  Map<C> tile[2][kMostCluster][32];
 };
 
 // Gives the state that this warp's run starts from, and moves `carry` past all
-// of the cluster's tiles. Run maps (L, F) are in time order for warps and
-// blocks `first` to `last`.
+// of the cluster's tiles.
 template <int C, bool kBack>
-__device__ __forceinline__ void join_runs(Joints<C>& j, int turn, int rank, int blocks,
-                                          const float (&L)[C], const float (&F)[C],
-                                          float (&carry)[C], float (&h)[C]) {
+__device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, int blocks,
+                                            const Map<C>& run, float (&carry)[C]) {
   namespace cg = cooperative_groups;
-  const cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-#pragma unroll
-  for (int k = 0; k < C; ++k) j.warp[turn][warp][lane * C + k] = make_float2(L[k], F[k]);
+  j.warp[turn][warp][lane] = run;
   __syncthreads();
-  // the tile's map, to every block of the cluster: warp w tells blocks w, w + 8
-  if (warp < blocks) {
-    float tl[C], tf[C];
+  float h[C];
+#pragma unroll
+  for (int k = 0; k < C; ++k) h[k] = carry[k];
+  if (blocks > 1) {
+    const cg::cluster_group cl = cg::this_cluster();
+    // the tile's map, to every block of the cluster: warp w tells blocks w, w + 8
+    if (warp < blocks) {
+      Map<C> tile = j.warp[turn][kBack ? kGateWarps - 1 : 0][lane];
+#pragma unroll
+      for (int i = 1; i < kGateWarps; ++i)
+        tile = map_join(tile, j.warp[turn][kBack ? kGateWarps - 1 - i : i][lane]);
+      for (int to = warp; to < blocks; to += kGateWarps)
+        *cl.map_shared_rank(&j.tile[turn][rank][lane], to) = tile;
+    }
+    cl.sync();
+    for (int i = 0; i < blocks; ++i) {
+      const int r = kBack ? blocks - 1 - i : i;
+#pragma unroll
+      for (int k = 0; k < C; ++k) h[k] = r == rank ? carry[k] : h[k];
+      j.tile[turn][r][lane].apply(carry);
+    }
+#pragma unroll
+    for (int i = 0; i < kGateWarps; ++i) {
+      const int w = kBack ? kGateWarps - 1 - i : i;
+      if (kBack ? w > warp : w < warp) j.warp[turn][w][lane].apply(h);
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < kGateWarps; ++i) {
       const int w = kBack ? kGateWarps - 1 - i : i;
 #pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const float2 m = j.warp[turn][w][lane * C + k];
-        if (i == 0) tl[k] = m.x, tf[k] = m.y;
-        else map_join(tl[k], tf[k], m.x, m.y);
-      }
-    }
-    for (int to = warp; to < blocks; to += kGateWarps) {
-      float2* p = cl.map_shared_rank(&j.tile[turn][rank][lane * C], to);
-#pragma unroll
-      for (int k = 0; k < C; ++k) p[k] = make_float2(tl[k], tf[k]);
+      for (int k = 0; k < C; ++k) h[k] = w == warp ? carry[k] : h[k];
+      j.warp[turn][w][lane].apply(carry);
     }
   }
-  cl.sync();
+  Vec<C> v;
 #pragma unroll
-  for (int k = 0; k < C; ++k) h[k] = carry[k];
-  for (int i = 0; i < blocks; ++i) {
-    const int r = kBack ? blocks - 1 - i : i;
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      const float2 m = j.tile[turn][r][lane * C + k];
-      if (r == rank) h[k] = carry[k];
-      carry[k] = map_apply(m.x, m.y, carry[k]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kGateWarps; ++i) {
-    const int w = kBack ? kGateWarps - 1 - i : i;
-    if (kBack ? w > warp : w < warp) {
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const float2 m = j.warp[turn][w][lane * C + k];
-        h[k] = map_apply(m.x, m.y, h[k]);
-      }
-    }
-  }
+  for (int k = 0; k < C; ++k) v.set(k, h[k]);
+  return v;
 }
 
 template <class T>
@@ -214,12 +379,20 @@ struct GateFwd {
   int64_t n_check;
 };
 
+template <int C>
+struct ForwardShared {
+  Joints<C> joints;
+  Staged staged[kGateWarps][3];  // kWide alone
+};
+
 template <class T, bool kZ, bool kWide>
 __global__ void __launch_bounds__(kGateWarps * 32, 2)
 gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
   constexpr int C = Lane<T>::C;
   using W = Word<T, kWide>;
-  __shared__ Joints<C> joints;
+  using V = Vec<C>;
+  extern __shared__ __align__(16) char shared[];
+  ForwardShared<C>& sh = *reinterpret_cast<ForwardShared<C>*>(shared);
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
@@ -227,93 +400,108 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
   const int64_t b = divide(blockIdx.x / (unsigned)blocks, per, group);
   const Channels<T, kWide> ch(group, in.dim);
   const int64_t n = sequence_length(in.lengths, in.index_bytes, b, in.len);
-  float carry[C];
+  Staged* st = kWide ? sh.staged[warp] : nullptr;
+  const Runs<T, kWide> rg(in.gate, b, group, ch.d, ch.have, in.dim, st, W::kHeld);
+  const Runs<T, kWide> rx(in.x, b, group, ch.d, ch.have, in.dim, st + 1);
+  const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, ch.d, ch.have, in.dim, st + 2);
+  float carry[C];  // -h
 #pragma unroll
   for (int k = 0; k < C; ++k)
-    carry[k] = in.state != nullptr && k < ch.have ? in.state[b * in.dim + ch.at(k)] : 0.0f;
+    carry[k] = in.state != nullptr && k < ch.have ? -in.state[b * in.dim + ch.at(k)] : 0.0f;
   const int64_t step = (int64_t)blocks * kTileSteps;
   int turn = 0;
   int64_t t0 = (int64_t)rank * kTileSteps + warp * kRun;  // this warp's run
+  auto steps = [&](int64_t t) { return (int)max((int64_t)0, min((int64_t)kRun, n - t)); };
+  int m = steps(t0);
+  rg.ask(t0, m);
+  rx.ask(t0, m);
+  copy_commit();
+  if constexpr (kZ) rz.ask(t0, m);
+  copy_commit();
   for (int64_t s0 = 0; s0 < n; s0 += step, t0 += step, turn ^= 1) {
-    uint32_t x[kRun], z[kRun];
-    float c[kRun][C];
-    const int m = (int)max((int64_t)0, min((int64_t)kRun, n - t0));
-    const T* px = in.x.p + b * in.x.bs + t0 * in.x.ts + ch.d;
-    const T* pg = in.gate.p + b * in.gate.bs + t0 * in.gate.ts + ch.d;
-    const T* pz = kZ ? in.z.p + b * in.z.bs + t0 * in.z.ts + ch.d : nullptr;
-    uint32_t g[kRun];
-    if (m == kRun) {
+    uint32_t g[kRun], xw[kRun];
+    copy_wait<1>();
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) g[i] = W::load(pg + i * in.gate.ts, ch.have);
+    for (int i = 0; i < kRun; ++i) g[i] = rg.get(t0, m, i);
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) x[i] = W::load(px + i * in.x.ts, ch.have);
-      if constexpr (kZ) {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) z[i] = W::load(pz + i * in.z.ts, ch.have);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const int have = i < m ? ch.have : 0;
-        g[i] = W::load(pg + i * in.gate.ts, have);
-        x[i] = W::load(px + i * in.x.ts, have);
-        if constexpr (kZ) z[i] = W::load(pz + i * in.z.ts, have);
-      }
-    }
-    float L[C], Q[C], P[C], F[C], h[C];
-#pragma unroll
-    for (int k = 0; k < C; ++k) L[k] = 0.0f, Q[k] = 0.0f, P[k] = 1.0f;
+    for (int i = 0; i < kRun; ++i) xw[i] = rx.get(t0, m, i);
+    __syncwarp();
+    const int64_t next = t0 + step;
+    const int m_next = steps(next);
+    rg.ask(next, m_next);
+    rx.ask(next, m_next);
+    copy_commit();
+    V r[kRun], x[kRun];  // -r
+    V L(0.0f), Q(0.0f), P(1.0f);
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        c[i][k] = i < m ? gate_coef(W::get(g[i], k)) : 0.0f;  // past the end: held
-        L[k] = gate_step(c[i][k], L[k], W::get(x[i], k));
-        Q[k] = gate_step(c[i][k], Q[k], 1.0f);
-        P[k] *= keep(c[i][k]);
-      }
+      r[i] = minus_sigmoid(W::get(g[i]), kLog2e);
+      x[i] = W::get(xw[i]);
+      L = fma(r[i], x[i], decay(r[i], L));  // of the negative state
+      Q = fma(r[i], P, Q);
+      P = decay(r[i], P);
     }
-#pragma unroll
-    for (int k = 0; k < C; ++k) F[k] = map_keep(Q[k], P[k]);
-    join_runs<C, false>(joints, turn, rank, blocks, L, F, carry, h);
+    V s = join_runs<C, false>(sh.joints, turn, rank, blocks, run_map(L, Q, P), carry);
     if (out.checkpoints != nullptr && m > 0) {
       float* p = out.checkpoints + (b * out.n_check + t0 / kRun) * in.dim;
 #pragma unroll
       for (int k = 0; k < C; ++k)
-        if (k < ch.have) p[ch.at(k)] = h[k];
+        if (k < ch.have) p[ch.at(k)] = -s.get(k);
     }
-    T* py = out.y + b * out.ybs + t0 * out.yts + ch.d;
+    if constexpr (kZ) {
+      copy_wait<1>();
+      __syncwarp();
+    }
+    uint32_t y[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      float o[C];
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        h[k] = gate_step(c[i][k], h[k], W::get(x[i], k));
-        o[k] = h[k];
-        if constexpr (kZ) {
-          const float v = W::get(z[i], k);
-          o[k] *= v * sigmoid(v);
-        }
+      s = fma(r[i], x[i], decay(r[i], s));
+      if constexpr (kZ) {
+        const V z = W::get(rz.get(t0, m, i));
+        y[i] = W::round(mul(mul(s, z), minus_sigmoid(z, -kLog2e)));
+      } else {
+        y[i] = W::round(mul(s, V(-1.0f)));
       }
-      if (i < m) W::store(py + i * out.yts, ch.have, o);
     }
+    if constexpr (kZ) {
+      __syncwarp();
+      rz.ask(next, m_next);
+    }
+    copy_commit();
+    T* py = out.y + b * out.ybs + t0 * out.yts + ch.d;
+    if (m == kRun) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) W::store(py + i * out.yts, ch.have, y[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+        if (i < m) W::store(py + i * out.yts, ch.have, y[i]);
+    }
+    m = m_next;
   }
+  copy_wait<0>();
   if (out.final_state != nullptr && rank == 0 && warp == 0) {
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (k < ch.have) out.final_state[b * in.dim + ch.at(k)] = carry[k];
+      if (k < ch.have) out.final_state[b * in.dim + ch.at(k)] = -carry[k];
   }
   // past the sequence's end
-  const float zero[C] = {};
   for (int64_t t = n + rank * kGateWarps + warp; t < in.len; t += blocks * kGateWarps)
-    W::store(out.y + b * out.ybs + t * out.yts + ch.d, ch.have, zero);
-  cooperative_groups::this_cluster().sync();  // others write here
+    W::store(out.y + b * out.ybs + t * out.yts + ch.d, ch.have, 0u);
+  if (blocks > 1) cooperative_groups::this_cluster().sync();  // others write here
 }
 
 template <class T>
 struct GateOut {
   T *dx, *dgate, *dz;  // contiguous
   float* dstate;
+};
+
+template <int C>
+struct BackwardShared {
+  Joints<C> joints;
+  Staged staged[kGateWarps][4];  // kWide alone
 };
 
 template <class T, bool kZ, bool kWide>
@@ -323,7 +511,9 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
                            int blocks) {
   constexpr int C = Lane<T>::C;
   using W = Word<T, kWide>;
-  __shared__ Joints<C> joints;
+  using V = Vec<C>;
+  extern __shared__ __align__(16) char shared[];
+  BackwardShared<C>& sh = *reinterpret_cast<BackwardShared<C>*>(shared);
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
@@ -331,101 +521,127 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
   const int64_t b = divide(blockIdx.x / (unsigned)blocks, per, group);
   const Channels<T, kWide> ch(group, in.dim);
   const int64_t n = sequence_length(in.lengths, in.index_bytes, b, in.len);
-  float carry[C];  // a[t+1] G[t+1]
+  Staged* st = kWide ? sh.staged[warp] : nullptr;
+  const Runs<T, kWide> rg(in.gate, b, group, ch.d, ch.have, in.dim, st, W::kHeld);
+  const Runs<T, kWide> rx(in.x, b, group, ch.d, ch.have, in.dim, st + 1);
+  const Runs<T, kWide> re(dy, b, group, ch.d, ch.have, in.dim, st + 2);
+  const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, ch.d, ch.have, in.dim, st + 3);
+  float carry[C];  // -a[t+1] G[t+1]
 #pragma unroll
   for (int k = 0; k < C; ++k)
-    carry[k] = dfinal != nullptr && k < ch.have ? dfinal[b * in.dim + ch.at(k)] : 0.0f;
+    carry[k] = dfinal != nullptr && k < ch.have ? -dfinal[b * in.dim + ch.at(k)] : 0.0f;
   const int64_t step = (int64_t)blocks * kTileSteps;
   int turn = 0;
-  for (int64_t s0 = (n + step - 1) / step * step - step; s0 >= 0; s0 -= step, turn ^= 1) {
-    const int64_t t0 = s0 + (int64_t)rank * kTileSteps + warp * kRun;
-    const int m = (int)max((int64_t)0, min((int64_t)kRun, n - t0));
-    uint32_t x[kRun], g[kRun], z[kRun], e[kRun];
-    const T* px = in.x.p + b * in.x.bs + t0 * in.x.ts + ch.d;
-    const T* pg = in.gate.p + b * in.gate.bs + t0 * in.gate.ts + ch.d;
-    const T* pz = kZ ? in.z.p + b * in.z.bs + t0 * in.z.ts + ch.d : nullptr;
-    const T* pe = dy.p + b * dy.bs + t0 * dy.ts + ch.d;
+  int64_t s0 = (n + step - 1) / step * step - step;
+  auto steps = [&](int64_t t) {
+    return t < 0 ? 0 : (int)max((int64_t)0, min((int64_t)kRun, n - t));
+  };
+  const int64_t mine = (int64_t)rank * kTileSteps + warp * kRun;
+  int m = s0 < 0 ? 0 : steps(s0 + mine);
+  float h[C];
+  auto ask = [&](int64_t t0, int m) {
+    rg.ask(t0, m);
+    rx.ask(t0, m);
+    re.ask(t0, m);
+    if constexpr (kZ) rz.ask(t0, m);
+    copy_commit();
+    const float* p = checkpoints + (b * n_check + t0 / kRun) * in.dim;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int have = i < m ? ch.have : 0;
-      g[i] = W::load(pg + i * in.gate.ts, have);
-      x[i] = W::load(px + i * in.x.ts, have);
-      e[i] = W::load(pe + i * dy.ts, have);
-      if constexpr (kZ) z[i] = W::load(pz + i * in.z.ts, have);
-    }
-    float h[C];
-    {
-      const float* p = checkpoints + (b * n_check + t0 / kRun) * in.dim;
-#pragma unroll
-      for (int k = 0; k < C; ++k) h[k] = m > 0 && k < ch.have ? p[ch.at(k)] : 0.0f;
-    }
-    // the states again; what the way back takes of each step
-    float c[kRun][C], d[kRun][C], v[kRun][C];
+    for (int k = 0; k < C; ++k) h[k] = m > 0 && k < ch.have ? p[ch.at(k)] : 0.0f;
+  };
+  ask(s0 + mine, m);
+  for (; s0 >= 0; s0 -= step, turn ^= 1) {
+    const int64_t t0 = s0 + mine;
     const int64_t at = (b * in.len + t0) * in.dim + ch.d;
+    copy_wait<0>();
+    __syncwarp();
+    // the states again; what the way back takes of each step, which goes by -G
+    V r[kRun], d[kRun], v[kRun];  // -r, (x - h[t-1]) a r, -dy silu(z)
+    V s;
+#pragma unroll
+    for (int k = 0; k < C; ++k) s.set(k, -h[k]);
+    V Q(0.0f), P(1.0f);
+    uint32_t dz[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      float o[C];
+      const V x = W::get(rx.get(t0, m, i));
+      V e;
+      r[i] = minus_sigmoid(W::get(W::bounded(rg.get(t0, m, i))), kLog2e, &e);
+      // e r = a keeps its digits where r is near 1
+      d[i] = mul(mul(add(s, x), r[i]), mul(e, r[i]));
+      s = fma(r[i], x, decay(r[i], s));
+      v[i] = W::get(re.get(t0, m, i));
+      if constexpr (kZ) {
+        const V z = W::get(rz.get(t0, m, i)), w = minus_sigmoid(z, -kLog2e);  // -sigmoid
+        const V silu = mul(z, w);                                            // -silu
+        // minus the slope: w + silu (1 + w), silu' = sigmoid + silu (1 - sigmoid)
+        const V slope = fma(silu, fma(w, V(1.0f), V(1.0f)), w);
+        dz[i] = W::round(mul(mul(v[i], s), slope));
+        v[i] = mul(v[i], silu);
+      } else {
+        v[i] = mul(v[i], V(-1.0f));
+      }
+    }
+    if constexpr (kZ) {
+      if (m == kRun) {
 #pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const float xv = W::get(x[i], k);
-        c[i][k] = i < m ? gate_coef(W::get(g[i], k)) : 0.0f;
-        d[i][k] = h[k] - xv;
-        h[k] = gate_step(c[i][k], h[k], xv);
-        v[i][k] = W::get(e[i], k);
-        if constexpr (kZ) {
-          const float q = W::get(z[i], k), s = sigmoid(q);
-          o[k] = v[i][k] * h[k] * (s * (1.0f + q * (1.0f - s)));
-          v[i][k] *= q * s;
+        for (int i = 0; i < kRun; ++i) W::store(out.dz + at + i * in.dim, ch.have, dz[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (i < m) W::store(out.dz + at + i * in.dim, ch.have, dz[i]);
+      }
+    }
+    __syncwarp();
+    const int64_t next = s0 - step;
+    const int m_next = next < 0 ? 0 : steps(next + mine);
+    ask(next < 0 ? t0 : next + mine, m_next);
+    V L(0.0f);
+#pragma unroll
+    for (int i = kRun - 1; i >= 0; --i) {
+      L = decay(r[i], fma(v[i], V(1.0f), L));  // (a sum with a product: see add2)
+      Q = fma(r[i], P, Q);
+      P = decay(r[i], P);
+    }
+    V B = join_runs<C, true>(sh.joints, turn, rank, blocks, run_map(L, Q, P), carry);
+    uint32_t ox[kRun], og[kRun];
+#pragma unroll
+    for (int i = kRun - 1; i >= 0; --i) {
+      const V G = fma(v[i], V(1.0f), B);
+      ox[i] = W::round(mul(r[i], G));
+      og[i] = W::round(mul(d[i], G));
+      B = decay(r[i], G);
+    }
+    if (m == kRun) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        W::store(out.dx + at + i * in.dim, ch.have, ox[i]);
+        W::store(out.dgate + at + i * in.dim, ch.have, og[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (i < m) {
+          W::store(out.dx + at + i * in.dim, ch.have, ox[i]);
+          W::store(out.dgate + at + i * in.dim, ch.have, og[i]);
         }
       }
-      if constexpr (kZ) {
-        if (i < m) W::store(out.dz + at + i * in.dim, ch.have, o);
-      }
     }
-    float L[C], Q[C], P[C], F[C], B[C];
-#pragma unroll
-    for (int k = 0; k < C; ++k) L[k] = 0.0f, Q[k] = 0.0f, P[k] = 1.0f;
-#pragma unroll
-    for (int i = kRun - 1; i >= 0; --i) {
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        L[k] = forget(c[i][k], L[k] + v[i][k]);
-        Q[k] = gate_step(c[i][k], Q[k], 1.0f);
-        P[k] *= keep(c[i][k]);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < C; ++k) F[k] = map_keep(Q[k], P[k]);
-    join_runs<C, true>(joints, turn, rank, blocks, L, F, carry, B);
-#pragma unroll
-    for (int i = kRun - 1; i >= 0; --i) {
-      float o[C], p[C];
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const float G = B[k] + v[i][k], a = fabsf(c[i][k]);
-        o[k] = take(c[i][k]) * G;
-        p[k] = d[i][k] * G * (a * (1.0f - a));
-        B[k] = forget(c[i][k], G);
-      }
-      if (i < m) {
-        W::store(out.dx + at + i * in.dim, ch.have, o);
-        W::store(out.dgate + at + i * in.dim, ch.have, p);
-      }
-    }
+    m = m_next;
   }
+  copy_wait<0>();
   if (out.dstate != nullptr && rank == 0 && warp == 0) {
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (k < ch.have) out.dstate[b * in.dim + ch.at(k)] = carry[k];
+      if (k < ch.have) out.dstate[b * in.dim + ch.at(k)] = -carry[k];
   }
-  const float zero[C] = {};
   for (int64_t t = n + rank * kGateWarps + warp; t < in.len; t += blocks * kGateWarps) {
     const int64_t at = (b * in.len + t) * in.dim + ch.d;
-    W::store(out.dx + at, ch.have, zero);
-    W::store(out.dgate + at, ch.have, zero);
-    if constexpr (kZ) W::store(out.dz + at, ch.have, zero);
+    W::store(out.dx + at, ch.have, 0u);
+    W::store(out.dgate + at, ch.have, 0u);
+    if constexpr (kZ) W::store(out.dz + at, ch.have, 0u);
   }
-  cooperative_groups::this_cluster().sync();
+  if (blocks > 1) cooperative_groups::this_cluster().sync();
 }
 
 template <class T>
@@ -440,7 +656,8 @@ gated_scan_step_kernel(GateIn<T> in, float* __restrict__ state, int64_t rows, co
     if (row >= 0 && row < rows) {
       float h = state[row * in.dim + d];
       const float x = to_f32(in.x.p[b * in.x.bs + d]);
-      h = gate_step(gate_coef(to_f32(in.gate.p[b * in.gate.bs + d])), h, x);
+      const float r = minus_sigmoid(Vec<1>(to_f32(in.gate.p[b * in.gate.bs + d])), kLog2e).v;
+      h = fmaf(-r, x, fmaf(r, h, h));
       state[row * in.dim + d] = h;
       o = h;
       if (in.z.p != nullptr) {
@@ -461,19 +678,21 @@ GateIn<T> gate_in(const cr_gated_scan_args* a) {
           a->state, a->lengths, a->index_bytes};
 }
 
-// Blocks that share a sequence's time.
-#ifndef CR_GATE_BLOCKS
-#define CR_GATE_BLOCKS 304
-#endif
+// Blocks that share a sequence's time: as many as fit the GPU at once with those
+// of the other sequences and channels (two an SM).
 int gate_blocks(int64_t groups, int64_t len) {
-  int c = 1;
-  while (c < kMostCluster && groups * c * 2 <= CR_GATE_BLOCKS && (int64_t)c * kTileSteps < len) c *= 2;
-  return c;
+  const int64_t c = std::min(304 / groups, ceil_div(len, kTileSteps));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(c, kMostCluster));
 }
 
 template <class... P, class... A>
-void launch_clusters(void (*kernel)(P...), int64_t blocks, int cluster, cudaStream_t s, A... args) {
+bool launch_clusters(void (*kernel)(P...), int64_t blocks, int cluster, size_t smem,
+                     cudaStream_t s, A... args) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return false;
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kGateWarps * 32);
   cfg.stream = s;
@@ -483,26 +702,21 @@ void launch_clusters(void (*kernel)(P...), int64_t blocks, int cluster, cudaStre
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  if (cluster > 8 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-          cudaSuccess)
-    return;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-// The kernel for a call with z or without, and for rows of whole words or any.
-// (For binary32 a word is a channel.)
-#define CR_GATE_KERNEL(NAME, T, Z, WIDE)                                      \
-  (Z ? WIDE ? NAME<T, true, true> : NAME<T, true, sizeof(T) == 4>             \
-     : WIDE ? NAME<T, false, true> : NAME<T, false, sizeof(T) == 4>)
+// The kernel for a call with z or without, and for rows on 16 bytes or anywhere.
+#define CR_GATE_KERNEL(NAME, T, Z, WIDE)             \
+  (Z ? WIDE ? NAME<T, true, true> : NAME<T, true, false> \
+     : WIDE ? NAME<T, false, true> : NAME<T, false, false>)
 
-template <class T>
+// Whether rows are on 16 bytes and whole accesses long.
 bool gate_wide(const cr_gated_scan_args* a) {
-  if (sizeof(T) == 4) return true;
-  const size_t es = sizeof(T);
-  return a->dim % 2 == 0 && rows_aligned(a->x, a->x_batch_stride, a->x_time_stride, es, 4) &&
-         rows_aligned(a->gate, a->gate_batch_stride, a->gate_time_stride, es, 4) &&
-         (a->z == nullptr || rows_aligned(a->z, a->z_batch_stride, a->z_time_stride, es, 4));
+  const size_t es = model_esize(a->dt);
+  return a->dim % (int64_t)(16 / es) == 0 &&
+         rows_aligned(a->x, a->x_batch_stride, a->x_time_stride, es, 16) &&
+         rows_aligned(a->gate, a->gate_batch_stride, a->gate_time_stride, es, 16) &&
+         (a->z == nullptr || rows_aligned(a->z, a->z_batch_stride, a->z_time_stride, es, 16));
 }
 
 cr_status check_gate(const cr_gated_scan_args* a, bool step) {
@@ -554,17 +768,20 @@ cr_status cr_gated_scan(const cr_gated_scan_args* a, void* y, int64_t y_batch_st
   const int64_t per = ceil_div(a->dim, 128 / (int64_t)es);
   if (a->batch > kMaxBlocks / kMostCluster / per) return CR_ERR_UNSUPPORTED;
   const int c = gate_blocks(a->batch * per, a->len);
+  bool done = false;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CR_MODEL_TYPE(a->dt, {
     const GateFwd<T> out = {static_cast<T*>(y), y_batch_stride, y_time_stride, final_state,
                             checkpoints, cr_gated_scan_checkpoints(a->len)};
-    const bool wide = gate_wide<T>(a) &&
-                      (es == 4 || rows_aligned(y, y_batch_stride, y_time_stride, es, 4));
+    const bool wide = gate_wide(a) && rows_aligned(y, y_batch_stride, y_time_stride, es, 4);
+    using Shared = ForwardShared<Lane<T>::C>;
+    const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
     auto kernel = CR_GATE_KERNEL(gated_scan_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScan, s,
-              launch_clusters(kernel, a->batch * per * c, c, s, gate_in<T>(a), out, c));
+              done = launch_clusters(kernel, a->batch * per * c, c, smem, s, gate_in<T>(a), out,
+                                     c));
   });
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_scan_grads* g,
@@ -589,21 +806,24 @@ cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_sca
   const int64_t per = ceil_div(a->dim, 128 / (int64_t)es);
   if (a->batch > kMaxBlocks / kMostCluster / per) return CR_ERR_UNSUPPORTED;
   const int c = gate_blocks(a->batch * per, a->len);
+  bool done = false;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CR_MODEL_TYPE(a->dt, {
     const Strided<T> dy = {static_cast<const T*>(g->dy), g->dy_batch_stride, g->dy_time_stride};
     const GateOut<T> out = {static_cast<T*>(g->dx), static_cast<T*>(g->dgate),
                             static_cast<T*>(g->dz), g->dstate};
-    const bool wide =
-        gate_wide<T>(a) &&
-        (es == 4 || (rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, 4) &&
-                     ptr_aligned(g->dx, 4) && ptr_aligned(g->dgate, 4) && ptr_aligned(g->dz, 4)));
+    const bool wide = gate_wide(a) &&
+                      rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, 16) &&
+                      ptr_aligned(g->dx, 4) && ptr_aligned(g->dgate, 4) && ptr_aligned(g->dz, 4);
+    using Shared = BackwardShared<Lane<T>::C>;
+    const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
     auto kernel = CR_GATE_KERNEL(gated_scan_backward_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScanBackward, s,
-              launch_clusters(kernel, a->batch * per * c, c, s, gate_in<T>(a), dy, g->dfinal,
-                              g->checkpoints, cr_gated_scan_checkpoints(a->len), out, c));
+              done = launch_clusters(kernel, a->batch * per * c, c, smem, s, gate_in<T>(a), dy,
+                                     g->dfinal, g->checkpoints,
+                                     cr_gated_scan_checkpoints(a->len), out, c));
   });
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 cr_status cr_gated_scan_step(const cr_gated_scan_args* a, float* state, int64_t state_rows,

@@ -76,14 +76,14 @@ def gated(x, gate, z, state, lengths, dy=None, dfinal=None):
     """x (B, T, D) etc. as float64 arrays. Returns {name: (value, bound)}, the
     gradients under "d" + name.
 
-    The smaller of a and r = 1 - a is off by K roundings of itself (the
-    exponent's, |gate| / 2 and one, the instruction's two and a half, the
-    reciprocal's and the product's), each step rounds the state twice; whole
-    tiles are joined by as much again."""
+    r = 1 - a is off by K roundings of itself (the exponent's, |gate| / 2 and
+    one, the instruction's two and a half, the reciprocal's two). A step is two
+    operations, h - r h and + r x, whose roundings are of results up to |h| and
+    up to the new state; a tile's map, applied the same way, rounds what it
+    starts from once more."""
     Bn, T, D = x.shape
     K = (8 + np.abs(np.where(np.isfinite(gate), gate, 0))) * U
     a, r = sigmoid(gate), sigmoid(-gate)
-    small = np.minimum(a, r)
     h, hm, he = (np.zeros((Bn, T + 1, D)) for _ in range(3))
     if state is not None:
         h[:, 0], hm[:, 0] = state, np.abs(state)
@@ -94,11 +94,11 @@ def gated(x, gate, z, state, lengths, dy=None, dfinal=None):
     ds, dse = np.zeros((Bn, D)), np.zeros((Bn, D))
     for b in range(Bn):
         for t in range(n[b]):
-            at, rt, st, xt = a[b, t], r[b, t], small[b, t], np.abs(x[b, t])
+            at, rt, xt = a[b, t], r[b, t], np.abs(x[b, t])
             h[b, t + 1] = at * h[b, t] + rt * x[b, t]
             hm[b, t + 1] = at * hm[b, t] + rt * xt
-            he[b, t + 1] = at * he[b, t] + 4 * (U * 2 * hm[b, t + 1] +
-                                                K[b, t] * st * (xt + hm[b, t]))
+            he[b, t + 1] = at * he[b, t] + 4 * (U * (hm[b, t + 1] + at * hm[b, t]) +
+                                                K[b, t] * rt * (xt + hm[b, t]))
         m = n[b]
         final[b], fe[b] = h[b, m], he[b, m]
         zb = None if z is None else z[b, :m]
@@ -122,13 +122,13 @@ def gated(x, gate, z, state, lengths, dy=None, dfinal=None):
             G = G + e
             Gm = Gm + np.abs(e)
             Ge = Ge + 4 * U * Gm + (0.0 if z is None else 4 * kz[t]) * np.abs(e)
-            at, rt, st, kt = a[b, t], r[b, t], small[b, t], K[b, t]
+            at, rt, kt = a[b, t], r[b, t], K[b, t]
             g["dx"][0][b, t] = rt * G
-            g["dx"][1][b, t] = rt * Ge + (kt * st + 4 * U * rt) * Gm
+            g["dx"][1][b, t] = rt * Ge + (kt * rt + 4 * U * rt) * Gm
             d, dm = h[b, t] - x[b, t], hm[b, t] + np.abs(x[b, t])
             g["dgate"][0][b, t] = d * G * at * rt
             g["dgate"][1][b, t] = at * rt * (dm * Ge + he[b, t] * Gm + (2 * kt + 8 * U) * dm * Gm)
-            Ge = at * Ge + 4 * (kt * st + 2 * U * at) * Gm
+            Ge = at * Ge + 4 * (kt * rt + 2 * U * at) * Gm
             G, Gm = at * G, at * Gm
         ds[b], dse[b] = G, Ge
     out = {"y": (y, ye), "final": (final, fe)}

@@ -121,6 +121,7 @@ def test_forgetting_what_was_large(scr):
     ref = reference(s)
     M.near(y, *ref["y"], "y")
     M.near(final, *ref["final"], "final")
+    assert torch.equal(y[:, 5:7, ::2], d["x"][:, 5:7, ::2])  # r is 1: nothing of it at all
 
 
 def test_decay_past_binary32(scr):
