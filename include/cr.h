@@ -601,9 +601,9 @@ cr_status cr_gated_scan_step(const cr_gated_scan_args* args, float* state, int64
  * 0 or NaN is taken as 0, u of 1 or more as 1 - 2^-24. A logit of -inf or NaN
  * is no candidate; where one is +inf, those of +inf have w = 1, the others 0.
  * A row without candidates gives -1.
- * Weights are evaluated to 2^-35 of their value and summed as integers, in
- * units of 2^-44 of the largest: the token is that of exact arithmetic unless u or top_p
- * lies that near to a border. */
+ * Weights are evaluated to 2^-32 of their value and summed as integers, in
+ * units of 2^-42 of the largest: the token is that of exact arithmetic unless
+ * u or top_p lies that near to a border. */
 typedef struct {
   int64_t rows, vocab;    /* vocab <= 2^20 (more: CR_ERR_UNSUPPORTED)         */
   int32_t dt;             /* cr_dtype of logits                               */

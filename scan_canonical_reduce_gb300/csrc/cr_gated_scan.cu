@@ -685,26 +685,6 @@ int gate_blocks(int64_t groups, int64_t len) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(c, kMostCluster));
 }
 
-template <class... P, class... A>
-bool launch_clusters(void (*kernel)(P...), int64_t blocks, int cluster, size_t smem,
-                     cudaStream_t s, A... args) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return false;
-  cudaLaunchConfig_t cfg = {};
-  cfg.dynamicSmemBytes = smem;
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kGateWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
-}
-
 // The kernel for a call with z or without, and for rows on 16 bytes or anywhere.
 #define CR_GATE_KERNEL(NAME, T, Z, WIDE)             \
   (Z ? WIDE ? NAME<T, true, true> : NAME<T, true, false> \
@@ -778,7 +758,7 @@ cr_status cr_gated_scan(const cr_gated_scan_args* a, void* y, int64_t y_batch_st
     const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
     auto kernel = CR_GATE_KERNEL(gated_scan_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScan, s,
-              done = launch_clusters(kernel, a->batch * per * c, c, smem, s, gate_in<T>(a), out,
+              done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s, gate_in<T>(a), out,
                                      c));
   });
   return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
@@ -819,7 +799,7 @@ cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_sca
     const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
     auto kernel = CR_GATE_KERNEL(gated_scan_backward_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScanBackward, s,
-              done = launch_clusters(kernel, a->batch * per * c, c, smem, s, gate_in<T>(a), dy,
+              done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s, gate_in<T>(a), dy,
                                      g->dfinal, g->checkpoints,
                                      cr_gated_scan_checkpoints(a->len), out, c));
   });

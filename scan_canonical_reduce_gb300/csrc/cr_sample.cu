@@ -3,9 +3,20 @@
 // The row's tokens in the order of falling logits (equal ones by index) are
 // kept up to a border, and the token is where the running sum of their weights
 // w = 2^-y, y = (largest - logit) log2(e) / temperature, exceeds u times the
-// kept sum. Sums are of integers in units of 2^-44, so that no order of
-// summation changes them.
+// kept sum. So each limit is a border in one order, and each is found the same
+// way: a histogram of y with 16 bins an octave, whose bins hold numbers and
+// sums of weights, gives the bin; the bin's few tokens, gathered and sorted,
+// give the place in it. (A bin of more tokens than can be sorted is cut again by
+// the logits' bits, and one logit's tokens by their index.) Sums are of
+// integers, so that no order of summation changes them, and are exact to 2^-32
+// of a weight: the token is the one that exact arithmetic gives.
+//
+// A row is one cluster of blocks, a slice each, held in shared memory where it
+// fits. The first block leads: it has the row's sums and the list of a bin.
+#include <algorithm>
 #include <cstdint>
+
+#include <cooperative_groups.h>
 
 #include "cr_device.cuh"
 #include "cr_launch.h"
@@ -14,84 +25,93 @@
 namespace cr {
 namespace {
 
-constexpr int kSampleThreads = 1024;
+namespace cg = cooperative_groups;
 
-// 2^(-j / 32) in units of 2^-63
-__constant__ unsigned long long kRoots[32] = {
-    0x8000000000000000ULL, 0x7D41D96DB915019DULL, 0x7A92BE8A92436616ULL, 0x77F25CCDEE6D7AE6ULL,
-    0x75606373EE921C97ULL, 0x72DC8373BE41A454ULL, 0x70666F76154A7089ULL, 0x6DFDDBCBED791BABULL,
-    0x6BA27E656B4EB57AULL, 0x69540EC8F895722DULL, 0x6712460A8FC24072ULL, 0x64DCDEC3371793D1ULL,
-    0x62B39508AA836D6FULL, 0x6096266533384A2BULL, 0x5E8451CFAC061B5FULL, 0x5C7DD7A3B17DCF75ULL,
-    0x5A827999FCEF3242ULL, 0x5891FAC0E95612C8ULL, 0x56AC1F752150A563ULL, 0x54D0AD5A753E077CULL,
-    0x52FF6B54D8A89C75ULL, 0x513821818624B40CULL, 0x4F7A993048D088D7ULL, 0x4DC69CDCEAA72A9CULL,
-    0x4C1BF828C6DC54B8ULL, 0x4A7A77D47F7B84B1ULL, 0x48E1E9B9D588E19BULL, 0x47521CC5A2E6A9E0ULL,
-    0x45CAE0F1F545EB73ULL, 0x444C0740496D4294ULL, 0x42D561B3E6243D8AULL, 0x4166C34C5615D0ECULL};
+constexpr int kThreads = 512;
+constexpr int kBins = 1024;   // 16 an octave
+constexpr int kList = 1024;   // most tokens that are sorted
+constexpr int kFew = 512;     // top_k up to which its tokens alone are looked at
+constexpr int kMostBlocks = 8;
+constexpr uint32_t kNone = 0xFFFFFFFFu;  // the key of what is no candidate
+
+// 2^(-j / 16) in units of 2^-63
+__constant__ unsigned long long kRoots[16] = {
+    0x8000000000000000ULL, 0x7A92BE8A92436616ULL, 0x75606373EE921C97ULL, 0x70666F76154A7089ULL,
+    0x6BA27E656B4EB57AULL, 0x6712460A8FC24072ULL, 0x62B39508AA836D6FULL, 0x5E8451CFAC061B5FULL,
+    0x5A827999FCEF3242ULL, 0x56AC1F752150A563ULL, 0x52FF6B54D8A89C75ULL, 0x4F7A993048D088D7ULL,
+    0x4C1BF828C6DC54B8ULL, 0x48E1E9B9D588E19BULL, 0x45CAE0F1F545EB73ULL, 0x42D561B3E6243D8AULL};
 
 struct Row {
   float top;     // the largest logit
   float ch, cl;  // log2(e) / temperature
 };
 
-// A logit as an unsigned number that falls as the logit rises; all ones for
-// what is no candidate.
+// A logit as an unsigned number that falls as the logit rises; kNone for what
+// is no candidate.
 __device__ __forceinline__ uint32_t order_key(float l) {
-  if (!(l > -INFINITY)) return 0xFFFFFFFFu;
+  if (!(l > -INFINITY)) return kNone;
   const uint32_t b = __float_as_uint(l + 0.0f);  // -0 is 0
   return (b & 0x80000000u) ? b : ~(b | 0x80000000u);
 }
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k : ~k & 0x7FFFFFFFu);
+}
 
-// y in units of 2^-37 as (bin of 1/32, 32 bits of what is left); false where
-// w < 2^-63.9.
-__device__ __forceinline__ bool far_down(const Row& r, float l, int& bin, uint32_t& rest) {
-  if (l == r.top) {
-    bin = 0;
-    rest = 0;
-    return true;
-  }
+// Where a candidate that is not the largest lies: its bin, and its weight in
+// it, 2^(bin / 16) w - that is 1 - g, g < 0.0425 - as g in units of 2^-33.
+// Returns false where y is 63.9 or more (the far bin): such weights together
+// are below 2^-42 of the largest's. Straight code, whose results then mean
+// nothing.
+constexpr int kFar = kBins - 1;
+constexpr int kIndexDigits = 10;  // 2^20 indices in kBins
+__device__ __forceinline__ bool split(const Row& r, float l, int& bin, uint32_t& g) {
+  // the difference in two numbers, then y in two
   const float s = r.top - l, bb = r.top - s, e = (r.top - (s + bb)) + (bb - l);
   const float yh = s * r.ch;
-  if (!(yh < 63.9f)) return false;
   const float yl = fmaf(e, r.ch, fmaf(s, r.cl, fmaf(s, r.ch, -yh)));
-  const float f = floorf(yh * 32.0f);
-  const long long x = __float2ll_rn(fmaf(f, -0.03125f, yh) * 0x1p37f) +
-                      __float2ll_rn(yl * 0x1p37f) + ((long long)f << 32);
-  bin = (int)(x >> 32);
-  rest = (uint32_t)x;
-  return bin >= 0 ? true : (bin = 0, rest = 0, true);
+  // y = bin / 16 + x, x in units of 2^-36; adding 2^23 rounded down is a floor
+  const float t = __fmaf_rd(yh, 16.0f, 8388608.0f);
+  const float xh = fmaf(t - 8388608.0f, -0.0625f, yh);
+  const uint32_t x0 = __float2uint_rn(xh * 0x1p36f);
+  const int x1 = __float2int_rn(yl * 0x1p36f);
+  const long long y = (((long long)(__float_as_uint(t) & 0x7FFFFFu) << 32) | x0) + x1;
+  bin = (int)(y >> 32);
+  // 1 - 2^-x = 1 - exp(-z) = z - z^2 (1/2 - z (1/6 - z (1/24 - z (1/120 - z /
+  // 720)))), z = x ln 2; z^7 / 5040 < 2^-44 is left out. What follows z is below
+  // 2^-10, and binary32 holds it to 2^-34.
+  const uint32_t z = __umulhi((uint32_t)y, 0xB17217F8u);
+  const float f = (float)z * -0x1p-36f;
+  const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.0f / 720.0f, 1.0f / 120.0f), 1.0f / 24.0f),
+                               1.0f / 6.0f), 0.5f);
+  const uint32_t tail = __float_as_uint(fmaf(f * f, q * 0x1p33f, 8388608.0f)) & 0x7FFFFFu;
+  const uint32_t first = (z >> 3) + (z >> 2 & 1);
+  g = first > tail ? first - tail : 0;
+  return yh < 63.9f;
 }
-
-// 1 - 2^-x in units of 2^-37 of x < 1/32 in units of 2^-37: z = x ln 2, 1 -
-// exp(-z) = z - z^2 (1/2 - z (1/6 - z (1/24 - z / 120))), left out z^6 / 720 <
-// 2^-42; what follows z is below 2^-12 and binary32 holds it to 2^-36.
-__device__ __forceinline__ uint32_t one_minus(uint32_t rest) {
-  const uint32_t z = __umulhi(rest, 0xB17217F8u);
-  const float f = (float)z * 0x1p-37f;
-  const float p = fmaf(-f, fmaf(-f, fmaf(-f, 1.0f / 120.0f, 1.0f / 24.0f), 1.0f / 6.0f), 0.5f);
-  return z - __float2uint_rn(f * f * p * 0x1p37f);
-}
-
-// w in units of 2^-44
-__device__ __forceinline__ uint64_t weight(const Row& r, float l) {
+__device__ __forceinline__ int place(const Row& r, float l, uint32_t& g) {
   int bin;
-  uint32_t rest;
-  if (!far_down(r, l, bin, rest)) return 0;
-  const uint64_t m = ((uint64_t)1 << 37) - one_minus(rest);
-  const uint64_t w = __umul64hi(m << 26, kRoots[bin & 31]);  // units of 2^-62
-  const int sh = 18 + (bin >> 5);
-  return sh >= 64 ? 0 : (w + ((uint64_t)1 << (sh - 1))) >> sh;
+  const bool near = split(r, l, bin, g);
+  if (l == r.top || !near) {
+    g = 0;
+    return l == r.top ? 0 : kFar;
+  }
+  return bin;
 }
 
-template <class V>
-__device__ V block_sum(V v, V* buf) {
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2) v += __shfl_xor_sync(~0u, v, s);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = buf[threadIdx.x % 32];
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2) v += __shfl_xor_sync(~0u, v, s);
-  return v;
+// A sum of weights within a bin (1 is 2^33) in units of 2^-42 of the largest.
+__device__ __forceinline__ uint64_t mass_of(int bin, uint64_t sum) {
+  const uint64_t v = __umul64hi(sum << 10, kRoots[bin & 15]);
+  const int n = bin >> 4;
+  return n == 0 ? v : (v + ((uint64_t)1 << (n - 1))) >> n;
+}
+
+// y in bins, to a few thousandths of one.
+__device__ __forceinline__ float rough(const Row& r, float l) {
+  return (r.top - l) * r.ch * 16.0f;
+}
+// Whether a logit's bin may be this one.
+__device__ __forceinline__ bool near(const Row& r, float l, int bin) {
+  return fabsf(rough(r, l) - ((float)bin + 0.5f)) < 0.51f || (bin == 0 && l == r.top);
 }
 
 template <class T>
@@ -107,97 +127,936 @@ struct SampleIn {
   int32_t index_bytes;
 };
 
-// A bisection over (key, index): the right answer, a pass over the row at a time.
-template <class T>
-__global__ void __launch_bounds__(kSampleThreads)
-sample_kernel(SampleIn<T> in, int64_t* __restrict__ tokens) {
-  __shared__ uint64_t buf[32];
-  const int64_t row = blockIdx.x;
-  const T* x = in.logits + row * in.stride;
-  const int V = (int)in.vocab, tid = threadIdx.x;
-  uint64_t least = ~0ull;  // the row's first, as (key, index)
-  for (int i = tid; i < V; i += kSampleThreads) {
-    const uint64_t k = (uint64_t)order_key(to_f32(x[i])) << 32 | (uint32_t)i;
-    least = min(least, k);
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2) least = min(least, (uint64_t)__shfl_xor_sync(~0u, least, s));
-  if (tid % 32 == 0) buf[tid / 32] = least;
-  __syncthreads();
-  least = buf[tid % 32];
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2) least = min(least, (uint64_t)__shfl_xor_sync(~0u, least, s));
-  const int first = (int)(uint32_t)least;
-  const double temp = in.temperatures != nullptr ? in.temperatures[row] : in.temperature;
-  if (least >> 32 == 0xFFFFFFFFu || !(temp > 0.0)) {
-    if (tid == 0) tokens[row] = least >> 32 == 0xFFFFFFFFu ? -1 : first;
-    return;
-  }
-  const double top_p = in.top_ps != nullptr ? in.top_ps[row] : in.top_p;
-  const double min_p = in.min_ps != nullptr ? in.min_ps[row] : in.min_p;
-  const int64_t top_k = in.top_ks != nullptr ? load_index(in.top_ks, in.index_bytes, row) : in.top_k;
-  Row r;
-  r.top = to_f32(x[first]) + 0.0f;
-  const double c = fmin(1.4426950408889634 / temp, 1e37);
-  r.ch = (float)c;
-  r.cl = (float)(c - (double)r.ch);
+// What the leader tells the others.
+struct Message {
+  int bin;          // the bin that is looked into
+  uint32_t lo, hi;  // and the keys
+  uint32_t number;  // of tokens there
+};
 
-  // what the tokens up to `to` sum up to: weights, or their number
-  auto upto = [&](uint64_t to, bool count) {
-    uint64_t s = 0;
-    for (int i = tid; i < V; i += kSampleThreads) {
-      const float l = to_f32(x[i]);
-      const uint32_t key = order_key(l);
-      if (key == 0xFFFFFFFFu || ((uint64_t)key << 32 | (uint32_t)i) > to) continue;
-      s += count ? 1 : weight(r, l);
-    }
-    return block_sum(s, buf);
+struct Shared {
+  union {
+    struct {
+      uint32_t cnt[kBins], ghi[kBins], glo[kBins];  // this slice's histogram
+    };
+    struct {
+      uint64_t list[kList], sums[kList];  // leader: gathered tokens, and their running sums
+      uint16_t bin_of[kList];
+      uint16_t first_in[kBins];  // where a bin's tokens begin
+    };
   };
-  // the least (key, index) up to which they sum up to more than `target`
-  auto search = [&](uint64_t target, uint64_t lo, uint64_t hi, bool count) {
+  uint64_t mass[kBins + 1];    // leader: the sums before a bin
+  uint32_t before[kBins + 1];  // leader: the tokens before it
+  uint32_t chosen[kBins / 32];  // bins whose tokens are gathered, by block
+  uint32_t listed;
+  uint64_t warp[2][kThreads / 32];
+  uint64_t said[2][kMostBlocks];  // by block
+  uint64_t part[2];               // leader
+  uint64_t want;                  // leader: what a border is looked for
+  int limit_bin, floor_bin;       // leader: of top_k and of min_p, kBins without one
+  float ch, cl, yh, yl;           // log2(e) / temperature, -log2(min_p)
+  Message message[2];             // one is read while the other is written
+  int found;
+};
+
+extern __shared__ __align__(16) char sample_shared[];
+constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
+// (By its own name: through a pointer that a function is handed, the compiler
+// would not know the memory, and its atomics took five times as long.)
+#define sh (*reinterpret_cast<Shared*>(sample_shared))
+
+template <class T>
+struct Sampler {
+  static constexpr int E = 16 / sizeof(T);  // elements of an access
+  const SampleIn<T>& in;
+  const int rank, blocks;
+  const T* x;        // this slice
+  bool held;         // whether shared memory has a copy
+  int n;             // its length
+  int start;         // its first index
+  bool wide;         // on 16 bytes
+  Row r;
+  mutable int turn = 0;  // of the messages
+
+  __device__ Sampler(const SampleIn<T>& i, int rk, int bl) : in(i), rank(rk), blocks(bl) {}
+  static __device__ __forceinline__ T* copy() {
+    return reinterpret_cast<T*>(sample_shared + kFixed);
+  }
+
+  __device__ __forceinline__ void sync() const {
+    if (blocks > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  }
+  // All of the cluster's blocks have begun, once this has been waited for.
+  __device__ __forceinline__ void begin() const {
+    if (blocks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  }
+  __device__ __forceinline__ void begun() const {
+    if (blocks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
+  template <class V>
+  __device__ __forceinline__ V* at(V* p, int block) const {
+    return blocks > 1 ? cg::this_cluster().map_shared_rank(p, block) : p;
+  }
+
+  __device__ __forceinline__ void unpack(uint4 q, float (&v)[E]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      if constexpr (sizeof(T) == 4) v[k] = __uint_as_float(w[k]);
+      else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        v[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+      else
+        v[k] = __half2float(__ushort_as_half((unsigned short)(w[k / 2] >> (k % 2 * 16))));
+    }
+  }
+
+  // f(logit, index) of every element of the slice. (An element at a time keeps
+  // the code short: f is long, and a call runs through it only a few times.)
+  template <int kUnroll, class F>
+  __device__ __forceinline__ void each(F f) const {
+    const T* const from = x;  // (copies: what f writes might be these, for the compiler)
+    const int end = n, first = start;
+    if (held) {
+#pragma unroll kUnroll
+      for (int i = threadIdx.x; i < end; i += kThreads) f(to_f32(copy()[i]), first + i);
+    } else {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < end; i += kThreads) f(to_f32(from[i]), first + i);
+    }
+  }
+
+  // The slice into shared memory; gives the thread's largest element.
+  __device__ __forceinline__ float load() const {
+    float top = -INFINITY;
+    const int whole = wide ? n / E * E : 0;
+#pragma unroll 4
+    for (int i = threadIdx.x * E; i < whole; i += kThreads * E) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + i));
+      if (held) *reinterpret_cast<uint4*>(copy() + i) = q;
+      float v[E];
+      unpack(q, v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) top = fmaxf(top, v[k]);
+    }
+#pragma unroll 4
+    for (int i = whole + threadIdx.x; i < n; i += kThreads) {
+      const T v = x[i];
+      if (held) copy()[i] = v;
+      top = fmaxf(top, to_f32(v));
+    }
+    return top;
+  }
+
+  // ------------------------------------------------ sums and extremes
+  // (Extremes are of values whose order is that of unsigned numbers.)
+  template <bool kMin>
+  __device__ uint64_t extreme(uint64_t v, int slot) const {  // over the cluster
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) {
+      const uint64_t o = __shfl_xor_sync(~0u, v, s);
+      v = kMin ? min(v, o) : max(v, o);
+    }
+    if (threadIdx.x % 32 == 0) sh.warp[slot][threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      v = sh.warp[slot][threadIdx.x % (kThreads / 32)];
+#pragma unroll
+      for (int s = 16; s > 0; s /= 2) {
+        const uint64_t o = __shfl_xor_sync(~0u, v, s);
+        v = kMin ? min(v, o) : max(v, o);
+      }
+      if (threadIdx.x < blocks) *at(&sh.said[slot][rank], threadIdx.x) = v;
+    }
+    sync();
+    v = sh.said[slot][0];
+    for (int b = 1; b < blocks; ++b) v = kMin ? min(v, sh.said[slot][b]) : max(v, sh.said[slot][b]);
+    return v;
+  }
+
+  // What a histogram's bins are.
+  enum Digit {
+    kCount,  // roughly those of place(), and only the number of tokens
+    kPlace,  // those of place(), their sums as masses
+    kKey,    // the keys lo..hi of m.bin, from lo on, 2^shift a bin
+    kIndex,  // the indices with the key lo, 1024 a bin
+  };
+  // Leaves the leader's running sums (in a bin's own units, but for kPlace).
+  __device__ __noinline__ void histogram(Digit digit, const Message& m, int shift) const {
+    __syncthreads();  // what the leader reads of its list is read
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+      sh.cnt[i] = 0;
+      if (digit != kCount) sh.ghi[i] = sh.glo[i] = 0;
+    }
+    __syncthreads();
+    uint32_t tops = 0, fars = 0;
+    const Row row = r;
+    const auto add = [](int d, uint32_t g) {
+      atomicAdd(&sh.cnt[d], 1u);
+      atomicAdd(&sh.ghi[d], g >> 14);
+      atomicAdd(&sh.glo[d], g & 0x3FFFu);
+    };
+    if (digit == kCount) {
+      each<4>([&, row](float l, int) {
+        if (!(l > -INFINITY)) return;
+        const float v = rough(row, l);
+        if (l == row.top) ++tops;
+        else if (!(v < (float)kFar)) ++fars;
+        else atomicAdd(&sh.cnt[(int)v], 1u);
+      });
+    } else if (digit == kPlace) {
+      each<4>([&, row](float l, int) {
+        uint32_t g;
+        int d;
+        const bool close = split(row, l, d, g), top = l == row.top;
+        // many may be alike there
+        tops += top;
+        fars += !close && !top && l > -INFINITY;
+        if (close && !top) add(d, g);
+      });
+    } else {
+      const int bin = m.bin;
+      const uint32_t lo = m.lo, hi = m.hi;
+      each<1>([&, row](float l, int i) {
+        if (!near(row, l, bin)) return;
+        const uint32_t k = order_key(l);
+        uint32_t g;
+        if (k < lo || k > hi || place(row, l, g) != bin) return;
+        add(digit == kKey ? (int)((k - lo) >> shift) : i >> kIndexDigits, g);
+      });
+    }
+    fars = __reduce_add_sync(~0u, fars);
+    tops = __reduce_add_sync(~0u, tops);
+    if (threadIdx.x % 32 == 0) {
+      if (tops) atomicAdd(&sh.cnt[0], tops);
+      if (fars) atomicAdd(&sh.cnt[kFar], fars);
+    }
+    sync();
+    // each block adds up a part of the bins, and tells the leader
+    const int share = kBins / blocks;
+    for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
+      uint32_t c[kMostBlocks], hi[kMostBlocks] = {}, lo[kMostBlocks] = {};
+#pragma unroll
+      for (int b = 0; b < kMostBlocks; ++b) {
+        c[b] = b < blocks ? at(sh.cnt, b)[i] : 0;
+        if (digit != kCount && b < blocks) hi[b] = at(sh.ghi, b)[i], lo[b] = at(sh.glo, b)[i];
+      }
+      uint32_t n = 0;
+      uint64_t g = 0;
+#pragma unroll
+      for (int b = 0; b < kMostBlocks; ++b) n += c[b], g += ((uint64_t)hi[b] << 14) + lo[b];
+      const uint64_t w = ((uint64_t)n << 33) - g;
+      at(sh.before, 0)[i] = n;
+      if (digit != kCount)
+        at(sh.mass, 0)[i] = digit != kPlace ? w : i == kFar ? 0 : mass_of(i, w);
+    }
+    sync();
+    if (rank == 0) running_sums();
+  }
+
+  // before and mass: from what a bin holds to what is before it
+  __device__ void running_sums() const {
+    constexpr int per = kBins / kThreads;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    uint32_t c[per], ct = 0;
+    uint64_t m[per], mt = 0;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      c[k] = sh.before[tid * per + k];
+      m[k] = sh.mass[tid * per + k];
+      ct += c[k];
+      mt += m[k];
+    }
+    uint32_t ci = ct;
+    uint64_t mi = mt;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const uint32_t a = __shfl_up_sync(~0u, ci, s);
+      const uint64_t b = __shfl_up_sync(~0u, mi, s);
+      if (lane >= s) ci += a, mi += b;
+    }
+    if (lane == 31) sh.warp[0][warp] = ci, sh.warp[1][warp] = mi;
+    __syncthreads();
+    uint32_t cb = ci - ct;
+    uint64_t mb = mi - mt;
+    for (int w = 0; w < warp; ++w) cb += (uint32_t)sh.warp[0][w], mb += sh.warp[1][w];
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      sh.before[tid * per + k] = cb;
+      sh.mass[tid * per + k] = mb;
+      cb += c[k];
+      mb += m[k];
+    }
+    if (tid == kThreads - 1) sh.before[kBins] = cb, sh.mass[kBins] = mb;
+    __syncthreads();
+  }
+
+  // Leader: the first bin up to which holds(number, sum) is true. before() is
+  // run by one thread first (GB300 has few binary64 units: a rounding of
+  // top_p times a sum by all of a block takes microseconds).
+  template <class F>
+  __device__ int first_bin(F holds) const {
+    return first_bin([] {}, holds);
+  }
+  template <class G, class F>
+  __device__ int first_bin(G before, F holds) const {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      before();
+      sh.found = kBins - 1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+      if (holds(sh.before[i + 1], sh.mass[i + 1]) && (i == 0 || !holds(sh.before[i], sh.mass[i])))
+        sh.found = i;
+    __syncthreads();
+    return sh.found;
+  }
+
+  // The leader's message, to all.
+  __device__ __forceinline__ void tell(const Message& m) const {
+    if (threadIdx.x < blocks) *at(&sh.message[turn], threadIdx.x) = m;
+  }
+  __device__ __forceinline__ Message hear() const {
+    sync();
+    const Message m = sh.message[turn];
+    turn ^= 1;
+    return m;
+  }
+
+  // Leader: the list sorted, with the running sums of its weights, in a bin's
+  // units or (masses) all in one; `number` of it.
+  __device__ __noinline__ void sort(int number, bool masses) const {
+    int size = 2;
+    while (size < number) size *= 2;
+    for (int i = number + threadIdx.x; i < size; i += kThreads) sh.list[i] = ~0ull;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2) {
+      for (int j = k / 2; j > 0; j /= 2) {
+        for (int p = threadIdx.x; p < size / 2; p += kThreads) {
+          const int i = 2 * p - (p & (j - 1)), o = i + j;
+          const uint64_t a = sh.list[i], b = sh.list[o];
+          if ((a > b) == ((i & k) == 0)) sh.list[i] = b, sh.list[o] = a;
+        }
+        __syncthreads();
+      }
+    }
+    constexpr int per = kList / kThreads;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    uint64_t m[per], mt = 0;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      const int i = tid * per + k;
+      m[k] = 0;
+      if (i < number) {
+        uint32_t g;
+        const int bin = place(r, key_logit((uint32_t)(sh.list[i] >> 32)), g);
+        m[k] = ((uint64_t)1 << 33) - g;
+        if (masses) {
+          m[k] = bin == kFar ? 0 : mass_of(bin, m[k]);
+          sh.bin_of[i] = (uint16_t)bin;
+        }
+      }
+      mt += m[k];
+    }
+    uint64_t mi = mt;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const uint64_t b = __shfl_up_sync(~0u, mi, s);
+      if (lane >= s) mi += b;
+    }
+    if (lane == 31) sh.warp[0][warp] = mi;
+    __syncthreads();
+    uint64_t mb = mi - mt;
+    for (int w = 0; w < warp; ++w) mb += sh.warp[0][w];
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      mb += m[k];
+      if (tid * per + k < number) sh.sums[tid * per + k] = mb;  // the element's own included
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ uint64_t weight_in_bin(uint32_t key) const {
+    uint32_t g;
+    place(r, key_logit(key), g);
+    return ((uint64_t)1 << 33) - g;
+  }
+
+  // What a border is the first place of: n tokens, or a mass of `want` with
+  // `base` before the bin.
+  struct Goal {
+    bool count;
+    int bin;
+    uint64_t want, base;
+    __device__ __forceinline__ bool operator()(uint64_t n, uint64_t sum) const {
+      return count ? n >= want : base + mass_of(bin, sum) >= want;
+    }
+  };
+  // A border in a bin.
+  struct Border {
+    int bin;
+    uint64_t number;  // tokens of the bin up to it
+    uint64_t sum;     // their weights
+    int64_t token;    // the last of them, where it was asked for
+  };
+
+  // The place in `bin` (of `number` tokens) that is the first where
+  // holds(number, sum) of the bin's tokens up to it. bin, number (0: nothing to
+  // be done) and holds are the leader's, as is the result; all blocks call it.
+  // used: whether the leader's running sums are gone.
+  __device__ __noinline__ Border look(int bin, uint32_t number, bool pick, bool& used,
+                                      Goal holds) const {
+    Border out = {bin, 0, 0, -1};
+    uint64_t nb = 0, sb = 0;  // tokens and weights before the keys lo..hi
+    uint32_t lo = 0, hi = kNone - 1;
+    if (rank == 0) tell({bin, lo, hi, number});
+    Message m = hear();
+    if (m.number == 0) return out;
+    used = used || m.number > kList;
+    while (m.number > kList) {
+      uint64_t kmin = kNone, kmax = 0;
+      each<1>([&](float l, int) {
+        if (!near(r, l, m.bin)) return;
+        const uint32_t k = order_key(l);
+        uint32_t g;
+        if (k < m.lo || k > m.hi || place(r, l, g) != m.bin) return;
+        kmin = min(kmin, (uint64_t)k);
+        kmax = max(kmax, (uint64_t)k);
+      });
+      m.lo = (uint32_t)extreme<true>(kmin, 0);
+      m.hi = (uint32_t)extreme<false>(kmax, 1);
+      if (m.lo == m.hi) return alike(m, nb, sb, pick, holds);
+      int shift = 32 - __clz(m.hi - m.lo) - 10;
+      if (shift < 0) shift = 0;
+      histogram(kKey, m, shift);
+      if (rank == 0) {
+        const int d = first_bin([&](uint32_t c, uint64_t s) { return holds(nb + c, sb + s); });
+        const uint32_t many = sh.before[d + 1] - sh.before[d];
+        nb += sh.before[d];
+        sb += sh.mass[d];
+        lo = m.lo + ((uint32_t)d << shift);
+        hi = lo + ((uint32_t)1 << shift) - 1;
+        tell({bin, lo, hi, many});
+      }
+      m = hear();
+    }
+    gather(m, false);
+    if (rank == 0) {
+      sort((int)m.number, false);
+      if (threadIdx.x == 0) sh.found = (int)m.number - 1;
+      __syncthreads();
+      for (int i = threadIdx.x; i < (int)m.number; i += kThreads)
+        if (holds(nb + i + 1, sb + sh.sums[i]) && (i == 0 || !holds(nb + i, sb + sh.sums[i - 1])))
+          sh.found = i;
+      __syncthreads();
+      out.number = nb + sh.found + 1;
+      out.sum = sb + sh.sums[sh.found];
+      out.token = (int64_t)(uint32_t)sh.list[sh.found];
+    }
+    return out;
+  }
+
+  // Collects the tokens of m.bin with keys lo..hi in the leader's list; of one
+  // key: those whose index is in [1024 bin, 1024 (bin + 1)).
+  __device__ __noinline__ void gather(const Message& m, bool one) const {
+    if (rank == 0 && threadIdx.x == 0) sh.listed = 0;
+    sync();
+    uint32_t* listed = at(&sh.listed, 0);
+    uint64_t* list = at(sh.list, 0);
+    const Row row = r;
+    const int bin = m.bin;
+    const uint32_t lo = m.lo, hi = m.hi;
+    each<4>([=](float l, int i) {
+      if (one ? i >> kIndexDigits != bin : !near(row, l, bin)) return;
+      const uint32_t k = order_key(l);
+      uint32_t g;
+      if (k < lo || k > hi || (!one && place(row, l, g) != bin)) return;
+      const uint32_t to = atomicAdd(listed, 1u);
+      if (to < (uint32_t)kList) list[to] = (uint64_t)k << 32 | (uint32_t)i;
+    });
+    sync();
+  }
+  // The same for all tokens whose rough bin is below `limit` (few), or whose bin
+  // is chosen, of bins from..to (!few).
+  __device__ __noinline__ void gather_chosen(bool few, int from, int to) const {
+    if (rank == 0 && threadIdx.x == 0) sh.listed = 0;
+    sync();
+    uint32_t* listed = at(&sh.listed, 0);
+    uint64_t* list = at(sh.list, 0);
+    const Row row = r;
+    const auto add = [=](float l, int i) {
+      const uint32_t at = atomicAdd(listed, 1u);
+      if (at < (uint32_t)kList) list[at] = (uint64_t)order_key(l) << 32 | (uint32_t)i;
+    };
+    if (few) {
+      const float limit = (float)(to + 1);
+      each<4>([=](float l, int i) {
+        if (rough(row, l) < limit || l == row.top) add(l, i);
+      });
+    } else {
+      const float mid = 0.5f * (float)(from + to + 1), half = 0.5f * (float)(to - from + 1) + 0.01f;
+      const bool tops = from == 0;
+      each<4>([=](float l, int i) {
+        const float v = rough(row, l);
+        if (!(fabsf(v - mid) < half) && !(tops && l == row.top)) return;
+        const int b = l == row.top ? 0 : (int)v;
+        const float f = v - (float)b;  // near an edge, place() may tell another bin
+        if ((sh.chosen[b / 32] >> b % 32 & 1) == 0 && f > 0.01f && f < 0.99f) return;
+        uint32_t g;
+        const int d = place(row, l, g);
+        if (sh.chosen[d / 32] >> d % 32 & 1) add(l, i);
+      });
+    }
+    sync();
+  }
+
+  // A warp: the first of n for which holds(i) (and for all after it), or n.
+  template <class F>
+  __device__ __forceinline__ int first_of(int n, F holds) const {
+    int lo = 0, hi = n;
+    const int lane = threadIdx.x % 32;
     while (lo < hi) {
-      const uint64_t mid = lo + (hi - lo) / 2;
-      if (upto(mid, count) > target) hi = mid;
-      else lo = mid + 1;
+      const int step = (hi - lo + 31) / 32, i = lo + step * (lane + 1) - 1;
+      const uint32_t yes = __ballot_sync(~0u, i >= hi || holds(i));
+      if (yes == 0) return hi;
+      const int k = __ffs(yes) - 1;
+      hi = min(hi, lo + step * (k + 1) - 1);
+      lo += step * k;
     }
     return lo;
+  }
+
+  // Masses that borders are looked for: at least 1, as the first is kept.
+  static __device__ __forceinline__ uint64_t share(double top_p, uint64_t kept) {
+    return max((unsigned long long)ceil(top_p * (double)kept), 1ull);
+  }
+  static __device__ __forceinline__ uint64_t beyond(double u, uint64_t kept) {
+    return (unsigned long long)(u * (double)kept) + 1;
+  }
+
+  // What limits a row, and its number; for the leader's first warp alone.
+  struct Limits {
+    uint64_t top_k;  // 0: none
+    double top_p, u;
+    bool least;
   };
-  uint64_t end = (uint64_t)0xFFFFFFFEu << 32 | 0xFFFFFFFFu;  // the last one kept
-  if (top_k > 0 && top_k < V && upto(end, true) > (uint64_t)top_k)
-    end = search((uint64_t)top_k - 1, least, end, true);
-  uint64_t all = upto(end, false);
-  if (top_p < 1.0) {
-    const double t = ceil((top_p > 0.0 ? top_p : 0.0) * (double)all);
-    // the first whose sum, itself included, reaches t
-    if (t >= 1.0) end = search((uint64_t)t - 1, least, end, false);
-    else end = least;
-  }
-  if (min_p > 0.0) {
-    // w >= min_p: y <= -log2(min_p)
-    const double y = fmax(-log2(min_p), 0.0) * 0x1p37;
-    uint64_t n = 0;
-    uint32_t worst = (uint32_t)(least >> 32);
-    for (int i = tid; i < V; i += kSampleThreads) {
-      const float l = to_f32(x[i]);
-      int bin;
-      uint32_t rest;
-      if (order_key(l) == 0xFFFFFFFFu || !far_down(r, l, bin, rest)) continue;
-      if ((double)((long long)bin << 32 | rest) <= y) worst = max(worst, order_key(l));
-      ++n;
+
+  // Leader's first warp: the bins in which the borders lie, as far as bins tell,
+  // to all blocks. A border's bin hangs on the sum of what the one before it
+  // keeps, of which a lower and an upper limit are known: all bins between.
+  // number 0: more tokens than the list holds.
+  __device__ __noinline__ void plan(const Limits& lim) const {
+    const int lane = threadIdx.x % 32;
+    uint32_t mine[kBins / 32 / 32] = {};  // of the chosen bins: words lane, lane + 32
+    uint32_t number = 0;
+    const auto choose = [&](int from, int to) {
+#pragma unroll
+      for (int k = 0; k < kBins / 32 / 32; ++k) {
+        const int w = (k * 32 + lane) * 32;
+        const int a = max(from - w, 0), b = min(to - w, 31);
+        if (a <= b) mine[k] |= (~0u >> (31 - (b - a))) << a;
+      }
+    };
+    const auto bin_of_mass = [&](uint64_t want) {
+      return min(first_of(kBins, [&](int i) { return sh.mass[i + 1] >= want; }), kBins - 1);
+    };
+    uint64_t lo = sh.mass[kBins], hi = lo;  // of the sum that is kept
+    int end = kBins, limit = kBins, floor_ = kBins;
+    if (lim.top_k > 0 && lim.top_k < sh.before[kBins]) {
+      const int d = first_of(kBins, [&](int i) { return sh.before[i + 1] >= lim.top_k; });
+      limit = end = d;
+      lo = sh.mass[d];
+      hi = sh.mass[d + 1];
+      if (d != kFar) choose(d, d);  // (the far bin weighs nothing)
     }
-    worst = __reduce_max_sync(~0u, worst);
-    __syncthreads();
-    if (tid % 32 == 0) buf[tid / 32] = worst;
-    __syncthreads();
-    worst = __reduce_max_sync(~0u, (uint32_t)buf[tid % 32]);
-    __syncthreads();
-    end = min(end, (uint64_t)worst << 32 | 0xFFFFFFFFu);
+    if (lim.top_p < 1.0) {
+      const int a = bin_of_mass(share(lim.top_p, lo)), b = bin_of_mass(share(lim.top_p, hi));
+      choose(a, b);
+      end = min(end, b);
+      lo = sh.mass[a];
+      hi = min(hi, sh.mass[b + 1]);
+    }
+    if (lim.least) {
+      uint32_t g;
+      const int d = place(r, key_logit(last_key()), g);
+      if (d <= end) {
+        floor_ = d;
+        if (d != kFar) choose(d, d);
+        lo = min(lo, sh.mass[d]);
+        hi = min(hi, sh.mass[d + 1]);
+      }
+    }
+    choose(bin_of_mass(beyond(lim.u, lo)), bin_of_mass(beyond(lim.u, hi)));
+#pragma unroll
+    for (int k = 0; k < kBins / 32 / 32; ++k) {
+      const int w = k * 32 + lane;
+      for (uint32_t left = mine[k]; left != 0; left &= left - 1) {
+        const int d = w * 32 + __ffs(left) - 1;
+        number += sh.before[d + 1] - sh.before[d];
+      }
+      for (int b = 0; b < blocks; ++b) *at(&sh.chosen[w], b) = mine[k];
+    }
+    number = __reduce_add_sync(~0u, number);
+    uint32_t least = kBins, most = 0;
+#pragma unroll
+    for (int k = 0; k < kBins / 32 / 32; ++k) {
+      if (mine[k] == 0) continue;
+      least = min(least, (uint32_t)((k * 32 + lane) * 32 + __ffs(mine[k]) - 1));
+      most = max(most, (uint32_t)((k * 32 + lane) * 32 + 31 - __clz(mine[k])));
+    }
+    least = __reduce_min_sync(~0u, least);
+    most = __reduce_max_sync(~0u, most);
+    if (lane == 0) sh.limit_bin = limit, sh.floor_bin = floor_;
+    tell({0, least, most, number > (uint32_t)kList ? 0 : number});
   }
-  all = upto(end, false);
-  const float u = in.u[row];
-  const double at = (u > 0.0f ? fmin((double)u, 1.0 - 0x1p-24) : 0.0) * (double)all;
-  const uint64_t got = search((uint64_t)at, least, end, false);
-  if (tid == 0) tokens[row] = (int64_t)(uint32_t)got;
+
+  // Leader: the token, of the first m.number tokens of all.
+  __device__ __noinline__ int64_t among_few(int number, const Limits& lim) const {
+    sort(number, true);
+    if (threadIdx.x >= 32) return -1;
+    int n = (int)min((uint64_t)number, lim.top_k);
+    if (lim.top_p < 1.0) {
+      const uint64_t want = share(lim.top_p, sh.sums[n - 1]);
+      n = min(n, 1 + first_of(n, [&](int i) { return sh.sums[i] >= want; }));
+    }
+    if (lim.least)
+      n = max(1, first_of(n, [&](int i) { return !at_most((uint32_t)(sh.list[i] >> 32)); }));
+    const uint64_t want = beyond(lim.u, sh.sums[n - 1]);
+    const int i = first_of(n, [&](int k) { return sh.sums[k] >= want; });
+    return (int64_t)(uint32_t)sh.list[min(i, n - 1)];
+  }
+
+  // Leader: the token, where the list has all tokens of the bins of plan().
+  __device__ __noinline__ int64_t among_chosen(int number, const Limits& lim) const {
+    sort(number, true);
+    // sums from the row's first token on; a bin's last one agrees with its sum
+    for (int i = threadIdx.x; i < number; i += kThreads)
+      if (i == 0 || sh.bin_of[i] != sh.bin_of[i - 1]) sh.first_in[sh.bin_of[i]] = (uint16_t)i;
+    __syncthreads();
+    uint64_t sum[kList / kThreads];
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i >= number) continue;
+      const int d = sh.bin_of[i], f = sh.first_in[d];
+      sum[k] = sh.mass[d] + sh.sums[i] - (f > 0 ? sh.sums[f - 1] : 0);
+      if (i + 1 == number || sh.bin_of[i + 1] != d) sum[k] = sh.mass[d + 1];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < number) sh.sums[i] = sum[k];
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32) return -1;
+    const auto place_of = [&](int i) {  // tokens up to this one
+      const int d = sh.bin_of[i];
+      return sh.before[d] + (uint32_t)(i - sh.first_in[d] + 1);
+    };
+    const auto reaches = [&](uint64_t want) {
+      return min(number - 1, first_of(number, [&](int i) { return sh.sums[i] >= want; }));
+    };
+    uint64_t kept = sh.mass[kBins];
+    uint32_t end = sh.before[kBins];
+    if (sh.limit_bin == kFar) {
+      end = (uint32_t)lim.top_k;
+    } else if (sh.limit_bin < kBins) {
+      const int i = min(number - 1, first_of(number, [&](int k) {
+                          return place_of(k) >= (uint32_t)lim.top_k;
+                        }));
+      end = place_of(i);
+      kept = sh.sums[i];
+    }
+    if (lim.top_p < 1.0) {
+      const int i = reaches(share(lim.top_p, kept));
+      end = place_of(i);
+      kept = sh.sums[i];
+    }
+    if (sh.floor_bin < kBins) {
+      const int d = sh.floor_bin;
+      const int j = first_of(number, [&](int i) { return !at_most((uint32_t)(sh.list[i] >> 32)); });
+      const bool in = j > 0 && sh.bin_of[j - 1] == d;  // else none of its bin
+      const uint32_t many = in ? place_of(j - 1) : sh.before[d];
+      if (many < end) kept = in ? sh.sums[j - 1] : sh.mass[d];
+    }
+    return (int64_t)(uint32_t)sh.list[reaches(beyond(lim.u, kept))];
+  }
+
+  // look() among m.number tokens of one logit (the key m.lo), more than can be
+  // sorted.
+  __device__ __noinline__ Border alike(Message m, uint64_t nb, uint64_t sb, bool pick,
+                                       Goal holds) const {
+    Border out = {m.bin, 0, 0, -1};
+    const uint64_t w = weight_in_bin(m.lo);
+    uint32_t lo = 1, hi = m.number;  // the first for which it holds
+    if (rank == 0) {
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (holds(nb + mid, sb + mid * w)) hi = mid;
+        else lo = mid + 1;
+      }
+      out.number = nb + lo;
+      out.sum = sb + lo * w;
+    }
+    if (!pick) return out;
+    // the lo-th by index
+    histogram(kIndex, m, 0);
+    if (rank == 0) {
+      const int d = first_bin([&](uint32_t c, uint64_t) { return c >= lo; });
+      tell({d, m.lo, m.lo, sh.before[d + 1] - sh.before[d]});
+      lo -= sh.before[d];
+    }
+    m = hear();
+    gather(m, true);
+    if (rank == 0) {
+      sort((int)m.number, false);
+      out.token = (int64_t)(uint32_t)sh.list[lo - 1];
+    }
+    return out;
+  }
+
+  // Leader: the last key whose y is at most -log2(min_p) (y rises with the key).
+  __device__ uint32_t last_key() const {
+    uint32_t lo = order_key(r.top), hi = kNone - 1;  // lo always is one
+    const int lane = threadIdx.x % 32;
+    while (lo < hi) {
+      const uint32_t step = (hi - lo + 31) / 32;
+      const uint64_t k = (uint64_t)lo + (uint64_t)step * (lane + 1);
+      const bool in = k <= hi && at_most((uint32_t)k);
+      const int many = __popc(__ballot_sync(~0u, in));
+      const uint64_t next = (uint64_t)lo + (uint64_t)step * (many + 1) - 1;
+      lo += step * many;
+      hi = (uint32_t)min((uint64_t)hi, next);
+    }
+    return lo;
+  }
+  __device__ __forceinline__ bool at_most(uint32_t key) const {
+    const float l = key_logit(key);
+    if (l == r.top) return true;
+    const float s = r.top - l, bb = r.top - s, e = (r.top - (s + bb)) + (bb - l);
+    const float yh = s * r.ch;
+    if (!(yh < 256.0f)) return false;  // min_p is 2^-149 at least
+    const float yl = fmaf(e, r.ch, fmaf(s, r.cl, fmaf(s, r.ch, -yh)));
+    return (yh - sh.yh) + (yl - sh.yl) <= 0.0f;
+  }
+
+  // Leader: number and sum of the tokens of `bin` whose key is at most `last`
+  // (leader's too; 0: nothing to be done).
+  __device__ Border upto(int bin, uint32_t last) const {
+    Border out = {bin, 0, 0, -1};
+    if (rank == 0) {
+      if (threadIdx.x < 2) sh.part[threadIdx.x] = 0;
+      tell({bin, 0, last, 0});
+    }
+    const Message m = hear();
+    if (m.hi == 0) return out;
+    uint64_t c = 0, s = 0;
+    const Row row = r;
+    each<4>([&, row](float l, int) {
+      if (!near(row, l, m.bin) || order_key(l) > m.hi) return;
+      uint32_t g;
+      if (place(row, l, g) != m.bin) return;
+      ++c;
+      s += ((uint64_t)1 << 33) - g;
+    });
+#pragma unroll
+    for (int k = 16; k > 0; k /= 2) {
+      c += __shfl_xor_sync(~0u, c, k);
+      s += __shfl_xor_sync(~0u, s, k);
+    }
+    if (threadIdx.x % 32 == 0 && c != 0) {
+      atomicAdd((unsigned long long*)at(&sh.part[0], 0), (unsigned long long)c);
+      atomicAdd((unsigned long long*)at(&sh.part[1], 0), (unsigned long long)s);
+    }
+    sync();
+    if (rank == 0) out.number = sh.part[0], out.sum = sh.part[1];
+    return out;
+  }
+
+  __device__ int64_t run(int64_t row);
+  __device__ __noinline__ int64_t one_by_one(const Limits& lim) const;
+};
+
+template <class T>
+__device__ int64_t Sampler<T>::run(int64_t row) {
+  const float* ts = in.temperatures;
+  const float *ps = in.top_ps, *ms = in.min_ps;
+  const double top_p = ps != nullptr ? ps[row] : in.top_p;
+  const bool cold = !(ts != nullptr ? ts[row] > 0.0f : in.temperature > 0.0);
+  const bool least = ms != nullptr ? ms[row] > 0.0f : in.min_p > 0.0;
+  const int64_t top_k = in.top_ks != nullptr ? load_index(in.top_ks, in.index_bytes, row) : in.top_k;
+  // what takes binary64, by a thread each
+  if (threadIdx.x == 0) {
+    const double c = fmin(1.4426950408889634 / (ts != nullptr ? ts[row] : in.temperature), 1e37);
+    sh.ch = (float)c;
+    sh.cl = (float)(c - (double)sh.ch);
+  }
+  if (threadIdx.x == 32 && rank == 0 && least) {
+    const double y = fmax(-log2(ms != nullptr ? (double)ms[row] : in.min_p), 0.0);
+    sh.yh = (float)y;
+    sh.yl = (float)(y - (double)sh.yh);
+  }
+
+  begin();
+  const float mine = load();
+  begun();
+  const uint32_t top = (uint32_t)extreme<true>((uint64_t)order_key(mine), 0);
+  if (top == kNone) return -1;
+  r.top = key_logit(top);
+  if (cold || top_k == 1 || top_p <= 0.0) {
+    uint64_t first = ~0ull;
+    each<4>([&](float l, int i) {
+      if (l == r.top) first = min(first, (uint64_t)i);
+    });
+    return (int64_t)extreme<true>(first, 1);
+  }
+  r.ch = sh.ch;
+  r.cl = sh.cl;
+  const float u0 = in.u[row];
+  const Limits lim = {top_k > 0 ? (uint64_t)top_k : 0, top_p,
+                      u0 > 0.0f ? fmin((double)u0, 1.0 - 0x1p-24) : 0.0, least};
+  // A few tokens by top_k: these and no others, from a histogram of numbers.
+  if (top_k > 0 && top_k <= kFew) {
+    histogram(kCount, {}, 0);
+    if (rank == 0 && threadIdx.x < 32) {
+      const int d = min(first_of(kBins, [&](int i) { return sh.before[i + 1] >= lim.top_k; }),
+                        kBins - 1);
+      const uint32_t n = sh.before[d + 1];
+      tell({d, 0, 0, n > (uint32_t)kList || d == kFar ? 0 : n});
+    }
+    const Message m = hear();
+    if (m.number != 0) {
+      gather_chosen(true, 0, m.bin);
+      return rank == 0 ? among_few((int)m.number, lim) : -1;
+    }
+  }
+  // Otherwise the borders' bins, from the sums of all.
+  histogram(kPlace, {}, 0);
+  if (rank == 0 && threadIdx.x < 32) plan(lim);
+  {
+    const Message m = hear();
+    if (m.number != 0) {
+      gather_chosen(false, (int)m.lo, (int)m.hi);
+      return rank == 0 ? among_chosen((int)m.number, lim) : -1;
+    }
+  }
+  return one_by_one(lim);
+}
+
+// The borders one after the other, where their bins hold more tokens than the
+// list: each bin is cut until its border's part fits.
+template <class T>
+__device__ __noinline__ int64_t Sampler<T>::one_by_one(const Limits& lim) const {
+  const uint64_t top_k = lim.top_k;
+  const double top_p = lim.top_p;
+  const bool least = lim.least;
+  const auto bins = [&] { histogram(kPlace, {}, 0); };
+
+  // The last bin of what is kept, how many of its tokens, and the sum of all of
+  // it (the leader's; all blocks know which limits there are).
+  bool used = false;
+  int end = kBins;
+  uint64_t number = 0, kept = rank == 0 ? sh.mass[kBins] : 0, base = 0;
+  if (top_k > 0) {
+    int d = 0;
+    uint32_t many = 0;
+    uint64_t want = 0;
+    if (rank == 0 && top_k < sh.before[kBins]) {
+      d = first_bin([&](uint32_t n, uint64_t) { return n >= top_k; });
+      want = top_k - sh.before[d];
+      many = sh.before[d + 1] - sh.before[d];
+      base = sh.mass[d];
+      end = d;
+      number = want;
+      kept = sh.mass[d + 1];
+      if (d == kFar || want == many) many = 0;  // weightless, or the whole bin
+    }
+    const Border b = look(d, many, false, used, {true, d, want, 0});
+    if (many != 0) kept = base + mass_of(d, b.sum);
+  }
+  if (top_p < 1.0) {
+    if (used) bins();
+    used = false;
+    int d = 0;
+    uint32_t many = 0;
+    uint64_t want = 0;
+    if (rank == 0) {
+      d = first_bin(
+          [&] { sh.want = share(top_p, kept); },
+          [&](uint32_t, uint64_t s) { return s >= sh.want; });
+      want = sh.want;
+      many = sh.before[d + 1] - sh.before[d];
+      base = sh.mass[d];
+      end = d;
+      number = many;
+      kept = sh.mass[d + 1];
+      if (many == 1) many = 0;
+    }
+    const Border b = look(d, many, false, used, {false, d, want, base});
+    if (many != 0) number = b.number, kept = base + mass_of(d, b.sum);
+  }
+  if (least) {
+    if (used) bins();
+    used = false;
+    int d = 0;
+    uint32_t last = 0;
+    if (rank == 0) {
+      last = last_key();
+      uint32_t g;
+      d = place(r, key_logit(last), g);
+      base = sh.mass[d];
+      if (d > end) last = 0;
+    }
+    const Border b = upto(d, last);
+    if (last != 0 && (d < end || b.number < number)) kept = base + mass_of(d, b.sum);
+  }
+  if (used) bins();
+  int d = 0;
+  uint32_t many = 0;
+  uint64_t want = 0;
+  if (rank == 0) {
+    d = first_bin(
+        [&] { sh.want = beyond(lim.u, kept); },
+        [&](uint32_t, uint64_t s) { return s >= sh.want; });
+    want = sh.want;
+    many = sh.before[d + 1] - sh.before[d];
+    base = sh.mass[d];
+  }
+  return look(d, many, true, used, {false, d, want, base}).token;
+}
+
+#ifndef CR_SAMPLE_RES
+#define CR_SAMPLE_RES 2
+#endif
+template <class T>
+__global__ void __launch_bounds__(kThreads, CR_SAMPLE_RES)
+sample_kernel(SampleIn<T> in, int64_t* __restrict__ tokens, int blocks, int slice, bool hold,
+              bool wide) {
+  const int rank = (int)(blockIdx.x % (unsigned)blocks);
+  const int64_t row = blockIdx.x / (unsigned)blocks;
+  Sampler<T> s(in, rank, blocks);
+  s.start = rank * slice;
+  s.n = max(0, min(slice, (int)in.vocab - s.start));
+  s.x = in.logits + row * in.stride + (s.n > 0 ? s.start : 0);
+  s.held = hold;
+  s.wide = wide;
+  // (What a block reads or writes of another is followed by a wait for all of
+  // them, so that none is gone too early.)
+  const int64_t token = s.run(row);
+  if (rank == 0 && threadIdx.x == 0) tokens[row] = token;
+}
+
+#ifndef CR_SAMPLE_SLICE
+#define CR_SAMPLE_SLICE 8192
+#endif
+#undef sh
+
+// Blocks a row.
+int sample_blocks(int64_t rows, int64_t vocab) {
+  int c = 1;
+  while (c < kMostBlocks && vocab > (int64_t)c * CR_SAMPLE_SLICE) c *= 2;
+  return c;
 }
 
 }  // namespace
@@ -221,16 +1080,23 @@ cr_status cr_sample(const cr_sample_args* a, int64_t* tokens, void* stream) {
       (a->top_ks != nullptr && !ptr_aligned(a->top_ks, a->index_bytes)) ||
       overwrites({tokens}, {a->logits, a->u, a->temperatures, a->top_ps, a->min_ps, a->top_ks}))
     return CR_ERR_INVALID_ARG;
-  if (a->vocab > (int64_t)1 << 20 || a->rows > kMaxBlocks) return CR_ERR_UNSUPPORTED;
+  if (a->vocab > (int64_t)1 << 20 || a->rows > kMaxBlocks / kMostBlocks) return CR_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int blocks = sample_blocks(a->rows, a->vocab);
+  const int slice = (int)ceil_div(ceil_div(a->vocab, blocks), 8) * 8;
+  const bool hold = kFixed + slice * es <= 200 * 1024;
+  const size_t smem = kFixed + (hold ? slice * es : 0);
+  const bool wide = rows_aligned(a->logits, a->row_stride, 0, es, 16);
+  bool done = false;
   CR_MODEL_TYPE(a->dt, {
     const SampleIn<T> in = {a->vocab, static_cast<const T*>(a->logits), a->row_stride, a->u,
                             a->temperature, a->top_p, a->min_p, a->top_k, a->temperatures,
                             a->top_ps, a->min_ps, a->top_ks, a->index_bytes};
     CR_LAUNCH(kKSample, s,
-              sample_kernel<T><<<(unsigned)a->rows, kSampleThreads, 0, s>>>(in, tokens));
+              done = launch_clusters(sample_kernel<T>, a->rows * blocks, blocks, kThreads, smem, s,
+                                     in, tokens, blocks, slice, hold, wide));
   });
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -505,7 +505,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
 
     Each setting is a number, or a tensor (...) with one a row: float32, and
     int32 or int64 for top_k. The result is that of exact arithmetic (weights to
-    2^-35, sums in integers) and never differentiated."""
+    2^-32, sums in integers) and never differentiated."""
     return _native.sample(logits, u, temperature, top_k, top_p, min_p, out, stream)
 
 
