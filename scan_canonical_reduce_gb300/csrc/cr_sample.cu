@@ -14,6 +14,7 @@
 // A row is one cluster of blocks, a slice each, held in shared memory where it
 // fits. The first block leads: it has the row's sums and the list of a bin.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include <cooperative_groups.h>
@@ -30,6 +31,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kBins = 1024;   // 16 an octave
 constexpr int kList = 1024;   // most tokens that are sorted
+constexpr int kRanked = 128;  // up to so many by their ranks
 constexpr int kFew = 512;     // top_k up to which its tokens alone are looked at
 constexpr int kMostBlocks = 8;
 constexpr uint32_t kNone = 0xFFFFFFFFu;  // the key of what is no candidate
@@ -114,17 +116,57 @@ __device__ __forceinline__ bool near(const Row& r, float l, int bin) {
   return fabsf(rough(r, l) - ((float)bin + 0.5f)) < 0.51f || (bin == 0 && l == r.top);
 }
 
+// A row's settings, as the kernel works with them. (GB300 has few binary64
+// units: a division by all of a block takes microseconds. What binary64 is
+// needed for is done by the host, by one warp, or in pairs of binary32.)
+struct Settings {
+  float ch, cl;    // log2(e) / temperature, in two numbers
+  bool cold;       // the first token, whatever u
+  uint64_t top_k;  // 0: no limit
+  double top_p;    // 1: no limit
+  uint64_t min_w;  // the least weight that is kept, in units of 2^-42; 0: no limit
+};
+constexpr double kLog2eD = 1.4426950408889634;
+constexpr float kLog2eHi = (float)kLog2eD, kLog2eLo = (float)(kLog2eD - (double)kLog2eHi);
+
 template <class T>
 struct SampleIn {
   int64_t vocab;
   const T* logits;
   int64_t stride;
   const float* u;
-  double temperature, top_p, min_p;
-  int64_t top_k;
+  Settings all;  // for every row, but for what has an array
   const float *temperatures, *top_ps, *min_ps;
   const void* top_ks;
   int32_t index_bytes;
+
+  __device__ __forceinline__ Settings of(int64_t row) const {
+    Settings s = all;
+    if (temperatures != nullptr) {
+      const float t = temperatures[row];
+      s.cold = !(t > 0.0f);
+      s.ch = fminf(kLog2eHi / t, 1e37f);
+      s.cl = (fmaf(-s.ch, t, kLog2eHi) + kLog2eLo) / t;
+      if (!(fabsf(s.cl) < s.ch)) s.cl = 0.0f;  // the ends of the range
+    }
+    if (top_ks != nullptr) {
+      const int64_t k = load_index(top_ks, index_bytes, row);
+      s.top_k = k > 0 ? (uint64_t)k : 0;
+    }
+    if (top_ps != nullptr) {
+      const float p = top_ps[row];
+      s.top_p = p < 1.0f ? (double)fmaxf(p, 0.0f) : 1.0;
+    }
+    if (min_ps != nullptr) {
+      const float p = min_ps[row];
+      s.min_w = p > 0.0f ? __float2ull_ru(fminf(p, 1.0f) * 0x1p42f) : 0;
+    }
+    return s;
+  }
+  __device__ __forceinline__ uint64_t uniform(int64_t row) const {  // in units of 2^-64
+    const float v = u[row];
+    return v > 0.0f ? __float2ull_rn(fminf(v, 1.0f - 0x1p-24f) * 0x1p64f) : 0;
+  }
 };
 
 // What the leader tells the others.
@@ -140,21 +182,22 @@ struct Shared {
       uint32_t cnt[kBins], ghi[kBins], glo[kBins];  // this slice's histogram
     };
     struct {
+      uint32_t kept[kBins];  // (a histogram of numbers is still read when the list is begun)
       uint64_t list[kList], sums[kList];  // leader: gathered tokens, and their running sums
       uint16_t bin_of[kList];
       uint16_t first_in[kBins];  // where a bin's tokens begin
     };
   };
-  uint64_t mass[kBins + 1];    // leader: the sums before a bin
-  uint32_t before[kBins + 1];  // leader: the tokens before it
-  uint32_t chosen[kBins / 32];  // bins whose tokens are gathered, by block
+  uint64_t mass[kBins + 1];     // the sums before a bin
+  uint32_t before[kBins + 1];   // the tokens before it
+  uint32_t chosen[kBins / 32];  // bins whose tokens are gathered
+  uint32_t number, from, to;    // of those tokens and bins
   uint32_t listed;
   uint64_t warp[2][kThreads / 32];
   uint64_t said[2][kMostBlocks];  // by block
   uint64_t part[2];               // leader
   uint64_t want;                  // leader: what a border is looked for
-  int limit_bin, floor_bin;       // leader: of top_k and of min_p, kBins without one
-  float ch, cl, yh, yl;           // log2(e) / temperature, -log2(min_p)
+  int limit_bin, floor_bin;       // of top_k and of min_p, kBins without one
   Message message[2];             // one is read while the other is written
   int found;
 };
@@ -281,12 +324,16 @@ struct Sampler {
     kKey,    // the keys lo..hi of m.bin, from lo on, 2^shift a bin
     kIndex,  // the indices with the key lo, 1024 a bin
   };
-  // Leaves the leader's running sums (in a bin's own units, but for kPlace).
-  __device__ __noinline__ void histogram(Digit digit, const Message& m, int shift) const {
-    __syncthreads();  // what the leader reads of its list is read
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      sh.cnt[i] = 0;
-      if (digit != kCount) sh.ghi[i] = sh.glo[i] = 0;
+  // Leaves the running sums (in a bin's own units, but for kPlace). clean: the
+  // bins are empty.
+  __device__ __forceinline__ void clear() const {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.ghi[i] = sh.glo[i] = 0;
+  }
+  __device__ __noinline__ void histogram(Digit digit, const Message& m, int shift,
+                                         bool clean = false) const {
+    if (!clean) {
+      __syncthreads();  // what the leader reads of its list is read
+      clear();
     }
     __syncthreads();
     uint32_t tops = 0, fars = 0;
@@ -332,26 +379,42 @@ struct Sampler {
       if (fars) atomicAdd(&sh.cnt[kFar], fars);
     }
     sync();
-    // each block adds up a part of the bins, and tells the leader
+    if (digit == kCount) {  // every block adds up all of them
+      for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        uint32_t c[kMostBlocks], n = 0;
+#pragma unroll
+        for (int b = 0; b < kMostBlocks; ++b) c[b] = b < blocks ? at(sh.cnt, b)[i] : 0;
+#pragma unroll
+        for (int b = 0; b < kMostBlocks; ++b) n += c[b];
+        sh.before[i] = n;
+        sh.mass[i] = 0;
+      }
+      __syncthreads();
+      running_sums();
+      return;
+    }
+    // each block adds up a part of the bins, and tells the others
     const int share = kBins / blocks;
     for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
-      uint32_t c[kMostBlocks], hi[kMostBlocks] = {}, lo[kMostBlocks] = {};
+      uint32_t c[kMostBlocks], hi[kMostBlocks], lo[kMostBlocks], n = 0;
+      uint64_t g = 0;
 #pragma unroll
       for (int b = 0; b < kMostBlocks; ++b) {
         c[b] = b < blocks ? at(sh.cnt, b)[i] : 0;
-        if (digit != kCount && b < blocks) hi[b] = at(sh.ghi, b)[i], lo[b] = at(sh.glo, b)[i];
+        hi[b] = b < blocks ? at(sh.ghi, b)[i] : 0;
+        lo[b] = b < blocks ? at(sh.glo, b)[i] : 0;
       }
-      uint32_t n = 0;
-      uint64_t g = 0;
 #pragma unroll
       for (int b = 0; b < kMostBlocks; ++b) n += c[b], g += ((uint64_t)hi[b] << 14) + lo[b];
-      const uint64_t w = ((uint64_t)n << 33) - g;
-      at(sh.before, 0)[i] = n;
-      if (digit != kCount)
-        at(sh.mass, 0)[i] = digit != kPlace ? w : i == kFar ? 0 : mass_of(i, w);
+      uint64_t w = ((uint64_t)n << 33) - g;
+      if (digit == kPlace) w = i == kFar ? 0 : mass_of(i, w);
+      for (int b = 0; b < blocks; ++b) {
+        at(sh.before, b)[i] = n;
+        at(sh.mass, b)[i] = w;
+      }
     }
     sync();
-    if (rank == 0) running_sums();
+    running_sums();
   }
 
   // before and mass: from what a bin holds to what is before it
@@ -416,6 +479,7 @@ struct Sampler {
   // The leader's message, to all.
   __device__ __forceinline__ void tell(const Message& m) const {
     if (threadIdx.x < blocks) *at(&sh.message[turn], threadIdx.x) = m;
+    if (threadIdx.x == 0) sh.listed = 0;  // of the gather that may follow
   }
   __device__ __forceinline__ Message hear() const {
     sync();
@@ -427,8 +491,21 @@ struct Sampler {
   // Leader: the list sorted, with the running sums of its weights, in a bin's
   // units or (masses) all in one; `number` of it.
   __device__ __noinline__ void sort(int number, bool masses) const {
+    if (number <= kRanked) {  // each finds its rank among all
+      uint64_t mine = 0;
+      int place_ = 0;
+      const bool one = threadIdx.x < number;
+      if (one) {
+        mine = sh.list[threadIdx.x];
+#pragma unroll 8
+        for (int i = 0; i < number; ++i) place_ += sh.list[i] < mine;
+      }
+      __syncthreads();
+      if (one) sh.list[place_] = mine;
+    }
     int size = 2;
     while (size < number) size *= 2;
+    if (number <= kRanked) size = 0;
     for (int i = number + threadIdx.x; i < size; i += kThreads) sh.list[i] = ~0ull;
     __syncthreads();
     for (int k = 2; k <= size; k *= 2) {
@@ -559,8 +636,6 @@ struct Sampler {
   // Collects the tokens of m.bin with keys lo..hi in the leader's list; of one
   // key: those whose index is in [1024 bin, 1024 (bin + 1)).
   __device__ __noinline__ void gather(const Message& m, bool one) const {
-    if (rank == 0 && threadIdx.x == 0) sh.listed = 0;
-    sync();
     uint32_t* listed = at(&sh.listed, 0);
     uint64_t* list = at(sh.list, 0);
     const Row row = r;
@@ -579,8 +654,6 @@ struct Sampler {
   // The same for all tokens whose rough bin is below `limit` (few), or whose bin
   // is chosen, of bins from..to (!few).
   __device__ __noinline__ void gather_chosen(bool few, int from, int to) const {
-    if (rank == 0 && threadIdx.x == 0) sh.listed = 0;
-    sync();
     uint32_t* listed = at(&sh.listed, 0);
     uint64_t* list = at(sh.list, 0);
     const Row row = r;
@@ -626,23 +699,21 @@ struct Sampler {
     return lo;
   }
 
-  // Masses that borders are looked for: at least 1, as the first is kept.
-  static __device__ __forceinline__ uint64_t share(double top_p, uint64_t kept) {
-    return max((unsigned long long)ceil(top_p * (double)kept), 1ull);
+  // Masses that borders are looked for: p kept, rounded up, and at least 1, as the
+  // first is kept (the product is one of binary64, where 0.9 of 10 is 9); the
+  // first that exceeds u kept, u in units of 2^-64.
+  static __device__ __forceinline__ uint64_t share(double p, uint64_t kept) {
+    return max((unsigned long long)ceil(p * (double)kept), 1ull);
   }
-  static __device__ __forceinline__ uint64_t beyond(double u, uint64_t kept) {
-    return (unsigned long long)(u * (double)kept) + 1;
+  static __device__ __forceinline__ uint64_t beyond(uint64_t u, uint64_t kept) {
+    return __umul64hi(u, kept) + 1;
   }
-
-  // What limits a row, and its number; for the leader's first warp alone.
-  struct Limits {
-    uint64_t top_k;  // 0: none
-    double top_p, u;
-    bool least;
+  struct Limits : Settings {
+    uint64_t u;
   };
 
-  // Leader's first warp: the bins in which the borders lie, as far as bins tell,
-  // to all blocks. A border's bin hangs on the sum of what the one before it
+  // A block's first warp: the bins in which the borders lie, as far as bins tell.
+  // A border's bin hangs on the sum of what the one before it
   // keeps, of which a lower and an upper limit are known: all bins between.
   // number 0: more tokens than the list holds.
   __device__ __noinline__ void plan(const Limits& lim) const {
@@ -676,9 +747,8 @@ struct Sampler {
       lo = sh.mass[a];
       hi = min(hi, sh.mass[b + 1]);
     }
-    if (lim.least) {
-      uint32_t g;
-      const int d = place(r, key_logit(last_key()), g);
+    if (lim.min_w != 0) {  // the last bin whose weights may be that large
+      const int d = first_of(kBins, [&](int i) { return mass_of(i, 1ull << 33) < lim.min_w; }) - 1;
       if (d <= end) {
         floor_ = d;
         if (d != kFar) choose(d, d);
@@ -694,7 +764,7 @@ struct Sampler {
         const int d = w * 32 + __ffs(left) - 1;
         number += sh.before[d + 1] - sh.before[d];
       }
-      for (int b = 0; b < blocks; ++b) *at(&sh.chosen[w], b) = mine[k];
+      sh.chosen[w] = mine[k];
     }
     number = __reduce_add_sync(~0u, number);
     uint32_t least = kBins, most = 0;
@@ -706,8 +776,13 @@ struct Sampler {
     }
     least = __reduce_min_sync(~0u, least);
     most = __reduce_max_sync(~0u, most);
-    if (lane == 0) sh.limit_bin = limit, sh.floor_bin = floor_;
-    tell({0, least, most, number > (uint32_t)kList ? 0 : number});
+    if (lane == 0) {
+      sh.limit_bin = limit;
+      sh.floor_bin = floor_;
+      sh.number = number > (uint32_t)kList ? 0 : number;
+      sh.from = least;
+      sh.to = most;
+    }
   }
 
   // Leader: the token, of the first m.number tokens of all.
@@ -719,8 +794,8 @@ struct Sampler {
       const uint64_t want = share(lim.top_p, sh.sums[n - 1]);
       n = min(n, 1 + first_of(n, [&](int i) { return sh.sums[i] >= want; }));
     }
-    if (lim.least)
-      n = max(1, first_of(n, [&](int i) { return !at_most((uint32_t)(sh.list[i] >> 32)); }));
+    if (lim.min_w != 0)
+      n = max(1, first_of(n, [&](int i) { return !heavy((uint32_t)(sh.list[i] >> 32), lim); }));
     const uint64_t want = beyond(lim.u, sh.sums[n - 1]);
     const int i = first_of(n, [&](int k) { return sh.sums[k] >= want; });
     return (int64_t)(uint32_t)sh.list[min(i, n - 1)];
@@ -775,7 +850,8 @@ struct Sampler {
     }
     if (sh.floor_bin < kBins) {
       const int d = sh.floor_bin;
-      const int j = first_of(number, [&](int i) { return !at_most((uint32_t)(sh.list[i] >> 32)); });
+      const int j =
+          first_of(number, [&](int i) { return !heavy((uint32_t)(sh.list[i] >> 32), lim); });
       const bool in = j > 0 && sh.bin_of[j - 1] == d;  // else none of its bin
       const uint32_t many = in ? place_of(j - 1) : sh.before[d];
       if (many < end) kept = in ? sh.sums[j - 1] : sh.mass[d];
@@ -816,29 +892,28 @@ struct Sampler {
     return out;
   }
 
-  // Leader: the last key whose y is at most -log2(min_p) (y rises with the key).
-  __device__ uint32_t last_key() const {
+  // Whether a key's weight is at least min_w.
+  __device__ __forceinline__ bool heavy(uint32_t key, const Settings& lim) const {
+    const float l = key_logit(key);
+    if (!(l > -INFINITY)) return false;
+    uint32_t g;
+    const int bin = place(r, l, g);
+    return bin != kFar && mass_of(bin, (1ull << 33) - g) >= lim.min_w;
+  }
+  // The last key of which that is true (weights fall as keys rise).
+  __device__ uint32_t last_key(const Settings& lim) const {
     uint32_t lo = order_key(r.top), hi = kNone - 1;  // lo always is one
     const int lane = threadIdx.x % 32;
     while (lo < hi) {
       const uint32_t step = (hi - lo + 31) / 32;
       const uint64_t k = (uint64_t)lo + (uint64_t)step * (lane + 1);
-      const bool in = k <= hi && at_most((uint32_t)k);
+      const bool in = k <= hi && heavy((uint32_t)k, lim);
       const int many = __popc(__ballot_sync(~0u, in));
       const uint64_t next = (uint64_t)lo + (uint64_t)step * (many + 1) - 1;
       lo += step * many;
       hi = (uint32_t)min((uint64_t)hi, next);
     }
     return lo;
-  }
-  __device__ __forceinline__ bool at_most(uint32_t key) const {
-    const float l = key_logit(key);
-    if (l == r.top) return true;
-    const float s = r.top - l, bb = r.top - s, e = (r.top - (s + bb)) + (bb - l);
-    const float yh = s * r.ch;
-    if (!(yh < 256.0f)) return false;  // min_p is 2^-149 at least
-    const float yl = fmaf(e, r.ch, fmaf(s, r.cl, fmaf(s, r.ch, -yh)));
-    return (yh - sh.yh) + (yl - sh.yl) <= 0.0f;
   }
 
   // Leader: number and sum of the tokens of `bin` whose key is at most `last`
@@ -880,66 +955,45 @@ struct Sampler {
 
 template <class T>
 __device__ int64_t Sampler<T>::run(int64_t row) {
-  const float* ts = in.temperatures;
-  const float *ps = in.top_ps, *ms = in.min_ps;
-  const double top_p = ps != nullptr ? ps[row] : in.top_p;
-  const bool cold = !(ts != nullptr ? ts[row] > 0.0f : in.temperature > 0.0);
-  const bool least = ms != nullptr ? ms[row] > 0.0f : in.min_p > 0.0;
-  const int64_t top_k = in.top_ks != nullptr ? load_index(in.top_ks, in.index_bytes, row) : in.top_k;
-  // what takes binary64, by a thread each
-  if (threadIdx.x == 0) {
-    const double c = fmin(1.4426950408889634 / (ts != nullptr ? ts[row] : in.temperature), 1e37);
-    sh.ch = (float)c;
-    sh.cl = (float)(c - (double)sh.ch);
-  }
-  if (threadIdx.x == 32 && rank == 0 && least) {
-    const double y = fmax(-log2(ms != nullptr ? (double)ms[row] : in.min_p), 0.0);
-    sh.yh = (float)y;
-    sh.yl = (float)(y - (double)sh.yh);
-  }
-
   begin();
+  clear();
+  if (threadIdx.x == 0) sh.listed = 0;
+  const Limits lim = {in.of(row), in.uniform(row)};
   const float mine = load();
   begun();
   const uint32_t top = (uint32_t)extreme<true>((uint64_t)order_key(mine), 0);
   if (top == kNone) return -1;
   r.top = key_logit(top);
-  if (cold || top_k == 1 || top_p <= 0.0) {
+  if (lim.cold || lim.top_k == 1) {
     uint64_t first = ~0ull;
     each<4>([&](float l, int i) {
       if (l == r.top) first = min(first, (uint64_t)i);
     });
     return (int64_t)extreme<true>(first, 1);
   }
-  r.ch = sh.ch;
-  r.cl = sh.cl;
-  const float u0 = in.u[row];
-  const Limits lim = {top_k > 0 ? (uint64_t)top_k : 0, top_p,
-                      u0 > 0.0f ? fmin((double)u0, 1.0 - 0x1p-24) : 0.0, least};
+  r.ch = lim.ch;
+  r.cl = lim.cl;
   // A few tokens by top_k: these and no others, from a histogram of numbers.
-  if (top_k > 0 && top_k <= kFew) {
-    histogram(kCount, {}, 0);
-    if (rank == 0 && threadIdx.x < 32) {
-      const int d = min(first_of(kBins, [&](int i) { return sh.before[i + 1] >= lim.top_k; }),
-                        kBins - 1);
-      const uint32_t n = sh.before[d + 1];
-      tell({d, 0, 0, n > (uint32_t)kList || d == kFar ? 0 : n});
+  bool clean = true;
+  if (lim.top_k > 0 && lim.top_k <= kFew) {
+    histogram(kCount, {}, 0, true);
+    const int d = min(first_of(kBins, [&](int i) { return sh.before[i + 1] >= lim.top_k; }),
+                      kBins - 1);
+    const uint32_t n = sh.before[d + 1];
+    if (n <= (uint32_t)kList && d != kFar) {
+      gather_chosen(true, 0, d);
+      return rank == 0 ? among_few((int)n, lim) : -1;
     }
-    const Message m = hear();
-    if (m.number != 0) {
-      gather_chosen(true, 0, m.bin);
-      return rank == 0 ? among_few((int)m.number, lim) : -1;
-    }
+    sync();  // others may still add up the numbers
+    clean = false;
   }
   // Otherwise the borders' bins, from the sums of all.
-  histogram(kPlace, {}, 0);
-  if (rank == 0 && threadIdx.x < 32) plan(lim);
-  {
-    const Message m = hear();
-    if (m.number != 0) {
-      gather_chosen(false, (int)m.lo, (int)m.hi);
-      return rank == 0 ? among_chosen((int)m.number, lim) : -1;
-    }
+  histogram(kPlace, {}, 0, clean);
+  if (threadIdx.x < 32) plan(lim);
+  __syncthreads();
+  if (sh.number != 0) {
+    gather_chosen(false, (int)sh.from, (int)sh.to);
+    return rank == 0 ? among_chosen((int)sh.number, lim) : -1;
   }
   return one_by_one(lim);
 }
@@ -949,8 +1003,6 @@ __device__ int64_t Sampler<T>::run(int64_t row) {
 template <class T>
 __device__ __noinline__ int64_t Sampler<T>::one_by_one(const Limits& lim) const {
   const uint64_t top_k = lim.top_k;
-  const double top_p = lim.top_p;
-  const bool least = lim.least;
   const auto bins = [&] { histogram(kPlace, {}, 0); };
 
   // The last bin of what is kept, how many of its tokens, and the sum of all of
@@ -975,7 +1027,7 @@ __device__ __noinline__ int64_t Sampler<T>::one_by_one(const Limits& lim) const 
     const Border b = look(d, many, false, used, {true, d, want, 0});
     if (many != 0) kept = base + mass_of(d, b.sum);
   }
-  if (top_p < 1.0) {
+  if (lim.top_p < 1.0) {
     if (used) bins();
     used = false;
     int d = 0;
@@ -983,7 +1035,7 @@ __device__ __noinline__ int64_t Sampler<T>::one_by_one(const Limits& lim) const 
     uint64_t want = 0;
     if (rank == 0) {
       d = first_bin(
-          [&] { sh.want = share(top_p, kept); },
+          [&] { sh.want = share(lim.top_p, kept); },
           [&](uint32_t, uint64_t s) { return s >= sh.want; });
       want = sh.want;
       many = sh.before[d + 1] - sh.before[d];
@@ -996,13 +1048,13 @@ __device__ __noinline__ int64_t Sampler<T>::one_by_one(const Limits& lim) const 
     const Border b = look(d, many, false, used, {false, d, want, base});
     if (many != 0) number = b.number, kept = base + mass_of(d, b.sum);
   }
-  if (least) {
+  if (lim.min_w != 0) {
     if (used) bins();
     used = false;
     int d = 0;
     uint32_t last = 0;
     if (rank == 0) {
-      last = last_key();
+      last = last_key(lim);
       uint32_t g;
       d = place(r, key_logit(last), g);
       base = sh.mass[d];
@@ -1087,11 +1139,20 @@ cr_status cr_sample(const cr_sample_args* a, int64_t* tokens, void* stream) {
   const bool hold = kFixed + slice * es <= 200 * 1024;
   const size_t smem = kFixed + (hold ? slice * es : 0);
   const bool wide = rows_aligned(a->logits, a->row_stride, 0, es, 16);
+  Settings all;
+  const double c = a->temperature > 0.0 ? std::min(kLog2eD / a->temperature, 1e37) : 0.0;
+  all.cold = !(a->temperature > 0.0);
+  all.ch = (float)c;
+  all.cl = (float)(c - (double)all.ch);
+  all.top_k = a->top_k > 0 ? (uint64_t)a->top_k : 0;
+  all.top_p = a->top_p < 1.0 ? std::max(a->top_p, 0.0) : 1.0;
+  all.min_w = 0;
+  if (a->min_p > 0.0) all.min_w = (uint64_t)std::ceil(std::ldexp(std::min(a->min_p, 1.0), 42));
   bool done = false;
   CR_MODEL_TYPE(a->dt, {
-    const SampleIn<T> in = {a->vocab, static_cast<const T*>(a->logits), a->row_stride, a->u,
-                            a->temperature, a->top_p, a->min_p, a->top_k, a->temperatures,
-                            a->top_ps, a->min_ps, a->top_ks, a->index_bytes};
+    const SampleIn<T> in = {a->vocab,  static_cast<const T*>(a->logits), a->row_stride, a->u,
+                            all,       a->temperatures, a->top_ps, a->min_ps, a->top_ks,
+                            a->index_bytes};
     CR_LAUNCH(kKSample, s,
               done = launch_clusters(sample_kernel<T>, a->rows * blocks, blocks, kThreads, smem, s,
                                      in, tokens, blocks, slice, hold, wide));
