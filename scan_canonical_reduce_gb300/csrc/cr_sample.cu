@@ -59,45 +59,50 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k : ~k & 0x7FFFFFFFu);
 }
 
-// Where a candidate that is not the largest lies: its bin, and its weight in
-// it, 2^(bin / 16) w - that is 1 - g, g < 0.0425 - as g in units of 2^-33.
+// Where a candidate that is not the largest lies: its bin, that of y rounded to
+// binary32 (which no order of two logits changes), and its weight in it, 2^(bin
+// / 16) w = 1 - z', as g = z' + 2^-18 in units of 2^-33: z' is -2^-19 to 0.0425.
 // Returns false where y is 63.9 or more (the far bin): such weights together
 // are below 2^-42 of the largest's. Straight code, whose results then mean
 // nothing.
 constexpr int kFar = kBins - 1;
 constexpr int kIndexDigits = 10;  // 2^20 indices in kBins
+constexpr uint32_t kShift = 1u << 15;
 __device__ __forceinline__ bool split(const Row& r, float l, int& bin, uint32_t& g) {
   // the difference in two numbers, then y in two
   const float s = r.top - l, bb = r.top - s, e = (r.top - (s + bb)) + (bb - l);
   const float yh = s * r.ch;
   const float yl = fmaf(e, r.ch, fmaf(s, r.cl, fmaf(s, r.ch, -yh)));
-  // y = bin / 16 + x, x in units of 2^-36; adding 2^23 rounded down is a floor
-  const float t = __fmaf_rd(yh, 16.0f, 8388608.0f);
-  const float xh = fmaf(t - 8388608.0f, -0.0625f, yh);
-  const uint32_t x0 = __float2uint_rn(xh * 0x1p36f);
-  const int x1 = __float2int_rn(yl * 0x1p36f);
-  const long long y = (((long long)(__float_as_uint(t) & 0x7FFFFFu) << 32) | x0) + x1;
-  bin = (int)(y >> 32);
+  // y = bin / 16 + x, x in units of 2^-34, from its two parts; adding 2^23
+  // rounded down is a floor, adding 3 2^22 a rounding (of 2^16 at most)
+  const float t = __fmaf_rd(yh, 16.0f, 0x1p23f);
+  bin = (int)(__float_as_uint(t) & 0x7FFFFFu);
+  const float xh = fmaf(t - 0x1p23f, -0.0625f, yh);
+  const int x = __float2int_rn(xh * 0x1p34f) +
+                (__float_as_int(fmaf(yl, 0x1p34f, 0x1.8p23f)) - 0x4B400000);
   // 1 - 2^-x = 1 - exp(-z) = z - z^2 (1/2 - z (1/6 - z (1/24 - z (1/120 - z /
   // 720)))), z = x ln 2; z^7 / 5040 < 2^-44 is left out. What follows z is below
   // 2^-10, and binary32 holds it to 2^-34.
-  const uint32_t z = __umulhi((uint32_t)y, 0xB17217F8u);
-  const float f = (float)z * -0x1p-36f;
+  const int z = __mulhi(x, 0x58B90BFC);  // units of 2^-33
+  const float f = (float)z * -0x1p-33f;
   const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.0f / 720.0f, 1.0f / 120.0f), 1.0f / 24.0f),
                                1.0f / 6.0f), 0.5f);
-  const uint32_t tail = __float_as_uint(fmaf(f * f, q * 0x1p33f, 8388608.0f)) & 0x7FFFFFu;
-  const uint32_t first = (z >> 3) + (z >> 2 & 1);
-  g = first > tail ? first - tail : 0;
+  const float tail = fmaf(f * f, q * 0x1p33f, 0x1p23f);
+  g = (uint32_t)z - __float_as_uint(tail) + (0x4B000000u + kShift);
   return yh < 63.9f;
 }
 __device__ __forceinline__ int place(const Row& r, float l, uint32_t& g) {
   int bin;
   const bool near = split(r, l, bin, g);
   if (l == r.top || !near) {
-    g = 0;
+    g = kShift;
     return l == r.top ? 0 : kFar;
   }
   return bin;
+}
+// The weights of n tokens of a bin whose g sum up to g, in units of 2^-33.
+__device__ __forceinline__ uint64_t weights(uint64_t n, uint64_t g) {
+  return (n << 33) + n * kShift - g;
 }
 
 // A sum of weights within a bin (1 is 2^33) in units of 2^-42 of the largest.
@@ -107,13 +112,14 @@ __device__ __forceinline__ uint64_t mass_of(int bin, uint64_t sum) {
   return n == 0 ? v : (v + ((uint64_t)1 << (n - 1))) >> n;
 }
 
-// y in bins, to a few thousandths of one.
-__device__ __forceinline__ float rough(const Row& r, float l) {
+// y in bins.
+__device__ __forceinline__ float in_bins(const Row& r, float l) {
   return (r.top - l) * r.ch * 16.0f;
 }
-// Whether a logit's bin may be this one.
-__device__ __forceinline__ bool near(const Row& r, float l, int bin) {
-  return fabsf(rough(r, l) - ((float)bin + 0.5f)) < 0.51f || (bin == 0 && l == r.top);
+// Whether a logit's bin is this one (not the far one).
+__device__ __forceinline__ bool in_bin(const Row& r, float l, int bin) {
+  const float v = in_bins(r, l);
+  return (v >= (float)bin && v < (float)(bin + 1)) || (bin == 0 && l == r.top);
 }
 
 // A row's settings, as the kernel works with them. (GB300 has few binary64
@@ -254,18 +260,44 @@ struct Sampler {
     }
   }
 
-  // f(logit, index) of every element of the slice. (An element at a time keeps
-  // the code short: f is long, and a call runs through it only a few times.)
-  template <int kUnroll, class F>
+  // f(logits, index of the first) of every element of the slice, kBatch at a
+  // time, kThreads apart; NaN stands for what is behind the end. (Straight code
+  // on several elements side by side hides its latencies: with one after the
+  // other, a block's sixteen warps issued one instruction a clock.)
+  static constexpr int kBatch = 4;
+  template <class F>
   __device__ __forceinline__ void each(F f) const {
     const T* const from = x;  // (copies: what f writes might be these, for the compiler)
     const int end = n, first = start;
     if (held) {
-#pragma unroll kUnroll
-      for (int i = threadIdx.x; i < end; i += kThreads) f(to_f32(copy()[i]), first + i);
-    } else {
 #pragma unroll 1
-      for (int i = threadIdx.x; i < end; i += kThreads) f(to_f32(from[i]), first + i);
+      for (int i0 = threadIdx.x; i0 < end; i0 += kBatch * kThreads) {
+        float l[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * kThreads;
+          l[k] = i < end ? to_f32(copy()[i]) : NAN;
+        }
+        f(l, first + i0);
+      }
+    } else {  // the next ones are read while f works on these
+      T next[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        next[k] = i < end ? from[i] : from_f32<T>(NAN);
+      }
+#pragma unroll 1
+      for (int i0 = threadIdx.x; i0 < end; i0 += kBatch * kThreads) {
+        float l[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          l[k] = to_f32(next[k]);
+          const int i = i0 + (kBatch + k) * kThreads;
+          next[k] = i < end ? from[i] : from_f32<T>(NAN);
+        }
+        f(l, first + i0);
+      }
     }
   }
 
@@ -319,7 +351,7 @@ struct Sampler {
 
   // What a histogram's bins are.
   enum Digit {
-    kCount,  // roughly those of place(), and only the number of tokens
+    kCount,  // those of place(), and only the number of tokens
     kPlace,  // those of place(), their sums as masses
     kKey,    // the keys lo..hi of m.bin, from lo on, 2^shift a bin
     kIndex,  // the indices with the key lo, 1024 a bin
@@ -344,38 +376,50 @@ struct Sampler {
       atomicAdd(&sh.glo[d], g & 0x3FFFu);
     };
     if (digit == kCount) {
-      each<4>([&, row](float l, int) {
-        if (!(l > -INFINITY)) return;
-        const float v = rough(row, l);
-        if (l == row.top) ++tops;
-        else if (!(v < (float)kFar)) ++fars;
-        else atomicAdd(&sh.cnt[(int)v], 1u);
+      each([&, row](const float (&l)[kBatch], int) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float v = in_bins(row, l[k]);
+          const bool close = v < (float)kFar, top = l[k] == row.top;
+          tops += top;
+          fars += !close && !top && l[k] > -INFINITY;
+          if (close && !top) atomicAdd(&sh.cnt[(int)v], 1u);
+        }
       });
     } else if (digit == kPlace) {
-      each<4>([&, row](float l, int) {
-        uint32_t g;
-        int d;
-        const bool close = split(row, l, d, g), top = l == row.top;
-        // many may be alike there
-        tops += top;
-        fars += !close && !top && l > -INFINITY;
-        if (close && !top) add(d, g);
+      each([&, row](const float (&l)[kBatch], int) {
+        uint32_t g[kBatch];
+        int d[kBatch];
+        bool in[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          in[k] = split(row, l[k], d[k], g[k]) && l[k] != row.top;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (in[k]) add(d[k], g[k]);
+          else if (l[k] == row.top) ++tops;  // many may be alike there
+          else fars += l[k] > -INFINITY;
+        }
       });
     } else {
       const int bin = m.bin;
       const uint32_t lo = m.lo, hi = m.hi;
-      each<1>([&, row](float l, int i) {
-        if (!near(row, l, bin)) return;
-        const uint32_t k = order_key(l);
-        uint32_t g;
-        if (k < lo || k > hi || place(row, l, g) != bin) return;
-        add(digit == kKey ? (int)((k - lo) >> shift) : i >> kIndexDigits, g);
+      each([&, row](const float (&l)[kBatch], int i) {
+#pragma unroll 1
+        for (int k = 0; k < kBatch; ++k, i += kThreads) {
+          if (!in_bin(row, l[k], bin)) continue;
+          const uint32_t key = order_key(l[k]);
+          if (key < lo || key > hi) continue;
+          uint32_t g;
+          place(row, l[k], g);
+          add(digit == kKey ? (int)((key - lo) >> shift) : i >> kIndexDigits, g);
+        }
       });
     }
     fars = __reduce_add_sync(~0u, fars);
     tops = __reduce_add_sync(~0u, tops);
     if (threadIdx.x % 32 == 0) {
-      if (tops) atomicAdd(&sh.cnt[0], tops);
+      if (tops) add(0, tops * kShift), atomicAdd(&sh.cnt[0], tops - 1);
       if (fars) atomicAdd(&sh.cnt[kFar], fars);
     }
     sync();
@@ -406,7 +450,7 @@ struct Sampler {
       }
 #pragma unroll
       for (int b = 0; b < kMostBlocks; ++b) n += c[b], g += ((uint64_t)hi[b] << 14) + lo[b];
-      uint64_t w = ((uint64_t)n << 33) - g;
+      uint64_t w = weights(n, g);
       if (digit == kPlace) w = i == kFar ? 0 : mass_of(i, w);
       for (int b = 0; b < blocks; ++b) {
         at(sh.before, b)[i] = n;
@@ -528,7 +572,7 @@ struct Sampler {
       if (i < number) {
         uint32_t g;
         const int bin = place(r, key_logit((uint32_t)(sh.list[i] >> 32)), g);
-        m[k] = ((uint64_t)1 << 33) - g;
+        m[k] = weights(1, g);
         if (masses) {
           m[k] = bin == kFar ? 0 : mass_of(bin, m[k]);
           sh.bin_of[i] = (uint16_t)bin;
@@ -556,7 +600,7 @@ struct Sampler {
   __device__ __forceinline__ uint64_t weight_in_bin(uint32_t key) const {
     uint32_t g;
     place(r, key_logit(key), g);
-    return ((uint64_t)1 << 33) - g;
+    return weights(1, g);
   }
 
   // What a border is the first place of: n tokens, or a mass of `want` with
@@ -592,13 +636,15 @@ struct Sampler {
     used = used || m.number > kList;
     while (m.number > kList) {
       uint64_t kmin = kNone, kmax = 0;
-      each<1>([&](float l, int) {
-        if (!near(r, l, m.bin)) return;
-        const uint32_t k = order_key(l);
-        uint32_t g;
-        if (k < m.lo || k > m.hi || place(r, l, g) != m.bin) return;
-        kmin = min(kmin, (uint64_t)k);
-        kmax = max(kmax, (uint64_t)k);
+      each([&](const float (&l)[kBatch], int) {
+#pragma unroll 1
+        for (int j = 0; j < kBatch; ++j) {
+          if (!in_bin(r, l[j], m.bin)) continue;
+          const uint32_t k = order_key(l[j]);
+          if (k < m.lo || k > m.hi) continue;
+          kmin = min(kmin, (uint64_t)k);
+          kmax = max(kmax, (uint64_t)k);
+        }
       });
       m.lo = (uint32_t)extreme<true>(kmin, 0);
       m.hi = (uint32_t)extreme<false>(kmax, 1);
@@ -641,18 +687,20 @@ struct Sampler {
     const Row row = r;
     const int bin = m.bin;
     const uint32_t lo = m.lo, hi = m.hi;
-    each<4>([=](float l, int i) {
-      if (one ? i >> kIndexDigits != bin : !near(row, l, bin)) return;
-      const uint32_t k = order_key(l);
-      uint32_t g;
-      if (k < lo || k > hi || (!one && place(row, l, g) != bin)) return;
-      const uint32_t to = atomicAdd(listed, 1u);
-      if (to < (uint32_t)kList) list[to] = (uint64_t)k << 32 | (uint32_t)i;
+    each([=](const float (&l)[kBatch], int i) {
+#pragma unroll 1
+      for (int j = 0; j < kBatch; ++j, i += kThreads) {
+        if (one ? i >> kIndexDigits != bin : !in_bin(row, l[j], bin)) continue;
+        const uint32_t k = order_key(l[j]);
+        if (k < lo || k > hi) continue;
+        const uint32_t to = atomicAdd(listed, 1u);
+        if (to < (uint32_t)kList) list[to] = (uint64_t)k << 32 | (uint32_t)i;
+      }
     });
     sync();
   }
-  // The same for all tokens whose rough bin is below `limit` (few), or whose bin
-  // is chosen, of bins from..to (!few).
+  // The same for all tokens of bins up to `to` (few), or of the chosen ones, which
+  // are of bins from..to.
   __device__ __noinline__ void gather_chosen(bool few, int from, int to) const {
     uint32_t* listed = at(&sh.listed, 0);
     uint64_t* list = at(sh.list, 0);
@@ -663,21 +711,29 @@ struct Sampler {
     };
     if (few) {
       const float limit = (float)(to + 1);
-      each<4>([=](float l, int i) {
-        if (rough(row, l) < limit || l == row.top) add(l, i);
+      each([=](const float (&l)[kBatch], int i) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (in_bins(row, l[k]) < limit || l[k] == row.top) add(l[k], i + k * kThreads);
       });
     } else {
-      const float mid = 0.5f * (float)(from + to + 1), half = 0.5f * (float)(to - from + 1) + 0.01f;
+      const float low = (float)from, high = (float)(to + 1);
       const bool tops = from == 0;
-      each<4>([=](float l, int i) {
-        const float v = rough(row, l);
-        if (!(fabsf(v - mid) < half) && !(tops && l == row.top)) return;
-        const int b = l == row.top ? 0 : (int)v;
-        const float f = v - (float)b;  // near an edge, place() may tell another bin
-        if ((sh.chosen[b / 32] >> b % 32 & 1) == 0 && f > 0.01f && f < 0.99f) return;
-        uint32_t g;
-        const int d = place(row, l, g);
-        if (sh.chosen[d / 32] >> d % 32 & 1) add(l, i);
+      each([=](const float (&l)[kBatch], int i) {
+        bool may[kBatch];
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float v = in_bins(row, l[k]);
+          may[k] = (v >= low && v < high) || (tops && l[k] == row.top);
+          any = any || may[k];
+        }
+        if (!any) return;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int b = l[k] == row.top ? 0 : (int)in_bins(row, l[k]);
+          if (may[k] && (sh.chosen[b / 32] >> b % 32 & 1)) add(l[k], i + k * kThreads);
+        }
       });
     }
     sync();
@@ -898,7 +954,7 @@ struct Sampler {
     if (!(l > -INFINITY)) return false;
     uint32_t g;
     const int bin = place(r, l, g);
-    return bin != kFar && mass_of(bin, (1ull << 33) - g) >= lim.min_w;
+    return bin != kFar && mass_of(bin, weights(1, g)) >= lim.min_w;
   }
   // The last key of which that is true (weights fall as keys rise).
   __device__ uint32_t last_key(const Settings& lim) const {
@@ -928,12 +984,15 @@ struct Sampler {
     if (m.hi == 0) return out;
     uint64_t c = 0, s = 0;
     const Row row = r;
-    each<4>([&, row](float l, int) {
-      if (!near(row, l, m.bin) || order_key(l) > m.hi) return;
-      uint32_t g;
-      if (place(row, l, g) != m.bin) return;
-      ++c;
-      s += ((uint64_t)1 << 33) - g;
+    each([&, row](const float (&l)[kBatch], int) {
+#pragma unroll 1
+      for (int k = 0; k < kBatch; ++k) {
+        if (!in_bin(row, l[k], m.bin) || order_key(l[k]) > m.hi) continue;
+        uint32_t g;
+        place(row, l[k], g);
+        ++c;
+        s += weights(1, g);
+      }
     });
 #pragma unroll
     for (int k = 16; k > 0; k /= 2) {
@@ -966,8 +1025,10 @@ __device__ int64_t Sampler<T>::run(int64_t row) {
   r.top = key_logit(top);
   if (lim.cold || lim.top_k == 1) {
     uint64_t first = ~0ull;
-    each<4>([&](float l, int i) {
-      if (l == r.top) first = min(first, (uint64_t)i);
+    each([&](const float (&l)[kBatch], int i) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (l[k] == r.top) first = min(first, (uint64_t)(i + k * kThreads));
     });
     return (int64_t)extreme<true>(first, 1);
   }
