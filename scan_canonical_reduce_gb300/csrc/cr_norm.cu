@@ -46,82 +46,338 @@ struct Stats {
   float mean, rest, rstd;
 };
 
-template <class T>
-__device__ Stats row_stats(const T* x, int64_t dim, float eps, int lane) {
+// A row's elements in the registers of `threads` threads, E each, 16 bytes of
+// neighbours at a time: whole accesses (kWide: rows on 16 bytes, a whole number
+// of accesses long) or, for the same bits, one by one (a warp's neighbours are
+// then in L1).
+template <class T, int E, bool kWide>
+struct Held {
+  static constexpr int V = 16 / sizeof(T);
+  static constexpr int kPacks = E / V;
+  static_assert(E % V == 0, "whole accesses");
+  uint4 q[kWide ? kPacks : 1];
+  T v[kWide ? 1 : E];
+
+  static __device__ __forceinline__ int column(int e, int t, int threads) {
+    return (e / V * threads + t) * V + e % V;
+  }
+  __device__ __forceinline__ void load(const T* p, int t, int threads, int dim) {
+    if constexpr (kWide) {
+#pragma unroll
+      for (int k = 0; k < kPacks; ++k) {
+        const int c = (k * threads + t) * V;
+        q[k] = c < dim ? __ldcs(reinterpret_cast<const uint4*>(p + c)) : make_uint4(0, 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = column(e, t, threads);
+        v[e] = c < dim ? p[c] : from_f32<T>(0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (kWide) {
+      const uint4& w4 = q[e / V];
+      const int i = e % V;
+      if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(i == 0 ? w4.x : i == 1 ? w4.y : i == 2 ? w4.z : w4.w);
+      } else {
+        const uint32_t w = i / 2 == 0 ? w4.x : i / 2 == 1 ? w4.y : i / 2 == 2 ? w4.z : w4.w;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+          return __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
+        else
+          return __half2float(__ushort_as_half((unsigned short)(w >> (i % 2 * 16))));
+      }
+    } else {
+      return to_f32(v[e]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&f)[E], int t, int threads,
+                                               int dim) {
+    if constexpr (kWide) {
+#pragma unroll
+      for (int k = 0; k < kPacks; ++k) {
+        const int c = (k * threads + t) * V;
+        if (c < dim) {
+          float g[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] = f[k * V + i];
+          store_f32<T, V>(p + c, true, V, g);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = column(e, t, threads);
+        if (c < dim) p[c] = from_f32<T>(f[e]);
+      }
+    }
+  }
+};
+
+// Weights of a thread's columns (`none` without them, and behind the row).
+template <int E, int V, bool kWide>
+__device__ __forceinline__ void load_vector(const float* w, float none, int t, int threads, int dim,
+                                            float (&f)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = none;
+  if (w == nullptr) return;
+  if constexpr (kWide) {
+#pragma unroll
+    for (int k = 0; k < E / V; ++k) {
+      const int c = (k * threads + t) * V;
+      if (c < dim) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(w + c + i));
+          f[k * V + i] = q.x, f[k * V + i + 1] = q.y;
+          f[k * V + i + 2] = q.z, f[k * V + i + 3] = q.w;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = (e / V * threads + t) * V + e % V;
+      if (c < dim) f[e] = __ldg(w + c);
+    }
+  }
+}
+
+// Sums of two numbers over the threads of a row (whole warps), in one order: by
+// lanes, then by warps. buf: two numbers a warp, not in use.
+__device__ __forceinline__ float2 row_sum(float a, float b, int threads, float2* buf) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if (threads <= 32) return make_float2(a, b);
+  const int warp = threadIdx.x / 32, warps = threads / 32, first = warp / warps * warps;
+  if (threadIdx.x % 32 == 0) buf[warp] = make_float2(a, b);
+  __syncthreads();
+  // (every warp adds up its row's in the same tree; absent ones count as zero)
+  const float2 v = threadIdx.x % 32 < warps ? buf[first + threadIdx.x % 32] : make_float2(0.0f, 0.0f);
+  a = v.x;
+  b = v.y;
+#pragma unroll
+  for (int s = 16; s > 0; s /= 2) {
+    if (s < warps) {
+      a = __fadd_rn(a, __shfl_xor_sync(~0u, a, s));
+      b = __fadd_rn(b, __shfl_xor_sync(~0u, b, s));
+    }
+  }
+  return make_float2(__shfl_sync(~0u, a, 0), __shfl_sync(~0u, b, 0));
+}
+
+// The statistics of a row whose elements are x; leaves x - mean in d.
+template <class T, int E, bool kWide>
+__device__ __forceinline__ Stats row_stats(const Held<T, E, kWide>& x, int t, int threads, int dim,
+                                           float eps, float2* buf, float (&d)[E]) {
   float s = 0.0f;
-  for (int64_t c = lane; c < dim; c += 32) s += to_f32(x[c]);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    d[e] = x.get(e);
+    s += d[e];
+  }
   Stats r;
-  r.mean = warp_sum(s) / (float)dim;
+  r.mean = row_sum(s, 0.0f, threads, buf).x / (float)dim;
   float d1 = 0.0f, d2 = 0.0f;
-  for (int64_t c = lane; c < dim; c += 32) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    d[e] = Held<T, E, kWide>::column(e, t, threads) < dim ? d[e] - r.mean : 0.0f;
+    d1 += d[e];
+    d2 = fmaf(d[e], d[e], d2);
+  }
+  const float2 v = row_sum(d1, d2, threads, buf + 32);
+  r.rest = v.x / (float)dim;
+  const float var = fmaxf(v.y / (float)dim - r.rest * r.rest, 0.0f);
+  r.rstd = 1.0f / sqrtf(var + eps);
+  return r;
+}
+
+// A row in the registers of `threads` threads, several rows a block.
+template <class T, int kThreads, int E, bool kWide>
+__global__ void __launch_bounds__(kThreads)
+layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
+                  float* __restrict__ stats) {
+  using H = Held<T, E, kWide>;
+  __shared__ float2 buf[64];
+  const int t = threadIdx.x % threads, dim = (int)in.dim;
+  const int64_t r = (int64_t)blockIdx.x * (kThreads / threads) + threadIdx.x / threads;
+  const bool real = r < in.rows;
+  H x;
+  x.load(in.x + row_offset(real ? r : 0, in.len, in.xs), t, threads, real ? dim : 0);
+  float d[E];
+  const Stats st = row_stats(x, t, threads, dim, in.eps, buf, d);
+  if (!real) return;
+  if (stats != nullptr && t == 0) {
+    stats[3 * r] = st.mean;
+    stats[3 * r + 1] = st.rest;
+    stats[3 * r + 2] = st.rstd;
+  }
+  if (y == nullptr) return;  // the statistics alone
+  float w[E], b[E];
+  load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
+  load_vector<E, H::V, kWide>(in.b, 0.0f, t, threads, dim, b);
+#pragma unroll
+  for (int e = 0; e < E; ++e) d[e] = fmaf((d[e] - st.rest) * st.rstd, w[e], b[e]);
+  H::store(y + row_offset(r, in.len, ys), d, t, threads, dim);
+}
+
+// Rows that registers do not hold: a block a row, read again from L2.
+constexpr int kLongThreads = 512;
+template <class T>
+__device__ Stats long_stats(const T* x, int64_t dim, float eps, float2* buf) {
+  float s = 0.0f;
+  for (int64_t c = threadIdx.x; c < dim; c += kLongThreads) s += to_f32(x[c]);
+  Stats r;
+  r.mean = row_sum(s, 0.0f, kLongThreads, buf).x / (float)dim;
+  float d1 = 0.0f, d2 = 0.0f;
+  for (int64_t c = threadIdx.x; c < dim; c += kLongThreads) {
     const float d = to_f32(x[c]) - r.mean;
     d1 += d;
     d2 = fmaf(d, d, d2);
   }
-  r.rest = warp_sum(d1) / (float)dim;
-  const float var = fmaxf(warp_sum(d2) / (float)dim - r.rest * r.rest, 0.0f);
+  const float2 v = row_sum(d1, d2, kLongThreads, buf + 32);
+  r.rest = v.x / (float)dim;
+  const float var = fmaxf(v.y / (float)dim - r.rest * r.rest, 0.0f);
   r.rstd = 1.0f / sqrtf(var + eps);
   return r;
 }
 
 template <class T>
-__global__ void __launch_bounds__(256)
-layer_norm_kernel(NormIn<T> in, T* __restrict__ y, Rows2 ys, float* __restrict__ stats) {
-  const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (r >= in.rows) return;
+__global__ void __launch_bounds__(kLongThreads)
+layer_norm_long_kernel(NormIn<T> in, T* __restrict__ y, Rows2 ys, float* __restrict__ stats) {
+  __shared__ float2 buf[64];
+  const int64_t r = blockIdx.x;
   const T* x = in.x + row_offset(r, in.len, in.xs);
-  const Stats st = row_stats(x, in.dim, in.eps, lane);
+  const Stats st = long_stats(x, in.dim, in.eps, buf);
   T* yr = y + row_offset(r, in.len, ys);
-  for (int64_t c = lane; c < in.dim; c += 32) {
+  for (int64_t c = threadIdx.x; y != nullptr && c < in.dim; c += kLongThreads) {
     const float n = ((to_f32(x[c]) - st.mean) - st.rest) * st.rstd;
     const float w = in.w != nullptr ? in.w[c] : 1.0f, b = in.b != nullptr ? in.b[c] : 0.0f;
     yr[c] = from_f32<T>(fmaf(n, w, b));
   }
-  if (stats != nullptr && lane == 0) {
+  if (stats != nullptr && threadIdx.x == 0) {
     stats[3 * r] = st.mean;
     stats[3 * r + 1] = st.rest;
     stats[3 * r + 2] = st.rstd;
   }
 }
 
-// dx, and the row's statistics for the sums over rows
-template <class T>
-__global__ void __launch_bounds__(256)
-layer_norm_backward_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds,
+// dx, and a block's part of the sums over rows, in registers: a block walks
+// rows `blocks` apart, the next one's elements in flight. part: [block][2][dim].
+template <class T, int kThreads, int E, bool kWide>
+__global__ void __launch_bounds__(kThreads)
+layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, Rows2 ds,
                            const float* __restrict__ stats, T* __restrict__ dx, Rows2 os,
-                           float* __restrict__ kept) {
-  const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (r >= in.rows) return;
+                           float* __restrict__ part) {
+  using H = Held<T, E, kWide>;
+  __shared__ float2 buf[2][96];
+  extern __shared__ float sums[];  // [2][dim], for several rows a block
+  const int t = threadIdx.x % threads, dim = (int)in.dim;
+  const int groups = kThreads / threads, group = threadIdx.x / threads;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  float w[E], dw[E], db[E];
+  load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
+#pragma unroll
+  for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.0f;
+  H x, g;
+  Stats next = {0.0f, 0.0f, 0.0f};
+  const auto fetch = [&](int64_t r) {
+    const bool real = r < in.rows;
+    x.load(in.x + row_offset(real ? r : 0, in.len, in.xs), t, threads, real ? dim : 0);
+    g.load(dy + row_offset(real ? r : 0, in.len, ds), t, threads, real ? dim : 0);
+    if (stats != nullptr && real)
+      next = {__ldg(stats + 3 * r), __ldg(stats + 3 * r + 1), __ldg(stats + 3 * r + 2)};
+  };
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  fetch(r);
+  // (as many turns for all rows of a block: they wait for one another)
+  for (int64_t r0 = (int64_t)blockIdx.x * groups, turn = 0; r0 < in.rows; r0 += step, ++turn) {
+    float2* const b = buf[turn & 1];
+    float n[E], q[E];
+    Stats st = next;
+    if (stats == nullptr) {
+      st = row_stats(x, t, threads, dim, in.eps, b, n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) n[e] = x.get(e) - st.mean;
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      n[e] = H::column(e, t, threads) < dim ? (n[e] - st.rest) * st.rstd : 0.0f;
+      const float v = g.get(e);
+      dw[e] = fmaf(v, n[e], dw[e]);
+      db[e] += v;
+      q[e] = v * w[e];
+      s1 += q[e];
+      s2 = fmaf(q[e], n[e], s2);
+    }
+    const int64_t now = r;
+    r += step;
+    fetch(r);
+    const float2 v = row_sum(s1, s2, threads, b + 64);
+    if (now < in.rows) {
+      const float a1 = v.x / (float)dim, a2 = v.y / (float)dim;
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] = st.rstd * fmaf(-n[e], a2, q[e] - a1);
+      H::store(dx + row_offset(now, in.len, os), q, t, threads, dim);
+    }
+  }
+  float* const out = part + (int64_t)blockIdx.x * 2 * dim;
+  if (groups == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = H::column(e, t, threads);
+      if (c < dim) out[c] = dw[e], out[dim + c] = db[e];
+    }
+    return;
+  }
+  for (int k = 0; k < groups; ++k) {  // group by group, in order
+    if (group == k) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = H::column(e, t, threads);
+        if (c < dim) {
+          sums[c] = k == 0 ? dw[e] : sums[c] + dw[e];
+          sums[dim + c] = k == 0 ? db[e] : sums[dim + c] + db[e];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < 2 * dim; c += kThreads) out[c] = sums[c];
+}
+
+// Long rows: dx alone.
+template <class T>
+__global__ void __launch_bounds__(kLongThreads)
+layer_norm_backward_long_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds,
+                                const float* __restrict__ stats, T* __restrict__ dx, Rows2 os) {
+  __shared__ float2 buf[32];
+  const int64_t r = blockIdx.x;
   const T* x = in.x + row_offset(r, in.len, in.xs);
   const T* d = dy + row_offset(r, in.len, ds);
-  Stats st;
-  if (stats != nullptr) st = {stats[3 * r], stats[3 * r + 1], stats[3 * r + 2]};
-  else st = row_stats(x, in.dim, in.eps, lane);
+  const Stats st = {stats[3 * r], stats[3 * r + 1], stats[3 * r + 2]};
   float s1 = 0.0f, s2 = 0.0f;
-  for (int64_t c = lane; c < in.dim; c += 32) {
+  for (int64_t c = threadIdx.x; c < in.dim; c += kLongThreads) {
     const float n = ((to_f32(x[c]) - st.mean) - st.rest) * st.rstd;
     const float g = to_f32(d[c]) * (in.w != nullptr ? in.w[c] : 1.0f);
     s1 += g;
     s2 = fmaf(g, n, s2);
   }
-  s1 = warp_sum(s1) / (float)in.dim;
-  s2 = warp_sum(s2) / (float)in.dim;
+  const float2 v = row_sum(s1, s2, kLongThreads, buf);
+  const float a1 = v.x / (float)in.dim, a2 = v.y / (float)in.dim;
   T* o = dx + row_offset(r, in.len, os);
-  for (int64_t c = lane; c < in.dim; c += 32) {
+  for (int64_t c = threadIdx.x; c < in.dim; c += kLongThreads) {
     const float n = ((to_f32(x[c]) - st.mean) - st.rest) * st.rstd;
     const float g = to_f32(d[c]) * (in.w != nullptr ? in.w[c] : 1.0f);
-    o[c] = from_f32<T>(st.rstd * fmaf(-n, s2, g - s1));
-  }
-  if (lane == 0) {
-    kept[3 * r] = st.mean;
-    kept[3 * r + 1] = st.rest;
-    kept[3 * r + 2] = st.rstd;
+    o[c] = from_f32<T>(st.rstd * fmaf(-n, a2, g - a1));
   }
 }
 
-constexpr int kSumRows = 256;  // rows of a partial sum
+constexpr int kSumRows = 256;  // rows of a partial sum of long rows
 
 template <class T>
 __global__ void __launch_bounds__(256)
@@ -132,6 +388,7 @@ layer_norm_part_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds,
   for (int64_t p = blockIdx.y; p * kSumRows < in.rows; p += gridDim.y) {
     float dw = 0.0f, db = 0.0f;
     const int64_t end = min(in.rows, (p + 1) * kSumRows);
+#pragma unroll 4
     for (int64_t r = p * kSumRows; r < end; ++r) {
       const float x = to_f32(in.x[row_offset(r, in.len, in.xs) + c]);
       const float d = to_f32(dy[row_offset(r, in.len, ds) + c]);
@@ -144,18 +401,30 @@ layer_norm_part_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds,
   }
 }
 
-__global__ void __launch_bounds__(256)
+// The sums of the parts: a block 32 columns, a warp every 32nd part, then the
+// warps in order.
+__global__ void __launch_bounds__(1024)
 layer_norm_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t dim,
                       float* __restrict__ dw, float* __restrict__ db) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= dim) return;
-  float w = 0.0f, b = 0.0f;
-  for (int64_t p = 0; p < parts; ++p) {
-    w += part[2 * p * dim + c];
-    b += part[(2 * p + 1) * dim + c];
+  __shared__ float buf[32][33];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // of 2 dim
+  float v = 0.0f;
+  if (c < 2 * dim) {
+#pragma unroll 8
+    for (int64_t p = warp; p < parts; p += 32) v += __ldg(part + p * 2 * dim + c);
   }
-  if (dw != nullptr) dw[c] = w;
-  if (db != nullptr) db[c] = b;
+  buf[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0) return;
+  v = buf[0][lane];
+#pragma unroll
+  for (int w = 1; w < 32; ++w) v += buf[w][lane];
+  if (c < dim) {
+    if (dw != nullptr) dw[c] = v;
+  } else if (c < 2 * dim) {
+    if (db != nullptr) db[c - dim] = v;
+  }
 }
 
 template <class T>
@@ -181,6 +450,80 @@ cr_status check_norm(const cr_layer_norm_args* a) {
   return CR_OK;
 }
 
+// How rows lie in threads: by their length alone, so that a row's bits are the
+// same among any others and in both directions.
+struct NormShape {
+  int block;    // threads of a block
+  int threads;  // of a row, 0: more than registers hold
+  int E;        // elements a thread
+};
+
+NormShape norm_shape(int64_t dim) {
+  NormShape sh = {256, 0, 8};
+  if (dim > 32768) return sh;
+  if (dim > 2048) sh.block = 512;
+  if (dim > 4096) sh.E = 16;
+  if (dim > 8192) sh.block = 1024, sh.E = 32;
+  sh.threads = 32;
+  while ((int64_t)sh.threads * sh.E < dim) sh.threads *= 2;
+  return sh;
+}
+
+// Blocks of the backward call, which leave a part of the sums over rows each; 0:
+// rows whose gradient goes another way.
+#ifndef CR_NORM_BLOCKS
+#define CR_NORM_BLOCKS 456
+#endif
+int64_t norm_blocks(int64_t rows, int64_t dim) {
+  if (dim > 8192) return 0;
+  const NormShape sh = norm_shape(dim);
+  const int64_t most = sh.block == 256 ? CR_NORM_BLOCKS : sh.E == 8 ? 304 : 152;
+  return std::min<int64_t>(ceil_div(rows, sh.block / sh.threads), most);
+}
+
+bool norm_wide(const cr_layer_norm_args* a) {
+  const size_t es = model_esize(a->dt);
+  return a->dim % (int64_t)(16 / es) == 0 &&
+         rows_aligned(a->x, a->x_batch_stride, a->x_time_stride, es, 16) &&
+         ptr_aligned(a->weight, 16) && ptr_aligned(a->bias, 16);
+}
+
+// Runs EXPR with a block's threads B, a thread's elements E and the access W.
+#define CR_NORM_CASE(B_, E_, WIDE, ...)                                       \
+  {                                                                           \
+    constexpr int B = B_, E = E_;                                             \
+    if (WIDE) { constexpr bool W = true; __VA_ARGS__; }                       \
+    else { constexpr bool W = false; __VA_ARGS__; }                           \
+  }
+#define CR_NORM_SHAPE(SH, WIDE, ...)                                          \
+  if (SH.block == 1024) CR_NORM_CASE(1024, 32, WIDE, __VA_ARGS__)             \
+  else CR_NORM_BACKWARD_SHAPE(SH, WIDE, __VA_ARGS__)
+#define CR_NORM_BACKWARD_SHAPE(SH, WIDE, ...)                                 \
+  if (SH.E == 16) CR_NORM_CASE(512, 16, WIDE, __VA_ARGS__)                    \
+  else if (SH.block == 512) CR_NORM_CASE(512, 8, WIDE, __VA_ARGS__)           \
+  else CR_NORM_CASE(256, 8, WIDE, __VA_ARGS__)
+
+void launch_norm(const cr_layer_norm_args* a, void* y, Rows2 ys, float* stats, bool wide,
+                 cudaStream_t s) {
+  const NormShape sh = norm_shape(a->dim);
+  const int64_t rows = a->batch * a->len;
+  CR_MODEL_TYPE(a->dt, {
+    T* out = static_cast<T*>(y);
+    if (sh.threads == 0) {
+      CR_LAUNCH(kKLayerNorm, s,
+                layer_norm_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(norm_in<T>(a), out,
+                                                                                  ys, stats));
+    } else {
+      CR_NORM_SHAPE(sh, wide, {
+        CR_LAUNCH(kKLayerNorm, s,
+                  layer_norm_kernel<T, B, E, W>
+                  <<<(unsigned)ceil_div(rows, B / sh.threads), B, 0, s>>>(norm_in<T>(a), sh.threads,
+                                                                          out, ys, stats));
+      });
+    }
+  });
+}
+
 }  // namespace
 }  // namespace cr
 
@@ -199,12 +542,9 @@ cr_status cr_layer_norm(const cr_layer_norm_args* a, void* y, int64_t y_batch_st
       !ptr_aligned(stats, 4) || overwrites({y, stats}, {a->x, a->weight, a->bias}))
     return CR_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CR_MODEL_TYPE(a->dt, {
-    CR_LAUNCH(kKLayerNorm, s,
-              layer_norm_kernel<T><<<(unsigned)ceil_div(rows, 8), 256, 0, s>>>(
-                  norm_in<T>(a), static_cast<T*>(y), Rows2{y_batch_stride, y_time_stride},
-                  stats));
-  });
+  const Rows2 ys = {y_batch_stride, y_time_stride};
+  const bool wide = norm_wide(a) && rows_aligned(y, y_batch_stride, y_time_stride, es, 16);
+  launch_norm(a, y, ys, stats, wide, s);
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
@@ -212,7 +552,9 @@ size_t cr_layer_norm_backward_workspace_bytes(int64_t batch, int64_t len, int64_
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || (len > 0 && batch > kMaxBlocks / len)) return 0;
   const int64_t rows = batch * len;
-  return round256((size_t)rows * 12) + round256((size_t)ceil_div(rows, kSumRows) * dim * 8) +
+  const int64_t blocks = norm_blocks(rows, dim);
+  const size_t parts = (size_t)(blocks != 0 ? blocks : ceil_div(rows, kSumRows));
+  return (blocks != 0 ? 0 : round256((size_t)rows * 12)) + round256(parts * dim * 8) +
          kStatusBytes;
 }
 
@@ -237,28 +579,48 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
   const size_t need = cr_layer_norm_backward_workspace_bytes(a->batch, a->len, a->dim);
   if (ws == nullptr || !ptr_aligned(ws, 256) || ws_bytes < need) return CR_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Rows2 ds = {g->dy_batch_stride, g->dy_time_stride};
+  const Rows2 os = {g->dx_batch_stride, g->dx_time_stride};
+  const NormShape sh = norm_shape(a->dim);
+  const int64_t blocks = norm_blocks(rows, a->dim);
+  const bool wide = norm_wide(a) &&
+                    rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, 16) &&
+                    rows_aligned(g->dx, g->dx_batch_stride, g->dx_time_stride, es, 16);
+  const int64_t sum_blocks = ceil_div(2 * a->dim, 32), cols = ceil_div(a->dim, 256);
+  if (sum_blocks > kMaxBlocks) return CR_ERR_UNSUPPORTED;
   char* at = past_status(ws);
   float* kept = reinterpret_cast<float*>(at);
-  float* part = reinterpret_cast<float*>(at + round256((size_t)rows * 12));
-  const int64_t parts = ceil_div(rows, kSumRows), cols = ceil_div(a->dim, 256);
-  if (cols > kMaxBlocks) return CR_ERR_UNSUPPORTED;
-  const Rows2 ds = {g->dy_batch_stride, g->dy_time_stride};
+  if (blocks == 0) at += round256((size_t)rows * 12);
+  float* part = reinterpret_cast<float*>(at);
+  const int64_t parts = blocks != 0 ? blocks : ceil_div(rows, kSumRows);
+  const float* stats = g->stats;
+  if (rows > 0 && blocks == 0 && stats == nullptr) {
+    launch_norm(a, nullptr, {0, 0}, kept, norm_wide(a), s);
+    stats = kept;
+  }
   CR_MODEL_TYPE(a->dt, {
     const T* dy = static_cast<const T*>(g->dy);
-    if (rows > 0) {
+    T* dx = static_cast<T*>(g->dx);
+    if (rows > 0 && blocks == 0) {
       CR_LAUNCH(kKLayerNormBackward, s,
-                layer_norm_backward_kernel<T><<<(unsigned)ceil_div(rows, 8), 256, 0, s>>>(
-                    norm_in<T>(a), dy, ds, g->stats, static_cast<T*>(g->dx),
-                    Rows2{g->dx_batch_stride, g->dx_time_stride}, kept));
+                layer_norm_backward_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(
+                    norm_in<T>(a), dy, ds, stats, dx, os));
       CR_LAUNCH(kKLayerNormSum, s,
                 layer_norm_part_kernel<T>
                 <<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(parts, 65535)), 256, 0, s>>>(
-                    norm_in<T>(a), dy, ds, kept, part));
+                    norm_in<T>(a), dy, ds, stats, part));
+    } else if (rows > 0) {
+      CR_NORM_BACKWARD_SHAPE(sh, wide, {
+        const size_t smem = sh.threads < B ? (size_t)a->dim * 8 : 0;
+        CR_LAUNCH(kKLayerNormBackward, s,
+                  layer_norm_backward_kernel<T, B, E, W><<<(unsigned)blocks, B, smem, s>>>(
+                      norm_in<T>(a), sh.threads, dy, ds, stats, dx, os, part));
+      });
     }
     if (g->dweight != nullptr || g->dbias != nullptr)
       CR_LAUNCH(kKLayerNormSum, s,
-                layer_norm_sum_kernel<<<(unsigned)cols, 256, 0, s>>>(part, parts, a->dim,
-                                                                     g->dweight, g->dbias));
+                layer_norm_sum_kernel<<<(unsigned)sum_blocks, 1024, 0, s>>>(part, parts, a->dim,
+                                                                            g->dweight, g->dbias));
   });
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }

@@ -35,6 +35,9 @@ constexpr int kRanked = 128;  // up to so many by their ranks
 constexpr int kFew = 512;     // top_k up to which its tokens alone are looked at
 constexpr int kMostBlocks = 8;
 constexpr uint32_t kNone = 0xFFFFFFFFu;  // the key of what is no candidate
+static_assert(kBins % kThreads == 0 && kList % kThreads == 0 && kBins % 1024 == 0,
+              "a thread's bins and tokens, a lane's words of chosen bins");
+static_assert(kBins % kMostBlocks == 0 && kRanked <= kThreads, "a block's bins, a token a thread");
 
 // 2^(-j / 16) in units of 2^-63
 __constant__ unsigned long long kRoots[16] = {
@@ -1139,11 +1142,8 @@ __device__ __noinline__ int64_t Sampler<T>::one_by_one(const Limits& lim) const 
   return look(d, many, true, used, {false, d, want, base}).token;
 }
 
-#ifndef CR_SAMPLE_RES
-#define CR_SAMPLE_RES 2
-#endif
 template <class T>
-__global__ void __launch_bounds__(kThreads, CR_SAMPLE_RES)
+__global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(SampleIn<T> in, int64_t* __restrict__ tokens, int blocks, int slice, bool hold,
               bool wide) {
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
@@ -1160,15 +1160,18 @@ sample_kernel(SampleIn<T> in, int64_t* __restrict__ tokens, int blocks, int slic
   if (rank == 0 && threadIdx.x == 0) tokens[row] = token;
 }
 
-#ifndef CR_SAMPLE_SLICE
-#define CR_SAMPLE_SLICE 8192
-#endif
-#undef sh
-
-// Blocks a row.
+// Blocks a row: as many as the GPU runs at a time, or nearly twice that (two an
+// SM; more would only wait, and each costs its waits for the others), while a
+// slice keeps 4096 tokens. Measured, blocks 1 / 2 / 4 / 8: one row of 65,536 29 /
+// 21 / 18 / 16 us, 200 rows 113 / 94 / 101 / 129, 64 rows of 262,144 237 / 141 /
+// 114 / 105, 37 of 10,007 22 / 21 / 23 / 26. At least so many that a slice's
+// histogram stays within 32 bits.
+constexpr int64_t kMostSlice = 1 << 17;
 int sample_blocks(int64_t rows, int64_t vocab) {
   int c = 1;
-  while (c < kMostBlocks && vocab > (int64_t)c * CR_SAMPLE_SLICE) c *= 2;
+  while (c < kMostBlocks && ((rows * c * 2 <= 512 && vocab >= (int64_t)c * 2 * 4096) ||
+                             vocab > (int64_t)c * kMostSlice))
+    c *= 2;
   return c;
 }
 
@@ -1197,7 +1200,9 @@ cr_status cr_sample(const cr_sample_args* a, int64_t* tokens, void* stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int blocks = sample_blocks(a->rows, a->vocab);
   const int slice = (int)ceil_div(ceil_div(a->vocab, blocks), 8) * 8;
-  const bool hold = kFixed + slice * es <= 200 * 1024;
+  // in shared memory where two blocks an SM fit (200 rows of 65,536 in two blocks
+  // each: 108 us with one, 94 with two that read their slices again from L2)
+  const bool hold = kFixed + slice * es <= 112 * 1024;
   const size_t smem = kFixed + (hold ? slice * es : 0);
   const bool wide = rows_aligned(a->logits, a->row_stride, 0, es, 16);
   Settings all;
