@@ -30,7 +30,9 @@ struct NormIn {
   const float *w, *b;
 };
 
+// (len 0: one batch, whose rows need no division)
 __device__ __forceinline__ int64_t row_offset(int64_t r, int64_t len, Rows2 s) {
+  if (len == 0) return r * s.ts;
   int64_t t;
   const int64_t b = divide(r, len, t);
   return b * s.bs + t * s.ts;
@@ -45,6 +47,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 struct Stats {
   float mean, rest, rstd;
 };
+// From the sums of x - mean and of its square.
+__device__ __forceinline__ Stats moments(float mean, const float (&v)[2], float share, float eps) {
+  Stats r = {mean, v[0] * share, 0.0f};
+  r.rstd = rsqrtf(fmaxf(fmaf(v[1], share, -r.rest * r.rest), 0.0f) + eps);
+  return r;
+}
 
 // A row's elements in the registers of `threads` threads, E each, 16 bytes of
 // neighbours at a time: whole accesses (kWide: rows on 16 bytes, a whole number
@@ -76,6 +84,7 @@ struct Held {
       }
     }
   }
+  __device__ __forceinline__ F2 pair(int i) const { return pack2(get(2 * i), get(2 * i + 1)); }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (kWide) {
       const uint4& w4 = q[e / V];
@@ -93,8 +102,11 @@ struct Held {
       return to_f32(v[e]);
     }
   }
-  static __device__ __forceinline__ void store(T* p, const float (&f)[E], int t, int threads,
+  static __device__ __forceinline__ void store(T* p, const F2 (&pairs)[E / 2], int t, int threads,
                                                int dim) {
+    float f[E];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) unpack2(pairs[i], f[2 * i], f[2 * i + 1]);
     if constexpr (kWide) {
 #pragma unroll
       for (int k = 0; k < kPacks; ++k) {
@@ -119,10 +131,11 @@ struct Held {
 // Weights of a thread's columns (`none` without them, and behind the row).
 template <int E, int V, bool kWide>
 __device__ __forceinline__ void load_vector(const float* w, float none, int t, int threads, int dim,
-                                            float (&f)[E]) {
+                                            F2 (&pairs)[E / 2]) {
+  float f[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) f[e] = none;
-  if (w == nullptr) return;
+  if (w != nullptr) {
   if constexpr (kWide) {
 #pragma unroll
     for (int k = 0; k < E / V; ++k) {
@@ -143,111 +156,176 @@ __device__ __forceinline__ void load_vector(const float* w, float none, int t, i
       if (c < dim) f[e] = __ldg(w + c);
     }
   }
+  }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) pairs[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
-// Sums of two numbers over the threads of a row (whole warps), in one order: by
-// lanes, then by warps. buf: two numbers a warp, not in use.
-__device__ __forceinline__ float2 row_sum(float a, float b, int threads, float2* buf) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (threads <= 32) return make_float2(a, b);
-  const int warp = threadIdx.x / 32, warps = threads / 32, first = warp / warps * warps;
-  if (threadIdx.x % 32 == 0) buf[warp] = make_float2(a, b);
+// The threads of a row: whole warps of a block.
+struct Team {
+  int threads, t;  // and this one's number
+  int warps, first;  // its warps, and the one that this lane adds up
+  bool full;         // whether all elements of this warp lie inside the row
+  __device__ Team(int threads_, int dim, int V, int packs) : threads(threads_) {
+    t = threadIdx.x % threads;
+    warps = threads / 32;
+    first = threadIdx.x / threads * warps + threadIdx.x % 32 % warps;
+    full = __all_sync(~0u, ((packs - 1) * threads + t) * V + V <= dim);
+  }
+};
+
+// Sums of N numbers over the threads of a row, in one order: by lanes, then by
+// warps, whose sums every warp adds up in the same tree. buf: N numbers a warp,
+// not in use.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], const Team& team, float (*buf)[32]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+  if (team.warps == 1) return;
+  if (threadIdx.x % 32 == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) buf[k][threadIdx.x / 32] = v[k];
+  }
   __syncthreads();
-  // (every warp adds up its row's in the same tree; absent ones count as zero)
-  const float2 v = threadIdx.x % 32 < warps ? buf[first + threadIdx.x % 32] : make_float2(0.0f, 0.0f);
-  a = v.x;
-  b = v.y;
+  // (lanes read the row's warps over and over: a tree of warps in every lane)
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = buf[k][team.first];
 #pragma unroll
   for (int s = 16; s > 0; s /= 2) {
-    if (s < warps) {
-      a = __fadd_rn(a, __shfl_xor_sync(~0u, a, s));
-      b = __fadd_rn(b, __shfl_xor_sync(~0u, b, s));
-    }
+    if (s >= team.warps) continue;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __fadd_rn(v[k], __shfl_xor_sync(~0u, v[k], s));
   }
-  return make_float2(__shfl_sync(~0u, a, 0), __shfl_sync(~0u, b, 0));
+}
+__device__ __forceinline__ float both(F2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return __fadd_rn(lo, hi);
+}
+
+// Zeros what is behind the row.
+template <class H, int N>
+__device__ __forceinline__ void clip(F2 (&d)[N], const Team& team, int dim) {
+  if (team.full) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float lo, hi;
+    unpack2(d[i], lo, hi);
+    d[i] = pack2(H::column(2 * i, team.t, team.threads) < dim ? lo : 0.0f,
+                 H::column(2 * i + 1, team.t, team.threads) < dim ? hi : 0.0f);
+  }
 }
 
 // The statistics of a row whose elements are x; leaves x - mean in d.
 template <class T, int E, bool kWide>
-__device__ __forceinline__ Stats row_stats(const Held<T, E, kWide>& x, int t, int threads, int dim,
-                                           float eps, float2* buf, float (&d)[E]) {
-  float s = 0.0f;
+__device__ __forceinline__ Stats row_stats(const Held<T, E, kWide>& x, const Team& team, int dim,
+                                           float share, float eps, float (*buf)[32],
+                                           F2 (&d)[E / 2]) {
+  F2 s = 0, s2 = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    d[e] = x.get(e);
-    s += d[e];
+  for (int i = 0; i < E / 2; ++i) {
+    d[i] = x.pair(i);
+    s = add2(s, d[i]);
   }
-  Stats r;
-  r.mean = row_sum(s, 0.0f, threads, buf).x / (float)dim;
-  float d1 = 0.0f, d2 = 0.0f;
+  float m[1] = {both(s)};
+  row_sum(m, team, buf);
+  const float mean = m[0] * share;
+  const F2 minus = pack2(-mean, -mean);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    d[e] = Held<T, E, kWide>::column(e, t, threads) < dim ? d[e] - r.mean : 0.0f;
-    d1 += d[e];
-    d2 = fmaf(d[e], d[e], d2);
+  for (int i = 0; i < E / 2; ++i) d[i] = add2(d[i], minus);
+  clip<Held<T, E, kWide>>(d, team, dim);
+  s = 0;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    s = add2(s, d[i]);
+    s2 = fma2(d[i], d[i], s2);
   }
-  const float2 v = row_sum(d1, d2, threads, buf + 32);
-  r.rest = v.x / (float)dim;
-  const float var = fmaxf(v.y / (float)dim - r.rest * r.rest, 0.0f);
-  r.rstd = 1.0f / sqrtf(var + eps);
-  return r;
+  float v[2] = {both(s), both(s2)};
+  row_sum(v, team, buf + 1);
+  return moments(mean, v, share, eps);
 }
 
-// A row in the registers of `threads` threads, several rows a block.
+// A row in the registers of `threads` threads, several rows a block, which walks
+// rows `blocks` apart, the next one's elements in flight. y NULL: the statistics
+// alone.
 template <class T, int kThreads, int E, bool kWide>
 __global__ void __launch_bounds__(kThreads)
 layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
                   float* __restrict__ stats) {
   using H = Held<T, E, kWide>;
-  __shared__ float2 buf[64];
-  const int t = threadIdx.x % threads, dim = (int)in.dim;
-  const int64_t r = (int64_t)blockIdx.x * (kThreads / threads) + threadIdx.x / threads;
-  const bool real = r < in.rows;
-  H x;
-  x.load(in.x + row_offset(real ? r : 0, in.len, in.xs), t, threads, real ? dim : 0);
-  float d[E];
-  const Stats st = row_stats(x, t, threads, dim, in.eps, buf, d);
-  if (!real) return;
-  if (stats != nullptr && t == 0) {
-    stats[3 * r] = st.mean;
-    stats[3 * r + 1] = st.rest;
-    stats[3 * r + 2] = st.rstd;
+  __shared__ float buf[2][3][32];
+  const int dim = (int)in.dim;
+  const Team team(threads, dim, H::V, E / H::V);
+  const int t = team.t, groups = kThreads / threads;
+  const float share = 1.0f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  // 1024 threads have 64 registers each: no room for the next row, nor to keep
+  // the weights
+  constexpr bool kLean = kThreads == 1024;
+  F2 w[E / 2], b[E / 2];
+  if constexpr (!kLean) {
+    load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
+    load_vector<E, H::V, kWide>(in.b, 0.0f, t, threads, dim, b);
   }
-  if (y == nullptr) return;  // the statistics alone
-  float w[E], b[E];
-  load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
-  load_vector<E, H::V, kWide>(in.b, 0.0f, t, threads, dim, b);
+  H next;
+  const auto fetch = [&](int64_t r) {
+    const bool real = r < in.rows;
+    next.load(in.x + row_offset(real ? r : 0, in.len, in.xs), t, threads, real ? dim : 0);
+  };
+  int64_t r = (int64_t)blockIdx.x * groups + threadIdx.x / threads;
+  if (!kLean) fetch(r);
+  // (as many turns for all rows of a block: they wait for one another)
+  for (int64_t r0 = (int64_t)blockIdx.x * groups, turn = 0; r0 < in.rows; r0 += step, ++turn) {
+    if (kLean) fetch(r);
+    const H x = next;
+    const int64_t now = r;
+    r += step;
+    if (!kLean && r0 + step < in.rows) fetch(r);
+    F2 d[E / 2];
+    const Stats st = row_stats(x, team, dim, share, in.eps, buf[turn & 1], d);
+    if (now >= in.rows) continue;
+    if (stats != nullptr && t == 0) {
+      stats[3 * now] = st.mean;
+      stats[3 * now + 1] = st.rest;
+      stats[3 * now + 2] = st.rstd;
+    }
+    if (y == nullptr) continue;
+    if constexpr (kLean) {
+      load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
+      load_vector<E, H::V, kWide>(in.b, 0.0f, t, threads, dim, b);
+    }
+    const F2 rstd = pack2(st.rstd, st.rstd);
+    const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
 #pragma unroll
-  for (int e = 0; e < E; ++e) d[e] = fmaf((d[e] - st.rest) * st.rstd, w[e], b[e]);
-  H::store(y + row_offset(r, in.len, ys), d, t, threads, dim);
+    for (int i = 0; i < E / 2; ++i) d[i] = fma2(fma2(d[i], rstd, shift), w[i], b[i]);
+    H::store(y + row_offset(now, in.len, ys), d, t, threads, dim);
+  }
 }
 
 // Rows that registers do not hold: a block a row, read again from L2.
 constexpr int kLongThreads = 512;
 template <class T>
-__device__ Stats long_stats(const T* x, int64_t dim, float eps, float2* buf) {
-  float s = 0.0f;
-  for (int64_t c = threadIdx.x; c < dim; c += kLongThreads) s += to_f32(x[c]);
-  Stats r;
-  r.mean = row_sum(s, 0.0f, kLongThreads, buf).x / (float)dim;
-  float d1 = 0.0f, d2 = 0.0f;
+__device__ Stats long_stats(const T* x, int64_t dim, float eps, float (*buf)[32]) {
+  const float share = 1.0f / (float)dim;
+  float s[1] = {0.0f};
+  for (int64_t c = threadIdx.x; c < dim; c += kLongThreads) s[0] += to_f32(x[c]);
+  const Team team(kLongThreads, 0, 1, 1);
+  row_sum(s, team, buf);
+  const float mean = s[0] * share;
+  float v[2] = {0.0f, 0.0f};
   for (int64_t c = threadIdx.x; c < dim; c += kLongThreads) {
-    const float d = to_f32(x[c]) - r.mean;
-    d1 += d;
-    d2 = fmaf(d, d, d2);
+    const float d = to_f32(x[c]) - mean;
+    v[0] += d;
+    v[1] = fmaf(d, d, v[1]);
   }
-  const float2 v = row_sum(d1, d2, kLongThreads, buf + 32);
-  r.rest = v.x / (float)dim;
-  const float var = fmaxf(v.y / (float)dim - r.rest * r.rest, 0.0f);
-  r.rstd = 1.0f / sqrtf(var + eps);
-  return r;
+  row_sum(v, team, buf + 1);
+  return moments(mean, v, share, eps);
 }
 
 template <class T>
 __global__ void __launch_bounds__(kLongThreads)
 layer_norm_long_kernel(NormIn<T> in, T* __restrict__ y, Rows2 ys, float* __restrict__ stats) {
-  __shared__ float2 buf[64];
+  __shared__ float buf[3][32];
   const int64_t r = blockIdx.x;
   const T* x = in.x + row_offset(r, in.len, in.xs);
   const Stats st = long_stats(x, in.dim, in.eps, buf);
@@ -272,15 +350,17 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
                            const float* __restrict__ stats, T* __restrict__ dx, Rows2 os,
                            float* __restrict__ part) {
   using H = Held<T, E, kWide>;
-  __shared__ float2 buf[2][96];
+  __shared__ float buf[2][5][32];
   extern __shared__ float sums[];  // [2][dim], for several rows a block
-  const int t = threadIdx.x % threads, dim = (int)in.dim;
-  const int groups = kThreads / threads, group = threadIdx.x / threads;
+  const int dim = (int)in.dim;
+  const Team team(threads, dim, H::V, E / H::V);
+  const int t = team.t, groups = kThreads / threads, group = threadIdx.x / threads;
   const int64_t step = (int64_t)gridDim.x * groups;
-  float w[E], dw[E], db[E];
+  const float share = 1.0f / (float)dim;
+  F2 w[E / 2], dw[E / 2], db[E / 2];
   load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
 #pragma unroll
-  for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.0f;
+  for (int i = 0; i < E / 2; ++i) dw[i] = db[i] = 0;
   H x, g;
   Stats next = {0.0f, 0.0f, 0.0f};
   const auto fetch = [&](int64_t r) {
@@ -294,43 +374,56 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
   fetch(r);
   // (as many turns for all rows of a block: they wait for one another)
   for (int64_t r0 = (int64_t)blockIdx.x * groups, turn = 0; r0 < in.rows; r0 += step, ++turn) {
-    float2* const b = buf[turn & 1];
-    float n[E], q[E];
+    float(*const b)[32] = buf[turn & 1];
+    F2 n[E / 2], q[E / 2];
     Stats st = next;
     if (stats == nullptr) {
-      st = row_stats(x, t, threads, dim, in.eps, b, n);
+      st = row_stats(x, team, dim, share, in.eps, b, n);
     } else {
+      const F2 minus = pack2(-st.mean, -st.mean);
 #pragma unroll
-      for (int e = 0; e < E; ++e) n[e] = x.get(e) - st.mean;
+      for (int i = 0; i < E / 2; ++i) n[i] = add2(x.pair(i), minus);
     }
-    float s1 = 0.0f, s2 = 0.0f;
+    const F2 rstd = pack2(st.rstd, st.rstd);
+    const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      n[e] = H::column(e, t, threads) < dim ? (n[e] - st.rest) * st.rstd : 0.0f;
-      const float v = g.get(e);
-      dw[e] = fmaf(v, n[e], dw[e]);
-      db[e] += v;
-      q[e] = v * w[e];
-      s1 += q[e];
-      s2 = fmaf(q[e], n[e], s2);
+    for (int i = 0; i < E / 2; ++i) n[i] = fma2(n[i], rstd, shift);
+    clip<H>(n, team, dim);
+    F2 s1 = 0, s2 = 0;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const F2 u = g.pair(i);
+      dw[i] = fma2(u, n[i], dw[i]);
+      db[i] = add2(db[i], u);
+      q[i] = mul2(u, w[i]);
+      s1 = fma2(u, w[i], s1);  // (a sum of q, which add2 is not for)
+      s2 = fma2(q[i], n[i], s2);
     }
     const int64_t now = r;
     r += step;
     fetch(r);
-    const float2 v = row_sum(s1, s2, threads, b + 64);
+    float v[2] = {both(s1), both(s2)};
+    row_sum(v, team, b + 3);
     if (now < in.rows) {
-      const float a1 = v.x / (float)dim, a2 = v.y / (float)dim;
+      const float a1 = v[0] * share * -st.rstd, a2 = v[1] * share * -st.rstd;
+      const F2 p1 = pack2(a1, a1), p2 = pack2(a2, a2);
 #pragma unroll
-      for (int e = 0; e < E; ++e) q[e] = st.rstd * fmaf(-n[e], a2, q[e] - a1);
+      for (int i = 0; i < E / 2; ++i) q[i] = fma2(n[i], p2, fma2(q[i], rstd, p1));
       H::store(dx + row_offset(now, in.len, os), q, t, threads, dim);
     }
+  }
+  float dw1[E], db1[E];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    unpack2(dw[i], dw1[2 * i], dw1[2 * i + 1]);
+    unpack2(db[i], db1[2 * i], db1[2 * i + 1]);
   }
   float* const out = part + (int64_t)blockIdx.x * 2 * dim;
   if (groups == 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int c = H::column(e, t, threads);
-      if (c < dim) out[c] = dw[e], out[dim + c] = db[e];
+      if (c < dim) out[c] = dw1[e], out[dim + c] = db1[e];
     }
     return;
   }
@@ -340,8 +433,8 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
       for (int e = 0; e < E; ++e) {
         const int c = H::column(e, t, threads);
         if (c < dim) {
-          sums[c] = k == 0 ? dw[e] : sums[c] + dw[e];
-          sums[dim + c] = k == 0 ? db[e] : sums[dim + c] + db[e];
+          sums[c] = k == 0 ? dw1[e] : sums[c] + dw1[e];
+          sums[dim + c] = k == 0 ? db1[e] : sums[dim + c] + db1[e];
         }
       }
     }
@@ -355,7 +448,7 @@ template <class T>
 __global__ void __launch_bounds__(kLongThreads)
 layer_norm_backward_long_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds,
                                 const float* __restrict__ stats, T* __restrict__ dx, Rows2 os) {
-  __shared__ float2 buf[32];
+  __shared__ float buf[2][32];
   const int64_t r = blockIdx.x;
   const T* x = in.x + row_offset(r, in.len, in.xs);
   const T* d = dy + row_offset(r, in.len, ds);
@@ -367,8 +460,9 @@ layer_norm_backward_long_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds
     s1 += g;
     s2 = fmaf(g, n, s2);
   }
-  const float2 v = row_sum(s1, s2, kLongThreads, buf);
-  const float a1 = v.x / (float)in.dim, a2 = v.y / (float)in.dim;
+  float v[2] = {s1, s2};
+  row_sum(v, Team(kLongThreads, 0, 1, 1), buf);
+  const float a1 = v[0] / (float)in.dim, a2 = v[1] / (float)in.dim;
   T* o = dx + row_offset(r, in.len, os);
   for (int64_t c = threadIdx.x; c < in.dim; c += kLongThreads) {
     const float n = ((to_f32(x[c]) - st.mean) - st.rest) * st.rstd;
@@ -427,9 +521,13 @@ layer_norm_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t dim
   }
 }
 
+// (A batch whose rows are evenly spaced is one sequence: its strides and all
+// others' are then the time strides alone.)
+bool even(int64_t batch, int64_t len, Rows2 s) { return batch <= 1 || s.bs == len * s.ts; }
+
 template <class T>
-NormIn<T> norm_in(const cr_layer_norm_args* a) {
-  return {a->batch * a->len, a->len, a->dim, a->eps, static_cast<const T*>(a->x),
+NormIn<T> norm_in(const cr_layer_norm_args* a, bool one_batch) {
+  return {a->batch * a->len, one_batch ? 0 : a->len, a->dim, a->eps, static_cast<const T*>(a->x),
           {a->x_batch_stride, a->x_time_stride}, a->weight, a->bias};
 }
 
@@ -460,10 +558,10 @@ struct NormShape {
 
 NormShape norm_shape(int64_t dim) {
   NormShape sh = {256, 0, 8};
-  if (dim > 32768) return sh;
+  if (dim > 16384) return sh;
   if (dim > 2048) sh.block = 512;
   if (dim > 4096) sh.E = 16;
-  if (dim > 8192) sh.block = 1024, sh.E = 32;
+  if (dim > 8192) sh.block = 1024;
   sh.threads = 32;
   while ((int64_t)sh.threads * sh.E < dim) sh.threads *= 2;
   return sh;
@@ -496,29 +594,34 @@ bool norm_wide(const cr_layer_norm_args* a) {
     else { constexpr bool W = false; __VA_ARGS__; }                           \
   }
 #define CR_NORM_SHAPE(SH, WIDE, ...)                                          \
-  if (SH.block == 1024) CR_NORM_CASE(1024, 32, WIDE, __VA_ARGS__)             \
+  if (SH.block == 1024) CR_NORM_CASE(1024, 16, WIDE, __VA_ARGS__)             \
   else CR_NORM_BACKWARD_SHAPE(SH, WIDE, __VA_ARGS__)
 #define CR_NORM_BACKWARD_SHAPE(SH, WIDE, ...)                                 \
   if (SH.E == 16) CR_NORM_CASE(512, 16, WIDE, __VA_ARGS__)                    \
   else if (SH.block == 512) CR_NORM_CASE(512, 8, WIDE, __VA_ARGS__)           \
   else CR_NORM_CASE(256, 8, WIDE, __VA_ARGS__)
 
+#ifndef CR_NORM_RES
+#define CR_NORM_RES(B) (1024 / (B))
+#endif
 void launch_norm(const cr_layer_norm_args* a, void* y, Rows2 ys, float* stats, bool wide,
                  cudaStream_t s) {
   const NormShape sh = norm_shape(a->dim);
   const int64_t rows = a->batch * a->len;
+  const Rows2 xs = {a->x_batch_stride, a->x_time_stride};
+  const bool one = even(a->batch, a->len, xs) && even(a->batch, a->len, ys);
   CR_MODEL_TYPE(a->dt, {
     T* out = static_cast<T*>(y);
     if (sh.threads == 0) {
       CR_LAUNCH(kKLayerNorm, s,
-                layer_norm_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(norm_in<T>(a), out,
+                layer_norm_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(norm_in<T>(a, one), out,
                                                                                   ys, stats));
     } else {
       CR_NORM_SHAPE(sh, wide, {
         CR_LAUNCH(kKLayerNorm, s,
                   layer_norm_kernel<T, B, E, W>
-                  <<<(unsigned)ceil_div(rows, B / sh.threads), B, 0, s>>>(norm_in<T>(a), sh.threads,
-                                                                          out, ys, stats));
+                  <<<(unsigned)std::min<int64_t>(ceil_div(rows, B / sh.threads), 152 * CR_NORM_RES(B)), B,
+                     0, s>>>(norm_in<T>(a, one), sh.threads, out, ys, stats));
       });
     }
   });
@@ -595,26 +698,29 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
   const int64_t parts = blocks != 0 ? blocks : ceil_div(rows, kSumRows);
   const float* stats = g->stats;
   if (rows > 0 && blocks == 0 && stats == nullptr) {
-    launch_norm(a, nullptr, {0, 0}, kept, norm_wide(a), s);
+    launch_norm(a, nullptr, {a->x_batch_stride, a->x_time_stride}, kept, norm_wide(a), s);
     stats = kept;
   }
+  const Rows2 xs = {a->x_batch_stride, a->x_time_stride};
+  const bool one = even(a->batch, a->len, xs) && even(a->batch, a->len, ds) &&
+                   even(a->batch, a->len, os);
   CR_MODEL_TYPE(a->dt, {
     const T* dy = static_cast<const T*>(g->dy);
     T* dx = static_cast<T*>(g->dx);
     if (rows > 0 && blocks == 0) {
       CR_LAUNCH(kKLayerNormBackward, s,
                 layer_norm_backward_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(
-                    norm_in<T>(a), dy, ds, stats, dx, os));
+                    norm_in<T>(a, one), dy, ds, stats, dx, os));
       CR_LAUNCH(kKLayerNormSum, s,
                 layer_norm_part_kernel<T>
                 <<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(parts, 65535)), 256, 0, s>>>(
-                    norm_in<T>(a), dy, ds, stats, part));
+                    norm_in<T>(a, one), dy, ds, stats, part));
     } else if (rows > 0) {
       CR_NORM_BACKWARD_SHAPE(sh, wide, {
         const size_t smem = sh.threads < B ? (size_t)a->dim * 8 : 0;
         CR_LAUNCH(kKLayerNormBackward, s,
                   layer_norm_backward_kernel<T, B, E, W><<<(unsigned)blocks, B, smem, s>>>(
-                      norm_in<T>(a), sh.threads, dy, ds, stats, dx, os, part));
+                      norm_in<T>(a, one), sh.threads, dy, ds, stats, dx, os, part));
       });
     }
     if (g->dweight != nullptr || g->dbias != nullptr)
