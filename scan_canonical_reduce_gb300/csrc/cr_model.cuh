@@ -323,15 +323,17 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kMaxBlocks = 0x7FFFFFFF;  // of a grid's x axis
 
 // Launches a kernel with `smem` bytes of dynamic shared memory and its blocks in
-// clusters; false: not launched.
+// clusters; false: not launched. (Kernels have up to 3 KB of other shared memory.)
 template <class... P, class... A>
 bool launch_clusters(void (*kernel)(P...), int64_t blocks, int cluster, int threads, size_t smem,
                      cudaStream_t s, A... args) {
   // (one value for all calls: several threads may be between here and the launch)
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-          cudaSuccess)
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024) !=
+          cudaSuccess) {
+    cudaGetLastError();  // not the next call's
     return false;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
@@ -343,7 +345,9 @@ bool launch_clusters(void (*kernel)(P...), int64_t blocks, int cluster, int thre
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 // A workspace begins with the status word of the calls that wait on the

@@ -17,6 +17,9 @@
 namespace cr {
 namespace {
 
+#ifndef CR_NORM_BW
+#define CR_NORM_BW 3
+#endif
 struct Rows2 {
   int64_t bs, ts;
 };
@@ -54,123 +57,14 @@ __device__ __forceinline__ Stats moments(float mean, const float (&v)[2], float 
   return r;
 }
 
-// A row's elements in the registers of `threads` threads, E each, 16 bytes of
-// neighbours at a time: whole accesses (kWide: rows on 16 bytes, a whole number
-// of accesses long) or, for the same bits, one by one (a warp's neighbours are
-// then in L1).
-template <class T, int E, bool kWide>
-struct Held {
-  static constexpr int V = 16 / sizeof(T);
-  static constexpr int kPacks = E / V;
-  static_assert(E % V == 0, "whole accesses");
-  uint4 q[kWide ? kPacks : 1];
-  T v[kWide ? 1 : E];
-
-  static __device__ __forceinline__ int column(int e, int t, int threads) {
-    return (e / V * threads + t) * V + e % V;
-  }
-  __device__ __forceinline__ void load(const T* p, int t, int threads, int dim) {
-    if constexpr (kWide) {
-#pragma unroll
-      for (int k = 0; k < kPacks; ++k) {
-        const int c = (k * threads + t) * V;
-        q[k] = c < dim ? __ldcs(reinterpret_cast<const uint4*>(p + c)) : make_uint4(0, 0, 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = column(e, t, threads);
-        v[e] = c < dim ? p[c] : from_f32<T>(0.0f);
-      }
-    }
-  }
-  __device__ __forceinline__ F2 pair(int i) const { return pack2(get(2 * i), get(2 * i + 1)); }
-  __device__ __forceinline__ float get(int e) const {
-    if constexpr (kWide) {
-      const uint4& w4 = q[e / V];
-      const int i = e % V;
-      if constexpr (sizeof(T) == 4) {
-        return __uint_as_float(i == 0 ? w4.x : i == 1 ? w4.y : i == 2 ? w4.z : w4.w);
-      } else {
-        const uint32_t w = i / 2 == 0 ? w4.x : i / 2 == 1 ? w4.y : i / 2 == 2 ? w4.z : w4.w;
-        if constexpr (std::is_same<T, __nv_bfloat16>::value)
-          return __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
-        else
-          return __half2float(__ushort_as_half((unsigned short)(w >> (i % 2 * 16))));
-      }
-    } else {
-      return to_f32(v[e]);
-    }
-  }
-  static __device__ __forceinline__ void store(T* p, const F2 (&pairs)[E / 2], int t, int threads,
-                                               int dim) {
-    float f[E];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) unpack2(pairs[i], f[2 * i], f[2 * i + 1]);
-    if constexpr (kWide) {
-#pragma unroll
-      for (int k = 0; k < kPacks; ++k) {
-        const int c = (k * threads + t) * V;
-        if (c < dim) {
-          float g[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) g[i] = f[k * V + i];
-          store_f32<T, V>(p + c, true, V, g);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = column(e, t, threads);
-        if (c < dim) p[c] = from_f32<T>(f[e]);
-      }
-    }
-  }
-};
-
-// Weights of a thread's columns (`none` without them, and behind the row).
-template <int E, int V, bool kWide>
-__device__ __forceinline__ void load_vector(const float* w, float none, int t, int threads, int dim,
-                                            F2 (&pairs)[E / 2]) {
-  float f[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) f[e] = none;
-  if (w != nullptr) {
-  if constexpr (kWide) {
-#pragma unroll
-    for (int k = 0; k < E / V; ++k) {
-      const int c = (k * threads + t) * V;
-      if (c < dim) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const float4 q = __ldg(reinterpret_cast<const float4*>(w + c + i));
-          f[k * V + i] = q.x, f[k * V + i + 1] = q.y;
-          f[k * V + i + 2] = q.z, f[k * V + i + 3] = q.w;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = (e / V * threads + t) * V + e % V;
-      if (c < dim) f[e] = __ldg(w + c);
-    }
-  }
-  }
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) pairs[i] = pack2(f[2 * i], f[2 * i + 1]);
-}
-
 // The threads of a row: whole warps of a block.
 struct Team {
-  int threads, t;  // and this one's number
+  int threads, t;    // and this one's number
   int warps, first;  // its warps, and the one that this lane adds up
-  bool full;         // whether all elements of this warp lie inside the row
-  __device__ Team(int threads_, int dim, int V, int packs) : threads(threads_) {
+  __device__ explicit Team(int threads_) : threads(threads_) {
     t = threadIdx.x % threads;
     warps = threads / 32;
     first = threadIdx.x / threads * warps + threadIdx.x % 32 % warps;
-    full = __all_sync(~0u, ((packs - 1) * threads + t) * V + V <= dim);
   }
 };
 
@@ -190,9 +84,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const Team& team, float (
   // (lanes read the row's warps over and over: a tree of warps in every lane)
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = buf[k][team.first];
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2) {
-    if (s >= team.warps) continue;
+  for (int s = team.warps / 2; s > 0; s /= 2) {
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = __fadd_rn(v[k], __shfl_xor_sync(~0u, v[k], s));
   }
@@ -203,103 +95,220 @@ __device__ __forceinline__ float both(F2 v) {
   return __fadd_rn(lo, hi);
 }
 
+// 16 bytes of neighbours: a whole access (kWide: rows on 16 bytes, a whole
+// number of accesses long) or, for the same bits, one by one (a warp's
+// neighbours are then in L1). have: elements inside the row.
+template <class T, bool kWide>
+struct Quad {
+  static constexpr int V = 16 / sizeof(T);
+  uint4 q;
+  __device__ __forceinline__ void load(const T* p, int have) {
+    q = make_uint4(0, 0, 0, 0);
+    if constexpr (kWide) {
+      if (have > 0) q = __ldcs(reinterpret_cast<const uint4*>(p));
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (i >= have) continue;
+        if constexpr (sizeof(T) == 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        else
+          w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << i % 2 * 16;
+      }
+      q = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ F2 pair(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return i == 0 ? pack2(__uint_as_float(q.x), __uint_as_float(q.y))
+                    : pack2(__uint_as_float(q.z), __uint_as_float(q.w));
+    } else {
+      const uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        return pack2(f.x, f.y);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const F2 (&v)[V / 2], int have) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    store_f32<T, V>(p, kWide && have > 0, have, f);
+  }
+};
+// The same of weights, V floats on 16 bytes; `none` without them.
+template <int V, bool kWide>
+__device__ __forceinline__ void load_vector(const float* w, int c, int have, float none,
+                                            F2 (&v)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v[i] = pack2(none, none);
+  if (w == nullptr) return;
+  if constexpr (kWide) {
+    if (have > 0) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(w + c + i));
+        v[i / 2] = pack2(q.x, q.y);
+        v[i / 2 + 1] = pack2(q.z, q.w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      v[i] = pack2(2 * i < have ? __ldg(w + c + 2 * i) : none,
+                   2 * i + 1 < have ? __ldg(w + c + 2 * i + 1) : none);
+  }
+}
 // Zeros what is behind the row.
-template <class H, int N>
-__device__ __forceinline__ void clip(F2 (&d)[N], const Team& team, int dim) {
-  if (team.full) return;
+template <int N>
+__device__ __forceinline__ void clip(F2 (&d)[N], int have) {
+  if (have >= 2 * N) return;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float lo, hi;
     unpack2(d[i], lo, hi);
-    d[i] = pack2(H::column(2 * i, team.t, team.threads) < dim ? lo : 0.0f,
-                 H::column(2 * i + 1, team.t, team.threads) < dim ? hi : 0.0f);
+    d[i] = pack2(2 * i < have ? lo : 0.0f, 2 * i + 1 < have ? hi : 0.0f);
   }
 }
 
-// The statistics of a row whose elements are x; leaves x - mean in d.
-template <class T, int E, bool kWide>
-__device__ __forceinline__ Stats row_stats(const Held<T, E, kWide>& x, const Team& team, int dim,
-                                           float share, float eps, float (*buf)[32],
-                                           F2 (&d)[E / 2]) {
-  F2 s = 0, s2 = 0;
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    d[i] = x.pair(i);
-    s = add2(s, d[i]);
-  }
-  float m[1] = {both(s)};
-  row_sum(m, team, buf);
-  const float mean = m[0] * share;
-  const F2 minus = pack2(-mean, -mean);
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) d[i] = add2(d[i], minus);
-  clip<Held<T, E, kWide>>(d, team, dim);
-  s = 0;
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    s = add2(s, d[i]);
-    s2 = fma2(d[i], d[i], s2);
-  }
-  float v[2] = {both(s), both(s2)};
-  row_sum(v, team, buf + 1);
-  return moments(mean, v, share, eps);
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A row in the registers of `threads` threads, several rows a block, which walks
-// rows `blocks` apart, the next one's elements in flight. y NULL: the statistics
-// alone.
-template <class T, int kThreads, int E, bool kWide>
-__global__ void __launch_bounds__(kThreads)
+// A row a warp, or several warps a row: a lane has kQuads times 16 bytes, so that
+// what a row costs besides its elements, sums over lanes above all, is shared by
+// many of them, and few rows wait at a barrier. Rows come by way of shared
+// memory, each thread's own part of it, two rows ahead, and stay there as they
+// stand in memory; the weights stand beside them. y NULL: the statistics alone.
+constexpr int kNormThreads = 256;
+template <int kQuads>
+struct NormShared {
+  uint4 q[2][kQuads][kNormThreads];  // rows
+  // Weights and biases, four columns of a lane at a time, so that a warp's
+  // accesses are consecutive: [2][quad][V / 4][thread].
+  float4 w[1];
+};
+template <class T, int kQuads, bool kWide>
+__global__ void __launch_bounds__(kNormThreads)
 layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
                   float* __restrict__ stats) {
-  using H = Held<T, E, kWide>;
+  using Q = Quad<T, kWide>;
+  constexpr int V = Q::V, N = V / 2;
   __shared__ float buf[2][3][32];
-  const int dim = (int)in.dim;
-  const Team team(threads, dim, H::V, E / H::V);
-  const int t = team.t, groups = kThreads / threads;
-  const float share = 1.0f / (float)dim;
+  extern __shared__ __align__(16) char shared[];
+  NormShared<kQuads>& sh = *reinterpret_cast<NormShared<kQuads>*>(shared);
+  const int dim = (int)in.dim, columns = kQuads * threads * V;
+  const Team team(threads);
+  const int groups = kNormThreads / threads;
   const int64_t step = (int64_t)gridDim.x * groups;
-  // 1024 threads have 64 registers each: no room for the next row, nor to keep
-  // the weights
-  constexpr bool kLean = kThreads == 1024;
-  F2 w[E / 2], b[E / 2];
-  if constexpr (!kLean) {
-    load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
-    load_vector<E, H::V, kWide>(in.b, 0.0f, t, threads, dim, b);
-  }
-  H next;
-  const auto fetch = [&](int64_t r) {
-    const bool real = r < in.rows;
-    next.load(in.x + row_offset(real ? r : 0, in.len, in.xs), t, threads, real ? dim : 0);
+  const auto column = [&](int k) { return (k * threads + team.t) * V; };
+  const auto fetch = [&](int64_t r, int turn) {
+    if (r < in.rows) {
+      const T* p = in.x + row_offset(r, in.len, in.xs);
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        if constexpr (kWide) {
+          if (column(k) < dim) copy16(&sh.q[turn][k][threadIdx.x], p + column(k));
+        } else {
+          Q q;
+          q.load(p + column(k), dim - column(k));
+          sh.q[turn][k][threadIdx.x] = q.q;
+        }
+      }
+    }
+    if constexpr (kWide) copy_commit();
   };
   int64_t r = (int64_t)blockIdx.x * groups + threadIdx.x / threads;
-  if (!kLean) fetch(r);
-  // (as many turns for all rows of a block: they wait for one another)
-  for (int64_t r0 = (int64_t)blockIdx.x * groups, turn = 0; r0 < in.rows; r0 += step, ++turn) {
-    if (kLean) fetch(r);
-    const H x = next;
-    const int64_t now = r;
-    r += step;
-    if (!kLean && r0 + step < in.rows) fetch(r);
-    F2 d[E / 2];
-    const Stats st = row_stats(x, team, dim, share, in.eps, buf[turn & 1], d);
-    if (now >= in.rows) continue;
-    if (stats != nullptr && t == 0) {
-      stats[3 * now] = st.mean;
-      stats[3 * now + 1] = st.rest;
-      stats[3 * now + 2] = st.rstd;
-    }
-    if (y == nullptr) continue;
-    if constexpr (kLean) {
-      load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
-      load_vector<E, H::V, kWide>(in.b, 0.0f, t, threads, dim, b);
-    }
-    const F2 rstd = pack2(st.rstd, st.rstd);
-    const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
+  if (column(kQuads - 1) >= dim) {  // what no row fills
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) d[i] = fma2(fma2(d[i], rstd, shift), w[i], b[i]);
-    H::store(y + row_offset(now, in.len, ys), d, t, threads, dim);
+    for (int k = 0; k < kQuads; ++k)
+      if (column(k) >= dim) sh.q[0][k][threadIdx.x] = sh.q[1][k][threadIdx.x] = make_uint4(0, 0, 0, 0);
   }
+  fetch(r, 0);
+  fetch(r + step, 1);
+  if (y != nullptr) {
+    float* const w = reinterpret_cast<float*>(sh.w);
+    for (int i = threadIdx.x; i < columns; i += kNormThreads) {
+      const int t = i / 4 % threads, four = i / 4 / threads;  // four = quad V / 4 + part
+      const int c = (four / (V / 4) * threads + t) * V + four % (V / 4) * 4 + i % 4;
+      w[i] = in.w != nullptr && c < dim ? in.w[c] : 1.0f;
+      w[columns + i] = in.b != nullptr && c < dim ? in.b[c] : 0.0f;
+    }
+  }
+  __syncthreads();
+  const float share = 1.0f / (float)dim;
+  // (as many turns for all rows of a block: they may wait for one another)
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < in.rows;
+       r0 += step, r += step, turn ^= 1) {
+    if constexpr (kWide) copy_wait<1>();
+    Q q[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) q[k].q = sh.q[turn][k][threadIdx.x];
+    fetch(r + 2 * step, turn);
+    F2 s[2] = {0, 0}, s2[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i % 2] = add2(s[i % 2], q[k].pair(i));
+    float m[1] = {both(add2(s[0], s[1]))};
+    row_sum(m, team, buf[turn]);
+    const float mean = m[0] * share;
+    const F2 minus = pack2(-mean, -mean);
+    s[0] = s[1] = 0;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      F2 d[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] = add2(q[k].pair(i), minus);
+      clip(d, dim - column(k));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s[i % 2] = add2(s[i % 2], d[i]);
+        s2[i % 2] = fma2(d[i], d[i], s2[i % 2]);
+      }
+    }
+    float v[2] = {both(add2(s[0], s[1])), both(s2[0]) + both(s2[1])};
+    row_sum(v, team, buf[turn] + 1);
+    const Stats st = moments(mean, v, share, in.eps);
+    if (r < in.rows && stats != nullptr && team.t == 0) {
+      stats[3 * r] = st.mean;
+      stats[3 * r + 1] = st.rest;
+      stats[3 * r + 2] = st.rstd;
+    }
+    if (r < in.rows && y != nullptr) {
+      const F2 rstd = pack2(st.rstd, st.rstd);
+      const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
+      T* out = y + row_offset(r, in.len, ys);
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        const int c = column(k), have = dim - c;
+        F2 o[N];
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const int at = (k * (V / 4) + i / 2) * threads + team.t;
+          const float4 w = sh.w[at], b = sh.w[columns / 4 + at];
+          o[i] = fma2(fma2(add2(q[k].pair(i), minus), rstd, shift), pack2(w.x, w.y),
+                      pack2(b.x, b.y));
+          o[i + 1] = fma2(fma2(add2(q[k].pair(i + 1), minus), rstd, shift), pack2(w.z, w.w),
+                          pack2(b.z, b.w));
+        }
+        if (have > 0) Q::store(out + c, o, have);
+      }
+    }
+  }
+  if constexpr (kWide) copy_wait<0>();
 }
 
 // Rows that registers do not hold: a block a row, read again from L2.
@@ -309,7 +318,7 @@ __device__ Stats long_stats(const T* x, int64_t dim, float eps, float (*buf)[32]
   const float share = 1.0f / (float)dim;
   float s[1] = {0.0f};
   for (int64_t c = threadIdx.x; c < dim; c += kLongThreads) s[0] += to_f32(x[c]);
-  const Team team(kLongThreads, 0, 1, 1);
+  const Team team(kLongThreads);
   row_sum(s, team, buf);
   const float mean = s[0] * share;
   float v[2] = {0.0f, 0.0f};
@@ -342,104 +351,171 @@ layer_norm_long_kernel(NormIn<T> in, T* __restrict__ y, Rows2 ys, float* __restr
   }
 }
 
-// dx, and a block's part of the sums over rows, in registers: a block walks
-// rows `blocks` apart, the next one's elements in flight. part: [block][2][dim].
-template <class T, int kThreads, int E, bool kWide>
-__global__ void __launch_bounds__(kThreads)
+// Sums of two numbers over the threads of a row, with half of the exchanges: each
+// lane gives one number away and goes on with the other. The same pairs are
+// added as by butterflies. buf: two numbers a warp, not in use.
+__device__ __forceinline__ void row_sum2(float& p, float& q, const Team& team, float (*buf)[16]) {
+  const int lane = threadIdx.x % 32;
+  const bool up = lane & 16;
+  float c = up ? q : p;
+  c = __fadd_rn(c, __shfl_xor_sync(~0u, up ? p : q, 16));
+#pragma unroll
+  for (int s = 8; s > 0; s /= 2) c = __fadd_rn(c, __shfl_xor_sync(~0u, c, s));
+  if (team.warps > 1) {
+    if (lane % 16 == 0) buf[lane / 16][threadIdx.x / 32] = c;
+    __syncthreads();
+    c = buf[lane / 16][threadIdx.x / team.threads * team.warps + lane % 16 % team.warps];
+#pragma unroll
+    for (int s = 8; s > 0; s /= 2)
+      if (s < team.warps) c = __fadd_rn(c, __shfl_xor_sync(~0u, c, s));
+  }
+  p = __shfl_sync(~0u, c, 0);
+  q = __shfl_sync(~0u, c, 16);
+}
+
+// dx, and a block's part of the sums over rows, in registers. The next rows'
+// elements come by way of shared memory, each thread's own part of it, so that
+// no registers wait for them. part: [block][2][dim].
+template <int kThreads, int kQuads>
+struct Ahead {
+  static constexpr int kDepth = 4;
+  uint4 q[kDepth][2][kQuads][kThreads];  // turn, x or dy
+};
+template <class T, int kThreads, int kQuads, bool kWide>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? CR_NORM_BW : 1)
 layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, Rows2 ds,
                            const float* __restrict__ stats, T* __restrict__ dx, Rows2 os,
                            float* __restrict__ part) {
-  using H = Held<T, E, kWide>;
-  __shared__ float buf[2][5][32];
-  extern __shared__ float sums[];  // [2][dim], for several rows a block
+  using Q = Quad<T, kWide>;
+  using A = Ahead<kThreads, kQuads>;
+  constexpr int V = Q::V, N = V / 2, kDepth = A::kDepth;
+  __shared__ float buf[2][2][16];
+  extern __shared__ __align__(16) char shared[];  // Ahead (kWide); then sums [2][dim]
+  A& ahead = *reinterpret_cast<A*>(shared);
   const int dim = (int)in.dim;
-  const Team team(threads, dim, H::V, E / H::V);
-  const int t = team.t, groups = kThreads / threads, group = threadIdx.x / threads;
-  const int64_t step = (int64_t)gridDim.x * groups;
+  const Team team(threads);
+  const int groups = kThreads / threads, group = threadIdx.x / threads;
   const float share = 1.0f / (float)dim;
-  F2 w[E / 2], dw[E / 2], db[E / 2];
-  load_vector<E, H::V, kWide>(in.w, 1.0f, t, threads, dim, w);
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const auto column = [&](int k) { return (k * threads + team.t) * V; };
+  F2 w[kQuads][N], dw[kQuads][N], db[kQuads][N];
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) dw[i] = db[i] = 0;
-  H x, g;
-  Stats next = {0.0f, 0.0f, 0.0f};
-  const auto fetch = [&](int64_t r) {
-    const bool real = r < in.rows;
-    x.load(in.x + row_offset(real ? r : 0, in.len, in.xs), t, threads, real ? dim : 0);
-    g.load(dy + row_offset(real ? r : 0, in.len, ds), t, threads, real ? dim : 0);
-    if (stats != nullptr && real)
-      next = {__ldg(stats + 3 * r), __ldg(stats + 3 * r + 1), __ldg(stats + 3 * r + 2)};
-  };
-  int64_t r = (int64_t)blockIdx.x * groups + group;
-  fetch(r);
-  // (as many turns for all rows of a block: they wait for one another)
-  for (int64_t r0 = (int64_t)blockIdx.x * groups, turn = 0; r0 < in.rows; r0 += step, ++turn) {
-    float(*const b)[32] = buf[turn & 1];
-    F2 n[E / 2], q[E / 2];
-    Stats st = next;
-    if (stats == nullptr) {
-      st = row_stats(x, team, dim, share, in.eps, b, n);
-    } else {
-      const F2 minus = pack2(-st.mean, -st.mean);
+  for (int k = 0; k < kQuads; ++k) {
+    load_vector<V, kWide>(in.w, column(k), dim - column(k), 1.0f, w[k]);
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) n[i] = add2(x.pair(i), minus);
-    }
-    const F2 rstd = pack2(st.rstd, st.rstd);
-    const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
+    for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0;
+    if (kWide && column(k) >= dim) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) n[i] = fma2(n[i], rstd, shift);
-    clip<H>(n, team, dim);
-    F2 s1 = 0, s2 = 0;
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const F2 u = g.pair(i);
-      dw[i] = fma2(u, n[i], dw[i]);
-      db[i] = add2(db[i], u);
-      q[i] = mul2(u, w[i]);
-      s1 = fma2(u, w[i], s1);  // (a sum of q, which add2 is not for)
-      s2 = fma2(q[i], n[i], s2);
-    }
-    const int64_t now = r;
-    r += step;
-    fetch(r);
-    float v[2] = {both(s1), both(s2)};
-    row_sum(v, team, b + 3);
-    if (now < in.rows) {
-      const float a1 = v[0] * share * -st.rstd, a2 = v[1] * share * -st.rstd;
-      const F2 p1 = pack2(a1, a1), p2 = pack2(a2, a2);
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) q[i] = fma2(n[i], p2, fma2(q[i], rstd, p1));
-      H::store(dx + row_offset(now, in.len, os), q, t, threads, dim);
+      for (int i = 0; i < kDepth; ++i)
+        ahead.q[i][0][k][threadIdx.x] = ahead.q[i][1][k][threadIdx.x] = make_uint4(0, 0, 0, 0);
     }
   }
-  float dw1[E], db1[E];
+  const auto fetch = [&](int64_t r, int turn) {
+    if constexpr (kWide) {
+      if (r < in.rows) {
+        const T* px = in.x + row_offset(r, in.len, in.xs);
+        const T* pg = dy + row_offset(r, in.len, ds);
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    unpack2(dw[i], dw1[2 * i], dw1[2 * i + 1]);
-    unpack2(db[i], db1[2 * i], db1[2 * i + 1]);
-  }
-  float* const out = part + (int64_t)blockIdx.x * 2 * dim;
-  if (groups == 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = H::column(e, t, threads);
-      if (c < dim) out[c] = dw1[e], out[dim + c] = db1[e];
-    }
-    return;
-  }
-  for (int k = 0; k < groups; ++k) {  // group by group, in order
-    if (group == k) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = H::column(e, t, threads);
-        if (c < dim) {
-          sums[c] = k == 0 ? dw1[e] : sums[c] + dw1[e];
-          sums[dim + c] = k == 0 ? db1[e] : sums[dim + c] + db1[e];
+        for (int k = 0; k < kQuads; ++k) {
+          if (column(k) >= dim) continue;
+          copy16(&ahead.q[turn][0][k][threadIdx.x], px + column(k));
+          copy16(&ahead.q[turn][1][k][threadIdx.x], pg + column(k));
         }
       }
+      copy_commit();
     }
-    __syncthreads();
+  };
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  Stats next;
+  const auto look = [&](int64_t r) {
+    const float* p = stats + 3 * (r < in.rows ? r : 0);
+    next = {__ldg(p), __ldg(p + 1), __ldg(p + 2)};
+  };
+  look(r);
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) fetch(r + i * step, i);
+  // (as many turns for all rows of a block: they wait for one another)
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < in.rows;
+       r0 += step, r += step, turn = (turn + 1) % kDepth) {
+    const Stats st = next;
+    const bool real = r < in.rows;
+    look(r + step);
+    if constexpr (kWide) copy_wait<kDepth - 1>();
+    const F2 minus = pack2(-st.mean, -st.mean), rstd = pack2(st.rstd, st.rstd);
+    const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
+    F2 n[kQuads][N], q[kQuads][N], s1 = 0, s2 = 0;
+    if (kWide && !real) {  // the last turn's rows of a block that has fewer
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k)
+        ahead.q[turn][0][k][threadIdx.x] = ahead.q[turn][1][k][threadIdx.x] =
+            make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      Q x, g;
+      if constexpr (kWide) {
+        x.q = ahead.q[turn][0][k][threadIdx.x];
+        g.q = ahead.q[turn][1][k][threadIdx.x];
+      } else {
+        const int have = real ? dim - column(k) : 0;
+        x.load(in.x + row_offset(real ? r : 0, in.len, in.xs) + column(k), have);
+        g.load(dy + row_offset(real ? r : 0, in.len, ds) + column(k), have);
+      }
+      // (behind the row dy is zero, and what n is there reaches nothing)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const F2 u = g.pair(i);
+        n[k][i] = fma2(add2(x.pair(i), minus), rstd, shift);
+        dw[k][i] = fma2(u, n[k][i], dw[k][i]);
+        db[k][i] = add2(db[k][i], u);
+        q[k][i] = mul2(u, w[k][i]);
+        s1 = fma2(u, w[k][i], s1);  // (a sum of q, which add2 is not for)
+        s2 = fma2(q[k][i], n[k][i], s2);
+      }
+    }
+    fetch(r + kDepth * step, turn);
+    float v1 = both(s1), v2 = both(s2);
+    row_sum2(v1, v2, team, buf[turn % 2]);
+    if (real) {
+      const float a1 = v1 * share * -st.rstd, a2 = v2 * share * -st.rstd;
+      const F2 p1 = pack2(a1, a1), p2 = pack2(a2, a2);
+      T* out = dx + row_offset(r, in.len, os);
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        if (column(k) >= dim) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[k][i] = fma2(n[k][i], p2, fma2(q[k][i], rstd, p1));
+        Q::store(out + column(k), q[k], dim - column(k));
+      }
+    }
   }
+  if constexpr (kWide) copy_wait<0>();
+  float* const out = part + (int64_t)blockIdx.x * 2 * dim;
+  float* const sums = reinterpret_cast<float*>(shared);
+  for (int g = 0; g < groups; ++g) {  // group by group, in order
+    if (groups > 1) __syncthreads();
+    if (group != g) continue;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int c = column(k) + e;
+        if (c >= dim) continue;
+        float a[2], b[2];
+        unpack2(dw[k][e / 2], a[0], a[1]);
+        unpack2(db[k][e / 2], b[0], b[1]);
+        if (groups == 1) {
+          out[c] = a[e % 2];
+          out[dim + c] = b[e % 2];
+        } else {
+          sums[c] = g == 0 ? a[e % 2] : sums[c] + a[e % 2];
+          sums[dim + c] = g == 0 ? b[e % 2] : sums[dim + c] + b[e % 2];
+        }
+      }
+  }
+  if (groups == 1) return;
+  __syncthreads();
   for (int c = threadIdx.x; c < 2 * dim; c += kThreads) out[c] = sums[c];
 }
 
@@ -461,7 +537,7 @@ layer_norm_backward_long_kernel(NormIn<T> in, const T* __restrict__ dy, Rows2 ds
     s2 = fmaf(g, n, s2);
   }
   float v[2] = {s1, s2};
-  row_sum(v, Team(kLongThreads, 0, 1, 1), buf);
+  row_sum(v, Team(kLongThreads), buf);
   const float a1 = v[0] / (float)in.dim, a2 = v[1] / (float)in.dim;
   T* o = dx + row_offset(r, in.len, os);
   for (int64_t c = threadIdx.x; c < in.dim; c += kLongThreads) {
@@ -548,35 +624,46 @@ cr_status check_norm(const cr_layer_norm_args* a) {
   return CR_OK;
 }
 
-// How rows lie in threads: by their length alone, so that a row's bits are the
-// same among any others and in both directions.
+#ifndef CR_NORM_QUADS
+#define CR_NORM_QUADS 8
+#endif
+#ifndef CR_NORM_FIT
+#define CR_NORM_FIT 4
+#endif
+#ifndef CR_NORM_RES
+#define CR_NORM_RES(SH) (SH.block == 256 ? 3 : 1)
+#endif
+// How a row lies in threads: by its length and type alone, so that its bits are
+// the same among any others.
 struct NormShape {
-  int block;    // threads of a block
+  int quads;    // 16 bytes a lane
   int threads;  // of a row, 0: more than registers hold
-  int E;        // elements a thread
 };
-
-NormShape norm_shape(int64_t dim) {
-  NormShape sh = {256, 0, 8};
-  if (dim > 16384) return sh;
-  if (dim > 2048) sh.block = 512;
-  if (dim > 4096) sh.E = 16;
-  if (dim > 8192) sh.block = 1024;
-  sh.threads = 32;
-  while ((int64_t)sh.threads * sh.E < dim) sh.threads *= 2;
+NormShape norm_shape(int64_t dim, size_t es) {
+  const int64_t quads = ceil_div(dim, (int64_t)(16 / es));
+  NormShape sh = {2, 32};
+  while (sh.quads < CR_NORM_QUADS && (int64_t)sh.quads * 32 < quads) sh.quads *= 2;
+  while ((int64_t)sh.quads * sh.threads < quads) sh.threads *= 2;
+  if (sh.threads > kNormThreads) sh.threads = 0;
   return sh;
 }
 
-// Blocks of the backward call, which leave a part of the sums over rows each; 0:
-// rows whose gradient goes another way.
-#ifndef CR_NORM_BLOCKS
-#define CR_NORM_BLOCKS 456
-#endif
-int64_t norm_blocks(int64_t rows, int64_t dim) {
-  if (dim > 8192) return 0;
-  const NormShape sh = norm_shape(dim);
-  const int64_t most = sh.block == 256 ? CR_NORM_BLOCKS : sh.E == 8 ? 304 : 152;
-  return std::min<int64_t>(ceil_div(rows, sh.block / sh.threads), most);
+// The backward call's: a block's threads, those of a row, and blocks, which leave
+// a part of the sums over rows each.
+struct BackwardShape {
+  int block, quads, threads;
+  int64_t blocks;  // 0: rows too long for it
+};
+BackwardShape backward_shape(int64_t rows, int64_t dim, size_t es) {
+  const int64_t quads = ceil_div(dim, (int64_t)(16 / es));
+  BackwardShape sh = {256, 1, 32, 0};
+  if (quads > 1024) return sh;
+  if (quads > 256) sh.block = 512;
+  if (quads > 512) sh.quads = 2;
+  while ((int64_t)sh.quads * sh.threads < quads) sh.threads *= 2;
+  const int64_t most = 152 * CR_NORM_RES(sh);
+  sh.blocks = std::min<int64_t>(ceil_div(rows, sh.block / sh.threads), most);
+  return sh;
 }
 
 bool norm_wide(const cr_layer_norm_args* a) {
@@ -586,45 +673,56 @@ bool norm_wide(const cr_layer_norm_args* a) {
          ptr_aligned(a->weight, 16) && ptr_aligned(a->bias, 16);
 }
 
-// Runs EXPR with a block's threads B, a thread's elements E and the access W.
-#define CR_NORM_CASE(B_, E_, WIDE, ...)                                       \
-  {                                                                           \
-    constexpr int B = B_, E = E_;                                             \
-    if (WIDE) { constexpr bool W = true; __VA_ARGS__; }                       \
-    else { constexpr bool W = false; __VA_ARGS__; }                           \
-  }
-#define CR_NORM_SHAPE(SH, WIDE, ...)                                          \
-  if (SH.block == 1024) CR_NORM_CASE(1024, 16, WIDE, __VA_ARGS__)             \
-  else CR_NORM_BACKWARD_SHAPE(SH, WIDE, __VA_ARGS__)
-#define CR_NORM_BACKWARD_SHAPE(SH, WIDE, ...)                                 \
-  if (SH.E == 16) CR_NORM_CASE(512, 16, WIDE, __VA_ARGS__)                    \
-  else if (SH.block == 512) CR_NORM_CASE(512, 8, WIDE, __VA_ARGS__)           \
-  else CR_NORM_CASE(256, 8, WIDE, __VA_ARGS__)
+// Runs EXPR with the access W bound.
+#define CR_NORM_WIDE(WIDE, ...)                     \
+  if (WIDE) { constexpr bool W = true; __VA_ARGS__; } \
+  else { constexpr bool W = false; __VA_ARGS__; }
 
-#ifndef CR_NORM_RES
-#define CR_NORM_RES(B) (1024 / (B))
-#endif
-void launch_norm(const cr_layer_norm_args* a, void* y, Rows2 ys, float* stats, bool wide,
+template <class T, int Q>
+bool launch_norm_quads(const NormIn<T>& in, int threads, T* y, Rows2 ys, float* stats, bool wide,
+                       cudaStream_t s) {
+  const size_t smem = sizeof(uint4) * 2 * Q * kNormThreads +
+                      (y != nullptr ? (size_t)8 * Q * threads * (16 / sizeof(T)) : 0);
+  const int64_t fit = std::min<int64_t>(CR_NORM_FIT, (int64_t)(224 * 1024 / (smem + 2048)));
+  const int64_t blocks = std::min(ceil_div(in.rows, kNormThreads / threads), 152 * fit);
+  bool done = false;
+  CR_NORM_WIDE(wide, CR_LAUNCH(kKLayerNorm, s,
+                               done = launch_clusters(layer_norm_kernel<T, Q, W>, blocks, 1,
+                                                      kNormThreads, smem, s, in, threads, y, ys,
+                                                      stats)))
+  return done;
+}
+
+bool launch_norm(const cr_layer_norm_args* a, void* y, Rows2 ys, float* stats, bool wide,
                  cudaStream_t s) {
-  const NormShape sh = norm_shape(a->dim);
-  const int64_t rows = a->batch * a->len;
+  const NormShape sh = norm_shape(a->dim, model_esize(a->dt));
   const Rows2 xs = {a->x_batch_stride, a->x_time_stride};
   const bool one = even(a->batch, a->len, xs) && even(a->batch, a->len, ys);
+  bool done = true;
   CR_MODEL_TYPE(a->dt, {
     T* out = static_cast<T*>(y);
-    if (sh.threads == 0) {
+    const NormIn<T> in = norm_in<T>(a, one);
+    if (sh.threads == 0)
       CR_LAUNCH(kKLayerNorm, s,
-                layer_norm_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(norm_in<T>(a, one), out,
-                                                                                  ys, stats));
-    } else {
-      CR_NORM_SHAPE(sh, wide, {
-        CR_LAUNCH(kKLayerNorm, s,
-                  layer_norm_kernel<T, B, E, W>
-                  <<<(unsigned)std::min<int64_t>(ceil_div(rows, B / sh.threads), 152 * CR_NORM_RES(B)), B,
-                     0, s>>>(norm_in<T>(a, one), sh.threads, out, ys, stats));
-      });
-    }
+                layer_norm_long_kernel<T><<<(unsigned)in.rows, kLongThreads, 0, s>>>(in, out, ys,
+                                                                                     stats));
+    else if (sh.quads == 2) done = launch_norm_quads<T, 2>(in, sh.threads, out, ys, stats, wide, s);
+    else if (sh.quads == 4) done = launch_norm_quads<T, 4>(in, sh.threads, out, ys, stats, wide, s);
+    else done = launch_norm_quads<T, 8>(in, sh.threads, out, ys, stats, wide, s);
   });
+  return done;
+}
+
+template <class T, int B, int Q, bool W>
+bool launch_norm_backward(const NormIn<T>& in, const BackwardShape& sh, const T* dy, Rows2 ds,
+                          const float* stats, T* dx, Rows2 os, float* part, cudaStream_t s) {
+  size_t smem = W ? sizeof(Ahead<B, Q>) : 0;
+  if (sh.threads < B) smem = std::max(smem, (size_t)in.dim * 8);
+  bool done = false;
+  CR_LAUNCH(kKLayerNormBackward, s,
+            done = launch_clusters(layer_norm_backward_kernel<T, B, Q, W>, sh.blocks, 1, B, smem, s,
+                                   in, sh.threads, dy, ds, stats, dx, os, part));
+  return done;
 }
 
 }  // namespace
@@ -647,18 +745,19 @@ cr_status cr_layer_norm(const cr_layer_norm_args* a, void* y, int64_t y_batch_st
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Rows2 ys = {y_batch_stride, y_time_stride};
   const bool wide = norm_wide(a) && rows_aligned(y, y_batch_stride, y_time_stride, es, 16);
-  launch_norm(a, y, ys, stats, wide, s);
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  const bool done = launch_norm(a, y, ys, stats, wide, s);
+  return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 size_t cr_layer_norm_backward_workspace_bytes(int64_t batch, int64_t len, int64_t dim) {
   using namespace cr;
   if (batch < 0 || len < 0 || dim < 0 || (len > 0 && batch > kMaxBlocks / len)) return 0;
   const int64_t rows = batch * len;
-  const int64_t blocks = norm_blocks(rows, dim);
-  const size_t parts = (size_t)(blocks != 0 ? blocks : ceil_div(rows, kSumRows));
-  return (blocks != 0 ? 0 : round256((size_t)rows * 12)) + round256(parts * dim * 8) +
-         kStatusBytes;
+  // (of the types' shapes the one with more parts)
+  const int64_t parts = std::max({backward_shape(rows, dim, 2).blocks,
+                                  backward_shape(rows, dim, 4).blocks,
+                                  dim > 4096 ? ceil_div(rows, kSumRows) : (int64_t)0});
+  return round256((size_t)rows * 12) + round256((size_t)parts * dim * 8) + kStatusBytes;
 }
 
 cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_norm_grads* g,
@@ -684,8 +783,7 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Rows2 ds = {g->dy_batch_stride, g->dy_time_stride};
   const Rows2 os = {g->dx_batch_stride, g->dx_time_stride};
-  const NormShape sh = norm_shape(a->dim);
-  const int64_t blocks = norm_blocks(rows, a->dim);
+  const BackwardShape sh = backward_shape(rows, a->dim, es);
   const bool wide = norm_wide(a) &&
                     rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, 16) &&
                     rows_aligned(g->dx, g->dx_batch_stride, g->dx_time_stride, es, 16);
@@ -693,42 +791,47 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
   if (sum_blocks > kMaxBlocks) return CR_ERR_UNSUPPORTED;
   char* at = past_status(ws);
   float* kept = reinterpret_cast<float*>(at);
-  if (blocks == 0) at += round256((size_t)rows * 12);
-  float* part = reinterpret_cast<float*>(at);
-  const int64_t parts = blocks != 0 ? blocks : ceil_div(rows, kSumRows);
+  float* part = reinterpret_cast<float*>(at + round256((size_t)rows * 12));
+  const int64_t parts = sh.blocks != 0 ? sh.blocks : ceil_div(rows, kSumRows);
+  const Rows2 xs = {a->x_batch_stride, a->x_time_stride};
   const float* stats = g->stats;
-  if (rows > 0 && blocks == 0 && stats == nullptr) {
-    launch_norm(a, nullptr, {a->x_batch_stride, a->x_time_stride}, kept, norm_wide(a), s);
+  bool done = true;
+  if (rows > 0 && stats == nullptr) {
+    done = launch_norm(a, nullptr, xs, kept, norm_wide(a), s);
     stats = kept;
   }
-  const Rows2 xs = {a->x_batch_stride, a->x_time_stride};
   const bool one = even(a->batch, a->len, xs) && even(a->batch, a->len, ds) &&
                    even(a->batch, a->len, os);
   CR_MODEL_TYPE(a->dt, {
     const T* dy = static_cast<const T*>(g->dy);
     T* dx = static_cast<T*>(g->dx);
-    if (rows > 0 && blocks == 0) {
+    const NormIn<T> in = norm_in<T>(a, one);
+    if (rows > 0 && sh.blocks == 0) {
       CR_LAUNCH(kKLayerNormBackward, s,
                 layer_norm_backward_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(
-                    norm_in<T>(a, one), dy, ds, stats, dx, os));
+                    in, dy, ds, stats, dx, os));
       CR_LAUNCH(kKLayerNormSum, s,
                 layer_norm_part_kernel<T>
                 <<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(parts, 65535)), 256, 0, s>>>(
-                    norm_in<T>(a, one), dy, ds, stats, part));
+                    in, dy, ds, stats, part));
     } else if (rows > 0) {
-      CR_NORM_BACKWARD_SHAPE(sh, wide, {
-        const size_t smem = sh.threads < B ? (size_t)a->dim * 8 : 0;
-        CR_LAUNCH(kKLayerNormBackward, s,
-                  layer_norm_backward_kernel<T, B, E, W><<<(unsigned)blocks, B, smem, s>>>(
-                      norm_in<T>(a, one), sh.threads, dy, ds, stats, dx, os, part));
-      });
+      if (sh.quads == 2) {
+        CR_NORM_WIDE(wide, done = done && (launch_norm_backward<T, 512, 2, W>(in, sh, dy, ds, stats, dx, os,
+                                                                     part, s)))
+      } else if (sh.block == 512) {
+        CR_NORM_WIDE(wide, done = done && (launch_norm_backward<T, 512, 1, W>(in, sh, dy, ds, stats, dx, os,
+                                                                     part, s)))
+      } else {
+        CR_NORM_WIDE(wide, done = done && (launch_norm_backward<T, 256, 1, W>(in, sh, dy, ds, stats, dx, os,
+                                                                     part, s)))
+      }
     }
     if (g->dweight != nullptr || g->dbias != nullptr)
       CR_LAUNCH(kKLayerNormSum, s,
                 layer_norm_sum_kernel<<<(unsigned)sum_blocks, 1024, 0, s>>>(part, parts, a->dim,
                                                                             g->dweight, g->dbias));
   });
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 }  // extern "C"
