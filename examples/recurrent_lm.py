@@ -1,6 +1,8 @@
 """A small recurrent language model on the library's model operators: tokens ->
 embedding -> (short causal convolution -> selective scan) -> logits, trained
-on a made-up sequence and then continued one token at a time.
+on a made-up sequence and then continued one token at a time. Beside it one
+with a norm in front of its layer and the gated recurrence in it, whose tokens
+are sampled.
 
     python examples/recurrent_lm.py
 
@@ -85,6 +87,61 @@ class RecurrentLM:
         return y @ p["out"]
 
 
+class GatedLM:
+    """tokens -> embedding -> norm -> gated scan, added to the embedding -> norm ->
+    logits. Parameters in float32, as are the activations here."""
+
+    def __init__(self, vocab, dim, seed=0, device="cuda"):
+        g = torch.Generator().manual_seed(seed)
+
+        def normal(*shape, std):
+            return (torch.randn(*shape, generator=g) * std).to(device)
+
+        self.vocab, self.dim, self.scale = vocab, dim, math.sqrt(dim)
+        steps = torch.exp(torch.rand(dim, generator=g) * math.log(50.0))
+        self.p = {
+            "table": normal(vocab, dim, std=1 / self.scale),
+            "norm_w": torch.ones(dim, device=device),
+            "norm_b": torch.zeros(dim, device=device),
+            "in": normal(dim, 3 * dim, std=1 / math.sqrt(dim)),
+            "gate_b": torch.log(steps).to(device),  # memories of 1 to 50 steps
+            "back": normal(dim, dim, std=1 / math.sqrt(dim)),
+            "last_w": torch.ones(dim, device=device),
+            "last_b": torch.zeros(dim, device=device),
+            "out": normal(dim, vocab, std=1 / math.sqrt(dim)),
+        }
+        for v in self.p.values():
+            v.requires_grad_(True)
+
+    def _inputs(self, x):
+        p = self.p
+        x, gate, z = (cr.layer_norm(x, p["norm_w"], p["norm_b"]) @ p["in"]).chunk(3, -1)
+        return x, gate + p["gate_b"], z
+
+    def _outputs(self, x, y):
+        p = self.p
+        return cr.layer_norm(x + y @ p["back"], p["last_w"], p["last_b"]) @ p["out"]
+
+    def logits(self, tokens):
+        """(batch, time) tokens to (batch, time, vocab) logits, with gradients."""
+        x = cr.embedding(tokens, self.p["table"], self.scale)
+        return self._outputs(x, cr.gated_scan(*self._inputs(x)))
+
+    @torch.no_grad()
+    def prompt(self, tokens, lengths=None):
+        """The logits of a prompt's positions and the state after it."""
+        x = cr.embedding(tokens, self.p["table"], self.scale)
+        y, state = cr.gated_scan(*self._inputs(x), lengths=lengths, return_state=True)
+        return self._outputs(x, y), state
+
+    @torch.no_grad()
+    def step(self, tokens, state):
+        """One token of each stream: (batch,) to (batch, vocab); updates state."""
+        x = cr.embedding(tokens, self.p["table"], self.scale)
+        u, gate, z = self._inputs(x)
+        return self._outputs(x, cr.gated_scan_step(u, gate, state, z))
+
+
 def sequence(batch, length, vocab, seed, device="cuda"):
     """Tokens that follow from the two before them."""
     g = torch.Generator().manual_seed(seed)
@@ -123,6 +180,16 @@ def generate(model, tokens, count):
     return torch.stack(out, 1)
 
 
+def sampled(model, tokens, u, **settings):
+    """Continues (batch, time) tokens by those that the uniform numbers u (count,
+    batch) pick, one step at a time."""
+    logits, state = model.prompt(tokens)
+    out = [cr.sample(logits[:, -1], u[0], **settings)]
+    for row in u[1:]:
+        out.append(cr.sample(model.step(out[-1], state), row, **settings))
+    return torch.stack(out, 1)
+
+
 def main():
     torch.backends.cuda.matmul.allow_tf32 = False
     model = RecurrentLM(vocab=31, dim=128)
@@ -132,6 +199,11 @@ def main():
     got = generate(model, t[:, :24], 16)
     right = (got == t[:, 24:]).float().mean().item()
     print("continued 4 sequences by 16 tokens: %.0f %% right" % (100 * right))
+    gated = GatedLM(vocab=31, dim=128)
+    more = train(gated, 150).tolist()
+    print("gated: loss %.3f at the start, %.3f at the end" % (more[0], more[-1]))
+    u = torch.rand(8, 4, generator=torch.Generator().manual_seed(7)).cuda()
+    print("sampled:", sampled(gated, t[:, :24], u, temperature=0.7, top_p=0.9).tolist())
     return losses, right
 
 

@@ -238,12 +238,23 @@ layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
   fetch(r, 0);
   fetch(r + step, 1);
   if (y != nullptr) {
-    float* const w = reinterpret_cast<float*>(sh.w);
-    for (int i = threadIdx.x; i < columns; i += kNormThreads) {
-      const int t = i / 4 % threads, four = i / 4 / threads;  // four = quad V / 4 + part
-      const int c = (four / (V / 4) * threads + t) * V + four % (V / 4) * 4 + i % 4;
-      w[i] = in.w != nullptr && c < dim ? in.w[c] : 1.0f;
-      w[columns + i] = in.b != nullptr && c < dim ? in.b[c] : 0.0f;
+    // (threads is a power of two; V / 4 accesses a quad)
+    constexpr int kParts = V / 4;
+    const int bits = 31 - __clz(threads);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < columns / 4; i += kNormThreads) {
+      const int t = i & (threads - 1), four = i >> bits;
+      const int c = (four / kParts * threads + t) * V + four % kParts * 4;
+      F2 w[2], b[2];
+      load_vector<4, kWide>(in.w, c, dim - c, 1.0f, w);
+      load_vector<4, kWide>(in.b, c, dim - c, 0.0f, b);
+      float4 f;
+      unpack2(w[0], f.x, f.y);
+      unpack2(w[1], f.z, f.w);
+      sh.w[i] = f;
+      unpack2(b[0], f.x, f.y);
+      unpack2(b[1], f.z, f.w);
+      sh.w[columns / 4 + i] = f;
     }
   }
   __syncthreads();
