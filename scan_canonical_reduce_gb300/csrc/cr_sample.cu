@@ -34,6 +34,8 @@ constexpr int kList = 1024;   // most tokens that are sorted
 constexpr int kRanked = 128;  // up to so many by their ranks
 constexpr int kFew = 512;     // top_k up to which its tokens alone are looked at
 constexpr int kMostBlocks = 8;
+constexpr int kMostSlice = 1 << 17;  // tokens of a block
+constexpr uint32_t kOverflow = 2 * kMostSlice;
 constexpr uint32_t kNone = 0xFFFFFFFFu;  // the key of what is no candidate
 static_assert(kBins % kThreads == 0 && kList % kThreads == 0 && kBins % 1024 == 0,
               "a thread's bins and tokens, a lane's words of chosen bins");
@@ -65,42 +67,53 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // Where a candidate that is not the largest lies: its bin, that of y rounded to
 // binary32 (which no order of two logits changes), and its weight in it, 2^(bin
 // / 16) w = 1 - z', as g = z' + 2^-18 in units of 2^-33: z' is -2^-19 to 0.0425.
-// Returns false where y is 63.9 or more (the far bin): such weights together
-// are below 2^-42 of the largest's. Straight code, whose results then mean
-// nothing.
+// Far is y of 63.9 or more (the far bin): such weights together are below 2^-42
+// of the largest's. Straight code, whose results then mean nothing.
 constexpr int kFar = kBins - 1;
+constexpr float kFarY = 63.9f;
 constexpr int kIndexDigits = 10;  // 2^20 indices in kBins
 constexpr uint32_t kShift = 1u << 15;
-__device__ __forceinline__ bool split(const Row& r, float l, int& bin, uint32_t& g) {
-  // the difference in two numbers, then y in two
-  const float s = r.top - l, bb = r.top - s, e = (r.top - (s + bb)) + (bb - l);
-  const float yh = s * r.ch;
-  const float yl = fmaf(e, r.ch, fmaf(s, r.cl, fmaf(s, r.ch, -yh)));
+// y in two numbers, of which the first is negative here, of two logits: the
+// difference in two numbers, times log2(e) / temperature in two.
+__device__ __forceinline__ void distance2(const Row& r, F2 l, F2& yh, F2& yl) {
+  const F2 top = pack2(r.top, r.top), ch = pack2(r.ch, r.ch), cl = pack2(r.cl, r.cl);
+  const F2 minus = pack2(-1.0f, -1.0f);
+  const F2 s = fma2(l, minus, top), bb = fma2(s, minus, top);
+  const F2 e = add2(fma2(add2(s, bb), minus, top), fma2(l, minus, bb));
+  yh = mul2(s, pack2(-r.ch, -r.ch));
+  yl = fma2(e, ch, fma2(s, cl, fma2(s, ch, yh)));
+}
+// The bin and the weight of minus y = yh - yl.
+__device__ __forceinline__ void split(float yh, float yl, int& bin, uint32_t& g) {
   // y = bin / 16 + x, x in units of 2^-34, from its two parts; adding 2^23
   // rounded down is a floor, adding 3 2^22 a rounding (of 2^16 at most)
-  const float t = __fmaf_rd(yh, 16.0f, 0x1p23f);
+  const float t = __fmaf_rd(yh, -16.0f, 0x1p23f);
   bin = (int)(__float_as_uint(t) & 0x7FFFFFu);
-  const float xh = fmaf(t - 0x1p23f, -0.0625f, yh);
+  const float xh = fmaf(t - 0x1p23f, -0.0625f, -yh);
   const int x = __float2int_rn(xh * 0x1p34f) +
                 (__float_as_int(fmaf(yl, 0x1p34f, 0x1.8p23f)) - 0x4B400000);
-  // 1 - 2^-x = 1 - exp(-z) = z - z^2 (1/2 - z (1/6 - z (1/24 - z (1/120 - z /
-  // 720)))), z = x ln 2; z^7 / 5040 < 2^-44 is left out. What follows z is below
-  // 2^-10, and binary32 holds it to 2^-34.
+  // 1 - 2^-x = 1 - exp(-z) = z - z^2 (1/2 - z (1/6 - z (1/24 - z / 120))), z = x
+  // ln 2; z^6 / 720 < 2^-36 is left out. What follows z is below 2^-10, and
+  // binary32 holds it to 2^-34.
   const int z = __mulhi(x, 0x58B90BFC);  // units of 2^-33
-  const float f = (float)z * -0x1p-33f;
-  const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.0f / 720.0f, 1.0f / 120.0f), 1.0f / 24.0f),
-                               1.0f / 6.0f), 0.5f);
-  const float tail = fmaf(f * f, q * 0x1p33f, 0x1p23f);
+  const float zf = (float)z, f = zf * -0x1p-33f;
+  const float q =
+      fmaf(f, fmaf(f, fmaf(f, 1.0f / 120.0f, 1.0f / 24.0f), 1.0f / 6.0f), 0.5f);
+  const float tail = fmaf(-f * zf, q, 0x1p23f);
   g = (uint32_t)z - __float_as_uint(tail) + (0x4B000000u + kShift);
-  return yh < 63.9f;
 }
 __device__ __forceinline__ int place(const Row& r, float l, uint32_t& g) {
-  int bin;
-  const bool near = split(r, l, bin, g);
-  if (l == r.top || !near) {
+  F2 h, w;
+  distance2(r, pack2(l, l), h, w);
+  float yh, yl, same;
+  unpack2(h, yh, same);
+  unpack2(w, yl, same);
+  if (l == r.top || !(yh > -kFarY)) {
     g = kShift;
     return l == r.top ? 0 : kFar;
   }
+  int bin;
+  split(yh, yl, bin, g);
   return bin;
 }
 // The weights of n tokens of a bin whose g sum up to g, in units of 2^-33.
@@ -117,7 +130,7 @@ __device__ __forceinline__ uint64_t mass_of(int bin, uint64_t sum) {
 
 // y in bins.
 __device__ __forceinline__ float in_bins(const Row& r, float l) {
-  return (r.top - l) * r.ch * 16.0f;
+  return (r.top - l) * (r.ch * 16.0f);
 }
 // Whether a logit's bin is this one (not the far one).
 __device__ __forceinline__ bool in_bin(const Row& r, float l, int bin) {
@@ -188,7 +201,7 @@ struct Message {
 struct Shared {
   union {
     struct {
-      uint32_t cnt[kBins], ghi[kBins], glo[kBins];  // this slice's histogram
+      uint32_t cnt[kBins], sum[kBins];  // this slice's histogram, of add()
     };
     struct {
       uint32_t kept[kBins];  // (a histogram of numbers is still read when the list is begun)
@@ -219,7 +232,7 @@ constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
 
 template <class T>
 struct Sampler {
-  static constexpr int E = 16 / sizeof(T);  // elements of an access
+  static constexpr int E = 16 / sizeof(T);  // elements of an access to memory
   const SampleIn<T>& in;
   const int rank, blocks;
   const T* x;        // this slice
@@ -251,55 +264,60 @@ struct Sampler {
     return blocks > 1 ? cg::this_cluster().map_shared_rank(p, block) : p;
   }
 
-  __device__ __forceinline__ void unpack(uint4 q, float (&v)[E]) const {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < E; ++k) {
-      if constexpr (sizeof(T) == 4) v[k] = __uint_as_float(w[k]);
-      else if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        v[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
-      else
-        v[k] = __half2float(__ushort_as_half((unsigned short)(w[k / 2] >> (k % 2 * 16))));
-    }
-  }
-
   // f(logits, index of the first) of every element of the slice, kBatch at a
-  // time, kThreads apart; NaN stands for what is behind the end. (Straight code
-  // on several elements side by side hides its latencies: with one after the
-  // other, a block's sixteen warps issued one instruction a clock.)
+  // time; NaN stands for what is behind the end. (Straight code on several
+  // elements side by side hides its latencies: with one after the other, a
+  // block's sixteen warps issued one instruction a clock.)
   static constexpr int kBatch = 4;
+  struct Batch {
+    uint32_t w[kBatch * sizeof(T) / 4];
+    __device__ __forceinline__ void unpack(float (&v)[kBatch]) const {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) v[k] = element(w, k);
+    }
+  };
+  using Words = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
+  static __device__ __forceinline__ float element(const uint32_t* w, int k) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+    else
+      return __half2float(__ushort_as_half((unsigned short)(w[k / 2] >> (k % 2 * 16))));
+  }
+  // Elements i to i + kBatch of p, aligned on their bytes.
+  static __device__ __forceinline__ Batch aligned(const T* p, int i) {
+    return __builtin_bit_cast(Batch, *reinterpret_cast<const Words*>(p + i));
+  }
+  // The same of any p, NaN from `end` on.
+  static __device__ __forceinline__ Batch guarded(const T* p, int i, int end, bool wide) {
+    if (wide && i + kBatch <= end) return aligned(p, i);
+    T v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v[k] = i + k < end ? p[i + k] : from_f32<T>(NAN);
+    Batch b;
+    memcpy(&b, v, sizeof(b));
+    return b;
+  }
   template <class F>
   __device__ __forceinline__ void each(F f) const {
     const T* const from = x;  // (copies: what f writes might be these, for the compiler)
     const int end = n, first = start;
+    const bool on16 = wide;
+    constexpr int step = kBatch * kThreads;
+    float l[kBatch];
     if (held) {
 #pragma unroll 1
-      for (int i0 = threadIdx.x; i0 < end; i0 += kBatch * kThreads) {
-        float l[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int i = i0 + k * kThreads;
-          l[k] = i < end ? to_f32(copy()[i]) : NAN;
-        }
-        f(l, first + i0);
+      for (int i = threadIdx.x * kBatch; i < end; i += step) {
+        aligned(copy(), i).unpack(l);
+        f(l, first + i);
       }
     } else {  // the next ones are read while f works on these
-      T next[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = threadIdx.x + k * kThreads;
-        next[k] = i < end ? from[i] : from_f32<T>(NAN);
-      }
+      Batch next = guarded(from, threadIdx.x * kBatch, end, on16);
 #pragma unroll 1
-      for (int i0 = threadIdx.x; i0 < end; i0 += kBatch * kThreads) {
-        float l[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          l[k] = to_f32(next[k]);
-          const int i = i0 + (kBatch + k) * kThreads;
-          next[k] = i < end ? from[i] : from_f32<T>(NAN);
-        }
-        f(l, first + i0);
+      for (int i = threadIdx.x * kBatch; i < end; i += step) {
+        next.unpack(l);
+        next = guarded(from, i + step, end, on16);
+        f(l, first + i);
       }
     }
   }
@@ -312,10 +330,9 @@ struct Sampler {
     for (int i = threadIdx.x * E; i < whole; i += kThreads * E) {
       const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + i));
       if (held) *reinterpret_cast<uint4*>(copy() + i) = q;
-      float v[E];
-      unpack(q, v);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int k = 0; k < E; ++k) top = fmaxf(top, v[k]);
+      for (int k = 0; k < E; ++k) top = fmaxf(top, element(w, k));
     }
 #pragma unroll 4
     for (int i = whole + threadIdx.x; i < n; i += kThreads) {
@@ -323,6 +340,8 @@ struct Sampler {
       if (held) copy()[i] = v;
       top = fmaxf(top, to_f32(v));
     }
+    if (held && threadIdx.x < kBatch && n + threadIdx.x < (n + kBatch - 1) / kBatch * kBatch)
+      copy()[n + threadIdx.x] = from_f32<T>(NAN);
     return top;
   }
 
@@ -362,7 +381,7 @@ struct Sampler {
   // Leaves the running sums (in a bin's own units, but for kPlace). clean: the
   // bins are empty.
   __device__ __forceinline__ void clear() const {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.ghi[i] = sh.glo[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.sum[i] = 0;
   }
   __device__ __noinline__ void histogram(Digit digit, const Message& m, int shift,
                                          bool clean = false) const {
@@ -373,10 +392,12 @@ struct Sampler {
     __syncthreads();
     uint32_t tops = 0, fars = 0;
     const Row row = r;
-    const auto add = [](int d, uint32_t g) {
-      atomicAdd(&sh.cnt[d], 1u);
-      atomicAdd(&sh.ghi[d], g >> 14);
-      atomicAdd(&sh.glo[d], g & 0x3FFFu);
+    // A bin's sum of g, below 2^46 in a slice, has its low 32 bits in sum; cnt
+    // counts its overflows above the number of tokens. (Two additions an element:
+    // with three 64 rows of 262,144 took 106 us for 102, with one of 64 bits 150.)
+    const auto add = [](int d, uint32_t g, uint32_t n) {
+      const uint32_t old = atomicAdd(&sh.sum[d], g);
+      atomicAdd(&sh.cnt[d], n + (old + g < old ? kOverflow : 0));
     };
     if (digit == kCount) {
       each([&, row](const float (&l)[kBatch], int) {
@@ -393,13 +414,19 @@ struct Sampler {
       each([&, row](const float (&l)[kBatch], int) {
         uint32_t g[kBatch];
         int d[kBatch];
-        bool in[kBatch];
+        float yh[kBatch], yl[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          in[k] = split(row, l[k], d[k], g[k]) && l[k] != row.top;
+        for (int k = 0; k < kBatch; k += 2) {
+          F2 h, w;
+          distance2(row, pack2(l[k], l[k + 1]), h, w);
+          unpack2(h, yh[k], yh[k + 1]);
+          unpack2(w, yl[k], yl[k + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) split(yh[k], yl[k], d[k], g[k]);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          if (in[k]) add(d[k], g[k]);
+          if (yh[k] > -kFarY && l[k] != row.top) add(d[k], g[k], 1);
           else if (l[k] == row.top) ++tops;  // many may be alike there
           else fars += l[k] > -INFINITY;
         }
@@ -409,20 +436,20 @@ struct Sampler {
       const uint32_t lo = m.lo, hi = m.hi;
       each([&, row](const float (&l)[kBatch], int i) {
 #pragma unroll 1
-        for (int k = 0; k < kBatch; ++k, i += kThreads) {
+        for (int k = 0; k < kBatch; ++k, ++i) {
           if (!in_bin(row, l[k], bin)) continue;
           const uint32_t key = order_key(l[k]);
           if (key < lo || key > hi) continue;
           uint32_t g;
           place(row, l[k], g);
-          add(digit == kKey ? (int)((key - lo) >> shift) : i >> kIndexDigits, g);
+          add(digit == kKey ? (int)((key - lo) >> shift) : i >> kIndexDigits, g, 1);
         }
       });
     }
     fars = __reduce_add_sync(~0u, fars);
     tops = __reduce_add_sync(~0u, tops);
     if (threadIdx.x % 32 == 0) {
-      if (tops) add(0, tops * kShift), atomicAdd(&sh.cnt[0], tops - 1);
+      if (tops) add(0, tops * kShift, tops);
       if (fars) atomicAdd(&sh.cnt[kFar], fars);
     }
     sync();
@@ -443,16 +470,18 @@ struct Sampler {
     // each block adds up a part of the bins, and tells the others
     const int share = kBins / blocks;
     for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
-      uint32_t c[kMostBlocks], hi[kMostBlocks], lo[kMostBlocks], n = 0;
+      uint32_t c[kMostBlocks], lo[kMostBlocks], n = 0;
       uint64_t g = 0;
 #pragma unroll
       for (int b = 0; b < kMostBlocks; ++b) {
         c[b] = b < blocks ? at(sh.cnt, b)[i] : 0;
-        hi[b] = b < blocks ? at(sh.ghi, b)[i] : 0;
-        lo[b] = b < blocks ? at(sh.glo, b)[i] : 0;
+        lo[b] = b < blocks ? at(sh.sum, b)[i] : 0;
       }
 #pragma unroll
-      for (int b = 0; b < kMostBlocks; ++b) n += c[b], g += ((uint64_t)hi[b] << 14) + lo[b];
+      for (int b = 0; b < kMostBlocks; ++b) {
+        n += c[b] % kOverflow;
+        g += ((uint64_t)(c[b] / kOverflow) << 32) + lo[b];
+      }
       uint64_t w = weights(n, g);
       if (digit == kPlace) w = i == kFar ? 0 : mass_of(i, w);
       for (int b = 0; b < blocks; ++b) {
@@ -692,7 +721,7 @@ struct Sampler {
     const uint32_t lo = m.lo, hi = m.hi;
     each([=](const float (&l)[kBatch], int i) {
 #pragma unroll 1
-      for (int j = 0; j < kBatch; ++j, i += kThreads) {
+      for (int j = 0; j < kBatch; ++j, ++i) {
         if (one ? i >> kIndexDigits != bin : !in_bin(row, l[j], bin)) continue;
         const uint32_t k = order_key(l[j]);
         if (k < lo || k > hi) continue;
@@ -717,7 +746,7 @@ struct Sampler {
       each([=](const float (&l)[kBatch], int i) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-          if (in_bins(row, l[k]) < limit || l[k] == row.top) add(l[k], i + k * kThreads);
+          if (in_bins(row, l[k]) < limit || l[k] == row.top) add(l[k], i + k);
       });
     } else {
       const float low = (float)from, high = (float)(to + 1);
@@ -735,7 +764,7 @@ struct Sampler {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int b = l[k] == row.top ? 0 : (int)in_bins(row, l[k]);
-          if (may[k] && (sh.chosen[b / 32] >> b % 32 & 1)) add(l[k], i + k * kThreads);
+          if (may[k] && (sh.chosen[b / 32] >> b % 32 & 1)) add(l[k], i + k);
         }
       });
     }
@@ -1031,7 +1060,7 @@ __device__ int64_t Sampler<T>::run(int64_t row) {
     each([&](const float (&l)[kBatch], int i) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (l[k] == r.top) first = min(first, (uint64_t)(i + k * kThreads));
+        if (l[k] == r.top) first = min(first, (uint64_t)(i + k));
     });
     return (int64_t)extreme<true>(first, 1);
   }
@@ -1160,18 +1189,23 @@ sample_kernel(SampleIn<T> in, int64_t* __restrict__ tokens, int blocks, int slic
   if (rank == 0 && threadIdx.x == 0) tokens[row] = token;
 }
 
-// Blocks a row: as many as the GPU runs at a time, or nearly twice that (two an
-// SM; more would only wait, and each costs its waits for the others), while a
-// slice keeps 4096 tokens. Measured, blocks 1 / 2 / 4 / 8: one row of 65,536 29 /
-// 21 / 18 / 16 us, 200 rows 113 / 94 / 101 / 129, 64 rows of 262,144 237 / 141 /
-// 114 / 105, 37 of 10,007 22 / 21 / 23 / 26. At least so many that a slice's
-// histogram stays within 32 bits.
-constexpr int64_t kMostSlice = 1 << 17;
+// Blocks a row: up to one an SM where a slice then keeps 2048 tokens, up to two
+// where it keeps 8192, up to 512 blocks, of which the last wait for others to end,
+// where it keeps 32,768. (Each step of a row costs a wait for all of its blocks,
+// and two blocks of an SM are in each other's way.) At least so many that a
+// slice's histogram stays within its 32 bits. Measured, us for blocks 1 / 2 / 4 / 8:
+// of 65,536 tokens 1 row 55 / 39 / 31 / 24, 48 rows 56 / 41 / 39 / 50, 76 rows 57 /
+// 44 / 57 / 70, 128 rows 60 / 58 / 74 / 100, 256 rows 90 / 107 / 131 / 189; of 10,007
+// 36 rows 21 / 21 / 19 / 23, 100 rows 21 / 25 / 38 / 57; of 262,144 16 rows - / 130 /
+// 62 / 72, 100 rows - / 195 / 174 / 170, 200 rows - / 281 / 265 / 320.
 int sample_blocks(int64_t rows, int64_t vocab) {
+  const auto worth = [&](int64_t c) {
+    return rows * c <= 152 ? vocab >= c * 2048
+                           : (rows * c <= 304 && vocab >= c * 8192) ||
+                                 (rows * c <= 512 && vocab >= c * 32768);
+  };
   int c = 1;
-  while (c < kMostBlocks && ((rows * c * 2 <= 512 && vocab >= (int64_t)c * 2 * 4096) ||
-                             vocab > (int64_t)c * kMostSlice))
-    c *= 2;
+  while (c < kMostBlocks && (worth(2 * c) || vocab > (int64_t)c * kMostSlice)) c *= 2;
   return c;
 }
 
