@@ -17,9 +17,6 @@
 namespace cr {
 namespace {
 
-#ifndef CR_NORM_BW
-#define CR_NORM_BW 3
-#endif
 struct Rows2 {
   int64_t bs, ts;
 };
@@ -362,146 +359,163 @@ layer_norm_long_kernel(NormIn<T> in, T* __restrict__ y, Rows2 ys, float* __restr
   }
 }
 
-// Sums of two numbers over the threads of a row, with half of the exchanges: each
-// lane gives one number away and goes on with the other. The same pairs are
-// added as by butterflies. buf: two numbers a warp, not in use.
-__device__ __forceinline__ void row_sum2(float& p, float& q, const Team& team, float (*buf)[16]) {
-  const int lane = threadIdx.x % 32;
-  const bool up = lane & 16;
+// The sums of p and of q over a warp, each in half of the lanes.
+__device__ __forceinline__ float warp_sum2(float p, float q) {
+  const bool up = threadIdx.x % 32 & 16;
   float c = up ? q : p;
   c = __fadd_rn(c, __shfl_xor_sync(~0u, up ? p : q, 16));
 #pragma unroll
   for (int s = 8; s > 0; s /= 2) c = __fadd_rn(c, __shfl_xor_sync(~0u, c, s));
-  if (team.warps > 1) {
-    if (lane % 16 == 0) buf[lane / 16][threadIdx.x / 32] = c;
-    __syncthreads();
-    c = buf[lane / 16][threadIdx.x / team.threads * team.warps + lane % 16 % team.warps];
-#pragma unroll
-    for (int s = 8; s > 0; s /= 2)
-      if (s < team.warps) c = __fadd_rn(c, __shfl_xor_sync(~0u, c, s));
-  }
-  p = __shfl_sync(~0u, c, 0);
-  q = __shfl_sync(~0u, c, 16);
+  return c;
 }
 
-// dx, and a block's part of the sums over rows, in registers. The next rows'
-// elements come by way of shared memory, each thread's own part of it, so that
-// no registers wait for them. part: [block][2][dim].
-template <int kThreads, int kQuads>
-struct Ahead {
-  static constexpr int kDepth = 4;
-  uint4 q[kDepth][2][kQuads][kThreads];  // turn, x or dy
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+
+// dx, and a block's part of the sums over rows, in registers. A turn is a few
+// rows, held in shared memory, where the next turn's rows are on their way. A
+// warp first takes a row, or a part of one, for its two sums; then a thread takes
+// its columns of the rows. So what a row costs besides its elements is shared by
+// many, and the block waits twice a turn, not for each row. (With all of a block's
+// threads on one row, four rows ahead, the gradient of 16,384 x 2048 in bf16 took
+// 60 us, its sums included; this takes 52, 57 % of the copy rate. Three blocks an SM
+// for two: 54; four turns held for two: 53 to 56.) part: [block][2][dim].
+template <int kThreads, int kRows>
+struct Turn {
+  static constexpr int kWarps = kThreads / 32 / kRows;  // of a row
+  float sums[kRows][2][kWarps];
+  float stats[2][kRows][3];  // turn
 };
-template <class T, int kThreads, int kQuads, bool kWide>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? CR_NORM_BW : 1)
+template <class T, int kThreads, int kQuads, int kRows, bool kWide>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
 layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, Rows2 ds,
                            const float* __restrict__ stats, T* __restrict__ dx, Rows2 os,
                            float* __restrict__ part) {
   using Q = Quad<T, kWide>;
-  using A = Ahead<kThreads, kQuads>;
-  constexpr int V = Q::V, N = V / 2, kDepth = A::kDepth;
-  __shared__ float buf[2][2][16];
-  extern __shared__ __align__(16) char shared[];  // Ahead (kWide); then sums [2][dim]
-  A& ahead = *reinterpret_cast<A*>(shared);
-  const int dim = (int)in.dim;
-  const Team team(threads);
-  const int groups = kThreads / threads, group = threadIdx.x / threads;
+  constexpr int V = Q::V, N = V / 2, W = Turn<kThreads, kRows>::kWarps;
+  __shared__ Turn<kThreads, kRows> sh;
+  // uint4 [turn][row][x or dy][quad], float4 [V / 4][quad] of weights; at the end
+  // sums [2][dim]
+  extern __shared__ __align__(16) char shared[];
+  const int dim = (int)in.dim, quads = (dim + V - 1) / V;
+  uint4* const held = reinterpret_cast<uint4*>(shared);
+  float4* const weights = reinterpret_cast<float4*>(held + 4 * kRows * quads);
+  const int group = threadIdx.x / threads, groups = kThreads / threads;
+  const int t = threadIdx.x % threads, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const float share = 1.0f / (float)dim;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  const auto column = [&](int k) { return (k * threads + team.t) * V; };
+  const auto place = [&](int turn, int row, int which, int q) {
+    return held + (((turn * kRows + row) * 2 + which) * quads + q);
+  };
   F2 w[kQuads][N], dw[kQuads][N], db[kQuads][N];
 #pragma unroll
   for (int k = 0; k < kQuads; ++k) {
-    load_vector<V, kWide>(in.w, column(k), dim - column(k), 1.0f, w[k]);
+    const int q = k * threads + t;
+    load_vector<V, kWide>(in.w, q * V, dim - q * V, 1.0f, w[k]);
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0;
-    if (kWide && column(k) >= dim) {
+    if (group != 0 || q >= quads) continue;
 #pragma unroll
-      for (int i = 0; i < kDepth; ++i)
-        ahead.q[i][0][k][threadIdx.x] = ahead.q[i][1][k][threadIdx.x] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < N; i += 2) {
+      float4 v;
+      unpack2(w[k][i], v.x, v.y);
+      unpack2(w[k][i + 1], v.z, v.w);
+      weights[i / 2 * quads + q] = v;
     }
   }
-  const auto fetch = [&](int64_t r, int turn) {
-    if constexpr (kWide) {
-      if (r < in.rows) {
-        const T* px = in.x + row_offset(r, in.len, in.xs);
-        const T* pg = dy + row_offset(r, in.len, ds);
-#pragma unroll
-        for (int k = 0; k < kQuads; ++k) {
-          if (column(k) >= dim) continue;
-          copy16(&ahead.q[turn][0][k][threadIdx.x], px + column(k));
-          copy16(&ahead.q[turn][1][k][threadIdx.x], pg + column(k));
-        }
-      }
-      copy_commit();
-    }
-  };
-  int64_t r = (int64_t)blockIdx.x * groups + group;
-  Stats next;
-  const auto look = [&](int64_t r) {
-    const float* p = stats + 3 * (r < in.rows ? r : 0);
-    next = {__ldg(p), __ldg(p + 1), __ldg(p + 2)};
-  };
-  look(r);
-#pragma unroll
-  for (int i = 0; i < kDepth; ++i) fetch(r + i * step, i);
-  // (as many turns for all rows of a block: they wait for one another)
-  int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < in.rows;
-       r0 += step, r += step, turn = (turn + 1) % kDepth) {
-    const Stats st = next;
-    const bool real = r < in.rows;
-    look(r + step);
-    if constexpr (kWide) copy_wait<kDepth - 1>();
-    const F2 minus = pack2(-st.mean, -st.mean), rstd = pack2(st.rstd, st.rstd);
-    const F2 shift = pack2(-st.rest * st.rstd, -st.rest * st.rstd);
-    F2 n[kQuads][N], q[kQuads][N], s1 = 0, s2 = 0;
-    if (kWide && !real) {  // the last turn's rows of a block that has fewer
-#pragma unroll
-      for (int k = 0; k < kQuads; ++k)
-        ahead.q[turn][0][k][threadIdx.x] = ahead.q[turn][1][k][threadIdx.x] =
-            make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-      Q x, g;
-      if constexpr (kWide) {
-        x.q = ahead.q[turn][0][k][threadIdx.x];
-        g.q = ahead.q[turn][1][k][threadIdx.x];
-      } else {
-        const int have = real ? dim - column(k) : 0;
-        x.load(in.x + row_offset(real ? r : 0, in.len, in.xs) + column(k), have);
-        g.load(dy + row_offset(real ? r : 0, in.len, ds) + column(k), have);
-      }
-      // (behind the row dy is zero, and what n is there reaches nothing)
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const F2 u = g.pair(i);
-        n[k][i] = fma2(add2(x.pair(i), minus), rstd, shift);
-        dw[k][i] = fma2(u, n[k][i], dw[k][i]);
-        db[k][i] = add2(db[k][i], u);
-        q[k][i] = mul2(u, w[k][i]);
-        s1 = fma2(u, w[k][i], s1);  // (a sum of q, which add2 is not for)
-        s2 = fma2(q[k][i], n[k][i], s2);
-      }
-    }
-    fetch(r + kDepth * step, turn);
-    float v1 = both(s1), v2 = both(s2);
-    row_sum2(v1, v2, team, buf[turn % 2]);
-    if (real) {
-      const float a1 = v1 * share * -st.rstd, a2 = v2 * share * -st.rstd;
-      const F2 p1 = pack2(a1, a1), p2 = pack2(a2, a2);
-      T* out = dx + row_offset(r, in.len, os);
+  const auto fetch = [&](int64_t r0, int turn) {
+    for (int i = group; i < kRows && r0 + i < in.rows; i += groups) {
+      const T* px = in.x + row_offset(r0 + i, in.len, in.xs);
+      const T* pg = dy + row_offset(r0 + i, in.len, ds);
 #pragma unroll
       for (int k = 0; k < kQuads; ++k) {
-        if (column(k) >= dim) continue;
+        const int q = k * threads + t;
+        if (q >= quads) continue;
+        if constexpr (kWide) {
+          copy16(place(turn, i, 0, q), px + q * V);
+          copy16(place(turn, i, 1, q), pg + q * V);
+        } else {
+          Q x, g;
+          x.load(px + q * V, dim - q * V);
+          g.load(pg + q * V, dim - q * V);
+          *place(turn, i, 0, q) = x.q;
+          *place(turn, i, 1, q) = g.q;
+        }
+      }
+    }
+    if (threadIdx.x < 3 * kRows && r0 + threadIdx.x / 3 < in.rows)
+      copy4(&sh.stats[turn][0][0] + threadIdx.x, stats + 3 * r0 + threadIdx.x);
+    copy_commit();
+  };
+  int64_t r0 = (int64_t)blockIdx.x * kRows;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  fetch(r0, 0);
+  for (int turn = 0; r0 < in.rows; r0 += step, turn ^= 1) {
+    copy_wait<0>();
+    __syncthreads();  // (and all have done with the turn before)
+    fetch(r0 + step, turn ^ 1);
+    const int many = (int)min((int64_t)kRows, in.rows - r0);
+    if (const int i = warp / W; i < many) {
+      const float* st = sh.stats[turn][i];
+      const F2 minus = pack2(-st[0], -st[0]), rstd = pack2(st[2], st[2]);
+      const F2 shift = pack2(-st[1] * st[2], -st[1] * st[2]);
+      F2 s1 = 0, s2 = 0;
+#pragma unroll 2
+      for (int q = warp % W * 32 + lane; q < quads; q += W * 32) {
+        Q x, g;
+        x.q = *place(turn, i, 0, q);
+        g.q = *place(turn, i, 1, q);
+        // (behind the row dy is zero, and what n is there reaches nothing)
 #pragma unroll
-        for (int i = 0; i < N; ++i) q[k][i] = fma2(n[k][i], p2, fma2(q[k][i], rstd, p1));
-        Q::store(out + column(k), q[k], dim - column(k));
+        for (int j = 0; j < N; j += 2) {
+          const float4 v = weights[j / 2 * quads + q];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const F2 u = g.pair(j + e), c = e == 0 ? pack2(v.x, v.y) : pack2(v.z, v.w);
+            const F2 n = fma2(add2(x.pair(j + e), minus), rstd, shift);
+            s1 = fma2(u, c, s1);
+            s2 = fma2(mul2(u, c), n, s2);
+          }
+        }
+      }
+      const float c = warp_sum2(both(s1), both(s2));
+      if (lane % 16 == 0) sh.sums[i][lane / 16][warp % W] = c;
+    }
+    __syncthreads();
+    for (int i = group; i < many; i += groups) {
+      const float* st = sh.stats[turn][i];
+      const F2 minus = pack2(-st[0], -st[0]), rstd = pack2(st[2], st[2]);
+      const F2 shift = pack2(-st[1] * st[2], -st[1] * st[2]);
+      float v1 = sh.sums[i][0][0], v2 = sh.sums[i][1][0];
+#pragma unroll
+      for (int k = 1; k < W; ++k) v1 += sh.sums[i][0][k], v2 += sh.sums[i][1][k];
+      const float a1 = v1 * share * -st[2], a2 = v2 * share * -st[2];
+      const F2 p1 = pack2(a1, a1), p2 = pack2(a2, a2);
+      T* out = dx + row_offset(r0 + i, in.len, os);
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        const int q = k * threads + t;
+        if (q >= quads) continue;
+        Q x, g;
+        x.q = *place(turn, i, 0, q);
+        g.q = *place(turn, i, 1, q);
+        F2 o[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const F2 u = g.pair(j);
+          const F2 n = fma2(add2(x.pair(j), minus), rstd, shift);
+          dw[k][j] = fma2(u, n, dw[k][j]);
+          db[k][j] = add2(db[k][j], u);
+          o[j] = fma2(n, p2, fma2(mul2(u, w[k][j]), rstd, p1));
+        }
+        Q::store(out + q * V, o, dim - q * V);
       }
     }
   }
-  if constexpr (kWide) copy_wait<0>();
+  copy_wait<0>();
   float* const out = part + (int64_t)blockIdx.x * 2 * dim;
   float* const sums = reinterpret_cast<float*>(shared);
   for (int g = 0; g < groups; ++g) {  // group by group, in order
@@ -511,7 +525,7 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
     for (int k = 0; k < kQuads; ++k)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const int c = column(k) + e;
+        const int c = (k * threads + t) * V + e;
         if (c >= dim) continue;
         float a[2], b[2];
         unpack2(dw[k][e / 2], a[0], a[1]);
@@ -635,17 +649,10 @@ cr_status check_norm(const cr_layer_norm_args* a) {
   return CR_OK;
 }
 
-#ifndef CR_NORM_QUADS
-#define CR_NORM_QUADS 8
-#endif
-#ifndef CR_NORM_FIT
-#define CR_NORM_FIT 4
-#endif
-#ifndef CR_NORM_RES
-#define CR_NORM_RES(SH) (SH.block == 256 ? 3 : 1)
-#endif
 // How a row lies in threads: by its length and type alone, so that its bits are
-// the same among any others.
+// the same among any others. (8 quads a lane before a second warp: with 4 rows of
+// 4096 in bf16 took 94 us for 87, rows of 1024 in fp32 23 for 22.)
+constexpr int kMostQuads = 8;
 struct NormShape {
   int quads;    // 16 bytes a lane
   int threads;  // of a row, 0: more than registers hold
@@ -653,27 +660,27 @@ struct NormShape {
 NormShape norm_shape(int64_t dim, size_t es) {
   const int64_t quads = ceil_div(dim, (int64_t)(16 / es));
   NormShape sh = {2, 32};
-  while (sh.quads < CR_NORM_QUADS && (int64_t)sh.quads * 32 < quads) sh.quads *= 2;
+  while (sh.quads < kMostQuads && (int64_t)sh.quads * 32 < quads) sh.quads *= 2;
   while ((int64_t)sh.quads * sh.threads < quads) sh.threads *= 2;
   if (sh.threads > kNormThreads) sh.threads = 0;
   return sh;
 }
 
-// The backward call's: a block's threads, those of a row, and blocks, which leave
-// a part of the sums over rows each.
+// The backward call's: a block's threads, those of a row's columns, the rows of a
+// turn, and blocks, which leave a part of the sums over rows each.
 struct BackwardShape {
-  int block, quads, threads;
+  int block, quads, threads, rows;
   int64_t blocks;  // 0: rows too long for it
 };
 BackwardShape backward_shape(int64_t rows, int64_t dim, size_t es) {
   const int64_t quads = ceil_div(dim, (int64_t)(16 / es));
-  BackwardShape sh = {256, 1, 32, 0};
+  BackwardShape sh = {256, 1, 32, 4, 0};
   if (quads > 1024) return sh;
   if (quads > 256) sh.block = 512;
-  if (quads > 512) sh.quads = 2;
+  if (quads > 512) sh.quads = 2, sh.rows = 2;
+  if (quads <= 32) sh.rows = 8;  // (a warp a row)
   while ((int64_t)sh.quads * sh.threads < quads) sh.threads *= 2;
-  const int64_t most = 152 * CR_NORM_RES(sh);
-  sh.blocks = std::min<int64_t>(ceil_div(rows, sh.block / sh.threads), most);
+  sh.blocks = std::min<int64_t>(ceil_div(rows, sh.rows), 152 * (sh.block == 256 ? 2 : 1));
   return sh;
 }
 
@@ -694,7 +701,11 @@ bool launch_norm_quads(const NormIn<T>& in, int threads, T* y, Rows2 ys, float* 
                        cudaStream_t s) {
   const size_t smem = sizeof(uint4) * 2 * Q * kNormThreads +
                       (y != nullptr ? (size_t)8 * Q * threads * (16 / sizeof(T)) : 0);
-  const int64_t fit = std::min<int64_t>(CR_NORM_FIT, (int64_t)(224 * 1024 / (smem + 2048)));
+  // blocks an SM: as many as registers hold (65,536 rows of 768 in bf16, 4 quads: 39
+  // us with 3, 45 with 4, 41 with 2; of 256, 2 quads: 23 with 3, 22 with 4, 23 with
+  // 6; 16,384 rows of 1024 in fp32, 8 quads: 22 with 2, 27 with 4)
+  constexpr int kFit = Q == 8 ? 2 : Q == 4 ? 3 : 4;
+  const int64_t fit = std::min<int64_t>(kFit, (int64_t)(224 * 1024 / (smem + 2048)));
   const int64_t blocks = std::min(ceil_div(in.rows, kNormThreads / threads), 152 * fit);
   bool done = false;
   CR_NORM_WIDE(wide, CR_LAUNCH(kKLayerNorm, s,
@@ -724,15 +735,17 @@ bool launch_norm(const cr_layer_norm_args* a, void* y, Rows2 ys, float* stats, b
   return done;
 }
 
-template <class T, int B, int Q, bool W>
+template <class T, int B, int Q, int R>
 bool launch_norm_backward(const NormIn<T>& in, const BackwardShape& sh, const T* dy, Rows2 ds,
-                          const float* stats, T* dx, Rows2 os, float* part, cudaStream_t s) {
-  size_t smem = W ? sizeof(Ahead<B, Q>) : 0;
-  if (sh.threads < B) smem = std::max(smem, (size_t)in.dim * 8);
+                          const float* stats, T* dx, Rows2 os, float* part, bool wide,
+                          cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const size_t smem = (size_t)ceil_div(in.dim, (int64_t)V) * 16 * (4 * R + V / 4);
   bool done = false;
-  CR_LAUNCH(kKLayerNormBackward, s,
-            done = launch_clusters(layer_norm_backward_kernel<T, B, Q, W>, sh.blocks, 1, B, smem, s,
-                                   in, sh.threads, dy, ds, stats, dx, os, part));
+  CR_NORM_WIDE(wide, CR_LAUNCH(kKLayerNormBackward, s,
+                               done = launch_clusters(layer_norm_backward_kernel<T, B, Q, R, W>,
+                                                      sh.blocks, 1, B, smem, s, in, sh.threads, dy,
+                                                      ds, stats, dx, os, part)))
   return done;
 }
 
@@ -826,16 +839,13 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
                 <<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(parts, 65535)), 256, 0, s>>>(
                     in, dy, ds, stats, part));
     } else if (rows > 0) {
-      if (sh.quads == 2) {
-        CR_NORM_WIDE(wide, done = done && (launch_norm_backward<T, 512, 2, W>(in, sh, dy, ds, stats, dx, os,
-                                                                     part, s)))
-      } else if (sh.block == 512) {
-        CR_NORM_WIDE(wide, done = done && (launch_norm_backward<T, 512, 1, W>(in, sh, dy, ds, stats, dx, os,
-                                                                     part, s)))
-      } else {
-        CR_NORM_WIDE(wide, done = done && (launch_norm_backward<T, 256, 1, W>(in, sh, dy, ds, stats, dx, os,
-                                                                     part, s)))
-      }
+      const auto run = [&](auto launch) {
+        return launch(in, sh, dy, ds, stats, dx, os, part, wide, s);
+      };
+      done = done && (sh.quads == 2     ? run(launch_norm_backward<T, 512, 2, 2>)
+                      : sh.block == 512 ? run(launch_norm_backward<T, 512, 1, 4>)
+                      : sh.rows == 4    ? run(launch_norm_backward<T, 256, 1, 4>)
+                                        : run(launch_norm_backward<T, 256, 1, 8>));
     }
     if (g->dweight != nullptr || g->dbias != nullptr)
       CR_LAUNCH(kKLayerNormSum, s,
