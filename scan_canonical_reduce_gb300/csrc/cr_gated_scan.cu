@@ -644,6 +644,9 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
   if (blocks > 1) cooperative_groups::this_cluster().sync();
 }
 
+// One token of each stream: a thread a channel, blocks of a stream side by side,
+// so that all the state's reads are in flight at once. (64 streams of 4096 in bf16
+// take 4.6 us, most of it the call's own; the bytes are 0.6.)
 template <class T>
 __global__ void __launch_bounds__(128)
 gated_scan_step_kernel(GateIn<T> in, float* __restrict__ state, int64_t rows, const void* slots,
@@ -679,7 +682,11 @@ GateIn<T> gate_in(const cr_gated_scan_args* a) {
 }
 
 // Blocks that share a sequence's time: as many as fit the GPU at once with those
-// of the other sequences and channels (two an SM).
+// of the other sequences and channels (two an SM). Each turn then waits for all of
+// them, which few sequences repay and many do not. Measured, bf16, us for 1 / 2 / 4
+// / 8 blocks: one sequence of 32,768 x 2048 481 / 300 / 156 / 134, 4 of 4096 x 4096
+// with their gradient 253 / 305 / 297 / 346, 9 ragged ones to 517 x 1000 in fp16 14
+// / 14 / 18 / 29.
 int gate_blocks(int64_t groups, int64_t len) {
   const int64_t c = std::min(304 / groups, ceil_div(len, kTileSteps));
   return (int)std::max<int64_t>(1, std::min<int64_t>(c, kMostCluster));
