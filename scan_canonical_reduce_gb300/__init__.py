@@ -19,12 +19,14 @@ Their results are bit-identical to the named expression on any GPU and launch
 shape.
 
 Beside them stand the operators of a recurrent language model's token path
-(``model.py``): embedding lookup, short causal convolution, selective state
-space scan, with their gradients and single-token forms. Their sums have one
-order each, whatever the launch, so that repeated calls give the same bits;
-the lookup and its gradient are exact expressions as above, while decays,
-SiLU and softplus rest on the GPU's approximate exponential and reciprocal
-instructions, which no CPU evaluation repeats bit for bit.
+(``model.py``): embedding lookup, layer norm, short causal convolution,
+selective state space scan and gated scan, with their gradients and
+single-token forms, and sampling of the next token. Their sums have one order
+each, whatever the launch, so that repeated calls give the same bits; the
+lookup and its gradient are exact expressions as above and a sampled token is
+that of exact arithmetic, while decays, gates, SiLU and softplus rest on the
+GPU's approximate exponential and reciprocal instructions, which no CPU
+evaluation repeats bit for bit.
 """
 from __future__ import annotations
 

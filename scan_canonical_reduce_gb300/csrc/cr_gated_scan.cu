@@ -228,18 +228,6 @@ struct Word {
   }
 };
 
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(to)),
-               "l"(from)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A run of one tensor in shared memory, a warp's own: kRun rows of 128 bytes.
 struct Staged {
   uint32_t w[kRun][32];
@@ -765,8 +753,8 @@ cr_status cr_gated_scan(const cr_gated_scan_args* a, void* y, int64_t y_batch_st
     const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
     auto kernel = CR_GATE_KERNEL(gated_scan_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScan, s,
-              done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s, gate_in<T>(a), out,
-                                     c));
+              done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s,
+                                     gate_in<T>(a), out, c));
   });
   return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
@@ -806,8 +794,8 @@ cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_sca
     const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
     auto kernel = CR_GATE_KERNEL(gated_scan_backward_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScanBackward, s,
-              done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s, gate_in<T>(a), dy,
-                                     g->dfinal, g->checkpoints,
+              done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s,
+                                     gate_in<T>(a), dy, g->dfinal, g->checkpoints,
                                      cr_gated_scan_checkpoints(a->len), out, c));
   });
   return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;

@@ -220,6 +220,29 @@ __device__ __forceinline__ float sigmoid(float v) {
   return reciprocal(1.0f + exp2_fast(v * -kLog2e));
 }
 
+// ------------------------------------------- copies into shared memory
+// 16 bytes, or 4, on their way while a thread goes on (both addresses aligned).
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits for all of a thread's groups but the last N.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------------- pairs of binary32
 // Two binary32 values in one 64-bit register pair, for the packed
 // arithmetic (one issue for two operations; fma and mul are rounded to nearest

@@ -171,18 +171,6 @@ __device__ __forceinline__ void clip(F2 (&d)[N], int have) {
   }
 }
 
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(to)),
-               "l"(from)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A row a warp, or several warps a row: a lane has kQuads times 16 bytes, so that
 // what a row costs besides its elements, sums over lanes above all, is shared by
 // many of them, and few rows wait at a barrier. Rows come by way of shared
@@ -230,7 +218,8 @@ layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
   if (column(kQuads - 1) >= dim) {  // what no row fills
 #pragma unroll
     for (int k = 0; k < kQuads; ++k)
-      if (column(k) >= dim) sh.q[0][k][threadIdx.x] = sh.q[1][k][threadIdx.x] = make_uint4(0, 0, 0, 0);
+      if (column(k) >= dim)
+        sh.q[0][k][threadIdx.x] = sh.q[1][k][threadIdx.x] = make_uint4(0, 0, 0, 0);
   }
   fetch(r, 0);
   fetch(r + step, 1);
@@ -367,13 +356,6 @@ __device__ __forceinline__ float warp_sum2(float p, float q) {
 #pragma unroll
   for (int s = 8; s > 0; s /= 2) c = __fadd_rn(c, __shfl_xor_sync(~0u, c, s));
   return c;
-}
-
-__device__ __forceinline__ void copy4(void* to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(to)),
-               "l"(from)
-               : "memory");
 }
 
 // dx, and a block's part of the sums over rows, in registers. A turn is a few

@@ -510,6 +510,6 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
 
 
 __all__ = ["layer_norm", "layer_norm_backward", "gated_scan", "gated_scan_backward",
-           "gated_scan_step", "sample", "embedding", "embedding_backward", "causal_conv", "causal_conv_backward",
-           "causal_conv_step", "selective_scan", "selective_scan_backward",
-           "selective_scan_step"]
+           "gated_scan_step", "sample", "embedding", "embedding_backward", "causal_conv",
+           "causal_conv_backward", "causal_conv_step", "selective_scan",
+           "selective_scan_backward", "selective_scan_step"]
