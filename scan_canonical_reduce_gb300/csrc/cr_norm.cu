@@ -28,6 +28,7 @@ struct NormIn {
   const T* x;
   Rows2 xs;
   const float *w, *b;
+  const T* end;  // of x
 };
 
 // (len 0: one batch, whose rows need no division)
@@ -92,28 +93,34 @@ __device__ __forceinline__ float both(F2 v) {
   return __fadd_rn(lo, hi);
 }
 
-// 16 bytes of neighbours: a whole access (kWide: rows on 16 bytes, a whole
-// number of accesses long) or, for the same bits, one by one (a warp's
-// neighbours are then in L1). have: elements inside the row.
-template <class T, bool kWide>
+// How rows move: where they lie on 16 bytes and are a whole number of those
+// long, by these (kWhole). Otherwise by the places of 16 bytes that they lie in
+// (kPlaces, Ragged), or, short ones, element by element (kElements): places cost a
+// row more, and its elements less. All give the same bits.
+enum Move { kElements, kPlaces, kWhole };
+
+// 16 bytes of neighbours.
+template <class T>
 struct Quad {
   static constexpr int V = 16 / sizeof(T);
   uint4 q;
+  // One by one (a warp's neighbours are then in L1); have: elements inside the row.
   __device__ __forceinline__ void load(const T* p, int have) {
-    q = make_uint4(0, 0, 0, 0);
-    if constexpr (kWide) {
-      if (have > 0) q = __ldcs(reinterpret_cast<const uint4*>(p));
-    } else {
-      uint32_t w[4] = {0, 0, 0, 0};
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i >= have) continue;
-        if constexpr (sizeof(T) == 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-        else
-          w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << i % 2 * 16;
-      }
-      q = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < V; ++i) {
+      if (i >= have) continue;
+      if constexpr (sizeof(T) == 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+      else
+        w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << i % 2 * 16;
     }
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ void store(T* p, const F2 (&v)[V / 2], int have) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    store_f32<T, V>(p, false, have, f);
   }
   __device__ __forceinline__ F2 pair(int i) const {
     if constexpr (sizeof(T) == 4) {
@@ -129,11 +136,96 @@ struct Quad {
       }
     }
   }
-  static __device__ __forceinline__ void store(T* p, const F2 (&v)[V / 2], int have) {
-    float f[V];
+  __device__ __forceinline__ static uint4 packed(const F2 (&v)[V / 2]) {
+    Pack<T, V> r;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
-    store_f32<T, V>(p, kWide && have > 0, have, f);
+    for (int i = 0; i < V / 2; ++i) {
+      float lo, hi;
+      unpack2(v[i], lo, hi);
+      r.v[2 * i] = from_f32<T>(lo);
+      r.v[2 * i + 1] = from_f32<T>(hi);
+    }
+    return __builtin_bit_cast(uint4, r);
+  }
+};
+
+// Rows that start anywhere or have no whole number of 16 bytes move by the 16-byte
+// places that they lie in, of which the first and the last may be shared with what
+// is beside the row. In shared memory a row lies in the same places, `shift`
+// elements off, and is put right by whoever reads it; a result is put in its
+// places as it is stored. (Loaded and stored element by element, eight a lane,
+// 16,384 rows of 2049 in bf16 took 110 us, their gradient 166; by words of 4 bytes
+// 98 and 193.)
+template <class T>
+struct Ragged {
+  static constexpr int V = 16 / sizeof(T), kHalves = 4 / sizeof(T);
+  using Elements = Pack<T, V>;
+  static __device__ __forceinline__ int shift(const T* p) {
+    return (int)((uintptr_t)p % 16) / (int)sizeof(T);
+  }
+  // The row of dim elements at p into `to` (one place more than its own 16 bytes
+  // may take), by thread t of several. lo and hi: where the tensor begins and
+  // ends, beyond which nothing is read.
+  static __device__ __forceinline__ void fetch(uint4* to, const T* p, int dim, const T* lo,
+                                               const T* hi, int t, int threads) {
+    const int s = shift(p), n = (dim + s + V - 1) / V;
+    const T* const a = p - s;
+    const bool inside = a >= lo && a + n * V <= hi;
+#pragma unroll 2
+    for (int q = t; q < n; q += threads) {
+      const int e = q * V;
+      if (inside || (a + e >= lo && a + e + V <= hi)) {
+        copy16(to + q, a + e);
+      } else {
+        Elements v;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          v.v[i] = e + i >= s && e + i - s < dim ? p[e + i - s] : from_f32<T>(0.0f);
+        to[q] = __builtin_bit_cast(uint4, v);
+      }
+    }
+  }
+  // The 16 bytes that begin s elements into a.
+  static __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int s) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int words = s / kHalves;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = words & 2 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = words & 1 ? w[i + 1] : w[i];
+    if constexpr (kHalves == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], s % 2 * 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // Elements q V to q V + V of a row in shared memory; zeros from `have` of them on.
+  static __device__ __forceinline__ uint4 quad(const uint4* row, int q, int s, int have) {
+    if (have <= 0) return make_uint4(0, 0, 0, 0);
+    const uint4 r = s == 0 ? row[q] : shifted(row[q], row[q + 1], s);
+    if (have >= V) return r;
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int left = have - i * kHalves;
+      w[i] = left <= 0 ? 0u : left < kHalves ? w[i] & 0xFFFFu : w[i];
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // A row that lies unshifted in shared memory (and a place behind it) to p, by
+  // thread t of at least 8: the elements before and after its whole places one by
+  // one.
+  static __device__ __forceinline__ void store(T* p, const uint4* row, int dim, int t,
+                                               int threads) {
+    const int head = min((V - shift(p)) % V, dim), full = (dim - head) / V;
+    const int done = head + full * V;
+    const T* const e = reinterpret_cast<const T*>(row);
+    if (t < head) p[t] = e[t];
+    if (t < dim - done) p[done + t] = e[done + t];
+    uint4* const to = reinterpret_cast<uint4*>(p + head);
+#pragma unroll 2
+    for (int q = t; q < full; q += threads)
+      to[q] = head == 0 ? row[q] : shifted(row[q], row[q + 1], head);
   }
 };
 // The same of weights, V floats on 16 bytes; `none` without them.
@@ -177,49 +269,64 @@ __device__ __forceinline__ void clip(F2 (&d)[N], int have) {
 // memory, each thread's own part of it, two rows ahead, and stay there as they
 // stand in memory; the weights stand beside them. y NULL: the statistics alone.
 constexpr int kNormThreads = 256;
-template <int kQuads>
-struct NormShared {
-  uint4 q[2][kQuads][kNormThreads];  // rows
-  // Weights and biases, four columns of a lane at a time, so that a warp's
-  // accesses are consecutive: [2][quad][V / 4][thread].
-  float4 w[1];
-};
-template <class T, int kQuads, bool kWide>
+// Bytes of the rows: [turn][row][quad], a place more a row with kPlaces.
+template <int kQuads, Move kMove>
+__host__ __device__ constexpr size_t norm_rows_bytes(int groups) {
+  return sizeof(uint4) * 2 * (kQuads * kNormThreads + (kMove == kPlaces ? groups : 0));
+}
+template <class T, int kQuads, Move kMove>
 __global__ void __launch_bounds__(kNormThreads)
 layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
                   float* __restrict__ stats) {
-  using Q = Quad<T, kWide>;
+  constexpr bool kWide = kMove == kWhole;
+  using Q = Quad<T>;
+  using R = Ragged<T>;
   constexpr int V = Q::V, N = V / 2;
   __shared__ float buf[2][3][32];
   extern __shared__ __align__(16) char shared[];
-  NormShared<kQuads>& sh = *reinterpret_cast<NormShared<kQuads>*>(shared);
   const int dim = (int)in.dim, columns = kQuads * threads * V;
   const Team team(threads);
   const int groups = kNormThreads / threads;
   const int64_t step = (int64_t)gridDim.x * groups;
+  const int group = threadIdx.x / threads, pitch = kQuads * threads + (kMove == kPlaces);
+  const auto row = [&](int turn) {
+    return reinterpret_cast<uint4*>(shared) + (turn * groups + group) * pitch;
+  };
+  // Weights and biases, four columns of a lane at a time, so that a warp's
+  // accesses are consecutive: [2][quad][V / 4][thread].
+  float4* const weights =
+      reinterpret_cast<float4*>(shared + norm_rows_bytes<kQuads, kMove>(groups));
   const auto column = [&](int k) { return (k * threads + team.t) * V; };
   const auto fetch = [&](int64_t r, int turn) {
     if (r < in.rows) {
       const T* p = in.x + row_offset(r, in.len, in.xs);
+      if constexpr (kWide) {
 #pragma unroll
-      for (int k = 0; k < kQuads; ++k) {
-        if constexpr (kWide) {
-          if (column(k) < dim) copy16(&sh.q[turn][k][threadIdx.x], p + column(k));
-        } else {
+        for (int k = 0; k < kQuads; ++k)
+          if (column(k) < dim) copy16(row(turn) + k * threads + team.t, p + column(k));
+      } else if constexpr (kMove == kElements) {
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
           Q q;
           q.load(p + column(k), dim - column(k));
-          sh.q[turn][k][threadIdx.x] = q.q;
+          row(turn)[k * threads + team.t] = q.q;
         }
+      } else {
+        R::fetch(row(turn), p, dim, in.x, in.end, team.t, threads);
       }
     }
-    if constexpr (kWide) copy_commit();
+    copy_commit();
   };
-  int64_t r = (int64_t)blockIdx.x * groups + threadIdx.x / threads;
-  if (column(kQuads - 1) >= dim) {  // what no row fills
+  const auto wait_for_team = [&] {
+    if (team.warps == 1) __syncwarp();
+    else __syncthreads();
+  };
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  if (kMove != kPlaces && column(kQuads - 1) >= dim) {  // what no row fills
 #pragma unroll
     for (int k = 0; k < kQuads; ++k)
       if (column(k) >= dim)
-        sh.q[0][k][threadIdx.x] = sh.q[1][k][threadIdx.x] = make_uint4(0, 0, 0, 0);
+        row(0)[k * threads + team.t] = row(1)[k * threads + team.t] = make_uint4(0, 0, 0, 0);
   }
   fetch(r, 0);
   fetch(r + step, 1);
@@ -237,10 +344,10 @@ layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
       float4 f;
       unpack2(w[0], f.x, f.y);
       unpack2(w[1], f.z, f.w);
-      sh.w[i] = f;
+      weights[i] = f;
       unpack2(b[0], f.x, f.y);
       unpack2(b[1], f.z, f.w);
-      sh.w[columns / 4 + i] = f;
+      weights[columns / 4 + i] = f;
     }
   }
   __syncthreads();
@@ -249,11 +356,21 @@ layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < in.rows;
        r0 += step, r += step, turn ^= 1) {
-    if constexpr (kWide) copy_wait<1>();
+    copy_wait<1>();
     Q q[kQuads];
+    if constexpr (kMove != kPlaces) {
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) q[k].q = sh.q[turn][k][threadIdx.x];
-    fetch(r + 2 * step, turn);
+      for (int k = 0; k < kQuads; ++k) q[k].q = row(turn)[k * threads + team.t];
+      fetch(r + 2 * step, turn);
+    } else {
+      wait_for_team();
+      const int shift = R::shift(in.x + row_offset(r < in.rows ? r : 0, in.len, in.xs));
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k)
+        q[k].q = R::quad(row(turn), k * threads + team.t, shift,
+                         r < in.rows ? dim - column(k) : 0);
+      wait_for_team();  // (y takes the row's place)
+    }
     F2 s[2] = {0, 0}, s2[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < kQuads; ++k)
@@ -295,17 +412,32 @@ layer_norm_kernel(NormIn<T> in, int threads, T* __restrict__ y, Rows2 ys,
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
           const int at = (k * (V / 4) + i / 2) * threads + team.t;
-          const float4 w = sh.w[at], b = sh.w[columns / 4 + at];
+          const float4 w = weights[at], b = weights[columns / 4 + at];
           o[i] = fma2(fma2(add2(q[k].pair(i), minus), rstd, shift), pack2(w.x, w.y),
                       pack2(b.x, b.y));
           o[i + 1] = fma2(fma2(add2(q[k].pair(i + 1), minus), rstd, shift), pack2(w.z, w.w),
                           pack2(b.z, b.w));
         }
-        if (have > 0) Q::store(out + c, o, have);
+        if constexpr (kWide) {
+          if (have > 0) *reinterpret_cast<uint4*>(out + c) = Q::packed(o);
+        } else if constexpr (kMove == kElements) {
+          if (have > 0) Q::store(out + c, o, have);
+        } else {
+          row(turn)[k * threads + team.t] = Q::packed(o);
+        }
       }
     }
+    if constexpr (kMove == kPlaces) {
+      if (y != nullptr) {
+        wait_for_team();
+        if (r < in.rows)
+          R::store(y + row_offset(r, in.len, ys), row(turn), dim, team.t, threads);
+        wait_for_team();
+      }
+      fetch(r + 2 * step, turn);
+    }
   }
-  if constexpr (kWide) copy_wait<0>();
+  copy_wait<0>();
 }
 
 // Rows that registers do not hold: a block a row, read again from L2.
@@ -371,26 +503,31 @@ struct Turn {
   static constexpr int kWarps = kThreads / 32 / kRows;  // of a row
   float sums[kRows][2][kWarps];
   float stats[2][kRows][3];  // turn
+  int shift[2][kRows][2];    // of x and dy, with kPlaces
 };
-template <class T, int kThreads, int kQuads, int kRows, bool kWide>
+template <class T, int kThreads, int kQuads, int kRows, Move kMove>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
 layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, Rows2 ds,
-                           const float* __restrict__ stats, T* __restrict__ dx, Rows2 os,
-                           float* __restrict__ part) {
-  using Q = Quad<T, kWide>;
+                           const T* __restrict__ dy_end, const float* __restrict__ stats,
+                           T* __restrict__ dx, Rows2 os, float* __restrict__ part) {
+  constexpr bool kWide = kMove == kWhole;
+  using Q = Quad<T>;
+  using R = Ragged<T>;
   constexpr int V = Q::V, N = V / 2, W = Turn<kThreads, kRows>::kWarps;
   __shared__ Turn<kThreads, kRows> sh;
-  // uint4 [turn][row][x or dy][quad], float4 [V / 4][quad] of weights; at the end
-  // sums [2][dim]
+  // uint4 [turn][row][x or dy][quad], and dx [row][quad] with kPlaces, float4 [V /
+  // 4][quad] of weights; at the end sums [2][dim]. (With kPlaces a place more a row.)
   extern __shared__ __align__(16) char shared[];
   const int dim = (int)in.dim, quads = (dim + V - 1) / V;
   uint4* const held = reinterpret_cast<uint4*>(shared);
-  float4* const weights = reinterpret_cast<float4*>(held + 4 * kRows * quads);
+  const int pitch = quads + (kMove == kPlaces);
+  uint4* const results = held + 4 * kRows * pitch;
+  float4* const weights = reinterpret_cast<float4*>(results + (kMove == kPlaces ? kRows * pitch : 0));
   const int group = threadIdx.x / threads, groups = kThreads / threads;
   const int t = threadIdx.x % threads, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const float share = 1.0f / (float)dim;
   const auto place = [&](int turn, int row, int which, int q) {
-    return held + (((turn * kRows + row) * 2 + which) * quads + q);
+    return held + (((turn * kRows + row) * 2 + which) * pitch + q);
   };
   F2 w[kQuads][N], dw[kQuads][N], db[kQuads][N];
 #pragma unroll
@@ -409,17 +546,14 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
     }
   }
   const auto fetch = [&](int64_t r0, int turn) {
-    for (int i = group; i < kRows && r0 + i < in.rows; i += groups) {
-      const T* px = in.x + row_offset(r0 + i, in.len, in.xs);
-      const T* pg = dy + row_offset(r0 + i, in.len, ds);
+    if constexpr (kMove == kElements) {
+      for (int i = group; i < kRows && r0 + i < in.rows; i += groups) {
+        const T* px = in.x + row_offset(r0 + i, in.len, in.xs);
+        const T* pg = dy + row_offset(r0 + i, in.len, ds);
 #pragma unroll
-      for (int k = 0; k < kQuads; ++k) {
-        const int q = k * threads + t;
-        if (q >= quads) continue;
-        if constexpr (kWide) {
-          copy16(place(turn, i, 0, q), px + q * V);
-          copy16(place(turn, i, 1, q), pg + q * V);
-        } else {
+        for (int k = 0; k < kQuads; ++k) {
+          const int q = k * threads + t;
+          if (q >= quads) continue;
           Q x, g;
           x.load(px + q * V, dim - q * V);
           g.load(pg + q * V, dim - q * V);
@@ -428,9 +562,38 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
         }
       }
     }
+    // a warp a row of x or of dy, or several warps one
+    constexpr int kWarps = kThreads / 32, kShare = kWarps > 2 * kRows ? kWarps / (2 * kRows) : 1;
+    const int first = warp % kShare * 32 + lane;
+    for (int u = warp / kShare;
+         kMove != kElements && u < 2 * kRows && r0 + u / 2 < in.rows; u += kWarps / kShare) {
+      const int i = u / 2, which = u % 2;
+      const T* p = which ? dy + row_offset(r0 + i, in.len, ds)
+                         : in.x + row_offset(r0 + i, in.len, in.xs);
+      uint4* to = place(turn, i, which, 0);
+      if constexpr (kWide) {
+#pragma unroll 2
+        for (int q = first; q < quads; q += 32 * kShare) copy16(to + q, p + q * V);
+      } else {
+        if (first == 0) sh.shift[turn][i][which] = R::shift(p);
+        R::fetch(to, p, dim, which ? dy : in.x, which ? dy_end : in.end, first, 32 * kShare);
+      }
+    }
     if (threadIdx.x < 3 * kRows && r0 + threadIdx.x / 3 < in.rows)
       copy4(&sh.stats[turn][0][0] + threadIdx.x, stats + 3 * r0 + threadIdx.x);
     copy_commit();
+  };
+  const auto row_quad = [&](int turn, int row, int which, int q) {
+    Q r;
+    if constexpr (kMove != kPlaces) r.q = *place(turn, row, which, q);
+    else r.q = R::quad(place(turn, row, which, 0), q, sh.shift[turn][row][which], dim - q * V);
+    return r;
+  };
+  const auto flush = [&](int64_t r0) {  // dx of a turn, with kPlaces
+    const int i = warp / W;  // (as for its sums)
+    if (r0 + i < in.rows)
+      R::store(dx + row_offset(r0 + i, in.len, os), results + i * pitch, dim,
+               warp % W * 32 + lane, 32 * W);
   };
   int64_t r0 = (int64_t)blockIdx.x * kRows;
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -439,6 +602,7 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
     copy_wait<0>();
     __syncthreads();  // (and all have done with the turn before)
     fetch(r0 + step, turn ^ 1);
+    if (kMove == kPlaces && r0 >= step) flush(r0 - step);
     const int many = (int)min((int64_t)kRows, in.rows - r0);
     if (const int i = warp / W; i < many) {
       const float* st = sh.stats[turn][i];
@@ -447,9 +611,7 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
       F2 s1 = 0, s2 = 0;
 #pragma unroll 2
       for (int q = warp % W * 32 + lane; q < quads; q += W * 32) {
-        Q x, g;
-        x.q = *place(turn, i, 0, q);
-        g.q = *place(turn, i, 1, q);
+        const Q x = row_quad(turn, i, 0, q), g = row_quad(turn, i, 1, q);
         // (behind the row dy is zero, and what n is there reaches nothing)
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
@@ -481,9 +643,7 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
       for (int k = 0; k < kQuads; ++k) {
         const int q = k * threads + t;
         if (q >= quads) continue;
-        Q x, g;
-        x.q = *place(turn, i, 0, q);
-        g.q = *place(turn, i, 1, q);
+        const Q x = row_quad(turn, i, 0, q), g = row_quad(turn, i, 1, q);
         F2 o[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -493,11 +653,17 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
           db[k][j] = add2(db[k][j], u);
           o[j] = fma2(n, p2, fma2(mul2(u, w[k][j]), rstd, p1));
         }
-        Q::store(out + q * V, o, dim - q * V);
+        if constexpr (kWide) *reinterpret_cast<uint4*>(out + q * V) = Q::packed(o);
+        else if constexpr (kMove == kElements) Q::store(out + q * V, o, dim - q * V);
+        else results[i * pitch + q] = Q::packed(o);
       }
     }
   }
   copy_wait<0>();
+  if constexpr (kMove == kPlaces) {
+    __syncthreads();
+    flush(r0 - step);
+  }
   float* const out = part + (int64_t)blockIdx.x * 2 * dim;
   float* const sums = reinterpret_cast<float*>(shared);
   for (int g = 0; g < groups; ++g) {  // group by group, in order
@@ -608,10 +774,18 @@ layer_norm_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t dim
 // others' are then the time strides alone.)
 bool even(int64_t batch, int64_t len, Rows2 s) { return batch <= 1 || s.bs == len * s.ts; }
 
+// Where a tensor of rows ends.
+template <class T>
+const T* rows_end(const cr_layer_norm_args* a, const void* p, Rows2 s) {
+  if (a->batch == 0 || a->len == 0) return static_cast<const T*>(p);
+  return static_cast<const T*>(p) + (a->batch - 1) * s.bs + (a->len - 1) * s.ts + a->dim;
+}
+
 template <class T>
 NormIn<T> norm_in(const cr_layer_norm_args* a, bool one_batch) {
   return {a->batch * a->len, one_batch ? 0 : a->len, a->dim, a->eps, static_cast<const T*>(a->x),
-          {a->x_batch_stride, a->x_time_stride}, a->weight, a->bias};
+          {a->x_batch_stride, a->x_time_stride}, a->weight, a->bias,
+          rows_end<T>(a, a->x, {a->x_batch_stride, a->x_time_stride})};
 }
 
 bool rows_fit(const cr_layer_norm_args* a, int64_t bs, int64_t ts) {
@@ -673,15 +847,42 @@ bool norm_wide(const cr_layer_norm_args* a) {
          ptr_aligned(a->weight, 16) && ptr_aligned(a->bias, 16);
 }
 
-// Runs EXPR with the access W bound.
-#define CR_NORM_WIDE(WIDE, ...)                     \
-  if (WIDE) { constexpr bool W = true; __VA_ARGS__; } \
-  else { constexpr bool W = false; __VA_ARGS__; }
+// Short rows are of fewer quads than this. Measured, 2^24 elements, us with elements
+// / places, 16 bits forward: 30 quads 41 / 49, 45 39 / 41, 60 39 / 31, 120 50 / 33,
+// 400 59 / 31 (32 bits: 45 / 62 at 45, 37 / 39 at 200, so elements alone); gradient:
+// 65,536 rows of 333 (42 quads) 103 / 126, 16,384 of 2049 166 / 124, 32,768 of 777
+// in 32 bits (195) 131 / 118.
+constexpr int kShortQuads = 48;
+template <class T>
+Move norm_move(bool wide, int64_t dim, bool backward) {
+  if (wide) return kWhole;
+  return (backward || sizeof(T) == 2) && ceil_div(dim, (int64_t)(16 / sizeof(T))) >= kShortQuads
+             ? kPlaces
+             : kElements;
+}
+
+// Runs EXPR with the move M bound; PLACES, ELEMENTS: whether a call may have it.
+#define CR_NORM_MOVE(MOVE, PLACES, ELEMENTS, ...)          \
+  if ((MOVE) == kWhole) {                                  \
+    constexpr Move M = kWhole;                             \
+    __VA_ARGS__;                                           \
+  } else if ((MOVE) == kPlaces) {                          \
+    if constexpr (PLACES) {                                \
+      constexpr Move M = kPlaces;                          \
+      __VA_ARGS__;                                         \
+    }                                                      \
+  } else if constexpr (ELEMENTS) {                         \
+    constexpr Move M = kElements;                          \
+    __VA_ARGS__;                                           \
+  }
 
 template <class T, int Q>
 bool launch_norm_quads(const NormIn<T>& in, int threads, T* y, Rows2 ys, float* stats, bool wide,
                        cudaStream_t s) {
-  const size_t smem = sizeof(uint4) * 2 * Q * kNormThreads +
+  const int groups = kNormThreads / threads;
+  const Move move = norm_move<T>(wide, in.dim, false);
+  const size_t smem = (move == kPlaces ? norm_rows_bytes<Q, kPlaces>(groups)
+                                       : norm_rows_bytes<Q, kWhole>(groups)) +
                       (y != nullptr ? (size_t)8 * Q * threads * (16 / sizeof(T)) : 0);
   // blocks an SM: as many as registers hold (65,536 rows of 768 in bf16, 4 quads: 39
   // us with 3, 45 with 4, 41 with 2; of 256, 2 quads: 23 with 3, 22 with 4, 23 with
@@ -690,10 +891,12 @@ bool launch_norm_quads(const NormIn<T>& in, int threads, T* y, Rows2 ys, float* 
   const int64_t fit = std::min<int64_t>(kFit, (int64_t)(224 * 1024 / (smem + 2048)));
   const int64_t blocks = std::min(ceil_div(in.rows, kNormThreads / threads), 152 * fit);
   bool done = false;
-  CR_NORM_WIDE(wide, CR_LAUNCH(kKLayerNorm, s,
-                               done = launch_clusters(layer_norm_kernel<T, Q, W>, blocks, 1,
-                                                      kNormThreads, smem, s, in, threads, y, ys,
-                                                      stats)))
+  // (2 quads a lane: rows of up to 64 quads, others longer ones)
+  CR_NORM_MOVE(move, sizeof(T) == 2, sizeof(T) == 4 || Q == 2,
+               CR_LAUNCH(kKLayerNorm, s,
+                         done = launch_clusters(layer_norm_kernel<T, Q, M>, blocks, 1,
+                                                kNormThreads, smem, s, in, threads, y, ys,
+                                                stats)))
   return done;
 }
 
@@ -719,15 +922,19 @@ bool launch_norm(const cr_layer_norm_args* a, void* y, Rows2 ys, float* stats, b
 
 template <class T, int B, int Q, int R>
 bool launch_norm_backward(const NormIn<T>& in, const BackwardShape& sh, const T* dy, Rows2 ds,
-                          const float* stats, T* dx, Rows2 os, float* part, bool wide,
+                          const T* dy_end, const float* stats, T* dx, Rows2 os, float* part, bool wide,
                           cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const size_t smem = (size_t)ceil_div(in.dim, (int64_t)V) * 16 * (4 * R + V / 4);
+  const size_t quads = (size_t)ceil_div(in.dim, (int64_t)V);
+  const Move move = norm_move<T>(wide, in.dim, true);
+  const size_t smem = 16 * (move == kPlaces ? (quads + 1) * 5 * R : quads * 4 * R) + 4 * V * quads;
   bool done = false;
-  CR_NORM_WIDE(wide, CR_LAUNCH(kKLayerNormBackward, s,
-                               done = launch_clusters(layer_norm_backward_kernel<T, B, Q, R, W>,
-                                                      sh.blocks, 1, B, smem, s, in, sh.threads, dy,
-                                                      ds, stats, dx, os, part)))
+  // (8 rows a turn: rows of up to 32 quads; 512 threads: of more than 256)
+  CR_NORM_MOVE(move, R != 8, B == 256,
+               CR_LAUNCH(kKLayerNormBackward, s,
+                         done = launch_clusters(layer_norm_backward_kernel<T, B, Q, R, M>,
+                                                sh.blocks, 1, B, smem, s, in, sh.threads, dy, ds,
+                                                dy_end, stats, dx, os, part)))
   return done;
 }
 
@@ -822,7 +1029,7 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
                     in, dy, ds, stats, part));
     } else if (rows > 0) {
       const auto run = [&](auto launch) {
-        return launch(in, sh, dy, ds, stats, dx, os, part, wide, s);
+        return launch(in, sh, dy, ds, rows_end<T>(a, dy, ds), stats, dx, os, part, wide, s);
       };
       done = done && (sh.quads == 2     ? run(launch_norm_backward<T, 512, 2, 2>)
                       : sh.block == 512 ? run(launch_norm_backward<T, 512, 1, 4>)
