@@ -11,8 +11,6 @@
 #include <algorithm>
 #include <cstdint>
 
-#include <cstddef>
-
 #include <cooperative_groups.h>
 
 #include "cr_device.cuh"
@@ -28,6 +26,7 @@ template <class T>
 struct Strided {
   const T* p;
   int64_t bs, ts;
+  const T* end;
 };
 
 template <class T>
@@ -159,9 +158,10 @@ __device__ __forceinline__ Map<C> map_join(const Map<C>& a, const Map<C>& b) {
 
 // A tile: 8 warps, each a run of kRun steps, a lane 32 bits of each step: one
 // channel of binary32, two neighbours of 16 bits, which come by way of shared
-// memory, 16 bytes an access, a tile ahead of their use (kWide: rows on 16
-// bytes). Otherwise a lane reads its channels one by one, two of 16 bits 32
-// apart.
+// memory a tile ahead of their use: 16 bytes an access (kWide: rows on 16 bytes),
+// or 4. (4 x 4096 x 2047 in bf16, whose rows start anywhere, takes 179 us, its
+// gradient 334, where 2048 takes 61 and 104; read channel by channel it took 461
+// and 627.)
 constexpr int kRun = kGateCheckpoint;
 constexpr int kGateWarps = 8;
 constexpr int kTileSteps = kRun * kGateWarps;
@@ -175,16 +175,6 @@ struct Lane {
 template <class T, bool kWide>
 struct Word {
   static constexpr int C = Lane<T>::C;
-  static __device__ __forceinline__ uint32_t load(const T* p, int have) {
-    if constexpr (sizeof(T) == 4) {
-      return have > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
-    } else {
-      static_assert(!kWide, "by way of shared memory");
-      const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-      const uint32_t lo = have > 0 ? __ldg(q) : 0u, hi = have > 1 ? __ldg(q + 32) : 0u;
-      return lo | hi << 16;
-    }
-  }
   static __device__ __forceinline__ Vec<C> get(uint32_t w) {
     if constexpr (sizeof(T) == 4) return Vec<C>(__uint_as_float(w));
     else if constexpr (std::is_same<T, __nv_bfloat16>::value)
@@ -222,82 +212,133 @@ struct Word {
       if (have > 0) *reinterpret_cast<uint32_t*>(p) = w;
     } else {
       unsigned short* q = reinterpret_cast<unsigned short*>(p);
-      if (have > 0) q[0] = (unsigned short)w;
-      if (have > 1) q[32] = (unsigned short)(w >> 16);
-    }
-  }
-};
-
-// A run of one tensor in shared memory, a warp's own: kRun rows of 128 bytes.
-struct Staged {
-  uint32_t w[kRun][32];
-};
-
-// One input's runs: through shared memory (kWide), or straight into registers.
-// Steps past the end read as `past` (two channels of it).
-template <class T, bool kWide>
-struct Runs {
-  Staged* staged;
-  const T* p;  // this lane's first access (kWide), or its channel, of step 0
-  int64_t ts;
-  int have;
-  uint32_t past;
-  __device__ __forceinline__ Runs(const Strided<T>& s, int64_t b, int64_t group, int64_t d, int h,
-                                  int64_t dim, Staged* st, uint32_t past_ = 0u)
-      : staged(st), ts(s.ts), past(past_) {
-    const T* row = s.p + b * s.bs;
-    if constexpr (kWide) {
-      constexpr int E = 16 / sizeof(T);  // elements of an access, which divide dim
-      const int lane = threadIdx.x % 32;
-      const int64_t c = group * 32 * Lane<T>::C + lane % 8 * E;
-      have = c < dim;
-      p = row + (have ? c : 0) + lane / 8 * ts;
-    } else {
-      p = row + d;
-      have = h;
-    }
-  }
-  // begins to fetch steps t0 .. t0 + m
-  __device__ __forceinline__ void ask(int64_t t0, int m) const {
-    if constexpr (kWide) {
-      const int lane = threadIdx.x % 32;
-      const T* from = p + t0 * ts;
-      uint32_t* to = &staged->w[lane / 8][lane % 8 * 4];
-      if (m == kRun) {
-#pragma unroll
-        for (int j = 0; j < kRun / 4; ++j)
-          if (have) copy16(to + j * 128, from + j * 4 * ts);
+      if (have > 1 && (uintptr_t)p % 4 == 0) {
+        *reinterpret_cast<uint32_t*>(q) = w;
       } else {
-#pragma unroll
-        for (int j = 0; j < kRun / 4; ++j) {
-          if (j * 4 + lane / 8 >= m)
-            *reinterpret_cast<uint4*>(to + j * 128) = make_uint4(past, past, past, past);
-          else if (have)
-            copy16(to + j * 128, from + j * 4 * ts);
-        }
+        if (have > 0) q[0] = (unsigned short)w;
+        if (have > 1) q[1] = (unsigned short)(w >> 16);
       }
     }
   }
-  __device__ __forceinline__ uint32_t get(int64_t t0, int m, int i) const {
-    if constexpr (kWide) return staged->w[i][threadIdx.x % 32];
-    else return i < m ? Word<T, kWide>::load(p + (t0 + i) * ts, have) : past;
+};
+
+// A run of one tensor in shared memory, a warp's own: kRun rows of 128 bytes, or
+// of the words that these lie in.
+template <bool kWide>
+struct Staged {
+  uint32_t w[kRun][kWide ? 32 : 33];
+};
+
+// One input's runs, by way of shared memory. Steps past the end read as `past`
+// (two channels of it).
+template <class T, bool kWide>
+struct Runs {
+  static constexpr int E = 16 / sizeof(T);  // elements of an access, which divide dim
+  Staged<kWide>* staged;
+  const T* p;  // this lane's first access of step 0
+  int64_t ts;
+  bool have;
+  uint32_t past;
+  __device__ __forceinline__ Runs(const Strided<T>& s, int64_t b, int64_t group, int64_t dim,
+                                  Staged<kWide>* st, uint32_t past_ = 0u)
+      : staged(st), ts(s.ts), past(past_) {
+    const int lane = threadIdx.x % 32;
+    const int64_t c = group * 32 * Lane<T>::C + lane % 8 * E;
+    have = c < dim;
+    p = s.p + b * s.bs + (have ? c : 0) + lane / 8 * ts;
+  }
+  // begins to fetch steps t0 .. t0 + m
+  __device__ __forceinline__ void ask(int64_t t0, int m) const {
+    const int lane = threadIdx.x % 32;
+    const T* from = p + t0 * ts;
+    uint32_t* to = &staged->w[lane / 8][lane % 8 * 4];
+    if (m == kRun) {
+#pragma unroll
+      for (int j = 0; j < kRun / 4; ++j)
+        if (have) copy16(to + j * 128, from + j * 4 * ts);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRun / 4; ++j) {
+        if (j * 4 + lane / 8 >= m)
+          *reinterpret_cast<uint4*>(to + j * 128) = make_uint4(past, past, past, past);
+        else if (have)
+          copy16(to + j * 128, from + j * 4 * ts);
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t get(int i) const { return staged->w[i][threadIdx.x % 32]; }
+};
+
+// Rows that start anywhere: word w of a step, lane w's, holds its two elements of 16
+// bits, or, where the row starts in the upper half of a word, the second of the
+// lane before and its first. What is beside the row in its first and last word is
+// read where the tensor has it, and left out.
+template <class T>
+struct Runs<T, false> {
+  static constexpr int kHalves = Lane<T>::C;
+  const Strided<T>& s;
+  Staged<false>* staged;
+  const T* p;  // the group's first channel of step 0
+  int n;       // channels from there on, 65 where there are more
+  uint32_t past;
+  __device__ __forceinline__ Runs(const Strided<T>& s_, int64_t b, int64_t group, int64_t dim,
+                                  Staged<false>* st, uint32_t past_ = 0u)
+      : s(s_), staged(st), past(past_) {
+    const int64_t c = group * 32 * kHalves;
+    p = s.p + b * s.bs + c;
+    n = (int)min((int64_t)65, dim - c);
+  }
+  static __device__ __forceinline__ int shift(const T* q) {
+    return kHalves == 2 ? (int)((uintptr_t)q >> 1 & 1) : 0;
+  }
+  static __device__ __forceinline__ uint32_t bits(const T* q) {
+    return *reinterpret_cast<const unsigned short*>(q);
+  }
+  __device__ __forceinline__ void word(uint32_t* to, const T* q, int w) const {
+    const int e = w * kHalves - shift(q);
+    if (e >= n) return;
+    if (kHalves == 1 || (e >= 0 && e + 1 < n) || (q + e >= s.p && q + e + 2 <= s.end))
+      copy4(to, q + e);
+    else
+      *to = e < 0 ? bits(q) << 16 : bits(q + e);
+  }
+  __device__ __forceinline__ void ask(int64_t t0, int m) const {
+    const int lane = threadIdx.x % 32;
+    const T* const from = p + t0 * s.ts;
+#pragma unroll 4
+    for (int j = 0; j < kRun; ++j) {
+      uint32_t* to = &staged->w[j][lane];
+      if (j < m) word(to, from + j * s.ts, lane);
+      else *to = past;
+    }
+    if (kHalves == 2 && lane < kRun) {  // the words behind
+      uint32_t* to = &staged->w[lane][32];
+      const T* q = from + lane * s.ts;
+      if (lane >= m) *to = past;
+      else if (shift(q) != 0) word(to, q, 32);
+    }
+  }
+  __device__ __forceinline__ uint32_t get(int i) const {
+    const int lane = threadIdx.x % 32;
+    if constexpr (kHalves == 1) return staged->w[i][lane];
+    // (runs begin at even steps)
+    const int off = shift(p) ^ (int)(i & s.ts & 1);
+    return __funnelshift_r(staged->w[i][lane], staged->w[i][lane + 1], off * 16);
   }
 };
 
 // Which channels a lane has.
-template <class T, bool kWide>
+template <class T>
 struct Channels {
   static constexpr int C = Lane<T>::C;
-  static constexpr int kStep = kWide || C == 1 ? 1 : 32;
   int64_t d;
   int have;
   __device__ Channels(int64_t group, int64_t dim) {
-    const int lane = threadIdx.x % 32;
-    d = group * 32 * C + (kWide ? lane * C : lane);
-    have = d >= dim ? 0 : C == 1 || d + kStep >= dim ? 1 : 2;
+    d = (group * 32 + threadIdx.x % 32) * C;
+    have = (int)max((int64_t)0, min((int64_t)C, dim - d));
     if (have == 0) d = 0;
   }
-  __device__ __forceinline__ int64_t at(int k) const { return d + k * kStep; }
+  __device__ __forceinline__ int64_t at(int k) const { return d + k; }
 };
 
 // The maps of a tile's warps and of a cluster's tiles, for this turn and the
@@ -367,10 +408,10 @@ struct GateFwd {
   int64_t n_check;
 };
 
-template <int C>
+template <int C, bool kWide>
 struct ForwardShared {
   Joints<C> joints;
-  Staged staged[kGateWarps][3];  // kWide alone
+  Staged<kWide> staged[kGateWarps][3];
 };
 
 template <class T, bool kZ, bool kWide>
@@ -380,18 +421,18 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
   using W = Word<T, kWide>;
   using V = Vec<C>;
   extern __shared__ __align__(16) char shared[];
-  ForwardShared<C>& sh = *reinterpret_cast<ForwardShared<C>*>(shared);
+  ForwardShared<C, kWide>& sh = *reinterpret_cast<ForwardShared<C, kWide>*>(shared);
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
   int64_t group;
   const int64_t b = divide(blockIdx.x / (unsigned)blocks, per, group);
-  const Channels<T, kWide> ch(group, in.dim);
+  const Channels<T> ch(group, in.dim);
   const int64_t n = sequence_length(in.lengths, in.index_bytes, b, in.len);
-  Staged* st = kWide ? sh.staged[warp] : nullptr;
-  const Runs<T, kWide> rg(in.gate, b, group, ch.d, ch.have, in.dim, st, W::kHeld);
-  const Runs<T, kWide> rx(in.x, b, group, ch.d, ch.have, in.dim, st + 1);
-  const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, ch.d, ch.have, in.dim, st + 2);
+  Staged<kWide>* st = sh.staged[warp];
+  const Runs<T, kWide> rg(in.gate, b, group, in.dim, st, W::kHeld);
+  const Runs<T, kWide> rx(in.x, b, group, in.dim, st + 1);
+  const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, in.dim, st + 2);
   float carry[C];  // -h
 #pragma unroll
   for (int k = 0; k < C; ++k)
@@ -411,9 +452,9 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
     copy_wait<1>();
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) g[i] = rg.get(t0, m, i);
+    for (int i = 0; i < kRun; ++i) g[i] = rg.get(i);
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) xw[i] = rx.get(t0, m, i);
+    for (int i = 0; i < kRun; ++i) xw[i] = rx.get(i);
     __syncwarp();
     const int64_t next = t0 + step;
     const int m_next = steps(next);
@@ -446,7 +487,7 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
     for (int i = 0; i < kRun; ++i) {
       s = fma(r[i], x[i], decay(r[i], s));
       if constexpr (kZ) {
-        const V z = W::get(rz.get(t0, m, i));
+        const V z = W::get(rz.get(i));
         y[i] = W::round(mul(mul(s, z), minus_sigmoid(z, -kLog2e)));
       } else {
         y[i] = W::round(mul(s, V(-1.0f)));
@@ -486,10 +527,10 @@ struct GateOut {
   float* dstate;
 };
 
-template <int C>
+template <int C, bool kWide>
 struct BackwardShared {
   Joints<C> joints;
-  Staged staged[kGateWarps][4];  // kWide alone
+  Staged<kWide> staged[kGateWarps][4];
 };
 
 template <class T, bool kZ, bool kWide>
@@ -501,19 +542,19 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
   using W = Word<T, kWide>;
   using V = Vec<C>;
   extern __shared__ __align__(16) char shared[];
-  BackwardShared<C>& sh = *reinterpret_cast<BackwardShared<C>*>(shared);
+  BackwardShared<C, kWide>& sh = *reinterpret_cast<BackwardShared<C, kWide>*>(shared);
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
   int64_t group;
   const int64_t b = divide(blockIdx.x / (unsigned)blocks, per, group);
-  const Channels<T, kWide> ch(group, in.dim);
+  const Channels<T> ch(group, in.dim);
   const int64_t n = sequence_length(in.lengths, in.index_bytes, b, in.len);
-  Staged* st = kWide ? sh.staged[warp] : nullptr;
-  const Runs<T, kWide> rg(in.gate, b, group, ch.d, ch.have, in.dim, st, W::kHeld);
-  const Runs<T, kWide> rx(in.x, b, group, ch.d, ch.have, in.dim, st + 1);
-  const Runs<T, kWide> re(dy, b, group, ch.d, ch.have, in.dim, st + 2);
-  const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, ch.d, ch.have, in.dim, st + 3);
+  Staged<kWide>* st = sh.staged[warp];
+  const Runs<T, kWide> rg(in.gate, b, group, in.dim, st, W::kHeld);
+  const Runs<T, kWide> rx(in.x, b, group, in.dim, st + 1);
+  const Runs<T, kWide> re(dy, b, group, in.dim, st + 2);
+  const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, in.dim, st + 3);
   float carry[C];  // -a[t+1] G[t+1]
 #pragma unroll
   for (int k = 0; k < C; ++k)
@@ -552,15 +593,15 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
     uint32_t dz[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const V x = W::get(rx.get(t0, m, i));
+      const V x = W::get(rx.get(i));
       V e;
-      r[i] = minus_sigmoid(W::get(W::bounded(rg.get(t0, m, i))), kLog2e, &e);
+      r[i] = minus_sigmoid(W::get(W::bounded(rg.get(i))), kLog2e, &e);
       // e r = a keeps its digits where r is near 1
       d[i] = mul(mul(add(s, x), r[i]), mul(e, r[i]));
       s = fma(r[i], x, decay(r[i], s));
-      v[i] = W::get(re.get(t0, m, i));
+      v[i] = W::get(re.get(i));
       if constexpr (kZ) {
-        const V z = W::get(rz.get(t0, m, i)), w = minus_sigmoid(z, -kLog2e);  // -sigmoid
+        const V z = W::get(rz.get(i)), w = minus_sigmoid(z, -kLog2e);  // -sigmoid
         const V silu = mul(z, w);                                            // -silu
         // minus the slope: w + silu (1 + w), silu' = sigmoid + silu (1 - sigmoid)
         const V slope = fma(silu, fma(w, V(1.0f), V(1.0f)), w);
@@ -661,11 +702,18 @@ gated_scan_step_kernel(GateIn<T> in, float* __restrict__ state, int64_t rows, co
 }
 
 template <class T>
+Strided<T> strided(const cr_gated_scan_args* a, const void* p, int64_t bs, int64_t ts) {
+  const T* q = static_cast<const T*>(p);
+  if (q == nullptr || a->batch == 0 || a->len == 0) return {q, bs, ts, q};
+  return {q, bs, ts, q + (a->batch - 1) * bs + (a->len - 1) * ts + a->dim};
+}
+
+template <class T>
 GateIn<T> gate_in(const cr_gated_scan_args* a) {
   return {a->batch, a->len, a->dim,
-          {static_cast<const T*>(a->x), a->x_batch_stride, a->x_time_stride},
-          {static_cast<const T*>(a->gate), a->gate_batch_stride, a->gate_time_stride},
-          {static_cast<const T*>(a->z), a->z_batch_stride, a->z_time_stride},
+          strided<T>(a, a->x, a->x_batch_stride, a->x_time_stride),
+          strided<T>(a, a->gate, a->gate_batch_stride, a->gate_time_stride),
+          strided<T>(a, a->z, a->z_batch_stride, a->z_time_stride),
           a->state, a->lengths, a->index_bytes};
 }
 
@@ -749,8 +797,8 @@ cr_status cr_gated_scan(const cr_gated_scan_args* a, void* y, int64_t y_batch_st
     const GateFwd<T> out = {static_cast<T*>(y), y_batch_stride, y_time_stride, final_state,
                             checkpoints, cr_gated_scan_checkpoints(a->len)};
     const bool wide = gate_wide(a) && rows_aligned(y, y_batch_stride, y_time_stride, es, 4);
-    using Shared = ForwardShared<Lane<T>::C>;
-    const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
+    const size_t smem = wide ? sizeof(ForwardShared<Lane<T>::C, true>)
+                             : sizeof(ForwardShared<Lane<T>::C, false>);
     auto kernel = CR_GATE_KERNEL(gated_scan_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScan, s,
               done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s,
@@ -784,14 +832,14 @@ cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_sca
   bool done = false;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CR_MODEL_TYPE(a->dt, {
-    const Strided<T> dy = {static_cast<const T*>(g->dy), g->dy_batch_stride, g->dy_time_stride};
+    const Strided<T> dy = strided<T>(a, g->dy, g->dy_batch_stride, g->dy_time_stride);
     const GateOut<T> out = {static_cast<T*>(g->dx), static_cast<T*>(g->dgate),
                             static_cast<T*>(g->dz), g->dstate};
     const bool wide = gate_wide(a) &&
                       rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, 16) &&
                       ptr_aligned(g->dx, 4) && ptr_aligned(g->dgate, 4) && ptr_aligned(g->dz, 4);
-    using Shared = BackwardShared<Lane<T>::C>;
-    const size_t smem = wide ? sizeof(Shared) : offsetof(Shared, staged);
+    const size_t smem = wide ? sizeof(BackwardShared<Lane<T>::C, true>)
+                             : sizeof(BackwardShared<Lane<T>::C, false>);
     auto kernel = CR_GATE_KERNEL(gated_scan_backward_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScanBackward, s,
               done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s,

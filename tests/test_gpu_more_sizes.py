@@ -137,3 +137,36 @@ def test_gated_scan_groups(scr, batch, T, D):
     got = scr.gated_scan_backward(dy.to(DEV), **d)
     for k in ("x", "gate", "z", "state"):
         M.near(got[k], *ref["d" + k], "d" + k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [1, 2, 63, 64, 65, 127, 129, 200])
+def test_gated_scan_rows_that_start_anywhere(scr, dtype, D):
+    """The same bits from rows at any offset and distance, odd and even, whatever
+    stands beside them, and from the first and the last elements of a buffer."""
+    g = torch.Generator().manual_seed(D)
+    B, T = 3, 37
+    s = {k: torch.randn(B, T, D, generator=g).to(dtype).to(DEV) for k in ("x", "gate", "z", "dy")}
+    lengths = torch.tensor([T, 0, 20], device=DEV)
+
+    def run(v, out=None):
+        y, kept = scr.gated_scan(v["x"], v["gate"], v["z"], lengths=lengths,
+                                 return_checkpoints=True)
+        if out is not None:
+            assert scr.gated_scan(v["x"], v["gate"], v["z"], lengths=lengths, out=out) is out
+            assert torch.equal(out, y)
+        return [y, *scr.gated_scan_backward(v["dy"], v["x"], v["gate"], v["z"], lengths=lengths,
+                                            checkpoints=kept).values()]
+    want = run(s)
+
+    def placed(v, offset, pad):
+        n = B * T * (D + pad) - pad
+        big = torch.full((n + offset,), float("nan"), dtype=dtype, device=DEV)
+        t = big[offset:].as_strided((B, T, D), (T * (D + pad), D + pad, 1))
+        return t.copy_(v)
+    cases = (((0, 1, 2, 3), 0), ((1, 1, 1, 1), 1), ((3, 0, 5, 2), 2), ((8, 8, 8, 8), 5))
+    for offsets, pad in cases:
+        v = {k: placed(s[k], o, pad) for k, o in zip(s, offsets)}
+        out = placed(torch.zeros_like(s["x"]), offsets[0], pad)
+        for a, b in zip(run(v, out), want):
+            assert torch.equal(a, b)
