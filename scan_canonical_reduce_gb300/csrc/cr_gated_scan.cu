@@ -158,10 +158,10 @@ __device__ __forceinline__ Map<C> map_join(const Map<C>& a, const Map<C>& b) {
 
 // A tile: 8 warps, each a run of kRun steps, a lane 32 bits of each step: one
 // channel of binary32, two neighbours of 16 bits, which come by way of shared
-// memory a tile ahead of their use: 16 bytes an access (kWide: rows on 16 bytes),
-// or 4. (4 x 4096 x 2047 in bf16, whose rows start anywhere, takes 179 us, its
-// gradient 334, where 2048 takes 61 and 104; read channel by channel it took 461
-// and 627.)
+// memory, 16 bytes an access, a tile ahead of their use (kWide: rows on 16 bytes;
+// otherwise the places of 16 bytes that they lie in: 4 x 4096 x 2047 in bf16 takes
+// 105 us, its gradient 199, where 2048 takes 62 and 104; by words of 4 bytes 179 and
+// 334, read channel by channel 461 and 627).
 constexpr int kRun = kGateCheckpoint;
 constexpr int kGateWarps = 8;
 constexpr int kTileSteps = kRun * kGateWarps;
@@ -223,10 +223,10 @@ struct Word {
 };
 
 // A run of one tensor in shared memory, a warp's own: kRun rows of 128 bytes, or
-// of the words that these lie in.
+// of the places of 16 bytes that these lie in.
 template <bool kWide>
 struct Staged {
-  uint32_t w[kRun][kWide ? 32 : 33];
+  uint32_t w[kRun][kWide ? 32 : 36];
 };
 
 // One input's runs, by way of shared memory. Steps past the end read as `past`
@@ -269,61 +269,70 @@ struct Runs {
   __device__ __forceinline__ uint32_t get(int i) const { return staged->w[i][threadIdx.x % 32]; }
 };
 
-// Rows that start anywhere: word w of a step, lane w's, holds its two elements of 16
-// bits, or, where the row starts in the upper half of a word, the second of the
-// lane before and its first. What is beside the row in its first and last word is
-// read where the tensor has it, and left out.
+// Rows that start anywhere lie in shared memory as they do in their places, some
+// elements off, and are put right as they are taken. What is beside the row in its
+// first and last place is read where the tensor has it, and left out.
 template <class T>
 struct Runs<T, false> {
-  static constexpr int kHalves = Lane<T>::C;
+  static constexpr int kHalves = Lane<T>::C, E = 16 / sizeof(T), kChannels = 32 * kHalves;
   const Strided<T>& s;
   Staged<false>* staged;
-  const T* p;  // the group's first channel of step 0
-  int n;       // channels from there on, 65 where there are more
+  const T* p;      // the group's first channel of step 0
+  int left;        // channels from there on
+  int first, more;  // elements that step 0 is off its place, and a step from the one before
   uint32_t past;
   __device__ __forceinline__ Runs(const Strided<T>& s_, int64_t b, int64_t group, int64_t dim,
                                   Staged<false>* st, uint32_t past_ = 0u)
       : s(s_), staged(st), past(past_) {
-    const int64_t c = group * 32 * kHalves;
+    const int64_t c = group * kChannels;
     p = s.p + b * s.bs + c;
-    n = (int)min((int64_t)65, dim - c);
+    left = (int)min((int64_t)(kChannels + E), dim - c);
+    first = shift(p);
+    more = (int)(s.ts % E);
   }
   static __device__ __forceinline__ int shift(const T* q) {
-    return kHalves == 2 ? (int)((uintptr_t)q >> 1 & 1) : 0;
+    return (int)((uintptr_t)q % 16) / (int)sizeof(T);
   }
-  static __device__ __forceinline__ uint32_t bits(const T* q) {
-    return *reinterpret_cast<const unsigned short*>(q);
-  }
-  __device__ __forceinline__ void word(uint32_t* to, const T* q, int w) const {
-    const int e = w * kHalves - shift(q);
-    if (e >= n) return;
-    if (kHalves == 1 || (e >= 0 && e + 1 < n) || (q + e >= s.p && q + e + 2 <= s.end))
-      copy4(to, q + e);
-    else
-      *to = e < 0 ? bits(q) << 16 : bits(q + e);
+  // Place `q` of the row at r.
+  __device__ __forceinline__ void place(uint32_t* to, const T* r, int q) const {
+    const int e = q * E - shift(r);
+    if (e >= min(left, kChannels)) return;
+    const T* const from = r + e;
+    if ((e >= 0 && e + E <= left) || (from >= s.p && from + E <= s.end)) {
+      copy16(to, from);
+    } else {
+      Pack<T, E> v;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        v.v[i] = e + i >= 0 && e + i < left ? from[i] : from_f32<T>(0.0f);
+      *reinterpret_cast<uint4*>(to) = __builtin_bit_cast(uint4, v);
+    }
   }
   __device__ __forceinline__ void ask(int64_t t0, int m) const {
     const int lane = threadIdx.x % 32;
     const T* const from = p + t0 * s.ts;
-#pragma unroll 4
-    for (int j = 0; j < kRun; ++j) {
-      uint32_t* to = &staged->w[j][lane];
-      if (j < m) word(to, from + j * s.ts, lane);
-      else *to = past;
+    const uint4 none = make_uint4(past, past, past, past);
+#pragma unroll
+    for (int j = 0; j < kRun / 4; ++j) {
+      const int i = j * 4 + lane / 8;
+      uint32_t* to = &staged->w[i][lane % 8 * 4];
+      if (i < m) place(to, from + i * s.ts, lane % 8);
+      else *reinterpret_cast<uint4*>(to) = none;
     }
-    if (kHalves == 2 && lane < kRun) {  // the words behind
+    if (lane < kRun) {  // the ninth places
       uint32_t* to = &staged->w[lane][32];
-      const T* q = from + lane * s.ts;
-      if (lane >= m) *to = past;
-      else if (shift(q) != 0) word(to, q, 32);
+      if (lane < m) place(to, from + lane * s.ts, 8);
+      else *reinterpret_cast<uint4*>(to) = none;
     }
   }
   __device__ __forceinline__ uint32_t get(int i) const {
-    const int lane = threadIdx.x % 32;
-    if constexpr (kHalves == 1) return staged->w[i][lane];
-    // (runs begin at even steps)
-    const int off = shift(p) ^ (int)(i & s.ts & 1);
-    return __funnelshift_r(staged->w[i][lane], staged->w[i][lane + 1], off * 16);
+    // (runs begin at steps that are multiples of 16)
+    int off = first;
+    asm volatile("" : "+r"(off));  // (not all of a run's held in registers between turns)
+    off = (off + i * more) & (E - 1);
+    const uint32_t* w = &staged->w[i][threadIdx.x % 32 + off / kHalves];
+    if constexpr (kHalves == 1) return *w;
+    else return __funnelshift_r(w[0], w[1], off % 2 * 16);
   }
 };
 
