@@ -359,7 +359,8 @@ struct Joints {
 };
 
 // Gives the state that this warp's run starts from, and moves `carry` past all
-// of the cluster's tiles.
+// of the cluster's tiles. (Its first call comes after cluster_wait(): it writes to
+// the other blocks' shared memory.)
 template <int C, bool kBack>
 __device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, int blocks,
                                             const Map<C>& run, float (&carry)[C]) {
@@ -431,6 +432,7 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
   using V = Vec<C>;
   extern __shared__ __align__(16) char shared[];
   ForwardShared<C, kWide>& sh = *reinterpret_cast<ForwardShared<C, kWide>*>(shared);
+  if (blocks > 1) cluster_arrive();
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
@@ -456,6 +458,7 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
   copy_commit();
   if constexpr (kZ) rz.ask(t0, m);
   copy_commit();
+  if (blocks > 1) cluster_wait();
   for (int64_t s0 = 0; s0 < n; s0 += step, t0 += step, turn ^= 1) {
     uint32_t g[kRun], xw[kRun];
     copy_wait<1>();
@@ -552,6 +555,7 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
   using V = Vec<C>;
   extern __shared__ __align__(16) char shared[];
   BackwardShared<C, kWide>& sh = *reinterpret_cast<BackwardShared<C, kWide>*>(shared);
+  if (blocks > 1) cluster_arrive();
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
@@ -588,6 +592,7 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
     for (int k = 0; k < C; ++k) h[k] = m > 0 && k < ch.have ? p[ch.at(k)] : 0.0f;
   };
   ask(s0 + mine, m);
+  if (blocks > 1) cluster_wait();
   for (; s0 >= 0; s0 -= step, turn ^= 1) {
     const int64_t t0 = s0 + mine;
     const int64_t at = (b * in.len + t0) * in.dim + ch.d;

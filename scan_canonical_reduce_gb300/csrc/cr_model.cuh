@@ -243,6 +243,16 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// --------------------------------------------------- blocks of a cluster
+// All of a cluster's blocks have begun, once each has arrived and this one has
+// waited: only then may one touch another's shared memory. (Both by all threads.)
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait;" ::: "memory");
+}
+
 // ------------------------------------------------- pairs of binary32
 // Two binary32 values in one 64-bit register pair, for the packed
 // arithmetic (one issue for two operations; fma and mul are rounded to nearest

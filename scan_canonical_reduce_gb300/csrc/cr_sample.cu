@@ -254,10 +254,10 @@ struct Sampler {
   }
   // All of the cluster's blocks have begun, once this has been waited for.
   __device__ __forceinline__ void begin() const {
-    if (blocks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    if (blocks > 1) cluster_arrive();
   }
   __device__ __forceinline__ void begun() const {
-    if (blocks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (blocks > 1) cluster_wait();
   }
   template <class V>
   __device__ __forceinline__ V* at(V* p, int block) const {
