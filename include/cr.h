@@ -603,7 +603,7 @@ cr_status cr_gated_scan_step(const cr_gated_scan_args* args, float* state, int64
  * A row without candidates gives -1.
  * Weights are evaluated to 2^-32 of their value and summed as integers, in
  * units of 2^-42 of the largest: the token is that of exact arithmetic unless
- * u or top_p lies that near to a border. */
+ * u, top_p or min_p lies that near to a border. */
 typedef struct {
   int64_t rows, vocab;    /* vocab <= 2^20 (more: CR_ERR_UNSUPPORTED)         */
   int32_t dt;             /* cr_dtype of logits                               */

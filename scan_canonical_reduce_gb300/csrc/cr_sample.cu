@@ -128,6 +128,11 @@ __device__ __forceinline__ uint64_t mass_of(int bin, uint64_t sum) {
   return n == 0 ? v : (v + ((uint64_t)1 << (n - 1))) >> n;
 }
 
+// Whether such a sum is at least `least`, in units of 2^-62 of the largest.
+__device__ __forceinline__ bool at_least(int bin, uint64_t sum, uint64_t least) {
+  return __umul64hi(sum << 30, kRoots[bin & 15]) >> (bin >> 4) >= least;
+}
+
 // y in bins.
 __device__ __forceinline__ float in_bins(const Row& r, float l) {
   return (r.top - l) * (r.ch * 16.0f);
@@ -146,7 +151,7 @@ struct Settings {
   bool cold;       // the first token, whatever u
   uint64_t top_k;  // 0: no limit
   double top_p;    // 1: no limit
-  uint64_t min_w;  // the least weight that is kept, in units of 2^-42; 0: no limit
+  uint64_t min_w;  // the least weight that is kept, in units of 2^-62; 0: no limit
 };
 constexpr double kLog2eD = 1.4426950408889634;
 constexpr float kLog2eHi = (float)kLog2eD, kLog2eLo = (float)(kLog2eD - (double)kLog2eHi);
@@ -181,7 +186,7 @@ struct SampleIn {
     }
     if (min_ps != nullptr) {
       const float p = min_ps[row];
-      s.min_w = p > 0.0f ? __float2ull_ru(fminf(p, 1.0f) * 0x1p42f) : 0;
+      s.min_w = p > 0.0f ? __float2ull_ru(fminf(p, 1.0f) * 0x1p62f) : 0;
     }
     return s;
   }
@@ -219,7 +224,7 @@ struct Shared {
   uint64_t said[2][kMostBlocks];  // by block
   uint64_t part[2];               // leader
   uint64_t want;                  // leader: what a border is looked for
-  int limit_bin, floor_bin;       // of top_k and of min_p, kBins without one
+  int limit_bin, floor_bin;       // of top_k and the first of min_p, kBins without one
   Message message[2];             // one is read while the other is written
   int found;
 };
@@ -835,12 +840,20 @@ struct Sampler {
       lo = sh.mass[a];
       hi = min(hi, sh.mass[b + 1]);
     }
-    if (lim.min_w != 0) {  // the last bin whose weights may be that large
-      const int d = first_of(kBins, [&](int i) { return mass_of(i, 1ull << 33) < lim.min_w; }) - 1;
-      if (d <= end) {
-        floor_ = d;
-        if (d != kFar) choose(d, d);
-        lo = min(lo, sh.mass[d]);
+    if (lim.min_w != 0) {
+      // (A weight passes its bin's ends by less than 2^-18 of itself: one near an end
+      // may be in the bin before or after.) The last bin that may hold weights of
+      // min_w, and the first that may hold smaller ones.
+      const int d = first_of(kFar, [&](int i) {
+                      return !at_least(i, (1ull << 33) + kShift, lim.min_w);
+                    }) - 1;
+      const int c = first_of(d, [&](int i) {
+        return !at_least(i + 1, (1ull << 33) - kShift, lim.min_w);
+      });
+      if (c <= end) {
+        floor_ = c;
+        choose(c, d);
+        lo = min(lo, sh.mass[c]);
         hi = min(hi, sh.mass[d + 1]);
       }
     }
@@ -940,7 +953,7 @@ struct Sampler {
       const int d = sh.floor_bin;
       const int j =
           first_of(number, [&](int i) { return !heavy((uint32_t)(sh.list[i] >> 32), lim); });
-      const bool in = j > 0 && sh.bin_of[j - 1] == d;  // else none of its bin
+      const bool in = j > 0 && sh.bin_of[j - 1] >= d;  // else none from its bin on
       const uint32_t many = in ? place_of(j - 1) : sh.before[d];
       if (many < end) kept = in ? sh.sums[j - 1] : sh.mass[d];
     }
@@ -986,7 +999,7 @@ struct Sampler {
     if (!(l > -INFINITY)) return false;
     uint32_t g;
     const int bin = place(r, l, g);
-    return bin != kFar && mass_of(bin, weights(1, g)) >= lim.min_w;
+    return bin != kFar && at_least(bin, weights(1, g), lim.min_w);
   }
   // The last key of which that is true (weights fall as keys rise).
   __device__ uint32_t last_key(const Settings& lim) const {
@@ -1247,7 +1260,7 @@ cr_status cr_sample(const cr_sample_args* a, int64_t* tokens, void* stream) {
   all.top_k = a->top_k > 0 ? (uint64_t)a->top_k : 0;
   all.top_p = a->top_p < 1.0 ? std::max(a->top_p, 0.0) : 1.0;
   all.min_w = 0;
-  if (a->min_p > 0.0) all.min_w = (uint64_t)std::ceil(std::ldexp(std::min(a->min_p, 1.0), 42));
+  if (a->min_p > 0.0) all.min_w = (uint64_t)std::ceil(std::ldexp(std::min(a->min_p, 1.0), 62));
   bool done = false;
   CR_MODEL_TYPE(a->dt, {
     const SampleIn<T> in = {a->vocab,  static_cast<const T*>(a->logits), a->row_stride, a->u,
