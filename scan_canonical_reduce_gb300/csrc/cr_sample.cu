@@ -67,10 +67,10 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // Where a candidate that is not the largest lies: its bin, that of y rounded to
 // binary32 (which no order of two logits changes), and its weight in it, 2^(bin
 // / 16) w = 1 - z', as g = z' + 2^-18 in units of 2^-33: z' is -2^-19 to 0.0425.
-// Far is y of 63.9 or more (the far bin): such weights together are below 2^-42
-// of the largest's. Straight code, whose results then mean nothing.
+// Far is y from the last bin's beginning on (the far bin): such weights together are
+// below 2^-42 of the largest's. Straight code, whose results then mean nothing.
 constexpr int kFar = kBins - 1;
-constexpr float kFarY = 63.9f;
+constexpr float kFarY = kFar / 16.0f;  // as in_bins() has it
 constexpr int kIndexDigits = 10;  // 2^20 indices in kBins
 constexpr uint32_t kShift = 1u << 15;
 // y in two numbers, of which the first is negative here, of two logits: the

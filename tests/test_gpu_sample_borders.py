@@ -89,3 +89,21 @@ def test_min_p_far_below_the_largest(scr):
     u = 1 - torch.rand(n, generator=g) * 2.0 ** -2
     check(scr, x, u, min_p=torch.exp(-(torch.rand(n, generator=g) * 4 + 11)))
     check(scr, x[:2], u[:2], min_p=1e-12)
+
+
+# ------------------------------------------------------- the farthest bins
+@pytest.mark.parametrize("rows,V", [(40, 1100), (40, 20000), (4, 70000)])
+@pytest.mark.parametrize("settings", [dict(), dict(top_p=0.8), dict(min_p=0.2)])
+def test_top_k_that_ends_among_the_lightest(scr, rows, V, settings):
+    """The last of top_k are tokens of weight 2^-63.88, behind which many of 2^-63.92
+    lie: the largest and the smallest that are still told apart from none."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.full((rows, V), -float("inf"))
+    for r in range(rows):
+        y = torch.cat([torch.rand(600, generator=g) * 2, 63.88 + 0.015 * torch.rand(10, generator=g),
+                       63.905 + 0.025 * torch.rand(400, generator=g)])
+        y[0] = 0
+        x[r, torch.randperm(V, generator=g)[:len(y)]] = -y * float(np.log(2.0))
+    u = torch.rand(rows, generator=g)
+    for k in (601, 605, 609):
+        check(scr, x, u, top_k=k, **settings)
