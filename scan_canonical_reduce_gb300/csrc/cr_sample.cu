@@ -695,7 +695,7 @@ struct Sampler {
         nb += sh.before[d];
         sb += sh.mass[d];
         lo = m.lo + ((uint32_t)d << shift);
-        hi = lo + ((uint32_t)1 << shift) - 1;
+        hi = min(m.hi, lo + ((uint32_t)1 << shift) - 1);  // (keys past m.hi are not counted)
         tell({bin, lo, hi, many});
       }
       m = hear();

@@ -107,3 +107,27 @@ def test_top_k_that_ends_among_the_lightest(scr, rows, V, settings):
     u = torch.rand(rows, generator=g)
     for k in (601, 605, 609):
         check(scr, x, u, top_k=k, **settings)
+
+
+# ------------------------------------------------------ bins that are cut
+@pytest.mark.parametrize("rows,V", [(60, 2400), (60, 30000), (3, 80000)])
+def test_cut_that_ends_beside_other_logits(scr, rows, V):
+    """2147 tokens of one bin, which is cut by the logits' bits: into parts of 8192
+    neighbouring numbers, then one of these, whose first 100 numbers are missing, into
+    parts of 8. The last of these reaches past it, to numbers that stand there."""
+    top = np.float32(100.0).view(np.uint32)
+    g = np.random.default_rng(V)
+    x = np.full((rows, V), -np.inf, dtype=np.float32)
+    begin = 40 * 8192  # of the part, in binary32 numbers below the largest
+    for r in range(rows):
+        below = np.concatenate([
+            [0, 2 ** 22 + 7], g.integers(begin + 101, begin + 8188, 1224), [begin + 100],
+            np.repeat(begin + 8188 + np.arange(4), 30), np.repeat(begin + 8192 + np.arange(4), 200)])
+        x[r, g.permutation(V)[:len(below)]] = (top - below.astype(np.uint32)).view(np.float32)
+    x = torch.from_numpy(x)
+    # all weights are within 4 % of one another; about the 1285th of 2147 is drawn
+    assert float(x[x > -np.inf].min()) > 64
+    u = torch.from_numpy(((1230 + 115 * g.random(rows)) / 2147).astype(np.float32))
+    check(scr, x, u, temperature=1000.0)
+    check(scr, x, torch.full((rows,), LAST), temperature=1000.0, top_k=1290)
+    check(scr, x, torch.full((rows,), LAST), temperature=1000.0, top_p=0.6)
