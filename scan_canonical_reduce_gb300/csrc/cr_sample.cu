@@ -66,13 +66,15 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 
 // Where a candidate that is not the largest lies: its bin, that of y rounded to
 // binary32 (which no order of two logits changes), and its weight in it, 2^(bin
-// / 16) w = 1 - z', as g = z' + 2^-18 in units of 2^-33: z' is -2^-19 to 0.0425.
+// / 16) w = 1 - z', as g = z' + 2^-16 in units of 2^-33: z' is -2^-16.9 to 0.0425. (y
+// is up to 3 2^-18 off its first number: half a step of the product, of the
+// difference and of log2(e) / temperature, each 2^-24 of y < 64 at most.)
 // Far is y from the last bin's beginning on (the far bin): such weights together are
 // below 2^-42 of the largest's. Straight code, whose results then mean nothing.
 constexpr int kFar = kBins - 1;
 constexpr float kFarY = kFar / 16.0f;  // as in_bins() has it
 constexpr int kIndexDigits = 10;  // 2^20 indices in kBins
-constexpr uint32_t kShift = 1u << 15;
+constexpr uint32_t kShift = 1u << 17;
 // y in two numbers, of which the first is negative here, of two logits: the
 // difference in two numbers, times log2(e) / temperature in two.
 __device__ __forceinline__ void distance2(const Row& r, F2 l, F2& yh, F2& yl) {
@@ -86,7 +88,7 @@ __device__ __forceinline__ void distance2(const Row& r, F2 l, F2& yh, F2& yl) {
 // The bin and the weight of minus y = yh - yl.
 __device__ __forceinline__ void split(float yh, float yl, int& bin, uint32_t& g) {
   // y = bin / 16 + x, x in units of 2^-34, from its two parts; adding 2^23
-  // rounded down is a floor, adding 3 2^22 a rounding (of 2^16 at most)
+  // rounded down is a floor, adding 3 2^22 a rounding (of 3 2^16 at most)
   const float t = __fmaf_rd(yh, -16.0f, 0x1p23f);
   bin = (int)(__float_as_uint(t) & 0x7FFFFFu);
   const float xh = fmaf(t - 0x1p23f, -0.0625f, -yh);
@@ -841,7 +843,7 @@ struct Sampler {
       hi = min(hi, sh.mass[b + 1]);
     }
     if (lim.min_w != 0) {
-      // (A weight passes its bin's ends by less than 2^-18 of itself: one near an end
+      // (A weight passes its bin's ends by less than 2^-16 of itself: one near an end
       // may be in the bin before or after.) The last bin that may hold weights of
       // min_w, and the first that may hold smaller ones.
       const int d = first_of(kFar, [&](int i) {

@@ -131,3 +131,22 @@ def test_cut_that_ends_beside_other_logits(scr, rows, V):
     check(scr, x, u, temperature=1000.0)
     check(scr, x, torch.full((rows,), LAST), temperature=1000.0, top_k=1290)
     check(scr, x, torch.full((rows,), LAST), temperature=1000.0, top_p=0.6)
+
+
+# ----------------------------------------------------- the largest roundings
+@pytest.mark.parametrize("rows", [1, 3])
+def test_weight_furthest_above_its_bins_own(scr, rows):
+    """A logit whose distance, in the two binary32 numbers that hold it, has nearly the
+    largest second number that it may have: its weight is 2^(-533 / 16) (1 + 1.04
+    2^-18). Alone it weighs nothing; a million of them are 2^-13.3."""
+    V, top, low, T = 1 << 20, 2.999998092651367, -30.16681671142578, 1.4363859649122808
+    x = torch.full((rows, V), low, device=DEV)
+    x[:, 77] = top
+    w = float(np.exp((np.float64(np.float32(low)) - np.float64(np.float32(top))) / T))
+    u = 1 - torch.arange(1, rows + 1) * 2.0 ** -15
+    got = scr.sample(x, u.to(DEV), temperature=T).tolist()
+    for a, v in zip(got, u.double().tolist()):
+        at = (v * (1 + (V - 1) * w) - 1) / w  # so many of them come before
+        assert at > 1000
+        # sums are right to 2^-42 (2^-42 / w < 1) and a weight to 2^-32
+        assert abs(a - at) <= 3
