@@ -538,7 +538,8 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* args, const cr_layer_
  *   a[t] = 1 / (1 + exp(-gate[t]))
  *   h[t] = a[t] h[t-1] + (1 - a[t]) x[t],  h[-1] = state (zero without one)
  *   y[t] = h[t] * z[t] / (1 + exp(-z[t]))  (h[t] without z)
- * All arithmetic is binary32. */
+ * All arithmetic is binary32. An infinite state stays infinite, whatever the gate,
+ * until it meets the other infinity or NaN. */
 typedef struct {
   int64_t batch, len, dim;
   int32_t dt;             /* cr_dtype of x, gate, z, y and their gradients    */

@@ -7,7 +7,9 @@
 //
 // The state goes by r alone: where a memory is long, a is near 1 and binary32
 // keeps few digits of r in it (a product by a would forget at a rate that is
-// off by 2^-25 / r). So a h is h - r h, one rounding, exact for r = 0 and 1.
+// off by 2^-25 / r). So a h is h - r h, one rounding, exact for r = 0 and 1. An
+// infinity becomes NaN in it, and NaN stays NaN: a sequence that ends in something not
+// finite is gone through again, with products that keep infinities (kInf).
 #include <algorithm>
 #include <cstdint>
 
@@ -105,10 +107,23 @@ __device__ __forceinline__ Vec<C> minus_sigmoid(Vec<C> v, float s, Vec<C>* e_out
   return reciprocal_of(fma(e, Vec<C>(-1.0f), Vec<C>(-1.0f)));
 }
 
-// A step for r: p - r p, and with what is added.
-template <int C>
+// A step for r: p - r p, and with what is added. kInf: what is infinite stays so (all
+// else has the same bits).
+template <bool kInf = false, int C>
 __device__ __forceinline__ Vec<C> decay(Vec<C> minus_r, Vec<C> p) {
-  return fma(minus_r, p, p);
+  Vec<C> v = fma(minus_r, p, p);
+  if constexpr (kInf) {
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (isinf(p.get(k))) v.set(k, p.get(k));
+  }
+  return v;
+}
+// Whether one of the channels that exist is infinite or NaN.
+template <class V>
+__device__ __forceinline__ bool odd(const V& v, int have) {
+  return (have > 0 && !(fabsf(v[0]) < INFINITY)) ||
+         (have > 1 && !(fabsf(v[sizeof(V) / 4 - 1]) < INFINITY));
 }
 
 // What a run of steps does to the state: h -> L + P h. Where P is near 1 its
@@ -117,11 +132,13 @@ __device__ __forceinline__ Vec<C> decay(Vec<C> minus_r, Vec<C> p) {
 template <int C>
 struct alignas(8 * C) Map {
   float L[C], F[C];
+  template <bool kInf>
   __device__ __forceinline__ void apply(float (&h)[C]) const {
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const float v = fmaf(-F[k], h[k], L[k]);
-      h[k] = __float_as_int(F[k]) >= 0 ? v + h[k] : v;
+      const float next = __float_as_int(F[k]) >= 0 ? v + h[k] : v;
+      h[k] = kInf && isinf(h[k]) ? h[k] + L[k] : next;
     }
   }
 };
@@ -137,7 +154,7 @@ __device__ __forceinline__ Map<C> run_map(Vec<C> L, Vec<C> minus_Q, Vec<C> P) {
   return m;
 }
 // The map b after the map a.
-template <int C>
+template <bool kInf, int C>
 __device__ __forceinline__ Map<C> map_join(const Map<C>& a, const Map<C>& b) {
   Vec<C> L, q, p;
   float l[C];
@@ -150,7 +167,7 @@ __device__ __forceinline__ Map<C> map_join(const Map<C>& a, const Map<C>& b) {
     p.set(k, Pa * Pb);
     l[k] = a.L[k];
   }
-  b.apply(l);
+  b.template apply<kInf>(l);
 #pragma unroll
   for (int k = 0; k < C; ++k) L.set(k, l[k]);
   return run_map(L, q, p);
@@ -361,7 +378,7 @@ struct Joints {
 // Gives the state that this warp's run starts from, and moves `carry` past all
 // of the cluster's tiles. (Its first call comes after cluster_wait(): it writes to
 // the other blocks' shared memory.)
-template <int C, bool kBack>
+template <int C, bool kBack, bool kInf>
 __device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, int blocks,
                                             const Map<C>& run, float (&carry)[C]) {
   namespace cg = cooperative_groups;
@@ -378,7 +395,7 @@ __device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, in
       Map<C> tile = j.warp[turn][kBack ? kGateWarps - 1 : 0][lane];
 #pragma unroll
       for (int i = 1; i < kGateWarps; ++i)
-        tile = map_join(tile, j.warp[turn][kBack ? kGateWarps - 1 - i : i][lane]);
+        tile = map_join<kInf>(tile, j.warp[turn][kBack ? kGateWarps - 1 - i : i][lane]);
       for (int to = warp; to < blocks; to += kGateWarps)
         *cl.map_shared_rank(&j.tile[turn][rank][lane], to) = tile;
     }
@@ -387,12 +404,12 @@ __device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, in
       const int r = kBack ? blocks - 1 - i : i;
 #pragma unroll
       for (int k = 0; k < C; ++k) h[k] = r == rank ? carry[k] : h[k];
-      j.tile[turn][r][lane].apply(carry);
+      j.tile[turn][r][lane].template apply<kInf>(carry);
     }
 #pragma unroll
     for (int i = 0; i < kGateWarps; ++i) {
       const int w = kBack ? kGateWarps - 1 - i : i;
-      if (kBack ? w > warp : w < warp) j.warp[turn][w][lane].apply(h);
+      if (kBack ? w > warp : w < warp) j.warp[turn][w][lane].template apply<kInf>(h);
     }
   } else {
 #pragma unroll
@@ -400,7 +417,7 @@ __device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, in
       const int w = kBack ? kGateWarps - 1 - i : i;
 #pragma unroll
       for (int k = 0; k < C; ++k) h[k] = w == warp ? carry[k] : h[k];
-      j.warp[turn][w][lane].apply(carry);
+      j.warp[turn][w][lane].template apply<kInf>(carry);
     }
   }
   Vec<C> v;
@@ -445,92 +462,105 @@ gated_scan_kernel(GateIn<T> in, GateFwd<T> out, int blocks) {
   const Runs<T, kWide> rx(in.x, b, group, in.dim, st + 1);
   const Runs<T, kWide> rz(kZ ? in.z : in.x, b, group, in.dim, st + 2);
   float carry[C];  // -h
+  const auto begin = [&] {
 #pragma unroll
-  for (int k = 0; k < C; ++k)
-    carry[k] = in.state != nullptr && k < ch.have ? -in.state[b * in.dim + ch.at(k)] : 0.0f;
+    for (int k = 0; k < C; ++k)
+      carry[k] = in.state != nullptr && k < ch.have ? -in.state[b * in.dim + ch.at(k)] : 0.0f;
+  };
+  begin();
   const int64_t step = (int64_t)blocks * kTileSteps;
-  int turn = 0;
-  int64_t t0 = (int64_t)rank * kTileSteps + warp * kRun;  // this warp's run
-  auto steps = [&](int64_t t) { return (int)max((int64_t)0, min((int64_t)kRun, n - t)); };
-  int m = steps(t0);
-  rg.ask(t0, m);
-  rx.ask(t0, m);
-  copy_commit();
-  if constexpr (kZ) rz.ask(t0, m);
-  copy_commit();
-  if (blocks > 1) cluster_wait();
-  for (int64_t s0 = 0; s0 < n; s0 += step, t0 += step, turn ^= 1) {
-    uint32_t g[kRun], xw[kRun];
-    copy_wait<1>();
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) g[i] = rg.get(i);
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) xw[i] = rx.get(i);
-    __syncwarp();
-    const int64_t next = t0 + step;
-    const int m_next = steps(next);
-    rg.ask(next, m_next);
-    rx.ask(next, m_next);
+  // all of it, from the beginning (begun: what is waited for after the first loads)
+  const auto turns = [&](auto inf, auto begun) {
+    int turn = 0;
+    int64_t t0 = (int64_t)rank * kTileSteps + warp * kRun;  // this warp's run
+    auto steps = [&](int64_t t) { return (int)max((int64_t)0, min((int64_t)kRun, n - t)); };
+    int m = steps(t0);
+    rg.ask(t0, m);
+    rx.ask(t0, m);
     copy_commit();
-    V r[kRun], x[kRun];  // -r
-    V L(0.0f), Q(0.0f), P(1.0f);
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      r[i] = minus_sigmoid(W::get(g[i]), kLog2e);
-      x[i] = W::get(xw[i]);
-      L = fma(r[i], x[i], decay(r[i], L));  // of the negative state
-      Q = fma(r[i], P, Q);
-      P = decay(r[i], P);
-    }
-    V s = join_runs<C, false>(sh.joints, turn, rank, blocks, run_map(L, Q, P), carry);
-    if (out.checkpoints != nullptr && m > 0) {
-      float* p = out.checkpoints + (b * out.n_check + t0 / kRun) * in.dim;
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (k < ch.have) p[ch.at(k)] = -s.get(k);
-    }
-    if constexpr (kZ) {
+    if constexpr (kZ) rz.ask(t0, m);
+    copy_commit();
+    begun();
+    for (int64_t s0 = 0; s0 < n; s0 += step, t0 += step, turn ^= 1) {
+      uint32_t g[kRun], xw[kRun];
       copy_wait<1>();
       __syncwarp();
-    }
-    uint32_t y[kRun];
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      s = fma(r[i], x[i], decay(r[i], s));
-      if constexpr (kZ) {
-        const V z = W::get(rz.get(i));
-        y[i] = W::round(mul(mul(s, z), minus_sigmoid(z, -kLog2e)));
-      } else {
-        y[i] = W::round(mul(s, V(-1.0f)));
-      }
-    }
-    if constexpr (kZ) {
+      for (int i = 0; i < kRun; ++i) g[i] = rg.get(i);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) xw[i] = rx.get(i);
       __syncwarp();
-      rz.ask(next, m_next);
-    }
-    copy_commit();
-    T* py = out.y + b * out.ybs + t0 * out.yts + ch.d;
-    if (m == kRun) {
+      const int64_t next = t0 + step;
+      const int m_next = steps(next);
+      rg.ask(next, m_next);
+      rx.ask(next, m_next);
+      copy_commit();
+      V r[kRun], x[kRun];  // -r
+      V L(0.0f), Q(0.0f), P(1.0f);
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) W::store(py + i * out.yts, ch.have, y[i]);
-    } else {
+      for (int i = 0; i < kRun; ++i) {
+        r[i] = minus_sigmoid(W::get(g[i]), kLog2e);
+        x[i] = W::get(xw[i]);
+        L = fma(r[i], x[i], decay<inf>(r[i], L));  // of the negative state
+        Q = fma(r[i], P, Q);
+        P = decay(r[i], P);
+      }
+      V s = join_runs<C, false, inf>(sh.joints, turn, rank, blocks, run_map(L, Q, P), carry);
+      if (out.checkpoints != nullptr && m > 0) {
+        float* p = out.checkpoints + (b * out.n_check + t0 / kRun) * in.dim;
 #pragma unroll
-      for (int i = 0; i < kRun; ++i)
-        if (i < m) W::store(py + i * out.yts, ch.have, y[i]);
+        for (int k = 0; k < C; ++k)
+          if (k < ch.have) p[ch.at(k)] = -s.get(k);
+      }
+      if constexpr (kZ) {
+        copy_wait<1>();
+        __syncwarp();
+      }
+      uint32_t y[kRun];
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        s = fma(r[i], x[i], decay<inf>(r[i], s));
+        if constexpr (kZ) {
+          const V z = W::get(rz.get(i));
+          y[i] = W::round(mul(mul(s, z), minus_sigmoid(z, -kLog2e)));
+        } else {
+          y[i] = W::round(mul(s, V(-1.0f)));
+        }
+      }
+      if constexpr (kZ) {
+        __syncwarp();
+        rz.ask(next, m_next);
+      }
+      copy_commit();
+      T* py = out.y + b * out.ybs + t0 * out.yts + ch.d;
+      if (m == kRun) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) W::store(py + i * out.yts, ch.have, y[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (i < m) W::store(py + i * out.yts, ch.have, y[i]);
+      }
+      m = m_next;
     }
-    m = m_next;
+    copy_wait<0>();
+  };
+  turns(std::false_type{}, [&] { if (blocks > 1) cluster_wait(); });
+  // past the sequence's end
+  for (int64_t t = n + rank * kGateWarps + warp; t < in.len; t += blocks * kGateWarps)
+    W::store(out.y + b * out.ybs + t * out.yts + ch.d, ch.have, 0u);
+  if (blocks > 1) cooperative_groups::this_cluster().sync();  // others write here
+  if (__any_sync(~0u, odd(carry, ch.have))) {  // (the same in all of the cluster's warps)
+    if (blocks == 1) __syncthreads();
+    begin();
+    turns(std::true_type{}, [] {});
+    if (blocks > 1) cooperative_groups::this_cluster().sync();
   }
-  copy_wait<0>();
   if (out.final_state != nullptr && rank == 0 && warp == 0) {
 #pragma unroll
     for (int k = 0; k < C; ++k)
       if (k < ch.have) out.final_state[b * in.dim + ch.at(k)] = -carry[k];
   }
-  // past the sequence's end
-  for (int64_t t = n + rank * kGateWarps + warp; t < in.len; t += blocks * kGateWarps)
-    W::store(out.y + b * out.ybs + t * out.yts + ch.d, ch.have, 0u);
-  if (blocks > 1) cooperative_groups::this_cluster().sync();  // others write here
 }
 
 template <class T>
@@ -543,19 +573,110 @@ template <int C, bool kWide>
 struct BackwardShared {
   Joints<C> joints;
   Staged<kWide> staged[kGateWarps][4];
+  int odd, any;  // whether a run's states are not all finite, of this block and of all
 };
+
+template <class T>
+struct GateGrads {
+  Strided<T> dy;
+  const float *dfinal, *checkpoints;
+  int64_t n_check;
+  GateOut<T> out;
+};
+
+// The same again, with infinities kept, where something in a sequence is not finite:
+// channel after channel of a lane, straight from memory, step after step of a run in
+// shared memory. (Few registers: with a second loop like the kernel's, or a call of
+// one, that one's spilled, and the gradient of 4 x 4096 x 4096 in bf16 took 172 to 220
+// us for 160. Where this runs for all of it, that takes 1050; the forward pass, which
+// has a second loop, 192 for 100.)
+template <class T, bool kZ, bool kWide>
+__device__ __forceinline__ void backward_again(const GateIn<T>& in, const GateGrads<T>& grads,
+                                               int rank, int blocks, int64_t b, int64_t n,
+                                               const Channels<T>& ch, Joints<1>& joints,
+                                               Staged<kWide> (*staged)[4]) {
+  using V = Vec<1>;
+  constexpr int C = Lane<T>::C;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t step = (int64_t)blocks * kTileSteps;
+  const auto held = [&](int which, int i) -> float& {
+    return reinterpret_cast<float&>(staged[warp][which].w[i][lane]);
+  };
+#pragma unroll 1
+  for (int k = 0; k < C; ++k) {
+    const bool have = k < ch.have;
+    const int64_t c = have ? ch.at(k) : 0;  // (lanes without one go through the first)
+    float carry[1] = {grads.dfinal != nullptr && have ? -grads.dfinal[b * in.dim + c] : 0.0f};
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t s0 = (n + step - 1) / step * step - step; s0 >= 0; s0 -= step, turn ^= 1) {
+      const int64_t t0 = s0 + rank * kTileSteps + warp * kRun;
+      const int m = (int)max((int64_t)0, min((int64_t)kRun, n - t0));
+      const auto read = [&](const Strided<T>& p, int i) {
+        return V(to_f32(p.p[b * p.bs + (t0 + i) * p.ts + c]));
+      };
+      const int64_t at = (b * in.len + t0) * in.dim + c;
+      V s(m > 0 ? -grads.checkpoints[(b * grads.n_check + t0 / kRun) * in.dim + c] : 0.0f);
+#pragma unroll 2
+      for (int i = 0; i < m; ++i) {
+        const V x = read(in.x, i), g = read(in.gate, i);
+        V e, v = read(grads.dy, i);
+        const V r = minus_sigmoid(V(g.v > 80.0f ? 80.0f : g.v), kLog2e, &e);
+        held(0, i) = r.v;
+        held(1, i) = mul(mul(add(s, x), r), mul(e, r)).v;
+        s = fma(r, x, decay<true>(r, s));
+        if constexpr (kZ) {
+          const V z = read(in.z, i), w = minus_sigmoid(z, -kLog2e);
+          const V silu = mul(z, w), slope = fma(silu, fma(w, V(1.0f), V(1.0f)), w);
+          if (have) grads.out.dz[at + i * in.dim] = from_f32<T>(mul(mul(v, s), slope).v);
+          v = mul(v, silu);
+        } else {
+          v = mul(v, V(-1.0f));
+        }
+        held(2, i) = v.v;
+      }
+      V L(0.0f), Q(0.0f), P(1.0f);
+#pragma unroll 1
+      for (int i = m - 1; i >= 0; --i) {
+        const V r(held(0, i));
+        L = decay<true>(r, fma(V(held(2, i)), V(1.0f), L));
+        Q = fma(r, P, Q);
+        P = decay(r, P);
+      }
+      V B = join_runs<1, true, true>(joints, turn, rank, blocks, run_map(L, Q, P), carry);
+#pragma unroll 1
+      for (int i = m - 1; i >= 0; --i) {
+        const V r(held(0, i)), G = fma(V(held(2, i)), V(1.0f), B);
+        if (have) {
+          grads.out.dx[at + i * in.dim] = from_f32<T>(mul(r, G).v);
+          grads.out.dgate[at + i * in.dim] = from_f32<T>(mul(V(held(1, i)), G).v);
+        }
+        B = decay<true>(r, G);
+      }
+    }
+    if (grads.out.dstate != nullptr && have && rank == 0 && warp == 0)
+      grads.out.dstate[b * in.dim + c] = -carry[0];
+    if (blocks > 1) cooperative_groups::this_cluster().sync();
+    else __syncthreads();
+  }
+}
 
 template <class T, bool kZ, bool kWide>
 __global__ void __launch_bounds__(kGateWarps * 32, 2)
-gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict__ dfinal,
-                           const float* __restrict__ checkpoints, int64_t n_check, GateOut<T> out,
-                           int blocks) {
+gated_scan_backward_kernel(const __grid_constant__ GateIn<T> in,
+                           const __grid_constant__ GateGrads<T> grads, int blocks) {
+  const Strided<T>& dy = grads.dy;
+  const GateOut<T>& out = grads.out;
+  const float* __restrict__ const dfinal = grads.dfinal;
+  const float* __restrict__ const checkpoints = grads.checkpoints;
   constexpr int C = Lane<T>::C;
   using W = Word<T, kWide>;
   using V = Vec<C>;
   extern __shared__ __align__(16) char shared[];
   BackwardShared<C, kWide>& sh = *reinterpret_cast<BackwardShared<C, kWide>*>(shared);
+  if (threadIdx.x == 0) sh.odd = sh.any = 0;
   if (blocks > 1) cluster_arrive();
+  else __syncthreads();
   const int warp = threadIdx.x / 32;
   const int rank = (int)(blockIdx.x % (unsigned)blocks);
   const int64_t per = (in.dim + 32 * C - 1) / (32 * C);
@@ -587,7 +708,7 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
     re.ask(t0, m);
     if constexpr (kZ) rz.ask(t0, m);
     copy_commit();
-    const float* p = checkpoints + (b * n_check + t0 / kRun) * in.dim;
+    const float* p = checkpoints + (b * grads.n_check + t0 / kRun) * in.dim;
 #pragma unroll
     for (int k = 0; k < C; ++k) h[k] = m > 0 && k < ch.have ? p[ch.at(k)] : 0.0f;
   };
@@ -625,6 +746,10 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
         v[i] = mul(v[i], V(-1.0f));
       }
     }
+    float last[C];
+#pragma unroll
+    for (int k = 0; k < C; ++k) last[k] = s.get(k);
+    if (odd(last, ch.have)) sh.odd = 1;
     if constexpr (kZ) {
       if (m == kRun) {
 #pragma unroll
@@ -646,7 +771,7 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
       Q = fma(r[i], P, Q);
       P = decay(r[i], P);
     }
-    V B = join_runs<C, true>(sh.joints, turn, rank, blocks, run_map(L, Q, P), carry);
+    V B = join_runs<C, true, false>(sh.joints, turn, rank, blocks, run_map(L, Q, P), carry);
     uint32_t ox[kRun], og[kRun];
 #pragma unroll
     for (int i = kRun - 1; i >= 0; --i) {
@@ -684,7 +809,16 @@ gated_scan_backward_kernel(GateIn<T> in, Strided<T> dy, const float* __restrict_
     W::store(out.dgate + at, ch.have, 0u);
     if constexpr (kZ) W::store(out.dz + at, ch.have, 0u);
   }
-  if (blocks > 1) cooperative_groups::this_cluster().sync();
+  __syncthreads();
+  if (blocks > 1) {
+    if (sh.odd && threadIdx.x < blocks)
+      *cooperative_groups::this_cluster().map_shared_rank(&sh.any, threadIdx.x) = 1;
+    cooperative_groups::this_cluster().sync();
+  }
+  // (the same in all of the cluster's warps)
+  if (__any_sync(~0u, odd(carry, ch.have)) || (blocks > 1 ? sh.any : sh.odd))
+    backward_again<T, kZ>(in, grads, rank, blocks, b, n, ch,
+                          reinterpret_cast<Joints<1>&>(sh.joints), sh.staged);
 }
 
 // One token of each stream: a thread a channel, blocks of a stream side by side,
@@ -703,7 +837,7 @@ gated_scan_step_kernel(GateIn<T> in, float* __restrict__ state, int64_t rows, co
       float h = state[row * in.dim + d];
       const float x = to_f32(in.x.p[b * in.x.bs + d]);
       const float r = minus_sigmoid(Vec<1>(to_f32(in.gate.p[b * in.gate.bs + d])), kLog2e).v;
-      h = fmaf(-r, x, fmaf(r, h, h));
+      h = fmaf(-r, x, isinf(h) ? h : fmaf(r, h, h));
       state[row * in.dim + d] = h;
       o = h;
       if (in.z.p != nullptr) {
@@ -846,9 +980,10 @@ cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_sca
   bool done = false;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CR_MODEL_TYPE(a->dt, {
-    const Strided<T> dy = strided<T>(a, g->dy, g->dy_batch_stride, g->dy_time_stride);
-    const GateOut<T> out = {static_cast<T*>(g->dx), static_cast<T*>(g->dgate),
-                            static_cast<T*>(g->dz), g->dstate};
+    const GateGrads<T> grads = {strided<T>(a, g->dy, g->dy_batch_stride, g->dy_time_stride),
+                                g->dfinal, g->checkpoints, cr_gated_scan_checkpoints(a->len),
+                                {static_cast<T*>(g->dx), static_cast<T*>(g->dgate),
+                                 static_cast<T*>(g->dz), g->dstate}};
     const bool wide = gate_wide(a) &&
                       rows_aligned(g->dy, g->dy_batch_stride, g->dy_time_stride, es, 16) &&
                       ptr_aligned(g->dx, 4) && ptr_aligned(g->dgate, 4) && ptr_aligned(g->dz, 4);
@@ -857,8 +992,7 @@ cr_status cr_gated_scan_backward(const cr_gated_scan_args* a, const cr_gated_sca
     auto kernel = CR_GATE_KERNEL(gated_scan_backward_kernel, T, (a->z != nullptr), wide);
     CR_LAUNCH(kKGatedScanBackward, s,
               done = launch_clusters(kernel, a->batch * per * c, c, kGateWarps * 32, smem, s,
-                                     gate_in<T>(a), dy, g->dfinal, g->checkpoints,
-                                     cr_gated_scan_checkpoints(a->len), out, c));
+                                     gate_in<T>(a), grads, c));
   });
   return done && cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
