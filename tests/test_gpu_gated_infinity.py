@@ -154,3 +154,22 @@ def test_strided_rows_with_nan_beside_them(scr):
                                   checkpoints=kept)
     assert torch.equal(y, want["y"]) and torch.equal(final, want["final"])
     assert all(torch.equal(v, want["d" + k]) for k, v in got.items())
+
+
+@pytest.mark.parametrize("T", [40, 1100])
+def test_final_state_over_the_initial_one(scr, T):
+    """A sequence that is gone through again begins from the state that it was given."""
+    import ctypes
+    from scan_canonical_reduce_gb300 import model as m
+    s, _, _ = make(2, T, 40, torch.bfloat16, 7)
+    s["x"][0, T // 2, 3] = INF
+    s["state"][1, 5] = -INF
+    x, gate, z, state = (s[k].to(DEV) for k in ("x", "gate", "z", "state"))
+    y, final = scr.gated_scan(x, gate, z, state=state, return_state=True)
+    y2 = torch.empty_like(y)
+    a = m._GateArgs(2, T, 40, 3, 8, *(v for k in (x, gate, z) for v in (k.data_ptr(), T * 40, 40)),
+                    state.data_ptr(), None)
+    assert scr.lib().cr_gated_scan(ctypes.byref(a), y2.data_ptr(), T * 40, 40, state.data_ptr(),
+                                   None, torch.cuda.current_stream(DEV).cuda_stream) == 0
+    assert torch.equal(y, y2) and torch.equal(final, state)
+    assert final[0, 3] == INF and final[1, 5] == -INF and final.isinf().sum() == 2
