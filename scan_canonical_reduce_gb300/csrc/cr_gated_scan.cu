@@ -390,14 +390,14 @@ __device__ __forceinline__ Vec<C> join_runs(Joints<C>& j, int turn, int rank, in
   for (int k = 0; k < C; ++k) h[k] = carry[k];
   if (blocks > 1) {
     const cg::cluster_group cl = cg::this_cluster();
-    // the tile's map, to every block of the cluster: warp w tells blocks w, w + 8
+    // the tile's map, to every block of the cluster: warp w tells block w
+    static_assert(kMostCluster <= kGateWarps, "a warp a block");
     if (warp < blocks) {
       Map<C> tile = j.warp[turn][kBack ? kGateWarps - 1 : 0][lane];
-#pragma unroll
+#pragma unroll 1  // (unrolled: one long prompt 131 us for 135, training 255 for 250)
       for (int i = 1; i < kGateWarps; ++i)
         tile = map_join<kInf>(tile, j.warp[turn][kBack ? kGateWarps - 1 - i : i][lane]);
-      for (int to = warp; to < blocks; to += kGateWarps)
-        *cl.map_shared_rank(&j.tile[turn][rank][lane], to) = tile;
+      *cl.map_shared_rank(&j.tile[turn][rank][lane], warp) = tile;
     }
     cl.sync();
     for (int i = 0; i < blocks; ++i) {
