@@ -497,7 +497,7 @@ __device__ __forceinline__ float warp_sum2(float p, float q) {
 // many, and the block waits twice a turn, not for each row. (With all of a block's
 // threads on one row, four rows ahead, the gradient of 16,384 x 2048 in bf16 took
 // 60 us, its sums included; this takes 52, 57 % of the copy rate. Three blocks an SM
-// for two: 54; four turns held for two: 53 to 56.) part: [block][2][dim].
+// for two: 54; four turns held for two: 53 to 56.) part: [block][2][dim], or NULL.
 template <int kThreads, int kRows>
 struct Turn {
   static constexpr int kWarps = kThreads / 32 / kRows;  // of a row
@@ -665,6 +665,7 @@ layer_norm_backward_kernel(NormIn<T> in, int threads, const T* __restrict__ dy, 
     __syncthreads();
     flush(r0 - step);
   }
+  if (part == nullptr) return;
   float* const out = part + (int64_t)blockIdx.x * 2 * dim;
   float* const sums = reinterpret_cast<float*>(shared);
   for (int g = 0; g < groups; ++g) {  // group by group, in order
@@ -1009,7 +1010,8 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
   if (sum_blocks > kMaxBlocks) return CR_ERR_UNSUPPORTED;
   char* at = past_status(ws);
   float* kept = reinterpret_cast<float*>(at);
-  float* part = reinterpret_cast<float*>(at + round256((size_t)rows * 12));
+  const bool sums = g->dweight != nullptr || g->dbias != nullptr;
+  float* part = sums ? reinterpret_cast<float*>(at + round256((size_t)rows * 12)) : nullptr;
   const int64_t parts = sh.blocks != 0 ? sh.blocks : ceil_div(rows, kSumRows);
   const Rows2 xs = {a->x_batch_stride, a->x_time_stride};
   const float* stats = g->stats;
@@ -1028,10 +1030,11 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
       CR_LAUNCH(kKLayerNormBackward, s,
                 layer_norm_backward_long_kernel<T><<<(unsigned)rows, kLongThreads, 0, s>>>(
                     in, dy, ds, stats, dx, os));
-      CR_LAUNCH(kKLayerNormSum, s,
-                layer_norm_part_kernel<T>
-                <<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(parts, 65535)), 256, 0, s>>>(
-                    in, dy, ds, stats, part));
+      if (sums)
+        CR_LAUNCH(kKLayerNormSum, s,
+                  layer_norm_part_kernel<T>
+                  <<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(parts, 65535)), 256, 0, s>>>(
+                      in, dy, ds, stats, part));
     } else if (rows > 0) {
       const auto run = [&](auto launch) {
         return launch(in, sh, dy, ds, rows_end<T>(a, dy, ds), stats, dx, os, part, wide, s);
@@ -1041,7 +1044,7 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* a, const cr_layer_nor
                       : sh.rows == 4    ? run(launch_norm_backward<T, 256, 1, 4>)
                                         : run(launch_norm_backward<T, 256, 1, 8>));
     }
-    if (g->dweight != nullptr || g->dbias != nullptr)
+    if (sums)
       CR_LAUNCH(kKLayerNormSum, s,
                 layer_norm_sum_kernel<<<(unsigned)sum_blocks, 1024, 0, s>>>(part, parts, a->dim,
                                                                             g->dweight, g->dbias));
