@@ -512,7 +512,8 @@ typedef struct {
 } cr_layer_norm_args;
 
 /* Forward. y: of dt with its own strides. stats: NULL, or batch x len x 3
- * floats for the backward call (the mean, what binary32 lacks of it, rstd). */
+ * floats for the backward call (the mean, what binary32 lacks of it, rstd; not
+ * written where dim is 0). */
 cr_status cr_layer_norm(const cr_layer_norm_args* args, void* y, int64_t y_batch_stride,
                         int64_t y_time_stride, float* stats, void* stream);
 

@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <array>
+#include <cmath>
 #include <cstdint>
 #include <exception>
 #include <initializer_list>
@@ -726,6 +727,7 @@ PyObject* layer_norm(PyObject* const* a) {
   const RowAxes o(y);
   at::Tensor stats;
   if (return_stats) stats = c.on.empty(c.stats_shape, at::kFloat);
+  if (return_stats && c.args.dim == 0) stats.fill_(NAN);  // of nothing, by no kernel
   check(f_layer_norm(&c.args, o.t.data_ptr(), o.bs, o.ts,
                      return_stats ? static_cast<float*>(stats.data_ptr()) : nullptr, c.on.ptr),
         "cr_layer_norm");

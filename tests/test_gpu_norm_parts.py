@@ -58,3 +58,13 @@ def test_long_rows_without_weight_or_bias(scr, D, weight, bias):
     assert set(got) == {"x"} | ({"weight"} if weight else set()) | ({"bias"} if bias else set())
     for k in got:
         M.near(got[k], *ref[k], "d" + k)
+
+
+@pytest.mark.parametrize("shape", [(3, 0), (2, 5, 0), (0, 0)])
+def test_rows_without_channels(scr, shape):
+    """The statistics of nothing are NaN, not what their memory held."""
+    x = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+    held = torch.full((4096,), 7.0, device=DEV)
+    del held
+    y, stats = scr.layer_norm(x, return_stats=True)
+    assert y.shape == shape and stats.shape == (*shape[:-1], 3) and bool(stats.isnan().all())
