@@ -127,8 +127,8 @@ __device__ __forceinline__ bool odd(const V& v, int have) {
 }
 
 // What a run of steps does to the state: h -> L + P h. Where P is near 1 its
-// digits are in Q = 1 - P, where it is near 0 in P: kept is Q, or -P from 1 -
-// 2^-7 on (below that, P's error is 2^-17 of itself at most).
+// digits are in Q = 1 - P, where it is near 0 in P: kept is the smaller one, as Q or
+// -P, so that a state's error is a few roundings of what is left of it.
 template <int C>
 struct alignas(8 * C) Map {
   float L[C], F[C];
@@ -149,7 +149,7 @@ __device__ __forceinline__ Map<C> run_map(Vec<C> L, Vec<C> minus_Q, Vec<C> P) {
   for (int k = 0; k < C; ++k) {
     m.L[k] = L.get(k);
     // (fabsf: the zero of a run that holds the state is not negative)
-    m.F[k] = minus_Q.get(k) >= 0x1p-7f - 1.0f ? fabsf(minus_Q.get(k)) : -P.get(k);
+    m.F[k] = minus_Q.get(k) >= -0.5f ? fabsf(minus_Q.get(k)) : -P.get(k);
   }
   return m;
 }
