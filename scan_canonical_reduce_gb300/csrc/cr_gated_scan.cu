@@ -11,6 +11,7 @@
 // infinity becomes NaN in it, and NaN stays NaN: a sequence that ends in something not
 // finite is gone through again, with products that keep infinities (kInf).
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 
 #include <cooperative_groups.h>
@@ -105,6 +106,15 @@ __device__ __forceinline__ Vec<C> minus_sigmoid(Vec<C> v, float s, Vec<C>* e_out
   const Vec<C> e = exp2_of(mul(v, Vec<C>(s)));
   if (e_out != nullptr) *e_out = e;
   return reciprocal_of(fma(e, Vec<C>(-1.0f), Vec<C>(-1.0f)));
+}
+
+// An exponential that may be infinite, as the largest number.
+template <int C>
+__device__ __forceinline__ Vec<C> finite_of(Vec<C> e) {
+  Vec<C> v;
+#pragma unroll
+  for (int k = 0; k < C; ++k) v.set(k, fminf(e.get(k), FLT_MAX));
+  return v;
 }
 
 // A step for r: p - r p, and with what is added. kInf: what is infinite stays so (all
@@ -203,17 +213,6 @@ struct Word {
   }
   static constexpr uint32_t kHeld =  // a gate of +infinity
       sizeof(T) == 4 ? 0x7F800000u : std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
-  // gates of at most 80, whose exponential is finite (NaN stays)
-  static __device__ __forceinline__ uint32_t bounded(uint32_t w) {
-    if constexpr (sizeof(T) == 4) {
-      asm("min.NaN.f32 %0, %0, 0f42A00000;" : "+r"(w));
-    } else if constexpr (std::is_same<T, __half>::value) {
-      asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(w) : "r"(0x55005500u));
-    } else {
-      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x42A042A0u));
-    }
-    return w;
-  }
   static __device__ __forceinline__ uint32_t round(Vec<C> f) {
     if constexpr (sizeof(T) == 4) return __float_as_uint(f.get(0));
     else if constexpr (std::is_same<T, __half>::value) {
@@ -621,9 +620,9 @@ __device__ __forceinline__ void backward_again(const GateIn<T>& in, const GateGr
       for (int i = 0; i < m; ++i) {
         const V x = read(in.x, i), g = read(in.gate, i);
         V e, v = read(grads.dy, i);
-        const V r = minus_sigmoid(V(g.v > 80.0f ? 80.0f : g.v), kLog2e, &e);
+        const V r = minus_sigmoid(g, kLog2e, &e);
         held(0, i) = r.v;
-        held(1, i) = mul(mul(add(s, x), r), mul(e, r)).v;
+        held(1, i) = mul(mul(add(s, x), r), mul(finite_of(e), r)).v;
         s = fma(r, x, decay<true>(r, s));
         if constexpr (kZ) {
           const V z = read(in.z, i), w = minus_sigmoid(z, -kLog2e);
@@ -730,9 +729,9 @@ gated_scan_backward_kernel(const __grid_constant__ GateIn<T> in,
     for (int i = 0; i < kRun; ++i) {
       const V x = W::get(rx.get(i));
       V e;
-      r[i] = minus_sigmoid(W::get(W::bounded(rg.get(i))), kLog2e, &e);
-      // e r = a keeps its digits where r is near 1
-      d[i] = mul(mul(add(s, x), r[i]), mul(e, r[i]));
+      r[i] = minus_sigmoid(W::get(rg.get(i)), kLog2e, &e);
+      // e r = a keeps its digits where r is near 1 (and is 0 with r)
+      d[i] = mul(mul(add(s, x), r[i]), mul(finite_of(e), r[i]));
       s = fma(r[i], x, decay(r[i], s));
       v[i] = W::get(re.get(i));
       if constexpr (kZ) {

@@ -51,3 +51,34 @@ def test_what_is_left(scr, T, left):
     back = scr.gated_scan_backward(zero, zero, gate.to(DEV), state=state.to(DEV),
                                    dfinal=state.to(DEV), checkpoints=kept)["state"]
     assert (np.abs(f64(back) - want[:, -1]) <= e[:, -1] * np.abs(want[:, -1]) + tiny).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("z", [True, False])
+def test_gradients_at_gates_that_hold(scr, dtype, z):
+    """r = exp(-gate) as long as binary32 has it, and zero for a gate of infinity,
+    where the gradients of x and gate are zero whatever comes back."""
+    B, T, D = 2, 40, 32
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    gate = (70 + 16 * torch.rand(B, T, D, generator=g)).to(dtype)
+    x, dy, zz = (r(B, T, D).to(dtype) for _ in range(3))
+    state = r(B, D)
+    gate[:, 7], x[:, 7] = float("inf"), 3e4
+    d = dict(x=x, gate=gate, z=zz if z else None, state=state)
+    d = {k: v if v is None else v.to(DEV) for k, v in d.items()}
+    got = scr.gated_scan_backward(dy.to(DEV) * 2.0 ** 20, **d, dfinal=torch.zeros(B, D, device=DEV))
+    s = f64(zz) * sigmoid(f64(zz)) if z else 1.0
+    G = np.cumsum((f64(dy) * 2.0 ** 20 * s)[:, ::-1], axis=1)[:, ::-1]  # a is 1 here
+    size = np.cumsum(np.abs(f64(dy) * 2.0 ** 20 * s)[:, ::-1], axis=1)[:, ::-1]
+    with np.errstate(over="ignore"):
+        rr = 1 / (1 + np.exp(f64(gate)))
+    step = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    e = (100 + 3 * 86) * U  # r's, and the sums of 40 terms and silu's
+    for name, want, many in (("x", rr * G, rr * size),
+                             ("gate", rr * G * (f64(state)[:, None] - f64(x)),
+                              rr * size * (np.abs(f64(state)[:, None]) + np.abs(f64(x))))):
+        # h is the state to 2^-100; results below 2^-126 are zero
+        off = np.abs(f64(got[name]) - want)
+        assert (off <= step * np.abs(want) + e * many + 2.0 ** -126).all(), name
+        assert not got[name][:, 7].any()
