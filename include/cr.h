@@ -539,8 +539,9 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* args, const cr_layer_
  *   a[t] = 1 / (1 + exp(-gate[t]))
  *   h[t] = a[t] h[t-1] + (1 - a[t]) x[t],  h[-1] = state (zero without one)
  *   y[t] = h[t] * z[t] / (1 + exp(-z[t]))  (h[t] without z)
- * All arithmetic is binary32. An infinite state stays infinite, whatever the gate,
- * until it meets the other infinity or NaN. */
+ * All arithmetic is binary32; a and 1 - a below 2^-126 are zero. An infinite state
+ * stays infinite, whatever the gate, until it meets the other infinity or NaN. The
+ * order of the sums, and with it the last bits, depends on batch, len and dim. */
 typedef struct {
   int64_t batch, len, dim;
   int32_t dt;             /* cr_dtype of x, gate, z, y and their gradients    */
@@ -605,7 +606,8 @@ cr_status cr_gated_scan_step(const cr_gated_scan_args* args, float* state, int64
  * A row without candidates gives -1.
  * Weights are evaluated to 2^-32 of their value and summed as integers, in
  * units of 2^-42 of the largest: the token is that of exact arithmetic unless
- * u, top_p or min_p lies that near to a border. */
+ * u, top_p or min_p lies that near to a border (for logits that differ by less
+ * than 2^100 from the largest, and temperatures of 2^-100 or more). */
 typedef struct {
   int64_t rows, vocab;    /* vocab <= 2^20 (more: CR_ERR_UNSUPPORTED)         */
   int32_t dt;             /* cr_dtype of logits                               */

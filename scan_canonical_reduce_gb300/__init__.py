@@ -21,12 +21,14 @@ shape.
 Beside them stand the operators of a recurrent language model's token path
 (``model.py``): embedding lookup, layer norm, short causal convolution,
 selective state space scan and gated scan, with their gradients and
-single-token forms, and sampling of the next token. Their sums have one order
-each, whatever the launch, so that repeated calls give the same bits; the
-lookup and its gradient are exact expressions as above and a sampled token is
-that of exact arithmetic, while decays, gates, SiLU and softplus rest on the
-GPU's approximate exponential and reciprocal instructions, which no CPU
-evaluation repeats bit for bit.
+single-token forms, and sampling of the next token. The order of their sums
+follows from a call's shapes alone, so that repeated calls give the same bits
+(the gated scan's differ between a sequence alone and the same one in a larger
+batch); the lookup and its gradient are exact expressions as above and a
+sampled token is that of exact arithmetic where no border lies within 2^-32
+(``include/cr.h``), while decays, gates, SiLU and softplus rest on the GPU's
+approximate exponential and reciprocal instructions, which no CPU evaluation
+repeats bit for bit.
 """
 from __future__ import annotations
 

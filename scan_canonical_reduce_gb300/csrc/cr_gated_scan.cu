@@ -187,7 +187,7 @@ __device__ __forceinline__ Map<C> map_join(const Map<C>& a, const Map<C>& b) {
 // channel of binary32, two neighbours of 16 bits, which come by way of shared
 // memory, 16 bytes an access, a tile ahead of their use (kWide: rows on 16 bytes;
 // otherwise the places of 16 bytes that they lie in: 4 x 4096 x 2047 in bf16 takes
-// 105 us, its gradient 199, where 2048 takes 62 and 104; by words of 4 bytes 179 and
+// 109 us, its gradient 198, where 2048 takes 61 and 105; by words of 4 bytes 179 and
 // 334, read channel by channel 461 and 627).
 constexpr int kRun = kGateCheckpoint;
 constexpr int kGateWarps = 8;
@@ -867,8 +867,8 @@ GateIn<T> gate_in(const cr_gated_scan_args* a) {
 // Blocks that share a sequence's time: as many as fit the GPU at once with those
 // of the other sequences and channels (two an SM). Each turn then waits for all of
 // them, which few sequences repay and many do not. Measured, bf16, us for 1 / 2 / 4
-// / 8 blocks: one sequence of 32,768 x 2048 481 / 300 / 156 / 134, 4 of 4096 x 4096
-// with their gradient 253 / 305 / 297 / 346, 9 ragged ones to 517 x 1000 in fp16 14
+// / 8 blocks: one sequence of 32,768 x 2048 481 / 300 / 156 / 135, 4 of 4096 x 4096
+// with their gradient 250 / 305 / 297 / 346, 9 ragged ones to 517 x 1000 in fp16 14
 // / 14 / 18 / 29.
 int gate_blocks(int64_t groups, int64_t len) {
   const int64_t c = std::min(304 / groups, ceil_div(len, kTileSteps));

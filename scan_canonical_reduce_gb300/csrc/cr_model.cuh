@@ -1,6 +1,7 @@
-// Shared pieces of the model operators (embedding, causal convolution,
-// selective scan): element types, vector access, the two nonlinearities, and
-// the host-side argument checks.
+// Shared pieces of the model operators (embedding, layer norm, causal convolution,
+// selective scan, gated scan, sampling): element types, vector access, the
+// nonlinearities, copies into shared memory, clusters, packed arithmetic, and the
+// host-side argument checks.
 //
 // Tensors of 16-bit types are read and written as such; everything between
 // is binary32. Rounding to 16 bits happens once, when a result is stored.

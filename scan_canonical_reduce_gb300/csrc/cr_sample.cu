@@ -9,7 +9,8 @@
 // give the place in it. (A bin of more tokens than can be sorted is cut again by
 // the logits' bits, and one logit's tokens by their index.) Sums are of
 // integers, so that no order of summation changes them, and are exact to 2^-32
-// of a weight: the token is the one that exact arithmetic gives.
+// of a weight: the token is the one that exact arithmetic gives, unless a setting lies
+// that near to a border.
 //
 // A row is one cluster of blocks, a slice each, held in shared memory where it
 // fits. The first block leads: it has the row's sums and the list of a bin.

@@ -15,8 +15,9 @@ is where the call runs (the current stream by default); copies, outputs and
 the call's workspace are made on it: those of a captured call are the graph's
 own.
 
-Every result is one fixed expression of the inputs: repeated calls give the
-same bits.
+Every result is one fixed expression of the inputs, by their shapes: repeated
+calls give the same bits. (A sequence of :func:`gated_scan` may differ in its last
+bits from the same one in a larger batch.)
 
 ``embedding``, ``layer_norm``, ``causal_conv``, ``selective_scan`` and
 ``gated_scan`` are differentiable: where autograd records, their results'
@@ -450,8 +451,9 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, z: torch.Tensor | None = Non
 
     x, gate, z (batch, time, dim), z optional; ``state`` (batch, dim), float32:
     h before time 0 (zeros without it). ``lengths`` (batch): later positions are
-    not read, give zeros and leave the state. Returns y, followed by the last
-    state (``return_state``) and the checkpoints that the backward call takes
+    not read, give zeros and leave the state. An infinite h stays infinite until it
+    meets the other infinity or NaN. Returns y, followed by the last state
+    (``return_state``) and the checkpoints that the backward call takes
     (``return_checkpoints``)."""
     y = _native.gated_scan(x, gate, z, state, lengths, return_state, return_checkpoints, out,
                            stream)
@@ -504,8 +506,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     :func:`embedding` takes as padding.
 
     Each setting is a number, or a tensor (...) with one a row: float32, and
-    int32 or int64 for top_k. The result is that of exact arithmetic (weights to
-    2^-32, sums in integers) and never differentiated."""
+    int32 or int64 for top_k. The result is that of exact arithmetic unless u,
+    top_p or min_p lies within 2^-32 of a border (weights to 2^-32, sums in
+    integers), and never differentiated."""
     return _native.sample(logits, u, temperature, top_k, top_p, min_p, out, stream)
 
 
