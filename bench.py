@@ -18,6 +18,9 @@ e2e   = the same through the public API with pinned host buffers, the
   python bench.py --one-row {reduce,scan,rows,cols} [--n --L --policy --B --rows
                   --cols --levels --dtype --warmup --steps]   (one row, for ncu)
 
+One JSON line goes to the standard output; another, with the single rows and
+kernels, to the standard error.
+
 With N > 1 (torchrun) every rank runs the same step on its own GPU
 (replicas: the rows are independent problems, no exchange); rank 0 prints.
 """
@@ -501,9 +504,22 @@ def run_native(args):
                       "fadd_per_s": fadd_rate},
             "cpu_baseline": cpu, "e2e": e2e, "gpu_launches": launches, "clocks": clocks,
         }
+        line, detail = split_line(line)
+        print(json.dumps(detail), file=sys.stderr)
         print(json.dumps(line))
     if dist:
         dist.destroy_process_group()
+
+
+# what is of single rows and kernels: tens of kilobytes, too long for a reader that
+# keeps a few of the output
+DETAIL = ("rows", "kernels", "extras", "peaks")
+
+
+def split_line(line: dict):
+    """The line for the standard output and the details for the standard error."""
+    return ({k: v for k, v in line.items() if k not in DETAIL},
+            {k: line[k] for k in DETAIL if k in line})
 
 
 L2_FLUSH_BYTES = 512 << 20  # more than the 126 MB L2
