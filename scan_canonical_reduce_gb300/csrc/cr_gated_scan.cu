@@ -125,7 +125,7 @@ __device__ __forceinline__ Vec<C> decay(Vec<C> minus_r, Vec<C> p) {
   if constexpr (kInf) {
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (isinf(p.get(k))) v.set(k, p.get(k));
+      if (isinf(p.get(k)) && !isnan(minus_r.get(k))) v.set(k, p.get(k));
   }
   return v;
 }

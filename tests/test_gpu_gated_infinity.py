@@ -173,3 +173,17 @@ def test_final_state_over_the_initial_one(scr, T):
                                    None, torch.cuda.current_stream(DEV).cuda_stream) == 0
     assert torch.equal(y, y2) and torch.equal(final, state)
     assert final[0, 3] == INF and final[1, 5] == -INF and final.isinf().sum() == 2
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("z", [True, False])
+def test_gates_that_are_nan(scr, dtype, z):
+    """What is infinite becomes NaN there, on its way on and on its way back."""
+    s, dfinal, _ = make(3, 300, 20, dtype, 8, z)
+    put = [("dy", (0, 250, 3), INF), ("gate", (0, 240, 3), NAN),
+           ("dy", (0, 100, 4), -INF), ("gate", (0, 100, 4), NAN),
+           ("dfinal", (1, 5), INF), ("gate", (1, 299, 5), NAN),
+           ("x", (1, 20, 6), INF), ("gate", (1, 21, 6), NAN),
+           ("x", (2, 20, 7), INF), ("dy", (2, 200, 7), INF), ("gate", (2, 120, 7), NAN),
+           ("state", (2, 8), INF), ("gate", (2, 0, 8), NAN)]
+    check(scr, s, dfinal, put)
