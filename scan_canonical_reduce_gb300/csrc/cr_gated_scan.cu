@@ -587,7 +587,7 @@ struct GateGrads {
 // channel after channel of a lane, straight from memory, step after step of a run in
 // shared memory. (Few registers: with a second loop like the kernel's, or a call of
 // one, that one's spilled, and the gradient of 4 x 4096 x 4096 in bf16 took 172 to 220
-// us for 160. Where this runs for all of it, that takes 1050; the forward pass, which
+// us for 160. Where this runs for all of it, that takes 1080; the forward pass, which
 // has a second loop, 192 for 100.)
 template <class T, bool kZ, bool kWide>
 __device__ __forceinline__ void backward_again(const GateIn<T>& in, const GateGrads<T>& grads,
