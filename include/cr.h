@@ -539,9 +539,10 @@ cr_status cr_layer_norm_backward(const cr_layer_norm_args* args, const cr_layer_
  *   a[t] = 1 / (1 + exp(-gate[t]))
  *   h[t] = a[t] h[t-1] + (1 - a[t]) x[t],  h[-1] = state (zero without one)
  *   y[t] = h[t] * z[t] / (1 + exp(-z[t]))  (h[t] without z)
- * All arithmetic is binary32; a and 1 - a below 2^-126 are zero. An infinite state
- * stays infinite, whatever the gate, until it meets the other infinity or NaN. The
- * order of the sums, and with it the last bits, depends on batch, len and dim. */
+ * All arithmetic is binary32; a h[t-1] is right to a rounding of h[t-1], and 1 - a
+ * below 2^-126 is zero. An infinite state stays infinite, whatever the gate, until it
+ * meets the other infinity or NaN. The order of the sums, and with it the last bits,
+ * depends on batch, len and dim. */
 typedef struct {
   int64_t batch, len, dim;
   int32_t dt;             /* cr_dtype of x, gate, z, y and their gradients    */

@@ -7,9 +7,10 @@
 //
 // The state goes by r alone: where a memory is long, a is near 1 and binary32
 // keeps few digits of r in it (a product by a would forget at a rate that is
-// off by 2^-25 / r). So a h is h - r h, one rounding, exact for r = 0 and 1. An
-// infinity becomes NaN in it, and NaN stays NaN: a sequence that ends in something not
-// finite is gone through again, with products that keep infinities (kInf).
+// off by 2^-25 / r). So a h is h - r h, one rounding (of h, where little of it is
+// left), exact for r = 0 and 1. An infinity becomes NaN in it, and NaN stays NaN: a
+// sequence that ends in something not finite is gone through again, with products that
+// keep infinities (kInf).
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
@@ -138,7 +139,7 @@ __device__ __forceinline__ bool odd(const V& v, int have) {
 
 // What a run of steps does to the state: h -> L + P h. Where P is near 1 its
 // digits are in Q = 1 - P, where it is near 0 in P: kept is the smaller one, as Q or
-// -P, so that a state's error is a few roundings of what is left of it.
+// -P, so that a run is as exact as its steps.
 template <int C>
 struct alignas(8 * C) Map {
   float L[C], F[C];
